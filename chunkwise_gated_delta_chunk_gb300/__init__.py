@@ -13,6 +13,11 @@ Names follow the C ABI: :func:`dn_chunk_fwd`,
 :func:`chunk_bwd` are conveniences for the token-serial entry point and the
 backward.  :func:`chunk_fwd` is a convenience that allocates
 ``o``, ``ht`` and the workspace with torch and calls :func:`dn_chunk_fwd`.
+
+The operators around the recurrence (``include/dn_layer_ops.h``) are
+:func:`causal_conv_fwd` and :func:`causal_conv_bwd`, :func:`selective_scan_fwd`
+and :func:`selective_scan_bwd`, :func:`layer_norm_fwd` and
+:func:`layer_norm_bwd`; they check their tensors and allocate what is not given.
 """
 from __future__ import annotations
 
@@ -34,11 +39,18 @@ DN_F32 = 1
 
 # Option bits of the ``flags`` argument.
 DN_QK_L2NORM = 1
+DN_CONV_SILU = 1
+DN_SCAN_SOFTPLUS = 1
+DN_NORM_RMS = 1
 
-# Every symbol the public header declares.
+# Every symbol the public headers declare.
 ABI_SYMBOLS = ("dn_chunk_fwd", "dn_chunk_fwd_workspace_bytes", "dn_chunk_fwd_noalloc",
                "dn_recurrent_fwd", "dn_chunk_bwd", "dn_chunk_bwd_workspace_bytes", "dn_check",
-               "dn_status_str", "dn_last_kernel")
+               "dn_status_str", "dn_last_kernel",
+               "dn_causal_conv_fwd", "dn_causal_conv_bwd", "dn_causal_conv_bwd_workspace_bytes",
+               "dn_selective_scan_fwd", "dn_selective_scan_fwd_workspace_bytes",
+               "dn_selective_scan_bwd", "dn_selective_scan_bwd_workspace_bytes",
+               "dn_layer_norm_fwd", "dn_layer_norm_bwd", "dn_layer_norm_bwd_workspace_bytes")
 
 # Size of the library's fixed scratch array used by dn_chunk_fwd_noalloc.
 DN_NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
@@ -82,6 +94,22 @@ def load(path: str | None = None):
         lib.dn_chunk_bwd.restype = I
         lib.dn_chunk_bwd_workspace_bytes.argtypes = [I, I, I, I, I, I, I, I]
         lib.dn_chunk_bwd_workspace_bytes.restype = Z
+        L = ctypes.c_longlong
+        lib.dn_causal_conv_fwd.argtypes = [P] * 5 + [I] * 6 + [U, P, P, P]
+        lib.dn_causal_conv_bwd.argtypes = [P] * 5 + [I] * 6 + [U, P, I] + [P] * 6 + [Z, P]
+        lib.dn_causal_conv_bwd_workspace_bytes.argtypes = [I] * 6
+        lib.dn_selective_scan_fwd.argtypes = [P] * 10 + [I] * 7 + [U, P, P, P, Z, P]
+        lib.dn_selective_scan_fwd_workspace_bytes.argtypes = [I] * 7
+        lib.dn_selective_scan_bwd.argtypes = [P] * 10 + [I] * 7 + [U] + [P] * 12 + [Z, P]
+        lib.dn_selective_scan_bwd_workspace_bytes.argtypes = [I] * 7
+        lib.dn_layer_norm_fwd.argtypes = [P] * 4 + [L, I, I, F, U, P, P]
+        lib.dn_layer_norm_bwd.argtypes = [P] * 4 + [L, I, I, F, U] + [P] * 6 + [Z, P]
+        lib.dn_layer_norm_bwd_workspace_bytes.argtypes = [L, I, I]
+        for op in ("causal_conv", "selective_scan", "layer_norm"):
+            getattr(lib, "dn_%s_fwd" % op).restype = I
+            getattr(lib, "dn_%s_bwd" % op).restype = I
+            getattr(lib, "dn_%s_bwd_workspace_bytes" % op).restype = Z
+        lib.dn_selective_scan_fwd_workspace_bytes.restype = Z
         lib.dn_check.argtypes = [P]
         lib.dn_check.restype = I
         lib.dn_status_str.argtypes = [I]
@@ -296,4 +324,263 @@ def chunk_bwd(q, k, v, beta, g=None, h0=None, cu_seqlens=None, scale=None, do=No
                       workspace, stream=stream)
     if st != DN_OK:
         raise DnError(st, "dn_chunk_bwd")
+    return out
+
+
+# ---- operators around the recurrence (include/dn_layer_ops.h) -------------
+
+
+def _operand(name, t, shape, dtype, device, optional=True):
+    """Refuse a tensor that is not what the C entry point takes it for."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError("%s is required" % name)
+    if t.device != device or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s, not %s of shape %s on %s%s"
+                         % (name, dtype, tuple(shape), device, t.dtype, tuple(t.shape), t.device,
+                            "" if t.is_contiguous() else ", not contiguous"))
+    return t.data_ptr()
+
+
+def _device_of(x):
+    """The device of a call's first tensor, which has to be the current one."""
+    import torch
+    device = x.device
+    if device.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device, not on %s" % device)
+    if device.index != torch.cuda.current_device():
+        raise ValueError("tensors are on %s, which is not the current device" % device)
+    return device
+
+
+def _sequences(B, cu_seqlens, device):
+    """Number of sequences and the offsets' address."""
+    import torch
+    if cu_seqlens is None:
+        return B, None
+    if B != 1:
+        raise ValueError("cu_seqlens needs B = 1, not %d" % B)
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must have one dimension of N + 1 offsets")
+    return cu_seqlens.numel() - 1, _operand("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int64,
+                                            device)
+
+
+def _space(nbytes, workspace, device):
+    """The caller's workspace, or a new one; and its address and bytes."""
+    import torch
+    if workspace is None:
+        if nbytes == 0:
+            return None, None, 0
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on %s" % device)
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def causal_conv_fwd(x, weight, bias=None, h0=None, cu_seqlens=None, silu=True,
+                    output_final_state=True, stream=None, y=None, ht=None):
+    """Short depthwise causal convolution (``dn_causal_conv_fwd``).
+
+    x ``[B, T, D]``; weight ``[D, W]`` and bias ``[D]`` fp32, W = 2..4; h0
+    ``[N, W-1, D]`` the inputs before each sequence, of x's type; cu_seqlens
+    int64 ``[N+1]`` on the device.  ``silu`` applies silu to the result.  One
+    decoding step is T = 1 with h0 given; ``ht`` may then be ``h0`` itself.
+    Returns ``(y, ht)`` (``ht`` is None unless ``output_final_state``).
+    """
+    import torch
+    device = _device_of(x)
+    B, T, D = x.shape
+    W = weight.shape[-1]
+    f32, dt = torch.float32, x.dtype
+    code = dtype_code(dt)
+    N, cu = _sequences(B, cu_seqlens, device)
+    state = (N, W - 1, D)
+    if y is None:
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+    if not output_final_state:
+        ht = None
+    elif ht is None:
+        ht = torch.empty(state, dtype=dt, device=device)
+    st = load().dn_causal_conv_fwd(
+        _operand("x", x, x.shape, dt, device), _operand("weight", weight, (D, W), f32, device, False),
+        _operand("bias", bias, (D,), f32, device), _operand("h0", h0, state, dt, device), cu, N, B, T,
+        D, W, code, DN_CONV_SILU if silu else 0, _operand("y", y, x.shape, dt, device),
+        _operand("ht", ht, state, dt, device), _stream(stream))
+    if st != DN_OK:
+        raise DnError(st, "dn_causal_conv_fwd")
+    return y, ht
+
+
+def causal_conv_bwd(x, weight, bias=None, h0=None, cu_seqlens=None, silu=True, dy=None, dht=None,
+                    stream=None, workspace=None):
+    """Gradients of :func:`causal_conv_fwd`'s loss ``sum(dy * y) + sum(dht * ht)``.
+
+    ``dy`` has x's type or fp32 (what :func:`chunk_bwd` returns).  Returns a
+    dict with ``dx`` and ``dh0`` (None when h0 is None) of x's type, and
+    ``dweight`` and ``dbias`` (None when bias is None) in fp32.
+    """
+    import torch
+    device = _device_of(x)
+    B, T, D = x.shape
+    W = weight.shape[-1]
+    f32, dt = torch.float32, x.dtype
+    code = dtype_code(dt)
+    N, cu = _sequences(B, cu_seqlens, device)
+    state = (N, W - 1, D)
+    if dy is None:
+        raise ValueError("dy is required")
+    gt = dy.dtype if dy.dtype == f32 else dt
+    lib = load()
+    out = dict(dx=torch.empty_like(x, memory_format=torch.contiguous_format),
+               dweight=torch.empty((D, W), dtype=f32, device=device),
+               dbias=None if bias is None else torch.empty(D, dtype=f32, device=device),
+               dh0=None if h0 is None else torch.empty(state, dtype=dt, device=device))
+    workspace, ws, wsb = _space(lib.dn_causal_conv_bwd_workspace_bytes(N, B, T, D, W, code), workspace,
+                                device)
+    st = lib.dn_causal_conv_bwd(
+        _operand("x", x, x.shape, dt, device), _operand("weight", weight, (D, W), f32, device, False),
+        _operand("bias", bias, (D,), f32, device), _operand("h0", h0, state, dt, device), cu, N, B, T,
+        D, W, code, DN_CONV_SILU if silu else 0, _operand("dy", dy, x.shape, gt, device),
+        dtype_code(gt), _operand("dht", dht, state, dt, device), out["dx"].data_ptr(),
+        out["dweight"].data_ptr(), _ptr(out["dbias"]), _ptr(out["dh0"]), ws, wsb, _stream(stream))
+    if st != DN_OK:
+        raise DnError(st, "dn_causal_conv_bwd")
+    return out
+
+
+def _scan_inputs(x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, dt_softplus):
+    """Checked addresses and sizes of a scan, in the order of the C arguments."""
+    import torch
+    device = _device_of(x)
+    Bt, T, Di = x.shape
+    G, Ns = B.shape[-2:]
+    f32, ty = torch.float32, x.dtype
+    code = dtype_code(ty)
+    N, cu = _sequences(Bt, cu_seqlens, device)
+    rows, bc, state = x.shape, (Bt, T, G, Ns), (N, Di, Ns)
+    ptrs = (_operand("x", x, rows, ty, device), _operand("dt", dt, rows, ty, device, False),
+            _operand("A", A, (Di, Ns), f32, device, False), _operand("B", B, bc, ty, device, False),
+            _operand("C", C, bc, ty, device, False), _operand("D", D, (Di,), f32, device),
+            _operand("z", z, rows, ty, device), _operand("dt_bias", dt_bias, (Di,), f32, device),
+            _operand("h0", h0, state, f32, device), cu)
+    sizes = (N, Bt, T, Di, G, Ns, code)
+    return device, ty, bc, state, ptrs, sizes, DN_SCAN_SOFTPLUS if dt_softplus else 0
+
+
+def selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, cu_seqlens=None,
+                       dt_softplus=True, output_final_state=True, stream=None, y=None, ht=None,
+                       workspace=None):
+    """Selective state space scan (``dn_selective_scan_fwd``).
+
+    x, dt, z ``[B, T, D]`` and B, C ``[B, T, G, N]`` of one type; A ``[D, N]``,
+    D and dt_bias ``[D]``, h0 ``[n_seqs, D, N]`` fp32; N = 16, 32, 64 or 128;
+    cu_seqlens int64 ``[n_seqs+1]`` on the device.  ``dt_softplus`` passes
+    dt + dt_bias through log(1 + e^.).  One decoding step is T = 1 with h0
+    given; ``ht`` may then be ``h0`` itself.  Returns ``(y, ht)`` (``ht`` is
+    None unless ``output_final_state``).
+    """
+    import torch
+    device, ty, bc, state, ptrs, sizes, flags = _scan_inputs(x, dt, A, B, C, D, z, dt_bias, h0,
+                                                             cu_seqlens, dt_softplus)
+    if y is None:
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+    if not output_final_state:
+        ht = None
+    elif ht is None:
+        ht = torch.empty(state, dtype=torch.float32, device=device)
+    lib = load()
+    workspace, ws, wsb = _space(lib.dn_selective_scan_fwd_workspace_bytes(*sizes), workspace, device)
+    st = lib.dn_selective_scan_fwd(*ptrs, *sizes, flags, _operand("y", y, x.shape, ty, device),
+                                   _operand("ht", ht, state, torch.float32, device), ws, wsb,
+                                   _stream(stream))
+    if st != DN_OK:
+        raise DnError(st, "dn_selective_scan_fwd")
+    return y, ht
+
+
+def selective_scan_bwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, cu_seqlens=None,
+                       dt_softplus=True, dy=None, dht=None, stream=None, workspace=None):
+    """Gradients of :func:`selective_scan_fwd`'s loss ``sum(dy * y) + sum(dht * ht)``.
+
+    Returns a dict with ``dx``, ``ddt``, ``dz``, ``dB``, ``dC`` of x's type and
+    ``dA``, ``dD``, ``ddt_bias``, ``dh0`` in fp32; those of absent inputs are None.
+    """
+    import torch
+    device, ty, bc, state, ptrs, sizes, flags = _scan_inputs(x, dt, A, B, C, D, z, dt_bias, h0,
+                                                             cu_seqlens, dt_softplus)
+    f32 = torch.float32
+
+    def like(t, shape, dtype):
+        return None if t is None else torch.empty(shape, dtype=dtype, device=device)
+
+    out = dict(dx=like(x, x.shape, ty), ddt=like(x, x.shape, ty), dA=like(A, A.shape, f32),
+               dB=like(B, bc, ty), dC=like(C, bc, ty), dD=like(D, (x.shape[2],), f32),
+               dz=like(z, x.shape, ty), ddt_bias=like(dt_bias, (x.shape[2],), f32),
+               dh0=like(h0, state, f32))
+    lib = load()
+    workspace, ws, wsb = _space(lib.dn_selective_scan_bwd_workspace_bytes(*sizes), workspace, device)
+    st = lib.dn_selective_scan_bwd(
+        *ptrs, *sizes, flags, _operand("dy", dy, x.shape, ty, device, False),
+        _operand("dht", dht, state, f32, device), _ptr(out["dx"]), _ptr(out["ddt"]), _ptr(out["dA"]),
+        _ptr(out["dB"]), _ptr(out["dC"]), _ptr(out["dD"]), _ptr(out["dz"]), _ptr(out["ddt_bias"]),
+        _ptr(out["dh0"]), ws, wsb, _stream(stream))
+    if st != DN_OK:
+        raise DnError(st, "dn_selective_scan_bwd")
+    return out
+
+
+def layer_norm_fwd(x, weight=None, bias=None, z=None, eps=1e-5, rms=False, stream=None, y=None):
+    """Layer norm over the last dimension of x (``dn_layer_norm_fwd``).
+
+    weight and bias ``[D]`` fp32; ``z`` of x's shape and type multiplies the
+    result by silu(z); ``rms`` takes no mean (root mean square norm).  ``y``
+    may be x or z.  Returns y.
+    """
+    import torch
+    device = _device_of(x)
+    D = x.shape[-1]
+    f32, dt = torch.float32, x.dtype
+    if y is None:
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+    st = load().dn_layer_norm_fwd(
+        _operand("x", x, x.shape, dt, device), _operand("weight", weight, (D,), f32, device),
+        _operand("bias", bias, (D,), f32, device), _operand("z", z, x.shape, dt, device),
+        x.numel() // D if D else 0, D, dtype_code(dt), eps, DN_NORM_RMS if rms else 0,
+        _operand("y", y, x.shape, dt, device), _stream(stream))
+    if st != DN_OK:
+        raise DnError(st, "dn_layer_norm_fwd")
+    return y
+
+
+def layer_norm_bwd(x, weight=None, bias=None, z=None, eps=1e-5, rms=False, dy=None, stream=None,
+                   workspace=None):
+    """Gradients of :func:`layer_norm_fwd`'s loss ``sum(dy * y)``.
+
+    Returns a dict with ``dx`` and ``dz`` of x's type and ``dweight`` and
+    ``dbias`` in fp32; those of absent inputs are None.
+    """
+    import torch
+    device = _device_of(x)
+    D = x.shape[-1]
+    rows = x.numel() // D if D else 0
+    f32, dt = torch.float32, x.dtype
+    code = dtype_code(dt)
+    lib = load()
+    out = dict(dx=torch.empty_like(x, memory_format=torch.contiguous_format),
+               dweight=None if weight is None else torch.empty(D, dtype=f32, device=device),
+               dbias=None if bias is None else torch.empty(D, dtype=f32, device=device),
+               dz=None if z is None else torch.empty_like(x, memory_format=torch.contiguous_format))
+    sums = weight is not None or bias is not None
+    workspace, ws, wsb = _space(lib.dn_layer_norm_bwd_workspace_bytes(rows, D, code) if sums else 0,
+                                workspace, device)
+    st = lib.dn_layer_norm_bwd(
+        _operand("x", x, x.shape, dt, device), _operand("weight", weight, (D,), f32, device),
+        _operand("bias", bias, (D,), f32, device), _operand("z", z, x.shape, dt, device), rows, D,
+        code, eps, DN_NORM_RMS if rms else 0, _operand("dy", dy, x.shape, dt, device, False),
+        out["dx"].data_ptr(), _ptr(out["dweight"]), _ptr(out["dbias"]), _ptr(out["dz"]), ws, wsb,
+        _stream(stream))
+    if st != DN_OK:
+        raise DnError(st, "dn_layer_norm_bwd")
     return out

@@ -9,6 +9,7 @@
 
 #include "dn_chunk_fwd.h"
 #include "dn_internal.h"
+#include "dn_layer.h"
 #include "dn_tc.h"
 
 #define DN_EXPORT extern "C" __attribute__((visibility("default")))
@@ -31,6 +32,10 @@ thread_local const char *t_last_kernel = "";
 thread_local unsigned t_test_stall = 0;
 #endif
 
+}  // namespace
+
+namespace dn {
+
 // Device address of g_dn_status on the current device (looked up once per
 // device; the lookup is a host call that allocates nothing).
 cudaError_t status_ptr(unsigned **out) {
@@ -48,6 +53,14 @@ cudaError_t status_ptr(unsigned **out) {
     *out = g_status_ptr[dev];
     return cudaSuccess;
 }
+
+void set_last_kernel(const char *name) { t_last_kernel = name; }
+
+}  // namespace dn
+
+namespace {
+
+using dn::status_ptr;
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

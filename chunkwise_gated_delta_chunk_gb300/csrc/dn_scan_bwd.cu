@@ -1,0 +1,561 @@
+// Selective state space scan, backward.
+//
+// With a_t[n] = e^{delta_t A[n]}, dyo = dy silu(z) and the states h of the forward:
+//     g_t[n]  = C_t[n] dyo_t + a_{t+1}[n] g_{t+1}[n]        (the gradient of h_t)
+//     s_t     = sum_n g_t[n] B_t[n],   q_t[n] = g_t[n] a_t[n] h_{t-1}[n]
+//     dx      = delta s + Dskip dyo,   ddelta = x s + sum_n q[n] A[n],   ddt = ddelta softplus'(dt + dt_bias)
+//     dA[n]   = sum_t delta q[n],      dB[n] = sum_d delta x g[n],       dC[n] = sum_d dyo h[n]
+//     dDskip  = sum_t dyo x,           ddt_bias = sum_t ddt,             dz = dy (C.h + Dskip x) silu'(z)
+//
+// Every sequence is cut into chunks of 64 tokens, and all chunks are worked on at
+// once:
+//   1. scan_bwd_state  per chunk, in one walk: the state from zero at its end, the sum
+//                      of delta, and the gradient that its own outputs send to the state
+//                      at its start (with the running product of a);
+//   2. scan_combine    steps both over the chunks, forward and back;
+//   3. scan_bwd        per chunk: the states again from its start, then the reverse walk;
+//   4. scan_bwd_bc, scan_bwd_sums  add the parts in a fixed order.
+//
+// The states of 8 tokens are kept in registers: the reverse walk takes the chunk in
+// pieces of 8 tokens, and computes the states of a piece again from the state at its
+// start, which a first walk over the chunk left in shared memory.  So a_t[n] is
+// computed three times, once in step 1; no state is ever written per token.
+//
+// The sums over channels (dB, dC) are folded over the lanes that hold the warp's
+// channels, joined over the warps in shared memory, and gathered there over all
+// channel tiles of the block: a block takes one chunk and a part of a group's channels,
+// and writes one row of 2 N sums per token.
+//
+// What bounds it: about 20 N fp32 operations and 3 N exponentials per channel and token.
+#include "dn_scan.cuh"
+
+namespace dn {
+namespace {
+
+using namespace scan;
+
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+constexpr int kTile = 16;   // tokens staged at a time
+constexpr int kPiece = 8;   // tokens whose states are in registers
+
+// One thread's place in a tile's rows: four channels of one token.
+struct Place {
+    int t, c, n;  // token of the tile, first channel, channels there (<= 0: none)
+};
+
+template <int CH>
+__device__ __forceinline__ Place place_of(int tid, const Channels &cs) {
+    constexpr int CV = CH / 4;
+    Place r;
+    r.t = tid / CV;
+    r.c = (tid % CV) * 4;
+    r.n = r.t < kTile ? cs.n - r.c : 0;
+    return r;
+}
+
+template <typename T, int N>
+struct BcRows {
+    static constexpr int kVecs = kTile * N / 2 / kThreads;
+    float v[kVecs][4];
+    __device__ __forceinline__ void fetch(const ScanParams &p, int g, long long t0, long long t1, bool c_too) {
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k) {
+            const int i = threadIdx.x + k * kThreads, which = i / (kTile * N / 4), r = i % (kTile * N / 4);
+            const int t = r / (N / 4), c = (r % (N / 4)) * 4;
+            if (which && !c_too) continue;
+            load4<T, true>(which ? p.Cm : p.Bm, (t0 + t) * p.G + g, N, c, 4, t0 + t < t1, v[k]);
+        }
+    }
+    __device__ __forceinline__ void put(float *bc, bool c_too) {  // bc [2][kTile][N]
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k) {
+            const int i = threadIdx.x + k * kThreads;
+            if (i >= kTile * N / 4 && !c_too) continue;
+            *reinterpret_cast<float4 *>(bc + i * 4) = make_float4(v[k][0], v[k][1], v[k][2], v[k][3]);
+        }
+    }
+};
+
+__device__ __forceinline__ void to4(float (&v)[4], const float4 &f) {
+    v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+}
+
+// ---- 1: what a chunk does to the state, and its outputs to the state's gradient ------
+
+template <typename T, int L, bool VEC>
+__global__ void __launch_bounds__(kThreads) scan_bwd_state(ScanParams p) {
+    constexpr int N = kS * L, CH = kThreads / L;
+    __shared__ float2 s_dx[kTile][CH];
+    __shared__ float s_g[kTile][CH];
+    __shared__ __align__(16) float s_bc[2 * kTile * N];
+    const int tid = threadIdx.x;
+    const int tiles = p.G * ((p.D / p.G + CH - 1) / CH);
+    const int ct = blockIdx.x % tiles;
+    const long long slot = blockIdx.x / tiles;
+    if (blockIdx.x == 0) check_offsets(p.seq, tid, kThreads);
+    const SeqTile seq = seq_tile(p.seq, slot, kChunk);
+    if (!seq.ok) return;
+    const Channels cs = channels_of<CH>(p, ct);
+    const int ch = tid / L, lane = tid % L;
+    const bool own = ch < cs.n;
+    const long long dn_at = (long long)(cs.d0 + ch) * N + lane * kS;
+    float a[kS] = {0.f, 0.f, 0.f, 0.f}, h[kS], pr[kS], rg[kS];
+    if (own) {
+        to4(a, *reinterpret_cast<const float4 *>(p.A + dn_at));
+#pragma unroll
+        for (int i = 0; i < kS; ++i) a[i] = log2_rate(a[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kS; ++i) h[i] = rg[i] = 0.f, pr[i] = 1.f;
+    const Place at = place_of<CH>(tid, cs);
+    float bias[4], dsum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bias[i] = i < at.n && p.dt_bias ? p.dt_bias[cs.d0 + at.c + i] : 0.f;
+
+    for (long long t0 = seq.t0; t0 < seq.t1; t0 += kTile) {
+        BcRows<T, N> bc;
+        bc.fetch(p, cs.g, t0, seq.t1, true);
+        if (at.t < kTile) {
+            const bool in = t0 + at.t < seq.t1;
+            float fx[4], fd[4], fg[4], fz[4];
+            load4<T, VEC>(p.x, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, fx);
+            load4<T, VEC>(p.dt, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, fd);
+            load4<T, VEC>(p.dy, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, fg);
+            if (p.z) load4<T, VEC>(p.z, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, fz);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float raw = fd[i] + bias[i];
+                const float delta = !in || i >= at.n ? 0.f : p.softplus ? softplus(raw) : raw;
+                s_dx[at.t][at.c + i] = make_float2(delta, delta * fx[i]);
+                s_g[at.t][at.c + i] = p.z ? fg[i] * silu_f(fz[i]) : fg[i];
+                dsum[i] += delta;
+            }
+        }
+        bc.put(s_bc, true);
+        __syncthreads();
+#pragma unroll 4
+        for (int t = 0; t < kTile; ++t) {
+            const float2 dx = s_dx[t][ch];
+            const float go = s_g[t][ch];
+            float b[4], c[4];
+            to4(b, *reinterpret_cast<const float4 *>(s_bc + t * N + lane * kS));
+            to4(c, *reinterpret_cast<const float4 *>(s_bc + (kTile + t) * N + lane * kS));
+#pragma unroll
+            for (int i = 0; i < kS; ++i) {
+                const float e = ex2(dx.x * a[i]);
+                h[i] = fmaf(e, h[i], dx.y * b[i]);
+                pr[i] *= e;
+                rg[i] = fmaf(pr[i], c[i] * go, rg[i]);
+            }
+        }
+        __syncthreads();
+    }
+    if (own) {
+        *reinterpret_cast<float4 *>(p.hs + slot * p.D * N + dn_at) = make_float4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<float4 *>(p.gs + slot * p.D * N + dn_at) = make_float4(rg[0], rg[1], rg[2], rg[3]);
+    }
+    if (at.t < kTile)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s_g[at.t][at.c + i] = dsum[i];
+    __syncthreads();
+    if (tid < cs.n) {
+        float s = 0.f;
+#pragma unroll
+        for (int t = 0; t < kTile; ++t) s += s_g[t][tid];
+        p.dsum[slot * p.D + cs.d0 + tid] = s;
+    }
+}
+
+// ---- 3: the reverse walk --------------------------------------------------------------
+
+template <int L>
+struct Smem {  // offsets in floats
+    static constexpr int N = kS * L, CH = kThreads / L;
+    static constexpr int kDx = 0;                              // float2 [kChunk][CH]
+    static constexpr int kBc = kDx + 2 * kChunk * CH;          // [2][kTile][N]
+    static constexpr int kGo = kBc + 2 * kTile * N;            // [kTile][CH]
+    static constexpr int kRes = kGo + kTile * CH;              // [3][kTile][CH]: s, sum q A, C.h
+    static constexpr int kStart = kRes + 3 * kTile * CH;       // [kChunk / kPiece][kThreads][4]
+    static constexpr int kRed = kStart + kChunk / kPiece * kThreads * 4;  // [kWarps][kPiece][2 N]
+    static constexpr int kAcc = kRed + kWarps * kPiece * 2 * N;  // [kChunk][2 N]
+    static constexpr int kAll = kAcc + kChunk * 2 * N;
+};
+
+template <typename T, int L, bool VEC>
+__global__ void __launch_bounds__(kThreads) scan_bwd(ScanParams p, int parts) {
+    using M = Smem<L>;
+    constexpr int N = M::N, CH = M::CH;
+    extern __shared__ __align__(16) float sm[];
+    float2(*s_dx)[CH] = reinterpret_cast<float2(*)[CH]>(sm + M::kDx);
+    float *s_bc = sm + M::kBc;
+    float(*s_go)[CH] = reinterpret_cast<float(*)[CH]>(sm + M::kGo);
+    float(*s_res)[kTile][CH] = reinterpret_cast<float(*)[kTile][CH]>(sm + M::kRes);
+    float4 *s_start = reinterpret_cast<float4 *>(sm + M::kStart);
+    float *s_red = sm + M::kRed, *s_acc = sm + M::kAcc;
+
+    const int tid = threadIdx.x, warp = tid >> 5;
+    const long long slot = blockIdx.x / (parts * p.G);
+    const int gp = blockIdx.x % (parts * p.G), g = gp / parts, part = gp % parts;
+    const int per = (p.D / p.G + CH - 1) / CH;  // channel tiles of a group
+    const int first = (int)((long long)per * part / parts), last = (int)((long long)per * (part + 1) / parts);
+    const SeqTile seq = seq_tile(p.seq, slot, kChunk);
+    const int ch = tid / L, lane = tid % L;
+    const int len = seq.ok ? (int)(seq.t1 - seq.t0) : 0;
+    const int nt = (len + kTile - 1) / kTile;
+
+    for (int i = tid; i < len * 2 * N; i += kThreads) s_acc[i] = 0.f;
+
+    for (int ct = g * per + first; ct < g * per + last; ++ct) {
+        const Channels cs = channels_of<CH>(p, ct);
+        const bool own = ch < cs.n;
+        const long long dn_at = slot * p.D * N + (long long)(cs.d0 + ch) * N + lane * kS;
+        const Place at = place_of<CH>(tid, cs);
+        if (nt == 0) {  // a slot without tokens adds nothing
+            if (own) *reinterpret_cast<float4 *>(p.gs + dn_at) = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (tid < cs.n) {
+                p.vec[slot * 2 * p.D + cs.d0 + tid] = 0.f;
+                p.vec[(slot * 2 + 1) * p.D + cs.d0 + tid] = 0.f;
+            }
+            continue;
+        }
+        float A[kS] = {0.f, 0.f, 0.f, 0.f}, a2[kS], h[kS] = {0.f, 0.f, 0.f, 0.f}, carry[kS] = {0.f, 0.f, 0.f, 0.f};
+        float dA[kS] = {0.f, 0.f, 0.f, 0.f};
+        if (own) {
+            to4(A, *reinterpret_cast<const float4 *>(p.A + (long long)(cs.d0 + ch) * N + lane * kS));
+            to4(h, *reinterpret_cast<const float4 *>(p.hs + dn_at));
+            to4(carry, *reinterpret_cast<const float4 *>(p.gs + dn_at));
+        }
+#pragma unroll
+        for (int i = 0; i < kS; ++i) a2[i] = log2_rate(A[i]);
+        float bias[4], skip[4], sD[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            bias[i] = i < at.n && p.dt_bias ? p.dt_bias[cs.d0 + at.c + i] : 0.f;
+            skip[i] = i < at.n && p.Dskip ? p.Dskip[cs.d0 + at.c + i] : 0.f;
+        }
+        // forward over the chunk: the state at the start of every piece
+        for (int k = 0; k < nt; ++k) {
+            const long long t0 = seq.t0 + k * kTile;
+            BcRows<T, N> bc;
+            bc.fetch(p, cs.g, t0, seq.t1, false);
+            if (at.t < kTile) {
+                const bool in = t0 + at.t < seq.t1;
+                float fx[4], fd[4];
+                load4<T, VEC>(p.x, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, fx);
+                load4<T, VEC>(p.dt, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, fd);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float raw = fd[i] + bias[i];
+                    const float delta = !in || i >= at.n ? 0.f : p.softplus ? softplus(raw) : raw;
+                    s_dx[k * kTile + at.t][at.c + i] = make_float2(delta, delta * fx[i]);
+                }
+            }
+            bc.put(s_bc, false);
+            __syncthreads();
+#pragma unroll 2
+            for (int q = 0; q < kTile; q += kPiece) {
+                s_start[((k * kTile + q) / kPiece) * kThreads + tid] = make_float4(h[0], h[1], h[2], h[3]);
+#pragma unroll
+                for (int t = 0; t < kPiece; ++t) {
+                    const float2 dx = s_dx[k * kTile + q + t][ch];
+                    float b[4];
+                    to4(b, *reinterpret_cast<const float4 *>(s_bc + (q + t) * N + lane * kS));
+#pragma unroll
+                    for (int i = 0; i < kS; ++i) h[i] = fmaf(ex2(dx.x * a2[i]), h[i], dx.y * b[i]);
+                }
+            }
+            __syncthreads();
+        }
+        // back over the chunk
+        for (int k = nt - 1; k >= 0; --k) {
+            const long long t0 = seq.t0 + k * kTile;
+            const bool in = t0 + at.t < seq.t1 && at.t < kTile;
+            BcRows<T, N> bc;
+            bc.fetch(p, cs.g, t0, seq.t1, true);
+            float fx[4], fd[4], fg[4], fz[4];
+            load4<T, VEC>(p.x, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, fx);
+            load4<T, VEC>(p.dt, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, fd);
+            load4<T, VEC>(p.dy, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, fg);
+            if (p.z) load4<T, VEC>(p.z, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, fz);
+            if (at.t < kTile)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s_go[at.t][at.c + i] = p.z ? fg[i] * silu_f(fz[i]) : fg[i];
+            bc.put(s_bc, true);
+            __syncthreads();
+            for (int q = kTile - kPiece; q >= 0; q -= kPiece) {
+                float e[kPiece][kS], hh[kPiece + 1][kS];
+                to4(hh[0], s_start[((k * kTile + q) / kPiece) * kThreads + tid]);
+#pragma unroll
+                for (int u = 0; u < kPiece; u += 4) {
+                    float part4[4];
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const int t = u + w;
+                        const float2 dx = s_dx[k * kTile + q + t][ch];
+                        float b[4], c[4];
+                        to4(b, *reinterpret_cast<const float4 *>(s_bc + (q + t) * N + lane * kS));
+                        to4(c, *reinterpret_cast<const float4 *>(s_bc + (kTile + q + t) * N + lane * kS));
+                        float y = 0.f;
+#pragma unroll
+                        for (int i = 0; i < kS; ++i) {
+                            e[t][i] = ex2(dx.x * a2[i]);
+                            hh[t + 1][i] = fmaf(e[t][i], hh[t][i], dx.y * b[i]);
+                            y = fmaf(c[i], hh[t + 1][i], y);
+                        }
+                        part4[w] = y;
+                    }
+                    if (p.z) {
+                        const float y = sum4<L>(part4, lane);
+                        if (lane < 4) s_res[2][q + u + lane][ch] = y;
+                    }
+                }
+#pragma unroll
+                for (int u = kPiece - 4; u >= 0; u -= 4) {
+                    float ps[4], pq[4];
+#pragma unroll
+                    for (int w = 3; w >= 0; --w) {
+                        const int t = u + w;
+                        const float2 dx = s_dx[k * kTile + q + t][ch];
+                        const float go = s_go[q + t][ch];
+                        float b[4], c[4], v[8];
+                        to4(b, *reinterpret_cast<const float4 *>(s_bc + (q + t) * N + lane * kS));
+                        to4(c, *reinterpret_cast<const float4 *>(s_bc + (kTile + q + t) * N + lane * kS));
+                        ps[w] = pq[w] = 0.f;
+#pragma unroll
+                        for (int i = 0; i < kS; ++i) {
+                            const float gr = fmaf(go, c[i], carry[i]);
+                            carry[i] = gr * e[t][i];
+                            const float qq = carry[i] * hh[t][i];
+                            dA[i] = fmaf(dx.x, qq, dA[i]);
+                            pq[w] = fmaf(qq, A[i], pq[w]);
+                            ps[w] = fmaf(gr, b[i], ps[w]);
+                            v[i] = gr * dx.y;
+                            v[4 + i] = go * hh[t + 1][i];
+                        }
+                        // sums over the warp's channels: each lane ends with L / 4 of the 8 values
+                        int base = 0;
+                        if constexpr (L <= 16) {
+                            fold<8>(v, 16, tid & 16);
+                            base = tid & 16 ? 4 : 0;
+                        }
+                        if constexpr (L <= 8) {
+                            float v4[4] = {v[0], v[1], v[2], v[3]};
+                            fold<4>(v4, 8, tid & 8);
+                            base += tid & 8 ? 2 : 0;
+                            v[0] = v4[0];
+                            v[1] = v4[1];
+                        }
+                        if constexpr (L <= 4) {
+                            float v2[2] = {v[0], v[1]};
+                            fold<2>(v2, 4, tid & 4);
+                            base += tid & 4 ? 1 : 0;
+                            v[0] = v2[0];
+                        }
+#pragma unroll
+                        for (int j = 0; j < L / 4; ++j) {
+                            const int vi = base + j;
+                            s_red[(warp * kPiece + t) * 2 * N + (vi >> 2) * N + lane * kS + (vi & 3)] = v[j];
+                        }
+                    }
+                    const float s = sum4<L>(ps, lane), r = sum4<L>(pq, lane);
+                    if (lane < 4) {
+                        s_res[0][q + u + lane][ch] = s;
+                        s_res[1][q + u + lane][ch] = r;
+                    }
+                }
+                __syncthreads();
+                for (int i = tid; i < kPiece * 2 * N; i += kThreads) {
+                    const int t = k * kTile + q + i / (2 * N);
+                    if (t < len) {
+                        float sum = 0.f;
+#pragma unroll
+                        for (int w = 0; w < kWarps; ++w) sum += s_red[w * kPiece * 2 * N + i];
+                        s_acc[t * 2 * N + i % (2 * N)] += sum;
+                    }
+                }
+                __syncthreads();
+            }
+            if (at.t < kTile) {
+                float ox[4], od[4], oz[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float s = s_res[0][at.t][at.c + i], r = s_res[1][at.t][at.c + i];
+                    const float delta = s_dx[k * kTile + at.t][at.c + i].x, go = s_go[at.t][at.c + i];
+                    ox[i] = fmaf(delta, s, skip[i] * go);
+                    od[i] = fmaf(fx[i], s, r);
+                    if (p.softplus) od[i] *= sigmoid_f(fd[i] + bias[i]);
+                    if (p.z) oz[i] = fg[i] * (s_res[2][at.t][at.c + i] + skip[i] * fx[i]) * silu_grad_f(fz[i]);
+                    if (in && i < at.n) {
+                        sD[i] = fmaf(go, fx[i], sD[i]);
+                        sb[i] += od[i];
+                    }
+                }
+                store4<T, VEC>(p.dx, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, ox);
+                store4<T, VEC>(p.ddt, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, od);
+                if (p.z) store4<T, VEC>(p.dz, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, oz);
+            }
+            __syncthreads();  // s_res, s_go and s_bc are written again
+        }
+        if (own) *reinterpret_cast<float4 *>(p.gs + dn_at) = make_float4(dA[0], dA[1], dA[2], dA[3]);
+        if (at.t < kTile)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                s_res[0][at.t][at.c + i] = sD[i];
+                s_res[1][at.t][at.c + i] = sb[i];
+            }
+        __syncthreads();
+        for (int i = tid; i < 2 * cs.n; i += kThreads) {
+            const int which = i / cs.n, c = i - which * cs.n;
+            float s = 0.f;
+#pragma unroll
+            for (int t = 0; t < kTile; ++t) s += s_res[which][t][c];
+            p.vec[(slot * 2 + which) * p.D + cs.d0 + c] = s;
+        }
+        __syncthreads();
+    }
+    for (int i = tid; i < len * 2 * N; i += kThreads) {
+        const long long t = seq.t0 + i / (2 * N);
+        p.bc[(((long long)part * p.seq.tokens + t) * p.G + g) * 2 * N + i % (2 * N)] = s_acc[i];
+    }
+}
+
+// ---- 4: the parts' sums ------------------------------------------------------------------
+
+// One vector of four states of a token and group: d_Bm and d_Cm rows lie one
+// after the other in every part.
+template <typename T>
+__global__ void __launch_bounds__(128) scan_bwd_bc(ScanParams p, int parts) {
+    const long long i = (long long)blockIdx.x * 128 + threadIdx.x;
+    const int q = p.N / 2;  // vectors of a row of both
+    const long long row = i / q;
+    const int v = (int)(i - row * q);
+    long long tokens = p.seq.tokens;
+    if (p.seq.cu) {  // rows behind the last sequence stay as they are
+        const long long end = p.seq.cu[p.seq.N];
+        tokens = end < 0 ? 0 : end < tokens ? end : tokens;
+    }
+    if (row >= tokens * p.G) return;
+    const float4 *src = reinterpret_cast<const float4 *>(p.bc) + i;
+    const long long step = p.seq.tokens * p.G * q;
+    float4 s = src[0];
+    for (int k = 1; k < parts; ++k) {
+        const float4 o = src[k * step];
+        s.x += o.x; s.y += o.y; s.z += o.z; s.w += o.w;
+    }
+    Vec<T, 4> out;
+    out.v[0] = s.x; out.v[1] = s.y; out.v[2] = s.z; out.v[3] = s.w;
+    const bool c = v >= q / 2;
+    out.store(static_cast<T *>(c ? p.dCm : p.dBm) + row * p.N + (c ? v - q / 2 : v) * 4);
+}
+
+// d_A (blockIdx.y = 0: columns of D N), d_Dskip and d_dt_bias (1: columns of 2 D),
+// over the slots: 32 columns and 8 slices of the slots per block.
+__global__ void __launch_bounds__(256) scan_bwd_sums(ScanParams p, long long slots) {
+    __shared__ float red[8][32];
+    const long long cols = blockIdx.y ? 2LL * p.D : (long long)p.D * p.N;
+    const long long c = (long long)blockIdx.x * 32 + threadIdx.x;
+    if ((long long)blockIdx.x * 32 >= cols) return;
+    const float *src = blockIdx.y ? p.vec : p.gs;
+    float a = 0.f;
+    if (c < cols)
+        for (long long s = threadIdx.y; s < slots; s += 8) a += src[s * cols + c];
+    red[threadIdx.y][threadIdx.x] = a;
+    __syncthreads();
+    if (threadIdx.y || c >= cols) return;
+    float v = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v += red[k][threadIdx.x];
+    if (blockIdx.y == 0) p.dA[c] = v;
+    else if (c < p.D) {
+        if (p.dDskip) p.dDskip[c] = v;
+    } else if (p.ddt_bias) {
+        p.ddt_bias[c - p.D] = v;
+    }
+}
+
+// Parts that a group's channels are split into: enough blocks to fill the GPU, at
+// most one per tile of channels.
+int channel_parts(int n_seqs, long long tokens, int D, int G, int N) {
+    const int ch = kThreads / (N / kS);
+    const long long tiles = (D / G + ch - 1) / ch;
+    const long long rows = (tokens / kChunk + n_seqs) * G;
+    const long long want = rows > 0 ? (kSms * 8 + rows - 1) / rows : 1;
+    return (int)(want < tiles ? want : tiles);
+}
+
+template <typename T, int L, bool VEC>
+cudaError_t bwd_l(const ScanParams &p, cudaStream_t stream) {
+    constexpr int CH = kThreads / L;
+    const long long slots = tile_slots(p.seq, kChunk);
+    const int parts = channel_parts(p.seq.N, p.seq.tokens, p.D, p.G, p.N);
+    const long long states = slots * channel_tiles<CH>(p.D, p.G);
+    const long long blocks = slots * p.G * parts;
+    if (states > 0x7fffffffLL || blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    cudaError_t err = cudaSuccess;
+    if (slots > 0) {
+        scan_bwd_state<T, L, VEC><<<(unsigned)states, kThreads, 0, stream>>>(p);
+        err = scan_combine_launch(p, true, stream);
+        if (err != cudaSuccess) return err;
+        constexpr size_t bytes = Smem<L>::kAll * sizeof(float);
+        err = cudaFuncSetAttribute(scan_bwd<T, L, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        if (err != cudaSuccess) return err;
+        scan_bwd<T, L, VEC><<<(unsigned)blocks, kThreads, bytes, stream>>>(p, parts);
+    }
+    const long long vecs = p.seq.tokens * p.G * (p.N / 2);
+    if (vecs > 0 && p.seq.N > 0) {
+        const long long grid = (vecs + 127) / 128;
+        if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+        scan_bwd_bc<T><<<(unsigned)grid, 128, 0, stream>>>(p, parts);
+    }
+    const long long cols = ((long long)p.D * p.N + 31) / 32;
+    scan_bwd_sums<<<dim3((unsigned)cols, 2), dim3(32, 8), 0, stream>>>(p, slots);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t bwd_t(const ScanParams &p, cudaStream_t stream) {
+    const bool vec = (p.D / p.G) % 4 == 0;
+    switch (p.N) {
+        case 16: return vec ? bwd_l<T, 4, true>(p, stream) : bwd_l<T, 4, false>(p, stream);
+        case 32: return vec ? bwd_l<T, 8, true>(p, stream) : bwd_l<T, 8, false>(p, stream);
+        case 64: return vec ? bwd_l<T, 16, true>(p, stream) : bwd_l<T, 16, false>(p, stream);
+        default: return vec ? bwd_l<T, 32, true>(p, stream) : bwd_l<T, 32, false>(p, stream);
+    }
+}
+
+// The workspace's parts, in floats, each a multiple of 4.
+struct Sizes {
+    size_t hs, dsum, gs, vec, bc;
+    size_t all() const { return (hs + dsum + gs + vec + bc) * 4; }
+};
+Sizes sizes(int n_seqs, long long tokens, int D, int G, int N) {
+    const size_t slots = (size_t)(tokens / kChunk + n_seqs);
+    const size_t parts = (size_t)channel_parts(n_seqs, tokens, D, G, N);
+    auto up = [](size_t v) { return (v + 3) / 4 * 4; };
+    return {slots * D * N, up(slots * D), slots * D * N, up(slots * 2 * D), parts * (size_t)tokens * G * 2 * N};
+}
+
+}  // namespace
+
+size_t scan_bwd_workspace(int n_seqs, long long tokens, int D, int G, int N) {
+    const size_t b = sizes(n_seqs, tokens, D, G, N).all();
+    return b > 16 ? b : 16;
+}
+
+void scan_bwd_carve(ScanParams &p, void *workspace) {
+    const Sizes s = sizes(p.seq.N, p.seq.tokens, p.D, p.G, p.N);
+    p.chunk = kChunk;
+    p.hs = static_cast<float *>(workspace);
+    p.dsum = p.hs + s.hs;
+    p.gs = p.dsum + s.dsum;
+    p.vec = p.gs + s.gs;
+    p.bc = p.vec + s.vec;
+}
+
+cudaError_t scan_bwd_launch(ScanParams p, bool bf16, cudaStream_t stream, const char **name) {
+    *name = bf16 ? "scan_bwd_state+scan_combine+scan_bwd<bf16>" : "scan_bwd_state+scan_combine+scan_bwd<f32>";
+    return bf16 ? bwd_t<__nv_bfloat16>(p, stream) : bwd_t<float>(p, stream);
+}
+
+}  // namespace dn
