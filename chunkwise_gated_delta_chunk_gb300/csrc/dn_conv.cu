@@ -2,26 +2,37 @@
 //
 //     u_t[d] = bias[d] + sum_j weight[d, j] x_{t-(W-1)+j}[d],   y = u or silu(u)
 //
-// Forward.  One thread owns V neighbouring channels (16 bytes of a row) and
-// walks the tokens of one tile, the last W - 1 inputs in registers, so that
-// x is read once but for the W - 1 rows before each tile.
+// Forward.  One thread owns 4 neighbouring channels and walks the tokens of one
+// tile, the last W - 1 inputs in registers, so that x is read once but for the
+// W - 1 rows before each tile.  Two groups of 8 rows are in flight: with 8 channels
+// a thread, or one group of 4 rows, 33 to 60 % of the memory rate instead of 79.
 //
 // Backward, du = dy act'(u):
 //     dx_s = sum_i weight[W-1-i] du_{s+i},  dweight[j] = sum_t du_t x_{t-(W-1)+j},  dbias = sum_t du_t
-// One thread owns V channels and walks a tile and the W - 1 tokens behind it
-// (whose du reach back into the tile), the last W du in registers.  The sums
-// over tokens stay in registers over all tiles of a block, are joined over its
-// warps in shared memory and written as one row per block; a second kernel adds
-// the rows in a fixed order.
+// One thread owns 4 (bf16) or 2 (fp32) channels and walks a tile and the W - 1
+// tokens behind it (whose du reach back into the tile), the last W inputs and du in
+// registers.  About 45 instructions per channel and token bound it if written
+// plainly; pairs of channels in the two-wide fp32 instructions, rings of W registers
+// that turn whole within an unrolled group, and a separate path for tokens at a
+// tile's edges bring that to about 20.  Rows come by asynchronous copies into the
+// thread's own part of shared memory, so that they hold no registers.  The sums over
+// tokens stay in registers over all tiles of a block, are joined over its warps and
+// written as one row per block; a second kernel adds the rows in a fixed order.
 //
-// Both move 2 (forward) and 3 (backward) elements per channel and token for
-// about W products and one exponential each: they are bound by memory.
+// Both move 2 (forward) and 3 (backward) elements per channel and token for about
+// W products and one exponential each.  Measured (bf16, W = 4, silu, 6144 channels):
+// forward over 20741 packed tokens 94.6 us, 5.39 TB/s, bound by memory; backward over
+// 4 x 2048 tokens 78.6 us, 3.85 TB/s, bound by the rate of issue.
+#include <type_traits>
+
 #include "dn_layer.cuh"
 
 namespace dn {
 namespace {
 
 constexpr int kConvThreads = 128;
+constexpr int kFwdV = 4;      // channels of a thread where rows allow it
+constexpr int kFwdAhead = 8;  // tokens a thread loads before it computes the last such group
 
 // Tokens of a tile: long tiles read fewer rows twice, short ones give a small
 // call enough threads.
@@ -31,13 +42,30 @@ int conv_fwd_tile(const ConvParams &p, long long cols) {
     return 8;
 }
 
+// The taps of V channels: V W consecutive floats.
+template <int W, int V>
+__device__ __forceinline__ void load_taps(const float *weight, float (&w)[W][V]) {
+    if constexpr (V % 4 == 0) {
+        Vec<float, V * W> r;
+        r.load(weight);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int j = 0; j < W; ++j) w[j][i] = r.v[i * W + j];
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int j = 0; j < W; ++j) w[j][i] = weight[i * W + j];
+    }
+}
+
 template <typename T, int W, int V>
-__global__ void __launch_bounds__(kConvThreads) conv_fwd(ConvParams p, int len, int cols, long long slots) {
+__global__ void __launch_bounds__(kConvThreads) conv_fwd(ConvParams p, int len, int cols, unsigned nbx, unsigned slots) {
     if (blockIdx.x == 0) check_offsets(p.seq, threadIdx.y * blockDim.x + threadIdx.x, kConvThreads);
-    const long long nbx = (cols + blockDim.x - 1) / blockDim.x;
-    const long long by = blockIdx.x / nbx;
+    const unsigned by = blockIdx.x / nbx;
     const int col = (int)(blockIdx.x - by * nbx) * blockDim.x + threadIdx.x;
-    const long long slot = by * blockDim.y + threadIdx.y;
+    const unsigned slot = by * blockDim.y + threadIdx.y;
     if (col >= cols || slot >= slots) return;
     const SeqTile tile = seq_tile(p.seq, slot, len);
     if (!tile.ok) return;
@@ -46,57 +74,60 @@ __global__ void __launch_bounds__(kConvThreads) conv_fwd(ConvParams p, int len, 
     T *y = static_cast<T *>(p.y) + d0;
     const T *h0 = p.h0 ? static_cast<const T *>(p.h0) + (long long)tile.n * (W - 1) * p.D + d0 : nullptr;
 
-    float w[W][V], b[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-#pragma unroll
-        for (int j = 0; j < W; ++j) w[j][i] = p.weight[(long long)(d0 + i) * W + j];
-        b[i] = p.bias ? p.bias[d0 + i] : 0.f;
-    }
-    Vec<T, V> past[W - 1];  // inputs before the next token, the oldest first
+    Pack<T, V> past[W - 1];  // inputs before the next token, the oldest first
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
         const long long t = tile.t0 - (W - 1) + j;
+        past[j].clear();
         if (t >= tile.bos) past[j].load(x + t * p.D);
         else if (h0) past[j].load(h0 + (t - tile.bos + W - 1) * p.D);
-        else zero(past[j]);
     }
+    float w[W][V], b[V];
+    load_taps<W, V>(p.weight + (long long)d0 * W, w);
+#pragma unroll
+    for (int i = 0; i < V; ++i) b[i] = p.bias ? p.bias[d0 + i] : 0.f;
     if (tile.c == 0 && p.ht) {
         // the last W - 1 inputs of the sequence; rows of h0 are all read before
         // any is written (ht may be h0), by the one thread that owns them
-        Vec<T, V> last[W - 1];
+        T *ht = static_cast<T *>(p.ht) + (long long)tile.n * (W - 1) * p.D + d0;
         const long long n = tile.eos - tile.bos;
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
             const long long r = n + j;  // row of (h0, x) put together
+            Pack<T, V> last;
+            last.clear();
             if (r >= W - 1) {
-                last[j].load(x + (tile.bos + r - (W - 1)) * p.D);
+                last.load(x + (tile.bos + r - (W - 1)) * p.D);
             } else {
-                zero(last[j]);
 #pragma unroll
                 for (int i = 0; i < W - 1; ++i)  // the tile begins where the sequence does: past is h0
-                    if (i == r) last[j] = past[i];
+                    if (i == r) last = past[i];
             }
+            last.store(ht + (long long)j * p.D);
         }
-        T *ht = static_cast<T *>(p.ht) + (long long)tile.n * (W - 1) * p.D + d0;
-#pragma unroll
-        for (int j = 0; j < W - 1; ++j) last[j].store(ht + (long long)j * p.D);
     }
-    constexpr int U = 4;  // tokens loaded ahead
-    for (long long t = tile.t0; t < tile.t1; t += U) {
-        Vec<T, V> in[U];
+    constexpr int U = kFwdAhead;
+    Pack<T, V> next[U];
 #pragma unroll
-        for (int k = 0; k < U; ++k)
-            if (t + k < tile.t1) in[k].load(x + (t + k) * p.D);
+    for (int k = 0; k < U; ++k)
+        if (tile.t0 + k < tile.t1) next[k].load(x + (tile.t0 + k) * p.D);
+    for (long long t = tile.t0; t < tile.t1; t += U) {
+        Pack<T, V> in[U];
+        const int n = tile.t1 - t < U ? (int)(tile.t1 - t) : U;
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-            if (t + k >= tile.t1) break;
+            in[k] = next[k];
+            if (t + U + k < tile.t1) next[k].load(x + (t + U + k) * p.D);
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            if (k >= n) break;
             Vec<T, V> out;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                float u = fmaf(w[W - 1][i], in[k].v[i], b[i]);
+                float u = fmaf(w[W - 1][i], in[k][i], b[i]);
 #pragma unroll
-                for (int j = 0; j < W - 1; ++j) u = fmaf(w[j][i], past[j].v[i], u);
+                for (int j = 0; j < W - 1; ++j) u = fmaf(w[j][i], past[j][i], u);
                 out.v[i] = p.silu ? silu_f(u) : u;
             }
             out.store(y + (t + k) * p.D);
@@ -115,16 +146,15 @@ cudaError_t conv_fwd_v(const ConvParams &p, cudaStream_t stream) {
     int tx = 8;
     while (tx < kConvThreads && tx < cols) tx <<= 1;
     const int ty = kConvThreads / tx;
-    const long long grid = ((cols + tx - 1) / tx) * ((slots + ty - 1) / ty);
-    if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-    conv_fwd<T, W, V><<<(unsigned)grid, dim3(tx, ty), 0, stream>>>(p, len, cols, slots);
+    const long long nbx = (cols + tx - 1) / tx, grid = nbx * ((slots + ty - 1) / ty);
+    if (grid > 0x7fffffffLL || slots > 0xffffffffLL) return cudaErrorInvalidValue;
+    conv_fwd<T, W, V><<<(unsigned)grid, dim3(tx, ty), 0, stream>>>(p, len, cols, (unsigned)nbx, (unsigned)slots);
     return cudaGetLastError();
 }
 
 template <typename T, int W>
 cudaError_t conv_fwd_w(const ConvParams &p, cudaStream_t stream) {
-    constexpr int V = 16 / sizeof(T);
-    // a row begins on 16 bytes where D fills whole vectors
+    constexpr int V = kFwdV;
     return p.D % V == 0 ? conv_fwd_v<T, W, V>(p, stream) : conv_fwd_v<T, W, 1>(p, stream);
 }
 
@@ -139,120 +169,257 @@ cudaError_t conv_fwd_t(const ConvParams &p, cudaStream_t stream) {
 
 // ---- backward ------------------------------------------------------------------
 
-constexpr int kBwdWarps = 8;
-constexpr int kBwdV = 4;     // channels of a thread where rows allow it
-constexpr int kBwdTile = 32;
+constexpr int kBwdWarps = 4;
+constexpr int kBwdThreads = kBwdWarps * 32;
+constexpr int kBwdTile = 64;
+constexpr int kGroups = 2;  // groups of tokens in flight (3 and 4 measured 2 % slower)
+
+// Channels of a thread where rows allow it.
+template <typename T>
+constexpr int kBwdV = 8 / (int)sizeof(T);
 
 // Blocks along the tokens: every one writes a row of partial sums, so no more
-// than fill the GPU a few times, and no more than there are tiles for their warps.
-// `slots` is taken from the sizes alone (an upper bound of the tiles), so that the
+// than the GPU holds at once, and each walks the same number of tiles.
+// The tiles are counted from the sizes alone (an upper bound), so that the
 // workspace is known without the offsets.
-int conv_bwd_rows(long long tokens, int n_seqs, int D) {
-    const long long cols = (D + 32 * kBwdV - 1) / (32 * kBwdV);
+int conv_bwd_rows(long long tokens, int n_seqs, int D, int V) {
+    const long long cols = (D + 32 * V - 1) / (32 * V);
     const long long slots = tokens / kBwdTile + n_seqs;
     const long long most = (slots + kBwdWarps - 1) / kBwdWarps;
-    const long long fill = (kSms * 6 + cols - 1) / cols;
-    const long long rows = most < fill ? most : fill;
-    return rows < 1 ? 1 : (int)rows;
+    if (most <= 1) return 1;
+    const long long fill = (kSms * 4 + cols - 1) / cols;
+    const long long each = (most + fill - 1) / fill;
+    return (int)((most + each - 1) / each);
 }
 
+// The rows of x and dy that a thread walks, V elements of each token, fetched
+// kGroups groups of K tokens ahead.  The copies go to shared memory
+// asynchronously; a thread reads only what it copied itself, so that no barrier
+// is needed.  (One 16-bit element is too small for such a copy: it is loaded a
+// group ahead into registers.)
+template <typename T, typename Tg, int V, int K>
+struct Feed {
+    static constexpr bool kAsync = sizeof(T) * V >= 4;
+    static constexpr int kAhead = kAsync ? kGroups : 1;
+    static constexpr int kX = kAsync ? (int)sizeof(T) * V : 0, kG = kAsync ? (int)sizeof(Tg) * V : 0;
+    static constexpr int kStage = K * kBwdThreads * (kX + kG);
+    static constexpr int kBytes = kAsync ? kAhead * kStage : 16;
+    Pack<T, V> now[kAsync ? 1 : K];
+    Pack<Tg, V> grad[kAsync ? 1 : K];
+    const char *ring;   // this thread's first bytes of x; those of dy lie kBwdThreads kX behind them
+    const T *xp;        // the next token to fetch
+    const Tg *gp;
+    int left;           // tokens not fetched yet (or less than none)
+
+    template <int B>
+    static __device__ __forceinline__ void copy(unsigned dst, const void *src) {
+        if constexpr (B == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src));
+        else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(B));
+    }
+    __device__ __forceinline__ int at_g(int s, int k) const {
+        return s * kStage + k * kBwdThreads * (kX + kG) + kBwdThreads * kX + threadIdx.x * (kG - kX);
+    }
+    __device__ __forceinline__ void issue(int s, long long D) {
+        const bool full = left >= K;
+        if constexpr (kAsync) {
+            const unsigned dst = (unsigned)__cvta_generic_to_shared(ring) + s * kStage;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                // what is not fetched keeps what lay there: no result depends on it
+                if (!full && k >= left) continue;
+                copy<kX>(dst + k * kBwdThreads * (kX + kG), xp + k * D);
+                copy<kG>((unsigned)__cvta_generic_to_shared(ring) + at_g(s, k), gp + k * D);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        } else {
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                now[k].clear();
+                grad[k].clear();
+                if (full || k < left) {
+                    now[k].load(xp + k * D);
+                    grad[k].load(gp + k * D);
+                }
+            }
+        }
+        left -= K;
+        xp += K * D;
+        gp += K * D;
+    }
+    __device__ __forceinline__ void start(const char *r, const T *x, const Tg *g, int n, long long D) {
+        ring = r + threadIdx.x * kX;
+        xp = x;
+        gp = g;
+        left = n;
+#pragma unroll
+        for (int s = 0; s < kAhead; ++s) issue(s, D);
+    }
+    // waits for the oldest of the groups in flight
+    __device__ __forceinline__ void wait() {
+        if constexpr (kAsync) asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+    }
+    __device__ __forceinline__ Pack<T, V> x(int s, int k) const {
+        if constexpr (!kAsync) return now[k];
+        Pack<T, V> r;
+        r.load(reinterpret_cast<const T *>(ring + s * kStage + k * kBwdThreads * (kX + kG)));
+        return r;
+    }
+    __device__ __forceinline__ Pack<Tg, V> g(int s, int k) const {
+        if constexpr (!kAsync) return grad[k];
+        Pack<Tg, V> r;
+        r.load(reinterpret_cast<const Tg *>(ring + at_g(s, k)));
+        return r;
+    }
+};
+
+// The channels of a thread as pairs: V / 2 of them, or one whose upper half is
+// never stored.
+template <int V>
+struct Pairs {
+    static constexpr int P = (V + 1) / 2;
+    f2 v[P];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < P; ++i) v[i] = 0ull;
+    }
+    template <typename T>
+    __device__ __forceinline__ void from(const Pack<T, V> &a) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) v[i] = pair(a[2 * i], V > 1 ? a[V > 1 ? 2 * i + 1 : 0] : 0.f);
+    }
+    __device__ __forceinline__ void to(float (&a)[V]) const {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            float lo, hi;
+            split(v[i], lo, hi);
+            a[2 * i] = lo;
+            if constexpr (V > 1) a[2 * i + 1] = hi;
+        }
+    }
+};
+
 template <typename T, typename Tg, int W, int V>
-__global__ void __launch_bounds__(kBwdWarps * 32) conv_bwd(ConvParams p, int cols, long long slots) {
-    if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(p.seq, threadIdx.x, kBwdWarps * 32);
+__global__ void __launch_bounds__(kBwdThreads) conv_bwd(ConvParams p, int cols, unsigned slots) {
+    if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(p.seq, threadIdx.x, kBwdThreads);
+    constexpr int P = Pairs<V>::P;
+    constexpr int K = W == 3 ? 3 : 4;  // tokens of a group: a multiple of W, so that rings of W turn whole
+    using F = Feed<T, Tg, V, K>;
+    __shared__ __align__(16) char ring[F::kBytes];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col = blockIdx.x * 32 + lane;
     const int d0 = col * V;
     const bool own = col < cols;
+    const long long D = p.D;
 
-    float w[W][V], b[V];
-    float sw[W][V], sb[V];  // sums over this thread's tokens
+    Pairs<V> w[W], b, sw[W], sb;  // sw, sb: sums over this thread's tokens
+    {
+        float f[W][V];
+        if (own) load_taps<W, V>(p.weight + (long long)d0 * W, f);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
+        for (int i = 0; i < P; ++i) {
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-            w[j][i] = own ? p.weight[(long long)(d0 + i) * W + j] : 0.f;
-            sw[j][i] = 0.f;
+            for (int j = 0; j < W; ++j) w[j].v[i] = pair(f[j][2 * i], V > 1 ? f[j][V > 1 ? 2 * i + 1 : 0] : 0.f);
+            b.v[i] = pair(own && p.bias ? p.bias[d0 + 2 * i] : 0.f, V > 1 && own && p.bias ? p.bias[d0 + 2 * i + 1] : 0.f);
         }
-        b[i] = own && p.bias ? p.bias[d0 + i] : 0.f;
-        sb[i] = 0.f;
+        sb.clear();
+#pragma unroll
+        for (int j = 0; j < W; ++j) sw[j].clear();
     }
-    const long long stride = (long long)gridDim.y * kBwdWarps;
-    for (long long slot = (long long)blockIdx.y * kBwdWarps + warp; own && slot < slots; slot += stride) {
+    const T *x = static_cast<const T *>(p.x) + d0;
+    const Tg *dy = static_cast<const Tg *>(p.dy) + d0;
+    T *dx = static_cast<T *>(p.dx) + d0;
+    for (unsigned slot = blockIdx.y * kBwdWarps + warp; own && slot < slots; slot += gridDim.y * kBwdWarps) {
         const SeqTile tile = seq_tile(p.seq, slot, kBwdTile);
         if (!tile.ok) continue;
-        const T *x = static_cast<const T *>(p.x) + d0;
-        const Tg *dy = static_cast<const Tg *>(p.dy) + d0;
-        T *dx = static_cast<T *>(p.dx) + d0;
-        const long long state = (long long)tile.n * (W - 1) * p.D + d0;
+        const long long state = (long long)tile.n * (W - 1) * D + d0;
         const T *h0 = p.h0 ? static_cast<const T *>(p.h0) + state : nullptr;
         const T *dht = p.dht ? static_cast<const T *>(p.dht) + state : nullptr;
+        T *dh0 = p.dh0 && tile.c == 0 ? static_cast<T *>(p.dh0) + state : nullptr;
 
-        Vec<T, V> past[W - 1];
+        // Token t of the tile completes the gradient of input t - (W - 1): a row of the
+        // tile, or of h0 in front of a sequence's first tile.  Behind the sequence du is 0.
+        const int own_n = (int)(tile.t1 - tile.t0), all_n = own_n + W - 1;
+        const long long left = tile.eos - tile.t0;
+        const int in_n = left < all_n ? (int)left : all_n;
+        const int first = dh0 ? -(W - 1) : 0;  // first row of the tile that is written
+        const int tail = !dht ? all_n : left - (W - 1) < all_n ? (int)(left - (W - 1)) : all_n;  // row that ht begins with
+        F feed;
+        feed.start(ring, x + tile.t0 * D, dy + tile.t0 * D, in_n, D);
+        T *op = dx + tile.t0 * D;  // the next row to write
+        Pairs<V> xs[W], du[W];     // token t at t % W
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
             const long long t = tile.t0 - (W - 1) + j;
-            if (t >= tile.bos) past[j].load(x + t * p.D);
-            else if (h0) past[j].load(h0 + (t - tile.bos + W - 1) * p.D);
-            else zero(past[j]);
+            Pack<T, V> r;
+            r.clear();
+            if (t >= tile.bos) r.load(x + t * D);
+            else if (h0) r.load(h0 + (t - tile.bos + W - 1) * D);
+            xs[j + 1].from(r);
         }
-        float du[W][V];  // du of the last W tokens, the newest last
 #pragma unroll
-        for (int j = 0; j < W; ++j)
-#pragma unroll
-            for (int i = 0; i < V; ++i) du[j][i] = 0.f;
-        // Token t completes the gradient of input t - (W - 1): a row of the tile, or
-        // of h0 in front of a sequence's first tile.  Behind the sequence du is zero.
-        for (long long t = tile.t0; t < tile.t1 + (W - 1); ++t) {
-            const bool in = t < tile.eos;
-            Vec<T, V> now;
-            Vec<Tg, V> grad;
-            zero(now);
-            zero(grad);
-            if (in) {
-                now.load(x + t * p.D);
-                grad.load(dy + t * p.D);
-            }
-            const bool mine = t < tile.t1;  // its sums are this tile's
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-#pragma unroll
-                for (int j = 0; j + 1 < W; ++j) du[j][i] = du[j + 1][i];
-                float u = fmaf(w[W - 1][i], now.v[i], b[i]);
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j) u = fmaf(w[j][i], past[j].v[i], u);
-                const float d = !in ? 0.f : p.silu ? grad.v[i] * silu_grad_f(u) : grad.v[i];
-                du[W - 1][i] = d;
-                if (mine) {
-                    sb[i] += d;
-#pragma unroll
-                    for (int j = 0; j < W - 1; ++j) sw[j][i] = fmaf(d, past[j].v[i], sw[j][i]);
-                    sw[W - 1][i] = fmaf(d, now.v[i], sw[W - 1][i]);
-                }
-            }
-#pragma unroll
-            for (int j = 0; j + 1 < W - 1; ++j) past[j] = past[j + 1];
-            past[W - 2] = now;
+        for (int j = 0; j < W; ++j) du[j].clear();
 
-            const long long s = t - (W - 1);
-            if (s >= tile.t0 || (tile.c == 0 && p.dh0)) {
-                Vec<T, V> out;
+        // one token; EDGE: it may lie behind the tile, and its row in front of it or in ht
+        auto token = [&](auto edge, int t, int k, int stage) {
+            constexpr bool EDGE = decltype(edge)::value;
+            Pairs<V> gs, sum;
+            xs[k % W].from(feed.x(stage, k));
+            gs.from(feed.g(stage, k));
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    float a = 0.f;
+            for (int i = 0; i < P; ++i) {
+                f2 d = gs.v[i];
+                if (p.silu) {
+                    f2 u = fma2(w[W - 1].v[i], xs[k % W].v[i], b.v[i]);
 #pragma unroll
-                    for (int j = 0; j < W; ++j) a = fmaf(w[W - 1 - j][i], du[j][i], a);
-                    out.v[i] = a;
+                    for (int j = 0; j < W - 1; ++j) u = fma2(w[j].v[i], xs[(k + 1 + j) % W].v[i], u);
+                    float u0, u1;
+                    split(u, u0, u1);
+                    // s (1 + u (1 - s)) with s of both halves
+                    const f2 s = pair(sigmoid_f(u0), sigmoid_f(u1));
+                    const f2 one = pair(1.f, 1.f), m = fma2(s, pair(-1.f, -1.f), one);
+                    d = mul2(d, mul2(s, fma2(u, m, one)));
                 }
-                const long long r = s - (tile.eos - (W - 1));  // row of ht that holds this input
-                if (dht && r >= 0) {
-                    Vec<T, V> add;
-                    add.load(dht + r * p.D);
+                if (EDGE && t >= in_n) d = 0ull;
+                du[k % W].v[i] = d;
+                if (!EDGE || t < own_n) {  // its sums are this tile's
+                    sb.v[i] = add2(sb.v[i], d);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) out.v[i] += add.v[i];
+                    for (int j = 0; j < W; ++j) sw[j].v[i] = fma2(d, xs[(k + 1 + j) % W].v[i], sw[j].v[i]);
                 }
-                if (s >= tile.t0) out.store(dx + s * p.D);
-                else out.store(static_cast<T *>(p.dh0) + state + (s - tile.bos + W - 1) * p.D);
+                sum.v[i] = mul2(w[W - 1].v[i], du[(k + 1) % W].v[i]);
+#pragma unroll
+                for (int j = 1; j < W; ++j) sum.v[i] = fma2(w[W - 1 - j].v[i], du[(k + 1 + j) % W].v[i], sum.v[i]);
             }
+            const int s = t - (W - 1);
+            if (EDGE && s < first) return;
+            Vec<T, V> out;
+            sum.to(out.v);
+            if (EDGE && s >= tail) {
+                Pack<T, V> add;
+                add.load(dht + (s - (left - (W - 1))) * D);
+#pragma unroll
+                for (int i = 0; i < V; ++i) out.v[i] += add[i];
+            }
+            if (EDGE && s < 0) {
+                out.store(dh0 + (long long)(s + W - 1) * D);
+            } else {
+                out.store(op);
+                op += D;
+            }
+        };
+        int stage = 0;
+        for (int t = 0; t < all_n; t += K) {
+            feed.wait();
+            if (t >= W - 1 && t + K <= own_n && t + K - (W - 1) <= tail) {
+#pragma unroll
+                for (int k = 0; k < K; ++k) token(std::false_type{}, t + k, k, stage);
+            } else {
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+                    if (t + k < all_n) token(std::true_type{}, t + k, k, stage);
+            }
+            feed.issue(stage, D);
+            stage = stage + 1 == F::kAhead ? 0 : stage + 1;
         }
     }
     // join the warps, tap by tap
@@ -260,10 +427,12 @@ __global__ void __launch_bounds__(kBwdWarps * 32) conv_bwd(ConvParams p, int col
 #pragma unroll
     for (int j = 0; j <= W; ++j) {
         __syncthreads();
+        float mine[V];
+        (j < W ? sw[j < W ? j : 0] : sb).to(mine);
 #pragma unroll
-        for (int i = 0; i < V; ++i) red[warp][lane * V + i] = j < W ? sw[j < W ? j : 0][i] : sb[i];
+        for (int i = 0; i < V; ++i) red[warp][lane * V + i] = mine[i];
         __syncthreads();
-        for (int i = threadIdx.x; i < 32 * V; i += kBwdWarps * 32) {
+        for (int i = threadIdx.x; i < 32 * V; i += kBwdThreads) {
             const int d = blockIdx.x * 32 * V + i;
             if (d < p.D) {
                 float a = 0.f;
@@ -288,9 +457,11 @@ __global__ void __launch_bounds__(128) conv_bwd_sums(ConvParams p, int rows) {
 template <typename T, typename Tg, int W, int V>
 cudaError_t conv_bwd_v(const ConvParams &p, cudaStream_t stream) {
     const int cols = p.D / V;
-    const int rows = conv_bwd_rows(p.seq.tokens, p.seq.N, p.D);
+    const int rows = conv_bwd_rows(p.seq.tokens, p.seq.N, p.D, kBwdV<T>);
     const dim3 grid((cols + 31) / 32, rows);
-    conv_bwd<T, Tg, W, V><<<grid, kBwdWarps * 32, 0, stream>>>(p, cols, tile_slots(p.seq, kBwdTile));
+    const long long slots = tile_slots(p.seq, kBwdTile);
+    if (slots > 0x7fffffffLL) return cudaErrorInvalidValue;
+    conv_bwd<T, Tg, W, V><<<grid, kBwdThreads, 0, stream>>>(p, cols, (unsigned)slots);
     const long long n = (long long)(W + 1) * p.D;
     conv_bwd_sums<<<(unsigned)((n + 127) / 128), 128, 0, stream>>>(p, rows);
     return cudaGetLastError();
@@ -298,11 +469,12 @@ cudaError_t conv_bwd_v(const ConvParams &p, cudaStream_t stream) {
 
 template <typename T, typename Tg>
 cudaError_t conv_bwd_t(const ConvParams &p, cudaStream_t stream) {
-    const bool vec = p.D % kBwdV == 0;
+    constexpr int V = kBwdV<T>;
+    const bool vec = p.D % V == 0;
     switch (p.W) {
-        case 2: return vec ? conv_bwd_v<T, Tg, 2, kBwdV>(p, stream) : conv_bwd_v<T, Tg, 2, 1>(p, stream);
-        case 3: return vec ? conv_bwd_v<T, Tg, 3, kBwdV>(p, stream) : conv_bwd_v<T, Tg, 3, 1>(p, stream);
-        default: return vec ? conv_bwd_v<T, Tg, 4, kBwdV>(p, stream) : conv_bwd_v<T, Tg, 4, 1>(p, stream);
+        case 2: return vec ? conv_bwd_v<T, Tg, 2, V>(p, stream) : conv_bwd_v<T, Tg, 2, 1>(p, stream);
+        case 3: return vec ? conv_bwd_v<T, Tg, 3, V>(p, stream) : conv_bwd_v<T, Tg, 3, 1>(p, stream);
+        default: return vec ? conv_bwd_v<T, Tg, 4, V>(p, stream) : conv_bwd_v<T, Tg, 4, 1>(p, stream);
     }
 }
 
@@ -313,8 +485,9 @@ cudaError_t conv_fwd_launch(const ConvParams &p, bool bf16, cudaStream_t stream,
     return bf16 ? conv_fwd_t<__nv_bfloat16>(p, stream) : conv_fwd_t<float>(p, stream);
 }
 
-size_t conv_bwd_workspace(long long tokens, int n_seqs, int D, int W) {
-    return (size_t)conv_bwd_rows(tokens, n_seqs, D) * (size_t)(W + 1) * (size_t)D * 4u;
+size_t conv_bwd_workspace(long long tokens, int n_seqs, int D, int W, bool bf16) {
+    const int V = bf16 ? kBwdV<__nv_bfloat16> : kBwdV<float>;
+    return (size_t)conv_bwd_rows(tokens, n_seqs, D, V) * (size_t)(W + 1) * (size_t)D * 4u;
 }
 
 cudaError_t conv_bwd_launch(const ConvParams &p, bool bf16, cudaStream_t stream, const char **name) {

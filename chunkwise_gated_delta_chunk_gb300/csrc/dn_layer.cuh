@@ -19,6 +19,9 @@ struct Vec<float, V> {
     __device__ __forceinline__ void load(const float *p) {
         if constexpr (V == 1) {
             v[0] = *p;
+        } else if constexpr (V == 2) {
+            const float2 r = *reinterpret_cast<const float2 *>(p);
+            v[0] = r.x; v[1] = r.y;
         } else {
 #pragma unroll
             for (int i = 0; i < V; i += 4) {
@@ -30,6 +33,8 @@ struct Vec<float, V> {
     __device__ __forceinline__ void store(float *p) const {
         if constexpr (V == 1) {
             *p = v[0];
+        } else if constexpr (V == 2) {
+            *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]);
         } else {
 #pragma unroll
             for (int i = 0; i < V; i += 4)
@@ -85,6 +90,53 @@ struct Vec<__nv_bfloat16, V> {
     }
 };
 
+// The same V elements as they lie in memory: what a load in flight holds (half
+// the registers of Vec for bf16).
+template <typename T, int V>
+struct Pack {
+    static constexpr int kWords = V * (int)sizeof(T) / 4 > 0 ? V * (int)sizeof(T) / 4 : 1;
+    unsigned w[kWords];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0u;
+    }
+    __device__ __forceinline__ void load(const T *p) {
+        if constexpr (sizeof(T) * V == 2) {
+            w[0] = *reinterpret_cast<const unsigned short *>(p);
+        } else if constexpr (kWords == 1) {
+            w[0] = *reinterpret_cast<const unsigned *>(p);
+        } else if constexpr (kWords == 2) {
+            const uint2 r = *reinterpret_cast<const uint2 *>(p);
+            w[0] = r.x; w[1] = r.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords; i += 4) {
+                const uint4 r = reinterpret_cast<const uint4 *>(p)[i / 4];
+                w[i] = r.x; w[i + 1] = r.y; w[i + 2] = r.z; w[i + 3] = r.w;
+            }
+        }
+    }
+    __device__ __forceinline__ void store(T *p) const {
+        if constexpr (sizeof(T) * V == 2) {
+            *reinterpret_cast<unsigned short *>(p) = (unsigned short)w[0];
+        } else if constexpr (kWords == 1) {
+            *reinterpret_cast<unsigned *>(p) = w[0];
+        } else if constexpr (kWords == 2) {
+            *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords; i += 4)
+                reinterpret_cast<uint4 *>(p)[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+        }
+    }
+    __device__ __forceinline__ float operator[](int i) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        else return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+    }
+};
+
+
+
 template <typename T, int V>
 __device__ __forceinline__ void zero(Vec<T, V> &a) {
 #pragma unroll
@@ -102,15 +154,16 @@ struct SeqTile {
     bool ok;
 };
 
-__device__ __forceinline__ SeqTile seq_tile(const SeqView &s, long long slot, int len) {
+__device__ __forceinline__ SeqTile seq_tile(const SeqView &s, unsigned slot, int len) {
     SeqTile r;
     if (!s.cu) {
-        const long long per = s.T > 0 ? ((long long)s.T + len - 1) / len : 1;
-        r.n = (int)(slot / per);
-        r.c = (int)(slot - r.n * per);
+        const unsigned per = s.T > 0 ? ((unsigned)s.T + len - 1) / len : 1;
+        const unsigned n = slot / per;
+        r.n = (int)n;
+        r.c = (int)(slot - n * per);
         r.bos = (long long)r.n * s.T;
         r.eos = r.bos + s.T;
-        r.ok = r.n < s.N;
+        r.ok = n < (unsigned)s.N;
     } else {
         int lo = 0, hi = s.N - 1;  // the last sequence whose first slot is not behind this one
         while (lo < hi) {
@@ -122,7 +175,7 @@ __device__ __forceinline__ SeqTile seq_tile(const SeqView &s, long long slot, in
         r.bos = s.cu[lo];
         r.eos = s.cu[lo + 1];
         r.ok = r.bos >= 0 && r.eos >= r.bos && r.eos <= s.tokens;
-        const long long c = slot - (r.bos / len + lo);
+        const long long c = (long long)slot - (r.bos / len + lo);
         r.ok = r.ok && c >= 0 && (c == 0 || r.bos + c * len < r.eos);
         r.c = r.ok ? (int)c : 0;
     }
@@ -153,14 +206,54 @@ __device__ __forceinline__ void check_offsets(const SeqView &s, int thread, int 
     if (bad) atomicOr(s.status, kStatusBadSeq);
 }
 
-// 1 / (1 + e^-u): __expf and __fdividef are within a few units of fp32's last
-// place here, far below the rounding of a bf16 result.
-__device__ __forceinline__ float sigmoid_f(float u) { return __fdividef(1.f, 1.f + __expf(-u)); }
-__device__ __forceinline__ float silu_f(float u) { return __fdividef(u, 1.f + __expf(-u)); }
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 1 / (1 + e^-u), from the two approximate instructions (each within two units
+// of fp32's last place; the exponent's rounding adds |u| 2^-24 of the value).
+__device__ __forceinline__ float sigmoid_f(float u) { return rcp(1.f + ex2(-kLog2e * u)); }
+__device__ __forceinline__ float silu_f(float u) { return u * sigmoid_f(u); }
 // d silu(u) / du = s (1 + u (1 - s)), s = sigmoid(u)
 __device__ __forceinline__ float silu_grad_f(float u) {
     const float s = sigmoid_f(u);
     return s * fmaf(u, 1.f - s, 1.f);
+}
+
+// Two fp32 values in one register pair, and the instructions that work on both
+// (the rate of issue is what bounds most of these kernels beside memory).
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pair(float lo, float hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void split(f2 v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 }  // namespace dn

@@ -52,7 +52,7 @@ struct ConvParams {
 };
 cudaError_t conv_fwd_launch(const ConvParams &p, bool bf16, cudaStream_t stream, const char **name);
 cudaError_t conv_bwd_launch(const ConvParams &p, bool bf16, cudaStream_t stream, const char **name);
-size_t conv_bwd_workspace(long long tokens, int n_seqs, int D, int W);
+size_t conv_bwd_workspace(long long tokens, int n_seqs, int D, int W, bool bf16);
 
 struct ScanParams {
     SeqView seq;

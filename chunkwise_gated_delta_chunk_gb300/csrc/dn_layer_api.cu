@@ -77,7 +77,7 @@ DN_EXPORT dn_status dn_causal_conv_fwd(const void *x, const float *weight, const
 
 DN_EXPORT size_t dn_causal_conv_bwd_workspace_bytes(int n_seqs, int B, int T, int D, int W, dn_dtype dtype) {
     if (n_seqs < 0 || B < 0 || T < 0 || D <= 0 || !conv_width_ok(W) || !dtype_ok(dtype)) return 0;
-    return dn::conv_bwd_workspace((long long)B * T, n_seqs, D, W);
+    return dn::conv_bwd_workspace((long long)B * T, n_seqs, D, W, dtype == DN_BF16);
 }
 
 DN_EXPORT dn_status dn_causal_conv_bwd(const void *x, const float *weight, const float *bias, const void *h0,
@@ -92,7 +92,7 @@ DN_EXPORT dn_status dn_causal_conv_bwd(const void *x, const float *weight, const
     if (!all_aligned(ptrs) || !d_weight) return DN_ERR_INVALID_ARG;
     if ((long long)B * T > 0 && (!d_y || !d_x)) return DN_ERR_INVALID_ARG;
     if (!conv_width_ok(W)) return DN_ERR_UNSUPPORTED;
-    const size_t need = dn::conv_bwd_workspace((long long)B * T, n_seqs, D, W);
+    const size_t need = dn::conv_bwd_workspace((long long)B * T, n_seqs, D, W, dtype == DN_BF16);
     if (!workspace || !aligned16(workspace) || workspace_bytes < need) return DN_ERR_INVALID_ARG;
     dn::ConvParams p{};
     if (seq_view(p.seq, cu_seqlens, n_seqs, B, T) != cudaSuccess) return DN_ERR_CUDA;

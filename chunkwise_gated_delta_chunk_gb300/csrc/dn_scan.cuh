@@ -12,13 +12,6 @@ namespace dn {
 namespace scan {
 
 constexpr int kS = 4;  // states of a thread
-constexpr float kLog2e = 1.4426950408889634f;
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 // log(1 + e^v) without loss on either side: for v << 0 it is e^v.
 __device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))); }
