@@ -213,8 +213,8 @@ struct Feed {
 
     template <int B>
     static __device__ __forceinline__ void copy(unsigned dst, const void *src) {
-        if constexpr (B == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src));
-        else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(B));
+        if constexpr (B == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+        else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(B) : "memory");
     }
     __device__ __forceinline__ int at_g(int s, int k) const {
         return s * kStage + k * kBwdThreads * (kX + kG) + kBwdThreads * kX + threadIdx.x * (kG - kX);

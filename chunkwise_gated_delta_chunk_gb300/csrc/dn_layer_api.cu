@@ -35,6 +35,9 @@ cudaError_t seq_view(dn::SeqView &s, const int64_t *cu, int n_seqs, int B, int T
     return dn::status_ptr(&s.status);
 }
 
+// Tokens of a sequence that the kernels count in 32 bits, with room for a tile.
+constexpr int kMaxT = 1 << 30;
+
 dn_status done(cudaError_t err, const char *name) {
     if (err != cudaSuccess) return DN_ERR_CUDA;
     dn::set_last_kernel(name);
@@ -64,7 +67,7 @@ DN_EXPORT dn_status dn_causal_conv_fwd(const void *x, const float *weight, const
     if (st != DN_OK) return st;
     const void *ptrs[] = {y, ht};
     if (!all_aligned(ptrs) || ((long long)B * T > 0 && !y)) return DN_ERR_INVALID_ARG;
-    if (!conv_width_ok(W)) return DN_ERR_UNSUPPORTED;
+    if (!conv_width_ok(W) || T > kMaxT) return DN_ERR_UNSUPPORTED;
     if (n_seqs == 0) return DN_OK;
     dn::ConvParams p{};
     if (seq_view(p.seq, cu_seqlens, n_seqs, B, T) != cudaSuccess) return DN_ERR_CUDA;
@@ -76,7 +79,7 @@ DN_EXPORT dn_status dn_causal_conv_fwd(const void *x, const float *weight, const
 }
 
 DN_EXPORT size_t dn_causal_conv_bwd_workspace_bytes(int n_seqs, int B, int T, int D, int W, dn_dtype dtype) {
-    if (n_seqs < 0 || B < 0 || T < 0 || D <= 0 || !conv_width_ok(W) || !dtype_ok(dtype)) return 0;
+    if (n_seqs < 0 || B < 0 || T < 0 || D <= 0 || !conv_width_ok(W) || T > kMaxT || !dtype_ok(dtype)) return 0;
     return dn::conv_bwd_workspace((long long)B * T, n_seqs, D, W, dtype == DN_BF16);
 }
 
@@ -91,7 +94,7 @@ DN_EXPORT dn_status dn_causal_conv_bwd(const void *x, const float *weight, const
     const void *ptrs[] = {d_y, d_ht, d_x, d_weight, d_bias, d_h0};
     if (!all_aligned(ptrs) || !d_weight) return DN_ERR_INVALID_ARG;
     if ((long long)B * T > 0 && (!d_y || !d_x)) return DN_ERR_INVALID_ARG;
-    if (!conv_width_ok(W)) return DN_ERR_UNSUPPORTED;
+    if (!conv_width_ok(W) || T > kMaxT) return DN_ERR_UNSUPPORTED;
     const size_t need = dn::conv_bwd_workspace((long long)B * T, n_seqs, D, W, dtype == DN_BF16);
     if (!workspace || !aligned16(workspace) || workspace_bytes < need) return DN_ERR_INVALID_ARG;
     dn::ConvParams p{};
@@ -112,7 +115,7 @@ namespace {
 bool scan_states_ok(int N) { return N == 16 || N == 32 || N == 64 || N == 128; }
 
 bool scan_sizes_ok(int n_seqs, int B, int T, int D, int G, int N, dn_dtype dtype) {
-    return n_seqs >= 0 && B >= 0 && T >= 0 && D > 0 && G > 0 && D % G == 0 && scan_states_ok(N) && dtype_ok(dtype);
+    return n_seqs >= 0 && B >= 0 && T >= 0 && T <= kMaxT && D > 0 && G > 0 && D % G == 0 && scan_states_ok(N) && dtype_ok(dtype);
 }
 
 dn_status scan_check(const void *x, const void *dt, const float *A, const void *Bm, const void *Cm,
@@ -145,7 +148,7 @@ DN_EXPORT dn_status dn_selective_scan_fwd(const void *x, const void *dt, const f
     if (st != DN_OK) return st;
     const void *ptrs[] = {y, ht};
     if (!all_aligned(ptrs) || ((long long)B * T > 0 && !y)) return DN_ERR_INVALID_ARG;
-    if (!scan_states_ok(N)) return DN_ERR_UNSUPPORTED;
+    if (!scan_states_ok(N) || T > kMaxT) return DN_ERR_UNSUPPORTED;
     if (n_seqs == 0) return DN_OK;
     const size_t need = dn::scan_fwd_workspace(n_seqs, (long long)B * T, D, G, N);
     if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return DN_ERR_INVALID_ARG;
@@ -180,7 +183,7 @@ DN_EXPORT dn_status dn_selective_scan_bwd(const void *x, const void *dt, const f
     if (!all_aligned(ptrs) || !d_A) return DN_ERR_INVALID_ARG;
     if ((long long)B * T > 0 && (!d_y || !d_x || !d_dt || !d_Bm || !d_Cm || (z != nullptr) != (d_z != nullptr)))
         return DN_ERR_INVALID_ARG;
-    if (!scan_states_ok(N)) return DN_ERR_UNSUPPORTED;
+    if (!scan_states_ok(N) || T > kMaxT) return DN_ERR_UNSUPPORTED;
     const size_t need = dn::scan_bwd_workspace(n_seqs, (long long)B * T, D, G, N);
     if (!workspace || !aligned16(workspace) || workspace_bytes < need) return DN_ERR_INVALID_ARG;
     dn::ScanParams p{};

@@ -3,21 +3,24 @@
 //     delta = softplus(dt + dt_bias),  h[n] = e^{delta A[n]} h[n] + delta B[n] x,
 //     y = (sum_n C[n] h[n] + Dskip x) silu(z)
 //
-// A block takes the channels of one tile (128 threads, 4 states of a channel
-// each) and walks the tokens of one sequence, or of one chunk of it, in tiles of
-// 16.  Per tile the threads first compute delta and delta x of every token and
-// channel once, into shared memory, with the rows of Bm and Cm beside them; then
-// each thread steps its states through the tokens; then y is finished and stored
-// by rows.  The next tile's rows are loaded into registers meanwhile.
+// A thread owns two neighbouring channels and 16 of their states (N / 16 lanes share
+// a channel pair), a block is one warp, and walks the tokens of one sequence or of
+// one chunk of it.  So a row of x, dt, z and y is read and written by its own
+// threads without any exchange, delta is computed where it is used, and only the
+// rows of Bm and Cm, which all channels of a group share, go through shared memory:
+// what a thread loads there serves two channels.  (With 4 states of one channel per
+// thread the shared-memory pipe and the shuffles of the sum over n took most of the
+// time: 39 instructions and 13 shared-memory cycles per 8 channels and token.)
 //
-// What bounds it: N exponentials and 4 N fp32 operations per channel and token
-// against 6 to 8 bytes.
+// What bounds it: N exponentials and 2 N paired fp32 instructions per channel and
+// token against 6 to 8 bytes.
 //
 // Few channels leave most SMs idle, so sequences are then cut into chunks: one
 // launch computes each chunk's state from zero and its sum of delta, a second
 // steps the states over the chunks (the state at a chunk's end is
 // e^{A sum delta} times the one at its start, plus the chunk's own), and the
-// scan itself starts every chunk from its state.
+// scan itself starts every chunk from its state.  A single token has a kernel of its
+// own, one thread per 4 states, so that the states are read and written in whole lines.
 #include "dn_scan.cuh"
 
 namespace dn {
@@ -25,150 +28,307 @@ namespace {
 
 using namespace scan;
 
-constexpr int kThreads = 128;
-constexpr int kTile = 16;    // tokens of a tile
+constexpr int kTile = 16;      // tokens whose rows of Bm and Cm are staged at a time
 constexpr int kMinChunk = 64;  // the shortest chunk
+constexpr int kT = 16;         // states of a thread
+#ifndef FB
+#define FB 16
+#endif
+#ifndef FU
+#define FU 4
+#endif
+#ifndef FW
+#define FW 16
+#endif
+
+// Two neighbouring elements; PAIR: their address is a multiple of their size.
+template <typename T, bool PAIR>
+__device__ __forceinline__ void load2(Pack<T, 2> &r, const T *src, bool has0, bool has1) {
+    if constexpr (PAIR) {
+        if (has0) r.load(src);
+    } else {
+        Pack<T, 1> a, b;
+        a.clear();
+        b.clear();
+        if (has0) a.load(src);
+        if (has1) b.load(src + 1);
+        if constexpr (sizeof(T) == 4) r.w[0] = a.w[0], r.w[1] = b.w[0];
+        else r.w[0] = a.w[0] | b.w[0] << 16;
+    }
+}
+template <typename T, bool PAIR>
+__device__ __forceinline__ void store2(T *dst, float a, float b, bool has0, bool has1) {
+    if constexpr (PAIR) {
+        Vec<T, 2> v;
+        v.v[0] = a;
+        v.v[1] = b;
+        if (has0) v.store(dst);
+    } else {
+        Vec<T, 1> v;
+        v.v[0] = a;
+        if (has0) v.store(dst);
+        v.v[0] = b;
+        if (has1) v.store(dst + 1);
+    }
+}
 
 // ---- the scan over the tokens of a sequence or a chunk ------------------------------
 
-template <typename T, int L, bool VEC, bool STATE>
-__global__ void __launch_bounds__(kThreads) scan_fwd(ScanParams p) {
-    constexpr int N = kS * L, CH = kThreads / L, CV = CH / 4;
-    constexpr int kVecs = (kTile * CV + kThreads - 1) / kThreads;  // vectors of a tile per thread (CH <= 32: one)
-    constexpr int kBc = kTile * N / 2 / kThreads;                  // vectors of B and C per thread
-    static_assert(kVecs == 1, "a tile is one vector per thread at most");
-    __shared__ float2 s_dx[kTile][CH];           // delta, delta x
-    __shared__ float s_skip[kTile][CH];          // Dskip x
-    __shared__ float s_y[kTile][CH];
-    __shared__ __align__(16) float s_bc[2][kTile][N];
+template <typename T, int L, bool PAIR, bool STATE>
+__global__ void __launch_bounds__(32, FB) scan_fwd(ScanParams p) {
+    constexpr int N = kT * L, CH = 64 / L, Q = kT / 4;
+    constexpr int kWhich = STATE ? 1 : 2;                // Bm alone, or Cm too
+    constexpr int kBc = kTile * N * kWhich / 4 / 32;     // their vectors of a tile per thread
+    constexpr int U = FU;                                // tokens of x, dt, z in flight
+    constexpr int S = N <= 64 ? 2 : 1;                   // tiles of Bm and Cm in flight
+    using Bcs = Ahead<T, kBc, 32, S, true>;
+    __shared__ __align__(16) char ring[Bcs::kBytes];
+    __shared__ __align__(16) float s_bc[kTile][kWhich][N];
+    constexpr int kRow = 2 * kT + 4;  // a thread's states in shared memory, rows apart by an odd number of vectors
+    __shared__ __align__(16) float s_st[32 * kRow];
 
     const int tid = threadIdx.x;
-    const int tiles = p.G * ((p.D / p.G + CH - 1) / CH);
-    const int ct = blockIdx.x % tiles;
-    const long long slot = blockIdx.x / tiles;
-    if (blockIdx.x == 0) check_offsets(p.seq, tid, kThreads);
+    const unsigned tiles = p.G * ((p.D / p.G + CH - 1) / CH);
+    const unsigned slot = blockIdx.x / tiles;
+    const int ct = blockIdx.x - slot * tiles;
+    if (blockIdx.x == 0) check_offsets(p.seq, tid, 32);
     const SeqTile seq = p.chunk ? seq_tile(p.seq, slot, p.chunk) : seq_whole(p.seq, (int)slot);
     if (!seq.ok) return;
     if (STATE && seq.t1 >= seq.eos) return;  // nothing starts from the last chunk's end
     const Channels cs = channels_of<CH>(p, ct);
-
-    // this thread's channel and states
-    const int ch = tid / L, lane = tid % L;
-    const bool own = ch < cs.n;
-    const int d = cs.d0 + ch;
-    float a[kS], h[kS];
-    const long long dn_at = (long long)d * N + lane * kS;
-#pragma unroll
-    for (int i = 0; i < kS; ++i) a[i] = h[i] = 0.f;
-    if (own) {
-        const float4 r = *reinterpret_cast<const float4 *>(p.A + dn_at);
-        a[0] = log2_rate(r.x); a[1] = log2_rate(r.y); a[2] = log2_rate(r.z); a[3] = log2_rate(r.w);
-        const float *from = STATE ? nullptr
-                            : p.chunk ? p.hs + slot * p.D * N
-                            : p.h0 ? p.h0 + (long long)seq.n * p.D * N : nullptr;
-        if (from) {
-            const float4 s = *reinterpret_cast<const float4 *>(from + dn_at);
-            h[0] = s.x; h[1] = s.y; h[2] = s.z; h[3] = s.w;
-        }
-    }
-    // this thread's part of a tile: four channels of one token
-    const int vt = tid / CV, vc = (tid % CV) * 4;
-    const bool loads = vt < kTile;
-    const int vn = loads ? cs.n - vc : 0;
-    float bias[4], skip[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        bias[i] = i < vn && p.dt_bias ? p.dt_bias[cs.d0 + vc + i] : 0.f;
-        skip[i] = i < vn && p.Dskip ? p.Dskip[cs.d0 + vc + i] : 0.f;
-    }
+    const int pi = tid / L, lane = tid % L, d = cs.d0 + 2 * pi;
+    const bool has0 = 2 * pi < cs.n, has1 = 2 * pi + 1 < cs.n;
+    const int len = (int)(seq.t1 - seq.t0);
     const bool gate = !STATE && p.z;
-    float dsum[4] = {0.f, 0.f, 0.f, 0.f};
 
-    float fx[4], fd[4], fz[4] = {0.f, 0.f, 0.f, 0.f}, fb[kBc][4];
-    auto fetch = [&](long long t0) {
-        const bool in = loads && t0 + vt < seq.t1;
-        load4<T, VEC>(p.x, t0 + vt, p.D, cs.d0 + vc, vn, in, fx);
-        load4<T, VEC>(p.dt, t0 + vt, p.D, cs.d0 + vc, vn, in, fd);
-        if (gate) load4<T, VEC>(p.z, t0 + vt, p.D, cs.d0 + vc, vn, in, fz);
+    Bcs bcs;
+    auto fetch_bc = [&](int t0, int s) {
 #pragma unroll
         for (int k = 0; k < kBc; ++k) {
-            const int v = tid + k * kThreads, which = v / (kTile * N / 4), r = v % (kTile * N / 4);
-            const int t = r / (N / 4), c = (r % (N / 4)) * 4;
-            if (STATE && which) break;
-            load4<T, true>(which ? p.Cm : p.Bm, (t0 + t) * p.G + cs.g, N, c, 4, t0 + t < seq.t1, fb[k]);
+            const int v = (tid + k * 32) * 4, t = v / (kWhich * N), which = v / N % kWhich, c = v % N;
+            bcs.issue(ring, s, k,
+                      static_cast<const T *>(which ? p.Cm : p.Bm) + ((seq.t0 + t0 + t) * p.G + cs.g) * N + c,
+                      t0 + t < len ? 4 : 0);
+        }
+        bcs.commit();
+    };
+#pragma unroll
+    for (int s = 0; s < S; ++s) fetch_bc(s * kTile, s);
+
+    // Rows of x, dt, z and y: a token's offset from the tensors' first element for this
+    // thread.  What is fetched lies U tokens ahead of what is computed.
+    const long long first = seq.t0 * p.D + d;
+    const T *xp = static_cast<const T *>(p.x) + first, *dp = static_cast<const T *>(p.dt) + first;
+    const T *zp = gate ? static_cast<const T *>(p.z) + first : xp;
+    T *yp = static_cast<T *>(p.y) + first;
+    const long long D = p.D;
+    Pack<T, 2> fx[U], fd[U], fz[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        fx[k].clear(), fd[k].clear(), fz[k].clear();
+        if (k < len) {
+            load2<T, PAIR>(fx[k], xp + k * D, has0, has1);
+            load2<T, PAIR>(fd[k], dp + k * D, has0, has1);
+            if (gate) load2<T, PAIR>(fz[k], zp + k * D, has0, has1);
+        }
+    }
+    xp += U * D, dp += U * D, zp += U * D;
+
+    f2 a[2][kT / 2], h[2][kT / 2];  // rates and states of both channels
+    const float *from = STATE ? nullptr
+                        : p.chunk ? p.hs + (long long)slot * p.D * N
+                        : p.h0 ? p.h0 + (long long)seq.n * p.D * N : nullptr;
+    // A block's states lie one after the other in memory: they are read in whole lines and
+    // handed to their threads through shared memory (each thread's 32 on their own are 32
+    // lines per access, and measured 10 % of a walk of 112 tokens).
+    auto exchange = [&](auto *global, f2 (&v)[2][kT / 2], bool out) {
+        const int block = cs.n * N;  // floats
+        if (out) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int i = 0; i < Q; ++i)
+                    *reinterpret_cast<ulonglong2 *>(s_st + tid * kRow + c * kT + i * 4) = make_ulonglong2(v[c][2 * i], v[c][2 * i + 1]);
+            __syncwarp();
+        }
+        for (int f = tid * 4; f < block; f += 128) {
+            // float f of the block: channel f / N, state f % N; thread (channel / 2) L + state / 16
+            const int c = f / N, n = f % N;
+            float *sp = s_st + ((c >> 1) * L + n / kT) * kRow + (c & 1) * kT + n % kT;
+            if (out) *reinterpret_cast<float4 *>(const_cast<float *>(global) + f) = *reinterpret_cast<float4 *>(sp);
+            else *reinterpret_cast<float4 *>(sp) = *reinterpret_cast<const float4 *>(global + f);
+        }
+        __syncwarp();
+        if (!out) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int i = 0; i < Q; ++i) {
+                    const ulonglong2 r = *reinterpret_cast<const ulonglong2 *>(s_st + tid * kRow + c * kT + i * 4);
+                    const bool has = c ? has1 : has0;
+                    v[c][2 * i] = has ? r.x : 0ull;
+                    v[c][2 * i + 1] = has ? r.y : 0ull;
+                }
+            __syncwarp();
         }
     };
-    fetch(seq.t0);
-    for (long long t0 = seq.t0; t0 < seq.t1; t0 += kTile) {
-        float z[4];
-        if (loads) {
-            const bool in = t0 + vt < seq.t1;
+    exchange(p.A + (long long)cs.d0 * N, a, false);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float raw = fd[i] + bias[i];
-                const float delta = !in || i >= vn ? 0.f : p.softplus ? softplus(raw) : raw;
-                s_dx[vt][vc + i] = make_float2(delta, delta * fx[i]);
-                if (!STATE) s_skip[vt][vc + i] = skip[i] * fx[i];
-                dsum[i] += delta;
-                z[i] = fz[i];
-            }
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int i = 0; i < kT / 2; ++i) {
+            float lo, hi;
+            split(a[c][i], lo, hi);
+            a[c][i] = pair(log2_rate(lo), log2_rate(hi));
+            h[c][i] = 0ull;
         }
+    if (from) exchange(from + (long long)cs.d0 * N, h, false);
+    const f2 bias = p.dt_bias ? pair(has0 ? p.dt_bias[d] : 0.f, has1 ? p.dt_bias[d + 1] : 0.f) : 0ull;
+    const f2 skip = !STATE && p.Dskip ? pair(has0 ? p.Dskip[d] : 0.f, has1 ? p.Dskip[d + 1] : 0.f) : 0ull;
+    f2 dsum = 0ull;
+
+    int stage = 0;
+    for (int t0 = 0; t0 < len; t0 += kTile) {
+        bcs.wait();
+        __syncwarp();  // the last tile's rows are done with
 #pragma unroll
         for (int k = 0; k < kBc; ++k) {
-            const int v = tid + k * kThreads, which = v / (kTile * N / 4), r = v % (kTile * N / 4);
-            if (STATE && which) break;
-            *reinterpret_cast<float4 *>(&s_bc[which][0][0] + r * 4) = make_float4(fb[k][0], fb[k][1], fb[k][2], fb[k][3]);
+            const Pack<T, 4> r = bcs.get(ring, stage, k);
+            const int v = (tid + k * 32) * 4;
+            const bool in = t0 + v / (kWhich * N) < len;  // rows behind the last token: zeros
+            *reinterpret_cast<float4 *>(&s_bc[0][0][0] + v) =
+                in ? make_float4(r[0], r[1], r[2], r[3]) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        __syncthreads();
-        if (t0 + kTile < seq.t1) fetch(t0 + kTile);
+        fetch_bc(t0 + S * kTile, stage);
+        stage = stage + 1 == S ? 0 : stage + 1;
+        __syncwarp();
+        for (int u = 0; u < kTile && t0 + u < len; u += U) {
+            const int left = len - t0 - u;  // tokens from here on
+            // the steps of U tokens together: each is a long chain of its own.  A token
+            // behind the last has none, and so leaves the states as they are.
+            f2 delta[U];
 #pragma unroll
-        for (int q = 0; q < kTile; q += 4) {
-            float part[4];
+            for (int k = 0; k < U; ++k) {
+                const f2 raw = add2(pair(fd[k][0], fd[k][1]), bias);
+                delta[k] = p.softplus ? softplus2(raw) : raw;
+                if (k >= left) delta[k] = 0ull;
+                if (k + U < left) load2<T, PAIR>(fd[k], dp, has0, has1);
+                dp += D;
+            }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 dx = s_dx[q + k][ch];
-                const float4 b = *reinterpret_cast<const float4 *>(&s_bc[0][q + k][lane * kS]);
-                const float bb[4] = {b.x, b.y, b.z, b.w};
+            for (int k = 0; k < U; ++k) {
+                const f2 xs = pair(fx[k][0], fx[k][1]);
+                f2 zs = 0ull;
+                if (gate) zs = pair(fz[k][0], fz[k][1]);
+                if (k + U < left) {
+                    load2<T, PAIR>(fx[k], xp, has0, has1);
+                    if (gate) load2<T, PAIR>(fz[k], zp, has0, has1);
+                }
+                xp += D, zp += D;
+                float e0, e1, x0, x1;
+                split(delta[k], e0, e1);
+                split(mul2(delta[k], xs), x0, x1);
+                const f2 dd[2] = {pair(e0, e0), pair(e1, e1)}, dx[2] = {pair(x0, x0), pair(x1, x1)};
+                const float *bc = &s_bc[u + k][0][lane * kT];
+                f2 y[2] = {0ull, 0ull};
 #pragma unroll
-                for (int i = 0; i < kS; ++i) h[i] = fmaf(ex2(dx.x * a[i]), h[i], dx.y * bb[i]);
-                if (!STATE) {
-                    const float4 c = *reinterpret_cast<const float4 *>(&s_bc[1][q + k][lane * kS]);
-                    part[k] = fmaf(c.x, h[0], fmaf(c.y, h[1], fmaf(c.z, h[2], c.w * h[3])));
+                for (int i = 0; i < Q; ++i) {
+                    const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(bc + i * 4);
+                    ulonglong2 cc = make_ulonglong2(0ull, 0ull);
+                    if (!STATE) cc = *reinterpret_cast<const ulonglong2 *>(bc + N + i * 4);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float w0, w1, w2, w3;
+                        split(mul2(dd[c], a[c][2 * i]), w0, w1);
+                        split(mul2(dd[c], a[c][2 * i + 1]), w2, w3);
+                        f2 &h0 = h[c][2 * i], &h1 = h[c][2 * i + 1];
+                        h0 = fma2(pair(ex2(w0), ex2(w1)), h0, mul2(dx[c], b.x));
+                        h1 = fma2(pair(ex2(w2), ex2(w3)), h1, mul2(dx[c], b.y));
+                        if (!STATE) y[c] = fma2(cc.y, h1, fma2(cc.x, h0, y[c]));
+                    }
+                }
+                if (STATE) {
+                    dsum = add2(dsum, delta[k]);
+                } else {
+                    float o[2];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float lo, hi;
+                        split(y[c], lo, hi);
+                        o[c] = lo + hi;
+#pragma unroll
+                        for (int bit = 1; bit < L; bit <<= 1) o[c] += __shfl_xor_sync(0xffffffffu, o[c], bit);
+                    }
+                    f2 out = fma2(skip, xs, pair(o[0], o[1]));
+                    if (gate) {
+                        float z0, z1;
+                        split(zs, z0, z1);
+                        out = mul2(out, mul2(zs, pair(sigmoid_f(z0), sigmoid_f(z1))));
+                    }
+                    split(out, o[0], o[1]);
+                    if (lane == 0 && k < left) store2<T, PAIR>(yp, o[0], o[1], has0, has1);
+                    yp += D;
                 }
             }
-            if (!STATE) {
-                const float sum = sum4<L>(part, lane);
-                if (lane < 4) s_y[q + lane][ch] = sum;
-            }
-        }
-        __syncthreads();
-        if (!STATE && loads) {
-            float out[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                out[i] = s_y[vt][vc + i] + s_skip[vt][vc + i];
-                if (gate) out[i] *= silu_f(z[i]);
-            }
-            store4<T, VEC>(p.y, t0 + vt, p.D, cs.d0 + vc, vn, t0 + vt < seq.t1, out);
         }
     }
-    if (own) {
-        float *to = STATE ? p.hs + slot * p.D * N
-                    : p.ht && seq.t1 >= seq.eos ? p.ht + (long long)seq.n * p.D * N : nullptr;
-        if (to) *reinterpret_cast<float4 *>(to + dn_at) = make_float4(h[0], h[1], h[2], h[3]);
+    float *to = STATE ? p.hs + (long long)slot * p.D * N
+                : p.ht && seq.t1 >= seq.eos ? p.ht + (long long)seq.n * p.D * N : nullptr;
+    if (to) exchange(to + (long long)cs.d0 * N, h, true);
+    if (STATE && lane == 0) {
+        float s0, s1;
+        split(dsum, s0, s1);
+        if (has0) p.dsum[(long long)slot * p.D + d] = s0;
+        if (has1) p.dsum[(long long)slot * p.D + d + 1] = s1;
     }
-    if (STATE) {  // the chunk's sum of delta, over the threads that share a channel
-        __syncthreads();
-        if (loads)
+}
+
+// ---- one token per sequence ----------------------------------------------------------
+
+// One thread per four states: L = N / 4 lanes of a channel.
+template <typename T, int L>
+__global__ void __launch_bounds__(128) scan_step(ScanParams p) {
+    constexpr int N = kS * L;
+    const long long i = (long long)blockIdx.x * 128 + threadIdx.x;
+    const unsigned row = (unsigned)(i / L);  // sequence and channel
+    const int lane = threadIdx.x % L;
+    const unsigned n = row / (unsigned)p.D, d = row - n * p.D;
+    const bool in = n < (unsigned)p.seq.N;
+    float part = 0.f, x = 0.f;
+    if (in) {
+        const unsigned g = d / (unsigned)(p.D / p.G);
+        const long long bc = ((long long)n * p.G + g) * N + lane * kS;
+        Vec<T, 4> b, c;
+        Vec<T, 1> fx, fd;
+        fx.load(static_cast<const T *>(p.x) + row);
+        fd.load(static_cast<const T *>(p.dt) + row);
+        b.load(static_cast<const T *>(p.Bm) + bc);
+        c.load(static_cast<const T *>(p.Cm) + bc);
+        const float4 A = *reinterpret_cast<const float4 *>(p.A + (long long)d * N + lane * kS);
+        float4 h = make_float4(0.f, 0.f, 0.f, 0.f);
+        const long long at = (long long)row * N + lane * kS;
+        if (p.h0) h = *reinterpret_cast<const float4 *>(p.h0 + at);
+        const float raw = fd.v[0] + (p.dt_bias ? p.dt_bias[d] : 0.f);
+        const float delta = p.softplus ? softplus(raw) : raw;
+        x = fx.v[0];
+        const float dx = delta * x;
+        h.x = fmaf(ex2(delta * log2_rate(A.x)), h.x, dx * b.v[0]);
+        h.y = fmaf(ex2(delta * log2_rate(A.y)), h.y, dx * b.v[1]);
+        h.z = fmaf(ex2(delta * log2_rate(A.z)), h.z, dx * b.v[2]);
+        h.w = fmaf(ex2(delta * log2_rate(A.w)), h.w, dx * b.v[3]);
+        if (p.ht) *reinterpret_cast<float4 *>(p.ht + at) = h;
+        part = fmaf(c.v[0], h.x, fmaf(c.v[1], h.y, fmaf(c.v[2], h.z, c.v[3] * h.w)));
+    }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s_y[vt][vc + i] = dsum[i];
-        __syncthreads();
-        if (tid < cs.n) {
-            float s = 0.f;
-#pragma unroll
-            for (int t = 0; t < kTile; ++t) s += s_y[t][tid];
-            p.dsum[slot * p.D + cs.d0 + tid] = s;
+    for (int bit = 1; bit < L; bit <<= 1) part += __shfl_xor_sync(0xffffffffu, part, bit);
+    if (in && lane == 0) {
+        Vec<T, 1> out, z;
+        out.v[0] = p.Dskip ? fmaf(p.Dskip[d], x, part) : part;
+        if (p.z) {
+            z.load(static_cast<const T *>(p.z) + row);
+            out.v[0] *= silu_f(z.v[0]);
         }
+        out.store(static_cast<T *>(p.y) + row);
     }
 }
 
@@ -246,37 +406,52 @@ __global__ void __launch_bounds__(128) scan_combine(ScanParams p) {
     if (p.dh0) reinterpret_cast<float4 *>(p.dh0)[mine] = g;
 }
 
-template <typename T, int L, bool VEC>
+template <typename T, int L, bool PAIR>
 cudaError_t fwd_l(const ScanParams &p, cudaStream_t stream) {
-    constexpr int CH = kThreads / L;
     const long long slots = p.chunk ? tile_slots(p.seq, p.chunk) : p.seq.N;
-    const long long grid = slots * channel_tiles<CH>(p.D, p.G);
+    const long long grid = slots * channel_tiles<64 / L>(p.D, p.G);
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
     if (p.chunk) {
-        scan_fwd<T, L, VEC, true><<<(unsigned)grid, kThreads, 0, stream>>>(p);
+        scan_fwd<T, L, PAIR, true><<<(unsigned)grid, 32, 0, stream>>>(p);
         const cudaError_t err = scan_combine_launch(p, false, stream);
         if (err != cudaSuccess) return err;
     }
-    scan_fwd<T, L, VEC, false><<<(unsigned)grid, kThreads, 0, stream>>>(p);
+    scan_fwd<T, L, PAIR, false><<<(unsigned)grid, 32, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t fwd_t(const ScanParams &p, cudaStream_t stream) {
-    const bool vec = (p.D / p.G) % 4 == 0;
+    const bool even = (p.D / p.G) % 2 == 0;  // rows and groups begin on a pair
     switch (p.N) {
-        case 16: return vec ? fwd_l<T, 4, true>(p, stream) : fwd_l<T, 4, false>(p, stream);
-        case 32: return vec ? fwd_l<T, 8, true>(p, stream) : fwd_l<T, 8, false>(p, stream);
-        case 64: return vec ? fwd_l<T, 16, true>(p, stream) : fwd_l<T, 16, false>(p, stream);
-        default: return vec ? fwd_l<T, 32, true>(p, stream) : fwd_l<T, 32, false>(p, stream);
+        case 16: return even ? fwd_l<T, 1, true>(p, stream) : fwd_l<T, 1, false>(p, stream);
+        case 32: return even ? fwd_l<T, 2, true>(p, stream) : fwd_l<T, 2, false>(p, stream);
+        case 64: return even ? fwd_l<T, 4, true>(p, stream) : fwd_l<T, 4, false>(p, stream);
+        default: return even ? fwd_l<T, 8, true>(p, stream) : fwd_l<T, 8, false>(p, stream);
     }
+}
+
+// Whether every sequence is one token, and their channels can be counted in 32 bits.
+bool one_token(const ScanParams &p) { return !p.seq.cu && p.seq.T == 1 && p.seq.tokens * p.D < 0x80000000LL; }
+
+template <typename T>
+cudaError_t step_t(const ScanParams &p, cudaStream_t stream) {
+    const long long grid = (p.seq.tokens * p.D * (p.N / kS) + 127) / 128;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+    switch (p.N) {
+        case 16: scan_step<T, 4><<<(unsigned)grid, 128, 0, stream>>>(p); break;
+        case 32: scan_step<T, 8><<<(unsigned)grid, 128, 0, stream>>>(p); break;
+        case 64: scan_step<T, 16><<<(unsigned)grid, 128, 0, stream>>>(p); break;
+        default: scan_step<T, 32><<<(unsigned)grid, 128, 0, stream>>>(p); break;
+    }
+    return cudaGetLastError();
 }
 
 // Length of the chunks that a forward's sequences are cut into; 0: they are not.
 int fwd_chunk(int n_seqs, long long tokens, int D, int G, int N) {
-    const int ch = kThreads / (N / kS);
+    const int ch = 64 / (N / kT);
     const long long blocks = (long long)n_seqs * G * ((D / G + ch - 1) / ch);
-    const long long want = kSms * 4;
+    const long long want = kSms * FW;
     if (blocks >= want || tokens / n_seqs < 2 * kMinChunk) return 0;
     const long long parts = (want + blocks - 1) / blocks;
     const long long len = (tokens / n_seqs + parts - 1) / parts;
@@ -310,6 +485,10 @@ void scan_fwd_carve(ScanParams &p, void *workspace) {
 }
 
 cudaError_t scan_fwd_launch(ScanParams p, bool bf16, cudaStream_t stream, const char **name) {
+    if (one_token(p)) {
+        *name = bf16 ? "scan_step<bf16>" : "scan_step<f32>";
+        return bf16 ? step_t<__nv_bfloat16>(p, stream) : step_t<float>(p, stream);
+    }
     *name = p.chunk ? bf16 ? "scan_state+scan_combine+scan_fwd<bf16>" : "scan_state+scan_combine+scan_fwd<f32>"
                     : bf16 ? "scan_fwd<bf16>" : "scan_fwd<f32>";
     return bf16 ? fwd_t<__nv_bfloat16>(p, stream) : fwd_t<float>(p, stream);

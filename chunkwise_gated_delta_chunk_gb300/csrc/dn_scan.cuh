@@ -13,8 +13,51 @@ namespace scan {
 
 constexpr int kS = 4;  // states of a thread
 
-// log(1 + e^v) without loss on either side: for v << 0 it is e^v.
-__device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))); }
+// log(1 + e^v) = max(v, 0) + log(1 + e^-|v|) without loss on either side (for v << 0
+// it is e^v).  With q = e^-|v| in (0, 1], log(1 + q) = 2 atanh(s), s = q / (2 + q) in
+// (0, 1/3]: the series s + s^3 / 3 + ... to s^13 / 13, whose rest is below s^15 / 15 /
+// (1 - s^2) = 5.3e-9, 1.5e-8 of the sum.  The exponential's argument is split in two
+// so that its rounding does not grow with |v|.
+__device__ __forceinline__ float softplus(float v) {
+    const float u = fmaxf(-fabsf(v), -104.f), m = u * kLog2e;  // below, q is 0 beside 1
+    const float rest = fmaf(u, kLog2e, -m) + u * 1.9259629911e-8f;  // u log2(e) - m
+    const float e = ex2(m);
+    const float q = fmaf(e * 0.6931471806f, rest, e);
+    const float s = q * rcp(2.f + q), w = s * s;
+    float r = fmaf(w, 1.f / 13.f, 1.f / 11.f);
+    r = fmaf(r, w, 1.f / 9.f);
+    r = fmaf(r, w, 1.f / 7.f);
+    r = fmaf(r, w, 1.f / 5.f);
+    r = fmaf(r, w, 1.f / 3.f);
+    r = fmaf(r * w, s, s);
+    return v != v ? v : fmaxf(v, 0.f) + (r + r);
+}
+
+// softplus of both halves: the same steps, most of them on pairs.
+__device__ __forceinline__ f2 softplus2(f2 v) {
+    auto both = [](float x) { return pair(x, x); };
+    float v0, v1;
+    split(v, v0, v1);
+    const f2 u = pair(fmaxf(-fabsf(v0), -104.f), fmaxf(-fabsf(v1), -104.f));
+    const f2 m = mul2(u, both(kLog2e));
+    const f2 rest = fma2(u, both(1.9259629911e-8f), fma2(u, both(kLog2e), mul2(u, both(-kLog2e))));
+    float m0, m1, d0, d1;
+    split(m, m0, m1);
+    const f2 e = pair(ex2(m0), ex2(m1));
+    const f2 q = fma2(mul2(e, both(0.6931471806f)), rest, e);
+    split(add2(q, both(2.f)), d0, d1);
+    const f2 s = mul2(q, pair(rcp(d0), rcp(d1))), w = mul2(s, s);
+    f2 r = fma2(w, both(1.f / 13.f), both(1.f / 11.f));
+    r = fma2(r, w, both(1.f / 9.f));
+    r = fma2(r, w, both(1.f / 7.f));
+    r = fma2(r, w, both(1.f / 5.f));
+    r = fma2(r, w, both(1.f / 3.f));
+    r = fma2(mul2(r, w), s, s);
+    r = fma2(r, both(2.f), pair(fmaxf(v0, 0.f), fmaxf(v1, 0.f)));
+    float r0, r1;
+    split(r, r0, r1);
+    return pair(v0 != v0 ? v0 : r0, v1 != v1 ? v1 : r1);
+}
 
 // A in units of log2; an infinite one becomes the largest finite one, so that a
 // token without a step (delta = 0) keeps the state.
@@ -67,9 +110,7 @@ __device__ __forceinline__ void load4(const void *base, long long row, int D, in
 }
 
 template <typename T, bool VEC>
-__device__ __forceinline__ void store4(void *base, long long row, int D, int d, int n, bool in, const float (&v)[4]) {
-    if (!in || n <= 0) return;
-    T *dst = static_cast<T *>(base) + row * D + d;
+__device__ __forceinline__ void store4(T *dst, int n, const float (&v)[4]) {
     if constexpr (VEC) {
         Vec<T, 4> a;
 #pragma unroll
@@ -85,6 +126,57 @@ __device__ __forceinline__ void store4(void *base, long long row, int D, int d, 
             }
     }
 }
+
+// What a thread reads of each tile, fetched S tiles ahead: K vectors of four
+// elements by asynchronous copies into its own part of shared memory (a thread
+// reads only what it copied itself: no barrier).  Without ASYNC the vectors may lie
+// anywhere: they are loaded one tile ahead into registers, element by element.
+template <typename T, int K, int NT, int S, bool ASYNC>
+struct Ahead {
+    static constexpr int kStages = ASYNC ? S : 1;
+    static constexpr int kB = 4 * (int)sizeof(T);
+    static constexpr int kBytes = ASYNC ? S * K * NT * kB : 16;
+    Pack<T, 4> reg[ASYNC ? 1 : K];
+    // vector k of the tile in stage s; n: elements that exist
+    __device__ __forceinline__ void issue(char *ring, int s, int k, const T *src, int n) {
+        if constexpr (ASYNC) {
+            if (n <= 0) return;
+            const unsigned dst = (unsigned)__cvta_generic_to_shared(ring) + ((s * K + k) * NT + threadIdx.x) * kB;
+            if constexpr (kB == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+            else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+        } else {
+            float v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                Vec<T, 1> a;
+                a.v[0] = 0.f;
+                if (i < n) a.load(src + i);
+                v[i] = a.v[0];
+            }
+            if constexpr (sizeof(T) == 4) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) reg[k].w[i] = __float_as_uint(v[i]);
+            } else {  // exact: each is an element of T
+                reg[k].w[0] = Vec<T, 4>::pack(v[0], v[1]);
+                reg[k].w[1] = Vec<T, 4>::pack(v[2], v[3]);
+            }
+        }
+    }
+    __device__ __forceinline__ void commit() {
+        if constexpr (ASYNC) asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    // Waits for the oldest of the S tiles in flight.
+    __device__ __forceinline__ void wait() {
+        if constexpr (ASYNC) asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+    }
+    // Elements that do not exist (n given to issue) hold anything.
+    __device__ __forceinline__ Pack<T, 4> get(const char *ring, int s, int k) const {
+        if constexpr (!ASYNC) return reg[k];
+        Pack<T, 4> r;
+        r.load(reinterpret_cast<const T *>(ring + ((s * K + k) * NT + threadIdx.x) * kB));
+        return r;
+    }
+};
 
 // Sum over the lanes that differ in bit `bit` of R values each, the lower half
 // of the values staying with the lane whose bit is 0: R / 2 shuffles.

@@ -391,9 +391,12 @@ __global__ void __launch_bounds__(kThreads) scan_bwd(ScanParams p, int parts) {
                         sb[i] += od[i];
                     }
                 }
-                store4<T, VEC>(p.dx, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, ox);
-                store4<T, VEC>(p.ddt, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, od);
-                if (p.z) store4<T, VEC>(p.dz, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, oz);
+                if (in && at.n > 0) {
+                    const long long o = (t0 + at.t) * p.D + cs.d0 + at.c;
+                    store4<T, VEC>(static_cast<T *>(p.dx) + o, at.n, ox);
+                    store4<T, VEC>(static_cast<T *>(p.ddt) + o, at.n, od);
+                    if (p.z) store4<T, VEC>(static_cast<T *>(p.dz) + o, at.n, oz);
+                }
             }
             __syncthreads();  // s_res, s_go and s_bc are written again
         }

@@ -26,7 +26,8 @@
  * device: a malformed one makes dn_check return DN_ERR_DEVICE_ARG and leaves
  * the outputs unspecified; nothing outside the tensors is touched.  Rows of
  * tokens behind the last sequence are not written.  A sequence may be empty:
- * its final state is its initial one.
+ * its final state is its initial one.  T is at most 2^30 (larger:
+ * DN_ERR_UNSUPPORTED).
  *
  * Every sum, state and statistic is held in fp32.  Outputs of type `dtype`
  * are rounded to it once (to nearest even).  Results do not depend on the
