@@ -240,6 +240,12 @@ __device__ __forceinline__ f2 pair(float lo, float hi) {
 __device__ __forceinline__ void split(f2 v, float &lo, float &hi) {
     asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
 }
+__device__ __forceinline__ f2 both(float x) { return pair(x, x); }
+__device__ __forceinline__ float sum_of(f2 v) {
+    float lo, hi;
+    split(v, lo, hi);
+    return lo + hi;
+}
 __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
     f2 r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));

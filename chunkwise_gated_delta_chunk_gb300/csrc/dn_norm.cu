@@ -9,18 +9,22 @@
 // A row is held in registers by R threads, K vectors of V elements each, so
 // that every tensor is read once and the variance is taken about the mean.
 // R <= 32: several rows per warp, sums by shuffles; larger R: one row per
-// block, sums through shared memory.  Both directions are bound by memory.
+// block, sums through shared memory.  Blocks walk rows; the vectors of the rows
+// ahead come by asynchronous copies into each thread's own part of shared memory,
+// so that the sums' latency and the barriers do not keep memory idle (loaded into
+// registers row by row, the backward of 4096 columns reached 31 % of the memory
+// rate).  The arithmetic is on pairs.  Both directions are bound by memory.
 //
-// Backward: a block walks rows with the sums of dw and db of its columns in
-// registers, joins the threads that share a column and writes one row of
-// partial sums; a second kernel adds these rows in a fixed order.
+// Backward: the sums of dw and db of a thread's columns stay in registers over all
+// rows of its block; the threads that share a column are joined and the block writes
+// one row of partial sums; a second kernel adds these rows in a fixed order.
 #include "dn_layer.cuh"
 
 namespace dn {
 namespace {
 
 // Sum over the R threads of a row; every one of them gets it.  R > 32: `buf`
-// has R / 32 floats, and two buffers are used in turn by consecutive sums.
+// has S R / 32 floats, and consecutive sums use buffers of their own in turn.
 template <int R, int S>
 __device__ __forceinline__ void row_sum(float (&a)[S], float *buf) {
     constexpr int kIn = R < 32 ? R : 32;
@@ -45,200 +49,320 @@ __device__ __forceinline__ void row_sum(float (&a)[S], float *buf) {
     }
 }
 
-// One row in registers: element (k, i) of a thread is column (k R + lane) V + i.
+// How a row lies on threads: vector k of a thread is V neighbouring columns from
+// (k R + lane) V on.  Rows that do not begin on 16 bytes are taken element by element
+// (V = 2): there vector k is columns 2 k R + lane and (2 k + 1) R + lane.
 template <typename T, int V, int K, int R>
 struct Row {
     static constexpr int kThreads = R < 128 ? 128 : R;
     static constexpr int kRows = kThreads / R;  // rows of a block
+    static constexpr int P = V / 2;             // pairs of a vector
+    static constexpr bool kWhole = sizeof(T) * V == 16;
+    typedef f2 Pairs[K][P];
+    static __device__ __forceinline__ int col(int k, int i) {
+        const int lane = threadIdx.x % R;
+        return kWhole ? (k * R + lane) * V + i : (k * V + i) * R + lane;
+    }
+    // Whether element i of vector k exists (a whole vector does or does not).
+    static __device__ __forceinline__ bool in(int k, int i, int D) { return col(k, kWhole ? 0 : i) < D; }
 };
 
-// Mean and reciprocal deviation; x becomes xhat.  Columns behind D hold 0.
-template <int V, int K, int R>
-__device__ __forceinline__ void normalise(float (&x)[K][V], int lane, int D, float eps, bool rms, float *buf,
-                                          float &r) {
-    const float inv = 1.f / (float)D;
-    if (!rms) {
-        float s[1] = {0.f};
+// Vector k of a row, and of one of the fp32 vectors, as pairs; `other` where it does not exist.
+template <typename L, int V, typename T>
+__device__ __forceinline__ void load_row(f2 (&v)[V / 2], const T *src, int k, int D) {
+    Pack<T, V> r;
+    if constexpr (L::kWhole) {
+        r.clear();
+        if (L::in(k, 0, D)) r.load(src + L::col(k, 0));
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) v[i] = pair(r[2 * i], r[2 * i + 1]);
+    } else {
+        Vec<T, 1> a, b;
+        a.v[0] = b.v[0] = 0.f;
+        if (L::in(k, 0, D)) a.load(src + L::col(k, 0));
+        if (L::in(k, 1, D)) b.load(src + L::col(k, 1));
+        v[0] = pair(a.v[0], b.v[0]);
+    }
+}
+template <typename L, int V>
+__device__ __forceinline__ void load_vec(f2 (&v)[V / 2], const float *src, int k, int D, float other) {
+    if constexpr (L::kWhole) {
+        Vec<float, V> r;
+#pragma unroll
+        for (int i = 0; i < V; ++i) r.v[i] = other;
+        if (src && L::in(k, 0, D)) r.load(src + L::col(k, 0));
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) v[i] = pair(r.v[2 * i], r.v[2 * i + 1]);
+    } else {
+        v[0] = pair(src && L::in(k, 0, D) ? src[L::col(k, 0)] : other, src && L::in(k, 1, D) ? src[L::col(k, 1)] : other);
+    }
+}
+template <typename L, int V, typename T>
+__device__ __forceinline__ void store_row(T *dst, const f2 (&v)[V / 2], int k, int D) {
+    Vec<T, L::kWhole ? V : 1> out;
+    if constexpr (L::kWhole) {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) split(v[i], out.v[2 * i], out.v[2 * i + 1]);
+        if (L::in(k, 0, D)) out.store(dst + L::col(k, 0));
+    } else {
+        float lo, hi;
+        split(v[0], lo, hi);
+        out.v[0] = lo;
+        if (L::in(k, 0, D)) out.store(dst + L::col(k, 0));
+        out.v[0] = hi;
+        if (L::in(k, 1, D)) out.store(dst + L::col(k, 1));
+    }
+}
+
+// The vectors of A tensors' rows that a thread works on, S iterations ahead.
+template <typename T, int V, int K, int R, int A>
+struct Ring {
+    using L = Row<T, V, K, R>;
+    static constexpr int kStage = L::kWhole ? A * K * L::kThreads * 16 : 0;
+    static constexpr int kFit = L::kWhole ? 65536 / kStage : 1;
+    static constexpr int S = kFit < 1 ? 1 : kFit > 4 ? 4 : kFit;
+    static constexpr int kBytes = L::kWhole ? S * kStage : 0;
+    const T *base[A];
+    __device__ __forceinline__ void issue(char *ring, int s, long long row, const NormParams &p) {
+        if constexpr (L::kWhole) {
+#pragma unroll
+            for (int a = 0; a < A; ++a)
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+                    if (row < p.rows && L::in(k, 0, p.D)) {
+                        const unsigned dst = (unsigned)__cvta_generic_to_shared(ring) + s * kStage +
+                                             ((a * K + k) * L::kThreads + threadIdx.x) * 16;
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
+                                     "l"(base[a] + row * p.D + L::col(k, 0))
+                                     : "memory");
+                    }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+    }
+    __device__ __forceinline__ void wait() {
+        if constexpr (L::kWhole) asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+    }
+    // vector k of tensor a as pairs; zeros where the row or the column does not exist
+    __device__ __forceinline__ void get(f2 (&v)[L::P], const char *ring, int s, int a, int k, long long row,
+                                        const NormParams &p) const {
+        if constexpr (L::kWhole) {
+            Pack<T, V> r;
+            r.clear();
+            if (row < p.rows && L::in(k, 0, p.D))
+                r.load(reinterpret_cast<const T *>(ring + s * kStage + ((a * K + k) * L::kThreads + threadIdx.x) * 16));
+#pragma unroll
+            for (int i = 0; i < L::P; ++i) v[i] = pair(r[2 * i], r[2 * i + 1]);
+        } else {
+            load_row<L, V>(v, base[a] + row * p.D, k, row < p.rows ? p.D : 0);
+        }
+    }
+};
+
+// x becomes xhat; returns the reciprocal deviation.  Columns behind D hold 0.
+template <typename L, int V, int K, int R>
+__device__ __forceinline__ float normalise(f2 (&x)[K][V / 2], const NormParams &p, float inv, float *buf) {
+    constexpr int P = V / 2;
+    if (!p.rms) {
+        f2 t = 0ull;
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
-            for (int i = 0; i < V; ++i) s[0] += x[k][i];
+            for (int i = 0; i < P; ++i) t = add2(t, x[k][i]);
+        float s[1] = {sum_of(t)};
         row_sum<R>(s, buf);
-        const float m = s[0] * inv;
+        const float m = -s[0] * inv;
 #pragma unroll
-        for (int k = 0; k < K; ++k)
+        for (int k = 0; k < K; ++k) {
+            const f2 mm = pair(L::in(k, 0, p.D) ? m : 0.f, L::in(k, 1, p.D) ? m : 0.f);
 #pragma unroll
-            for (int i = 0; i < V; ++i) x[k][i] = (k * R + lane) * V + i < D ? x[k][i] - m : 0.f;
+            for (int i = 0; i < P; ++i) x[k][i] = add2(x[k][i], mm);
+        }
     }
-    float q[1] = {0.f};
+    f2 t = 0ull;
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int i = 0; i < V; ++i) q[0] = fmaf(x[k][i], x[k][i], q[0]);
-    row_sum<R>(q, buf + 2 * (R / 32 + 1));
-    r = 1.f / sqrtf(fmaf(q[0], inv, eps));
+        for (int i = 0; i < P; ++i) t = fma2(x[k][i], x[k][i], t);
+    float q[1] = {sum_of(t)};
+    row_sum<R>(q, buf + R / 32 + 1);
+    const float r = 1.f / sqrtf(fmaf(q[0], inv, p.eps));
+    const f2 rr = both(r);
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int i = 0; i < V; ++i) x[k][i] *= r;
+        for (int i = 0; i < P; ++i) x[k][i] = mul2(x[k][i], rr);
+    return r;
 }
 
-template <typename T, int V, int K, int R>
+// sigmoid of both halves
+__device__ __forceinline__ f2 sigmoid2(f2 u) {
+    float a, b;
+    split(u, a, b);
+    return pair(sigmoid_f(a), sigmoid_f(b));
+}
+
+extern __shared__ __align__(16) char s_ring[];
+
+template <typename T, int V, int K, int R, bool GATE>
 __global__ void __launch_bounds__(Row<T, V, K, R>::kThreads) norm_fwd(NormParams p) {
-    __shared__ float buf[4 * (R / 32 + 1)];
-    const int lane = threadIdx.x % R;
-    const long long row = (long long)blockIdx.x * Row<T, V, K, R>::kRows + threadIdx.x / R;
-    const bool in = row < p.rows;
-    const T *x = static_cast<const T *>(p.x) + row * p.D;
-    const T *z = p.z ? static_cast<const T *>(p.z) + row * p.D : nullptr;
-    T *y = static_cast<T *>(p.y) + row * p.D;
-    float a[K][V];
-    Vec<T, V> gate[K];
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int c = (k * R + lane) * V;
-        Vec<T, V> l;
-        zero(l);
-        zero(gate[k]);
-        if (in && c < p.D) {
-            l.load(x + c);
-            if (z) gate[k].load(z + c);
-        }
-#pragma unroll
-        for (int i = 0; i < V; ++i) a[k][i] = l.v[i];
-    }
-    float r;
-    normalise<V, K, R>(a, lane, p.D, p.eps, p.rms, buf, r);
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int c = (k * R + lane) * V;
-        if (!in || c >= p.D) continue;
-        Vec<float, V> w, b;
-        if (p.weight) w.load(p.weight + c);
-        if (p.bias) b.load(p.bias + c);
-        Vec<T, V> out;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            float n = p.weight ? a[k][i] * w.v[i] : a[k][i];
-            if (p.bias) n += b.v[i];
-            out.v[i] = z ? n * silu_f(gate[k].v[i]) : n;
-        }
-        out.store(y + c);
-    }
-}
-
-template <typename T, int V, int K, int R>
-__global__ void __launch_bounds__(Row<T, V, K, R>::kThreads) norm_bwd(NormParams p) {
-    constexpr int kRows = Row<T, V, K, R>::kRows;
-    __shared__ float buf[8 * (R / 32 + 1)];
-    const int lane = threadIdx.x % R;
+    using L = Row<T, V, K, R>;
+    using G = Ring<T, V, K, R, GATE ? 2 : 1>;
+    constexpr int P = L::P;
+    __shared__ float buf[2 * (R / 32 + 1)];
     const int sub = threadIdx.x / R;
     const float inv = 1.f / (float)p.D;
-    float sw[K][V], sb[K][V];
+    const long long step = (long long)gridDim.x * L::kRows;
+    long long row = (long long)blockIdx.x * L::kRows + sub;
+    G ring;
+    ring.base[0] = static_cast<const T *>(p.x);
+    if (GATE) ring.base[GATE ? 1 : 0] = static_cast<const T *>(p.z);
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int i = 0; i < V; ++i) sw[k][i] = sb[k][i] = 0.f;
-    for (long long first = (long long)blockIdx.x * kRows; first < p.rows; first += (long long)gridDim.x * kRows) {
-        const long long row = first + sub;
-        const bool in = row < p.rows;
-        const T *x = static_cast<const T *>(p.x) + row * p.D;
-        const T *dy = static_cast<const T *>(p.dy) + row * p.D;
-        const T *z = p.z ? static_cast<const T *>(p.z) + row * p.D : nullptr;
-        float a[K][V];
-        Vec<T, V> grad[K], gate[K];
+    for (int s = 0; s < G::S; ++s) ring.issue(s_ring, s, row + s * step, p);
+    int stage = 0;
+    for (long long first = (long long)blockIdx.x * L::kRows; first < p.rows; first += step, row += step) {
+        typename L::Pairs a, z;
+        ring.wait();
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = (k * R + lane) * V;
-            Vec<T, V> l;
-            zero(l);
-            zero(grad[k]);
-            zero(gate[k]);
-            if (in && c < p.D) {
-                l.load(x + c);
-                grad[k].load(dy + c);
-                if (z) gate[k].load(z + c);
-            }
-#pragma unroll
-            for (int i = 0; i < V; ++i) a[k][i] = l.v[i];
+            ring.get(a[k], s_ring, stage, 0, k, row, p);
+            if (GATE) ring.get(z[k], s_ring, stage, GATE ? 1 : 0, k, row, p);
         }
-        float r;
-        normalise<V, K, R>(a, lane, p.D, p.eps, p.rms, buf, r);
-        float s[2] = {0.f, 0.f};  // sums of d xhat and of d
+        ring.issue(s_ring, stage, row + G::S * step, p);
+        stage = stage + 1 == G::S ? 0 : stage + 1;
+        normalise<L, V, K, R>(a, p, inv, buf);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = (k * R + lane) * V;
-            if (!in || c >= p.D) continue;
-            Vec<float, V> w;
-            if (p.weight) w.load(p.weight + c);
-            if (z) {
-                Vec<float, V> b;
-                if (p.bias) b.load(p.bias + c);
-                Vec<T, V> out;
+            if (row >= p.rows) continue;
+            f2 w[P], b[P];
+            if (p.weight) load_vec<L, V>(w, p.weight, k, p.D, 1.f);
+            if (p.bias) load_vec<L, V>(b, p.bias, k, p.D, 0.f);
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    float n = p.weight ? a[k][i] * w.v[i] : a[k][i];
-                    if (p.bias) n += b.v[i];
-                    const float u = gate[k].v[i], g = sigmoid_f(u);
-                    out.v[i] = grad[k].v[i] * n * (g * fmaf(u, 1.f - g, 1.f));
-                    grad[k].v[i] *= u * g;
+            for (int i = 0; i < P; ++i) {
+                f2 n = a[k][i];
+                if (p.weight) n = p.bias ? fma2(n, w[i], b[i]) : mul2(n, w[i]);
+                else if (p.bias) n = add2(n, b[i]);
+                if (GATE) n = mul2(n, mul2(z[k][i], sigmoid2(z[k][i])));
+                a[k][i] = n;
+            }
+            store_row<L, V>(static_cast<T *>(p.y) + row * p.D, a[k], k, p.D);
+        }
+    }
+}
+
+template <typename T, int V, int K, int R, bool GATE>
+__global__ void __launch_bounds__(Row<T, V, K, R>::kThreads) norm_bwd(NormParams p) {
+    using L = Row<T, V, K, R>;
+    using G = Ring<T, V, K, R, GATE ? 3 : 2>;
+    constexpr int P = L::P;
+    __shared__ float buf[4 * (R / 32 + 1)];
+    const int sub = threadIdx.x / R;
+    const float inv = 1.f / (float)p.D;
+    const long long step = (long long)gridDim.x * L::kRows;
+    long long row = (long long)blockIdx.x * L::kRows + sub;
+    G ring;
+    ring.base[0] = static_cast<const T *>(p.x);
+    ring.base[1] = static_cast<const T *>(p.dy);
+    if (GATE) ring.base[GATE ? 2 : 0] = static_cast<const T *>(p.z);
+#pragma unroll
+    for (int s = 0; s < G::S; ++s) ring.issue(s_ring, s, row + s * step, p);
+    typename L::Pairs w, sw, sb;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        load_vec<L, V>(w[k], p.weight, k, p.D, 1.f);
+#pragma unroll
+        for (int i = 0; i < P; ++i) sw[k][i] = sb[k][i] = 0ull;
+    }
+    int stage = 0;
+    for (long long first = (long long)blockIdx.x * L::kRows; first < p.rows; first += step, row += step) {
+        typename L::Pairs a, g, z;
+        ring.wait();
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            ring.get(a[k], s_ring, stage, 0, k, row, p);
+            ring.get(g[k], s_ring, stage, 1, k, row, p);
+            if (GATE) ring.get(z[k], s_ring, stage, GATE ? 2 : 0, k, row, p);
+        }
+        ring.issue(s_ring, stage, row + G::S * step, p);
+        stage = stage + 1 == G::S ? 0 : stage + 1;
+        const float r = normalise<L, V, K, R>(a, p, inv, buf);
+        f2 t0 = 0ull, t1 = 0ull;  // sums of d xhat and of d
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if (row >= p.rows) continue;
+            if (GATE) {
+                f2 b[P], out[P];
+                if (p.bias) load_vec<L, V>(b, p.bias, k, p.D, 0.f);
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    const f2 n = p.bias ? fma2(a[k][i], w[k][i], b[i]) : mul2(a[k][i], w[k][i]);
+                    const f2 u = z[k][i], s = sigmoid2(u), one = both(1.f);
+                    // silu' = s (1 + u (1 - s))
+                    out[i] = mul2(mul2(g[k][i], n), mul2(s, fma2(u, fma2(s, both(-1.f), one), one)));
+                    g[k][i] = mul2(g[k][i], mul2(u, s));
                 }
-                out.store(static_cast<T *>(p.dz) + row * p.D + c);
+                store_row<L, V>(static_cast<T *>(p.dz) + row * p.D, out, k, p.D);
             }
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                sw[k][i] = fmaf(grad[k].v[i], a[k][i], sw[k][i]);
-                sb[k][i] += grad[k].v[i];
-                if (p.weight) grad[k].v[i] *= w.v[i];
-                s[0] = fmaf(grad[k].v[i], a[k][i], s[0]);
-                s[1] += grad[k].v[i];
+            for (int i = 0; i < P; ++i) {
+                sw[k][i] = fma2(g[k][i], a[k][i], sw[k][i]);
+                sb[k][i] = add2(sb[k][i], g[k][i]);
+                g[k][i] = mul2(g[k][i], w[k][i]);
+                t0 = fma2(g[k][i], a[k][i], t0);
+                t1 = add2(t1, g[k][i]);
             }
         }
-        row_sum<R>(s, buf + 4 * (R / 32 + 1));
-        const float c1 = s[0] * inv, c2 = p.rms ? 0.f : s[1] * inv;
+        float c1, c2 = 0.f;
+        if (p.rms) {
+            float s[1] = {sum_of(t0)};
+            row_sum<R>(s, buf + 2 * (R / 32 + 1));
+            c1 = s[0] * inv;
+        } else {
+            float s[2] = {sum_of(t0), sum_of(t1)};
+            row_sum<R>(s, buf + 2 * (R / 32 + 1));
+            c1 = s[0] * inv;
+            c2 = s[1] * inv;
+        }
+        const f2 rr = both(r), r1 = both(-r * c1), r2 = both(-r * c2);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = (k * R + lane) * V;
-            if (!in || c >= p.D) continue;
-            Vec<T, V> out;
+            if (row >= p.rows) continue;
 #pragma unroll
-            for (int i = 0; i < V; ++i) out.v[i] = r * (grad[k].v[i] - c2 - a[k][i] * c1);
-            out.store(static_cast<T *>(p.dx) + row * p.D + c);
+            for (int i = 0; i < P; ++i) g[k][i] = fma2(a[k][i], r1, fma2(g[k][i], rr, r2));
+            store_row<L, V>(static_cast<T *>(p.dx) + row * p.D, g[k], k, p.D);
         }
     }
     if (!p.partial) return;
     float *part = p.partial + (long long)blockIdx.x * 2 * p.D;
-    if constexpr (kRows == 1) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int c = (k * R + lane) * V + i;
-                if (c < p.D) {
-                    part[c] = sw[k][i];
-                    part[p.D + c] = sb[k][i];
+            for (int i = 0; i < P; ++i) {
+                float v[2];
+                split(h ? sb[k][i] : sw[k][i], v[0], v[1]);
+                // the rows of a warp first, then its warps
+#pragma unroll
+                for (int off = R; off < 32; off <<= 1) {
+                    v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
+                    v[1] += __shfl_xor_sync(0xffffffffu, v[1], off);
                 }
+                if constexpr (R <= 32) {
+                    __shared__ float red[4][2][32];
+                    __syncthreads();
+                    red[threadIdx.x >> 5][0][threadIdx.x & 31] = v[0];
+                    red[threadIdx.x >> 5][1][threadIdx.x & 31] = v[1];
+                    __syncthreads();
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        v[q] = (red[0][q][threadIdx.x & 31] + red[1][q][threadIdx.x & 31]) +
+                               (red[2][q][threadIdx.x & 31] + red[3][q][threadIdx.x & 31]);
+                }
+                if (threadIdx.x < R)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        if (L::in(k, 2 * i + q, p.D)) part[(long long)h * p.D + L::col(k, 2 * i + q)] = v[q];
             }
-    } else {
-        __shared__ float red[kRows][R];
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    __syncthreads();
-                    red[sub][lane] = h ? sb[k][i] : sw[k][i];
-                    __syncthreads();
-                    const int c = (k * R + lane) * V + i;
-                    if (sub == 0 && c < p.D) {
-                        float v = 0.f;
-#pragma unroll
-                        for (int q = 0; q < kRows; ++q) v += red[q][lane];
-                        part[(long long)h * p.D + c] = v;
-                    }
-                }
-    }
 }
 
 // dweight and dbias from the blocks' rows: 32 columns and 8 slices of the rows per block.
@@ -260,31 +384,45 @@ __global__ void __launch_bounds__(256) norm_bwd_sums(NormParams p, int blocks) {
     }
 }
 
-// Blocks of the backward: enough to fill the GPU, no more than there are rows
-// for them.  From the sizes alone, since every block has a row of workspace.
-int norm_bwd_blocks(long long rows, int per_block) {
+// Blocks that walk the rows: as many as the GPU holds at once, no more than there are
+// rows for them.  From the sizes alone, since every block of the backward has a row of
+// workspace; all of them walk the same number of rows, or one less.
+int norm_blocks(long long rows, int threads, int per_block, int regs) {
     const long long most = (rows + per_block - 1) / per_block;
-    const long long fill = kSms * 4;
-    return (int)(most < fill ? most : fill);
+    const long long fill = (long long)kSms * (65536 / (regs * threads) > 0 ? 65536 / (regs * threads) : 1);
+    if (most <= fill) return (int)most;
+    const long long each = (most + fill - 1) / fill;
+    return (int)((most + each - 1) / each);
+}
+
+template <typename T, int V, int K, int R, bool GATE>
+cudaError_t norm_launch_g(const NormParams &p, bool bwd, cudaStream_t stream) {
+    constexpr int kRows = Row<T, V, K, R>::kRows, kThreads = Row<T, V, K, R>::kThreads;
+    if (!bwd) {
+        constexpr int bytes = Ring<T, V, K, R, GATE ? 2 : 1>::kBytes;
+        cudaError_t err = cudaFuncSetAttribute(norm_fwd<T, V, K, R, GATE>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (err != cudaSuccess) return err;
+        norm_fwd<T, V, K, R, GATE><<<norm_blocks(p.rows, kThreads, kRows, 64), kThreads, bytes, stream>>>(p);
+    } else {
+        const int grid = norm_blocks(p.rows, kThreads, kRows, 128);
+        if (grid > 0) {
+            constexpr int bytes = Ring<T, V, K, R, GATE ? 3 : 2>::kBytes;
+            cudaError_t err = cudaFuncSetAttribute(norm_bwd<T, V, K, R, GATE>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+            if (err != cudaSuccess) return err;
+            norm_bwd<T, V, K, R, GATE><<<grid, kThreads, bytes, stream>>>(p);
+        }
+        if (p.partial) norm_bwd_sums<<<dim3((p.D + 31) / 32, 2), dim3(32, 8), 0, stream>>>(p, grid);
+    }
+    return cudaGetLastError();
 }
 
 template <typename T, int V, int K, int R>
 cudaError_t norm_launch(const NormParams &p, bool bwd, cudaStream_t stream, int *blocks) {
-    constexpr int kRows = Row<T, V, K, R>::kRows, kThreads = Row<T, V, K, R>::kThreads;
     if (blocks) {  // the size of the backward's grid only
-        *blocks = norm_bwd_blocks(p.rows, kRows);
+        *blocks = norm_blocks(p.rows, Row<T, V, K, R>::kThreads, Row<T, V, K, R>::kRows, 128);
         return cudaSuccess;
     }
-    if (!bwd) {
-        const long long grid = (p.rows + kRows - 1) / kRows;
-        if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-        norm_fwd<T, V, K, R><<<(unsigned)grid, kThreads, 0, stream>>>(p);
-    } else {
-        const int grid = norm_bwd_blocks(p.rows, kRows);
-        if (grid > 0) norm_bwd<T, V, K, R><<<grid, kThreads, 0, stream>>>(p);
-        if (p.partial) norm_bwd_sums<<<dim3((p.D + 31) / 32, 2), dim3(32, 8), 0, stream>>>(p, grid);
-    }
-    return cudaGetLastError();
+    return p.z ? norm_launch_g<T, V, K, R, true>(p, bwd, stream) : norm_launch_g<T, V, K, R, false>(p, bwd, stream);
 }
 
 // Threads and vectors of a row by its length in vectors: as few threads as
@@ -302,15 +440,15 @@ cudaError_t norm_dispatch(const NormParams &p, bool bwd, cudaStream_t stream, in
         if (n <= 256) return norm_launch<T, V, 2, 128>(p, bwd, stream, blocks);
         if (n <= 512) return norm_launch<T, V, 2, 256>(p, bwd, stream, blocks);
         if (n <= 1024) return norm_launch<T, V, 2, 512>(p, bwd, stream, blocks);
-        return norm_launch<T, V, 16 / V * 2, 512>(p, bwd, stream, blocks);
+        return norm_launch<T, V, 16 / V, 1024>(p, bwd, stream, blocks);
     }
     // rows that do not begin on 16 bytes: single elements
-    if (p.D <= 32) return norm_launch<T, 1, 1, 32>(p, bwd, stream, blocks);
-    if (p.D <= 128) return norm_launch<T, 1, 4, 32>(p, bwd, stream, blocks);
-    if (p.D <= 512) return norm_launch<T, 1, 4, 128>(p, bwd, stream, blocks);
-    if (p.D <= 2048) return norm_launch<T, 1, 8, 256>(p, bwd, stream, blocks);
-    if (p.D <= 8192) return norm_launch<T, 1, 16, 512>(p, bwd, stream, blocks);
-    return norm_launch<T, 1, 32, 512>(p, bwd, stream, blocks);
+    if (p.D <= 32) return norm_launch<T, 2, 1, 16>(p, bwd, stream, blocks);
+    if (p.D <= 128) return norm_launch<T, 2, 2, 32>(p, bwd, stream, blocks);
+    if (p.D <= 512) return norm_launch<T, 2, 2, 128>(p, bwd, stream, blocks);
+    if (p.D <= 2048) return norm_launch<T, 2, 4, 256>(p, bwd, stream, blocks);
+    if (p.D <= 8192) return norm_launch<T, 2, 8, 512>(p, bwd, stream, blocks);
+    return norm_launch<T, 2, 8, 1024>(p, bwd, stream, blocks);
 }
 
 }  // namespace

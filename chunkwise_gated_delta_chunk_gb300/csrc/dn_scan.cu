@@ -31,15 +31,7 @@ using namespace scan;
 constexpr int kTile = 16;      // tokens whose rows of Bm and Cm are staged at a time
 constexpr int kMinChunk = 64;  // the shortest chunk
 constexpr int kT = 16;         // states of a thread
-#ifndef FB
-#define FB 16
-#endif
-#ifndef FU
-#define FU 4
-#endif
-#ifndef FW
-#define FW 16
-#endif
+constexpr int kResident = 16;  // blocks of an SM (128 registers a thread)
 
 // Two neighbouring elements; PAIR: their address is a multiple of their size.
 template <typename T, bool PAIR>
@@ -75,11 +67,11 @@ __device__ __forceinline__ void store2(T *dst, float a, float b, bool has0, bool
 // ---- the scan over the tokens of a sequence or a chunk ------------------------------
 
 template <typename T, int L, bool PAIR, bool STATE>
-__global__ void __launch_bounds__(32, FB) scan_fwd(ScanParams p) {
+__global__ void __launch_bounds__(32, kResident) scan_fwd(ScanParams p) {
     constexpr int N = kT * L, CH = 64 / L, Q = kT / 4;
     constexpr int kWhich = STATE ? 1 : 2;                // Bm alone, or Cm too
     constexpr int kBc = kTile * N * kWhich / 4 / 32;     // their vectors of a tile per thread
-    constexpr int U = FU;                                // tokens of x, dt, z in flight
+    constexpr int U = 4;                                // tokens of x, dt, z in flight
     constexpr int S = N <= 64 ? 2 : 1;                   // tiles of Bm and Cm in flight
     using Bcs = Ahead<T, kBc, 32, S, true>;
     __shared__ __align__(16) char ring[Bcs::kBytes];
@@ -451,7 +443,7 @@ cudaError_t step_t(const ScanParams &p, cudaStream_t stream) {
 int fwd_chunk(int n_seqs, long long tokens, int D, int G, int N) {
     const int ch = 64 / (N / kT);
     const long long blocks = (long long)n_seqs * G * ((D / G + ch - 1) / ch);
-    const long long want = kSms * FW;
+    const long long want = kSms * kResident;  // one block too many would be a second wave
     if (blocks >= want || tokens / n_seqs < 2 * kMinChunk) return 0;
     const long long parts = (want + blocks - 1) / blocks;
     const long long len = (tokens / n_seqs + parts - 1) / parts;

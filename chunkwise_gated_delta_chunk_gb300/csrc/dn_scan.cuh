@@ -35,7 +35,6 @@ __device__ __forceinline__ float softplus(float v) {
 
 // softplus of both halves: the same steps, most of them on pairs.
 __device__ __forceinline__ f2 softplus2(f2 v) {
-    auto both = [](float x) { return pair(x, x); };
     float v0, v1;
     split(v, v0, v1);
     const f2 u = pair(fmaxf(-fabsf(v0), -104.f), fmaxf(-fabsf(v1), -104.f));
