@@ -40,11 +40,14 @@ __device__ __forceinline__ void row_sum(float (&a)[S], float *buf) {
             for (int s = 0; s < S; ++s) buf[s * kWarps + warp] = a[s];
         __syncthreads();
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            float v = lane < kWarps ? buf[s * kWarps + lane] : 0.f;
+        for (int s = 0; s < S; ++s) {  // every thread adds all of them: shorter than shuffles
+            float4 v = reinterpret_cast<const float4 *>(buf)[s * kWarps / 4];
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-            a[s] = v;
+            for (int w = 1; w < kWarps / 4; ++w) {
+                const float4 o = reinterpret_cast<const float4 *>(buf)[s * kWarps / 4 + w];
+                v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+            }
+            a[s] = (v.x + v.y) + (v.z + v.w);
         }
     }
 }
@@ -184,8 +187,8 @@ __device__ __forceinline__ float normalise(f2 (&x)[K][V / 2], const NormParams &
 #pragma unroll
         for (int i = 0; i < P; ++i) t = fma2(x[k][i], x[k][i], t);
     float q[1] = {sum_of(t)};
-    row_sum<R>(q, buf + R / 32 + 1);
-    const float r = 1.f / sqrtf(fmaf(q[0], inv, p.eps));
+    row_sum<R>(q, buf + R / 32);
+    const float r = rsqrtf(fmaf(q[0], inv, p.eps));
     const f2 rr = both(r);
 #pragma unroll
     for (int k = 0; k < K; ++k)
@@ -208,7 +211,7 @@ __global__ void __launch_bounds__(Row<T, V, K, R>::kThreads) norm_fwd(NormParams
     using L = Row<T, V, K, R>;
     using G = Ring<T, V, K, R, GATE ? 2 : 1>;
     constexpr int P = L::P;
-    __shared__ float buf[2 * (R / 32 + 1)];
+    __shared__ __align__(16) float buf[4 * (R / 32) + 4];  // of even and of odd rows: one sum may be all that separates them
     const int sub = threadIdx.x / R;
     const float inv = 1.f / (float)p.D;
     const long long step = (long long)gridDim.x * L::kRows;
@@ -218,7 +221,13 @@ __global__ void __launch_bounds__(Row<T, V, K, R>::kThreads) norm_fwd(NormParams
     if (GATE) ring.base[GATE ? 1 : 0] = static_cast<const T *>(p.z);
 #pragma unroll
     for (int s = 0; s < G::S; ++s) ring.issue(s_ring, s, row + s * step, p);
-    int stage = 0;
+    f2 w[P], b[P];
+    auto vectors = [&](int k) {  // weight and bias of vector k
+        if (p.weight) load_vec<L, V>(w, p.weight, k, p.D, 1.f);
+        if (p.bias) load_vec<L, V>(b, p.bias, k, p.D, 0.f);
+    };
+    if (K == 1) vectors(0);  // the same for all rows
+    int stage = 0, odd = 0;
     for (long long first = (long long)blockIdx.x * L::kRows; first < p.rows; first += step, row += step) {
         typename L::Pairs a, z;
         ring.wait();
@@ -229,13 +238,12 @@ __global__ void __launch_bounds__(Row<T, V, K, R>::kThreads) norm_fwd(NormParams
         }
         ring.issue(s_ring, stage, row + G::S * step, p);
         stage = stage + 1 == G::S ? 0 : stage + 1;
-        normalise<L, V, K, R>(a, p, inv, buf);
+        normalise<L, V, K, R>(a, p, inv, buf + odd * 2 * (R / 32));
+        odd ^= 1;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             if (row >= p.rows) continue;
-            f2 w[P], b[P];
-            if (p.weight) load_vec<L, V>(w, p.weight, k, p.D, 1.f);
-            if (p.bias) load_vec<L, V>(b, p.bias, k, p.D, 0.f);
+            if (K > 1) vectors(k);
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 f2 n = a[k][i];
@@ -254,7 +262,7 @@ __global__ void __launch_bounds__(Row<T, V, K, R>::kThreads) norm_bwd(NormParams
     using L = Row<T, V, K, R>;
     using G = Ring<T, V, K, R, GATE ? 3 : 2>;
     constexpr int P = L::P;
-    __shared__ float buf[4 * (R / 32 + 1)];
+    __shared__ __align__(16) float buf[4 * (R / 32) + 4];
     const int sub = threadIdx.x / R;
     const float inv = 1.f / (float)p.D;
     const long long step = (long long)gridDim.x * L::kRows;
@@ -314,11 +322,11 @@ __global__ void __launch_bounds__(Row<T, V, K, R>::kThreads) norm_bwd(NormParams
         float c1, c2 = 0.f;
         if (p.rms) {
             float s[1] = {sum_of(t0)};
-            row_sum<R>(s, buf + 2 * (R / 32 + 1));
+            row_sum<R>(s, buf + 2 * (R / 32));
             c1 = s[0] * inv;
         } else {
             float s[2] = {sum_of(t0), sum_of(t1)};
-            row_sum<R>(s, buf + 2 * (R / 32 + 1));
+            row_sum<R>(s, buf + 2 * (R / 32));
             c1 = s[0] * inv;
             c2 = s[1] * inv;
         }
@@ -365,23 +373,23 @@ __global__ void __launch_bounds__(Row<T, V, K, R>::kThreads) norm_bwd(NormParams
             }
 }
 
-// dweight and dbias from the blocks' rows: 32 columns and 8 slices of the rows per block.
-__global__ void __launch_bounds__(256) norm_bwd_sums(NormParams p, int blocks) {
-    __shared__ float red[8][32];
+// dweight and dbias from the blocks' rows: 32 columns and 32 slices of the rows per block.
+__global__ void __launch_bounds__(1024) norm_bwd_sums(NormParams p, int blocks) {
+    __shared__ float red[32][33];
     const int c = blockIdx.x * 32 + threadIdx.x;
     const int h = blockIdx.y;
     float a = 0.f;
     if (c < p.D)
-        for (int b = threadIdx.y; b < blocks; b += 8) a += p.partial[((long long)b * 2 + h) * p.D + c];
+#pragma unroll 4
+        for (int b = threadIdx.y; b < blocks; b += 32) a += p.partial[((long long)b * 2 + h) * p.D + c];
     red[threadIdx.y][threadIdx.x] = a;
     __syncthreads();
-    float *out = h ? p.dbias : p.dweight;
-    if (threadIdx.y == 0 && c < p.D && out) {
-        float v = 0.f;
+    float v = red[threadIdx.x][threadIdx.y];  // column threadIdx.y, slice threadIdx.x
 #pragma unroll
-        for (int q = 0; q < 8; ++q) v += red[q][threadIdx.x];
-        out[c] = v;
-    }
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    float *out = h ? p.dbias : p.dweight;
+    const int o = blockIdx.x * 32 + threadIdx.y;
+    if (threadIdx.x == 0 && o < p.D && out) out[o] = v;
 }
 
 // Blocks that walk the rows: as many as the GPU holds at once, no more than there are
@@ -411,7 +419,7 @@ cudaError_t norm_launch_g(const NormParams &p, bool bwd, cudaStream_t stream) {
             if (err != cudaSuccess) return err;
             norm_bwd<T, V, K, R, GATE><<<grid, kThreads, bytes, stream>>>(p);
         }
-        if (p.partial) norm_bwd_sums<<<dim3((p.D + 31) / 32, 2), dim3(32, 8), 0, stream>>>(p, grid);
+        if (p.partial) norm_bwd_sums<<<dim3((p.D + 31) / 32, 2), dim3(32, 32), 0, stream>>>(p, grid);
     }
     return cudaGetLastError();
 }
@@ -439,6 +447,7 @@ cudaError_t norm_dispatch(const NormParams &p, bool bwd, cudaStream_t stream, in
         if (n <= 128) return norm_launch<T, V, 1, 128>(p, bwd, stream, blocks);
         if (n <= 256) return norm_launch<T, V, 2, 128>(p, bwd, stream, blocks);
         if (n <= 512) return norm_launch<T, V, 2, 256>(p, bwd, stream, blocks);
+
         if (n <= 1024) return norm_launch<T, V, 2, 512>(p, bwd, stream, blocks);
         return norm_launch<T, V, 16 / V, 1024>(p, bwd, stream, blocks);
     }

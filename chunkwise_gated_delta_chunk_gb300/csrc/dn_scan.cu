@@ -326,9 +326,11 @@ __global__ void __launch_bounds__(128) scan_step(ScanParams p) {
 
 // ---- states over the chunks of a sequence ------------------------------------------
 
-// (see scan_combine_launch)
+// (see scan_combine_launch; blockIdx.y = 1: the gradients' walk back).  A thread takes four
+// states and loads kAhead chunks at a time: the walk is bound by latency.
 template <bool BWD>
 __global__ void __launch_bounds__(128) scan_combine(ScanParams p) {
+    constexpr int kAhead = 8;
     const long long i = (long long)blockIdx.x * 128 + threadIdx.x;
     const int q = p.N / 4;  // vectors of a channel's states
     const long long per = (long long)p.D * q;
@@ -346,56 +348,40 @@ __global__ void __launch_bounds__(128) scan_combine(ScanParams p) {
         chunks = ((long long)p.seq.T + p.chunk - 1) / p.chunk;
         slot = (chunks > 0 ? chunks : 1) * (long long)n;
     }
-    const float4 A = *reinterpret_cast<const float4 *>(p.A + at * 4);
+    float4 A = *reinterpret_cast<const float4 *>(p.A + at * 4);
+    A = make_float4(log2_rate(A.x), log2_rate(A.y), log2_rate(A.z), log2_rate(A.w));
     const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
     const long long mine = (long long)n * per + at;
-    float4 *hs = reinterpret_cast<float4 *>(p.hs) + slot * per + at;
-    const float *ds = p.dsum + slot * p.D + d;
-    auto step = [&](float4 &s, float sum, const float4 &own) {
-        s.x = fmaf(ex2(sum * log2_rate(A.x)), s.x, own.x);
-        s.y = fmaf(ex2(sum * log2_rate(A.y)), s.y, own.y);
-        s.z = fmaf(ex2(sum * log2_rate(A.z)), s.z, own.z);
-        s.w = fmaf(ex2(sum * log2_rate(A.w)), s.w, own.w);
-    };
-    constexpr int U = 4;  // chunks loaded ahead
-    float4 s = p.h0 ? reinterpret_cast<const float4 *>(p.h0)[mine] : none;
-    if (chunks == 0) hs[0] = s;  // an empty sequence's slot
-    for (long long c = 0; c < chunks; c += U) {
-        float4 own[U];
-        float sum[U];
+    const bool back = BWD && blockIdx.y;
+    // chunk c of the walk: from the first on, or from the last back
+    const long long first = back ? slot + chunks - 1 : slot, step = back ? -1 : 1;
+    float4 *vs = reinterpret_cast<float4 *>(back ? p.gs : p.hs) + first * per + at;
+    const float *ds = p.dsum + first * p.D + d;
+    const float *from = back ? p.dht : p.h0;
+    float4 s = from ? reinterpret_cast<const float4 *>(from)[mine] : none;
+    if (!back && chunks == 0) vs[0] = s;  // an empty sequence's slot
+    for (long long c = 0; c < chunks; c += kAhead) {
+        float4 own[kAhead];
+        float sum[kAhead];
 #pragma unroll
-        for (int k = 0; k < U; ++k)
-            if (c + k < chunks - 1) {
-                own[k] = hs[(c + k) * per];
-                sum[k] = ds[(c + k) * p.D];
+        for (int k = 0; k < kAhead; ++k)
+            if (c + k < chunks && (back || c + k < chunks - 1)) {  // the last chunk's own state is not made
+                own[k] = vs[(c + k) * step * per];
+                sum[k] = ds[(c + k) * step * p.D];
             }
 #pragma unroll
-        for (int k = 0; k < U; ++k)
+        for (int k = 0; k < kAhead; ++k)
             if (c + k < chunks) {
-                hs[(c + k) * per] = s;
-                if (c + k < chunks - 1) step(s, sum[k], own[k]);
+                vs[(c + k) * step * per] = s;
+                if (back || c + k < chunks - 1) {
+                    s.x = fmaf(ex2(sum[k] * A.x), s.x, own[k].x);
+                    s.y = fmaf(ex2(sum[k] * A.y), s.y, own[k].y);
+                    s.z = fmaf(ex2(sum[k] * A.z), s.z, own[k].z);
+                    s.w = fmaf(ex2(sum[k] * A.w), s.w, own[k].w);
+                }
             }
     }
-    if (!BWD) return;
-    float4 *gs = reinterpret_cast<float4 *>(p.gs) + slot * per + at;
-    float4 g = p.dht ? reinterpret_cast<const float4 *>(p.dht)[mine] : none;
-    for (long long c = chunks - 1; c >= 0; c -= U) {
-        float4 own[U];
-        float sum[U];
-#pragma unroll
-        for (int k = 0; k < U; ++k)
-            if (c - k >= 0) {
-                own[k] = gs[(c - k) * per];
-                sum[k] = ds[(c - k) * p.D];
-            }
-#pragma unroll
-        for (int k = 0; k < U; ++k)
-            if (c - k >= 0) {
-                gs[(c - k) * per] = g;
-                step(g, sum[k], own[k]);
-            }
-    }
-    if (p.dh0) reinterpret_cast<float4 *>(p.dh0)[mine] = g;
+    if (back && p.dh0) reinterpret_cast<float4 *>(p.dh0)[mine] = s;
 }
 
 template <typename T, int L, bool PAIR>
@@ -457,7 +443,7 @@ cudaError_t scan_combine_launch(const ScanParams &p, bool bwd, cudaStream_t stre
     const long long grid = (n + 127) / 128;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
     if (grid == 0) return cudaSuccess;
-    if (bwd) scan_combine<true><<<(unsigned)grid, 128, 0, stream>>>(p);
+    if (bwd) scan_combine<true><<<dim3((unsigned)grid, 2), 128, 0, stream>>>(p);
     else scan_combine<false><<<(unsigned)grid, 128, 0, stream>>>(p);
     return cudaGetLastError();
 }

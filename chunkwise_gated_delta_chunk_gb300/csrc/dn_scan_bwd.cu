@@ -77,10 +77,6 @@ struct BcRows {
     }
 };
 
-__device__ __forceinline__ void to4(float (&v)[4], const float4 &f) {
-    v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
-}
-
 // ---- 1: what a chunk does to the state, and its outputs to the state's gradient ------
 
 template <typename T, int L, bool VEC>
@@ -100,14 +96,12 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_state(ScanParams p) {
     const int ch = tid / L, lane = tid % L;
     const bool own = ch < cs.n;
     const long long dn_at = (long long)(cs.d0 + ch) * N + lane * kS;
-    float a[kS] = {0.f, 0.f, 0.f, 0.f}, h[kS], pr[kS], rg[kS];
+    f2 a[2] = {0ull, 0ull}, h[2] = {0ull, 0ull}, pr[2] = {both(1.f), both(1.f)}, rg[2] = {0ull, 0ull};
     if (own) {
-        to4(a, *reinterpret_cast<const float4 *>(p.A + dn_at));
-#pragma unroll
-        for (int i = 0; i < kS; ++i) a[i] = log2_rate(a[i]);
+        const float4 r = *reinterpret_cast<const float4 *>(p.A + dn_at);
+        a[0] = pair(log2_rate(r.x), log2_rate(r.y));
+        a[1] = pair(log2_rate(r.z), log2_rate(r.w));
     }
-#pragma unroll
-    for (int i = 0; i < kS; ++i) h[i] = rg[i] = 0.f, pr[i] = 1.f;
     const Place at = place_of<CH>(tid, cs);
     float bias[4], dsum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -138,22 +132,25 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_state(ScanParams p) {
         for (int t = 0; t < kTile; ++t) {
             const float2 dx = s_dx[t][ch];
             const float go = s_g[t][ch];
-            float b[4], c[4];
-            to4(b, *reinterpret_cast<const float4 *>(s_bc + t * N + lane * kS));
-            to4(c, *reinterpret_cast<const float4 *>(s_bc + (kTile + t) * N + lane * kS));
+            const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(s_bc + t * N + lane * kS);
+            const ulonglong2 c = *reinterpret_cast<const ulonglong2 *>(s_bc + (kTile + t) * N + lane * kS);
+            const f2 d2 = both(dx.x), x2 = both(dx.y), g2 = both(go);
+            const f2 bb[2] = {b.x, b.y}, cc[2] = {c.x, c.y};
 #pragma unroll
-            for (int i = 0; i < kS; ++i) {
-                const float e = ex2(dx.x * a[i]);
-                h[i] = fmaf(e, h[i], dx.y * b[i]);
-                pr[i] *= e;
-                rg[i] = fmaf(pr[i], c[i] * go, rg[i]);
+            for (int i = 0; i < 2; ++i) {
+                float e0, e1;
+                split(mul2(d2, a[i]), e0, e1);
+                const f2 e = pair(ex2(e0), ex2(e1));
+                h[i] = fma2(e, h[i], mul2(x2, bb[i]));
+                pr[i] = mul2(pr[i], e);
+                rg[i] = fma2(pr[i], mul2(cc[i], g2), rg[i]);
             }
         }
         __syncthreads();
     }
     if (own) {
-        *reinterpret_cast<float4 *>(p.hs + slot * p.D * N + dn_at) = make_float4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<float4 *>(p.gs + slot * p.D * N + dn_at) = make_float4(rg[0], rg[1], rg[2], rg[3]);
+        *reinterpret_cast<ulonglong2 *>(p.hs + slot * p.D * N + dn_at) = make_ulonglong2(h[0], h[1]);
+        *reinterpret_cast<ulonglong2 *>(p.gs + slot * p.D * N + dn_at) = make_ulonglong2(rg[0], rg[1]);
     }
     if (at.t < kTile)
 #pragma unroll
@@ -191,7 +188,7 @@ __global__ void __launch_bounds__(kThreads) scan_bwd(ScanParams p, int parts) {
     float *s_bc = sm + M::kBc;
     float(*s_go)[CH] = reinterpret_cast<float(*)[CH]>(sm + M::kGo);
     float(*s_res)[kTile][CH] = reinterpret_cast<float(*)[kTile][CH]>(sm + M::kRes);
-    float4 *s_start = reinterpret_cast<float4 *>(sm + M::kStart);
+    ulonglong2 *s_start = reinterpret_cast<ulonglong2 *>(sm + M::kStart);
     float *s_red = sm + M::kRed, *s_acc = sm + M::kAcc;
 
     const int tid = threadIdx.x, warp = tid >> 5;
@@ -219,15 +216,23 @@ __global__ void __launch_bounds__(kThreads) scan_bwd(ScanParams p, int parts) {
             }
             continue;
         }
-        float A[kS] = {0.f, 0.f, 0.f, 0.f}, a2[kS], h[kS] = {0.f, 0.f, 0.f, 0.f}, carry[kS] = {0.f, 0.f, 0.f, 0.f};
-        float dA[kS] = {0.f, 0.f, 0.f, 0.f};
+        f2 A[2] = {0ull, 0ull}, a2[2] = {0ull, 0ull}, h[2] = {0ull, 0ull}, carry[2] = {0ull, 0ull}, dA[2] = {0ull, 0ull};
         if (own) {
-            to4(A, *reinterpret_cast<const float4 *>(p.A + (long long)(cs.d0 + ch) * N + lane * kS));
-            to4(h, *reinterpret_cast<const float4 *>(p.hs + dn_at));
-            to4(carry, *reinterpret_cast<const float4 *>(p.gs + dn_at));
+            const float4 r = *reinterpret_cast<const float4 *>(p.A + (long long)(cs.d0 + ch) * N + lane * kS);
+            A[0] = pair(r.x, r.y);
+            A[1] = pair(r.z, r.w);
+            a2[0] = pair(log2_rate(r.x), log2_rate(r.y));
+            a2[1] = pair(log2_rate(r.z), log2_rate(r.w));
+            const ulonglong2 hr = *reinterpret_cast<const ulonglong2 *>(p.hs + dn_at);
+            const ulonglong2 gr = *reinterpret_cast<const ulonglong2 *>(p.gs + dn_at);
+            h[0] = hr.x; h[1] = hr.y;
+            carry[0] = gr.x; carry[1] = gr.y;
         }
-#pragma unroll
-        for (int i = 0; i < kS; ++i) a2[i] = log2_rate(A[i]);
+        auto decay = [&](f2 d2, int i) {  // e^{delta A} of pair i
+            float e0, e1;
+            split(mul2(d2, a2[i]), e0, e1);
+            return pair(ex2(e0), ex2(e1));
+        };
         float bias[4], skip[4], sD[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -255,14 +260,14 @@ __global__ void __launch_bounds__(kThreads) scan_bwd(ScanParams p, int parts) {
             __syncthreads();
 #pragma unroll 2
             for (int q = 0; q < kTile; q += kPiece) {
-                s_start[((k * kTile + q) / kPiece) * kThreads + tid] = make_float4(h[0], h[1], h[2], h[3]);
+                s_start[((k * kTile + q) / kPiece) * kThreads + tid] = make_ulonglong2(h[0], h[1]);
 #pragma unroll
                 for (int t = 0; t < kPiece; ++t) {
                     const float2 dx = s_dx[k * kTile + q + t][ch];
-                    float b[4];
-                    to4(b, *reinterpret_cast<const float4 *>(s_bc + (q + t) * N + lane * kS));
-#pragma unroll
-                    for (int i = 0; i < kS; ++i) h[i] = fmaf(ex2(dx.x * a2[i]), h[i], dx.y * b[i]);
+                    const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(s_bc + (q + t) * N + lane * kS);
+                    const f2 d2 = both(dx.x), x2 = both(dx.y);
+                    h[0] = fma2(decay(d2, 0), h[0], mul2(x2, b.x));
+                    h[1] = fma2(decay(d2, 1), h[1], mul2(x2, b.y));
                 }
             }
             __syncthreads();
@@ -284,8 +289,12 @@ __global__ void __launch_bounds__(kThreads) scan_bwd(ScanParams p, int parts) {
             bc.put(s_bc, true);
             __syncthreads();
             for (int q = kTile - kPiece; q >= 0; q -= kPiece) {
-                float e[kPiece][kS], hh[kPiece + 1][kS];
-                to4(hh[0], s_start[((k * kTile + q) / kPiece) * kThreads + tid]);
+                f2 e[kPiece][2], hh[kPiece + 1][2];
+                {
+                    const ulonglong2 r = s_start[((k * kTile + q) / kPiece) * kThreads + tid];
+                    hh[0][0] = r.x;
+                    hh[0][1] = r.y;
+                }
 #pragma unroll
                 for (int u = 0; u < kPiece; u += 4) {
                     float part4[4];
@@ -293,17 +302,16 @@ __global__ void __launch_bounds__(kThreads) scan_bwd(ScanParams p, int parts) {
                     for (int w = 0; w < 4; ++w) {
                         const int t = u + w;
                         const float2 dx = s_dx[k * kTile + q + t][ch];
-                        float b[4], c[4];
-                        to4(b, *reinterpret_cast<const float4 *>(s_bc + (q + t) * N + lane * kS));
-                        to4(c, *reinterpret_cast<const float4 *>(s_bc + (kTile + q + t) * N + lane * kS));
-                        float y = 0.f;
-#pragma unroll
-                        for (int i = 0; i < kS; ++i) {
-                            e[t][i] = ex2(dx.x * a2[i]);
-                            hh[t + 1][i] = fmaf(e[t][i], hh[t][i], dx.y * b[i]);
-                            y = fmaf(c[i], hh[t + 1][i], y);
+                        const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(s_bc + (q + t) * N + lane * kS);
+                        const f2 d2 = both(dx.x), x2 = both(dx.y);
+                        e[t][0] = decay(d2, 0);
+                        e[t][1] = decay(d2, 1);
+                        hh[t + 1][0] = fma2(e[t][0], hh[t][0], mul2(x2, b.x));
+                        hh[t + 1][1] = fma2(e[t][1], hh[t][1], mul2(x2, b.y));
+                        if (p.z) {
+                            const ulonglong2 c = *reinterpret_cast<const ulonglong2 *>(s_bc + (kTile + q + t) * N + lane * kS);
+                            part4[w] = sum_of(fma2(c.x, hh[t + 1][0], mul2(c.y, hh[t + 1][1])));
                         }
-                        part4[w] = y;
                     }
                     if (p.z) {
                         const float y = sum4<L>(part4, lane);
@@ -318,21 +326,25 @@ __global__ void __launch_bounds__(kThreads) scan_bwd(ScanParams p, int parts) {
                         const int t = u + w;
                         const float2 dx = s_dx[k * kTile + q + t][ch];
                         const float go = s_go[q + t][ch];
-                        float b[4], c[4], v[8];
-                        to4(b, *reinterpret_cast<const float4 *>(s_bc + (q + t) * N + lane * kS));
-                        to4(c, *reinterpret_cast<const float4 *>(s_bc + (kTile + q + t) * N + lane * kS));
-                        ps[w] = pq[w] = 0.f;
+                        const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(s_bc + (q + t) * N + lane * kS);
+                        const ulonglong2 c = *reinterpret_cast<const ulonglong2 *>(s_bc + (kTile + q + t) * N + lane * kS);
+                        const f2 d2 = both(dx.x), x2 = both(dx.y), g2 = both(go);
+                        const f2 bb[2] = {b.x, b.y}, cc[2] = {c.x, c.y};
+                        f2 s2 = 0ull, q2 = 0ull;
+                        float v[8];
 #pragma unroll
-                        for (int i = 0; i < kS; ++i) {
-                            const float gr = fmaf(go, c[i], carry[i]);
-                            carry[i] = gr * e[t][i];
-                            const float qq = carry[i] * hh[t][i];
-                            dA[i] = fmaf(dx.x, qq, dA[i]);
-                            pq[w] = fmaf(qq, A[i], pq[w]);
-                            ps[w] = fmaf(gr, b[i], ps[w]);
-                            v[i] = gr * dx.y;
-                            v[4 + i] = go * hh[t + 1][i];
+                        for (int i = 0; i < 2; ++i) {
+                            const f2 gr = fma2(g2, cc[i], carry[i]);
+                            carry[i] = mul2(gr, e[t][i]);
+                            const f2 qq = mul2(carry[i], hh[t][i]);
+                            dA[i] = fma2(d2, qq, dA[i]);
+                            q2 = fma2(qq, A[i], q2);
+                            s2 = fma2(gr, bb[i], s2);
+                            split(mul2(gr, x2), v[2 * i], v[2 * i + 1]);
+                            split(mul2(g2, hh[t + 1][i]), v[4 + 2 * i], v[5 + 2 * i]);
                         }
+                        ps[w] = sum_of(s2);
+                        pq[w] = sum_of(q2);
                         // sums over the warp's channels: each lane ends with L / 4 of the 8 values
                         int base = 0;
                         if constexpr (L <= 16) {
@@ -400,7 +412,7 @@ __global__ void __launch_bounds__(kThreads) scan_bwd(ScanParams p, int parts) {
             }
             __syncthreads();  // s_res, s_go and s_bc are written again
         }
-        if (own) *reinterpret_cast<float4 *>(p.gs + dn_at) = make_float4(dA[0], dA[1], dA[2], dA[3]);
+        if (own) *reinterpret_cast<ulonglong2 *>(p.gs + dn_at) = make_ulonglong2(dA[0], dA[1]);
         if (at.t < kTile)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
