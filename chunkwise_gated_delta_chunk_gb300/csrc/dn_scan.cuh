@@ -108,6 +108,26 @@ __device__ __forceinline__ void load4(const void *base, long long row, int D, in
     }
 }
 
+// The same as they lie in memory.
+template <typename T, bool VEC>
+__device__ __forceinline__ void load4(const void *base, long long row, int D, int d, int n, bool in, Pack<T, 4> &r) {
+    r.clear();
+    if (!in || n <= 0) return;
+    const T *src = static_cast<const T *>(base) + row * D + d;
+    if constexpr (VEC) {
+        r.load(src);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) {
+                Pack<T, 1> a;
+                a.load(src + i);
+                if constexpr (sizeof(T) == 4) r.w[i] = a.w[0];
+                else r.w[i >> 1] |= a.w[0] << (16 * (i & 1));
+            }
+    }
+}
+
 template <typename T, bool VEC>
 __device__ __forceinline__ void store4(T *dst, int n, const float (&v)[4]) {
     if constexpr (VEC) {

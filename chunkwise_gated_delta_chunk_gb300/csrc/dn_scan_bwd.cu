@@ -57,7 +57,7 @@ __device__ __forceinline__ Place place_of(int tid, const Channels &cs) {
 template <typename T, int N>
 struct BcRows {
     static constexpr int kVecs = kTile * N / 2 / kThreads;
-    float v[kVecs][4];
+    Pack<T, 4> v[kVecs];
     __device__ __forceinline__ void fetch(const ScanParams &p, int g, long long t0, long long t1, bool c_too) {
 #pragma unroll
         for (int k = 0; k < kVecs; ++k) {
@@ -107,27 +107,37 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_state(ScanParams p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) bias[i] = i < at.n && p.dt_bias ? p.dt_bias[cs.d0 + at.c + i] : 0.f;
 
-    for (long long t0 = seq.t0; t0 < seq.t1; t0 += kTile) {
-        BcRows<T, N> bc;
+    BcRows<T, N> bc;
+    Pack<T, 4> fx, fd, fg, fz;
+    auto fetch = [&](long long t0) {  // this thread's rows of a tile, one tile ahead
+        const bool in = t0 + at.t < seq.t1;
         bc.fetch(p, cs.g, t0, seq.t1, true);
+        load4<T, VEC>(p.x, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, fx);
+        load4<T, VEC>(p.dt, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, fd);
+        load4<T, VEC>(p.dy, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, fg);
+        if (p.z) load4<T, VEC>(p.z, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, fz);
+    };
+    fetch(seq.t0);
+    for (long long t0 = seq.t0; t0 < seq.t1; t0 += kTile) {
         if (at.t < kTile) {
             const bool in = t0 + at.t < seq.t1;
-            float fx[4], fd[4], fg[4], fz[4];
-            load4<T, VEC>(p.x, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, fx);
-            load4<T, VEC>(p.dt, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, fd);
-            load4<T, VEC>(p.dy, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, fg);
-            if (p.z) load4<T, VEC>(p.z, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, fz);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float raw = fd[i] + bias[i];
-                const float delta = !in || i >= at.n ? 0.f : p.softplus ? softplus(raw) : raw;
-                s_dx[at.t][at.c + i] = make_float2(delta, delta * fx[i]);
-                s_g[at.t][at.c + i] = p.z ? fg[i] * silu_f(fz[i]) : fg[i];
-                dsum[i] += delta;
+            for (int i = 0; i < 4; i += 2) {
+                const f2 raw = pair(fd[i] + bias[i], fd[i + 1] + bias[i + 1]);
+                float d[2];
+                split(p.softplus ? softplus2(raw) : raw, d[0], d[1]);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float delta = in && i + j < at.n ? d[j] : 0.f;
+                    s_dx[at.t][at.c + i + j] = make_float2(delta, delta * fx[i + j]);
+                    s_g[at.t][at.c + i + j] = p.z ? fg[i + j] * silu_f(fz[i + j]) : fg[i + j];
+                    dsum[i + j] += delta;
+                }
             }
         }
         bc.put(s_bc, true);
         __syncthreads();
+        if (t0 + kTile < seq.t1) fetch(t0 + kTile);
 #pragma unroll 4
         for (int t = 0; t < kTile; ++t) {
             const float2 dx = s_dx[t][ch];
@@ -179,8 +189,14 @@ struct Smem {  // offsets in floats
     static constexpr int kAll = kAcc + kChunk * 2 * N;
 };
 
+#ifndef BWP
+#define BWP 8
+#endif
+#ifndef BWB
+#define BWB 3
+#endif
 template <typename T, int L, bool VEC>
-__global__ void __launch_bounds__(kThreads) scan_bwd(ScanParams p, int parts) {
+__global__ void __launch_bounds__(kThreads, L <= 8 ? BWB : 1) scan_bwd(ScanParams p, int parts) {
     using M = Smem<L>;
     constexpr int N = M::N, CH = M::CH;
     extern __shared__ __align__(16) float sm[];
@@ -239,25 +255,38 @@ __global__ void __launch_bounds__(kThreads) scan_bwd(ScanParams p, int parts) {
             bias[i] = i < at.n && p.dt_bias ? p.dt_bias[cs.d0 + at.c + i] : 0.f;
             skip[i] = i < at.n && p.Dskip ? p.Dskip[cs.d0 + at.c + i] : 0.f;
         }
-        // forward over the chunk: the state at the start of every piece
-        for (int k = 0; k < nt; ++k) {
+        // This thread's rows of a tile, loaded one tile ahead.
+        BcRows<T, N> bc;
+        Pack<T, 4> nx, nd, ng, nz;
+        auto fetch = [&](int k, bool back) {
             const long long t0 = seq.t0 + k * kTile;
-            BcRows<T, N> bc;
-            bc.fetch(p, cs.g, t0, seq.t1, false);
+            const bool in = t0 + at.t < seq.t1;
+            bc.fetch(p, cs.g, t0, seq.t1, back);
+            load4<T, VEC>(p.x, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, nx);
+            load4<T, VEC>(p.dt, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, nd);
+            if (back) load4<T, VEC>(p.dy, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, ng);
+            if (back && p.z) load4<T, VEC>(p.z, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, nz);
+        };
+        // forward over the chunk: the state at the start of every piece
+        fetch(0, false);
+        for (int k = 0; k < nt; ++k) {
             if (at.t < kTile) {
-                const bool in = t0 + at.t < seq.t1;
-                float fx[4], fd[4];
-                load4<T, VEC>(p.x, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, fx);
-                load4<T, VEC>(p.dt, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, fd);
+                const bool in = seq.t0 + k * kTile + at.t < seq.t1;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float raw = fd[i] + bias[i];
-                    const float delta = !in || i >= at.n ? 0.f : p.softplus ? softplus(raw) : raw;
-                    s_dx[k * kTile + at.t][at.c + i] = make_float2(delta, delta * fx[i]);
+                for (int i = 0; i < 4; i += 2) {
+                    const f2 raw = pair(nd[i] + bias[i], nd[i + 1] + bias[i + 1]);
+                    float d0, d1;
+                    split(p.softplus ? softplus2(raw) : raw, d0, d1);
+                    d0 = in && i < at.n ? d0 : 0.f;
+                    d1 = in && i + 1 < at.n ? d1 : 0.f;
+                    s_dx[k * kTile + at.t][at.c + i] = make_float2(d0, d0 * nx[i]);
+                    s_dx[k * kTile + at.t][at.c + i + 1] = make_float2(d1, d1 * nx[i + 1]);
                 }
             }
             bc.put(s_bc, false);
             __syncthreads();
+            if (k + 1 < nt) fetch(k + 1, false);
+            else fetch(k, true);
 #pragma unroll 2
             for (int q = 0; q < kTile; q += kPiece) {
                 s_start[((k * kTile + q) / kPiece) * kThreads + tid] = make_ulonglong2(h[0], h[1]);
@@ -276,18 +305,13 @@ __global__ void __launch_bounds__(kThreads) scan_bwd(ScanParams p, int parts) {
         for (int k = nt - 1; k >= 0; --k) {
             const long long t0 = seq.t0 + k * kTile;
             const bool in = t0 + at.t < seq.t1 && at.t < kTile;
-            BcRows<T, N> bc;
-            bc.fetch(p, cs.g, t0, seq.t1, true);
-            float fx[4], fd[4], fg[4], fz[4];
-            load4<T, VEC>(p.x, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, fx);
-            load4<T, VEC>(p.dt, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, fd);
-            load4<T, VEC>(p.dy, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, fg);
-            if (p.z) load4<T, VEC>(p.z, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, fz);
+            const Pack<T, 4> fx = nx, fd = nd, fg = ng, fz = nz;
             if (at.t < kTile)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) s_go[at.t][at.c + i] = p.z ? fg[i] * silu_f(fz[i]) : fg[i];
             bc.put(s_bc, true);
             __syncthreads();
+            if (k > 0) fetch(k - 1, true);
             for (int q = kTile - kPiece; q >= 0; q -= kPiece) {
                 f2 e[kPiece][2], hh[kPiece + 1][2];
                 {
@@ -495,7 +519,7 @@ int channel_parts(int n_seqs, long long tokens, int D, int G, int N) {
     const int ch = kThreads / (N / kS);
     const long long tiles = (D / G + ch - 1) / ch;
     const long long rows = (tokens / kChunk + n_seqs) * G;
-    const long long want = rows > 0 ? (kSms * 8 + rows - 1) / rows : 1;
+    const long long want = rows > 0 ? (kSms * BWP + rows - 1) / rows : 1;
     return (int)(want < tiles ? want : tiles);
 }
 
@@ -514,6 +538,8 @@ cudaError_t bwd_l(const ScanParams &p, cudaStream_t stream) {
         if (err != cudaSuccess) return err;
         constexpr size_t bytes = Smem<L>::kAll * sizeof(float);
         err = cudaFuncSetAttribute(scan_bwd<T, L, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        if (err != cudaSuccess) return err;
+        err = cudaFuncSetAttribute(scan_bwd<T, L, VEC>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
         if (err != cudaSuccess) return err;
         scan_bwd<T, L, VEC><<<(unsigned)blocks, kThreads, bytes, stream>>>(p, parts);
     }
