@@ -36,8 +36,8 @@ using namespace scan;
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kTile = 16;   // tokens staged at a time
-constexpr int kPiece = 8;   // tokens whose states are in registers
+constexpr int kLen = 64;   // tokens of a chunk
+constexpr int kPiece = 8;  // tokens staged at a time; step 3 holds their states in registers
 
 // One thread's place in a tile's rows: four channels of one token.
 struct Place {
@@ -50,28 +50,28 @@ __device__ __forceinline__ Place place_of(int tid, const Channels &cs) {
     Place r;
     r.t = tid / CV;
     r.c = (tid % CV) * 4;
-    r.n = r.t < kTile ? cs.n - r.c : 0;
+    r.n = r.t < kPiece ? cs.n - r.c : 0;
     return r;
 }
 
 template <typename T, int N>
 struct BcRows {
-    static constexpr int kVecs = kTile * N / 2 / kThreads;
+    static constexpr int kAll = kPiece * N / 2, kVecs = (kAll + kThreads - 1) / kThreads;
     Pack<T, 4> v[kVecs];
     __device__ __forceinline__ void fetch(const ScanParams &p, int g, long long t0, long long t1, bool c_too) {
 #pragma unroll
         for (int k = 0; k < kVecs; ++k) {
-            const int i = threadIdx.x + k * kThreads, which = i / (kTile * N / 4), r = i % (kTile * N / 4);
+            const int i = threadIdx.x + k * kThreads, which = i / (kPiece * N / 4), r = i % (kPiece * N / 4);
             const int t = r / (N / 4), c = (r % (N / 4)) * 4;
-            if (which && !c_too) continue;
+            if (i >= kAll || (which && !c_too)) continue;
             load4<T, true>(which ? p.Cm : p.Bm, (t0 + t) * p.G + g, N, c, 4, t0 + t < t1, v[k]);
         }
     }
-    __device__ __forceinline__ void put(float *bc, bool c_too) {  // bc [2][kTile][N]
+    __device__ __forceinline__ void put(float *bc, bool c_too) {  // bc [2][kPiece][N]
 #pragma unroll
         for (int k = 0; k < kVecs; ++k) {
             const int i = threadIdx.x + k * kThreads;
-            if (i >= kTile * N / 4 && !c_too) continue;
+            if (i >= (c_too ? kAll : kAll / 2)) continue;
             *reinterpret_cast<float4 *>(bc + i * 4) = make_float4(v[k][0], v[k][1], v[k][2], v[k][3]);
         }
     }
@@ -79,28 +79,38 @@ struct BcRows {
 
 // ---- 1: what a chunk does to the state, and its outputs to the state's gradient ------
 
+// A thread holds 4 states of two neighbouring channels: what it reads of Bm and Cm, and
+// (in step 3) its sums over channels, then serve both.
 template <typename T, int L, bool VEC>
 __global__ void __launch_bounds__(kThreads) scan_bwd_state(ScanParams p) {
-    constexpr int N = kS * L, CH = kThreads / L;
-    __shared__ float2 s_dx[kTile][CH];
-    __shared__ float s_g[kTile][CH];
-    __shared__ __align__(16) float s_bc[2 * kTile * N];
+    constexpr int N = kS * L, CH = 2 * kThreads / L;
+    // two tiles in turn: a tile is written where the one before the last lay, which every
+    // thread has left when it is behind the barrier of the last
+    __shared__ __align__(16) float2 s_dx[2][kPiece][CH];
+    __shared__ __align__(16) float s_g[2][kPiece][CH];
+    __shared__ __align__(16) float s_bc[2][2 * kPiece * N];
     const int tid = threadIdx.x;
-    const int tiles = p.G * ((p.D / p.G + CH - 1) / CH);
-    const int ct = blockIdx.x % tiles;
-    const long long slot = blockIdx.x / tiles;
+    const unsigned tiles = p.G * ((p.D / p.G + CH - 1) / CH);
+    const unsigned slot = blockIdx.x / tiles;
+    const int ct = blockIdx.x - slot * tiles;
     if (blockIdx.x == 0) check_offsets(p.seq, tid, kThreads);
-    const SeqTile seq = seq_tile(p.seq, slot, kChunk);
+    const SeqTile seq = seq_tile(p.seq, slot, kLen);
     if (!seq.ok) return;
     const Channels cs = channels_of<CH>(p, ct);
-    const int ch = tid / L, lane = tid % L;
-    const bool own = ch < cs.n;
-    const long long dn_at = (long long)(cs.d0 + ch) * N + lane * kS;
-    f2 a[2] = {0ull, 0ull}, h[2] = {0ull, 0ull}, pr[2] = {both(1.f), both(1.f)}, rg[2] = {0ull, 0ull};
-    if (own) {
-        const float4 r = *reinterpret_cast<const float4 *>(p.A + dn_at);
-        a[0] = pair(log2_rate(r.x), log2_rate(r.y));
-        a[1] = pair(log2_rate(r.z), log2_rate(r.w));
+    const int ch = tid / L * 2, lane = tid % L;  // the first of this thread's channels
+    const bool own[2] = {ch < cs.n, ch + 1 < cs.n};
+    const long long dn = (long long)(cs.d0 + ch) * N + lane * kS, dn_at = (long long)slot * p.D * N + dn;
+    f2 a[2][2], h[2][2], pr[2][2], rg[2][2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        a[c][0] = a[c][1] = 0ull;
+        if (own[c]) {
+            const float4 r = *reinterpret_cast<const float4 *>(p.A + dn + c * N);
+            a[c][0] = pair(log2_rate(r.x), log2_rate(r.y));
+            a[c][1] = pair(log2_rate(r.z), log2_rate(r.w));
+        }
+        h[c][0] = h[c][1] = rg[c][0] = rg[c][1] = 0ull;
+        pr[c][0] = pr[c][1] = both(1.f);
     }
     const Place at = place_of<CH>(tid, cs);
     float bias[4], dsum[4] = {0.f, 0.f, 0.f, 0.f};
@@ -118,59 +128,67 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_state(ScanParams p) {
         if (p.z) load4<T, VEC>(p.z, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, fz);
     };
     fetch(seq.t0);
-    for (long long t0 = seq.t0; t0 < seq.t1; t0 += kTile) {
-        if (at.t < kTile) {
+    int turn = 0;
+    for (long long t0 = seq.t0; t0 < seq.t1; t0 += kPiece, turn ^= 1) {
+        if (at.t < kPiece) {
             const bool in = t0 + at.t < seq.t1;
+            float g[4];
 #pragma unroll
             for (int i = 0; i < 4; i += 2) {
                 const f2 raw = pair(fd[i] + bias[i], fd[i + 1] + bias[i + 1]);
-                float d[2];
-                split(p.softplus ? softplus2(raw) : raw, d[0], d[1]);
+                float d0, d1;
+                split(p.softplus ? softplus2(raw) : raw, d0, d1);
+                d0 = in && i < at.n ? d0 : 0.f;
+                d1 = in && i + 1 < at.n ? d1 : 0.f;
+                *reinterpret_cast<float4 *>(&s_dx[turn][at.t][at.c + i]) = make_float4(d0, d0 * fx[i], d1, d1 * fx[i + 1]);
+                dsum[i] += d0;
+                dsum[i + 1] += d1;
+                g[i] = p.z ? fg[i] * silu_f(fz[i]) : fg[i];
+                g[i + 1] = p.z ? fg[i + 1] * silu_f(fz[i + 1]) : fg[i + 1];
+            }
+            *reinterpret_cast<float4 *>(&s_g[turn][at.t][at.c]) = make_float4(g[0], g[1], g[2], g[3]);
+        }
+        bc.put(s_bc[turn], true);
+        __syncthreads();
+        if (t0 + kPiece < seq.t1) fetch(t0 + kPiece);
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float delta = in && i + j < at.n ? d[j] : 0.f;
-                    s_dx[at.t][at.c + i + j] = make_float2(delta, delta * fx[i + j]);
-                    s_g[at.t][at.c + i + j] = p.z ? fg[i + j] * silu_f(fz[i + j]) : fg[i + j];
-                    dsum[i + j] += delta;
+        for (int t = 0; t < kPiece; ++t) {
+            const float4 dx = *reinterpret_cast<const float4 *>(&s_dx[turn][t][ch]);
+            const float2 go = *reinterpret_cast<const float2 *>(&s_g[turn][t][ch]);
+            const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(s_bc[turn] + t * N + lane * kS);
+            const ulonglong2 cv = *reinterpret_cast<const ulonglong2 *>(s_bc[turn] + (kPiece + t) * N + lane * kS);
+            const f2 bb[2] = {b.x, b.y}, cc[2] = {cv.x, cv.y};
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const f2 d2 = both(c ? dx.z : dx.x), x2 = both(c ? dx.w : dx.y), g2 = both(c ? go.y : go.x);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float e0, e1;
+                    split(mul2(d2, a[c][i]), e0, e1);
+                    const f2 e = pair(ex2(e0), ex2(e1));
+                    h[c][i] = fma2(e, h[c][i], mul2(x2, bb[i]));
+                    pr[c][i] = mul2(pr[c][i], e);
+                    rg[c][i] = fma2(pr[c][i], mul2(cc[i], g2), rg[c][i]);
                 }
             }
         }
-        bc.put(s_bc, true);
-        __syncthreads();
-        if (t0 + kTile < seq.t1) fetch(t0 + kTile);
-#pragma unroll 4
-        for (int t = 0; t < kTile; ++t) {
-            const float2 dx = s_dx[t][ch];
-            const float go = s_g[t][ch];
-            const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(s_bc + t * N + lane * kS);
-            const ulonglong2 c = *reinterpret_cast<const ulonglong2 *>(s_bc + (kTile + t) * N + lane * kS);
-            const f2 d2 = both(dx.x), x2 = both(dx.y), g2 = both(go);
-            const f2 bb[2] = {b.x, b.y}, cc[2] = {c.x, c.y};
+    }
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float e0, e1;
-                split(mul2(d2, a[i]), e0, e1);
-                const f2 e = pair(ex2(e0), ex2(e1));
-                h[i] = fma2(e, h[i], mul2(x2, bb[i]));
-                pr[i] = mul2(pr[i], e);
-                rg[i] = fma2(pr[i], mul2(cc[i], g2), rg[i]);
-            }
+    for (int c = 0; c < 2; ++c)
+        if (own[c]) {
+            *reinterpret_cast<ulonglong2 *>(p.hs + dn_at + c * N) = make_ulonglong2(h[c][0], h[c][1]);
+            *reinterpret_cast<ulonglong2 *>(p.gs + dn_at + c * N) = make_ulonglong2(rg[c][0], rg[c][1]);
         }
-        __syncthreads();
-    }
-    if (own) {
-        *reinterpret_cast<ulonglong2 *>(p.hs + slot * p.D * N + dn_at) = make_ulonglong2(h[0], h[1]);
-        *reinterpret_cast<ulonglong2 *>(p.gs + slot * p.D * N + dn_at) = make_ulonglong2(rg[0], rg[1]);
-    }
-    if (at.t < kTile)
+    __syncthreads();
+    if (at.t < kPiece)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s_g[at.t][at.c + i] = dsum[i];
+        for (int i = 0; i < 4; ++i) s_g[0][at.t][at.c + i] = dsum[i];
     __syncthreads();
     if (tid < cs.n) {
         float s = 0.f;
 #pragma unroll
-        for (int t = 0; t < kTile; ++t) s += s_g[t][tid];
-        p.dsum[slot * p.D + cs.d0 + tid] = s;
+        for (int t = 0; t < kPiece; ++t) s += s_g[0][t][tid];
+        p.dsum[(long long)slot * p.D + cs.d0 + tid] = s;
     }
 }
 
@@ -178,75 +196,72 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_state(ScanParams p) {
 
 template <int L>
 struct Smem {  // offsets in floats
-    static constexpr int N = kS * L, CH = kThreads / L;
-    static constexpr int kDx = 0;                              // float2 [kChunk][CH]
-    static constexpr int kBc = kDx + 2 * kChunk * CH;          // [2][kTile][N]
-    static constexpr int kGo = kBc + 2 * kTile * N;            // [kTile][CH]
-    static constexpr int kRes = kGo + kTile * CH;              // [3][kTile][CH]: s, sum q A, C.h
-    static constexpr int kStart = kRes + 3 * kTile * CH;       // [kChunk / kPiece][kThreads][4]
-    static constexpr int kRed = kStart + kChunk / kPiece * kThreads * 4;  // [kWarps][kPiece][2 N]
-    static constexpr int kAcc = kRed + kWarps * kPiece * 2 * N;  // [kChunk][2 N]
-    static constexpr int kAll = kAcc + kChunk * 2 * N;
+    static constexpr int N = kS * L, CH = 2 * kThreads / L;
+    static constexpr int kDx = 0;                            // float2 [kLen][CH]: delta, delta x
+    static constexpr int kBc = kDx + 2 * kLen * CH;        // [2][2][kPiece][N], two tiles in turn
+    static constexpr int kGo = kBc + 4 * kPiece * N;         // [kPiece][CH]
+    static constexpr int kRes = kGo + kPiece * CH;           // [3][kPiece][CH]: s, sum q A, C.h
+    static constexpr int kStart = kRes + 3 * kPiece * CH;    // [kLen / kPiece][2][kThreads][4]
+    static constexpr int kRed = kStart + kLen / kPiece * 2 * kThreads * 4;  // [kWarps][kPiece][2 N]
+    static constexpr int kAcc = kRed + kWarps * kPiece * 2 * N;               // [kLen][2 N]
+    static constexpr int kAll = kAcc + kLen * 2 * N;
 };
 
-#ifndef BWP
-#define BWP 8
-#endif
-#ifndef BWB
-#define BWB 3
-#endif
 template <typename T, int L, bool VEC>
-__global__ void __launch_bounds__(kThreads, L <= 8 ? BWB : 1) scan_bwd(ScanParams p, int parts) {
+__global__ void __launch_bounds__(kThreads, 2) scan_bwd(ScanParams p, int parts) {
     using M = Smem<L>;
     constexpr int N = M::N, CH = M::CH;
     extern __shared__ __align__(16) float sm[];
     float2(*s_dx)[CH] = reinterpret_cast<float2(*)[CH]>(sm + M::kDx);
-    float *s_bc = sm + M::kBc;
     float(*s_go)[CH] = reinterpret_cast<float(*)[CH]>(sm + M::kGo);
-    float(*s_res)[kTile][CH] = reinterpret_cast<float(*)[kTile][CH]>(sm + M::kRes);
+    float(*s_res)[kPiece][CH] = reinterpret_cast<float(*)[kPiece][CH]>(sm + M::kRes);
     ulonglong2 *s_start = reinterpret_cast<ulonglong2 *>(sm + M::kStart);
     float *s_red = sm + M::kRed, *s_acc = sm + M::kAcc;
 
     const int tid = threadIdx.x, warp = tid >> 5;
-    const long long slot = blockIdx.x / (parts * p.G);
-    const int gp = blockIdx.x % (parts * p.G), g = gp / parts, part = gp % parts;
+    const unsigned split_by = parts * p.G, slot = blockIdx.x / split_by;
+    const int gp = blockIdx.x - slot * split_by, g = gp / parts, part = gp - g * parts;
     const int per = (p.D / p.G + CH - 1) / CH;  // channel tiles of a group
     const int first = (int)((long long)per * part / parts), last = (int)((long long)per * (part + 1) / parts);
-    const SeqTile seq = seq_tile(p.seq, slot, kChunk);
-    const int ch = tid / L, lane = tid % L;
+    const SeqTile seq = seq_tile(p.seq, slot, kLen);
+    const int ch = tid / L * 2, lane = tid % L;  // the first of this thread's channels
     const int len = seq.ok ? (int)(seq.t1 - seq.t0) : 0;
-    const int nt = (len + kTile - 1) / kTile;
+    const int nt = (len + kPiece - 1) / kPiece;
 
     for (int i = tid; i < len * 2 * N; i += kThreads) s_acc[i] = 0.f;
 
     for (int ct = g * per + first; ct < g * per + last; ++ct) {
         const Channels cs = channels_of<CH>(p, ct);
-        const bool own = ch < cs.n;
-        const long long dn_at = slot * p.D * N + (long long)(cs.d0 + ch) * N + lane * kS;
+        const bool own[2] = {ch < cs.n, ch + 1 < cs.n};
+        const long long dn = (long long)(cs.d0 + ch) * N + lane * kS, dn_at = (long long)slot * p.D * N + dn;
         const Place at = place_of<CH>(tid, cs);
         if (nt == 0) {  // a slot without tokens adds nothing
-            if (own) *reinterpret_cast<float4 *>(p.gs + dn_at) = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (tid < cs.n) {
-                p.vec[slot * 2 * p.D + cs.d0 + tid] = 0.f;
-                p.vec[(slot * 2 + 1) * p.D + cs.d0 + tid] = 0.f;
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+                if (own[c]) *reinterpret_cast<float4 *>(p.gs + dn_at + c * N) = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int i = tid; i < 2 * cs.n; i += kThreads) {
+                const int which = i / cs.n, c = i - which * cs.n;
+                p.vec[((long long)slot * 2 + which) * p.D + cs.d0 + c] = 0.f;
             }
             continue;
         }
-        f2 A[2] = {0ull, 0ull}, a2[2] = {0ull, 0ull}, h[2] = {0ull, 0ull}, carry[2] = {0ull, 0ull}, dA[2] = {0ull, 0ull};
-        if (own) {
-            const float4 r = *reinterpret_cast<const float4 *>(p.A + (long long)(cs.d0 + ch) * N + lane * kS);
-            A[0] = pair(r.x, r.y);
-            A[1] = pair(r.z, r.w);
-            a2[0] = pair(log2_rate(r.x), log2_rate(r.y));
-            a2[1] = pair(log2_rate(r.z), log2_rate(r.w));
-            const ulonglong2 hr = *reinterpret_cast<const ulonglong2 *>(p.hs + dn_at);
-            const ulonglong2 gr = *reinterpret_cast<const ulonglong2 *>(p.gs + dn_at);
-            h[0] = hr.x; h[1] = hr.y;
-            carry[0] = gr.x; carry[1] = gr.y;
+        f2 a2[2][2], h[2][2], carry[2][2], dA[2][2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            a2[c][0] = a2[c][1] = h[c][0] = h[c][1] = carry[c][0] = carry[c][1] = dA[c][0] = dA[c][1] = 0ull;
+            if (own[c]) {
+                const float4 r = *reinterpret_cast<const float4 *>(p.A + dn + c * N);
+                a2[c][0] = pair(log2_rate(r.x), log2_rate(r.y));
+                a2[c][1] = pair(log2_rate(r.z), log2_rate(r.w));
+                const ulonglong2 hr = *reinterpret_cast<const ulonglong2 *>(p.hs + dn_at + c * N);
+                const ulonglong2 gr = *reinterpret_cast<const ulonglong2 *>(p.gs + dn_at + c * N);
+                h[c][0] = hr.x; h[c][1] = hr.y;
+                carry[c][0] = gr.x; carry[c][1] = gr.y;
+            }
         }
-        auto decay = [&](f2 d2, int i) {  // e^{delta A} of pair i
+        auto decay = [&](f2 d2, int c, int i) {  // e^{delta A} of pair i of channel c
             float e0, e1;
-            split(mul2(d2, a2[i]), e0, e1);
+            split(mul2(d2, a2[c][i]), e0, e1);
             return pair(ex2(e0), ex2(e1));
         };
         float bias[4], skip[4], sD[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
@@ -259,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, L <= 8 ? BWB : 1) scan_bwd(ScanParam
         BcRows<T, N> bc;
         Pack<T, 4> nx, nd, ng, nz;
         auto fetch = [&](int k, bool back) {
-            const long long t0 = seq.t0 + k * kTile;
+            const long long t0 = seq.t0 + k * kPiece;
             const bool in = t0 + at.t < seq.t1;
             bc.fetch(p, cs.g, t0, seq.t1, back);
             load4<T, VEC>(p.x, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, nx);
@@ -267,11 +282,14 @@ __global__ void __launch_bounds__(kThreads, L <= 8 ? BWB : 1) scan_bwd(ScanParam
             if (back) load4<T, VEC>(p.dy, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, ng);
             if (back && p.z) load4<T, VEC>(p.z, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, nz);
         };
-        // forward over the chunk: the state at the start of every piece
+        auto bc_of = [&](int k) { return sm + M::kBc + (k & 1) * 2 * kPiece * N; };
+        // forward over the chunk: the state at the start of every piece.  A tile's rows of
+        // Bm lie where those of the tile before the last lay, which every thread has left
+        // when it is behind the barrier of the last.
         fetch(0, false);
         for (int k = 0; k < nt; ++k) {
-            if (at.t < kTile) {
-                const bool in = seq.t0 + k * kTile + at.t < seq.t1;
+            if (at.t < kPiece) {
+                const bool in = seq.t0 + k * kPiece + at.t < seq.t1;
 #pragma unroll
                 for (int i = 0; i < 4; i += 2) {
                     const f2 raw = pair(nd[i] + bias[i], nd[i + 1] + bias[i + 1]);
@@ -279,165 +297,187 @@ __global__ void __launch_bounds__(kThreads, L <= 8 ? BWB : 1) scan_bwd(ScanParam
                     split(p.softplus ? softplus2(raw) : raw, d0, d1);
                     d0 = in && i < at.n ? d0 : 0.f;
                     d1 = in && i + 1 < at.n ? d1 : 0.f;
-                    s_dx[k * kTile + at.t][at.c + i] = make_float2(d0, d0 * nx[i]);
-                    s_dx[k * kTile + at.t][at.c + i + 1] = make_float2(d1, d1 * nx[i + 1]);
+                    *reinterpret_cast<float4 *>(&s_dx[k * kPiece + at.t][at.c + i]) = make_float4(d0, d0 * nx[i], d1, d1 * nx[i + 1]);
                 }
             }
+            float *s_bc = bc_of(k);
             bc.put(s_bc, false);
             __syncthreads();
             if (k + 1 < nt) fetch(k + 1, false);
             else fetch(k, true);
-#pragma unroll 2
-            for (int q = 0; q < kTile; q += kPiece) {
-                s_start[((k * kTile + q) / kPiece) * kThreads + tid] = make_ulonglong2(h[0], h[1]);
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+                s_start[(k * 2 + c) * kThreads + tid] = make_ulonglong2(h[c][0], h[c][1]);
+            if (k + 1 < nt) {
 #pragma unroll
                 for (int t = 0; t < kPiece; ++t) {
-                    const float2 dx = s_dx[k * kTile + q + t][ch];
-                    const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(s_bc + (q + t) * N + lane * kS);
-                    const f2 d2 = both(dx.x), x2 = both(dx.y);
-                    h[0] = fma2(decay(d2, 0), h[0], mul2(x2, b.x));
-                    h[1] = fma2(decay(d2, 1), h[1], mul2(x2, b.y));
+                    const float4 dx = *reinterpret_cast<const float4 *>(&s_dx[k * kPiece + t][ch]);
+                    const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(s_bc + t * N + lane * kS);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const f2 d2 = both(c ? dx.z : dx.x), x2 = both(c ? dx.w : dx.y);
+                        h[c][0] = fma2(decay(d2, c, 0), h[c][0], mul2(x2, b.x));
+                        h[c][1] = fma2(decay(d2, c, 1), h[c][1], mul2(x2, b.y));
+                    }
                 }
             }
-            __syncthreads();
         }
         // back over the chunk
         for (int k = nt - 1; k >= 0; --k) {
-            const long long t0 = seq.t0 + k * kTile;
-            const bool in = t0 + at.t < seq.t1 && at.t < kTile;
+            const long long t0 = seq.t0 + k * kPiece;
+            const bool in = t0 + at.t < seq.t1 && at.t < kPiece;
             const Pack<T, 4> fx = nx, fd = nd, fg = ng, fz = nz;
-            if (at.t < kTile)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) s_go[at.t][at.c + i] = p.z ? fg[i] * silu_f(fz[i]) : fg[i];
+            // (the barriers of two tiles lie between the writes of one place of Bm and Cm)
+            float *s_bc = bc_of(nt - 1 - k + nt);
+            if (at.t < kPiece) {
+                float4 go;
+                go.x = p.z ? fg[0] * silu_f(fz[0]) : fg[0];
+                go.y = p.z ? fg[1] * silu_f(fz[1]) : fg[1];
+                go.z = p.z ? fg[2] * silu_f(fz[2]) : fg[2];
+                go.w = p.z ? fg[3] * silu_f(fz[3]) : fg[3];
+                *reinterpret_cast<float4 *>(&s_go[at.t][at.c]) = go;
+            }
             bc.put(s_bc, true);
             __syncthreads();
             if (k > 0) fetch(k - 1, true);
-            for (int q = kTile - kPiece; q >= 0; q -= kPiece) {
-                f2 e[kPiece][2], hh[kPiece + 1][2];
-                {
-                    const ulonglong2 r = s_start[((k * kTile + q) / kPiece) * kThreads + tid];
-                    hh[0][0] = r.x;
-                    hh[0][1] = r.y;
-                }
+            f2 hh[kPiece + 1][2][2];
 #pragma unroll
-                for (int u = 0; u < kPiece; u += 4) {
-                    float part4[4];
+            for (int c = 0; c < 2; ++c) {
+                const ulonglong2 r = s_start[(k * 2 + c) * kThreads + tid];
+                hh[0][c][0] = r.x;
+                hh[0][c][1] = r.y;
+            }
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const int t = u + w;
-                        const float2 dx = s_dx[k * kTile + q + t][ch];
-                        const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(s_bc + (q + t) * N + lane * kS);
-                        const f2 d2 = both(dx.x), x2 = both(dx.y);
-                        e[t][0] = decay(d2, 0);
-                        e[t][1] = decay(d2, 1);
-                        hh[t + 1][0] = fma2(e[t][0], hh[t][0], mul2(x2, b.x));
-                        hh[t + 1][1] = fma2(e[t][1], hh[t][1], mul2(x2, b.y));
-                        if (p.z) {
-                            const ulonglong2 c = *reinterpret_cast<const ulonglong2 *>(s_bc + (kTile + q + t) * N + lane * kS);
-                            part4[w] = sum_of(fma2(c.x, hh[t + 1][0], mul2(c.y, hh[t + 1][1])));
-                        }
-                    }
-                    if (p.z) {
-                        const float y = sum4<L>(part4, lane);
-                        if (lane < 4) s_res[2][q + u + lane][ch] = y;
+            for (int u = 0; u < kPiece; u += 4) {
+                float py[2][4];
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const int t = u + w;
+                    const float4 dx = *reinterpret_cast<const float4 *>(&s_dx[k * kPiece + t][ch]);
+                    const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(s_bc + t * N + lane * kS);
+                    ulonglong2 cc = make_ulonglong2(0ull, 0ull);
+                    if (p.z) cc = *reinterpret_cast<const ulonglong2 *>(s_bc + (kPiece + t) * N + lane * kS);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const f2 d2 = both(c ? dx.z : dx.x), x2 = both(c ? dx.w : dx.y);
+                        hh[t + 1][c][0] = fma2(decay(d2, c, 0), hh[t][c][0], mul2(x2, b.x));
+                        hh[t + 1][c][1] = fma2(decay(d2, c, 1), hh[t][c][1], mul2(x2, b.y));
+                        if (p.z) py[c][w] = sum_of(fma2(cc.x, hh[t + 1][c][0], mul2(cc.y, hh[t + 1][c][1])));
                     }
                 }
+                if (p.z)
 #pragma unroll
-                for (int u = kPiece - 4; u >= 0; u -= 4) {
-                    float ps[4], pq[4];
+                    for (int c = 0; c < 2; ++c) {
+                        const float y = sum4<L>(py[c], lane);
+                        if (lane < 4) s_res[2][u + lane][ch + c] = y;
+                    }
+            }
 #pragma unroll
-                    for (int w = 3; w >= 0; --w) {
-                        const int t = u + w;
-                        const float2 dx = s_dx[k * kTile + q + t][ch];
-                        const float go = s_go[q + t][ch];
-                        const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(s_bc + (q + t) * N + lane * kS);
-                        const ulonglong2 c = *reinterpret_cast<const ulonglong2 *>(s_bc + (kTile + q + t) * N + lane * kS);
-                        const f2 d2 = both(dx.x), x2 = both(dx.y), g2 = both(go);
-                        const f2 bb[2] = {b.x, b.y}, cc[2] = {c.x, c.y};
+            for (int u = kPiece - 4; u >= 0; u -= 4) {
+                float ps[2][4], pq[2][4];
+#pragma unroll
+                for (int w = 3; w >= 0; --w) {
+                    const int t = u + w;
+                    const float4 dx = *reinterpret_cast<const float4 *>(&s_dx[k * kPiece + t][ch]);
+                    const float2 go = *reinterpret_cast<const float2 *>(&s_go[t][ch]);
+                    const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(s_bc + t * N + lane * kS);
+                    const ulonglong2 cv = *reinterpret_cast<const ulonglong2 *>(s_bc + (kPiece + t) * N + lane * kS);
+                    const f2 bb[2] = {b.x, b.y}, cc[2] = {cv.x, cv.y};
+                    f2 vb[2] = {0ull, 0ull}, vc[2] = {0ull, 0ull};  // parts of dB and dC
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const f2 d2 = both(c ? dx.z : dx.x), x2 = both(c ? dx.w : dx.y), g2 = both(c ? go.y : go.x);
                         f2 s2 = 0ull, q2 = 0ull;
-                        float v[8];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            const f2 gr = fma2(g2, cc[i], carry[i]);
-                            carry[i] = mul2(gr, e[t][i]);
-                            const f2 qq = mul2(carry[i], hh[t][i]);
-                            dA[i] = fma2(d2, qq, dA[i]);
-                            q2 = fma2(qq, A[i], q2);
+                            const f2 gr = fma2(g2, cc[i], carry[c][i]);
+                            carry[c][i] = mul2(gr, decay(d2, c, i));
+                            const f2 qq = mul2(carry[c][i], hh[t][c][i]);
+                            dA[c][i] = fma2(d2, qq, dA[c][i]);
+                            q2 = fma2(qq, a2[c][i], q2);
                             s2 = fma2(gr, bb[i], s2);
-                            split(mul2(gr, x2), v[2 * i], v[2 * i + 1]);
-                            split(mul2(g2, hh[t + 1][i]), v[4 + 2 * i], v[5 + 2 * i]);
+                            vb[i] = fma2(gr, x2, vb[i]);
+                            vc[i] = fma2(g2, hh[t + 1][c][i], vc[i]);
                         }
-                        ps[w] = sum_of(s2);
-                        pq[w] = sum_of(q2);
-                        // sums over the warp's channels: each lane ends with L / 4 of the 8 values
-                        int base = 0;
-                        if constexpr (L <= 16) {
-                            fold<8>(v, 16, tid & 16);
-                            base = tid & 16 ? 4 : 0;
-                        }
-                        if constexpr (L <= 8) {
-                            float v4[4] = {v[0], v[1], v[2], v[3]};
-                            fold<4>(v4, 8, tid & 8);
-                            base += tid & 8 ? 2 : 0;
-                            v[0] = v4[0];
-                            v[1] = v4[1];
-                        }
-                        if constexpr (L <= 4) {
-                            float v2[2] = {v[0], v[1]};
-                            fold<2>(v2, 4, tid & 4);
-                            base += tid & 4 ? 1 : 0;
-                            v[0] = v2[0];
-                        }
-#pragma unroll
-                        for (int j = 0; j < L / 4; ++j) {
-                            const int vi = base + j;
-                            s_red[(warp * kPiece + t) * 2 * N + (vi >> 2) * N + lane * kS + (vi & 3)] = v[j];
-                        }
+                        ps[c][w] = sum_of(s2);
+                        pq[c][w] = sum_of(q2);
                     }
-                    const float s = sum4<L>(ps, lane), r = sum4<L>(pq, lane);
+                    float v[8];
+                    split(vb[0], v[0], v[1]);
+                    split(vb[1], v[2], v[3]);
+                    split(vc[0], v[4], v[5]);
+                    split(vc[1], v[6], v[7]);
+                    // sums over the warp's channels: each lane ends with L / 4 of the 8 values
+                    int base = 0;
+                    if constexpr (L <= 16) {
+                        fold<8>(v, 16, tid & 16);
+                        base = tid & 16 ? 4 : 0;
+                    }
+                    if constexpr (L <= 8) {
+                        float v4[4] = {v[0], v[1], v[2], v[3]};
+                        fold<4>(v4, 8, tid & 8);
+                        base += tid & 8 ? 2 : 0;
+                        v[0] = v4[0];
+                        v[1] = v4[1];
+                    }
+                    if constexpr (L <= 4) {
+                        float v2[2] = {v[0], v[1]};
+                        fold<2>(v2, 4, tid & 4);
+                        base += tid & 4 ? 1 : 0;
+                        v[0] = v2[0];
+                    }
+#pragma unroll
+                    for (int j = 0; j < L / 4; ++j) {
+                        const int vi = base + j;
+                        s_red[(warp * kPiece + t) * 2 * N + (vi >> 2) * N + lane * kS + (vi & 3)] = v[j];
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float s = sum4<L>(ps[c], lane), r = sum4<L>(pq[c], lane);
                     if (lane < 4) {
-                        s_res[0][q + u + lane][ch] = s;
-                        s_res[1][q + u + lane][ch] = r;
+                        s_res[0][u + lane][ch + c] = s;
+                        s_res[1][u + lane][ch + c] = r * 0.6931471806f;  // the rates are in units of log2
                     }
                 }
-                __syncthreads();
-                for (int i = tid; i < kPiece * 2 * N; i += kThreads) {
-                    const int t = k * kTile + q + i / (2 * N);
-                    if (t < len) {
-                        float sum = 0.f;
-#pragma unroll
-                        for (int w = 0; w < kWarps; ++w) sum += s_red[w * kPiece * 2 * N + i];
-                        s_acc[t * 2 * N + i % (2 * N)] += sum;
-                    }
-                }
-                __syncthreads();
             }
-            if (at.t < kTile) {
+            __syncthreads();
+            // what follows reads what lies before this barrier, and ends before the next
+            for (int i = tid; i < kPiece * 2 * N; i += kThreads) {
+                const int t = k * kPiece + i / (2 * N);
+                if (t < len) {
+                    float sum = 0.f;
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) sum += s_red[w * kPiece * 2 * N + i];
+                    s_acc[t * 2 * N + i % (2 * N)] += sum;
+                }
+            }
+            if (in && at.n > 0) {
                 float ox[4], od[4], oz[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float s = s_res[0][at.t][at.c + i], r = s_res[1][at.t][at.c + i];
-                    const float delta = s_dx[k * kTile + at.t][at.c + i].x, go = s_go[at.t][at.c + i];
+                    const float delta = s_dx[k * kPiece + at.t][at.c + i].x, go = s_go[at.t][at.c + i];
                     ox[i] = fmaf(delta, s, skip[i] * go);
                     od[i] = fmaf(fx[i], s, r);
                     if (p.softplus) od[i] *= sigmoid_f(fd[i] + bias[i]);
-                    if (p.z) oz[i] = fg[i] * (s_res[2][at.t][at.c + i] + skip[i] * fx[i]) * silu_grad_f(fz[i]);
-                    if (in && i < at.n) {
+                    if (p.z) oz[i] = fg[i] * fmaf(skip[i], fx[i], s_res[2][at.t][at.c + i]) * silu_grad_f(fz[i]);
+                    if (i < at.n) {
                         sD[i] = fmaf(go, fx[i], sD[i]);
                         sb[i] += od[i];
                     }
                 }
-                if (in && at.n > 0) {
-                    const long long o = (t0 + at.t) * p.D + cs.d0 + at.c;
-                    store4<T, VEC>(static_cast<T *>(p.dx) + o, at.n, ox);
-                    store4<T, VEC>(static_cast<T *>(p.ddt) + o, at.n, od);
-                    if (p.z) store4<T, VEC>(static_cast<T *>(p.dz) + o, at.n, oz);
-                }
+                const long long o = (t0 + at.t) * p.D + cs.d0 + at.c;
+                store4<T, VEC>(static_cast<T *>(p.dx) + o, at.n, ox);
+                store4<T, VEC>(static_cast<T *>(p.ddt) + o, at.n, od);
+                if (p.z) store4<T, VEC>(static_cast<T *>(p.dz) + o, at.n, oz);
             }
-            __syncthreads();  // s_res, s_go and s_bc are written again
         }
-        if (own) *reinterpret_cast<ulonglong2 *>(p.gs + dn_at) = make_ulonglong2(dA[0], dA[1]);
-        if (at.t < kTile)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+            if (own[c]) *reinterpret_cast<ulonglong2 *>(p.gs + dn_at + c * N) = make_ulonglong2(dA[c][0], dA[c][1]);
+        __syncthreads();
+        if (at.t < kPiece)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 s_res[0][at.t][at.c + i] = sD[i];
@@ -448,8 +488,8 @@ __global__ void __launch_bounds__(kThreads, L <= 8 ? BWB : 1) scan_bwd(ScanParam
             const int which = i / cs.n, c = i - which * cs.n;
             float s = 0.f;
 #pragma unroll
-            for (int t = 0; t < kTile; ++t) s += s_res[which][t][c];
-            p.vec[(slot * 2 + which) * p.D + cs.d0 + c] = s;
+            for (int t = 0; t < kPiece; ++t) s += s_res[which][t][c];
+            p.vec[((long long)slot * 2 + which) * p.D + cs.d0 + c] = s;
         }
         __syncthreads();
     }
@@ -516,17 +556,17 @@ __global__ void __launch_bounds__(256) scan_bwd_sums(ScanParams p, long long slo
 // Parts that a group's channels are split into: enough blocks to fill the GPU, at
 // most one per tile of channels.
 int channel_parts(int n_seqs, long long tokens, int D, int G, int N) {
-    const int ch = kThreads / (N / kS);
+    const int ch = 2 * kThreads / (N / kS);
     const long long tiles = (D / G + ch - 1) / ch;
-    const long long rows = (tokens / kChunk + n_seqs) * G;
-    const long long want = rows > 0 ? (kSms * BWP + rows - 1) / rows : 1;
+    const long long rows = (tokens / kLen + n_seqs) * G;
+    const long long want = rows > 0 ? (kSms * 32 + rows - 1) / rows : 1;
     return (int)(want < tiles ? want : tiles);
 }
 
 template <typename T, int L, bool VEC>
 cudaError_t bwd_l(const ScanParams &p, cudaStream_t stream) {
-    constexpr int CH = kThreads / L;
-    const long long slots = tile_slots(p.seq, kChunk);
+    constexpr int CH = 2 * kThreads / L;
+    const long long slots = tile_slots(p.seq, kLen);
     const int parts = channel_parts(p.seq.N, p.seq.tokens, p.D, p.G, p.N);
     const long long states = slots * channel_tiles<CH>(p.D, p.G);
     const long long blocks = slots * p.G * parts;
@@ -571,7 +611,7 @@ struct Sizes {
     size_t all() const { return (hs + dsum + gs + vec + bc) * 4; }
 };
 Sizes sizes(int n_seqs, long long tokens, int D, int G, int N) {
-    const size_t slots = (size_t)(tokens / kChunk + n_seqs);
+    const size_t slots = (size_t)(tokens / kLen + n_seqs);
     const size_t parts = (size_t)channel_parts(n_seqs, tokens, D, G, N);
     auto up = [](size_t v) { return (v + 3) / 4 * 4; };
     return {slots * D * N, up(slots * D), slots * D * N, up(slots * 2 * D), parts * (size_t)tokens * G * 2 * N};
@@ -586,7 +626,7 @@ size_t scan_bwd_workspace(int n_seqs, long long tokens, int D, int G, int N) {
 
 void scan_bwd_carve(ScanParams &p, void *workspace) {
     const Sizes s = sizes(p.seq.N, p.seq.tokens, p.D, p.G, p.N);
-    p.chunk = kChunk;
+    p.chunk = kLen;
     p.hs = static_cast<float *>(workspace);
     p.dsum = p.hs + s.hs;
     p.gs = p.dsum + s.dsum;
