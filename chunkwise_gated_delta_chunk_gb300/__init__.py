@@ -22,6 +22,7 @@ and :func:`selective_scan_bwd`, :func:`layer_norm_fwd` and
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -332,21 +333,20 @@ def chunk_bwd(q, k, v, beta, g=None, h0=None, cu_seqlens=None, scale=None, do=No
 
 
 def _operand(name, t, shape, dtype, device, optional=True):
-    """Refuse a tensor that is not what the C entry point takes it for."""
+    """Address of a tensor that is what the C entry point takes it for (else ValueError)."""
     if t is None:
         if optional:
             return None
         raise ValueError("%s is required" % name)
-    if t.device != device or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s, not %s of shape %s on %s%s"
-                         % (name, dtype, tuple(shape), device, t.dtype, tuple(t.shape), t.device,
-                            "" if t.is_contiguous() else ", not contiguous"))
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError("%s must be a contiguous %s tensor of shape %s on %s, not %s of shape %s on %s%s"
+                     % (name, dtype, tuple(shape), device, t.dtype, tuple(t.shape), t.device,
+                        "" if t.is_contiguous() else ", not contiguous"))
 
 
-def _device_of(x):
+def _device_of(x, torch):
     """The device of a call's first tensor, which has to be the current one."""
-    import torch
     device = x.device
     if device.type != "cuda":
         raise ValueError("tensors must be on a CUDA device, not on %s" % device)
@@ -366,6 +366,12 @@ def _sequences(B, cu_seqlens, device):
         raise ValueError("cu_seqlens must have one dimension of N + 1 offsets")
     return cu_seqlens.numel() - 1, _operand("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int64,
                                             device)
+
+
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(entry, *sizes):
+    """What a *_workspace_bytes entry point gives for these sizes (they alone decide)."""
+    return getattr(load(), entry)(*sizes)
 
 
 def _space(nbytes, workspace, device):
@@ -391,7 +397,7 @@ def causal_conv_fwd(x, weight, bias=None, h0=None, cu_seqlens=None, silu=True,
     Returns ``(y, ht)`` (``ht`` is None unless ``output_final_state``).
     """
     import torch
-    device = _device_of(x)
+    device = _device_of(x, torch)
     B, T, D = x.shape
     W = weight.shape[-1]
     f32, dt = torch.float32, x.dtype
@@ -423,7 +429,7 @@ def causal_conv_bwd(x, weight, bias=None, h0=None, cu_seqlens=None, silu=True, d
     ``dweight`` and ``dbias`` (None when bias is None) in fp32.
     """
     import torch
-    device = _device_of(x)
+    device = _device_of(x, torch)
     B, T, D = x.shape
     W = weight.shape[-1]
     f32, dt = torch.float32, x.dtype
@@ -438,8 +444,8 @@ def causal_conv_bwd(x, weight, bias=None, h0=None, cu_seqlens=None, silu=True, d
                dweight=torch.empty((D, W), dtype=f32, device=device),
                dbias=None if bias is None else torch.empty(D, dtype=f32, device=device),
                dh0=None if h0 is None else torch.empty(state, dtype=dt, device=device))
-    workspace, ws, wsb = _space(lib.dn_causal_conv_bwd_workspace_bytes(N, B, T, D, W, code), workspace,
-                                device)
+    need = _workspace_bytes("dn_causal_conv_bwd_workspace_bytes", N, B, T, D, W, code)
+    workspace, ws, wsb = _space(need, workspace, device)
     st = lib.dn_causal_conv_bwd(
         _operand("x", x, x.shape, dt, device), _operand("weight", weight, (D, W), f32, device, False),
         _operand("bias", bias, (D,), f32, device), _operand("h0", h0, state, dt, device), cu, N, B, T,
@@ -454,7 +460,7 @@ def causal_conv_bwd(x, weight, bias=None, h0=None, cu_seqlens=None, silu=True, d
 def _scan_inputs(x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, dt_softplus):
     """Checked addresses and sizes of a scan, in the order of the C arguments."""
     import torch
-    device = _device_of(x)
+    device = _device_of(x, torch)
     Bt, T, Di = x.shape
     G, Ns = B.shape[-2:]
     f32, ty = torch.float32, x.dtype
@@ -492,7 +498,8 @@ def selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, cu
     elif ht is None:
         ht = torch.empty(state, dtype=torch.float32, device=device)
     lib = load()
-    workspace, ws, wsb = _space(lib.dn_selective_scan_fwd_workspace_bytes(*sizes), workspace, device)
+    need = _workspace_bytes("dn_selective_scan_fwd_workspace_bytes", *sizes)
+    workspace, ws, wsb = _space(need, workspace, device)
     st = lib.dn_selective_scan_fwd(*ptrs, *sizes, flags, _operand("y", y, x.shape, ty, device),
                                    _operand("ht", ht, state, torch.float32, device), ws, wsb,
                                    _stream(stream))
@@ -521,7 +528,8 @@ def selective_scan_bwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, cu
                dz=like(z, x.shape, ty), ddt_bias=like(dt_bias, (x.shape[2],), f32),
                dh0=like(h0, state, f32))
     lib = load()
-    workspace, ws, wsb = _space(lib.dn_selective_scan_bwd_workspace_bytes(*sizes), workspace, device)
+    need = _workspace_bytes("dn_selective_scan_bwd_workspace_bytes", *sizes)
+    workspace, ws, wsb = _space(need, workspace, device)
     st = lib.dn_selective_scan_bwd(
         *ptrs, *sizes, flags, _operand("dy", dy, x.shape, ty, device, False),
         _operand("dht", dht, state, f32, device), _ptr(out["dx"]), _ptr(out["ddt"]), _ptr(out["dA"]),
@@ -540,7 +548,7 @@ def layer_norm_fwd(x, weight=None, bias=None, z=None, eps=1e-5, rms=False, strea
     may be x or z.  Returns y.
     """
     import torch
-    device = _device_of(x)
+    device = _device_of(x, torch)
     D = x.shape[-1]
     f32, dt = torch.float32, x.dtype
     if y is None:
@@ -563,7 +571,7 @@ def layer_norm_bwd(x, weight=None, bias=None, z=None, eps=1e-5, rms=False, dy=No
     ``dbias`` in fp32; those of absent inputs are None.
     """
     import torch
-    device = _device_of(x)
+    device = _device_of(x, torch)
     D = x.shape[-1]
     rows = x.numel() // D if D else 0
     f32, dt = torch.float32, x.dtype
@@ -573,9 +581,10 @@ def layer_norm_bwd(x, weight=None, bias=None, z=None, eps=1e-5, rms=False, dy=No
                dweight=None if weight is None else torch.empty(D, dtype=f32, device=device),
                dbias=None if bias is None else torch.empty(D, dtype=f32, device=device),
                dz=None if z is None else torch.empty_like(x, memory_format=torch.contiguous_format))
-    sums = weight is not None or bias is not None
-    workspace, ws, wsb = _space(lib.dn_layer_norm_bwd_workspace_bytes(rows, D, code) if sums else 0,
-                                workspace, device)
+    need = 0
+    if weight is not None or bias is not None:
+        need = _workspace_bytes("dn_layer_norm_bwd_workspace_bytes", rows, D, code)
+    workspace, ws, wsb = _space(need, workspace, device)
     st = lib.dn_layer_norm_bwd(
         _operand("x", x, x.shape, dt, device), _operand("weight", weight, (D,), f32, device),
         _operand("bias", bias, (D,), f32, device), _operand("z", z, x.shape, dt, device), rows, D,

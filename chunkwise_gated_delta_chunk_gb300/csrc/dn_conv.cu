@@ -445,10 +445,12 @@ __global__ void __launch_bounds__(kBwdThreads) conv_bwd(ConvParams p, int cols, 
 }
 
 __global__ void __launch_bounds__(128) conv_bwd_sums(ConvParams p, int rows) {
+    wait_for_launches();
     const long long i = (long long)blockIdx.x * 128 + threadIdx.x;
     if (i >= (long long)(p.W + 1) * p.D) return;
     const int j = (int)(i / p.D), d = (int)(i - (long long)j * p.D);
     float a = 0.f;
+#pragma unroll 8
     for (int r = 0; r < rows; ++r) a += p.partial[((long long)r * (p.W + 1) + j) * p.D + d];
     if (j < p.W) p.dweight[(long long)d * p.W + j] = a;
     else if (p.dbias) p.dbias[d] = a;
@@ -463,8 +465,9 @@ cudaError_t conv_bwd_v(const ConvParams &p, cudaStream_t stream) {
     if (slots > 0x7fffffffLL) return cudaErrorInvalidValue;
     conv_bwd<T, Tg, W, V><<<grid, kBwdThreads, 0, stream>>>(p, cols, (unsigned)slots);
     const long long n = (long long)(W + 1) * p.D;
-    conv_bwd_sums<<<(unsigned)((n + 127) / 128), 128, 0, stream>>>(p, rows);
-    return cudaGetLastError();
+    const cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
+    return launch_after(conv_bwd_sums, dim3((unsigned)((n + 127) / 128)), dim3(128), 0, stream, p, rows);
 }
 
 template <typename T, typename Tg>

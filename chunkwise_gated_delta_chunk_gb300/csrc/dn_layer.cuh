@@ -8,6 +8,25 @@
 
 namespace dn {
 
+// Launch of a kernel that works on what the launch before it in the stream wrote.  It may
+// be set up while that one still runs; the kernel itself calls wait_for_launches() before
+// it touches anything.
+template <typename... P, typename... A>
+inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, A... args) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+__device__ __forceinline__ void wait_for_launches() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // V consecutive elements of T in one access (V = 1, or a power of two whose
 // bytes are the pointer's alignment), as fp32.
 template <typename T, int V>

@@ -376,11 +376,12 @@ __global__ void __launch_bounds__(Row<T, V, K, R>::kThreads) norm_bwd(NormParams
 // dweight and dbias from the blocks' rows: 32 columns and 32 slices of the rows per block.
 __global__ void __launch_bounds__(1024) norm_bwd_sums(NormParams p, int blocks) {
     __shared__ float red[32][33];
+    wait_for_launches();
     const int c = blockIdx.x * 32 + threadIdx.x;
     const int h = blockIdx.y;
     float a = 0.f;
     if (c < p.D)
-#pragma unroll 4
+#pragma unroll 8
         for (int b = threadIdx.y; b < blocks; b += 32) a += p.partial[((long long)b * 2 + h) * p.D + c];
     red[threadIdx.y][threadIdx.x] = a;
     __syncthreads();
@@ -418,8 +419,10 @@ cudaError_t norm_launch_g(const NormParams &p, bool bwd, cudaStream_t stream) {
             cudaError_t err = cudaFuncSetAttribute(norm_bwd<T, V, K, R, GATE>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
             if (err != cudaSuccess) return err;
             norm_bwd<T, V, K, R, GATE><<<grid, kThreads, bytes, stream>>>(p);
+            err = cudaGetLastError();
+            if (err != cudaSuccess) return err;
         }
-        if (p.partial) norm_bwd_sums<<<dim3((p.D + 31) / 32, 2), dim3(32, 32), 0, stream>>>(p, grid);
+        if (p.partial) return launch_after(norm_bwd_sums, dim3((p.D + 31) / 32, 2), dim3(32, 32), 0, stream, p, grid);
     }
     return cudaGetLastError();
 }

@@ -83,6 +83,7 @@ __global__ void __launch_bounds__(32, kResident) scan_fwd(ScanParams p) {
     const unsigned tiles = p.G * ((p.D / p.G + CH - 1) / CH);
     const unsigned slot = blockIdx.x / tiles;
     const int ct = blockIdx.x - slot * tiles;
+    if (!STATE && p.chunk) wait_for_launches();
     if (blockIdx.x == 0) check_offsets(p.seq, tid, 32);
     const SeqTile seq = p.chunk ? seq_tile(p.seq, slot, p.chunk) : seq_whole(p.seq, (int)slot);
     if (!seq.ok) return;
@@ -331,6 +332,7 @@ __global__ void __launch_bounds__(128) scan_step(ScanParams p) {
 template <bool BWD>
 __global__ void __launch_bounds__(128) scan_combine(ScanParams p) {
     constexpr int kAhead = 8;
+    wait_for_launches();
     const long long i = (long long)blockIdx.x * 128 + threadIdx.x;
     const int q = p.N / 4;  // vectors of a channel's states
     const long long per = (long long)p.D * q;
@@ -391,8 +393,10 @@ cudaError_t fwd_l(const ScanParams &p, cudaStream_t stream) {
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
     if (p.chunk) {
         scan_fwd<T, L, PAIR, true><<<(unsigned)grid, 32, 0, stream>>>(p);
-        const cudaError_t err = scan_combine_launch(p, false, stream);
+        cudaError_t err = cudaGetLastError();
+        if (err == cudaSuccess) err = scan_combine_launch(p, false, stream);
         if (err != cudaSuccess) return err;
+        return launch_after(scan_fwd<T, L, PAIR, false>, dim3((unsigned)grid), dim3(32), 0, stream, p);
     }
     scan_fwd<T, L, PAIR, false><<<(unsigned)grid, 32, 0, stream>>>(p);
     return cudaGetLastError();
@@ -443,9 +447,8 @@ cudaError_t scan_combine_launch(const ScanParams &p, bool bwd, cudaStream_t stre
     const long long grid = (n + 127) / 128;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
     if (grid == 0) return cudaSuccess;
-    if (bwd) scan_combine<true><<<dim3((unsigned)grid, 2), 128, 0, stream>>>(p);
-    else scan_combine<false><<<(unsigned)grid, 128, 0, stream>>>(p);
-    return cudaGetLastError();
+    if (bwd) return launch_after(scan_combine<true>, dim3((unsigned)grid, 2), dim3(128), 0, stream, p);
+    return launch_after(scan_combine<false>, dim3((unsigned)grid), dim3(128), 0, stream, p);
 }
 
 size_t scan_fwd_workspace(int n_seqs, long long tokens, int D, int G, int N) {

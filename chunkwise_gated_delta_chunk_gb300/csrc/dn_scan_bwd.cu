@@ -218,6 +218,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd(ScanParams p, int parts)
     ulonglong2 *s_start = reinterpret_cast<ulonglong2 *>(sm + M::kStart);
     float *s_red = sm + M::kRed, *s_acc = sm + M::kAcc;
 
+    wait_for_launches();
     const int tid = threadIdx.x, warp = tid >> 5;
     const unsigned split_by = parts * p.G, slot = blockIdx.x / split_by;
     const int gp = blockIdx.x - slot * split_by, g = gp / parts, part = gp - g * parts;
@@ -505,6 +506,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd(ScanParams p, int parts)
 // after the other in every part.
 template <typename T>
 __global__ void __launch_bounds__(128) scan_bwd_bc(ScanParams p, int parts) {
+    wait_for_launches();
     const long long i = (long long)blockIdx.x * 128 + threadIdx.x;
     const int q = p.N / 2;  // vectors of a row of both
     const long long row = i / q;
@@ -518,6 +520,7 @@ __global__ void __launch_bounds__(128) scan_bwd_bc(ScanParams p, int parts) {
     const float4 *src = reinterpret_cast<const float4 *>(p.bc) + i;
     const long long step = p.seq.tokens * p.G * q;
     float4 s = src[0];
+#pragma unroll 8
     for (int k = 1; k < parts; ++k) {
         const float4 o = src[k * step];
         s.x += o.x; s.y += o.y; s.z += o.z; s.w += o.w;
@@ -532,12 +535,14 @@ __global__ void __launch_bounds__(128) scan_bwd_bc(ScanParams p, int parts) {
 // over the slots: 32 columns and 8 slices of the slots per block.
 __global__ void __launch_bounds__(256) scan_bwd_sums(ScanParams p, long long slots) {
     __shared__ float red[8][32];
+    wait_for_launches();
     const long long cols = blockIdx.y ? 2LL * p.D : (long long)p.D * p.N;
     const long long c = (long long)blockIdx.x * 32 + threadIdx.x;
     if ((long long)blockIdx.x * 32 >= cols) return;
     const float *src = blockIdx.y ? p.vec : p.gs;
     float a = 0.f;
     if (c < cols)
+#pragma unroll 8
         for (long long s = threadIdx.y; s < slots; s += 8) a += src[s * cols + c];
     red[threadIdx.y][threadIdx.x] = a;
     __syncthreads();
@@ -574,24 +579,26 @@ cudaError_t bwd_l(const ScanParams &p, cudaStream_t stream) {
     cudaError_t err = cudaSuccess;
     if (slots > 0) {
         scan_bwd_state<T, L, VEC><<<(unsigned)states, kThreads, 0, stream>>>(p);
-        err = scan_combine_launch(p, true, stream);
+        err = cudaGetLastError();
+        if (err == cudaSuccess) err = scan_combine_launch(p, true, stream);
         if (err != cudaSuccess) return err;
         constexpr size_t bytes = Smem<L>::kAll * sizeof(float);
         err = cudaFuncSetAttribute(scan_bwd<T, L, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
         if (err != cudaSuccess) return err;
         err = cudaFuncSetAttribute(scan_bwd<T, L, VEC>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
         if (err != cudaSuccess) return err;
-        scan_bwd<T, L, VEC><<<(unsigned)blocks, kThreads, bytes, stream>>>(p, parts);
+        err = launch_after(scan_bwd<T, L, VEC>, dim3((unsigned)blocks), dim3(kThreads), bytes, stream, p, parts);
+        if (err != cudaSuccess) return err;
     }
     const long long vecs = p.seq.tokens * p.G * (p.N / 2);
     if (vecs > 0 && p.seq.N > 0) {
         const long long grid = (vecs + 127) / 128;
         if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-        scan_bwd_bc<T><<<(unsigned)grid, 128, 0, stream>>>(p, parts);
+        err = launch_after(scan_bwd_bc<T>, dim3((unsigned)grid), dim3(128), 0, stream, p, parts);
+        if (err != cudaSuccess) return err;
     }
     const long long cols = ((long long)p.D * p.N + 31) / 32;
-    scan_bwd_sums<<<dim3((unsigned)cols, 2), dim3(32, 8), 0, stream>>>(p, slots);
-    return cudaGetLastError();
+    return launch_after(scan_bwd_sums, dim3((unsigned)cols, 2), dim3(32, 8), 0, stream, p, slots);
 }
 
 template <typename T>
