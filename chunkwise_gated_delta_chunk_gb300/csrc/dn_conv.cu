@@ -171,25 +171,30 @@ cudaError_t conv_fwd_t(const ConvParams &p, cudaStream_t stream) {
 
 constexpr int kBwdWarps = 4;
 constexpr int kBwdThreads = kBwdWarps * 32;
-constexpr int kBwdTile = 64;
 constexpr int kGroups = 2;  // groups of tokens in flight (3 and 4 measured 2 % slower)
 
 // Channels of a thread where rows allow it.
 template <typename T>
 constexpr int kBwdV = 8 / (int)sizeof(T);
 
-// Blocks along the tokens: every one writes a row of partial sums, so no more
-// than the GPU holds at once, and each walks the same number of tiles.
-// The tiles are counted from the sizes alone (an upper bound), so that the
-// workspace is known without the offsets.
-int conv_bwd_rows(long long tokens, int n_seqs, int D, int V) {
+// Tokens of a tile (64, or fewer where these make too few warps to fill the GPU; each
+// tile computes W - 1 tokens of the next again) and blocks along the tokens: every block
+// writes a row of partial sums, so no more than the GPU holds at once, and each walks the
+// same number of tiles.  The tiles are counted from the sizes alone (an upper bound), so
+// that the workspace is known without the offsets.
+struct BwdGrid {
+    int tile, rows;
+};
+BwdGrid conv_bwd_grid(long long tokens, int n_seqs, int D, int V) {
     const long long cols = (D + 32 * V - 1) / (32 * V);
-    const long long slots = tokens / kBwdTile + n_seqs;
-    const long long most = (slots + kBwdWarps - 1) / kBwdWarps;
-    if (most <= 1) return 1;
+    BwdGrid g{64, 1};
+    while (g.tile > 16 && (tokens / g.tile + n_seqs) * cols < (long long)kSms * 16) g.tile >>= 1;
+    const long long most = (tokens / g.tile + n_seqs + kBwdWarps - 1) / kBwdWarps;
+    if (most <= 1) return g;
     const long long fill = (kSms * 4 + cols - 1) / cols;
     const long long each = (most + fill - 1) / fill;
-    return (int)((most + each - 1) / each);
+    g.rows = (int)((most + each - 1) / each);
+    return g;
 }
 
 // The rows of x and dy that a thread walks, V elements of each token, fetched
@@ -299,7 +304,7 @@ struct Pairs {
 };
 
 template <typename T, typename Tg, int W, int V>
-__global__ void __launch_bounds__(kBwdThreads) conv_bwd(ConvParams p, int cols, unsigned slots) {
+__global__ void __launch_bounds__(kBwdThreads) conv_bwd(ConvParams p, int len, int cols, unsigned slots) {
     if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(p.seq, threadIdx.x, kBwdThreads);
     constexpr int P = Pairs<V>::P;
     constexpr int K = W == 3 ? 3 : 4;  // tokens of a group: a multiple of W, so that rings of W turn whole
@@ -329,7 +334,7 @@ __global__ void __launch_bounds__(kBwdThreads) conv_bwd(ConvParams p, int cols, 
     const Tg *dy = static_cast<const Tg *>(p.dy) + d0;
     T *dx = static_cast<T *>(p.dx) + d0;
     for (unsigned slot = blockIdx.y * kBwdWarps + warp; own && slot < slots; slot += gridDim.y * kBwdWarps) {
-        const SeqTile tile = seq_tile(p.seq, slot, kBwdTile);
+        const SeqTile tile = seq_tile(p.seq, slot, len);
         if (!tile.ok) continue;
         const long long state = (long long)tile.n * (W - 1) * D + d0;
         const T *h0 = p.h0 ? static_cast<const T *>(p.h0) + state : nullptr;
@@ -459,15 +464,15 @@ __global__ void __launch_bounds__(128) conv_bwd_sums(ConvParams p, int rows) {
 template <typename T, typename Tg, int W, int V>
 cudaError_t conv_bwd_v(const ConvParams &p, cudaStream_t stream) {
     const int cols = p.D / V;
-    const int rows = conv_bwd_rows(p.seq.tokens, p.seq.N, p.D, kBwdV<T>);
-    const dim3 grid((cols + 31) / 32, rows);
-    const long long slots = tile_slots(p.seq, kBwdTile);
+    const BwdGrid g = conv_bwd_grid(p.seq.tokens, p.seq.N, p.D, kBwdV<T>);
+    const dim3 grid((cols + 31) / 32, g.rows);
+    const long long slots = tile_slots(p.seq, g.tile);
     if (slots > 0x7fffffffLL) return cudaErrorInvalidValue;
-    conv_bwd<T, Tg, W, V><<<grid, kBwdThreads, 0, stream>>>(p, cols, (unsigned)slots);
+    conv_bwd<T, Tg, W, V><<<grid, kBwdThreads, 0, stream>>>(p, g.tile, cols, (unsigned)slots);
     const long long n = (long long)(W + 1) * p.D;
     const cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
-    return launch_after(conv_bwd_sums, dim3((unsigned)((n + 127) / 128)), dim3(128), 0, stream, p, rows);
+    return launch_after(conv_bwd_sums, dim3((unsigned)((n + 127) / 128)), dim3(128), 0, stream, p, g.rows);
 }
 
 template <typename T, typename Tg>
@@ -490,7 +495,7 @@ cudaError_t conv_fwd_launch(const ConvParams &p, bool bf16, cudaStream_t stream,
 
 size_t conv_bwd_workspace(long long tokens, int n_seqs, int D, int W, bool bf16) {
     const int V = bf16 ? kBwdV<__nv_bfloat16> : kBwdV<float>;
-    return (size_t)conv_bwd_rows(tokens, n_seqs, D, V) * (size_t)(W + 1) * (size_t)D * 4u;
+    return (size_t)conv_bwd_grid(tokens, n_seqs, D, V).rows * (size_t)(W + 1) * (size_t)D * 4u;
 }
 
 cudaError_t conv_bwd_launch(const ConvParams &p, bool bf16, cudaStream_t stream, const char **name) {

@@ -197,14 +197,14 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_state(ScanParams p) {
 template <int L>
 struct Smem {  // offsets in floats
     static constexpr int N = kS * L, CH = 2 * kThreads / L;
-    static constexpr int kDx = 0;                            // float2 [kLen][CH]: delta, delta x
-    static constexpr int kBc = kDx + 2 * kLen * CH;        // [2][2][kPiece][N], two tiles in turn
-    static constexpr int kGo = kBc + 4 * kPiece * N;         // [kPiece][CH]
-    static constexpr int kRes = kGo + kPiece * CH;           // [3][kPiece][CH]: s, sum q A, C.h
-    static constexpr int kStart = kRes + 3 * kPiece * CH;    // [kLen / kPiece][2][kThreads][4]
+    static constexpr int kD = 0;                           // [kLen][CH]: delta
+    static constexpr int kX = kD + kLen * CH;              // [2][kPiece][CH]: x, two tiles in turn
+    static constexpr int kBc = kX + 2 * kPiece * CH;       // [2][2][kPiece][N], two tiles in turn
+    static constexpr int kGo = kBc + 4 * kPiece * N;       // [kPiece][CH]
+    static constexpr int kRes = kGo + kPiece * CH;         // [3][kPiece][CH]: s, sum q A, C.h
+    static constexpr int kStart = kRes + 3 * kPiece * CH;  // [kLen / kPiece][2][kThreads][4]
     static constexpr int kRed = kStart + kLen / kPiece * 2 * kThreads * 4;  // [kWarps][kPiece][2 N]
-    static constexpr int kAcc = kRed + kWarps * kPiece * 2 * N;               // [kLen][2 N]
-    static constexpr int kAll = kAcc + kLen * 2 * N;
+    static constexpr int kAll = kRed + kWarps * kPiece * 2 * N;
 };
 
 template <typename T, int L, bool VEC>
@@ -212,11 +212,12 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd(ScanParams p, int parts)
     using M = Smem<L>;
     constexpr int N = M::N, CH = M::CH;
     extern __shared__ __align__(16) float sm[];
-    float2(*s_dx)[CH] = reinterpret_cast<float2(*)[CH]>(sm + M::kDx);
+    float(*s_d)[CH] = reinterpret_cast<float(*)[CH]>(sm + M::kD);
+    float(*s_x)[CH] = reinterpret_cast<float(*)[CH]>(sm + M::kX);
     float(*s_go)[CH] = reinterpret_cast<float(*)[CH]>(sm + M::kGo);
     float(*s_res)[kPiece][CH] = reinterpret_cast<float(*)[kPiece][CH]>(sm + M::kRes);
     ulonglong2 *s_start = reinterpret_cast<ulonglong2 *>(sm + M::kStart);
-    float *s_red = sm + M::kRed, *s_acc = sm + M::kAcc;
+    float *s_red = sm + M::kRed;
 
     wait_for_launches();
     const int tid = threadIdx.x, warp = tid >> 5;
@@ -229,7 +230,9 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd(ScanParams p, int parts)
     const int len = seq.ok ? (int)(seq.t1 - seq.t0) : 0;
     const int nt = (len + kPiece - 1) / kPiece;
 
-    for (int i = tid; i < len * 2 * N; i += kThreads) s_acc[i] = 0.f;
+    // the block's row of sums over channels: token t of the chunk at t * bc_step
+    float *bc_out = p.bc + (((long long)part * p.seq.tokens + seq.t0) * p.G + g) * 2 * N;
+    const long long bc_step = (long long)p.G * 2 * N;
 
     for (int ct = g * per + first; ct < g * per + last; ++ct) {
         const Channels cs = channels_of<CH>(p, ct);
@@ -284,6 +287,10 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd(ScanParams p, int parts)
             if (back && p.z) load4<T, VEC>(p.z, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, nz);
         };
         auto bc_of = [&](int k) { return sm + M::kBc + (k & 1) * 2 * kPiece * N; };
+        auto x_of = [&](int k) { return s_x + (k & 1) * kPiece; };
+        auto put_x = [&](int k, const Pack<T, 4> &v) {  // absent channels: zeros, as they were loaded
+            *reinterpret_cast<float4 *>(&x_of(k)[at.t][at.c]) = make_float4(v[0], v[1], v[2], v[3]);
+        };
         // forward over the chunk: the state at the start of every piece.  A tile's rows of
         // Bm lie where those of the tile before the last lay, which every thread has left
         // when it is behind the barrier of the last.
@@ -298,8 +305,9 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd(ScanParams p, int parts)
                     split(p.softplus ? softplus2(raw) : raw, d0, d1);
                     d0 = in && i < at.n ? d0 : 0.f;
                     d1 = in && i + 1 < at.n ? d1 : 0.f;
-                    *reinterpret_cast<float4 *>(&s_dx[k * kPiece + at.t][at.c + i]) = make_float4(d0, d0 * nx[i], d1, d1 * nx[i + 1]);
+                    *reinterpret_cast<float2 *>(&s_d[k * kPiece + at.t][at.c + i]) = make_float2(d0, d1);
                 }
+                put_x(k, nx);
             }
             float *s_bc = bc_of(k);
             bc.put(s_bc, false);
@@ -312,11 +320,12 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd(ScanParams p, int parts)
             if (k + 1 < nt) {
 #pragma unroll
                 for (int t = 0; t < kPiece; ++t) {
-                    const float4 dx = *reinterpret_cast<const float4 *>(&s_dx[k * kPiece + t][ch]);
+                    const float2 dd = *reinterpret_cast<const float2 *>(&s_d[k * kPiece + t][ch]);
+                    const float2 xx = *reinterpret_cast<const float2 *>(&x_of(k)[t][ch]);
                     const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(s_bc + t * N + lane * kS);
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const f2 d2 = both(c ? dx.z : dx.x), x2 = both(c ? dx.w : dx.y);
+                        const f2 d2 = both(c ? dd.y : dd.x), x2 = both(c ? dd.y * xx.y : dd.x * xx.x);
                         h[c][0] = fma2(decay(d2, c, 0), h[c][0], mul2(x2, b.x));
                         h[c][1] = fma2(decay(d2, c, 1), h[c][1], mul2(x2, b.y));
                     }
@@ -329,8 +338,10 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd(ScanParams p, int parts)
             const bool in = t0 + at.t < seq.t1 && at.t < kPiece;
             const Pack<T, 4> fx = nx, fd = nd, fg = ng, fz = nz;
             // (the barriers of two tiles lie between the writes of one place of Bm and Cm)
-            float *s_bc = bc_of(nt - 1 - k + nt);
+            const int turn = nt - 1 - k + nt;
+            float *s_bc = bc_of(turn);
             if (at.t < kPiece) {
+                put_x(turn, fx);
                 float4 go;
                 go.x = p.z ? fg[0] * silu_f(fz[0]) : fg[0];
                 go.y = p.z ? fg[1] * silu_f(fz[1]) : fg[1];
@@ -354,13 +365,14 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd(ScanParams p, int parts)
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
                     const int t = u + w;
-                    const float4 dx = *reinterpret_cast<const float4 *>(&s_dx[k * kPiece + t][ch]);
+                    const float2 dd = *reinterpret_cast<const float2 *>(&s_d[k * kPiece + t][ch]);
+                    const float2 xx = *reinterpret_cast<const float2 *>(&x_of(turn)[t][ch]);
                     const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(s_bc + t * N + lane * kS);
                     ulonglong2 cc = make_ulonglong2(0ull, 0ull);
                     if (p.z) cc = *reinterpret_cast<const ulonglong2 *>(s_bc + (kPiece + t) * N + lane * kS);
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const f2 d2 = both(c ? dx.z : dx.x), x2 = both(c ? dx.w : dx.y);
+                        const f2 d2 = both(c ? dd.y : dd.x), x2 = both(c ? dd.y * xx.y : dd.x * xx.x);
                         hh[t + 1][c][0] = fma2(decay(d2, c, 0), hh[t][c][0], mul2(x2, b.x));
                         hh[t + 1][c][1] = fma2(decay(d2, c, 1), hh[t][c][1], mul2(x2, b.y));
                         if (p.z) py[c][w] = sum_of(fma2(cc.x, hh[t + 1][c][0], mul2(cc.y, hh[t + 1][c][1])));
@@ -379,7 +391,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd(ScanParams p, int parts)
 #pragma unroll
                 for (int w = 3; w >= 0; --w) {
                     const int t = u + w;
-                    const float4 dx = *reinterpret_cast<const float4 *>(&s_dx[k * kPiece + t][ch]);
+                    const float2 dd = *reinterpret_cast<const float2 *>(&s_d[k * kPiece + t][ch]);
+                    const float2 xx = *reinterpret_cast<const float2 *>(&x_of(turn)[t][ch]);
                     const float2 go = *reinterpret_cast<const float2 *>(&s_go[t][ch]);
                     const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(s_bc + t * N + lane * kS);
                     const ulonglong2 cv = *reinterpret_cast<const ulonglong2 *>(s_bc + (kPiece + t) * N + lane * kS);
@@ -387,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd(ScanParams p, int parts)
                     f2 vb[2] = {0ull, 0ull}, vc[2] = {0ull, 0ull};  // parts of dB and dC
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const f2 d2 = both(c ? dx.z : dx.x), x2 = both(c ? dx.w : dx.y), g2 = both(c ? go.y : go.x);
+                        const f2 d2 = both(c ? dd.y : dd.x), x2 = both(c ? dd.y * xx.y : dd.x * xx.x), g2 = both(c ? go.y : go.x);
                         f2 s2 = 0ull, q2 = 0ull;
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
@@ -450,7 +463,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd(ScanParams p, int parts)
                     float sum = 0.f;
 #pragma unroll
                     for (int w = 0; w < kWarps; ++w) sum += s_red[w * kPiece * 2 * N + i];
-                    s_acc[t * 2 * N + i % (2 * N)] += sum;
+                    float *o = bc_out + t * bc_step + i % (2 * N);
+                    *o = ct > g * per + first ? *o + sum : sum;
                 }
             }
             if (in && at.n > 0) {
@@ -458,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd(ScanParams p, int parts)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float s = s_res[0][at.t][at.c + i], r = s_res[1][at.t][at.c + i];
-                    const float delta = s_dx[k * kPiece + at.t][at.c + i].x, go = s_go[at.t][at.c + i];
+                    const float delta = s_d[k * kPiece + at.t][at.c + i], go = s_go[at.t][at.c + i];
                     ox[i] = fmaf(delta, s, skip[i] * go);
                     od[i] = fmaf(fx[i], s, r);
                     if (p.softplus) od[i] *= sigmoid_f(fd[i] + bias[i]);
@@ -493,10 +507,6 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd(ScanParams p, int parts)
             p.vec[((long long)slot * 2 + which) * p.D + cs.d0 + c] = s;
         }
         __syncthreads();
-    }
-    for (int i = tid; i < len * 2 * N; i += kThreads) {
-        const long long t = seq.t0 + i / (2 * N);
-        p.bc[(((long long)part * p.seq.tokens + t) * p.G + g) * 2 * N + i % (2 * N)] = s_acc[i];
     }
 }
 
