@@ -31,23 +31,24 @@ using namespace scan;
 constexpr int kTile = 16;      // tokens whose rows of Bm and Cm are staged at a time
 constexpr int kMinChunk = 64;  // the shortest chunk
 constexpr int kT = 16;         // states of a thread
-constexpr int kResident = 16;  // blocks of an SM (128 registers a thread)
+constexpr int kResident = 16;  // warps of an SM (128 registers a thread)
+constexpr int kCh = 64;        // channels of a block: two for each of its threads, N / kT threads sharing two
 
-// Two neighbouring elements; PAIR: their address is a multiple of their size.
+// Two neighbouring elements; PAIR: their address is a multiple of their size.  (Else
+// they stay apart until they are used: joining them would wait for their loads.)
 template <typename T, bool PAIR>
-__device__ __forceinline__ void load2(Pack<T, 2> &r, const T *src, bool has0, bool has1) {
-    if constexpr (PAIR) {
-        if (has0) r.load(src);
-    } else {
-        Pack<T, 1> a, b;
+struct Two {
+    Pack<T, PAIR ? 2 : 1> a, b;
+    __device__ __forceinline__ void clear() {
         a.clear();
         b.clear();
-        if (has0) a.load(src);
-        if (has1) b.load(src + 1);
-        if constexpr (sizeof(T) == 4) r.w[0] = a.w[0], r.w[1] = b.w[0];
-        else r.w[0] = a.w[0] | b.w[0] << 16;
     }
-}
+    __device__ __forceinline__ void load(const T *src, bool has0, bool has1) {
+        if (has0) a.load(src);
+        if (!PAIR && has1) b.load(src + 1);
+    }
+    __device__ __forceinline__ f2 get() const { return PAIR ? pair(a[0], a[PAIR ? 1 : 0]) : pair(a[0], b[0]); }
+};
 template <typename T, bool PAIR>
 __device__ __forceinline__ void store2(T *dst, float a, float b, bool has0, bool has1) {
     if constexpr (PAIR) {
@@ -67,24 +68,28 @@ __device__ __forceinline__ void store2(T *dst, float a, float b, bool has0, bool
 // ---- the scan over the tokens of a sequence or a chunk ------------------------------
 
 template <typename T, int L, bool PAIR, bool STATE>
-__global__ void __launch_bounds__(32, kResident) scan_fwd(ScanParams p) {
-    constexpr int N = kT * L, CH = 64 / L, Q = kT / 4;
+__global__ void __launch_bounds__(32 * L, kResident / L) scan_fwd(ScanParams p) {
+    constexpr int NT = 32 * L, N = kT * L, CH = kCh, Q = kT / 4;
     constexpr int kWhich = STATE ? 1 : 2;                // Bm alone, or Cm too
-    constexpr int kBc = kTile * N * kWhich / 4 / 32;     // their vectors of a tile per thread
-    constexpr int U = 4;                                // tokens of x, dt, z in flight
+    constexpr int kBc = kTile * N * kWhich / 4 / NT;     // their vectors of a tile per thread
+    constexpr int U = 2;                                 // tokens of x, dt, z in flight
     constexpr int S = N <= 64 ? 2 : 1;                   // tiles of Bm and Cm in flight
-    using Bcs = Ahead<T, kBc, 32, S, true>;
+    using Bcs = Ahead<T, kBc, NT, S, true>;
     __shared__ __align__(16) char ring[Bcs::kBytes];
     __shared__ __align__(16) float s_bc[kTile][kWhich][N];
     constexpr int kRow = 2 * kT + 4;  // a thread's states in shared memory, rows apart by an odd number of vectors
-    __shared__ __align__(16) float s_st[32 * kRow];
+    __shared__ __align__(16) float s_st[L == 1 ? 32 * kRow : 4];
+    auto sync = [] {
+        if constexpr (L == 1) __syncwarp();
+        else __syncthreads();
+    };
 
     const int tid = threadIdx.x;
     const unsigned tiles = p.G * ((p.D / p.G + CH - 1) / CH);
     const unsigned slot = blockIdx.x / tiles;
     const int ct = blockIdx.x - slot * tiles;
     if (!STATE && p.chunk) wait_for_launches();
-    if (blockIdx.x == 0) check_offsets(p.seq, tid, 32);
+    if (blockIdx.x == 0) check_offsets(p.seq, tid, NT);
     const SeqTile seq = p.chunk ? seq_tile(p.seq, slot, p.chunk) : seq_whole(p.seq, (int)slot);
     if (!seq.ok) return;
     if (STATE && seq.t1 >= seq.eos) return;  // nothing starts from the last chunk's end
@@ -98,7 +103,7 @@ __global__ void __launch_bounds__(32, kResident) scan_fwd(ScanParams p) {
     auto fetch_bc = [&](int t0, int s) {
 #pragma unroll
         for (int k = 0; k < kBc; ++k) {
-            const int v = (tid + k * 32) * 4, t = v / (kWhich * N), which = v / N % kWhich, c = v % N;
+            const int v = (tid + k * NT) * 4, t = v / (kWhich * N), which = v / N % kWhich, c = v % N;
             bcs.issue(ring, s, k,
                       static_cast<const T *>(which ? p.Cm : p.Bm) + ((seq.t0 + t0 + t) * p.G + cs.g) * N + c,
                       t0 + t < len ? 4 : 0);
@@ -115,54 +120,77 @@ __global__ void __launch_bounds__(32, kResident) scan_fwd(ScanParams p) {
     const T *zp = gate ? static_cast<const T *>(p.z) + first : xp;
     T *yp = static_cast<T *>(p.y) + first;
     const long long D = p.D;
-    Pack<T, 2> fx[U], fd[U], fz[U];
+    Two<T, PAIR> nx[U], nd[U], nz[U];
+    // All rows of U tokens at once, and waited for at once when the next U are at hand: a
+    // load among those still in flight would make the wait for an older one wait for it too.
+    auto fetch = [&](int left) {
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-        fx[k].clear(), fd[k].clear(), fz[k].clear();
-        if (k < len) {
-            load2<T, PAIR>(fx[k], xp + k * D, has0, has1);
-            load2<T, PAIR>(fd[k], dp + k * D, has0, has1);
-            if (gate) load2<T, PAIR>(fz[k], zp + k * D, has0, has1);
-        }
-    }
-    xp += U * D, dp += U * D, zp += U * D;
+        for (int k = 0; k < U; ++k)
+            if (k < left) {
+                nx[k].load(xp + k * D, has0, has1);
+                nd[k].load(dp + k * D, has0, has1);
+                if (gate) nz[k].load(zp + k * D, has0, has1);
+            }
+        xp += U * D, dp += U * D, zp += U * D;
+    };
+#pragma unroll
+    for (int k = 0; k < U; ++k) nx[k].clear(), nd[k].clear(), nz[k].clear();
+    fetch(len);
 
     f2 a[2][kT / 2], h[2][kT / 2];  // rates and states of both channels
     const float *from = STATE ? nullptr
                         : p.chunk ? p.hs + (long long)slot * p.D * N
                         : p.h0 ? p.h0 + (long long)seq.n * p.D * N : nullptr;
-    // A block's states lie one after the other in memory: they are read in whole lines and
-    // handed to their threads through shared memory (each thread's 32 on their own are 32
-    // lines per access, and measured 10 % of a walk of 112 tokens).
+    // The states of this thread, from or to [channel][N].  L = 1: a block's states lie one
+    // after the other in memory; they are read in whole lines and handed to their threads
+    // through shared memory (each thread's 32 on their own are 32 lines per access).
     auto exchange = [&](auto *global, f2 (&v)[2][kT / 2], bool out) {
-        const int block = cs.n * N;  // floats
-        if (out) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int i = 0; i < Q; ++i)
-                    *reinterpret_cast<ulonglong2 *>(s_st + tid * kRow + c * kT + i * 4) = make_ulonglong2(v[c][2 * i], v[c][2 * i + 1]);
-            __syncwarp();
-        }
-        for (int f = tid * 4; f < block; f += 128) {
-            // float f of the block: channel f / N, state f % N; thread (channel / 2) L + state / 16
-            const int c = f / N, n = f % N;
-            float *sp = s_st + ((c >> 1) * L + n / kT) * kRow + (c & 1) * kT + n % kT;
-            if (out) *reinterpret_cast<float4 *>(const_cast<float *>(global) + f) = *reinterpret_cast<float4 *>(sp);
-            else *reinterpret_cast<float4 *>(sp) = *reinterpret_cast<const float4 *>(global + f);
-        }
-        __syncwarp();
-        if (!out) {
+        if constexpr (L > 1) {
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int i = 0; i < Q; ++i) {
-                    const ulonglong2 r = *reinterpret_cast<const ulonglong2 *>(s_st + tid * kRow + c * kT + i * 4);
                     const bool has = c ? has1 : has0;
-                    v[c][2 * i] = has ? r.x : 0ull;
-                    v[c][2 * i + 1] = has ? r.y : 0ull;
+                    auto *at = global + (long long)(2 * pi + c) * N + lane * kT + i * 4;
+                    if (out) {
+                        if (has) *reinterpret_cast<ulonglong2 *>(const_cast<float *>(at)) = make_ulonglong2(v[c][2 * i], v[c][2 * i + 1]);
+                    } else {
+                        ulonglong2 r = make_ulonglong2(0ull, 0ull);
+                        if (has) r = *reinterpret_cast<const ulonglong2 *>(at);
+                        v[c][2 * i] = r.x;
+                        v[c][2 * i + 1] = r.y;
+                    }
                 }
+        } else {
+            const int block = cs.n * N;  // floats
+            if (out) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int i = 0; i < Q; ++i)
+                        *reinterpret_cast<ulonglong2 *>(s_st + tid * kRow + c * kT + i * 4) =
+                            make_ulonglong2(v[c][2 * i], v[c][2 * i + 1]);
+                __syncwarp();
+            }
+            for (int f = tid * 4; f < block; f += 128) {
+                // float f of the block: channel f / N of thread f / N / 2, state f % N
+                float *sp = s_st + f / N / 2 * kRow + f / N % 2 * kT + f % N;
+                if (out) *reinterpret_cast<float4 *>(const_cast<float *>(global) + f) = *reinterpret_cast<float4 *>(sp);
+                else *reinterpret_cast<float4 *>(sp) = *reinterpret_cast<const float4 *>(global + f);
+            }
             __syncwarp();
+            if (!out) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int i = 0; i < Q; ++i) {
+                        const ulonglong2 r = *reinterpret_cast<const ulonglong2 *>(s_st + tid * kRow + c * kT + i * 4);
+                        const bool has = c ? has1 : has0;
+                        v[c][2 * i] = has ? r.x : 0ull;
+                        v[c][2 * i + 1] = has ? r.y : 0ull;
+                    }
+                __syncwarp();
+            }
         }
     };
     exchange(p.A + (long long)cs.d0 * N, a, false);
@@ -183,41 +211,40 @@ __global__ void __launch_bounds__(32, kResident) scan_fwd(ScanParams p) {
     int stage = 0;
     for (int t0 = 0; t0 < len; t0 += kTile) {
         bcs.wait();
-        __syncwarp();  // the last tile's rows are done with
+        sync();  // the last tile's rows are done with
 #pragma unroll
         for (int k = 0; k < kBc; ++k) {
             const Pack<T, 4> r = bcs.get(ring, stage, k);
-            const int v = (tid + k * 32) * 4;
+            const int v = (tid + k * NT) * 4;
             const bool in = t0 + v / (kWhich * N) < len;  // rows behind the last token: zeros
             *reinterpret_cast<float4 *>(&s_bc[0][0][0] + v) =
                 in ? make_float4(r[0], r[1], r[2], r[3]) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
         fetch_bc(t0 + S * kTile, stage);
         stage = stage + 1 == S ? 0 : stage + 1;
-        __syncwarp();
+        sync();
         for (int u = 0; u < kTile && t0 + u < len; u += U) {
             const int left = len - t0 - u;  // tokens from here on
             // the steps of U tokens together: each is a long chain of its own.  A token
             // behind the last has none, and so leaves the states as they are.
             f2 delta[U];
+            Two<T, PAIR> fx[U], fz[U];
 #pragma unroll
             for (int k = 0; k < U; ++k) {
-                const f2 raw = add2(pair(fd[k][0], fd[k][1]), bias);
-                delta[k] = p.softplus ? softplus2(raw) : raw;
+                fx[k] = nx[k], fz[k] = nz[k];
+                delta[k] = add2(nd[k].get(), bias);
+            }
+            fetch(left - U);
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                if (p.softplus) delta[k] = softplus2(delta[k]);
                 if (k >= left) delta[k] = 0ull;
-                if (k + U < left) load2<T, PAIR>(fd[k], dp, has0, has1);
-                dp += D;
             }
 #pragma unroll
             for (int k = 0; k < U; ++k) {
-                const f2 xs = pair(fx[k][0], fx[k][1]);
+                const f2 xs = fx[k].get();
                 f2 zs = 0ull;
-                if (gate) zs = pair(fz[k][0], fz[k][1]);
-                if (k + U < left) {
-                    load2<T, PAIR>(fx[k], xp, has0, has1);
-                    if (gate) load2<T, PAIR>(fz[k], zp, has0, has1);
-                }
-                xp += D, zp += D;
+                if (gate) zs = fz[k].get();
                 float e0, e1, x0, x1;
                 split(delta[k], e0, e1);
                 split(mul2(delta[k], xs), x0, x1);
@@ -389,16 +416,16 @@ __global__ void __launch_bounds__(128) scan_combine(ScanParams p) {
 template <typename T, int L, bool PAIR>
 cudaError_t fwd_l(const ScanParams &p, cudaStream_t stream) {
     const long long slots = p.chunk ? tile_slots(p.seq, p.chunk) : p.seq.N;
-    const long long grid = slots * channel_tiles<64 / L>(p.D, p.G);
+    const long long grid = slots * channel_tiles<kCh>(p.D, p.G);
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
     if (p.chunk) {
-        scan_fwd<T, L, PAIR, true><<<(unsigned)grid, 32, 0, stream>>>(p);
+        scan_fwd<T, L, PAIR, true><<<(unsigned)grid, 32 * L, 0, stream>>>(p);
         cudaError_t err = cudaGetLastError();
         if (err == cudaSuccess) err = scan_combine_launch(p, false, stream);
         if (err != cudaSuccess) return err;
-        return launch_after(scan_fwd<T, L, PAIR, false>, dim3((unsigned)grid), dim3(32), 0, stream, p);
+        return launch_after(scan_fwd<T, L, PAIR, false>, dim3((unsigned)grid), dim3(32 * L), 0, stream, p);
     }
-    scan_fwd<T, L, PAIR, false><<<(unsigned)grid, 32, 0, stream>>>(p);
+    scan_fwd<T, L, PAIR, false><<<(unsigned)grid, 32 * L, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -434,9 +461,8 @@ cudaError_t step_t(const ScanParams &p, cudaStream_t stream) {
 // chunks as fill them once (one block too many would be a second wave: 4 x 2048 tokens of
 // 2048 channels in 19 chunks take 160 us, in 15 or 20 chunks 190 to 210).
 int fwd_chunk(int n_seqs, long long tokens, int D, int G, int N) {
-    const int ch = 64 / (N / kT);
-    const long long blocks = (long long)n_seqs * G * ((D / G + ch - 1) / ch);
-    const long long parts = (long long)kSms * kResident / blocks;
+    const long long blocks = (long long)n_seqs * G * ((D / G + kCh - 1) / kCh);
+    const long long parts = (long long)kSms * (kResident / (N / kT)) / blocks;
     if (parts < 2 || tokens / n_seqs < 2 * kMinChunk) return 0;
     const long long len = (tokens / n_seqs + parts - 1) / parts;
     return len < kMinChunk ? kMinChunk : (int)((len + kTile - 1) / kTile * kTile);
