@@ -374,13 +374,16 @@ def _workspace_bytes(entry, *sizes):
     return getattr(load(), entry)(*sizes)
 
 
-def _space(nbytes, workspace, device):
+def _space(nbytes, workspace, device, stream):
     """The caller's workspace, or a new one; and its address and bytes."""
     import torch
     if workspace is None:
         if nbytes == 0:
             return None, None, 0
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        if stream is not None:  # it is freed on return: not before that stream is done with it
+            workspace.record_stream(torch.cuda.ExternalStream(stream, device=device)
+                                    if isinstance(stream, int) else stream)
     elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on %s" % device)
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -445,7 +448,7 @@ def causal_conv_bwd(x, weight, bias=None, h0=None, cu_seqlens=None, silu=True, d
                dbias=None if bias is None else torch.empty(D, dtype=f32, device=device),
                dh0=None if h0 is None else torch.empty(state, dtype=dt, device=device))
     need = _workspace_bytes("dn_causal_conv_bwd_workspace_bytes", N, B, T, D, W, code)
-    workspace, ws, wsb = _space(need, workspace, device)
+    workspace, ws, wsb = _space(need, workspace, device, stream)
     st = lib.dn_causal_conv_bwd(
         _operand("x", x, x.shape, dt, device), _operand("weight", weight, (D, W), f32, device, False),
         _operand("bias", bias, (D,), f32, device), _operand("h0", h0, state, dt, device), cu, N, B, T,
@@ -499,7 +502,7 @@ def selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, cu
         ht = torch.empty(state, dtype=torch.float32, device=device)
     lib = load()
     need = _workspace_bytes("dn_selective_scan_fwd_workspace_bytes", *sizes)
-    workspace, ws, wsb = _space(need, workspace, device)
+    workspace, ws, wsb = _space(need, workspace, device, stream)
     st = lib.dn_selective_scan_fwd(*ptrs, *sizes, flags, _operand("y", y, x.shape, ty, device),
                                    _operand("ht", ht, state, torch.float32, device), ws, wsb,
                                    _stream(stream))
@@ -529,7 +532,7 @@ def selective_scan_bwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, cu
                dh0=like(h0, state, f32))
     lib = load()
     need = _workspace_bytes("dn_selective_scan_bwd_workspace_bytes", *sizes)
-    workspace, ws, wsb = _space(need, workspace, device)
+    workspace, ws, wsb = _space(need, workspace, device, stream)
     st = lib.dn_selective_scan_bwd(
         *ptrs, *sizes, flags, _operand("dy", dy, x.shape, ty, device, False),
         _operand("dht", dht, state, f32, device), _ptr(out["dx"]), _ptr(out["ddt"]), _ptr(out["dA"]),
@@ -584,7 +587,7 @@ def layer_norm_bwd(x, weight=None, bias=None, z=None, eps=1e-5, rms=False, dy=No
     need = 0
     if weight is not None or bias is not None:
         need = _workspace_bytes("dn_layer_norm_bwd_workspace_bytes", rows, D, code)
-    workspace, ws, wsb = _space(need, workspace, device)
+    workspace, ws, wsb = _space(need, workspace, device, stream)
     st = lib.dn_layer_norm_bwd(
         _operand("x", x, x.shape, dt, device), _operand("weight", weight, (D,), f32, device),
         _operand("bias", bias, (D,), f32, device), _operand("z", z, x.shape, dt, device), rows, D,

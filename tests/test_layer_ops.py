@@ -509,6 +509,30 @@ def test_calls_on_two_streams_at_once(lib):
         assert same(got1, want1) and same(got2, want2)
 
 
+def test_calls_given_a_stream(lib):
+    """The stream is an argument; the workspace that a call makes for itself outlives the call there."""
+    lengths = [70, 0, 33, 200]
+    cu = ref.offsets(lengths, DEV)
+    s, sg = scan_inputs(torch.bfloat16, D=48, lengths=lengths, seed=35)
+    n, ndy = norm_inputs(torch.bfloat16, 303, 128, seed=35)
+
+    def go(stream):
+        outs = list(lib.selective_scan_fwd(*scan_args(s), cu, stream=stream))
+        outs += lib.selective_scan_bwd(*scan_args(s), cu, dy=sg["dy"], stream=stream).values()
+        outs += lib.layer_norm_bwd(n["x"], n["weight"], n["bias"], dy=ndy, stream=stream).values()
+        return [o for o in outs if o is not None]
+
+    want = go(None)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        got = go(stream)
+        junk = [torch.full((1 << 20,), 7, dtype=torch.uint8, device=DEV) for _ in range(20)]  # the caller's own stream goes on
+        torch.cuda.synchronize()
+        assert same(got, want)
+        del junk
+
+
 def test_calls_captured_and_replayed(lib):
     go, (c, s, n) = all_calls(lib, 34)
     go()
@@ -601,3 +625,65 @@ def test_scan_layer_prompt_then_tokens(lib):
     ref.close(scan_state, ss64, 10 * T + 128, "layer state")
     assert torch.equal(conv_state.double().cpu(), cs64)
     ref.close(torch.cat(ys, 1), want, (10 * T + 256) * ratio, "layer y")
+
+
+# ---- more than 2^31 elements ------------------------------------------------------------
+
+
+def test_conv_beyond_32_bits(lib):
+    """The last tokens of 600000 x 4096 elements."""
+    T, D, n = 600_000, 4096, 40
+    g = torch.Generator(device=DEV).manual_seed(61)
+    x = torch.randn(1, T, D, generator=g, device=DEV, dtype=torch.bfloat16)
+    dy = torch.randn(1, T, D, generator=g, device=DEV, dtype=torch.bfloat16)
+    w = torch.randn(D, 4, generator=g, device=DEV)
+    y, ht = lib.causal_conv_fwd(x, w)
+    assert torch.equal(ht, x[:, -3:])
+    out = lib.causal_conv_bwd(x, w, dy=dy)
+    leaves = ref.in_64_bits(dict(x=x[:, -n - 3:], weight=w), grad=True)
+    y64, _ = ref.conv(leaves)
+    terms = float(x[:, -n:].abs().max()) * float(w.abs().sum(1).max())
+    ref.close(y[:, -n:], y64[:, 3:], 48, "long conv y", scale=terms)
+    grad = ref.gradients([y64], [torch.cat([torch.zeros_like(dy[:, :3]), dy[:, -n:]], 1)], leaves)["x"]
+    ref.close(out["dx"][:, -n:], grad[:, 3:], 48, "long conv dx", scale=max(terms, float(grad.abs().max())))
+    ok(lib)
+
+
+def test_norm_beyond_32_bits(lib):
+    """The last rows of 1100000 x 2048 elements."""
+    rows, D, n = 1_100_000, 2048, 5
+    g = torch.Generator(device=DEV).manual_seed(62)
+    x = torch.randn(rows, D, generator=g, device=DEV, dtype=torch.bfloat16)
+    w = torch.randn(D, generator=g, device=DEV)
+    y = lib.layer_norm_fwd(x, w)
+    leaves = ref.in_64_bits(dict(x=x[-n:], weight=w), grad=True)
+    y64 = ref.norm(leaves)
+    ref.close(y[-n:], y64, 128 * 6, "long norm y")
+    out = lib.layer_norm_bwd(x, w, dy=y)
+    grad = ref.gradients([y64], [y[-n:]], leaves)["x"]
+    ref.close(out["dx"][-n:], grad, 128 * 6, "long norm dx", scale=float((y[-n:].abs().max() * w.abs().max()) * 4))
+
+
+def test_scan_beyond_32_bits(lib):
+    """The last tokens of 1100000 x 2048 elements, whose states forget within a few of them: the decay of a
+    token is at most e^-4, that of the 24 tokens before those compared below e^-96."""
+    T, D, N, n = 1_100_000, 2048, 16, 48
+    g = torch.Generator(device=DEV).manual_seed(63)
+    x = torch.randn(1, T, D, generator=g, device=DEV, dtype=torch.bfloat16)
+    dt = (1 + torch.rand(1, T, D, generator=g, device=DEV)).bfloat16()
+    A = -4 - torch.rand(D, N, generator=g, device=DEV)
+    B = torch.randn(1, T, 1, N, generator=g, device=DEV, dtype=torch.bfloat16)
+    C = torch.randn(1, T, 1, N, generator=g, device=DEV, dtype=torch.bfloat16)
+    y, ht = lib.selective_scan_fwd(x, dt, A, B, C, dt_softplus=False)
+    tail = dict(x=x[:, -n:], dt=dt[:, -n:], A=A, B=B[:, -n:], C=C[:, -n:])
+    leaves = ref.in_64_bits(tail, grad=True)
+    y64, ht64 = ref.scan(leaves, softplus=False)
+    keep = n - 24
+    ref.close(y[:, -keep:], y64[:, -keep:], 10 * n + 64, "long scan y")
+    ref.close(ht, ht64, 10 * n + 64, "long scan ht")
+    dy = y
+    out = lib.selective_scan_bwd(x, dt, A, B, C, dt_softplus=False, dy=dy)
+    grads = ref.gradients([y64], [dy[:, -n:]], leaves)
+    for name in ("x", "dt", "B", "C"):
+        ref.close(out["d" + name][:, -keep:], grads[name][:, -keep:], 30 * n + 64 + D, "long scan d" + name)
+    ok(lib)
