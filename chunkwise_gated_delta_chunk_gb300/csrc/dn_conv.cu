@@ -11,18 +11,18 @@
 //     dx_s = sum_i weight[W-1-i] du_{s+i},  dweight[j] = sum_t du_t x_{t-(W-1)+j},  dbias = sum_t du_t
 // One thread owns 4 (bf16) or 2 (fp32) channels and walks a tile and the W - 1
 // tokens behind it (whose du reach back into the tile), the last W inputs and du in
-// registers.  About 45 instructions per channel and token bound it if written
-// plainly; pairs of channels in the two-wide fp32 instructions, rings of W registers
-// that turn whole within an unrolled group, and a separate path for tokens at a
-// tile's edges bring that to about 20.  Rows come by asynchronous copies into the
-// thread's own part of shared memory, so that they hold no registers.  The sums over
-// tokens stay in registers over all tiles of a block, are joined over its warps and
+// registers.  The rate of issue bounds it: written plainly it takes 182 instructions for
+// 4 channels of a token.  Pairs of channels in the two-wide fp32 instructions, rings of W
+// registers that turn whole within an unrolled group, and a path of its own for tokens at
+// a tile's edges bring that to 106 (and 221 us to 78).  Rows come by asynchronous copies
+// into the thread's own part of shared memory, so that they hold no registers.  The sums
+// over tokens stay in registers over all tiles of a block, are joined over its warps and
 // written as one row per block; a second kernel adds the rows in a fixed order.
 //
 // Both move 2 (forward) and 3 (backward) elements per channel and token for about
 // W products and one exponential each.  Measured (bf16, W = 4, silu, 6144 channels):
-// forward over 20741 packed tokens 94.6 us, 5.39 TB/s, bound by memory; backward over
-// 4 x 2048 tokens 78.6 us, 3.85 TB/s, bound by the rate of issue.
+// forward over 20741 packed tokens 93 us, 5.5 TB/s, bound by memory; backward over
+// 4 x 2048 tokens 78 us, 3.9 TB/s.
 #include <type_traits>
 
 #include "dn_layer.cuh"
@@ -42,21 +42,52 @@ int conv_fwd_tile(const ConvParams &p, long long cols) {
     return 8;
 }
 
-// The taps of V channels: V W consecutive floats.
+// The channels of a thread as pairs: V / 2 of them, or one whose upper half is
+// never stored.
+template <int V>
+struct Pairs {
+    static constexpr int P = (V + 1) / 2;
+    f2 v[P];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < P; ++i) v[i] = 0ull;
+    }
+    template <typename T>
+    __device__ __forceinline__ void from(const Pack<T, V> &a) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) v[i] = pair(a[2 * i], V > 1 ? a[V > 1 ? 2 * i + 1 : 0] : 0.f);
+    }
+    __device__ __forceinline__ void to(float (&a)[V]) const {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            float lo, hi;
+            split(v[i], lo, hi);
+            a[2 * i] = lo;
+            if constexpr (V > 1) a[2 * i + 1] = hi;
+        }
+    }
+};
+
+// The taps (V W consecutive floats) and the bias of V channels.
 template <int W, int V>
-__device__ __forceinline__ void load_taps(const float *weight, float (&w)[W][V]) {
+__device__ __forceinline__ void load_taps(const ConvParams &p, int d0, Pairs<V> (&w)[W], Pairs<V> &b) {
+    constexpr int P = Pairs<V>::P;
+    const float *src = p.weight + (long long)d0 * W;
+    float f[V * W];
     if constexpr (V % 4 == 0) {
         Vec<float, V * W> r;
-        r.load(weight);
+        r.load(src);
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-#pragma unroll
-            for (int j = 0; j < W; ++j) w[j][i] = r.v[i * W + j];
+        for (int i = 0; i < V * W; ++i) f[i] = r.v[i];
     } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i)
+        for (int i = 0; i < V * W; ++i) f[i] = src[i];
+    }
 #pragma unroll
-            for (int j = 0; j < W; ++j) w[j][i] = weight[i * W + j];
+    for (int i = 0; i < P; ++i) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) w[j].v[i] = pair(f[2 * i * W + j], V > 1 ? f[V > 1 ? (2 * i + 1) * W + j : 0] : 0.f);
+        b.v[i] = p.bias ? pair(p.bias[d0 + 2 * i], V > 1 ? p.bias[d0 + (V > 1 ? 2 * i + 1 : 0)] : 0.f) : 0ull;
     }
 }
 
@@ -82,10 +113,8 @@ __global__ void __launch_bounds__(kConvThreads) conv_fwd(ConvParams p, int len, 
         if (t >= tile.bos) past[j].load(x + t * p.D);
         else if (h0) past[j].load(h0 + (t - tile.bos + W - 1) * p.D);
     }
-    float w[W][V], b[V];
-    load_taps<W, V>(p.weight + (long long)d0 * W, w);
-#pragma unroll
-    for (int i = 0; i < V; ++i) b[i] = p.bias ? p.bias[d0 + i] : 0.f;
+    Pairs<V> w[W], b;
+    load_taps<W, V>(p, d0, w, b);
     if (tile.c == 0 && p.ht) {
         // the last W - 1 inputs of the sequence; rows of h0 are all read before
         // any is written (ht may be h0), by the one thread that owns them
@@ -106,34 +135,50 @@ __global__ void __launch_bounds__(kConvThreads) conv_fwd(ConvParams p, int len, 
             last.store(ht + (long long)j * p.D);
         }
     }
-    constexpr int U = kFwdAhead;
+    constexpr int U = kFwdAhead, P = Pairs<V>::P;
+    const int tokens = (int)(tile.t1 - tile.t0);
+    const T *xt = x + tile.t0 * p.D;
+    T *yt = y + tile.t0 * p.D;
+    Pairs<V> before[W - 1];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) before[j].from(past[j]);
     Pack<T, V> next[U];
 #pragma unroll
     for (int k = 0; k < U; ++k)
-        if (tile.t0 + k < tile.t1) next[k].load(x + (tile.t0 + k) * p.D);
-    for (long long t = tile.t0; t < tile.t1; t += U) {
+        if (k < tokens) next[k].load(xt + (long long)k * p.D);
+    for (int t = 0; t < tokens; t += U) {
         Pack<T, V> in[U];
-        const int n = tile.t1 - t < U ? (int)(tile.t1 - t) : U;
+        const int n = tokens - t;  // tokens from here on
+        xt += (long long)U * p.D;
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             in[k] = next[k];
-            if (t + U + k < tile.t1) next[k].load(x + (t + U + k) * p.D);
+            if (U + k < n) next[k].load(xt + (long long)k * p.D);
         }
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             if (k >= n) break;
-            Vec<T, V> out;
+            Pairs<V> now, out;
+            now.from(in[k]);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                float u = fmaf(w[W - 1][i], in[k][i], b[i]);
+            for (int i = 0; i < P; ++i) {
+                f2 u = fma2(w[W - 1].v[i], now.v[i], b.v[i]);
 #pragma unroll
-                for (int j = 0; j < W - 1; ++j) u = fmaf(w[j][i], past[j][i], u);
-                out.v[i] = p.silu ? silu_f(u) : u;
+                for (int j = 0; j < W - 1; ++j) u = fma2(w[j].v[i], before[j].v[i], u);
+                if (p.silu) {
+                    float u0, u1;
+                    split(u, u0, u1);
+                    u = mul2(u, pair(sigmoid_f(u0), sigmoid_f(u1)));
+                }
+                out.v[i] = u;
             }
-            out.store(y + (t + k) * p.D);
+            Vec<T, V> o;
+            out.to(o.v);
+            o.store(yt);
+            yt += p.D;
 #pragma unroll
-            for (int j = 0; j + 1 < W - 1; ++j) past[j] = past[j + 1];
-            past[W - 2] = in[k];
+            for (int j = 0; j + 1 < W - 1; ++j) before[j] = before[j + 1];
+            before[W - 2] = now;
         }
     }
 }
@@ -277,32 +322,6 @@ struct Feed {
     }
 };
 
-// The channels of a thread as pairs: V / 2 of them, or one whose upper half is
-// never stored.
-template <int V>
-struct Pairs {
-    static constexpr int P = (V + 1) / 2;
-    f2 v[P];
-    __device__ __forceinline__ void clear() {
-#pragma unroll
-        for (int i = 0; i < P; ++i) v[i] = 0ull;
-    }
-    template <typename T>
-    __device__ __forceinline__ void from(const Pack<T, V> &a) {
-#pragma unroll
-        for (int i = 0; i < P; ++i) v[i] = pair(a[2 * i], V > 1 ? a[V > 1 ? 2 * i + 1 : 0] : 0.f);
-    }
-    __device__ __forceinline__ void to(float (&a)[V]) const {
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-            float lo, hi;
-            split(v[i], lo, hi);
-            a[2 * i] = lo;
-            if constexpr (V > 1) a[2 * i + 1] = hi;
-        }
-    }
-};
-
 template <typename T, typename Tg, int W, int V>
 __global__ void __launch_bounds__(kBwdThreads) conv_bwd(ConvParams p, int len, int cols, unsigned slots) {
     if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(p.seq, threadIdx.x, kBwdThreads);
@@ -317,19 +336,11 @@ __global__ void __launch_bounds__(kBwdThreads) conv_bwd(ConvParams p, int len, i
     const long long D = p.D;
 
     Pairs<V> w[W], b, sw[W], sb;  // sw, sb: sums over this thread's tokens
-    {
-        float f[W][V];
-        if (own) load_taps<W, V>(p.weight + (long long)d0 * W, f);
+    b.clear();
+    sb.clear();
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-#pragma unroll
-            for (int j = 0; j < W; ++j) w[j].v[i] = pair(f[j][2 * i], V > 1 ? f[j][V > 1 ? 2 * i + 1 : 0] : 0.f);
-            b.v[i] = pair(own && p.bias ? p.bias[d0 + 2 * i] : 0.f, V > 1 && own && p.bias ? p.bias[d0 + 2 * i + 1] : 0.f);
-        }
-        sb.clear();
-#pragma unroll
-        for (int j = 0; j < W; ++j) sw[j].clear();
-    }
+    for (int j = 0; j < W; ++j) w[j].clear(), sw[j].clear();
+    if (own) load_taps<W, V>(p, d0, w, b);
     const T *x = static_cast<const T *>(p.x) + d0;
     const Tg *dy = static_cast<const Tg *>(p.dy) + d0;
     T *dx = static_cast<T *>(p.dx) + d0;

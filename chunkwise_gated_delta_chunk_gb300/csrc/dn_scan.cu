@@ -3,17 +3,19 @@
 //     delta = softplus(dt + dt_bias),  h[n] = e^{delta A[n]} h[n] + delta B[n] x,
 //     y = (sum_n C[n] h[n] + Dskip x) silu(z)
 //
-// A thread owns two neighbouring channels and 16 of their states (N / 16 lanes share
-// a channel pair), a block is one warp, and walks the tokens of one sequence or of
-// one chunk of it.  So a row of x, dt, z and y is read and written by its own
-// threads without any exchange, delta is computed where it is used, and only the
-// rows of Bm and Cm, which all channels of a group share, go through shared memory:
-// what a thread loads there serves two channels.  (With 4 states of one channel per
-// thread the shared-memory pipe and the shuffles of the sum over n took most of the
-// time: 39 instructions and 13 shared-memory cycles per 8 channels and token.)
+// A thread owns two neighbouring channels and 16 of their states (N / 16 threads share a
+// channel pair, a block has 64 channels), and walks the tokens of one sequence or of one
+// chunk of it.  So a row of x, dt, z and y is read and written by its own threads
+// without any exchange, delta is computed where it is used, and only the rows of Bm and
+// Cm, which all channels of a group share, go through shared memory: what a thread loads
+// there serves two channels.  (With 4 states of one channel per thread the shared-memory
+// pipe, 13 of its cycles per 8 channels and token, and the shuffles of the sum over n took
+// most of the time: 252 us at the shape below.)
 //
-// What bounds it: N exponentials and 2 N paired fp32 instructions per channel and
-// token against 6 to 8 bytes.
+// What bounds it: N exponentials (32 a cycle and SM) and 2 N paired fp32 instructions (64
+// pairs a cycle and SM) per channel and token, each 36 us of the shape below, against 6 to
+// 8 bytes (20 us).  Both pipes are half busy: 128 registers a thread leave 4 warps for
+// each scheduler, and more of them spill.
 //
 // Few channels leave most SMs idle, so sequences are then cut into chunks: one
 // launch computes each chunk's state from zero and its sum of delta, a second
@@ -21,6 +23,10 @@
 // e^{A sum delta} times the one at its start, plus the chunk's own), and the
 // scan itself starts every chunk from its state.  A single token has a kernel of its
 // own, one thread per 4 states, so that the states are read and written in whole lines.
+//
+// Measured (bf16, N = 16, gate): 4 x 2048 tokens of 2048 channels 161 us (states 64,
+// their steps 8, scan 89); 64 x 256 tokens of 4096 channels, uncut, 341 us; one token of
+// 64 sequences, 2048 channels, 7 us.
 #include "dn_scan.cuh"
 
 namespace dn {
