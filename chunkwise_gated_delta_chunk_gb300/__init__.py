@@ -350,9 +350,16 @@ def _device_of(x, torch):
     device = x.device
     if device.type != "cuda":
         raise ValueError("tensors must be on a CUDA device, not on %s" % device)
-    if device.index != torch.cuda.current_device():
+    if device.index != torch._C._cuda_getDevice():
         raise ValueError("tensors are on %s, which is not the current device" % device)
     return device
+
+
+def _stream_on(device, stream, torch):
+    """Handle of the given stream, or of the current one of this (the current) device."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _sequences(B, cu_seqlens, device):
@@ -417,7 +424,7 @@ def causal_conv_fwd(x, weight, bias=None, h0=None, cu_seqlens=None, silu=True,
         _operand("x", x, x.shape, dt, device), _operand("weight", weight, (D, W), f32, device, False),
         _operand("bias", bias, (D,), f32, device), _operand("h0", h0, state, dt, device), cu, N, B, T,
         D, W, code, DN_CONV_SILU if silu else 0, _operand("y", y, x.shape, dt, device),
-        _operand("ht", ht, state, dt, device), _stream(stream))
+        _operand("ht", ht, state, dt, device), _stream_on(device, stream, torch))
     if st != DN_OK:
         raise DnError(st, "dn_causal_conv_fwd")
     return y, ht
@@ -454,7 +461,8 @@ def causal_conv_bwd(x, weight, bias=None, h0=None, cu_seqlens=None, silu=True, d
         _operand("bias", bias, (D,), f32, device), _operand("h0", h0, state, dt, device), cu, N, B, T,
         D, W, code, DN_CONV_SILU if silu else 0, _operand("dy", dy, x.shape, gt, device),
         dtype_code(gt), _operand("dht", dht, state, dt, device), out["dx"].data_ptr(),
-        out["dweight"].data_ptr(), _ptr(out["dbias"]), _ptr(out["dh0"]), ws, wsb, _stream(stream))
+        out["dweight"].data_ptr(), _ptr(out["dbias"]), _ptr(out["dh0"]), ws, wsb,
+        _stream_on(device, stream, torch))
     if st != DN_OK:
         raise DnError(st, "dn_causal_conv_bwd")
     return out
@@ -505,7 +513,7 @@ def selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, cu
     workspace, ws, wsb = _space(need, workspace, device, stream)
     st = lib.dn_selective_scan_fwd(*ptrs, *sizes, flags, _operand("y", y, x.shape, ty, device),
                                    _operand("ht", ht, state, torch.float32, device), ws, wsb,
-                                   _stream(stream))
+                                   _stream_on(device, stream, torch))
     if st != DN_OK:
         raise DnError(st, "dn_selective_scan_fwd")
     return y, ht
@@ -537,7 +545,7 @@ def selective_scan_bwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, cu
         *ptrs, *sizes, flags, _operand("dy", dy, x.shape, ty, device, False),
         _operand("dht", dht, state, f32, device), _ptr(out["dx"]), _ptr(out["ddt"]), _ptr(out["dA"]),
         _ptr(out["dB"]), _ptr(out["dC"]), _ptr(out["dD"]), _ptr(out["dz"]), _ptr(out["ddt_bias"]),
-        _ptr(out["dh0"]), ws, wsb, _stream(stream))
+        _ptr(out["dh0"]), ws, wsb, _stream_on(device, stream, torch))
     if st != DN_OK:
         raise DnError(st, "dn_selective_scan_bwd")
     return out
@@ -560,7 +568,7 @@ def layer_norm_fwd(x, weight=None, bias=None, z=None, eps=1e-5, rms=False, strea
         _operand("x", x, x.shape, dt, device), _operand("weight", weight, (D,), f32, device),
         _operand("bias", bias, (D,), f32, device), _operand("z", z, x.shape, dt, device),
         x.numel() // D if D else 0, D, dtype_code(dt), eps, DN_NORM_RMS if rms else 0,
-        _operand("y", y, x.shape, dt, device), _stream(stream))
+        _operand("y", y, x.shape, dt, device), _stream_on(device, stream, torch))
     if st != DN_OK:
         raise DnError(st, "dn_layer_norm_fwd")
     return y
@@ -593,7 +601,7 @@ def layer_norm_bwd(x, weight=None, bias=None, z=None, eps=1e-5, rms=False, dy=No
         _operand("bias", bias, (D,), f32, device), _operand("z", z, x.shape, dt, device), rows, D,
         code, eps, DN_NORM_RMS if rms else 0, _operand("dy", dy, x.shape, dt, device, False),
         out["dx"].data_ptr(), _ptr(out["dweight"]), _ptr(out["dbias"]), _ptr(out["dz"]), ws, wsb,
-        _stream(stream))
+        _stream_on(device, stream, torch))
     if st != DN_OK:
         raise DnError(st, "dn_layer_norm_bwd")
     return out

@@ -113,6 +113,13 @@ __global__ void __launch_bounds__(kConvThreads) conv_fwd(ConvParams p, int len, 
         if (t >= tile.bos) past[j].load(x + t * p.D);
         else if (h0) past[j].load(h0 + (t - tile.bos + W - 1) * p.D);
     }
+    constexpr int U = kFwdAhead, P = Pairs<V>::P;
+    const int tokens = (int)(tile.t1 - tile.t0);
+    const T *xt = x + tile.t0 * p.D;
+    Pack<T, V> next[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+        if (k < tokens) next[k].load(xt + (long long)k * p.D);
     Pairs<V> w[W], b;
     load_taps<W, V>(p, d0, w, b);
     if (tile.c == 0 && p.ht) {
@@ -135,17 +142,10 @@ __global__ void __launch_bounds__(kConvThreads) conv_fwd(ConvParams p, int len, 
             last.store(ht + (long long)j * p.D);
         }
     }
-    constexpr int U = kFwdAhead, P = Pairs<V>::P;
-    const int tokens = (int)(tile.t1 - tile.t0);
-    const T *xt = x + tile.t0 * p.D;
     T *yt = y + tile.t0 * p.D;
     Pairs<V> before[W - 1];
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) before[j].from(past[j]);
-    Pack<T, V> next[U];
-#pragma unroll
-    for (int k = 0; k < U; ++k)
-        if (k < tokens) next[k].load(xt + (long long)k * p.D);
     for (int t = 0; t < tokens; t += U) {
         Pack<T, V> in[U];
         const int n = tokens - t;  // tokens from here on
@@ -183,9 +183,52 @@ __global__ void __launch_bounds__(kConvThreads) conv_fwd(ConvParams p, int len, 
     }
 }
 
+// One token per sequence: all loads of a thread at once, and few registers, so that the
+// whole call is one wave (the kernel above, one token of 64 sequences and 6144 channels:
+// 7 us, half of it in a second wave of 8 blocks).
+template <typename T, int W, int V>
+__global__ void __launch_bounds__(kConvThreads) conv_step(ConvParams p, int cols, unsigned nbx) {
+    const unsigned n = blockIdx.x / nbx;
+    const int col = (int)(blockIdx.x - n * nbx) * kConvThreads + threadIdx.x;
+    if (col >= cols) return;
+    const int d0 = col * V;
+    const long long state = (long long)n * (W - 1) * p.D + d0;
+    Pack<T, V> in[W];  // the last W - 1 inputs, the oldest first, and the token's own
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+        in[j].clear();
+        if (p.h0) in[j].load(static_cast<const T *>(p.h0) + state + (long long)j * p.D);
+    }
+    in[W - 1].load(static_cast<const T *>(p.x) + (long long)n * p.D + d0);
+    Pairs<V> w[W], b;
+    load_taps<W, V>(p, d0, w, b);
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+        Pairs<V> v;
+        v.from(in[j]);
+#pragma unroll
+        for (int i = 0; i < Pairs<V>::P; ++i) b.v[i] = fma2(w[j].v[i], v.v[i], b.v[i]);
+    }
+    Vec<T, V> out;
+    b.to(out.v);
+#pragma unroll
+    for (int i = 0; i < V; ++i) out.v[i] = p.silu ? silu_f(out.v[i]) : out.v[i];
+    out.store(static_cast<T *>(p.y) + (long long)n * p.D + d0);
+    if (p.ht)
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) in[j + 1].store(static_cast<T *>(p.ht) + state + (long long)j * p.D);
+}
+
 template <typename T, int W, int V>
 cudaError_t conv_fwd_v(const ConvParams &p, cudaStream_t stream) {
     const int cols = p.D / V;
+    if (!p.seq.cu && p.seq.T == 1) {
+        const long long nbx = (cols + kConvThreads - 1) / kConvThreads, grid = nbx * p.seq.N;
+        if (grid <= 0x7fffffffLL) {
+            conv_step<T, W, V><<<(unsigned)grid, kConvThreads, 0, stream>>>(p, cols, (unsigned)nbx);
+            return cudaGetLastError();
+        }
+    }
     const int len = conv_fwd_tile(p, cols);
     const long long slots = tile_slots(p.seq, len);
     int tx = 8;

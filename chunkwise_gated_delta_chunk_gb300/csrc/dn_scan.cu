@@ -311,50 +311,67 @@ __global__ void __launch_bounds__(32 * L, kResident / L) scan_fwd(ScanParams p) 
 
 // ---- one token per sequence ----------------------------------------------------------
 
-// One thread per four states: L = N / 4 lanes of a channel.
-template <typename T, int L>
+// One thread per four states (L = N / 4 lanes of a channel) of K sequences, blockIdx.y and
+// every gridDim.y-th behind it: the loads of all of them are in flight at once, and the
+// rates are read once.
+template <typename T, int L, int K>
 __global__ void __launch_bounds__(128) scan_step(ScanParams p) {
     constexpr int N = kS * L;
-    const long long i = (long long)blockIdx.x * 128 + threadIdx.x;
-    const unsigned row = (unsigned)(i / L);  // sequence and channel
-    const int lane = threadIdx.x % L;
-    const unsigned n = row / (unsigned)p.D, d = row - n * p.D;
-    const bool in = n < (unsigned)p.seq.N;
-    float part = 0.f, x = 0.f;
+    const unsigned at = blockIdx.x * 128 + threadIdx.x, d = at / L;
+    const int lane = at % L;
+    const bool in = d < (unsigned)p.D;
+    float part[K], x[K], z[K];
     if (in) {
         const unsigned g = d / (unsigned)(p.D / p.G);
-        const long long bc = ((long long)n * p.G + g) * N + lane * kS;
-        Vec<T, 4> b, c;
-        Vec<T, 1> fx, fd;
-        fx.load(static_cast<const T *>(p.x) + row);
-        fd.load(static_cast<const T *>(p.dt) + row);
-        b.load(static_cast<const T *>(p.Bm) + bc);
-        c.load(static_cast<const T *>(p.Cm) + bc);
         const float4 A = *reinterpret_cast<const float4 *>(p.A + (long long)d * N + lane * kS);
-        float4 h = make_float4(0.f, 0.f, 0.f, 0.f);
-        const long long at = (long long)row * N + lane * kS;
-        if (p.h0) h = *reinterpret_cast<const float4 *>(p.h0 + at);
-        const float raw = fd.v[0] + (p.dt_bias ? p.dt_bias[d] : 0.f);
-        const float delta = p.softplus ? softplus(raw) : raw;
-        x = fx.v[0];
-        const float dx = delta * x;
-        h.x = fmaf(ex2(delta * log2_rate(A.x)), h.x, dx * b.v[0]);
-        h.y = fmaf(ex2(delta * log2_rate(A.y)), h.y, dx * b.v[1]);
-        h.z = fmaf(ex2(delta * log2_rate(A.z)), h.z, dx * b.v[2]);
-        h.w = fmaf(ex2(delta * log2_rate(A.w)), h.w, dx * b.v[3]);
-        if (p.ht) *reinterpret_cast<float4 *>(p.ht + at) = h;
-        part = fmaf(c.v[0], h.x, fmaf(c.v[1], h.y, fmaf(c.v[2], h.z, c.v[3] * h.w)));
+        Vec<T, 4> b[K], c[K];
+        Vec<T, 1> fx[K], fd[K], fz[K];
+        float4 h[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const long long n = blockIdx.y + k * gridDim.y;
+            if (n >= p.seq.N) break;
+            const long long row = n * p.D + d, bc = (n * p.G + g) * N + lane * kS;
+            h[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (p.h0) h[k] = *reinterpret_cast<const float4 *>(p.h0 + row * N + lane * kS);
+            fx[k].load(static_cast<const T *>(p.x) + row);
+            fd[k].load(static_cast<const T *>(p.dt) + row);
+            if (p.z) fz[k].load(static_cast<const T *>(p.z) + row);
+            b[k].load(static_cast<const T *>(p.Bm) + bc);
+            c[k].load(static_cast<const T *>(p.Cm) + bc);
+        }
+        const float bias = p.dt_bias ? p.dt_bias[d] : 0.f;
+        const float a[4] = {log2_rate(A.x), log2_rate(A.y), log2_rate(A.z), log2_rate(A.w)};
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const long long n = blockIdx.y + k * gridDim.y;
+            if (n >= p.seq.N) break;
+            const float raw = fd[k].v[0] + bias, delta = p.softplus ? softplus(raw) : raw;
+            x[k] = fx[k].v[0];
+            if (p.z) z[k] = fz[k].v[0];
+            const float dx = delta * x[k];
+            h[k].x = fmaf(ex2(delta * a[0]), h[k].x, dx * b[k].v[0]);
+            h[k].y = fmaf(ex2(delta * a[1]), h[k].y, dx * b[k].v[1]);
+            h[k].z = fmaf(ex2(delta * a[2]), h[k].z, dx * b[k].v[2]);
+            h[k].w = fmaf(ex2(delta * a[3]), h[k].w, dx * b[k].v[3]);
+            if (p.ht) *reinterpret_cast<float4 *>(p.ht + (n * p.D + d) * N + lane * kS) = h[k];
+            part[k] = fmaf(c[k].v[0], h[k].x, fmaf(c[k].v[1], h[k].y, fmaf(c[k].v[2], h[k].z, c[k].v[3] * h[k].w)));
+        }
     }
 #pragma unroll
-    for (int bit = 1; bit < L; bit <<= 1) part += __shfl_xor_sync(0xffffffffu, part, bit);
-    if (in && lane == 0) {
-        Vec<T, 1> out, z;
-        out.v[0] = p.Dskip ? fmaf(p.Dskip[d], x, part) : part;
-        if (p.z) {
-            z.load(static_cast<const T *>(p.z) + row);
-            out.v[0] *= silu_f(z.v[0]);
-        }
-        out.store(static_cast<T *>(p.y) + row);
+    for (int bit = 1; bit < L; bit <<= 1)
+#pragma unroll
+        for (int k = 0; k < K; ++k) part[k] += __shfl_xor_sync(0xffffffffu, part[k], bit);
+    if (!in || lane != 0) return;
+    const float skip = p.Dskip ? p.Dskip[d] : 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const long long n = blockIdx.y + k * gridDim.y;
+        if (n >= p.seq.N) break;
+        Vec<T, 1> out;
+        out.v[0] = p.Dskip ? fmaf(skip, x[k], part[k]) : part[k];
+        if (p.z) out.v[0] *= silu_f(z[k]);
+        out.store(static_cast<T *>(p.y) + n * p.D + d);
     }
 }
 
@@ -446,20 +463,31 @@ cudaError_t fwd_t(const ScanParams &p, cudaStream_t stream) {
     }
 }
 
-// Whether every sequence is one token, and their channels can be counted in 32 bits.
-bool one_token(const ScanParams &p) { return !p.seq.cu && p.seq.T == 1 && p.seq.tokens * p.D < 0x80000000LL; }
+// Whether every sequence is one token (and the grid of their kernel can hold them).
+bool one_token(const ScanParams &p) {
+    return !p.seq.cu && p.seq.T == 1 && p.seq.N <= 4 * 65535 && (long long)p.D * (p.N / kS) < 0x7fffff00LL;
+}
+
+// Four sequences a thread where that still makes a block for most places of the GPU.
+template <typename T, int L>
+cudaError_t step_l(const ScanParams &p, cudaStream_t stream) {
+    const long long cols = ((long long)p.D * L + 127) / 128;
+    const int rows = (p.seq.N + 3) / 4;
+    if (cols * rows >= kSms * 4 || p.seq.N > 65535)
+        scan_step<T, L, 4><<<dim3((unsigned)cols, rows), 128, 0, stream>>>(p);
+    else
+        scan_step<T, L, 1><<<dim3((unsigned)cols, p.seq.N), 128, 0, stream>>>(p);
+    return cudaGetLastError();
+}
 
 template <typename T>
 cudaError_t step_t(const ScanParams &p, cudaStream_t stream) {
-    const long long grid = (p.seq.tokens * p.D * (p.N / kS) + 127) / 128;
-    if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
     switch (p.N) {
-        case 16: scan_step<T, 4><<<(unsigned)grid, 128, 0, stream>>>(p); break;
-        case 32: scan_step<T, 8><<<(unsigned)grid, 128, 0, stream>>>(p); break;
-        case 64: scan_step<T, 16><<<(unsigned)grid, 128, 0, stream>>>(p); break;
-        default: scan_step<T, 32><<<(unsigned)grid, 128, 0, stream>>>(p); break;
+        case 16: return step_l<T, 4>(p, stream);
+        case 32: return step_l<T, 8>(p, stream);
+        case 64: return step_l<T, 16>(p, stream);
+        default: return step_l<T, 32>(p, stream);
     }
-    return cudaGetLastError();
 }
 
 // Length of the chunks that a forward's sequences are cut into; 0: they are not.  Whole

@@ -242,6 +242,38 @@ def test_scan_steps_in_place_continue_a_prompt(lib):
     ref.close(state, ht64, 10 * 150 + 64, "steps ht")
 
 
+@pytest.mark.parametrize("n", [1, 3, 64, 613])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_single_tokens(lib, dtype, n):
+    """One token of n sequences, with and without a state before it."""
+    for h0 in (True, False):
+        t, grads = scan_inputs(dtype, B=n, T=1, D=36, G=2, h0=h0, seed=n)
+        scan_check(lib, t, grads, None, "scan one token", dht=h0)
+        t, grads = conv_inputs(dtype, B=n, T=1, D=36, h0=h0, seed=n)
+        conv_check(lib, t, grads, None, True, "conv one token", dht=h0)
+    t, grads = conv_inputs(dtype, B=n, T=1, D=7, W=3, seed=n)
+    conv_check(lib, t, grads, None, False, "conv one token", dht=True)
+
+
+def test_many_single_tokens(lib):
+    """More sequences than a grid has rows of blocks."""
+    n, D = 300_000, 8
+    g = torch.Generator(device=DEV).manual_seed(64)
+    rnd = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
+    x, dt, B, C, A = rnd(n, 1, D), rnd(n, 1, D), rnd(n, 1, 1, 16), rnd(n, 1, 1, 16), -rnd(D, 16).abs()
+    for m in (300_000, 262_000, 66_000):
+        y, ht = lib.selective_scan_fwd(x[:m], dt[:m], A, B[:m], C[:m])
+        tail = dict(x=x[m - 3:m], dt=dt[m - 3:m], A=A, B=B[m - 3:m], C=C[m - 3:m])
+        y64, ht64 = ref.scan(ref.in_64_bits(tail))
+        ref.close(y[-3:], y64, 74, "many y")
+        ref.close(ht[-3:], ht64, 74, "many ht")
+    w = rnd(D, 4)
+    y, ht = lib.causal_conv_fwd(x, w)
+    y64, ht64 = ref.conv(ref.in_64_bits(dict(x=x[-3:], weight=w)))
+    ref.close(y[-3:], y64, 48, "many conv")
+    assert torch.equal(ht[-3:].double().cpu(), ht64)
+
+
 def test_scan_long_prompt_in_place(lib):
     """A single sequence long enough to be cut into chunks, its state given back in the buffer it came in."""
     t, _ = scan_inputs(torch.float32, B=1, T=1000, D=12, seed=12)
