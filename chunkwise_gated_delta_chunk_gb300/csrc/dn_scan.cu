@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(32 * L, kResident / L) scan_fwd(ScanParams p) 
     constexpr int kBc = kTile * N * kWhich / 4 / NT;     // their vectors of a tile per thread
     constexpr int U = 2;                                 // tokens of x, dt, z in flight
     constexpr int S = N <= 64 ? 2 : 1;                   // tiles of Bm and Cm in flight
-    using Bcs = Ahead<T, kBc, NT, S, true>;
+    using Bcs = Ahead<T, kBc, NT, S>;
     __shared__ __align__(16) char ring[Bcs::kBytes];
     __shared__ __align__(16) float s_bc[kTile][kWhich][N];
     constexpr int kRow = 2 * kT + 4;  // a thread's states in shared memory, rows apart by an odd number of vectors
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(32 * L, kResident / L) scan_fwd(ScanParams p) 
             const int v = (tid + k * NT) * 4, t = v / (kWhich * N), which = v / N % kWhich, c = v % N;
             bcs.issue(ring, s, k,
                       static_cast<const T *>(which ? p.Cm : p.Bm) + ((seq.t0 + t0 + t) * p.G + cs.g) * N + c,
-                      t0 + t < len ? 4 : 0);
+                      t0 + t < len);
         }
         bcs.commit();
     };

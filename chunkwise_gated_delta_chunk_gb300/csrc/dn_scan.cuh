@@ -1,9 +1,6 @@
-// What the selective scan's kernels share: how channels and states lie on
-// threads, the tiles of tokens in shared memory, and the sums over lanes.
-//
-// Every thread holds 4 of a channel's N states, so a channel takes
-// L = N / 4 neighbouring lanes and a warp 32 / L channels.  A block works on
-// channels of one group (they read the same rows of Bm and Cm).
+// What the selective scan's kernels share: softplus, the channels of a block
+// (all of one group: they read the same rows of Bm and Cm), loads of rows, and
+// the sums over lanes.
 #pragma once
 
 #include "dn_layer.cuh"
@@ -11,7 +8,7 @@
 namespace dn {
 namespace scan {
 
-constexpr int kS = 4;  // states of a thread
+constexpr int kS = 4;  // states in one access: those of a thread in the backward and the single-token kernel
 
 // log(1 + e^v) = max(v, 0) + log(1 + e^-|v|) without loss on either side (for v << 0
 // it is e^v).  With q = e^-|v| in (0, 1], log(1 + q) = 2 atanh(s), s = q / (2 + q) in
@@ -85,48 +82,21 @@ inline int channel_tiles(int D, int G) {
     return G * ((D / G + CH - 1) / CH);
 }
 
-// Four neighbouring channels of one token as fp32; absent ones are 0.
-// VEC: rows and tiles begin on a multiple of four elements.
+// Four neighbouring channels of one token as they lie in memory; absent ones are 0.
+// VEC: rows and tiles begin on a multiple of four elements.  (Else they stay apart until
+// they are used: joining them would wait for their loads.)
 template <typename T, bool VEC>
-__device__ __forceinline__ void load4(const void *base, long long row, int D, int d, int n, bool in, float (&v)[4]) {
-    v[0] = v[1] = v[2] = v[3] = 0.f;
-    if (!in || n <= 0) return;
-    const T *src = static_cast<const T *>(base) + row * D + d;
-    if constexpr (VEC) {
-        Vec<T, 4> a;
-        a.load(src);
+struct Four {
+    Pack<T, VEC ? 4 : 1> p[VEC ? 1 : 4];
+    __device__ __forceinline__ void load(const void *base, long long row, int D, int d, int n, bool in) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = a.v[i];
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < n) {
-                Vec<T, 1> a;
-                a.load(src + i);
-                v[i] = a.v[0];
-            }
+        for (int i = 0; i < (VEC ? 1 : 4); ++i) {
+            p[i].clear();
+            if (in && i < n) p[i].load(static_cast<const T *>(base) + row * D + d + i);
+        }
     }
-}
-
-// The same as they lie in memory.
-template <typename T, bool VEC>
-__device__ __forceinline__ void load4(const void *base, long long row, int D, int d, int n, bool in, Pack<T, 4> &r) {
-    r.clear();
-    if (!in || n <= 0) return;
-    const T *src = static_cast<const T *>(base) + row * D + d;
-    if constexpr (VEC) {
-        r.load(src);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < n) {
-                Pack<T, 1> a;
-                a.load(src + i);
-                if constexpr (sizeof(T) == 4) r.w[i] = a.w[0];
-                else r.w[i >> 1] |= a.w[0] << (16 * (i & 1));
-            }
-    }
-}
+    __device__ __forceinline__ float operator[](int i) const { return VEC ? p[0][VEC ? i : 0] : p[VEC ? 0 : i][0]; }
+};
 
 template <typename T, bool VEC>
 __device__ __forceinline__ void store4(T *dst, int n, const float (&v)[4]) {
@@ -148,51 +118,26 @@ __device__ __forceinline__ void store4(T *dst, int n, const float (&v)[4]) {
 
 // What a thread reads of each tile, fetched S tiles ahead: K vectors of four
 // elements by asynchronous copies into its own part of shared memory (a thread
-// reads only what it copied itself: no barrier).  Without ASYNC the vectors may lie
-// anywhere: they are loaded one tile ahead into registers, element by element.
-template <typename T, int K, int NT, int S, bool ASYNC>
+// reads only what it copied itself: no barrier).
+template <typename T, int K, int NT, int S>
 struct Ahead {
-    static constexpr int kStages = ASYNC ? S : 1;
     static constexpr int kB = 4 * (int)sizeof(T);
-    static constexpr int kBytes = ASYNC ? S * K * NT * kB : 16;
-    Pack<T, 4> reg[ASYNC ? 1 : K];
-    // vector k of the tile in stage s; n: elements that exist
-    __device__ __forceinline__ void issue(char *ring, int s, int k, const T *src, int n) {
-        if constexpr (ASYNC) {
-            if (n <= 0) return;
-            const unsigned dst = (unsigned)__cvta_generic_to_shared(ring) + ((s * K + k) * NT + threadIdx.x) * kB;
-            if constexpr (kB == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-            else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-        } else {
-            float v[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                Vec<T, 1> a;
-                a.v[0] = 0.f;
-                if (i < n) a.load(src + i);
-                v[i] = a.v[0];
-            }
-            if constexpr (sizeof(T) == 4) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) reg[k].w[i] = __float_as_uint(v[i]);
-            } else {  // exact: each is an element of T
-                reg[k].w[0] = Vec<T, 4>::pack(v[0], v[1]);
-                reg[k].w[1] = Vec<T, 4>::pack(v[2], v[3]);
-            }
-        }
+    static constexpr int kBytes = S * K * NT * kB;
+    static __device__ __forceinline__ int at(int s, int k) { return ((s * K + k) * NT + (int)threadIdx.x) * kB; }
+    // vector k of the tile in stage s
+    __device__ __forceinline__ void issue(char *ring, int s, int k, const T *src, bool in) {
+        if (!in) return;
+        const unsigned dst = (unsigned)__cvta_generic_to_shared(ring) + at(s, k);
+        if constexpr (kB == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+        else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
     }
-    __device__ __forceinline__ void commit() {
-        if constexpr (ASYNC) asm volatile("cp.async.commit_group;" ::: "memory");
-    }
+    __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
     // Waits for the oldest of the S tiles in flight.
-    __device__ __forceinline__ void wait() {
-        if constexpr (ASYNC) asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
-    }
-    // Elements that do not exist (n given to issue) hold anything.
+    __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory"); }
+    // A vector that was not issued holds anything.
     __device__ __forceinline__ Pack<T, 4> get(const char *ring, int s, int k) const {
-        if constexpr (!ASYNC) return reg[k];
         Pack<T, 4> r;
-        r.load(reinterpret_cast<const T *>(ring + ((s * K + k) * NT + threadIdx.x) * kB));
+        r.load(reinterpret_cast<const T *>(ring + at(s, k)));
         return r;
     }
 };

@@ -73,7 +73,8 @@ struct BcRows {
             const int i = threadIdx.x + k * kThreads, which = i / (kPiece * N / 4), r = i % (kPiece * N / 4);
             const int t = r / (N / 4), c = (r % (N / 4)) * 4;
             if (i >= kAll || (which && !c_too)) continue;
-            load4<T, true>(which ? p.Cm : p.Bm, (t0 + t) * p.G + g, N, c, 4, t0 + t < t1, v[k]);
+            v[k].clear();
+            if (t0 + t < t1) v[k].load(static_cast<const T *>(which ? p.Cm : p.Bm) + ((t0 + t) * p.G + g) * N + c);
         }
     }
     __device__ __forceinline__ void put(float *bc, bool c_too) {  // bc [2][kPiece][N]
@@ -127,14 +128,14 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_state(ScanParams p) {
     for (int i = 0; i < 4; ++i) bias[i] = i < at.n && p.dt_bias ? p.dt_bias[cs.d0 + at.c + i] : 0.f;
 
     BcRows<T, N> bc;
-    Pack<T, 4> fx, fd, fg, fz;
+    Four<T, VEC> fx, fd, fg, fz;
     auto fetch = [&](long long t0) {  // this thread's rows of a tile, one tile ahead
         const bool in = t0 + at.t < seq.t1;
         bc.fetch(p, cs.g, t0, seq.t1, true);
-        load4<T, VEC>(p.x, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, fx);
-        load4<T, VEC>(p.dt, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, fd);
-        load4<T, VEC>(p.dy, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, fg);
-        if (p.z) load4<T, VEC>(p.z, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, fz);
+        fx.load(p.x, t0 + at.t, p.D, cs.d0 + at.c, at.n, in);
+        fd.load(p.dt, t0 + at.t, p.D, cs.d0 + at.c, at.n, in);
+        fg.load(p.dy, t0 + at.t, p.D, cs.d0 + at.c, at.n, in);
+        if (p.z) fz.load(p.z, t0 + at.t, p.D, cs.d0 + at.c, at.n, in);
     };
     fetch(seq.t0);
     int turn = 0;
@@ -285,19 +286,19 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd(ScanParams p, int parts)
         }
         // This thread's rows of a tile, loaded one tile ahead.
         BcRows<T, N> bc;
-        Pack<T, 4> nx, nd, ng, nz;
+        Four<T, VEC> nx, nd, ng, nz;
         auto fetch = [&](int k, bool back) {
             const long long t0 = seq.t0 + k * kPiece;
             const bool in = t0 + at.t < seq.t1;
             bc.fetch(p, cs.g, t0, seq.t1, back);
-            load4<T, VEC>(p.x, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, nx);
-            load4<T, VEC>(p.dt, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, nd);
-            if (back) load4<T, VEC>(p.dy, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, ng);
-            if (back && p.z) load4<T, VEC>(p.z, t0 + at.t, p.D, cs.d0 + at.c, at.n, in, nz);
+            nx.load(p.x, t0 + at.t, p.D, cs.d0 + at.c, at.n, in);
+            nd.load(p.dt, t0 + at.t, p.D, cs.d0 + at.c, at.n, in);
+            if (back) ng.load(p.dy, t0 + at.t, p.D, cs.d0 + at.c, at.n, in);
+            if (back && p.z) nz.load(p.z, t0 + at.t, p.D, cs.d0 + at.c, at.n, in);
         };
         auto bc_of = [&](int k) { return sm + M::kBc + (k & 1) * 2 * kPiece * N; };
         auto x_of = [&](int k) { return s_x + (k & 1) * kPiece; };
-        auto put_x = [&](int k, const Pack<T, 4> &v) {  // absent channels: zeros, as they were loaded
+        auto put_x = [&](int k, const Four<T, VEC> &v) {  // absent channels: zeros, as they were loaded
             *reinterpret_cast<float4 *>(&x_of(k)[at.t][at.c]) = make_float4(v[0], v[1], v[2], v[3]);
         };
         // forward over the chunk: the state at the start of every piece.  A tile's rows of
@@ -345,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd(ScanParams p, int parts)
         for (int k = nt - 1; k >= 0; --k) {
             const long long t0 = seq.t0 + k * kPiece;
             const bool in = t0 + at.t < seq.t1 && at.t < kPiece;
-            const Pack<T, 4> fx = nx, fd = nd, fg = ng, fz = nz;
+            const Four<T, VEC> fx = nx, fd = nd, fg = ng, fz = nz;
             // (the barriers of two tiles lie between the writes of one place of Bm and Cm)
             const int turn = nt - 1 - k + nt;
             float *s_bc = bc_of(turn);
