@@ -16,26 +16,26 @@
 //   3. scan_bwd        per chunk: the states again from its start, then the reverse walk;
 //   4. scan_bwd_bc, scan_bwd_sums  add the parts in a fixed order.
 //
-// The states of 8 tokens are kept in registers: the reverse walk takes the chunk in
-// pieces of 8 tokens, and computes the states of a piece again from the state at its
-// start, which a first walk over the chunk left in shared memory.  The factors a_t[n] are
-// computed each time they are used (four times in all): no state and no factor is ever
+// The states of 4 tokens are kept in registers: the reverse walk takes the chunk in
+// pieces of 8 tokens, a half at a time, and computes the states of a half again from the
+// state at the piece's start, which a first walk over the chunk left in shared memory.
+// The factors a_t[n] are computed each time they are used: no state and no factor is ever
 // written per token.
 //
 // A thread holds 4 states of two neighbouring channels.  The sums over channels (dB, dC)
 // are taken over its two channels, folded over the lanes that hold the warp's channels,
 // joined over the warps in shared memory, and added there over the channel tiles of the
 // block, which takes one chunk and a part of a group's channels and writes one row of 2 N
-// sums per token.  (With one channel per thread the shared-memory pipe bounds it: 567 us
-// instead of 443 at the shape below.)
+// sums per token.  (With one channel per thread the shared-memory pipe bounds it.)
 //
 // What bounds it: about 30 paired fp32 instructions for every 4 states of a channel and
 // token, 150 us of the shape below; shuffles, shared memory and staging are as many
-// instructions again, and with 253 registers a thread (two blocks an SM; with 168 they
-// spill, and three blocks are slower) a scheduler issues in 46 % of the cycles.
+// instructions again, and 12 warps an SM (168 registers a thread) issue in about half of
+// the cycles.  With the states of 8 tokens in registers, 253 a thread and 8 warps, the
+// reverse walk took 443 us.
 //
-// Measured (bf16, N = 16, gate, 4 x 2048 tokens of 2048 channels): 568 us (states 100,
-// their steps 14, reverse walk 443, sums 12).
+// Measured (bf16, N = 16, gate, 4 x 2048 tokens of 2048 channels): 512 us (states 100,
+// their steps 14, reverse walk 386, sums 12).
 #include "dn_scan.cuh"
 
 namespace dn {
@@ -46,7 +46,7 @@ using namespace scan;
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kLen = 64;   // tokens of a chunk
-constexpr int kPiece = 8;  // tokens staged at a time; step 3 holds their states in registers
+constexpr int kPiece = 8;  // tokens staged at a time; step 3 keeps the state at the start of each piece
 
 // One thread's place in a tile's rows: four channels of one token.
 struct Place {
@@ -218,7 +218,7 @@ struct Smem {  // offsets in floats
 };
 
 template <typename T, int L, bool VEC>
-__global__ void __launch_bounds__(kThreads, 2) scan_bwd(ScanParams p, int parts) {
+__global__ void __launch_bounds__(kThreads, 3) scan_bwd(ScanParams p, int parts) {
     using M = Smem<L>;
     constexpr int N = M::N, CH = M::CH;
     extern __shared__ __align__(16) float sm[];
@@ -362,30 +362,40 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd(ScanParams p, int parts)
             bc.put(s_bc, true);
             __syncthreads();
             if (k > 0) fetch(k - 1, true);
-            f2 hh[kPiece + 1][2][2];
+            // The piece in two halves of four tokens, the second first (its states need the
+            // first half's steps once more): half the registers for the states.
+#pragma unroll 1
+            for (int u = kPiece - 4; u >= 0; u -= 4) {
+                f2 hh[5][2][2];
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const ulonglong2 r = s_start[(k * 2 + c) * kThreads + tid];
-                hh[0][c][0] = r.x;
-                hh[0][c][1] = r.y;
-            }
-#pragma unroll
-            for (int u = 0; u < kPiece; u += 4) {
-                float py[2][4];
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    const int t = u + w;
+                for (int c = 0; c < 2; ++c) {
+                    const ulonglong2 r = s_start[(k * 2 + c) * kThreads + tid];
+                    hh[0][c][0] = r.x;
+                    hh[0][c][1] = r.y;
+                }
+                auto step = [&](int t, f2 (&to)[2][2], const f2 (&from)[2][2]) {  // token t of the tile
                     const float2 dd = *reinterpret_cast<const float2 *>(&s_d[k * kPiece + t][ch]);
                     const float2 xx = *reinterpret_cast<const float2 *>(&x_of(turn)[t][ch]);
                     const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(s_bc + t * N + lane * kS);
-                    ulonglong2 cc = make_ulonglong2(0ull, 0ull);
-                    if (p.z) cc = *reinterpret_cast<const ulonglong2 *>(s_bc + (kPiece + t) * N + lane * kS);
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         const f2 d2 = both(c ? dd.y : dd.x), x2 = both(c ? dd.y * xx.y : dd.x * xx.x);
-                        hh[t + 1][c][0] = fma2(decay(d2, c, 0), hh[t][c][0], mul2(x2, b.x));
-                        hh[t + 1][c][1] = fma2(decay(d2, c, 1), hh[t][c][1], mul2(x2, b.y));
-                        if (p.z) py[c][w] = sum_of(fma2(cc.x, hh[t + 1][c][0], mul2(cc.y, hh[t + 1][c][1])));
+                        to[c][0] = fma2(decay(d2, c, 0), from[c][0], mul2(x2, b.x));
+                        to[c][1] = fma2(decay(d2, c, 1), from[c][1], mul2(x2, b.y));
+                    }
+                };
+                if (u > 0)
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) step(t, hh[0], hh[0]);
+                float py[2][4];
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    step(u + w, hh[w + 1], hh[w]);
+                    if (p.z) {
+                        const ulonglong2 cc = *reinterpret_cast<const ulonglong2 *>(s_bc + (kPiece + u + w) * N + lane * kS);
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            py[c][w] = sum_of(fma2(cc.x, hh[w + 1][c][0], mul2(cc.y, hh[w + 1][c][1])));
                     }
                 }
                 if (p.z)
@@ -394,9 +404,6 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd(ScanParams p, int parts)
                         const float y = sum4<L>(py[c], lane);
                         if (lane < 4) s_res[2][u + lane][ch + c] = y;
                     }
-            }
-#pragma unroll
-            for (int u = kPiece - 4; u >= 0; u -= 4) {
                 float ps[2][4], pq[2][4];
 #pragma unroll
                 for (int w = 3; w >= 0; --w) {
@@ -416,12 +423,12 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd(ScanParams p, int parts)
                         for (int i = 0; i < 2; ++i) {
                             const f2 gr = fma2(g2, cc[i], carry[c][i]);
                             carry[c][i] = mul2(gr, decay(d2, c, i));
-                            const f2 qq = mul2(carry[c][i], hh[t][c][i]);
+                            const f2 qq = mul2(carry[c][i], hh[w][c][i]);
                             dA[c][i] = fma2(d2, qq, dA[c][i]);
                             q2 = fma2(qq, a2[c][i], q2);
                             s2 = fma2(gr, bb[i], s2);
                             vb[i] = fma2(gr, x2, vb[i]);
-                            vc[i] = fma2(g2, hh[t + 1][c][i], vc[i]);
+                            vc[i] = fma2(g2, hh[w + 1][c][i], vc[i]);
                         }
                         ps[c][w] = sum_of(s2);
                         pq[c][w] = sum_of(q2);
