@@ -589,8 +589,8 @@ def layer_norm_bwd(x, weight=None, bias=None, z=None, eps=1e-5, rms=False, dy=No
     code = dtype_code(dt)
     lib = load()
     out = dict(dx=torch.empty_like(x, memory_format=torch.contiguous_format),
-               dweight=None if weight is None else torch.empty(D, dtype=f32, device=device),
-               dbias=None if bias is None else torch.empty(D, dtype=f32, device=device),
+               dweight=None if weight is None else torch.empty_like(weight),
+               dbias=None if bias is None else torch.empty_like(bias),
                dz=None if z is None else torch.empty_like(x, memory_format=torch.contiguous_format))
     need = 0
     if weight is not None or bias is not None:

@@ -4,6 +4,8 @@
 
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "dn_layer.h"
 
 namespace dn {
@@ -26,6 +28,24 @@ inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, siz
     return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
 }
 __device__ __forceinline__ void wait_for_launches() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Lets a kernel have `bytes` of dynamic shared memory beside a few KB of its own: nothing
+// to do up to 32 KB (48 KB in all need no leave), else
+// once for every device (the attribute stays).
+template <auto kKernel>
+inline cudaError_t allow_smem(int bytes) {
+    static std::atomic<unsigned long long> done{0};
+    if (bytes <= 32 * 1024) return cudaSuccess;
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    err = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (err == cudaSuccess) err = cudaFuncSetAttribute(kKernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return err;
+}
 
 // V consecutive elements of T in one access (V = 1, or a power of two whose
 // bytes are the pointer's alignment), as fp32.

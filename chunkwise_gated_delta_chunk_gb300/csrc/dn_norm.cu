@@ -412,14 +412,14 @@ cudaError_t norm_launch_g(const NormParams &p, bool bwd, cudaStream_t stream) {
     constexpr int kRows = Row<T, V, K, R>::kRows, kThreads = Row<T, V, K, R>::kThreads;
     if (!bwd) {
         constexpr int bytes = Ring<T, V, K, R, GATE ? 2 : 1>::kBytes;
-        cudaError_t err = cudaFuncSetAttribute(norm_fwd<T, V, K, R, GATE>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        const cudaError_t err = allow_smem<norm_fwd<T, V, K, R, GATE>>(bytes);
         if (err != cudaSuccess) return err;
         norm_fwd<T, V, K, R, GATE><<<norm_blocks(p.rows, kThreads, kRows, 64), kThreads, bytes, stream>>>(p);
     } else {
         const int grid = norm_blocks(p.rows, kThreads, kRows, 128);
         if (grid > 0) {
             constexpr int bytes = Ring<T, V, K, R, GATE ? 3 : 2>::kBytes;
-            cudaError_t err = cudaFuncSetAttribute(norm_bwd<T, V, K, R, GATE>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+            cudaError_t err = allow_smem<norm_bwd<T, V, K, R, GATE>>(bytes);
             if (err != cudaSuccess) return err;
             norm_bwd<T, V, K, R, GATE><<<grid, kThreads, bytes, stream>>>(p);
             err = cudaGetLastError();

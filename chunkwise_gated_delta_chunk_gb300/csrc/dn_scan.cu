@@ -35,7 +35,6 @@ namespace {
 using namespace scan;
 
 constexpr int kTile = 16;      // tokens whose rows of Bm and Cm are staged at a time
-constexpr int kMinChunk = 64;  // the shortest chunk
 constexpr int kT = 16;         // states of a thread
 constexpr int kResident = 16;  // warps of an SM (128 registers a thread)
 constexpr int kCh = 64;        // channels of a block: two for each of its threads, N / kT threads sharing two
@@ -497,9 +496,11 @@ cudaError_t step_t(const ScanParams &p, cudaStream_t stream) {
 int fwd_chunk(int n_seqs, long long tokens, int D, int G, int N) {
     const long long blocks = (long long)n_seqs * G * ((D / G + kCh - 1) / kCh);
     const long long parts = (long long)kSms * (kResident / (N / kT)) / blocks;
-    if (parts < 2 || tokens / n_seqs < 2 * kMinChunk) return 0;
-    const long long len = (tokens / n_seqs + parts - 1) / parts;
-    return len < kMinChunk ? kMinChunk : (int)((len + kTile - 1) / kTile * kTile);
+    const long long mean = tokens / n_seqs;
+    const int least = scan_least_chunk(mean);
+    if (parts < 2 || mean < 2 * least) return 0;
+    const long long len = (mean + parts - 1) / parts;
+    return len < least ? least : (int)((len + kTile - 1) / kTile * kTile);
 }
 
 }  // namespace

@@ -7,8 +7,8 @@
 //     dA[n]   = sum_t delta q[n],      dB[n] = sum_d delta x g[n],       dC[n] = sum_d dyo h[n]
 //     dDskip  = sum_t dyo x,           ddt_bias = sum_t ddt,             dz = dy (C.h + Dskip x) silu'(z)
 //
-// Every sequence is cut into chunks of 64 tokens, and all chunks are worked on at
-// once:
+// Every sequence is cut into chunks of 64 tokens (fewer in small calls), and all chunks
+// are worked on at once:
 //   1. scan_bwd_state  per chunk, in one walk: the state from zero at its end, the sum
 //                      of delta, and the gradient that its own outputs send to the state
 //                      at its start (with the running product of a);
@@ -45,7 +45,7 @@ using namespace scan;
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kLen = 64;   // tokens of a chunk
+constexpr int kLen = 64;   // tokens of a chunk at most
 constexpr int kPiece = 8;  // tokens staged at a time; step 3 keeps the state at the start of each piece
 
 // One thread's place in a tile's rows: four channels of one token.
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_state(ScanParams p) {
     const unsigned slot = blockIdx.x / tiles;
     const int ct = blockIdx.x - slot * tiles;
     if (blockIdx.x == 0) check_offsets(p.seq, tid, kThreads);
-    const SeqTile seq = seq_tile(p.seq, slot, kLen);
+    const SeqTile seq = seq_tile(p.seq, slot, p.chunk);
     if (!seq.ok) return;
     const Channels cs = channels_of<CH>(p, ct);
     const int ch = tid / L * 2, lane = tid % L;  // the first of this thread's channels
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd(ScanParams p, int parts)
     const int gp = blockIdx.x - slot * split_by, g = gp / parts, part = gp - g * parts;
     const int per = (p.D / p.G + CH - 1) / CH;  // channel tiles of a group
     const int first = (int)((long long)per * part / parts), last = (int)((long long)per * (part + 1) / parts);
-    const SeqTile seq = seq_tile(p.seq, slot, kLen);
+    const SeqTile seq = seq_tile(p.seq, slot, p.chunk);
     const int ch = tid / L * 2, lane = tid % L;  // the first of this thread's channels
     const int len = seq.ok ? (int)(seq.t1 - seq.t0) : 0;
     const int nt = (len + kPiece - 1) / kPiece;
@@ -585,12 +585,24 @@ __global__ void __launch_bounds__(256) scan_bwd_sums(ScanParams p, long long slo
     }
 }
 
-// Parts that a group's channels are split into: enough blocks to fill the GPU, at
-// most one per tile of channels.
-int channel_parts(int n_seqs, long long tokens, int D, int G, int N) {
+int tiles_of_group(int D, int G, int N) {
     const int ch = 2 * kThreads / (N / kS);
-    const long long tiles = (D / G + ch - 1) / ch;
-    const long long rows = (tokens / kLen + n_seqs) * G;
+    return (D / G + ch - 1) / ch;
+}
+
+// Tokens of a chunk: 64, or fewer where that leaves places of the GPU without a block.
+int bwd_chunk(int n_seqs, long long tokens, int D, int G, int N) {
+    const long long tiles = (long long)G * tiles_of_group(D, G, N);
+    int len = n_seqs > 0 ? scan_least_chunk(tokens / n_seqs) : kLen;
+    while (len < kLen && (tokens / (2 * len) + n_seqs) * tiles >= kSms * 3) len *= 2;
+    return len < kLen ? len : kLen;
+}
+
+// Parts that a group's channels are split into: enough blocks to fill the GPU many times,
+// at most one per tile of channels.
+int channel_parts(int n_seqs, long long tokens, int D, int G, int N) {
+    const long long tiles = tiles_of_group(D, G, N);
+    const long long rows = (tokens / bwd_chunk(n_seqs, tokens, D, G, N) + n_seqs) * G;
     const long long want = rows > 0 ? (kSms * 32 + rows - 1) / rows : 1;
     return (int)(want < tiles ? want : tiles);
 }
@@ -598,7 +610,7 @@ int channel_parts(int n_seqs, long long tokens, int D, int G, int N) {
 template <typename T, int L, bool VEC>
 cudaError_t bwd_l(const ScanParams &p, cudaStream_t stream) {
     constexpr int CH = 2 * kThreads / L;
-    const long long slots = tile_slots(p.seq, kLen);
+    const long long slots = tile_slots(p.seq, p.chunk);
     const int parts = channel_parts(p.seq.N, p.seq.tokens, p.D, p.G, p.N);
     const long long states = slots * channel_tiles<CH>(p.D, p.G);
     const long long blocks = slots * p.G * parts;
@@ -609,10 +621,8 @@ cudaError_t bwd_l(const ScanParams &p, cudaStream_t stream) {
         err = cudaGetLastError();
         if (err == cudaSuccess) err = scan_combine_launch(p, true, stream);
         if (err != cudaSuccess) return err;
-        constexpr size_t bytes = Smem<L>::kAll * sizeof(float);
-        err = cudaFuncSetAttribute(scan_bwd<T, L, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-        if (err != cudaSuccess) return err;
-        err = cudaFuncSetAttribute(scan_bwd<T, L, VEC>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+        constexpr int bytes = Smem<L>::kAll * sizeof(float);
+        err = allow_smem<scan_bwd<T, L, VEC>>(bytes);
         if (err != cudaSuccess) return err;
         err = launch_after(scan_bwd<T, L, VEC>, dim3((unsigned)blocks), dim3(kThreads), bytes, stream, p, parts);
         if (err != cudaSuccess) return err;
@@ -645,7 +655,7 @@ struct Sizes {
     size_t all() const { return (hs + dsum + gs + vec + bc) * 4; }
 };
 Sizes sizes(int n_seqs, long long tokens, int D, int G, int N) {
-    const size_t slots = (size_t)(tokens / kLen + n_seqs);
+    const size_t slots = (size_t)(tokens / bwd_chunk(n_seqs, tokens, D, G, N) + n_seqs);
     const size_t parts = (size_t)channel_parts(n_seqs, tokens, D, G, N);
     auto up = [](size_t v) { return (v + 3) / 4 * 4; };
     return {slots * D * N, up(slots * D), slots * D * N, up(slots * 2 * D), parts * (size_t)tokens * G * 2 * N};
@@ -660,7 +670,7 @@ size_t scan_bwd_workspace(int n_seqs, long long tokens, int D, int G, int N) {
 
 void scan_bwd_carve(ScanParams &p, void *workspace) {
     const Sizes s = sizes(p.seq.N, p.seq.tokens, p.D, p.G, p.N);
-    p.chunk = kLen;
+    p.chunk = bwd_chunk(p.seq.N, p.seq.tokens, p.D, p.G, p.N);
     p.hs = static_cast<float *>(workspace);
     p.dsum = p.hs + s.hs;
     p.gs = p.dsum + s.dsum;
