@@ -14,7 +14,7 @@
 // registers.  The rate of issue bounds it: written plainly it takes 182 instructions for
 // 4 channels of a token.  Pairs of channels in the two-wide fp32 instructions, rings of W
 // registers that turn whole within an unrolled group, and a path of its own for tokens at
-// a tile's edges bring that to 106 (and 221 us to 78).  Rows come by asynchronous copies
+// a tile's edges bring that to 106 (and 221 us to 75).  Rows come by asynchronous copies
 // into the thread's own part of shared memory, so that they hold no registers.  The sums
 // over tokens stay in registers over all tiles of a block, are joined over its warps and
 // written as one row per block; a second kernel adds the rows in a fixed order.
@@ -22,7 +22,7 @@
 // Both move 2 (forward) and 3 (backward) elements per channel and token for about
 // W products and one exponential each.  Measured (bf16, W = 4, silu, 6144 channels):
 // forward over 20741 packed tokens 90 us, 5.6 TB/s, bound by memory; backward over
-// 4 x 2048 tokens 78 us, 3.9 TB/s.
+// 4 x 2048 tokens 75 us, 4.0 TB/s.
 #include <type_traits>
 
 #include "dn_layer.cuh"
@@ -259,7 +259,8 @@ cudaError_t conv_fwd_t(const ConvParams &p, cudaStream_t stream) {
 
 constexpr int kBwdWarps = 4;
 constexpr int kBwdThreads = kBwdWarps * 32;
-constexpr int kGroups = 2;  // groups of tokens in flight (3 and 4 measured 2 % slower)
+constexpr int kGroups = 2;       // groups of tokens in flight (3 and 4 take as long)
+constexpr int kBwdResident = 3;  // blocks of an SM (up to 168 registers a thread; 4 take 2 % longer, 5 spill)
 
 // Channels of a thread where rows allow it.
 template <typename T>
@@ -279,7 +280,7 @@ BwdGrid conv_bwd_grid(long long tokens, int n_seqs, int D, int V) {
     while (g.tile > 16 && (tokens / g.tile + n_seqs) * cols < (long long)kSms * 16) g.tile >>= 1;
     const long long most = (tokens / g.tile + n_seqs + kBwdWarps - 1) / kBwdWarps;
     if (most <= 1) return g;
-    const long long fill = (kSms * 4 + cols - 1) / cols;
+    const long long fill = (kSms * kBwdResident + cols - 1) / cols;
     const long long each = (most + fill - 1) / fill;
     g.rows = (int)((most + each - 1) / each);
     return g;
@@ -366,7 +367,7 @@ struct Feed {
 };
 
 template <typename T, typename Tg, int W, int V>
-__global__ void __launch_bounds__(kBwdThreads) conv_bwd(ConvParams p, int len, int cols, unsigned slots) {
+__global__ void __launch_bounds__(kBwdThreads, kBwdResident) conv_bwd(ConvParams p, int len, int cols, unsigned slots) {
     if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(p.seq, threadIdx.x, kBwdThreads);
     constexpr int P = Pairs<V>::P;
     constexpr int K = W == 3 ? 3 : 4;  // tokens of a group: a multiple of W, so that rings of W turn whole
