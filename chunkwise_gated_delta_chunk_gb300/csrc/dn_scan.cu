@@ -247,7 +247,8 @@ __global__ void __launch_bounds__(32 * L, kResident / L) scan_fwd(ScanParams p) 
             }
 #pragma unroll
             for (int k = 0; k < U; ++k) {
-                const f2 xs = fx[k].get();
+                f2 xs = fx[k].get();
+                if (k >= left) xs = 0ull;  // not an infinity of two tokens before, times no step
                 f2 zs = 0ull;
                 if (gate) zs = fz[k].get();
                 float e0, e1, x0, x1;

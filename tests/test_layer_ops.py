@@ -297,6 +297,22 @@ def test_scan_total_forgetting(lib):
     assert torch.isfinite(y).all() and torch.equal(y, y2) and torch.equal(ht, ht2)
 
 
+@pytest.mark.parametrize("T", [2, 3, 15, 31, 33])
+@pytest.mark.parametrize("D", [6, 7])
+def test_scan_infinite_state_stays_infinite(lib, T, D):
+    """An input that overflows leaves an infinity in its channel, whatever the length; the others stay finite."""
+    t, _ = scan_inputs(torch.float32, B=1, T=T, D=D, gate=False, seed=14)
+    t["x"][0, (T // 2) * 2 - 1, 3] = float("inf")  # the second token of the last whole pair
+    y64, ht64 = ref.scan(ref.in_64_bits(t))
+    y, ht = lib.selective_scan_fwd(*scan_args(t))
+    ok(lib)
+    assert torch.isinf(ht64[0, 3]).all()
+    assert torch.equal(ht[0, 3].double().cpu(), ht64[0, 3])
+    keep = [d for d in range(D) if d != 3]
+    ref.close(y[:, :, keep], y64[:, :, keep], 10 * T + 64, "y of the others")
+    ref.close(ht[:, keep], ht64[:, keep], 10 * T + 64, "ht of the others")
+
+
 # ---- layer norm ------------------------------------------------------------------
 
 
@@ -429,6 +445,52 @@ def test_rows_behind_the_last_sequence_are_left(lib):
     y = torch.full_like(t["x"], 7.0)
     lib.selective_scan_fwd(*scan_args(t), cu, y=y)
     assert (y[:, 73:] == 7).all()
+    ok(lib)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_gradients_behind_the_last_sequence_are_left(lib, dtype):
+    """The gradients' rows there keep what they held, and no value of x or dy there counts."""
+    lengths, pad, D, W, N = [3, 0, 70], 9, 40, 4, 16
+    used, T = sum(lengths), sum(lengths) + pad
+    cu = ref.offsets(lengths, DEV)
+    c, code, raw = len(lengths), lib.dtype_code(dtype), lib.load()
+
+    def ptr(x):
+        return x.data_ptr()
+
+    def left(*outs):
+        for o in outs:
+            assert (o[:, used:] == 7).all() and torch.isfinite(o[:, :used]).all() and not (o[:, :used] == 7).all()
+
+    stream = torch.cuda.current_stream().cuda_stream
+    t, grads = conv_inputs(dtype, D=D, lengths=lengths, pad=pad, seed=2)
+    t["x"][:, used:] = float("nan")
+    grads["dy"][:, used:] = float("inf")
+    dx = torch.full_like(t["x"], 7.0)
+    dw, db, dh0 = torch.empty_like(t["weight"]), torch.empty_like(t["bias"]), torch.empty_like(t["h0"])
+    n = raw.dn_causal_conv_bwd_workspace_bytes(c, 1, T, D, W, code)
+    space = torch.empty(n, dtype=torch.uint8, device=DEV)
+    assert raw.dn_causal_conv_bwd(
+        ptr(t["x"]), ptr(t["weight"]), ptr(t["bias"]), ptr(t["h0"]), ptr(cu), c, 1, T, D, W, code, 1,
+        ptr(grads["dy"]), code, ptr(grads["dht"]), ptr(dx), ptr(dw), ptr(db), ptr(dh0), ptr(space), n,
+        stream) == lib.DN_OK
+    left(dx)
+    assert all(torch.isfinite(v).all() for v in (dw, db, dh0))
+    t, grads = scan_inputs(dtype, D=D, N=N, lengths=lengths, pad=pad, seed=2)
+    for name in ("x", "dt", "B", "C", "z"):
+        t[name][:, used:] = float("nan")
+    grads["dy"][:, used:] = float("inf")
+    rows = {k: torch.full_like(t[k], 7.0) for k in ("x", "dt", "B", "C", "z")}
+    sums = {k: torch.empty_like(t[k]) for k in ("A", "D", "dt_bias", "h0")}
+    n = raw.dn_selective_scan_bwd_workspace_bytes(c, 1, T, D, 1, N, code)
+    space = torch.empty(n, dtype=torch.uint8, device=DEV)
+    assert raw.dn_selective_scan_bwd(
+        *[ptr(t[k]) for k in NAMES], ptr(cu), c, 1, T, D, 1, N, code, 1, ptr(grads["dy"]), ptr(grads["dht"]),
+        ptr(rows["x"]), ptr(rows["dt"]), ptr(sums["A"]), ptr(rows["B"]), ptr(rows["C"]), ptr(sums["D"]),
+        ptr(rows["z"]), ptr(sums["dt_bias"]), ptr(sums["h0"]), ptr(space), n, stream) == lib.DN_OK
+    left(*rows.values())
+    assert all(torch.isfinite(v).all() for v in sums.values())
     ok(lib)
 
 
