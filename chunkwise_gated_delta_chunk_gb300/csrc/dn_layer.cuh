@@ -174,14 +174,6 @@ struct Pack {
     }
 };
 
-
-
-template <typename T, int V>
-__device__ __forceinline__ void zero(Vec<T, V> &a) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) a.v[i] = 0.f;
-}
-
 // One tile of a sequence (see tile_slots).  `ok` is false where the slot holds
 // none; every access a tile leads to is inside the tensors whatever the
 // offsets hold.

@@ -24,8 +24,8 @@
 // scan itself starts every chunk from its state.  A single token has a kernel of its
 // own, one thread per 4 states, so that the states are read and written in whole lines.
 //
-// Measured (bf16, N = 16, gate): 4 x 2048 tokens of 2048 channels 161 us (states 64,
-// their steps 8, scan 89); 64 x 256 tokens of 4096 channels, uncut, 341 us; one token of
+// Measured (bf16, N = 16, gate): 4 x 2048 tokens of 2048 channels 156 us (states 64,
+// their steps 8, scan 84); 64 x 256 tokens of 4096 channels, uncut, 341 us; one token of
 // 64 sequences, 2048 channels, 7 us.
 #include "dn_scan.cuh"
 
@@ -493,7 +493,7 @@ cudaError_t step_t(const ScanParams &p, cudaStream_t stream) {
 // Length of the chunks that a forward's sequences are cut into; 0: they are not.  Whole
 // sequences where their blocks fill more than half of the GPU's places; else as many
 // chunks as fill them once (one block too many would be a second wave: 4 x 2048 tokens of
-// 2048 channels in 19 chunks take 160 us, in 15 or 20 chunks 190 to 210).
+// 2048 channels in 19 chunks take 156 us, in 15 or 20 chunks 190 to 210).
 int fwd_chunk(int n_seqs, long long tokens, int D, int G, int N) {
     const long long blocks = (long long)n_seqs * G * ((D / G + kCh - 1) / kCh);
     const long long parts = (long long)kSms * (kResident / (N / kT)) / blocks;
