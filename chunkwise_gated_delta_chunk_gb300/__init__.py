@@ -18,6 +18,9 @@ The operators around the recurrence (``include/dn_layer_ops.h``) are
 :func:`causal_conv_fwd` and :func:`causal_conv_bwd`, :func:`selective_scan_fwd`
 and :func:`selective_scan_bwd`, :func:`layer_norm_fwd` and
 :func:`layer_norm_bwd`; they check their tensors and allocate what is not given.
+
+A call given a ``stream`` is made as under ``torch.cuda.stream(stream)``: what it
+allocates is that stream's memory, and what it reads has to be ready there.
 """
 from __future__ import annotations
 
@@ -355,11 +358,19 @@ def _device_of(x, torch):
     return device
 
 
-def _stream_on(device, stream, torch):
-    """Handle of the given stream, or of the current one of this (the current) device."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
-    return stream if isinstance(stream, int) else stream.cuda_stream
+def _under(stream, device, torch):
+    """The context of a given stream (an object or a raw handle), for a call that was given one.
+
+    The whole call is made in it, so that what it allocates comes from that stream's memory.
+    A tensor of another stream's could still be in use there when the call writes it, and
+    could be handed on there before the call is done with it.
+    """
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream if isinstance(stream, int) else stream.cuda_stream
+        # 0 and 1 name the default stream (torch makes a new stream of a handle of 0)
+        stream = (torch.cuda.default_stream(device) if handle in (0, 1)
+                  else torch.cuda.ExternalStream(handle, device=device))
+    return torch.cuda.stream(stream)
 
 
 def _sequences(B, cu_seqlens, device):
@@ -381,16 +392,13 @@ def _workspace_bytes(entry, *sizes):
     return getattr(load(), entry)(*sizes)
 
 
-def _space(nbytes, workspace, device, stream):
+def _space(nbytes, workspace, device):
     """The caller's workspace, or a new one; and its address and bytes."""
     import torch
     if workspace is None:
         if nbytes == 0:
             return None, None, 0
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        if stream is not None:  # it is freed on return: not before that stream is done with it
-            workspace.record_stream(torch.cuda.ExternalStream(stream, device=device)
-                                    if isinstance(stream, int) else stream)
     elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on %s" % device)
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -408,6 +416,10 @@ def causal_conv_fwd(x, weight, bias=None, h0=None, cu_seqlens=None, silu=True,
     """
     import torch
     device = _device_of(x, torch)
+    if stream is not None:
+        with _under(stream, device, torch):
+            return causal_conv_fwd(x, weight, bias, h0, cu_seqlens, silu, output_final_state, None,
+                                   y, ht)
     B, T, D = x.shape
     W = weight.shape[-1]
     f32, dt = torch.float32, x.dtype
@@ -424,7 +436,7 @@ def causal_conv_fwd(x, weight, bias=None, h0=None, cu_seqlens=None, silu=True,
         _operand("x", x, x.shape, dt, device), _operand("weight", weight, (D, W), f32, device, False),
         _operand("bias", bias, (D,), f32, device), _operand("h0", h0, state, dt, device), cu, N, B, T,
         D, W, code, DN_CONV_SILU if silu else 0, _operand("y", y, x.shape, dt, device),
-        _operand("ht", ht, state, dt, device), _stream_on(device, stream, torch))
+        _operand("ht", ht, state, dt, device), torch._C._cuda_getCurrentRawStream(device.index))
     if st != DN_OK:
         raise DnError(st, "dn_causal_conv_fwd")
     return y, ht
@@ -440,6 +452,9 @@ def causal_conv_bwd(x, weight, bias=None, h0=None, cu_seqlens=None, silu=True, d
     """
     import torch
     device = _device_of(x, torch)
+    if stream is not None:
+        with _under(stream, device, torch):
+            return causal_conv_bwd(x, weight, bias, h0, cu_seqlens, silu, dy, dht, None, workspace)
     B, T, D = x.shape
     W = weight.shape[-1]
     f32, dt = torch.float32, x.dtype
@@ -455,14 +470,14 @@ def causal_conv_bwd(x, weight, bias=None, h0=None, cu_seqlens=None, silu=True, d
                dbias=None if bias is None else torch.empty(D, dtype=f32, device=device),
                dh0=None if h0 is None else torch.empty(state, dtype=dt, device=device))
     need = _workspace_bytes("dn_causal_conv_bwd_workspace_bytes", N, B, T, D, W, code)
-    workspace, ws, wsb = _space(need, workspace, device, stream)
+    workspace, ws, wsb = _space(need, workspace, device)
     st = lib.dn_causal_conv_bwd(
         _operand("x", x, x.shape, dt, device), _operand("weight", weight, (D, W), f32, device, False),
         _operand("bias", bias, (D,), f32, device), _operand("h0", h0, state, dt, device), cu, N, B, T,
         D, W, code, DN_CONV_SILU if silu else 0, _operand("dy", dy, x.shape, gt, device),
         dtype_code(gt), _operand("dht", dht, state, dt, device), out["dx"].data_ptr(),
         out["dweight"].data_ptr(), _ptr(out["dbias"]), _ptr(out["dh0"]), ws, wsb,
-        _stream_on(device, stream, torch))
+        torch._C._cuda_getCurrentRawStream(device.index))
     if st != DN_OK:
         raise DnError(st, "dn_causal_conv_bwd")
     return out
@@ -500,6 +515,10 @@ def selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, cu
     None unless ``output_final_state``).
     """
     import torch
+    if stream is not None:
+        with _under(stream, _device_of(x, torch), torch):
+            return selective_scan_fwd(x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, dt_softplus,
+                                      output_final_state, None, y, ht, workspace)
     device, ty, bc, state, ptrs, sizes, flags = _scan_inputs(x, dt, A, B, C, D, z, dt_bias, h0,
                                                              cu_seqlens, dt_softplus)
     if y is None:
@@ -510,10 +529,10 @@ def selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, cu
         ht = torch.empty(state, dtype=torch.float32, device=device)
     lib = load()
     need = _workspace_bytes("dn_selective_scan_fwd_workspace_bytes", *sizes)
-    workspace, ws, wsb = _space(need, workspace, device, stream)
+    workspace, ws, wsb = _space(need, workspace, device)
     st = lib.dn_selective_scan_fwd(*ptrs, *sizes, flags, _operand("y", y, x.shape, ty, device),
                                    _operand("ht", ht, state, torch.float32, device), ws, wsb,
-                                   _stream_on(device, stream, torch))
+                                   torch._C._cuda_getCurrentRawStream(device.index))
     if st != DN_OK:
         raise DnError(st, "dn_selective_scan_fwd")
     return y, ht
@@ -527,6 +546,10 @@ def selective_scan_bwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, cu
     ``dA``, ``dD``, ``ddt_bias``, ``dh0`` in fp32; those of absent inputs are None.
     """
     import torch
+    if stream is not None:
+        with _under(stream, _device_of(x, torch), torch):
+            return selective_scan_bwd(x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, dt_softplus,
+                                      dy, dht, None, workspace)
     device, ty, bc, state, ptrs, sizes, flags = _scan_inputs(x, dt, A, B, C, D, z, dt_bias, h0,
                                                              cu_seqlens, dt_softplus)
     f32 = torch.float32
@@ -540,12 +563,12 @@ def selective_scan_bwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, cu
                dh0=like(h0, state, f32))
     lib = load()
     need = _workspace_bytes("dn_selective_scan_bwd_workspace_bytes", *sizes)
-    workspace, ws, wsb = _space(need, workspace, device, stream)
+    workspace, ws, wsb = _space(need, workspace, device)
     st = lib.dn_selective_scan_bwd(
         *ptrs, *sizes, flags, _operand("dy", dy, x.shape, ty, device, False),
         _operand("dht", dht, state, f32, device), _ptr(out["dx"]), _ptr(out["ddt"]), _ptr(out["dA"]),
         _ptr(out["dB"]), _ptr(out["dC"]), _ptr(out["dD"]), _ptr(out["dz"]), _ptr(out["ddt_bias"]),
-        _ptr(out["dh0"]), ws, wsb, _stream_on(device, stream, torch))
+        _ptr(out["dh0"]), ws, wsb, torch._C._cuda_getCurrentRawStream(device.index))
     if st != DN_OK:
         raise DnError(st, "dn_selective_scan_bwd")
     return out
@@ -560,6 +583,9 @@ def layer_norm_fwd(x, weight=None, bias=None, z=None, eps=1e-5, rms=False, strea
     """
     import torch
     device = _device_of(x, torch)
+    if stream is not None:
+        with _under(stream, device, torch):
+            return layer_norm_fwd(x, weight, bias, z, eps, rms, None, y)
     D = x.shape[-1]
     f32, dt = torch.float32, x.dtype
     if y is None:
@@ -568,7 +594,7 @@ def layer_norm_fwd(x, weight=None, bias=None, z=None, eps=1e-5, rms=False, strea
         _operand("x", x, x.shape, dt, device), _operand("weight", weight, (D,), f32, device),
         _operand("bias", bias, (D,), f32, device), _operand("z", z, x.shape, dt, device),
         x.numel() // D if D else 0, D, dtype_code(dt), eps, DN_NORM_RMS if rms else 0,
-        _operand("y", y, x.shape, dt, device), _stream_on(device, stream, torch))
+        _operand("y", y, x.shape, dt, device), torch._C._cuda_getCurrentRawStream(device.index))
     if st != DN_OK:
         raise DnError(st, "dn_layer_norm_fwd")
     return y
@@ -583,6 +609,9 @@ def layer_norm_bwd(x, weight=None, bias=None, z=None, eps=1e-5, rms=False, dy=No
     """
     import torch
     device = _device_of(x, torch)
+    if stream is not None:
+        with _under(stream, device, torch):
+            return layer_norm_bwd(x, weight, bias, z, eps, rms, dy, None, workspace)
     D = x.shape[-1]
     rows = x.numel() // D if D else 0
     f32, dt = torch.float32, x.dtype
@@ -595,13 +624,13 @@ def layer_norm_bwd(x, weight=None, bias=None, z=None, eps=1e-5, rms=False, dy=No
     need = 0
     if weight is not None or bias is not None:
         need = _workspace_bytes("dn_layer_norm_bwd_workspace_bytes", rows, D, code)
-    workspace, ws, wsb = _space(need, workspace, device, stream)
+    workspace, ws, wsb = _space(need, workspace, device)
     st = lib.dn_layer_norm_bwd(
         _operand("x", x, x.shape, dt, device), _operand("weight", weight, (D,), f32, device),
         _operand("bias", bias, (D,), f32, device), _operand("z", z, x.shape, dt, device), rows, D,
         code, eps, DN_NORM_RMS if rms else 0, _operand("dy", dy, x.shape, dt, device, False),
         out["dx"].data_ptr(), _ptr(out["dweight"]), _ptr(out["dbias"]), _ptr(out["dz"]), ws, wsb,
-        _stream_on(device, stream, torch))
+        torch._C._cuda_getCurrentRawStream(device.index))
     if st != DN_OK:
         raise DnError(st, "dn_layer_norm_bwd")
     return out

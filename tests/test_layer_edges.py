@@ -1,0 +1,125 @@
+"""The operators around the recurrence where calls go wrong: streams of their own, states and
+gradients beside infinities, sizes that a kernel's integers do not hold, paths that only large
+calls take.  References are the definitions in 64 bits (layer_reference)."""
+import pytest
+import torch
+
+import layer_reference as ref
+from conftest import cuda_ok
+from test_layer_ops import DEV, DTYPES, NAMES, conv_inputs, norm_inputs, ok, same, scan_args, scan_inputs
+
+gpu = [pytest.mark.gpu, pytest.mark.skipif(not cuda_ok(), reason="needs a CUDA GPU")]
+
+
+def gpu_test(f):
+    for mark in gpu:
+        f = mark(f)
+    return f
+
+
+# ---- a stream of the call's own ---------------------------------------------------------
+
+
+def stream_calls(lib, seed=35):
+    """Every entry point as a function of its stream that returns the tensors it made."""
+    lengths = [700, 0, 33, 2000]
+    cu = ref.offsets(lengths, DEV)
+    c, cg = conv_inputs(torch.bfloat16, D=512, lengths=lengths, seed=seed)
+    s, sg = scan_inputs(torch.bfloat16, D=512, lengths=lengths, seed=seed)
+    n, ndy = norm_inputs(torch.bfloat16, 3003, 512, gate=True, seed=seed)
+
+    conv = (c["x"], c["weight"], c["bias"], c["h0"], cu)
+    calls = dict(
+        causal_conv_fwd=lambda st: lib.causal_conv_fwd(*conv, stream=st),
+        causal_conv_bwd=lambda st: lib.causal_conv_bwd(*conv, dy=cg["dy"], dht=cg["dht"], stream=st),
+        selective_scan_fwd=lambda st: lib.selective_scan_fwd(*scan_args(s), cu, stream=st),
+        selective_scan_bwd=lambda st: lib.selective_scan_bwd(*scan_args(s), cu, dy=sg["dy"], dht=sg["dht"], stream=st),
+        layer_norm_fwd=lambda st: [lib.layer_norm_fwd(n["x"], n["weight"], n["bias"], n["z"], stream=st)],
+        layer_norm_bwd=lambda st: lib.layer_norm_bwd(n["x"], n["weight"], n["bias"], n["z"], dy=ndy, stream=st))
+    return {k: (lambda st, f=f: outputs(f(st))) for k, f in calls.items()}
+
+
+def outputs(o):
+    return [v for v in (o.values() if isinstance(o, dict) else o) if v is not None]
+
+
+CALLS = ("causal_conv_fwd", "causal_conv_bwd", "selective_scan_fwd", "selective_scan_bwd", "layer_norm_fwd",
+         "layer_norm_bwd")
+
+
+def stream_of(tensor):
+    """Handle of the stream whose memory a tensor lies in."""
+    at = tensor.data_ptr()
+    return next(s["stream"] for s in torch.cuda.memory_snapshot()
+                if s["address"] <= at < s["address"] + s["total_size"])
+
+
+def reserved(handle):
+    return sum(s["total_size"] for s in torch.cuda.memory_snapshot() if s["stream"] == handle)
+
+
+@gpu_test
+@pytest.mark.parametrize("name", CALLS)
+def test_what_a_call_allocates_is_its_streams(lib, name):
+    """Outputs and workspace come from the memory of the stream that the call was given."""
+    call = stream_calls(lib)[name]
+    side = torch.cuda.Stream()
+    here = torch.cuda.current_stream().cuda_stream
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        torch.cuda.empty_cache()
+        before = reserved(here)
+        outs = call(stream)
+        assert [stream_of(o) for o in outs] == [side.cuda_stream] * len(outs)
+        assert reserved(here) == before
+        side.synchronize()
+    assert all(stream_of(o) == here for o in call(None))
+    torch.cuda.synchronize()
+    ok(lib)
+
+
+@gpu_test
+@pytest.mark.parametrize("name", CALLS)
+def test_calls_on_a_stream_beside_another(lib, name):
+    """Neither memory that the current stream gave back while its work on it waits, nor outputs dropped
+    while the call has yet to run, pass between the two streams."""
+    call = stream_calls(lib)[name]
+    want = call(None)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        # what the current stream will read only later, given back at once
+        held = [torch.full_like(w, 3.0) for w in want for _ in range(2)]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)
+        later = [h.clone() for h in held]
+        del held
+        got = call(stream)
+        torch.cuda.synchronize()
+        assert all((v == 3).all() for v in later)
+        assert same(got, want)
+        # outputs dropped before the call has run
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        del got
+        got = call(stream)[:1]
+        mine = [torch.full_like(w, 5.0) for w in want for _ in range(2)]
+        torch.cuda.synchronize()
+        assert all((v == 5).all() for v in mine)
+        assert same(got, want[:1])
+    ok(lib)
+
+
+@gpu_test
+def test_calls_given_the_default_stream(lib):
+    """The default stream by its handle, 0 or 1, from under another stream."""
+    calls = stream_calls(lib)
+    want = {k: f(None) for k, f in calls.items()}
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        got = [{k: f(handle) for k, f in calls.items()} for handle in (0, 1)]
+    torch.cuda.synchronize()
+    for g in got:
+        for k in want:
+            assert same(g[k], want[k]), k
+            assert all(stream_of(o) == 0 for o in g[k])
