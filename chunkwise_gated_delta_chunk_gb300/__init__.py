@@ -19,8 +19,9 @@ The operators around the recurrence (``include/dn_layer_ops.h``) are
 and :func:`selective_scan_bwd`, :func:`layer_norm_fwd` and
 :func:`layer_norm_bwd`; they check their tensors and allocate what is not given.
 
-A call given a ``stream`` is made as under ``torch.cuda.stream(stream)``: what it
-allocates is that stream's memory, and what it reads has to be ready there.
+These and the conveniences above, given a ``stream``, work as under
+``torch.cuda.stream(stream)``: what they allocate is that stream's memory, and what they
+read has to be ready there.
 """
 from __future__ import annotations
 
@@ -146,6 +147,21 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _under(stream, device, torch):
+    """The context of a given stream (an object or a raw handle), for a call that was given one.
+
+    The whole call is made in it, so that what it allocates comes from that stream's memory.
+    A tensor of another stream's could still be in use there when the call writes it, and
+    could be handed on there before the call is done with it.
+    """
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream if isinstance(stream, int) else stream.cuda_stream
+        # 0 and 1 name the default stream (torch makes a new stream of a handle of 0)
+        stream = (torch.cuda.default_stream(device) if handle in (0, 1)
+                  else torch.cuda.ExternalStream(handle, device=device))
+    return torch.cuda.stream(stream)
+
+
 def dn_chunk_fwd(q, k, v, beta, g, h0, cu_seqlens, n_seqs, B, T, Nk, Nv, dk, dv, dtype,
                  scale, chunk, o, ht, workspace=None, workspace_bytes=None, stream=None,
                  flags=0) -> int:
@@ -194,6 +210,10 @@ def recurrent_fwd(q, k, v, beta, g=None, h0=None, cu_seqlens=None, scale=None,
     """Allocate ``o`` (and ``ht``) and run :func:`dn_recurrent_fwd` (shapes
     and options as for :func:`chunk_fwd`)."""
     import torch
+    if stream is not None:
+        with _under(stream, q.device, torch):
+            return recurrent_fwd(q, k, v, beta, g, h0, cu_seqlens, scale, output_final_state, None,
+                                 o, ht, use_qk_l2norm_in_kernel)
     B, T, Nk, dk = q.shape
     Nv, dv = v.shape[2], v.shape[3]
     N = (cu_seqlens.numel() - 1) if cu_seqlens is not None else B
@@ -262,6 +282,10 @@ def chunk_fwd(q, k, v, beta, g=None, h0=None, cu_seqlens=None, scale=None,
     ``output_final_state``).
     """
     import torch
+    if stream is not None:
+        with _under(stream, q.device, torch):
+            return chunk_fwd(q, k, v, beta, g, h0, cu_seqlens, scale, output_final_state, chunk,
+                             None, o, ht, workspace, use_qk_l2norm_in_kernel)
     B, T, Nk, dk = q.shape
     Nv, dv = v.shape[2], v.shape[3]
     N = (cu_seqlens.numel() - 1) if cu_seqlens is not None else B
@@ -311,6 +335,10 @@ def chunk_bwd(q, k, v, beta, g=None, h0=None, cu_seqlens=None, scale=None, do=No
     ``dbeta``, ``dg`` (None when g is None) and ``dh0`` (None when h0 is None).
     """
     import torch
+    if stream is not None:
+        with _under(stream, q.device, torch):
+            return chunk_bwd(q, k, v, beta, g, h0, cu_seqlens, scale, do, dht, None, workspace,
+                             use_qk_l2norm_in_kernel)
     B, T, Nk, dk = q.shape
     Nv, dv = v.shape[2], v.shape[3]
     N = (cu_seqlens.numel() - 1) if cu_seqlens is not None else B
@@ -356,21 +384,6 @@ def _device_of(x, torch):
     if device.index != torch._C._cuda_getDevice():
         raise ValueError("tensors are on %s, which is not the current device" % device)
     return device
-
-
-def _under(stream, device, torch):
-    """The context of a given stream (an object or a raw handle), for a call that was given one.
-
-    The whole call is made in it, so that what it allocates comes from that stream's memory.
-    A tensor of another stream's could still be in use there when the call writes it, and
-    could be handed on there before the call is done with it.
-    """
-    if not isinstance(stream, torch.cuda.Stream):
-        handle = stream if isinstance(stream, int) else stream.cuda_stream
-        # 0 and 1 name the default stream (torch makes a new stream of a handle of 0)
-        stream = (torch.cuda.default_stream(device) if handle in (0, 1)
-                  else torch.cuda.ExternalStream(handle, device=device))
-    return torch.cuda.stream(stream)
 
 
 def _sequences(B, cu_seqlens, device):
