@@ -34,8 +34,8 @@
 // the cycles.  With the states of 8 tokens in registers, 253 a thread and 8 warps, the
 // reverse walk took 443 us.
 //
-// Measured (bf16, N = 16, gate, 4 x 2048 tokens of 2048 channels): 514 us (states 100,
-// their steps 14, reverse walk 386, sums 12).
+// Measured (bf16, N = 16, gate, 4 x 2048 tokens of 2048 channels): 516 us (states 100,
+// their steps 14, reverse walk 388, sums 12).
 #include "dn_scan.cuh"
 
 namespace dn {
@@ -405,6 +405,9 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd(ScanParams p, int parts)
                         if (lane < 4) s_res[2][u + lane][ch + c] = y;
                     }
                 float ps[2][4], pq[2][4];
+                // Tokens of the half up to the chunk's last.  Those behind it have no step, but the
+                // state before them may be infinite, and no step times that is not 0: d_A skips them.
+                const int left = len - k * kPiece - u;
 #pragma unroll
                 for (int w = 3; w >= 0; --w) {
                     const int t = u + w;
@@ -424,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd(ScanParams p, int parts)
                             const f2 gr = fma2(g2, cc[i], carry[c][i]);
                             carry[c][i] = mul2(gr, decay(d2, c, i));
                             const f2 qq = mul2(carry[c][i], hh[w][c][i]);
-                            dA[c][i] = fma2(d2, qq, dA[c][i]);
+                            dA[c][i] = fma2(d2, w < left ? qq : 0ull, dA[c][i]);
                             q2 = fma2(qq, a2[c][i], q2);
                             s2 = fma2(gr, bb[i], s2);
                             vb[i] = fma2(gr, x2, vb[i]);

@@ -138,3 +138,34 @@ def test_calls_given_the_default_stream(lib):
         for k in want:
             assert agree(k, g[k], want[k]), k
             assert all(stream_of(o) == 0 for o in g[k])
+
+
+# ---- infinities -----------------------------------------------------------------------------
+
+
+@gpu_test
+@pytest.mark.parametrize("lengths", [[21], [24], [1, 9, 16, 30], [131], [0, 70, 3]])
+@pytest.mark.parametrize("N", [16, 64])
+def test_scan_gradient_of_the_rates_beside_an_overflow(lib, lengths, N):
+    """The last token's state overflows fp32 in one channel.  d_A takes the states before a token alone, and
+    those are finite: it is what it is in 64 bits, whether or not the length fills the kernel's pieces."""
+    t, grads = scan_inputs(torch.float32, D=12, N=N, lengths=lengths, gate=False, seed=15)
+    t["dt"], t["dt_bias"] = t["dt"].abs() * 0.2 + 0.05, None
+    at, n = 0, []
+    for length in lengths:
+        if length:
+            last = at + length - 1
+            t["dt"][0, last], t["B"][0, last], t["x"][0, last, 3] = 1.0, 4.0, 2e38
+            n.append(last)
+        at += length
+    grads["dy"][0, n] *= 1e-3
+    cu = ref.offsets(lengths, DEV)
+    y, ht = lib.selective_scan_fwd(*scan_args(t), cu, dt_softplus=False)
+    assert all(torch.isinf(ht[i, 3]).all() for i, length in enumerate(lengths) if length)
+    out = lib.selective_scan_bwd(*scan_args(t), cu, dt_softplus=False, dy=grads["dy"])
+    ok(lib)
+    leaves = ref.in_64_bits(t, grad=True)
+    y64, ht64 = ref.scan(leaves, lengths, softplus=False)
+    want = ref.gradients([y64, ht64], [grads["dy"], None], leaves)["A"]
+    # roundings of test_layer_ops.scan_check
+    ref.close(out["dA"], want, 30 * max(lengths) + 64 + sum(lengths), "dA")
