@@ -377,6 +377,16 @@ __global__ void __launch_bounds__(128) scan_step(ScanParams p) {
 
 // ---- states over the chunks of a sequence ------------------------------------------
 
+// e^{sum A} s + own over one chunk, `half` being half the rate.  A chunk's decay can lie below
+// (or its growth above) what fp32 holds while no token's does, and then one factor of 0 (or
+// infinity) would make NaN of an infinite state (or of none).  So it is taken as two equal
+// factors, neither of them 0 or infinite: a finite state that the limits change is below
+// 2^-124 all the same (or infinite).
+__device__ __forceinline__ float step_chunk(float sum, float half, float s, float own) {
+    const float f = ex2(fminf(fmaxf(sum * half, -126.f), 127.f));
+    return fmaf(f, f * s, own);
+}
+
 // (see scan_combine_launch; blockIdx.y = 1: the gradients' walk back).  A thread takes four
 // states and loads kAhead chunks at a time: the walk is bound by latency.
 template <bool BWD>
@@ -401,7 +411,7 @@ __global__ void __launch_bounds__(128) scan_combine(ScanParams p) {
         slot = (chunks > 0 ? chunks : 1) * (long long)n;
     }
     float4 A = *reinterpret_cast<const float4 *>(p.A + at * 4);
-    A = make_float4(log2_rate(A.x), log2_rate(A.y), log2_rate(A.z), log2_rate(A.w));
+    A = make_float4(0.5f * log2_rate(A.x), 0.5f * log2_rate(A.y), 0.5f * log2_rate(A.z), 0.5f * log2_rate(A.w));
     const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
     const long long mine = (long long)n * per + at;
     const bool back = BWD && blockIdx.y;
@@ -426,10 +436,10 @@ __global__ void __launch_bounds__(128) scan_combine(ScanParams p) {
             if (c + k < chunks) {
                 vs[(c + k) * step * per] = s;
                 if (back || c + k < chunks - 1) {
-                    s.x = fmaf(ex2(sum[k] * A.x), s.x, own[k].x);
-                    s.y = fmaf(ex2(sum[k] * A.y), s.y, own[k].y);
-                    s.z = fmaf(ex2(sum[k] * A.z), s.z, own[k].z);
-                    s.w = fmaf(ex2(sum[k] * A.w), s.w, own[k].w);
+                    s.x = step_chunk(sum[k], A.x, s.x, own[k].x);
+                    s.y = step_chunk(sum[k], A.y, s.y, own[k].y);
+                    s.z = step_chunk(sum[k], A.z, s.z, own[k].z);
+                    s.w = step_chunk(sum[k], A.w, s.w, own[k].w);
                 }
             }
     }

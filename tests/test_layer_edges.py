@@ -169,3 +169,29 @@ def test_scan_gradient_of_the_rates_beside_an_overflow(lib, lengths, N):
     want = ref.gradients([y64, ht64], [grads["dy"], None], leaves)["A"]
     # roundings of test_layer_ops.scan_check
     ref.close(out["dA"], want, 30 * max(lengths) + 64 + sum(lengths), "dA")
+
+
+@gpu_test
+@pytest.mark.parametrize("lengths", [[200], [40, 333, 0, 75], [1000]])
+def test_scan_infinite_state_stays_infinite_over_chunks(lib, lengths):
+    """Each token's decay is e^-6, a chunk's lies below what fp32 holds: an infinite state decays to
+    an infinite one all the same."""
+    t, _ = scan_inputs(torch.float32, D=7, lengths=lengths, gate=False, seed=16)
+    t["dt"], t["dt_bias"], t["A"] = torch.full_like(t["dt"], 2.0), None, torch.full_like(t["A"], -3.0)
+    at = 0
+    for length in lengths:
+        if length:
+            t["x"][0, at + 5, 3] = float("inf")
+        at += length
+    cu = ref.offsets(lengths, DEV)
+    assert lib.load().dn_selective_scan_fwd_workspace_bytes(len(lengths), 1, sum(lengths), 7, 1, 16, lib.DN_F32) > 0
+    y64, ht64 = ref.scan(ref.in_64_bits(t), lengths, softplus=False)
+    y, ht = lib.selective_scan_fwd(*scan_args(t), cu, dt_softplus=False)
+    ok(lib)
+    for n, length in enumerate(lengths):
+        if length:
+            assert torch.isinf(ht64[n, 3]).all()
+            assert torch.equal(ht[n, 3].double().cpu(), ht64[n, 3])
+    keep = [d for d in range(7) if d != 3]
+    ref.close(y[:, :, keep], y64[:, :, keep], 10 * max(lengths) + 64, "y of the others")
+    ref.close(ht[:, keep], ht64[:, keep], 10 * max(lengths) + 64, "ht of the others")
