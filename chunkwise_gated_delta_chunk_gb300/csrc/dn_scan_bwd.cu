@@ -493,10 +493,13 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd(ScanParams p, int parts)
                 for (int i = 0; i < 4; ++i) {
                     const float s = s_res[0][at.t][at.c + i], r = s_res[1][at.t][at.c + i];
                     const float delta = s_d[k * kPiece + at.t][at.c + i], go = s_go[at.t][at.c + i];
-                    ox[i] = fmaf(delta, s, skip[i] * go);
+                    ox[i] = p.Dskip ? fmaf(delta, s, skip[i] * go) : delta * s;
                     od[i] = fmaf(fx[i], s, r);
                     if (p.softplus) od[i] *= sigmoid_f(fd[i] + bias[i]);
-                    if (p.z) oz[i] = fg[i] * fmaf(skip[i], fx[i], s_res[2][at.t][at.c + i]) * silu_grad_f(fz[i]);
+                    if (p.z) {
+                        const float y = s_res[2][at.t][at.c + i];
+                        oz[i] = fg[i] * (p.Dskip ? fmaf(skip[i], fx[i], y) : y) * silu_grad_f(fz[i]);
+                    }
                     if (i < at.n) {
                         sD[i] = fmaf(go, fx[i], sD[i]);
                         sb[i] += od[i];

@@ -106,7 +106,7 @@ size_t dn_causal_conv_bwd_workspace_bytes(int n_seqs, int B, int T, int D, int W
  *   x, dt    [B, T, D]       dtype
  *   A        [D, N]          float32
  *   Bm, Cm   [B, T, G, N]    dtype
- *   Dskip    [D]             float32   or NULL: zero
+ *   Dskip    [D]             float32   or NULL: no such term
  *   z        [B, T, D]       dtype     or NULL: no factor silu(z)
  *   dt_bias  [D]             float32   or NULL: zero
  *   h0, ht   [n_seqs, D, N]  float32   NULL: zero / not written.  ht may be h0.

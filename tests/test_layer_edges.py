@@ -195,3 +195,23 @@ def test_scan_infinite_state_stays_infinite_over_chunks(lib, lengths):
     keep = [d for d in range(7) if d != 3]
     ref.close(y[:, :, keep], y64[:, :, keep], 10 * max(lengths) + 64, "y of the others")
     ref.close(ht[:, keep], ht64[:, keep], 10 * max(lengths) + 64, "ht of the others")
+
+
+@gpu_test
+@pytest.mark.parametrize("T", [1, 2, 33, 200])
+@pytest.mark.parametrize("G", [1, 2])
+def test_scan_without_d_has_no_such_term(lib, T, G):
+    """D absent: an infinite input gives what C h gives, not a NaN of 0 times infinity; the same in a prompt
+    and in a single token, and in the gradient of the gate."""
+    t, grads = scan_inputs(torch.float32, B=2, T=T, D=2 * 3 * G, G=G, extras=False, seed=17)
+    t["B"], t["C"], t["z"] = t["B"].abs() + 0.1, t["C"].abs() + 0.1, t["z"].abs() + 0.1
+    t["x"][1, T - 1, 4] = float("inf")
+    y64, ht64 = ref.scan(ref.in_64_bits(t))
+    y, ht = lib.selective_scan_fwd(*scan_args(t))
+    out = lib.selective_scan_bwd(*scan_args(t), dy=grads["dy"])
+    ok(lib)
+    assert y64[1, T - 1, 4] == float("inf") and y[1, T - 1, 4] == float("inf")
+    assert torch.isinf(ht[1, 4]).all()
+    assert torch.isinf(out["dz"][1, T - 1, 4])
+    keep = [d for d in range(t["x"].shape[2]) if d != 4]
+    ref.close(y[:, :, keep], y64[:, :, keep], 10 * T + 64, "y of the others")
