@@ -183,6 +183,38 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_state(ScanParams p) {
             }
         }
     }
+    // A sum that is not finite: the product of the decays may have left fp32 (rates above zero, or
+    // a decay below it beside an infinite d_y) where the gradient itself does not.  It is taken
+    // again as it is defined, from the last token back; only such calls pay for it.
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        float r[4], w[4];
+        split(rg[c][0], r[0], r[1]);
+        split(rg[c][1], r[2], r[3]);
+        if (!own[c] || (r[0] - r[0]) + (r[1] - r[1]) + (r[2] - r[2]) + (r[3] - r[3]) == 0.f) continue;
+        split(a[c][0], w[0], w[1]);
+        split(a[c][1], w[2], w[3]);
+        r[0] = r[1] = r[2] = r[3] = 0.f;
+        const int d = cs.d0 + ch + c;
+#pragma unroll 1
+        for (long long t = seq.t1 - 1; t >= seq.t0; --t) {
+            Vec<T, 1> dt, dy, z;
+            Vec<T, 4> cv;
+            dt.load(static_cast<const T *>(p.dt) + t * p.D + d);
+            dy.load(static_cast<const T *>(p.dy) + t * p.D + d);
+            cv.load(static_cast<const T *>(p.Cm) + (t * p.G + cs.g) * N + lane * kS);
+            float go = dy.v[0];
+            if (p.z) {
+                z.load(static_cast<const T *>(p.z) + t * p.D + d);
+                go *= silu_f(z.v[0]);
+            }
+            const float raw = dt.v[0] + (p.dt_bias ? p.dt_bias[d] : 0.f), delta = p.softplus ? softplus(raw) : raw;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r[i] = fmaf(cv.v[i], go, r[i]) * ex2(delta * w[i]);
+        }
+        rg[c][0] = pair(r[0], r[1]);
+        rg[c][1] = pair(r[2], r[3]);
+    }
 #pragma unroll
     for (int c = 0; c < 2; ++c)
         if (own[c]) {

@@ -215,3 +215,44 @@ def test_scan_without_d_has_no_such_term(lib, T, G):
     assert torch.isinf(out["dz"][1, T - 1, 4])
     keep = [d for d in range(t["x"].shape[2]) if d != 4]
     ref.close(y[:, :, keep], y64[:, :, keep], 10 * T + 64, "y of the others")
+
+
+@gpu_test
+@pytest.mark.parametrize("T", [100, 333])
+def test_scan_growing_rates(lib, T):
+    """Rates above zero: a chunk's growth passes what fp32 holds while nothing is there to grow (no input
+    before the last tokens, no gradient behind the first).  Nothing stays nothing, in states and gradients."""
+    t, grads = scan_inputs(torch.float32, B=1, T=T, D=9, gate=True, h0=False, seed=18)
+    t["dt"], t["dt_bias"] = torch.full_like(t["dt"], 1.0), None
+    t["A"] = torch.full_like(t["A"], 6.0 if T == 100 else 2.0)
+    t["x"][:, :T - 8] = 0
+    grads["dy"][:, 8:] = 0
+    y64, ht64 = ref.scan(leaves := ref.in_64_bits(t, grad=True), softplus=False)
+    y, ht = lib.selective_scan_fwd(*scan_args(t), dt_softplus=False)
+    ref.close(y, y64, 10 * T + 64, "y")
+    ref.close(ht, ht64, 10 * T + 64, "ht")
+    out = lib.selective_scan_bwd(*scan_args(t), dt_softplus=False, dy=grads["dy"])
+    ok(lib)
+    want = ref.gradients([y64], [grads["dy"]], leaves)
+    for name in NAMES:
+        if t[name] is not None:
+            ref.close(out["d" + name], want[name], 30 * T + 64, "d" + name)
+
+
+@gpu_test
+def test_scan_small_gradient_grows_past_a_chunk_s_factor(lib):
+    """A gradient of 1e-30 eleven tokens on, rates of e^9: the product of the rates passes fp32, the gradient
+    at the first token does not."""
+    t, grads = scan_inputs(torch.float32, B=1, T=40, D=9, gate=False, h0=True, extras=False, seed=19)
+    t["dt"], t["A"] = torch.full_like(t["dt"], 1.0), torch.full_like(t["A"], 9.0)
+    t["x"][:] = 0
+    t["h0"][:] = 0
+    grads["dy"][:] = 0
+    grads["dy"][0, 11] = 1e-30
+    out = lib.selective_scan_bwd(*scan_args(t), dt_softplus=False, dy=grads["dy"])
+    ok(lib)
+    leaves = ref.in_64_bits(t, grad=True)
+    y64, _ = ref.scan(leaves, softplus=False)
+    want = ref.gradients([y64], [grads["dy"]], leaves)
+    for name in ("x", "h0"):
+        ref.close(out["d" + name], want[name], 30 * 40 + 64, "d" + name)
