@@ -220,11 +220,13 @@ __global__ void __launch_bounds__(kConvThreads) conv_step(ConvParams p, int cols
 }
 
 template <typename T, int W, int V>
-cudaError_t conv_fwd_v(const ConvParams &p, cudaStream_t stream) {
+cudaError_t conv_fwd_v(const ConvParams &p, cudaStream_t stream, bool &step) {
     const int cols = p.D / V;
+    step = false;
     if (!p.seq.cu && p.seq.T == 1) {
         const long long nbx = (cols + kConvThreads - 1) / kConvThreads, grid = nbx * p.seq.N;
         if (grid <= 0x7fffffffLL) {
+            step = true;
             conv_step<T, W, V><<<(unsigned)grid, kConvThreads, 0, stream>>>(p, cols, (unsigned)nbx);
             return cudaGetLastError();
         }
@@ -241,17 +243,18 @@ cudaError_t conv_fwd_v(const ConvParams &p, cudaStream_t stream) {
 }
 
 template <typename T, int W>
-cudaError_t conv_fwd_w(const ConvParams &p, cudaStream_t stream) {
+cudaError_t conv_fwd_w(const ConvParams &p, cudaStream_t stream, bool &step) {
     constexpr int V = kFwdV;
-    return p.D % V == 0 ? conv_fwd_v<T, W, V>(p, stream) : conv_fwd_v<T, W, 1>(p, stream);
+    return p.D % V == 0 ? conv_fwd_v<T, W, V>(p, stream, step) : conv_fwd_v<T, W, 1>(p, stream, step);
 }
 
+// `step`: whether the kernel for single tokens was taken
 template <typename T>
-cudaError_t conv_fwd_t(const ConvParams &p, cudaStream_t stream) {
+cudaError_t conv_fwd_t(const ConvParams &p, cudaStream_t stream, bool &step) {
     switch (p.W) {
-        case 2: return conv_fwd_w<T, 2>(p, stream);
-        case 3: return conv_fwd_w<T, 3>(p, stream);
-        default: return conv_fwd_w<T, 4>(p, stream);
+        case 2: return conv_fwd_w<T, 2>(p, stream, step);
+        case 3: return conv_fwd_w<T, 3>(p, stream, step);
+        default: return conv_fwd_w<T, 4>(p, stream, step);
     }
 }
 
@@ -544,8 +547,10 @@ cudaError_t conv_bwd_t(const ConvParams &p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t conv_fwd_launch(const ConvParams &p, bool bf16, cudaStream_t stream, const char **name) {
-    *name = bf16 ? "conv_fwd<bf16>" : "conv_fwd<f32>";
-    return bf16 ? conv_fwd_t<__nv_bfloat16>(p, stream) : conv_fwd_t<float>(p, stream);
+    bool step = false;
+    const cudaError_t err = bf16 ? conv_fwd_t<__nv_bfloat16>(p, stream, step) : conv_fwd_t<float>(p, stream, step);
+    *name = step ? bf16 ? "conv_step<bf16>" : "conv_step<f32>" : bf16 ? "conv_fwd<bf16>" : "conv_fwd<f32>";
+    return err;
 }
 
 size_t conv_bwd_workspace(long long tokens, int n_seqs, int D, int W, bool bf16) {
@@ -554,7 +559,7 @@ size_t conv_bwd_workspace(long long tokens, int n_seqs, int D, int W, bool bf16)
 }
 
 cudaError_t conv_bwd_launch(const ConvParams &p, bool bf16, cudaStream_t stream, const char **name) {
-    *name = bf16 ? "conv_bwd<bf16>" : "conv_bwd<f32>";
+    *name = bf16 ? "conv_bwd+conv_bwd_sums<bf16>" : "conv_bwd+conv_bwd_sums<f32>";
     if (!bf16) return conv_bwd_t<float, float>(p, stream);
     return p.dy_f32 ? conv_bwd_t<__nv_bfloat16, float>(p, stream) : conv_bwd_t<__nv_bfloat16, __nv_bfloat16>(p, stream);
 }

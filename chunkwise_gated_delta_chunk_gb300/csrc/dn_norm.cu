@@ -475,7 +475,9 @@ cudaError_t norm_fwd_launch(const NormParams &p, bool bf16, cudaStream_t stream,
 }
 
 cudaError_t norm_bwd_launch(const NormParams &p, bool bf16, cudaStream_t stream, const char **name) {
-    *name = bf16 ? "norm_bwd<bf16>" : "norm_bwd<f32>";
+    if (p.rows == 0) *name = "norm_bwd_sums";
+    else if (p.partial) *name = bf16 ? "norm_bwd+norm_bwd_sums<bf16>" : "norm_bwd+norm_bwd_sums<f32>";
+    else *name = bf16 ? "norm_bwd<bf16>" : "norm_bwd<f32>";
     return bf16 ? norm_dispatch<__nv_bfloat16>(p, true, stream, nullptr) : norm_dispatch<float>(p, true, stream, nullptr);
 }
 

@@ -717,7 +717,11 @@ void scan_bwd_carve(ScanParams &p, void *workspace) {
 }
 
 cudaError_t scan_bwd_launch(ScanParams p, bool bf16, cudaStream_t stream, const char **name) {
-    *name = bf16 ? "scan_bwd_state+scan_combine+scan_bwd<bf16>" : "scan_bwd_state+scan_combine+scan_bwd<f32>";
+#define DN_SCAN_BWD "scan_bwd_state+scan_combine+scan_bwd+"
+    if (p.seq.N == 0) *name = "scan_bwd_sums";
+    else if (p.seq.tokens == 0) *name = bf16 ? DN_SCAN_BWD "scan_bwd_sums<bf16>" : DN_SCAN_BWD "scan_bwd_sums<f32>";
+    else *name = bf16 ? DN_SCAN_BWD "scan_bwd_bc+scan_bwd_sums<bf16>" : DN_SCAN_BWD "scan_bwd_bc+scan_bwd_sums<f32>";
+#undef DN_SCAN_BWD
     return bf16 ? bwd_t<__nv_bfloat16>(p, stream) : bwd_t<float>(p, stream);
 }
 

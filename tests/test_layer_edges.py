@@ -256,3 +256,35 @@ def test_scan_small_gradient_grows_past_a_chunk_s_factor(lib):
     want = ref.gradients([y64], [grads["dy"]], leaves)
     for name in ("x", "h0"):
         ref.close(out["d" + name], want[name], 30 * 40 + 64, "d" + name)
+
+
+# ---- what the library says of a call, and what it refuses --------------------------------------
+
+
+@gpu_test
+@pytest.mark.parametrize("dtype,short", [(torch.bfloat16, "bf16"), (torch.float32, "f32")])
+def test_last_kernel_tells_the_path(lib, dtype, short):
+    """dn_last_kernel names the kernels that a call launched: single tokens, whole sequences, chunks."""
+    for T, conv, scan in ((1, "conv_step", "scan_step"), (20, "conv_fwd", "scan_fwd"),
+                          (500, "conv_fwd", "scan_state+scan_combine+scan_fwd")):
+        c, _ = conv_inputs(dtype, B=2, T=T, D=24, seed=1)
+        lib.causal_conv_fwd(c["x"], c["weight"], c["bias"], c["h0"])
+        assert lib.dn_last_kernel() == "%s<%s>" % (conv, short)
+        s, _ = scan_inputs(dtype, B=2, T=T, D=24, seed=1)
+        lib.selective_scan_fwd(*scan_args(s))
+        assert lib.dn_last_kernel() == "%s<%s>" % (scan, short)
+        lib.causal_conv_bwd(c["x"], c["weight"], c["bias"], c["h0"], dy=c["x"])
+        assert lib.dn_last_kernel() == "conv_bwd+conv_bwd_sums<%s>" % short
+        lib.selective_scan_bwd(*scan_args(s), dy=s["x"])
+        assert lib.dn_last_kernel() == "scan_bwd_state+scan_combine+scan_bwd+scan_bwd_bc+scan_bwd_sums<%s>" % short
+    n, dy = norm_inputs(dtype, 5, 24, seed=1)
+    lib.layer_norm_fwd(n["x"], n["weight"])
+    assert lib.dn_last_kernel() == "norm_fwd<%s>" % short
+    lib.layer_norm_bwd(n["x"], n["weight"], dy=dy)
+    assert lib.dn_last_kernel() == "norm_bwd+norm_bwd_sums<%s>" % short
+    lib.layer_norm_bwd(n["x"], dy=dy)
+    assert lib.dn_last_kernel() == "norm_bwd<%s>" % short
+    cu = ref.offsets([1, 1], DEV)  # offsets are on the device: these tokens are not known to be single ones
+    lib.causal_conv_fwd(c["x"][:1, :2].contiguous(), c["weight"], c["bias"], c["h0"], cu)
+    assert lib.dn_last_kernel() == "conv_fwd<%s>" % short
+    ok(lib)
