@@ -73,23 +73,16 @@ struct Row {
     static __device__ __forceinline__ bool in(int k, int i, int D) { return col(k, kWhole ? 0 : i) < D; }
 };
 
-// Vector k of a row, and of one of the fp32 vectors, as pairs; `other` where it does not exist.
-template <typename L, int V, typename T>
-__device__ __forceinline__ void load_row(f2 (&v)[V / 2], const T *src, int k, int D) {
-    Pack<T, V> r;
-    if constexpr (L::kWhole) {
-        r.clear();
-        if (L::in(k, 0, D)) r.load(src + L::col(k, 0));
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) v[i] = pair(r[2 * i], r[2 * i + 1]);
-    } else {
-        Vec<T, 1> a, b;
-        a.v[0] = b.v[0] = 0.f;
-        if (L::in(k, 0, D)) a.load(src + L::col(k, 0));
-        if (L::in(k, 1, D)) b.load(src + L::col(k, 1));
-        v[0] = pair(a.v[0], b.v[0]);
-    }
+// Vector k of a row taken element by element, as one pair; zeros where it does not exist.
+template <typename L, typename T>
+__device__ __forceinline__ f2 load_elements(const T *src, int k, int D) {
+    Vec<T, 1> a, b;
+    a.v[0] = b.v[0] = 0.f;
+    if (L::in(k, 0, D)) a.load(src + L::col(k, 0));
+    if (L::in(k, 1, D)) b.load(src + L::col(k, 1));
+    return pair(a.v[0], b.v[0]);
 }
+// Vector k of one of the fp32 vectors as pairs; `other` where it does not exist.
 template <typename L, int V>
 __device__ __forceinline__ void load_vec(f2 (&v)[V / 2], const float *src, int k, int D, float other) {
     if constexpr (L::kWhole) {
@@ -159,7 +152,7 @@ struct Ring {
 #pragma unroll
             for (int i = 0; i < L::P; ++i) v[i] = pair(r[2 * i], r[2 * i + 1]);
         } else {
-            load_row<L, V>(v, base[a] + row * p.D, k, row < p.rows ? p.D : 0);
+            v[0] = load_elements<L>(base[a] + row * p.D, k, row < p.rows ? p.D : 0);
         }
     }
 };
