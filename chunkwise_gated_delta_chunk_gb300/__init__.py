@@ -386,6 +386,12 @@ def _device_of(x, torch):
     return device
 
 
+def _fit(what, sizes):
+    """Refuses sizes (or'ed together) that an int of the C arguments would cut short."""
+    if sizes >> 31:
+        raise DnError(DN_ERR_UNSUPPORTED, what)
+
+
 def _sequences(B, cu_seqlens, device):
     """Number of sequences and the offsets' address."""
     import torch
@@ -438,6 +444,7 @@ def causal_conv_fwd(x, weight, bias=None, h0=None, cu_seqlens=None, silu=True,
     f32, dt = torch.float32, x.dtype
     code = dtype_code(dt)
     N, cu = _sequences(B, cu_seqlens, device)
+    _fit("dn_causal_conv_fwd", N | B | T | D | W)
     state = (N, W - 1, D)
     if y is None:
         y = torch.empty_like(x, memory_format=torch.contiguous_format)
@@ -473,6 +480,7 @@ def causal_conv_bwd(x, weight, bias=None, h0=None, cu_seqlens=None, silu=True, d
     f32, dt = torch.float32, x.dtype
     code = dtype_code(dt)
     N, cu = _sequences(B, cu_seqlens, device)
+    _fit("dn_causal_conv_bwd", N | B | T | D | W)
     state = (N, W - 1, D)
     if dy is None:
         raise ValueError("dy is required")
@@ -496,7 +504,7 @@ def causal_conv_bwd(x, weight, bias=None, h0=None, cu_seqlens=None, silu=True, d
     return out
 
 
-def _scan_inputs(x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, dt_softplus):
+def _scan_inputs(what, x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, dt_softplus):
     """Checked addresses and sizes of a scan, in the order of the C arguments."""
     import torch
     device = _device_of(x, torch)
@@ -505,6 +513,7 @@ def _scan_inputs(x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, dt_softplus):
     f32, ty = torch.float32, x.dtype
     code = dtype_code(ty)
     N, cu = _sequences(Bt, cu_seqlens, device)
+    _fit(what, N | Bt | T | Di | G | Ns)
     rows, bc, state = x.shape, (Bt, T, G, Ns), (N, Di, Ns)
     ptrs = (_operand("x", x, rows, ty, device), _operand("dt", dt, rows, ty, device, False),
             _operand("A", A, (Di, Ns), f32, device, False), _operand("B", B, bc, ty, device, False),
@@ -532,8 +541,8 @@ def selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, cu
         with _under(stream, _device_of(x, torch), torch):
             return selective_scan_fwd(x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, dt_softplus,
                                       output_final_state, None, y, ht, workspace)
-    device, ty, bc, state, ptrs, sizes, flags = _scan_inputs(x, dt, A, B, C, D, z, dt_bias, h0,
-                                                             cu_seqlens, dt_softplus)
+    device, ty, bc, state, ptrs, sizes, flags = _scan_inputs(
+        "dn_selective_scan_fwd", x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, dt_softplus)
     if y is None:
         y = torch.empty_like(x, memory_format=torch.contiguous_format)
     if not output_final_state:
@@ -563,8 +572,8 @@ def selective_scan_bwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, cu
         with _under(stream, _device_of(x, torch), torch):
             return selective_scan_bwd(x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, dt_softplus,
                                       dy, dht, None, workspace)
-    device, ty, bc, state, ptrs, sizes, flags = _scan_inputs(x, dt, A, B, C, D, z, dt_bias, h0,
-                                                             cu_seqlens, dt_softplus)
+    device, ty, bc, state, ptrs, sizes, flags = _scan_inputs(
+        "dn_selective_scan_bwd", x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, dt_softplus)
     f32 = torch.float32
 
     def like(t, shape, dtype):
@@ -600,6 +609,7 @@ def layer_norm_fwd(x, weight=None, bias=None, z=None, eps=1e-5, rms=False, strea
         with _under(stream, device, torch):
             return layer_norm_fwd(x, weight, bias, z, eps, rms, None, y)
     D = x.shape[-1]
+    _fit("dn_layer_norm_fwd", D)
     f32, dt = torch.float32, x.dtype
     if y is None:
         y = torch.empty_like(x, memory_format=torch.contiguous_format)
@@ -626,6 +636,7 @@ def layer_norm_bwd(x, weight=None, bias=None, z=None, eps=1e-5, rms=False, dy=No
         with _under(stream, device, torch):
             return layer_norm_bwd(x, weight, bias, z, eps, rms, dy, None, workspace)
     D = x.shape[-1]
+    _fit("dn_layer_norm_bwd", D)
     rows = x.numel() // D if D else 0
     f32, dt = torch.float32, x.dtype
     code = dtype_code(dt)

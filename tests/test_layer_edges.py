@@ -288,3 +288,35 @@ def test_last_kernel_tells_the_path(lib, dtype, short):
     lib.causal_conv_fwd(c["x"][:1, :2].contiguous(), c["weight"], c["bias"], c["h0"], cu)
     assert lib.dn_last_kernel() == "conv_fwd<%s>" % short
     ok(lib)
+
+
+@pytest.mark.parametrize("shape", [(1, 2**32 + 3, 1), (2**32 + 2, 1, 1), (1, 1, 2**32 + 8)])
+def test_sizes_above_an_int_are_refused(monkeypatch, shape):
+    """A size that the C arguments cannot hold is an error, not another size (tensors without memory)."""
+    import chunkwise_gated_delta_chunk_gb300 as dn
+    monkeypatch.setattr(dn, "_device_of", lambda x, torch: x.device)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 0, raising=False)
+
+    def empty(*s):
+        return torch.empty(s, device="meta")
+
+    B, T, D = shape
+    x = empty(*shape)
+    calls = [lambda: dn.causal_conv_fwd(x, empty(D, 4)), lambda: dn.causal_conv_bwd(x, empty(D, 4), dy=x),
+             lambda: dn.selective_scan_fwd(x, x, empty(D, 16), empty(B, T, 1, 16), empty(B, T, 1, 16)),
+             lambda: dn.selective_scan_bwd(x, x, empty(D, 16), empty(B, T, 1, 16), empty(B, T, 1, 16), dy=x)]
+    if D > 1:
+        calls += [lambda: dn.layer_norm_fwd(x), lambda: dn.layer_norm_bwd(x, dy=x)]
+    for call in calls:
+        with pytest.raises(dn.DnError) as e:
+            call()
+        assert e.value.status == dn.DN_ERR_UNSUPPORTED
+
+
+def test_more_sequences_than_an_int_are_refused(monkeypatch):
+    import chunkwise_gated_delta_chunk_gb300 as dn
+    monkeypatch.setattr(dn, "_device_of", lambda x, torch: x.device)
+    x, cu = torch.empty(1, 8, 8, device="meta"), torch.empty(2**32 + 2, dtype=torch.int64, device="meta")
+    with pytest.raises(dn.DnError) as e:
+        dn.causal_conv_fwd(x, torch.empty(8, 4, device="meta"), cu_seqlens=cu, output_final_state=False)
+    assert e.value.status == dn.DN_ERR_UNSUPPORTED
