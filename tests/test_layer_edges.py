@@ -140,6 +140,28 @@ def test_calls_given_the_default_stream(lib):
             assert all(stream_of(o) == 0 for o in g[k])
 
 
+@gpu_test
+@pytest.mark.parametrize("name", CALLS)
+def test_calls_given_a_stream_that_is_captured(lib, name):
+    """The capturing stream as an argument, by object and by handle: replays give the call's results."""
+    call = stream_calls(lib)[name]
+    want = call(None)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(side):
+            with torch.cuda.graph(graph, stream=side):
+                held = call(stream)
+        for _ in range(2):
+            for h in held:
+                h.fill_(7)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert agree(name, held, want)
+    ok(lib)
+
+
 # ---- infinities -----------------------------------------------------------------------------
 
 
