@@ -11,10 +11,11 @@
 //     dx_s = sum_i weight[W-1-i] du_{s+i},  dweight[j] = sum_t du_t x_{t-(W-1)+j},  dbias = sum_t du_t
 // One thread owns 4 (bf16) or 2 (fp32) channels and walks a tile and the W - 1
 // tokens behind it (whose du reach back into the tile), the last W inputs and du in
-// registers.  The rate of issue bounds it: written plainly it takes 182 instructions for
+// registers.  Its instructions cost it more than its bytes: written plainly it takes 182 for
 // 4 channels of a token.  Pairs of channels in the two-wide fp32 instructions, rings of W
 // registers that turn whole within an unrolled group, and a path of its own for tokens at
-// a tile's edges bring that to 106 (and 221 us to 75).  Rows come by asynchronous copies
+// a tile's edges bring that to 106 (and 221 us to 74).  Now the latency between dependent ones bounds it:
+// 12 warps an SM issue in 0.49 of the cycles, and each thread has two chains of W fma2.  Rows come by asynchronous copies
 // into the thread's own part of shared memory, so that they hold no registers.  The sums
 // over tokens stay in registers over all tiles of a block, are joined over its warps and
 // written as one row per block; a second kernel adds the rows in a fixed order.
@@ -22,7 +23,7 @@
 // Both move 2 (forward) and 3 (backward) elements per channel and token for about
 // W products and one exponential each.  Measured (bf16, W = 4, silu, 6144 channels):
 // forward over 20741 packed tokens 90 us, 5.6 TB/s, bound by memory; backward over
-// 4 x 2048 tokens 75 us, 4.0 TB/s.
+// 4 x 2048 tokens 74 us, 4.1 TB/s.
 #include <type_traits>
 
 #include "dn_layer.cuh"

@@ -252,6 +252,7 @@ __device__ __forceinline__ float rcp(float x) {
 
 // 1 / (1 + e^-u), from the two approximate instructions (each within two units
 // of fp32's last place; the exponent's rounding adds |u| 2^-24 of the value).
+// Below u = -87.3 it is 0, and so is silu, whose value there is above -1.2e-36.
 __device__ __forceinline__ float sigmoid_f(float u) { return rcp(1.f + ex2(-kLog2e * u)); }
 __device__ __forceinline__ float silu_f(float u) { return u * sigmoid_f(u); }
 // d silu(u) / du = s (1 + u (1 - s)), s = sigmoid(u)
@@ -261,7 +262,7 @@ __device__ __forceinline__ float silu_grad_f(float u) {
 }
 
 // Two fp32 values in one register pair, and the instructions that work on both
-// (the rate of issue is what bounds most of these kernels beside memory).
+// (beside memory, the number of instructions is what most of these kernels pay for).
 typedef unsigned long long f2;
 __device__ __forceinline__ f2 pair(float lo, float hi) {
     f2 r;

@@ -13,9 +13,10 @@
 // ahead come by asynchronous copies into each thread's own part of shared memory,
 // so that the sums' latency and the barriers do not keep memory idle (loaded into
 // registers row by row, the backward of 4096 columns reached 31 % of the memory
-// rate).  The arithmetic is on pairs.  Both directions are bound by memory: measured
-// (bf16) 131072 rows of 128, root mean square and gate, forward 20.8 us (4.8 TB/s),
-// backward 34 us (4.9); 16383 rows of 4096, backward 95 us (4.2 TB/s).
+// rate).  The arithmetic is on pairs.  Short rows are bound by memory and issue, long ones
+// in the backward by three barriers a row against 2 blocks an SM: measured
+// (bf16) 131072 rows of 128, root mean square and gate, forward 20.6 us (4.9 TB/s),
+// backward 33 us (5.0); 16383 rows of 4096, backward 94 us (4.3 TB/s).
 //
 // Backward: the sums of dw and db of a thread's columns stay in registers over all
 // rows of its block; the threads that share a column are joined and the block writes

@@ -13,9 +13,10 @@
 // most of the time: 252 us at the shape below.)
 //
 // What bounds it: N exponentials (32 a cycle and SM) and 2 N paired fp32 instructions (64
-// pairs a cycle and SM) per channel and token, each 36 us of the shape below, against 6 to
-// 8 bytes (20 us).  Both pipes are half busy: 128 registers a thread leave 4 warps for
-// each scheduler, and more of them spill.
+// pairs a cycle and SM) per channel and token, each 55000 cycles of the shape below (27 us at
+// the 2.07 GHz it runs at), against 6 to 8 bytes (20 us).  A cut sequence pays the
+// exponentials twice.  The schedulers issue in 0.56 to 0.59 of the cycles: 128 registers a
+// thread leave 4 warps for each of them, and more warps spill.
 //
 // Few channels leave most SMs idle, so sequences are then cut into chunks: one
 // launch computes each chunk's state from zero and its sum of delta, a second
@@ -24,8 +25,8 @@
 // scan itself starts every chunk from its state.  A single token has a kernel of its
 // own, one thread per 4 states, so that the states are read and written in whole lines.
 //
-// Measured (bf16, N = 16, gate): 4 x 2048 tokens of 2048 channels 156 us (states 64,
-// their steps 8, scan 84); 64 x 256 tokens of 4096 channels, uncut, 341 us; one token of
+// Measured (bf16, N = 16, gate): 4 x 2048 tokens of 2048 channels 157 us (states 64,
+// their steps 8, scan 85); 64 x 256 tokens of 4096 channels, uncut, 341 us; one token of
 // 64 sequences, 2048 channels, 7 us.
 #include "dn_scan.cuh"
 

@@ -28,14 +28,17 @@
 // block, which takes one chunk and a part of a group's channels and writes one row of 2 N
 // sums per token.  (With one channel per thread the shared-memory pipe bounds it.)
 //
-// What bounds it: about 30 paired fp32 instructions for every 4 states of a channel and
-// token, 150 us of the shape below; shuffles, shared memory and staging are as many
-// instructions again, and 12 warps an SM (168 registers a thread) issue in about half of
-// the cycles.  With the states of 8 tokens in registers, 253 a thread and 8 warps, the
-// reverse walk took 443 us.
+// What bounds it: every factor is computed 4.4 times (once in step 1, then 7/8, 1/2, 1 and
+// 1 times in step 3's walks), 1.2e9 exponentials of the shape below, 117 us of their pipe at
+// 2.07 GHz; beside them about 30 paired fp32 instructions for every 4 states of a channel
+// and token, 100 us of theirs; shuffles, shared memory and staging are as many instructions
+// again, and 12 warps an SM (168 registers a thread) issue in 0.60 of the cycles.  With the
+// states of 8 tokens in registers, 253 a thread and 8 warps, the reverse walk took 443 us.
+// For N = 64 and 128 a block's tile is 16 and 8 channels, and each tile adds its sums of dB
+// and dC to the block's row in global memory: no case of that width is timed.
 //
-// Measured (bf16, N = 16, gate, 4 x 2048 tokens of 2048 channels): 516 us (states 100,
-// their steps 14, reverse walk 388, sums 12).
+// Measured (bf16, N = 16, gate, 4 x 2048 tokens of 2048 channels): 518 us (states 102,
+// their steps 14, reverse walk 390, sums 12).
 #include "dn_scan.cuh"
 
 namespace dn {

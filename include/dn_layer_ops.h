@@ -31,7 +31,10 @@
  *
  * Every sum, state and statistic is held in fp32.  Outputs of type `dtype`
  * are rounded to it once (to nearest even).  Results do not depend on the
- * order in which blocks run: the same call gives the same bits.
+ * order in which blocks run: the same call gives the same bits.  Exponentials
+ * and quotients are the hardware's approximate ones, for fp32 tensors too:
+ * fp32 outputs are up to about 3 times as far from exact ones as those of the
+ * formulas evaluated with the standard fp32 functions.
  */
 #ifndef DN_LAYER_OPS_H
 #define DN_LAYER_OPS_H
@@ -159,6 +162,9 @@ size_t dn_selective_scan_bwd_workspace_bytes(int n_seqs, int B, int T, int D, in
  *   x, z, y  [rows, D]  dtype    z NULL: no factor silu(z).  y may be x or z.
  *   weight   [D]        float32  NULL: one
  *   bias     [D]        float32  NULL: zero
+ * The squares are taken in fp32: those of values beyond 1e19 overflow (y is 0),
+ * those of values below 1e-23 are 0 (with eps = 0 and no larger value in the
+ * row, y is not finite).
  * 1 <= D <= 16384 (larger: DN_ERR_UNSUPPORTED); rows >= 0; eps >= 0, finite.
  */
 dn_status dn_layer_norm_fwd(const void *x, const float *weight, const float *bias, const void *z,
