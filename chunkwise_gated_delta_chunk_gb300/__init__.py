@@ -17,7 +17,11 @@ backward.  :func:`chunk_fwd` is a convenience that allocates
 The operators around the recurrence (``include/dn_layer_ops.h``) are
 :func:`causal_conv_fwd` and :func:`causal_conv_bwd`, :func:`selective_scan_fwd`
 and :func:`selective_scan_bwd`, :func:`layer_norm_fwd` and
-:func:`layer_norm_bwd`; they check their tensors and allocate what is not given.
+:func:`layer_norm_bwd`, :func:`block_norm_fwd` and :func:`block_norm_bwd`; they check
+their tensors and allocate what is not given.  So do those of the attention over a sliding
+window that stands between such layers (``include/dn_window_ops.h``):
+:func:`window_attn_fwd`, :func:`window_attn_bwd`, :func:`window_cache_fill`,
+:func:`window_attn_step`.
 
 These and the conveniences above, given a ``stream``, work as under
 ``torch.cuda.stream(stream)``: what they allocate is that stream's memory, and what they
@@ -47,6 +51,7 @@ DN_QK_L2NORM = 1
 DN_CONV_SILU = 1
 DN_SCAN_SOFTPLUS = 1
 DN_NORM_RMS = 1
+DN_NORM_POST = 2
 
 # Every symbol the public headers declare.
 ABI_SYMBOLS = ("dn_chunk_fwd", "dn_chunk_fwd_workspace_bytes", "dn_chunk_fwd_noalloc",
@@ -55,7 +60,10 @@ ABI_SYMBOLS = ("dn_chunk_fwd", "dn_chunk_fwd_workspace_bytes", "dn_chunk_fwd_noa
                "dn_causal_conv_fwd", "dn_causal_conv_bwd", "dn_causal_conv_bwd_workspace_bytes",
                "dn_selective_scan_fwd", "dn_selective_scan_fwd_workspace_bytes",
                "dn_selective_scan_bwd", "dn_selective_scan_bwd_workspace_bytes",
-               "dn_layer_norm_fwd", "dn_layer_norm_bwd", "dn_layer_norm_bwd_workspace_bytes")
+               "dn_layer_norm_fwd", "dn_layer_norm_bwd", "dn_layer_norm_bwd_workspace_bytes",
+               "dn_block_norm_fwd", "dn_block_norm_bwd", "dn_block_norm_bwd_workspace_bytes",
+               "dn_window_attn_fwd", "dn_window_attn_bwd", "dn_window_attn_bwd_workspace_bytes",
+               "dn_window_cache_fill", "dn_window_attn_step")
 
 # Size of the library's fixed scratch array used by dn_chunk_fwd_noalloc.
 DN_NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
@@ -110,7 +118,17 @@ def load(path: str | None = None):
         lib.dn_layer_norm_fwd.argtypes = [P] * 4 + [L, I, I, F, U, P, P]
         lib.dn_layer_norm_bwd.argtypes = [P] * 4 + [L, I, I, F, U] + [P] * 6 + [Z, P]
         lib.dn_layer_norm_bwd_workspace_bytes.argtypes = [L, I, I]
-        for op in ("causal_conv", "selective_scan", "layer_norm"):
+        lib.dn_block_norm_fwd.argtypes = [P] * 8 + [L, I, I, I, F, U, P, P, P]
+        lib.dn_block_norm_bwd.argtypes = [P] * 8 + [L, I, I, I, F, U] + [P] * 11 + [Z, P]
+        lib.dn_block_norm_bwd_workspace_bytes.argtypes = [L, I, I, I]
+        lib.dn_window_attn_fwd.argtypes = [P] * 4 + [I] * 9 + [F, P, P, P]
+        lib.dn_window_attn_bwd.argtypes = [P] * 6 + [I] * 9 + [F] + [P] * 5 + [Z, P]
+        lib.dn_window_attn_bwd_workspace_bytes.argtypes = [I] * 10
+        lib.dn_window_cache_fill.argtypes = [P] * 3 + [I] * 8 + [P] * 4
+        lib.dn_window_cache_fill.restype = I
+        lib.dn_window_attn_step.argtypes = [P] * 3 + [I] * 8 + [F] + [P] * 5
+        lib.dn_window_attn_step.restype = I
+        for op in ("causal_conv", "selective_scan", "layer_norm", "block_norm", "window_attn"):
             getattr(lib, "dn_%s_fwd" % op).restype = I
             getattr(lib, "dn_%s_bwd" % op).restype = I
             getattr(lib, "dn_%s_bwd_workspace_bytes" % op).restype = Z
@@ -658,3 +676,253 @@ def layer_norm_bwd(x, weight=None, bias=None, z=None, eps=1e-5, rms=False, dy=No
     if st != DN_OK:
         raise DnError(st, "dn_layer_norm_bwd")
     return out
+
+
+def _block_inputs(what, x, residual, z, scale, post_weight, post_bias, weight, bias, eps, rms, post):
+    """Checked addresses and sizes of a block's norms, in the order of the C arguments."""
+    import torch
+    device = _device_of(x, torch)
+    D = x.shape[-1]
+    _fit(what, D)
+    f32, dt = torch.float32, x.dtype
+    code = dtype_code(dt)
+    if residual is None:
+        raise ValueError("residual is required")
+    rt = f32 if residual.dtype == f32 else dt
+    vectors = [_operand(name, t, (D,), f32, device) for name, t in
+               (("scale", scale), ("post_weight", post_weight), ("post_bias", post_bias),
+                ("weight", weight), ("bias", bias))]
+    ptrs = (_operand("x", x, x.shape, dt, device), _operand("residual", residual, x.shape, rt, device),
+            _operand("z", z, x.shape, dt, device), *vectors)
+    rows = x.numel() // D if D else 0
+    flags = (DN_NORM_RMS if rms else 0) | (DN_NORM_POST if post else 0)
+    return device, rt, ptrs, (rows, D, code, dtype_code(rt)), (eps, flags)
+
+
+def block_norm_fwd(x, residual, z=None, scale=None, post_weight=None, post_bias=None, weight=None,
+                   bias=None, eps=1e-5, rms=False, post=True, stream=None, y=None,
+                   residual_out=None):
+    """The norm after a block, its gate and residual scale, and the norm before the next block
+    (``dn_block_norm_fwd``)::
+
+        h = residual + scale sigmoid(z) (norm(x) post_weight + post_bias)
+        y = norm(h) weight + bias
+
+    x is the block's output, z (of x's shape and type) its gate; residual is of x's type or
+    fp32; the five vectors are fp32 ``[D]``.  ``post=False`` leaves the norm of x out, ``rms``
+    takes no mean in either norm.  ``y`` may be x or z, ``residual_out`` may be residual.
+    Returns ``(y, residual_out)``, the latter being h.
+    """
+    import torch
+    if stream is not None:
+        with _under(stream, _device_of(x, torch), torch):
+            return block_norm_fwd(x, residual, z, scale, post_weight, post_bias, weight, bias, eps,
+                                  rms, post, None, y, residual_out)
+    device, rt, ptrs, sizes, kind = _block_inputs("dn_block_norm_fwd", x, residual, z, scale, post_weight,
+                                                  post_bias, weight, bias, eps, rms, post)
+    if y is None:
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+    if residual_out is None:
+        residual_out = torch.empty_like(residual, memory_format=torch.contiguous_format)
+    st = load().dn_block_norm_fwd(*ptrs, *sizes, *kind, _operand("y", y, x.shape, x.dtype, device),
+                                  _operand("residual_out", residual_out, x.shape, rt, device),
+                                  torch._C._cuda_getCurrentRawStream(device.index))
+    if st != DN_OK:
+        raise DnError(st, "dn_block_norm_fwd")
+    return y, residual_out
+
+
+def block_norm_bwd(x, residual, z=None, scale=None, post_weight=None, post_bias=None, weight=None,
+                   bias=None, eps=1e-5, rms=False, post=True, dy=None, dresidual_out=None,
+                   stream=None, workspace=None):
+    """Gradients of :func:`block_norm_fwd`'s loss ``sum(dy * y) + sum(dresidual_out * residual_out)``.
+
+    ``dresidual_out`` has residual's type (None: zero).  Returns a dict with ``dx``, ``dz`` of x's
+    type, ``dresidual`` of residual's and ``dscale``, ``dpost_weight``, ``dpost_bias``, ``dweight``,
+    ``dbias`` in fp32; those of absent inputs are None.
+    """
+    import torch
+    if stream is not None:
+        with _under(stream, _device_of(x, torch), torch):
+            return block_norm_bwd(x, residual, z, scale, post_weight, post_bias, weight, bias, eps, rms,
+                                  post, dy, dresidual_out, None, workspace)
+    device, rt, ptrs, sizes, kind = _block_inputs("dn_block_norm_bwd", x, residual, z, scale, post_weight,
+                                                  post_bias, weight, bias, eps, rms, post)
+    lib = load()
+
+    def like(t):
+        return None if t is None else torch.empty_like(t, memory_format=torch.contiguous_format)
+
+    out = dict(dx=like(x), dresidual=like(residual), dz=like(z), dscale=like(scale),
+               dpost_weight=like(post_weight), dpost_bias=like(post_bias), dweight=like(weight),
+               dbias=like(bias))
+    need = 0
+    if any(out[k] is not None for k in ("dscale", "dpost_weight", "dpost_bias", "dweight", "dbias")):
+        need = _workspace_bytes("dn_block_norm_bwd_workspace_bytes", *sizes)
+    workspace, ws, wsb = _space(need, workspace, device)
+    st = lib.dn_block_norm_bwd(*ptrs, *sizes, *kind, _operand("dy", dy, x.shape, x.dtype, device, False),
+                               _operand("dresidual_out", dresidual_out, x.shape, rt, device),
+                               *(_ptr(t) for t in out.values()), ws, wsb,
+                               torch._C._cuda_getCurrentRawStream(device.index))
+    if st != DN_OK:
+        raise DnError(st, "dn_block_norm_bwd")
+    return out
+
+
+# ---- attention over a sliding window (include/dn_window_ops.h) ------------
+
+
+def _window_inputs(what, q, k, v, window, sinks, cu_seqlens, scale):
+    """Checked addresses and sizes of a windowed attention, in the order of the C arguments."""
+    import torch
+    device = _device_of(q, torch)
+    B, T, Nq, d = q.shape
+    Nk = k.shape[-2]
+    dt = q.dtype
+    code = dtype_code(dt)
+    N, cu = _sequences(B, cu_seqlens, device)
+    if window < 1 or sinks < 0:
+        raise ValueError("window must be 1 or more and sinks 0 or more, not %s and %s" % (window, sinks))
+    _fit(what, N | B | T | Nq | Nk | d | sinks)
+    kv = (B, T, Nk, d)
+    ptrs = (_operand("q", q, q.shape, dt, device), _operand("k", k, kv, dt, device, False),
+            _operand("v", v, kv, dt, device, False))
+    # a window beyond the sequence's length is that length: what an int holds is enough
+    sizes = (N, B, T, Nq, Nk, d, min(window, 2**31 - 1), sinks, code)
+    return device, dt, ptrs, cu, sizes, 0.0 if scale is None else scale
+
+
+def window_attn_fwd(q, k, v, window, sinks=0, cu_seqlens=None, scale=None, stream=None, o=None,
+                    lse=None):
+    """Causal attention over the last ``window`` tokens, the own one among them, and the first
+    ``sinks`` ones (``dn_window_attn_fwd``).
+
+    q ``[B, T, Nq, d]``; k, v ``[B, T, Nk, d]``, Nq a multiple of Nk; d = 64 or 128; bf16 or
+    fp32; sinks up to 128; cu_seqlens int64 ``[N+1]`` on the device; ``scale`` None: 1 / sqrt(d).
+    Returns ``(o, lse)``, the latter ``[B, T, Nq]`` fp32: the logarithms of the softmax's sums,
+    which :func:`window_attn_bwd` takes.
+    """
+    import torch
+    if stream is not None:
+        with _under(stream, _device_of(q, torch), torch):
+            return window_attn_fwd(q, k, v, window, sinks, cu_seqlens, scale, None, o, lse)
+    device, dt, ptrs, cu, sizes, scale = _window_inputs("dn_window_attn_fwd", q, k, v, window, sinks,
+                                                        cu_seqlens, scale)
+    if o is None:
+        o = torch.empty_like(q, memory_format=torch.contiguous_format)
+    if lse is None:
+        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=device)
+    st = load().dn_window_attn_fwd(*ptrs, cu, *sizes, scale, _operand("o", o, q.shape, dt, device),
+                                   _operand("lse", lse, q.shape[:3], torch.float32, device),
+                                   torch._C._cuda_getCurrentRawStream(device.index))
+    if st != DN_OK:
+        raise DnError(st, "dn_window_attn_fwd")
+    return o, lse
+
+
+def window_attn_bwd(q, k, v, o, lse, window, sinks=0, cu_seqlens=None, scale=None, do=None,
+                    stream=None, workspace=None):
+    """Gradients of :func:`window_attn_fwd`'s loss ``sum(do * o)``; o and lse are its results.
+
+    Returns a dict with ``dq``, ``dk`` and ``dv`` of q's type.
+    """
+    import torch
+    if stream is not None:
+        with _under(stream, _device_of(q, torch), torch):
+            return window_attn_bwd(q, k, v, o, lse, window, sinks, cu_seqlens, scale, do, None,
+                                   workspace)
+    device, dt, ptrs, cu, sizes, scale = _window_inputs("dn_window_attn_bwd", q, k, v, window, sinks,
+                                                        cu_seqlens, scale)
+    lib = load()
+    rest = (_operand("o", o, q.shape, dt, device, False),
+            _operand("lse", lse, q.shape[:3], torch.float32, device, False))
+    out = dict(dq=torch.empty_like(q, memory_format=torch.contiguous_format),
+               dk=torch.empty_like(k, memory_format=torch.contiguous_format),
+               dv=torch.empty_like(v, memory_format=torch.contiguous_format))
+    need = _workspace_bytes("dn_window_attn_bwd_workspace_bytes", 0 if cu is None else 1, *sizes)
+    workspace, ws, wsb = _space(need, workspace, device)
+    st = lib.dn_window_attn_bwd(*ptrs, *rest, cu, *sizes, scale, _operand("do", do, q.shape, dt, device, False),
+                                *(t.data_ptr() for t in out.values()), ws, wsb,
+                                torch._C._cuda_getCurrentRawStream(device.index))
+    if st != DN_OK:
+        raise DnError(st, "dn_window_attn_bwd")
+    return out
+
+
+def _cache(k_cache, v_cache, N, Nk, d, sinks, dt, device):
+    """Checked addresses of a ring cache, and its ring."""
+    slots = k_cache.shape[2] if k_cache.dim() == 4 else 0
+    shape = (N, Nk, slots, d)
+    if slots <= sinks:
+        raise ValueError("the cache must be [N, Nk, sinks + ring, d] with a ring of one slot at least")
+    return (_operand("k_cache", k_cache, shape, dt, device, False),
+            _operand("v_cache", v_cache, shape, dt, device, False)), slots - sinks
+
+
+def window_cache_fill(k, v, k_cache, v_cache, lengths=None, sinks=0, cu_seqlens=None, stream=None):
+    """Puts the tokens of k and v ``[B, T, Nk, d]`` into the ring caches
+    ``[N, Nk, sinks + ring, d]`` (``dn_window_cache_fill``).
+
+    The token at position p of its sequence goes to slot p (p < sinks), else to
+    ``sinks + (p - sinks) % ring``.  ``lengths`` int64 ``[N]`` on the device are the tokens that
+    each sequence had before these (None: none).  Returns ``(k_cache, v_cache)``.
+    """
+    import torch
+    device = _device_of(k, torch)
+    if stream is not None:
+        with _under(stream, device, torch):
+            return window_cache_fill(k, v, k_cache, v_cache, lengths, sinks, cu_seqlens)
+    B, T, Nk, d = k.shape
+    dt = k.dtype
+    code = dtype_code(dt)
+    N, cu = _sequences(B, cu_seqlens, device)
+    if sinks < 0:
+        raise ValueError("sinks must be 0 or more, not %s" % sinks)
+    _fit("dn_window_cache_fill", N | B | T | Nk | d | sinks)
+    caches, ring = _cache(k_cache, v_cache, N, Nk, d, sinks, dt, device)
+    _fit("dn_window_cache_fill", ring)
+    st = load().dn_window_cache_fill(
+        _operand("k", k, k.shape, dt, device), _operand("v", v, k.shape, dt, device, False), cu, N, B, T, Nk, d,
+        sinks, ring, code, _operand("lengths", lengths, (N,), torch.int64, device), *caches,
+        torch._C._cuda_getCurrentRawStream(device.index))
+    if st != DN_OK:
+        raise DnError(st, "dn_window_cache_fill")
+    return k_cache, v_cache
+
+
+def window_attn_step(q, k, v, k_cache, v_cache, lengths, window, sinks=0, scale=None, stream=None,
+                     o=None):
+    """One decoding step of :func:`window_attn_fwd` over the ring caches (``dn_window_attn_step``).
+
+    q ``[N, 1, Nq, d]``, k, v ``[N, 1, Nk, d]``: the new token of every sequence; its key and value
+    are put into the caches.  ``lengths`` int64 ``[N]`` on the device: the tokens that each
+    sequence had before (the caller adds one when all layers have run).  The ring has ``window``
+    slots at least.  Returns o.
+    """
+    import torch
+    device = _device_of(q, torch)
+    if stream is not None:
+        with _under(stream, device, torch):
+            return window_attn_step(q, k, v, k_cache, v_cache, lengths, window, sinks, scale, None, o)
+    N, T, Nq, d = q.shape
+    if T != 1:
+        raise ValueError("a step takes one token of every sequence, not %d" % T)
+    Nk = k.shape[-2]
+    dt = q.dtype
+    code = dtype_code(dt)
+    if window < 1 or sinks < 0:
+        raise ValueError("window must be 1 or more and sinks 0 or more, not %s and %s" % (window, sinks))
+    _fit("dn_window_attn_step", N | Nq | Nk | d | window | sinks)
+    caches, ring = _cache(k_cache, v_cache, N, Nk, d, sinks, dt, device)
+    _fit("dn_window_attn_step", ring)
+    if o is None:
+        o = torch.empty_like(q, memory_format=torch.contiguous_format)
+    kv = (N, 1, Nk, d)
+    st = load().dn_window_attn_step(
+        _operand("q", q, q.shape, dt, device), _operand("k", k, kv, dt, device, False),
+        _operand("v", v, kv, dt, device, False), N, Nq, Nk, d, window, sinks, ring, code,
+        0.0 if scale is None else scale, _operand("lengths", lengths, (N,), torch.int64, device, False),
+        *caches, _operand("o", o, q.shape, dt, device), torch._C._cuda_getCurrentRawStream(device.index))
+    if st != DN_OK:
+        raise DnError(st, "dn_window_attn_step")
+    return o

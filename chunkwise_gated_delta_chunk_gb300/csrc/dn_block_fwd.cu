@@ -1,0 +1,92 @@
+// Norms around a block, forward: y = norm(h) w2 + b2 with h = residual + scale sigmoid(z) p,
+// p = norm(x) w1 + b1 (or x w1 + b1), in one pass over x, z and the residual stream.
+//
+// A row is held in registers by R threads as in the layer norm; h stays there between the
+// two norms, so every tensor is read once and written once, and y is normed from the h that
+// is not yet rounded to the residual's type.  Bound by memory.
+#include "dn_block.cuh"
+
+namespace dn {
+namespace {
+
+extern __shared__ __align__(16) char s_ring[];
+
+template <typename T, typename TR, int V, int K, int R>
+__global__ void __launch_bounds__(Row<T, V, K, R>::kThreads) block_fwd(BlockParams p) {
+    using L = Row<T, V, K, R>;
+    using G = BlockRing<T, TR, V, K, R, 2, 1>;
+    constexpr int P = L::P, kBuf = 2 * (R / 32);
+    __shared__ __align__(16) float buf[2 * kBuf + 4];  // consecutive norms in turn
+    const float inv = 1.f / (float)p.D;
+    const Norm norm{p.D, p.eps, p.rms};
+    const long long step = (long long)gridDim.x * L::kRows;
+    long long row = (long long)blockIdx.x * L::kRows + threadIdx.x / R;
+    G ring;
+    ring.a[0] = static_cast<const T *>(p.x);
+    ring.a[1] = static_cast<const T *>(p.z);
+    ring.b[0] = static_cast<const TR *>(p.residual);
+#pragma unroll
+    for (int s = 0; s < G::S; ++s) ring.issue(s_ring, s, row + s * step, p.rows, p.D);
+    int stage = 0, turn = 0;
+    for (long long first = (long long)blockIdx.x * L::kRows; first < p.rows; first += step, row += step) {
+        typename L::Pairs h;
+        ring.wait();
+#pragma unroll
+        for (int k = 0; k < K; ++k) ring.get_a(h[k], s_ring, stage, 0, k, row, p.rows, p.D);
+        if (p.post) {
+            normalise<L, V, K, R>(h, norm, inv, buf + turn * kBuf);
+            turn ^= 1;
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            affine<L, V>(h[k], p.post_weight, p.post_bias, k, p.D);
+            if (p.z) {
+                f2 z[P];
+                ring.get_a(z, s_ring, stage, 1, k, row, p.rows, p.D);
+#pragma unroll
+                for (int i = 0; i < P; ++i) h[k][i] = mul2(h[k][i], sigmoid2(z[i]));
+            }
+            affine<L, V>(h[k], p.scale, nullptr, k, p.D);
+            f2 r[P];
+            ring.get_b(r, s_ring, stage, 0, k, row, p.rows, p.D);
+#pragma unroll
+            for (int i = 0; i < P; ++i) h[k][i] = add2(h[k][i], r[i]);
+        }
+        ring.issue(s_ring, stage, row + G::S * step, p.rows, p.D);
+        stage = stage + 1 == G::S ? 0 : stage + 1;
+        if (row < p.rows)
+#pragma unroll
+            for (int k = 0; k < K; ++k) store_row<L, V>(static_cast<TR *>(p.residual_out) + row * p.D, h[k], k, p.D);
+        normalise<L, V, K, R>(h, norm, inv, buf + turn * kBuf);
+        turn ^= 1;
+        if (row < p.rows)
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                affine<L, V>(h[k], p.weight, p.bias, k, p.D);
+                store_row<L, V>(static_cast<T *>(p.y) + row * p.D, h[k], k, p.D);
+            }
+    }
+}
+
+struct Launch {
+    const BlockParams &p;
+    cudaStream_t stream;
+    template <typename T, typename TR, int V, int K, int R>
+    cudaError_t operator()() const {
+        constexpr int kThreads = Row<T, V, K, R>::kThreads;
+        constexpr int bytes = BlockRing<T, TR, V, K, R, 2, 1>::kBytes;
+        const cudaError_t err = allow_smem<block_fwd<T, TR, V, K, R>>(bytes);
+        if (err != cudaSuccess) return err;
+        block_fwd<T, TR, V, K, R><<<norm_blocks(p.rows, kThreads, Row<T, V, K, R>::kRows, 64), kThreads, bytes, stream>>>(p);
+        return cudaGetLastError();
+    }
+};
+
+}  // namespace
+
+cudaError_t block_fwd_launch(const BlockParams &p, cudaStream_t stream, const char **name) {
+    *name = p.bf16 ? "block_fwd<bf16>" : "block_fwd<f32>";
+    return block_types(p, Launch{p, stream});
+}
+
+}  // namespace dn

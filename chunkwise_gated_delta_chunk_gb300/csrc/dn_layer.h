@@ -99,4 +99,24 @@ cudaError_t norm_fwd_launch(const NormParams &p, bool bf16, cudaStream_t stream,
 cudaError_t norm_bwd_launch(const NormParams &p, bool bf16, cudaStream_t stream, const char **name);
 size_t norm_bwd_workspace(long long rows, int D, bool bf16);
 
+// Norms around a block (dn_block_fwd.cu, dn_block_bwd.cu).
+struct BlockParams {
+    const void *x, *residual, *z;
+    const float *scale, *post_weight, *post_bias, *weight, *bias;
+    long long rows;
+    int D;
+    bool bf16, res_f32;  // types of x, z, y; of the residual stream
+    float eps;
+    bool rms, post;
+    void *y, *residual_out;
+    // backward
+    const void *dy, *dresidual_out;
+    void *dx, *dresidual, *dz;
+    float *dscale, *dpost_weight, *dpost_bias, *dweight, *dbias;
+    float *partial;  // [blocks][5][D]
+};
+cudaError_t block_fwd_launch(const BlockParams &p, cudaStream_t stream, const char **name);
+cudaError_t block_bwd_launch(const BlockParams &p, cudaStream_t stream, const char **name);
+size_t block_bwd_workspace(long long rows, int D, bool bf16, bool res_f32);
+
 }  // namespace dn

@@ -262,3 +262,78 @@ DN_EXPORT dn_status dn_layer_norm_bwd(const void *x, const float *weight, const 
     const char *name = "";
     return done(dn::norm_bwd_launch(p, dtype == DN_BF16, (cudaStream_t)stream, &name), name);
 }
+
+// ---- norms around a block --------------------------------------------------------
+
+namespace {
+
+dn_status block_check(dn::BlockParams &p, const void *x, const void *residual, const void *z, const float *scale,
+                      const float *post_weight, const float *post_bias, const float *weight, const float *bias,
+                      int64_t rows, int D, dn_dtype dtype, dn_dtype residual_dtype, float eps, unsigned flags) {
+    if (!dtype_ok(dtype) || rows < 0 || D <= 0) return DN_ERR_INVALID_ARG;
+    if (residual_dtype != dtype && residual_dtype != DN_F32) return DN_ERR_INVALID_ARG;
+    if (!(eps >= 0.f) || isinf(eps)) return DN_ERR_INVALID_ARG;
+    if (flags & ~(DN_NORM_RMS | DN_NORM_POST)) return DN_ERR_INVALID_ARG;
+    if (rows > 0 && (!x || !residual)) return DN_ERR_INVALID_ARG;
+    const void *ptrs[] = {x, residual, z, scale, post_weight, post_bias, weight, bias};
+    if (!all_aligned(ptrs)) return DN_ERR_INVALID_ARG;
+    p.x = x; p.residual = residual; p.z = z;
+    p.scale = scale; p.post_weight = post_weight; p.post_bias = post_bias; p.weight = weight; p.bias = bias;
+    p.rows = rows; p.D = D;
+    p.bf16 = dtype == DN_BF16; p.res_f32 = residual_dtype == DN_F32;
+    p.eps = eps; p.rms = flags & DN_NORM_RMS; p.post = flags & DN_NORM_POST;
+    return DN_OK;
+}
+
+}  // namespace
+
+DN_EXPORT dn_status dn_block_norm_fwd(const void *x, const void *residual, const void *z, const float *scale,
+                                      const float *post_weight, const float *post_bias, const float *weight,
+                                      const float *bias, int64_t rows, int D, dn_dtype dtype, dn_dtype residual_dtype,
+                                      float eps, unsigned flags, void *y, void *residual_out, dn_stream_t stream) {
+    dn::BlockParams p{};
+    const dn_status st = block_check(p, x, residual, z, scale, post_weight, post_bias, weight, bias, rows, D, dtype,
+                                     residual_dtype, eps, flags);
+    if (st != DN_OK) return st;
+    const void *ptrs[] = {y, residual_out};
+    if (!all_aligned(ptrs) || (rows > 0 && (!y || !residual_out))) return DN_ERR_INVALID_ARG;
+    if (D > kNormMaxD) return DN_ERR_UNSUPPORTED;
+    if (rows == 0) return DN_OK;
+    p.y = y; p.residual_out = residual_out;
+    const char *name = "";
+    return done(dn::block_fwd_launch(p, (cudaStream_t)stream, &name), name);
+}
+
+DN_EXPORT size_t dn_block_norm_bwd_workspace_bytes(int64_t rows, int D, dn_dtype dtype, dn_dtype residual_dtype) {
+    if (rows < 0 || D <= 0 || D > kNormMaxD || !dtype_ok(dtype)) return 0;
+    if (residual_dtype != dtype && residual_dtype != DN_F32) return 0;
+    return dn::block_bwd_workspace(rows, D, dtype == DN_BF16, residual_dtype == DN_F32);
+}
+
+DN_EXPORT dn_status dn_block_norm_bwd(const void *x, const void *residual, const void *z, const float *scale,
+                                      const float *post_weight, const float *post_bias, const float *weight,
+                                      const float *bias, int64_t rows, int D, dn_dtype dtype, dn_dtype residual_dtype,
+                                      float eps, unsigned flags, const void *d_y, const void *d_residual_out, void *d_x,
+                                      void *d_residual, void *d_z, float *d_scale, float *d_post_weight,
+                                      float *d_post_bias, float *d_weight, float *d_bias, void *workspace,
+                                      size_t workspace_bytes, dn_stream_t stream) {
+    dn::BlockParams p{};
+    const dn_status st = block_check(p, x, residual, z, scale, post_weight, post_bias, weight, bias, rows, D, dtype,
+                                     residual_dtype, eps, flags);
+    if (st != DN_OK) return st;
+    const void *ptrs[] = {d_y, d_residual_out, d_x, d_residual, d_z, d_scale, d_post_weight, d_post_bias, d_weight, d_bias};
+    if (!all_aligned(ptrs)) return DN_ERR_INVALID_ARG;
+    if (rows > 0 && (!d_y || !d_x || !d_residual || (z != nullptr) != (d_z != nullptr))) return DN_ERR_INVALID_ARG;
+    if (D > kNormMaxD) return DN_ERR_UNSUPPORTED;
+    const bool sums = d_scale || d_post_weight || d_post_bias || d_weight || d_bias;
+    if (sums && (!workspace || !aligned16(workspace) ||
+                 workspace_bytes < dn::block_bwd_workspace(rows, D, p.bf16, p.res_f32)))
+        return DN_ERR_INVALID_ARG;
+    if (rows == 0 && !sums) return DN_OK;
+    p.dy = d_y; p.dresidual_out = d_residual_out;
+    p.dx = d_x; p.dresidual = d_residual; p.dz = d_z;
+    p.dscale = d_scale; p.dpost_weight = d_post_weight; p.dpost_bias = d_post_bias; p.dweight = d_weight; p.dbias = d_bias;
+    p.partial = sums ? static_cast<float *>(workspace) : nullptr;
+    const char *name = "";
+    return done(dn::block_bwd_launch(p, (cudaStream_t)stream, &name), name);
+}

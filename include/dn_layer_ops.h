@@ -49,8 +49,10 @@ extern "C" {
 #define DN_CONV_SILU 1u
 /* Option bit of dn_selective_scan_*: delta = log(1 + e^(dt + dt_bias)). */
 #define DN_SCAN_SOFTPLUS 1u
-/* Option bit of dn_layer_norm_*: no mean is taken (root mean square norm). */
+/* Option bit of dn_layer_norm_* and dn_block_norm_*: no mean is taken (root mean square norm). */
 #define DN_NORM_RMS 1u
+/* Option bit of dn_block_norm_*: the block's output is normed before it is added. */
+#define DN_NORM_POST 2u
 
 /*
  * dn_causal_conv_fwd -- depthwise causal convolution over the last W tokens.
@@ -190,6 +192,51 @@ dn_status dn_layer_norm_bwd(const void *x, const float *weight, const float *bia
                             void *workspace, size_t workspace_bytes, dn_stream_t stream);
 
 size_t dn_layer_norm_bwd_workspace_bytes(int64_t rows, int D, dn_dtype dtype);
+
+/*
+ * dn_block_norm_fwd -- the norm after a block, its gate and residual scale, the
+ * residual sum and the norm before the next block, of every row of length D:
+ *
+ *     p = norm(x) post_weight + post_bias   (with DN_NORM_POST; else x post_weight + post_bias)
+ *     h = residual + scale sigmoid(z) p
+ *     y = norm(h) weight + bias
+ *
+ * with norm() as in dn_layer_norm_fwd (and what is said there of its squares), one
+ * eps and one form (DN_NORM_RMS) for both.  y comes from the fp32 h.
+ *   x, z, y                 [rows, D]  dtype  z NULL: no factor sigmoid(z)
+ *   residual, residual_out  [rows, D]  residual_dtype: dtype, or DN_F32.
+ *                                      residual_out is h.
+ *   scale, post_weight, weight [D]     float32  NULL: one
+ *   post_bias, bias         [D]        float32  NULL: zero
+ * y may be x or z; residual_out may be residual.
+ * 1 <= D <= 16384 (larger: DN_ERR_UNSUPPORTED); rows >= 0; eps >= 0, finite.
+ */
+dn_status dn_block_norm_fwd(const void *x, const void *residual, const void *z, const float *scale,
+                            const float *post_weight, const float *post_bias, const float *weight, const float *bias,
+                            int64_t rows, int D, dn_dtype dtype, dn_dtype residual_dtype, float eps, unsigned flags,
+                            void *y, void *residual_out, dn_stream_t stream);
+
+/*
+ * dn_block_norm_bwd -- gradients of dn_block_norm_fwd's inputs for the loss
+ * sum(d_y . y) + sum(d_residual_out . residual_out); h is computed again.
+ *   d_y, d_x, d_z               [rows, D]  dtype    d_z is required exactly when z is given
+ *   d_residual_out, d_residual  [rows, D]  residual_dtype; d_residual_out NULL: zero
+ *   d_scale, d_post_weight, d_post_bias, d_weight, d_bias
+ *                               [D]        float32  NULL: not computed; of an input that is
+ *                                                   NULL: the gradient at its default
+ * The last five are sums over all rows (zero for rows = 0).  d_x may be d_y or x, d_z may
+ * be z, d_residual may be d_residual_out or residual.
+ * workspace: dn_block_norm_bwd_workspace_bytes() bytes (for any of the five; else it may
+ * be NULL).
+ */
+dn_status dn_block_norm_bwd(const void *x, const void *residual, const void *z, const float *scale,
+                            const float *post_weight, const float *post_bias, const float *weight, const float *bias,
+                            int64_t rows, int D, dn_dtype dtype, dn_dtype residual_dtype, float eps, unsigned flags,
+                            const void *d_y, const void *d_residual_out, void *d_x, void *d_residual, void *d_z,
+                            float *d_scale, float *d_post_weight, float *d_post_bias, float *d_weight, float *d_bias,
+                            void *workspace, size_t workspace_bytes, dn_stream_t stream);
+
+size_t dn_block_norm_bwd_workspace_bytes(int64_t rows, int D, dn_dtype dtype, dn_dtype residual_dtype);
 
 #ifdef __cplusplus
 }
