@@ -5,7 +5,7 @@ namespace dn {
 
 cudaError_t window_fwd_launch(const WindowParams &p, bool bf16, cudaStream_t stream, const char **name) {
     *name = bf16 ? "window_fwd<bf16>" : "window_fwd<f32>";
-    const cudaError_t err = window_simt_fwd(p, bf16, false, stream);
+    const cudaError_t err = bf16 ? window_tc_fwd(p, stream) : window_simt_fwd(p, bf16, false, stream);
     if (err != cudaSuccess) return err;
     return window_simt_fwd(p, bf16, true, stream);
 }

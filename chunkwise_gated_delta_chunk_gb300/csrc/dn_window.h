@@ -41,6 +41,9 @@ size_t window_bwd_workspace(long long tokens, int n_seqs, bool packed, int T, in
                             bool bf16);
 void window_bwd_carve(WindowParams &p, void *workspace, bool bf16);
 
+// Tensor-core kernels: bf16 tensors.
+cudaError_t window_tc_fwd(const WindowParams &p, cudaStream_t stream);
+
 // CUDA-core kernels: fp32 tensors, and (redo) rows that the other kernels marked.
 cudaError_t window_simt_fwd(const WindowParams &p, bool bf16, bool redo, cudaStream_t stream);
 cudaError_t window_simt_bwd(const WindowParams &p, bool bf16, bool redo, cudaStream_t stream);

@@ -160,6 +160,20 @@ struct Half {
     }
 };
 
+// What a block of a grid does: item after item, or (REDO) a look at many marks at a time and only the
+// marked ones.  `marked(i)`: thread-wise, is group i of `group` items marked anywhere.
+template <bool REDO, typename Marked, typename Work>
+__device__ __forceinline__ void walk(long long items, int group, Marked marked, Work work) {
+    if constexpr (!REDO) {
+        for (long long item = blockIdx.x; item < items; item += gridDim.x) work(item);
+    } else {
+        for (long long g = blockIdx.x; g * group < items; g += gridDim.x) {
+            if (!__syncthreads_or(marked(g))) continue;
+            for (int i = 0; i < group && g * group + i < items; ++i) work(g * group + i);
+        }
+    }
+}
+
 template <typename T, int D, bool REDO>
 __global__ void __launch_bounds__(NT, 2) simt_fwd(WindowParams p, long long items) {
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
@@ -168,9 +182,18 @@ __global__ void __launch_bounds__(NT, 2) simt_fwd(WindowParams p, long long item
     float *Qs = s_win, *Ks = Qs + Smem<D>::kTile, *Ps = Ks + Smem<D>::kTile;
     wait_for_launches();
     if (!REDO && blockIdx.x == 0) check_offsets(p.seq, threadIdx.x, NT);
-    for (long long item = blockIdx.x; item < items; item += gridDim.x) {
+    // a group: the heads of half a slot
+    auto marked = [&](long long g) {
+        const Half it(p.seq, g * p.Nq, p.Nq);
+        bool any = false;
+        if (it.ok)
+            for (int i = threadIdx.x; i < (it.t1 - it.t0) * p.Nq; i += NT)
+                any |= is_redo(p.lse[(it.s.bos + it.t0) * p.Nq + i]);
+        return any;
+    };
+    walk<REDO>(items, p.Nq, marked, [&](long long item) {
         const Half it(p.seq, item, p.Nq);
-        if (!it.ok) continue;
+        if (!it.ok) return;
         const long long bos = it.s.bos;
         float *lse = p.lse + bos * p.Nq + it.head;
         bool write[4];
@@ -181,7 +204,7 @@ __global__ void __launch_bounds__(NT, 2) simt_fwd(WindowParams p, long long item
             write[i] = t < it.t1 && (!REDO || is_redo(lse[(long long)t * p.Nq]));
             any |= write[i];
         }
-        if (REDO && !__syncthreads_or(any)) continue;
+        if (REDO && !__syncthreads_or(any)) return;
         const int hk = it.head / (p.Nq / p.Nk);
         load_rows<T, D>(Qs, static_cast<const T *>(p.q), bos + it.t0, it.s.eos, p.Nq, it.head);
         f2 acc[4][D / 32];
@@ -242,7 +265,7 @@ __global__ void __launch_bounds__(NT, 2) simt_fwd(WindowParams p, long long item
                 lse[(long long)t * p.Nq] = !REDO && nan ? redo_mark() : (m[i] + log2f(sum)) * 0.6931471805599453f;
         }
         __syncthreads();
-    }
+    });
 }
 
 // Weights p and score gradients dS of a tile: s holds q . k, g holds dO . v; rows (i) and
@@ -262,14 +285,18 @@ __global__ void __launch_bounds__(NT) simt_dq(WindowParams p, long long items) {
     float *Qs = s_win, *Gs = Qs + kTile, *Ks = Gs + kTile, *Vs = Ks + kTile, *Ss = Vs + kTile;
     wait_for_launches();
     if (!REDO && blockIdx.x == 0) check_offsets(p.seq, threadIdx.x, NT);
-    for (long long item = blockIdx.x; item < items; item += gridDim.x) {
+    auto marked = [&](long long g) {
+        const long long i = g * NT + threadIdx.x;
+        return i < items && p.redo[i / p.Nq * (p.Nq + p.Nk) + i % p.Nq] != 0;
+    };
+    walk<REDO>(items, NT, marked, [&](long long item) {
         const Half it(p.seq, item, p.Nq);
         unsigned *flag = p.redo + it.flag * (p.Nq + p.Nk) + it.head;
         if (REDO) {
-            if (!it.ok || !*flag) continue;
+            if (!it.ok || !*flag) return;
         } else if (!it.ok) {
             if (threadIdx.x == 0) *flag = 0;
-            continue;
+            return;
         }
         const long long bos = it.s.bos;
         const int hk = it.head / (p.Nq / p.Nk);
@@ -325,7 +352,7 @@ __global__ void __launch_bounds__(NT) simt_dq(WindowParams p, long long items) {
         } else {
             __syncthreads();
         }
-    }
+    });
 }
 
 template <typename T, int D, bool REDO>
@@ -337,14 +364,18 @@ __global__ void __launch_bounds__(NT) simt_dkv(WindowParams p, long long items) 
     constexpr int kTile = Smem<D>::kTile;
     float *Ks = s_win, *Vs = Ks + kTile, *Qs = Vs + kTile, *Gs = Qs + kTile, *Ps = Gs + kTile, *Ss = Ps + BT * PS;
     wait_for_launches();
-    for (long long item = blockIdx.x; item < items; item += gridDim.x) {
+    auto marked = [&](long long g) {
+        const long long i = g * NT + threadIdx.x;
+        return i < items && p.redo[i / p.Nk * (p.Nq + p.Nk) + p.Nq + i % p.Nk] != 0;
+    };
+    walk<REDO>(items, NT, marked, [&](long long item) {
         const Half it(p.seq, item, p.Nk);
         unsigned *flag = p.redo + it.flag * (p.Nq + p.Nk) + p.Nq + it.head;
         if (REDO) {
-            if (!it.ok || !*flag) continue;
+            if (!it.ok || !*flag) return;
         } else if (!it.ok) {
             if (threadIdx.x == 0) *flag = 0;
-            continue;
+            return;
         }
         const long long bos = it.s.bos;
         const int L = (int)(it.s.eos - bos), k0 = it.t0;
@@ -401,32 +432,33 @@ __global__ void __launch_bounds__(NT) simt_dkv(WindowParams p, long long items) 
         } else {
             __syncthreads();
         }
-    }
+    });
 }
 
-template <auto kKernel>
-cudaError_t launch_items(int bytes, long long items, const WindowParams &p, cudaStream_t stream) {
+template <auto kKernel, bool REDO>
+cudaError_t launch_items(int bytes, long long items, int group, const WindowParams &p, cudaStream_t stream) {
     if (items <= 0) return cudaSuccess;
     const cudaError_t err = allow_smem<kKernel>(bytes);
     if (err != cudaSuccess) return err;
-    // more items than this walk on in the same blocks
-    const unsigned grid = (unsigned)(items < kSms * 64 ? items : kSms * 64);
+    // looks at marks: one block an SM; else one block an item, up to where blocks walk on
+    const long long most = REDO ? kSms : kSms * 64, want = REDO ? (items + group - 1) / group : items;
+    const unsigned grid = (unsigned)(want < most ? want : most);
     return launch_after(kKernel, dim3(grid), dim3(NT), bytes, stream, p, items);
 }
 
 template <typename T, int D, bool REDO>
 cudaError_t bwd(const WindowParams &p, cudaStream_t stream) {
     const long long halves = 2 * tile_slots(p.seq, kWinTile);
-    const cudaError_t err = launch_items<simt_dq<T, D, REDO>>(Smem<D>::kDq, halves * p.Nq, p, stream);
+    const cudaError_t err = launch_items<simt_dq<T, D, REDO>, REDO>(Smem<D>::kDq, halves * p.Nq, NT, p, stream);
     if (err != cudaSuccess) return err;
-    return launch_items<simt_dkv<T, D, REDO>>(Smem<D>::kDkv, halves * p.Nk, p, stream);
+    return launch_items<simt_dkv<T, D, REDO>, REDO>(Smem<D>::kDkv, halves * p.Nk, NT, p, stream);
 }
 
 template <typename T, int D>
 cudaError_t fwd(const WindowParams &p, bool redo, cudaStream_t stream) {
     const long long items = 2 * tile_slots(p.seq, kWinTile) * p.Nq;
-    return redo ? launch_items<simt_fwd<T, D, true>>(Smem<D>::kFwd, items, p, stream)
-                : launch_items<simt_fwd<T, D, false>>(Smem<D>::kFwd, items, p, stream);
+    return redo ? launch_items<simt_fwd<T, D, true>, true>(Smem<D>::kFwd, items, p.Nq, p, stream)
+                : launch_items<simt_fwd<T, D, false>, false>(Smem<D>::kFwd, items, p.Nq, p, stream);
 }
 
 }  // namespace
