@@ -19,6 +19,7 @@ struct Sight {
 // [0, sink_end) before them for the sinks alone.
 struct KeyTiles {
     int first, last, sink_end;
+    KeyTiles() = default;
     __device__ __forceinline__ KeyTiles(int t0, int t1, int len, const Sight &s) {
         const int lo = t0 - s.window + 1;  // window <= 2^30
         first = lo > 0 ? lo / len : 0;

@@ -24,10 +24,12 @@ struct WindowParams {
     const void *dout;  // [tokens, Nq, d]
     void *dq, *dk, *dv;
     float *dsum;      // [tokens, Nq] sum over d of dout o
-    unsigned *redo;   // [slots of kWinTile tokens][Nq + Nk]: tiles of dq and of dk, dv to take again
-    float *sink_part; // parts of the sinks' dk and dv (see window_bwd_carve)
-    int parts;        // of every (sequence, key head): parts of its sinks' sums
-    int part_tiles;   // query tiles that one part covers
+    unsigned *redo;   // [slots of kWinTile tokens][2 halves][Nq + Nk]: marks of dq, and of dk and dv
+    // tensor-core kernels: fp32 parts of the sinks' dv and dk, [slots of part_tiles tiles, then
+    // sequences][Nk][2][sinks][d], where some query sees the sinks by themselves (parts)
+    float *sink_part;
+    bool parts;
+    int part_tiles;
 };
 
 // A row of o that came out with a NaN may hold what a masked key's value did (0 times
@@ -43,6 +45,7 @@ void window_bwd_carve(WindowParams &p, void *workspace, bool bf16);
 
 // Tensor-core kernels: bf16 tensors.
 cudaError_t window_tc_fwd(const WindowParams &p, cudaStream_t stream);
+cudaError_t window_tc_bwd(const WindowParams &p, cudaStream_t stream);
 
 // CUDA-core kernels: fp32 tensors, and (redo) rows that the other kernels marked.
 cudaError_t window_simt_fwd(const WindowParams &p, bool bf16, bool redo, cudaStream_t stream);

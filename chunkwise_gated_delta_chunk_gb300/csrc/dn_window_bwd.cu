@@ -1,0 +1,755 @@
+// Attention over a sliding window with sinks, backward, bf16: tcgen05 / TMEM / TMA.
+//
+//     p = e^{scale q . k - lse},  dp = do . v,  ds = p (dp - D),  D = sum do o
+//     dq = scale ds k     (window_dq:  tiles of 128 queries, one head; keys stream by)
+//     dk = scale ds^T q,  dv = p^T do   (window_dkv: tiles of 128 keys, one key head; the
+//                                        group's heads' queries and do stream by)
+//
+// Two kernels, so that no sum is added by atomics: 7 products of 128 x 128 x d a tile
+// instead of 5, but every sum stays in tensor memory until it is done, in a fixed order.
+// window_dq computes D of its rows (from o and do) and leaves it for window_dkv.
+//
+// Warps 0-3 and 4-7: the first and the second 64 columns of every tile of scores, one row a
+// thread; warp 8: TMA loads; warp 9: issues the MMAs (one thread); warp 10 (window_dkv): the
+// columns' lse and D into shared memory.
+//
+// window_dq, tensor memory: S, dP (128 columns each), dQ (d), dS as bf16 (2 x 64).  As soon as
+// S and dP of a tile are in registers the tensor cores go on with those of the next one.
+// window_dkv: S^T and dP^T (overwritten by P^T and dS^T as bf16), dV and dK.  The products
+// alternate with the threads' work on the other matrix:
+//     threads   P(n)        dS(n)          P(n+1)
+//     MMAs      ...         dV(n) S(n+1)   dK(n) dP(n+1)
+//
+// All queries see the sinks.  Query tiles behind the window of the first key tile are taken
+// in parts (a run of part_tiles tiles each) by items of their own, which leave fp32 sums of
+// the sinks' rows; window_sink_sums adds them up in order.
+#include "dn_window_tc.cuh"
+
+namespace dn {
+namespace {
+
+using namespace ptx;
+using namespace tcs;
+
+constexpr int kThreads = 352;
+constexpr uint32_t kPanel = 128 * 128;  // 128 rows of 64 columns of bf16
+
+// Shared memory of both kernels: two tiles that stay, and two stages of two that stream by.
+template <int D>
+struct Lay {
+    static constexpr uint32_t kTile = (D / 64) * kPanel;
+    static constexpr int NS = D == 64 ? 4 : 2;
+    static constexpr uint32_t kA = 0, kB = kTile, kX = 2 * kTile, kY = kX + NS * kTile, kCols = kY + NS * kTile;
+    static constexpr uint32_t kBar = kCols + NS * 1024;  // lse and D of the stage's queries before it
+    static constexpr int bHold = 0, bHoldEmpty = 1, bFull = 2, bEmpty = bFull + NS, bCol = bEmpty + NS, bS = bCol + NS, bDP = bS + 1,
+                         bP = bDP + 1, bDS = bP + 1, bOut = bDS + 1, bOutEmpty = bOut + 1, bDrain = bOutEmpty + 1, kBars = bDrain + 1;
+    static constexpr uint32_t kMisc = kBar + 8 * kBars, kAlloc = kMisc + 16 + 1024;
+    static_assert(kAlloc <= 232448, "exceeds the 227 KB of shared memory per CTA");
+};
+
+template <int D>
+struct Base {
+    using Y = Lay<D>;
+    Ctx x;
+    const WindowParams &p;
+    uint32_t tm;
+    __device__ __forceinline__ uint32_t bar(int i) const { return x.base + Y::kBar + 8u * i; }
+
+    // rows of 128 x D by panels
+    __device__ __forceinline__ void tma_tile(uint32_t at, const CUtensorMap *m, uint32_t b, int head, int row) const {
+        for (int c = 0; c < D / 64; ++c) tma_load_3d(x.base + at + c * kPanel, m, b, 64 * c, head, row);
+    }
+    // C[128 x n] = A[128 x D] B[n x D]^T, both rows in shared memory
+    __device__ __forceinline__ void mma_rows(uint32_t c, uint32_t a, uint32_t b, uint32_t id) const {
+#pragma unroll
+        for (int s = 0; s < D / 64; ++s)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+                mma_ss(tm + c, sdesc(x.base + a + s * kPanel + kk * 32, 16, 1024), sdesc(x.base + b + s * kPanel + kk * 32, 16, 1024), id,
+                       (s | kk) != 0);
+    }
+    // the warp's byte in the mark of its half of the rows (two warps of each column half)
+    __device__ __forceinline__ void mark(bool nan, long long flag) const {
+        const int warp = threadIdx.x >> 5;
+        nan = __any_sync(0xffffffffu, nan);
+        unsigned char *m = reinterpret_cast<unsigned char *>(p.redo + flag + (warp >> 1 & 1) * (p.Nq + p.Nk));
+        if ((threadIdx.x & 31) == 0) m[2 * (warp >> 2) + (warp & 1)] = nan;
+    }
+    // 64 columns of a row of an accumulator times f, to bf16; true where a NaN is among them
+    __device__ __forceinline__ bool store64(uint32_t from, __nv_bfloat16 *to, float f, bool write) const {
+        uint32_t o[2][32];
+        tmem_ld32(from, o[0]);
+        tmem_ld32(from + 32, o[1]);
+        tmem_wait_ld();
+        tmem_ld_dep(o[0]);
+        tmem_ld_dep(o[1]);
+        bool nan = false;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            uint32_t w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float a = __uint_as_float(o[h / 2][(h & 1) * 16 + 2 * e]) * f;
+                const float b = __uint_as_float(o[h / 2][(h & 1) * 16 + 2 * e + 1]) * f;
+                nan |= isnan(a) | isnan(b);
+                w[e] = pack_bf16(a, b);
+            }
+            if (write) store32(to + 16 * h, w);
+        }
+        return nan && write;
+    }
+};
+
+// ---- dq -------------------------------------------------------------------------
+
+template <int D>
+struct Dq : Base<D> {
+    using Y = Lay<D>;
+    using B = Base<D>;
+    using B::bar;
+    using B::p;
+    using B::tm;
+    using B::x;
+    unsigned items;
+    long long slots;
+    static constexpr uint32_t tS = 0, tDP = 128, tDQ = 256, tDS = 384;
+
+    struct Plan {
+        long long bos, flag;
+        int L, h, hk, t0;
+        KeyTiles kt;
+        bool narrow;
+        __device__ __forceinline__ bool small(int i) const { return narrow && i == 0; }
+    };
+    // late tiles first: under a causal mask these are the long ones
+    __device__ __forceinline__ bool plan(Plan &u, unsigned item) const {
+        u.h = item % p.Nq;
+        const unsigned slot = (unsigned)(slots - 1 - item / p.Nq);
+        u.flag = (long long)slot * 2 * (p.Nq + p.Nk) + u.h;
+        const SeqTile s = seq_tile(p.seq, slot, 128);
+        if (!s.ok || s.t0 >= s.t1) return false;
+        u.bos = s.bos;
+        u.L = (int)(s.eos - s.bos);
+        u.hk = u.h / (p.Nq / p.Nk);
+        u.t0 = (int)(s.t0 - s.bos);
+        u.kt = KeyTiles(u.t0, (int)(s.t1 - s.bos), 128, Sight{p.window, p.sinks});
+        u.narrow = u.kt.sink_end > 0 && p.sinks <= kSinkCols;
+        return true;
+    }
+
+    __device__ void load(const CUtensorMap *mq, const CUtensorMap *mg, const CUtensorMap *mk, const CUtensorMap *mv,
+                         const CUtensorMap *mks, const CUtensorMap *mvs) {
+        unsigned kv = 0, qn = 0;
+        bool fine = true;
+        for (unsigned item = blockIdx.x; fine && item < items; item += gridDim.x) {
+            Plan u;
+            if (!plan(u, item)) continue;
+            if (!wait(x, bar(Y::bHoldEmpty), (qn & 1) ^ 1)) break;
+            mbar_arrive_expect_tx(bar(Y::bHold), 2 * Y::kTile);
+            B::tma_tile(Y::kA, mq, bar(Y::bHold), u.h, (int)(u.bos + u.t0));
+            B::tma_tile(Y::kB, mg, bar(Y::bHold), u.h, (int)(u.bos + u.t0));
+            ++qn;
+            for (int i = 0; i < u.kt.count(); ++i, ++kv) {
+                const int s = kv % Y::NS;
+                if (!(fine = wait(x, bar(Y::bEmpty + s), ((kv / Y::NS) & 1) ^ 1))) break;
+                const int row = (int)(u.bos + (long long)u.kt.tile(i) * 128);
+                mbar_arrive_expect_tx(bar(Y::bFull + s), u.small(i) ? 2 * kSinkCols * D * 2 : 2 * Y::kTile);
+                B::tma_tile(Y::kX + s * Y::kTile, u.small(i) ? mks : mk, bar(Y::bFull + s), u.hk, row);
+                B::tma_tile(Y::kY + s * Y::kTile, u.small(i) ? mvs : mv, bar(Y::bFull + s), u.hk, row);
+            }
+        }
+        if (qn) wait_drain(bar(Y::bHold), (qn - 1) & 1);
+        for (unsigned i = kv > Y::NS ? kv - Y::NS : 0; i < kv; ++i) wait_drain(bar(Y::bFull + i % Y::NS), (i / Y::NS) & 1);
+    }
+
+    __device__ __forceinline__ bool issue_s(bool small, unsigned k) const {
+        const int s = k % Y::NS;
+        if (!wait(x, bar(Y::bFull + s), (k / Y::NS) & 1)) return false;
+        tc_fence_after();
+        const uint32_t id = small ? idesc_bf16(128, kSinkCols, 0, 0) : idesc_bf16(128, 128, 0, 0);
+        B::mma_rows(tS, Y::kA, Y::kX + s * Y::kTile, id);
+        B::mma_rows(tDP, Y::kB, Y::kY + s * Y::kTile, id);
+        mma_commit(bar(Y::bS));
+        return true;
+    }
+
+    __device__ void mma() {
+        unsigned kv = 0, qn = 0;
+        bool fine = true;
+        for (unsigned item = blockIdx.x; fine && item < items; item += gridDim.x) {
+            Plan u;
+            if (!plan(u, item)) continue;
+            const int n = u.kt.count();
+            fine = wait(x, bar(Y::bHold), qn & 1) && issue_s(u.small(0), kv);
+            for (int i = 0; fine && i < n; ++i) {
+                const unsigned k = kv + i;
+                // both in registers: the next tile's may come
+                if (!(fine = wait(x, bar(Y::bP), k & 1))) break;
+                if (i + 1 < n) {
+                    if (!(fine = issue_s(u.small(i + 1), k + 1))) break;
+                } else {
+                    mma_commit(bar(Y::bHoldEmpty));
+                }
+                if (i == 0 && !(fine = wait(x, bar(Y::bOutEmpty), (qn & 1) ^ 1))) break;
+                if (!(fine = wait(x, bar(Y::bDS), k & 1))) break;
+                tc_fence_after();
+                const uint32_t b = x.base + Y::kX + (k % Y::NS) * Y::kTile;
+                const int steps = u.small(i) ? kSinkCols / 16 : 8;
+                for (int kk = 0; kk < steps; ++kk)
+                    mma_ts(tm + tDQ, tm + tDS + 64 * (k & 1) + 8 * kk, sdesc(b + kk * 2048, kPanel, 1024), idesc_bf16(128, D, 0, 1),
+                           (i | kk) != 0);
+                mma_commit(bar(Y::bEmpty + k % Y::NS));
+                if (i + 1 == n) mma_commit(bar(Y::bOut));
+            }
+            kv += n;
+            ++qn;
+        }
+        mma_commit(bar(Y::bDrain));
+        wait_drain(bar(Y::bDrain), 0);
+    }
+
+    __device__ void threads() {
+        const int warp = threadIdx.x >> 5, row = threadIdx.x & 127, w = warp >> 2;
+        const uint32_t lane = lane_base(tm, warp);
+        const float c = p.scale * kLog2e;
+        const Sight sight{p.window, p.sinks};
+        unsigned k = 0, qn = 0;
+        for (unsigned item = blockIdx.x; item < items; item += gridDim.x) {
+            Plan u;
+            if (!plan(u, item)) {
+                if (threadIdx.x < 2) p.redo[u.flag + threadIdx.x * (p.Nq + p.Nk)] = 0;
+                continue;
+            }
+            const int t = u.t0 + row;
+            const bool live = t < u.L;
+            const long long at = (u.bos + t) * p.Nq + u.h;
+            // D of the row, by each of its two threads
+            float dsum = 0.f;
+            if (live) {
+                const __nv_bfloat16 *o = static_cast<const __nv_bfloat16 *>(p.o) + at * D;
+                const __nv_bfloat16 *g = static_cast<const __nv_bfloat16 *>(p.dout) + at * D;
+#pragma unroll 4
+                for (int i = 0; i < D; i += 8) {
+                    Vec<__nv_bfloat16, 8> a, b;
+                    a.load(o + i);
+                    b.load(g + i);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) dsum = fmaf(a.v[e], b.v[e], dsum);
+                }
+            }
+            if (w == 0 && live) p.dsum[at] = dsum;
+            const float lse2 = live ? p.lse[at] * kLog2e : 0.f;
+            const f2 cc = both(c), ll = both(-lse2), dd = both(-dsum);
+            for (int i = 0; i < u.kt.count(); ++i, ++k) {
+                const int k0 = u.kt.tile(i) * 128;
+                if (!wwait(x, bar(Y::bS), k & 1)) return;
+                tc_fence_after();
+                const int cols = u.small(i) ? (w == 0 ? 1 : 0) : 2;  // groups of 32 columns
+                uint32_t s[2][32], g[2][32];
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    if (q < cols) {
+                        tmem_ld32(lane + tS + 64 * w + 32 * q, s[q]);
+                        tmem_ld32(lane + tDP + 64 * w + 32 * q, g[q]);
+                    }
+                tmem_wait_ld();
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    tmem_ld_dep(s[q]);
+                    tmem_ld_dep(g[q]);
+                }
+                tc_fence_before();
+                warp_arrive(bar(Y::bP));
+                const bool edge = k0 + 127 > u.t0 || u.t0 + 127 - k0 >= p.window;
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    if (q < cols) {
+                        const uint32_t mask = edge ? seen32(t, k0 + 64 * w + 32 * q, sight) : 0xffffffffu;
+                        uint32_t ds[16];
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            float a, b;
+                            split(fma2(pair(__uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1])), cc, ll), a, b);
+                            split(mul2(pair(ex2(a), ex2(b)), add2(pair(__uint_as_float(g[q][e]), __uint_as_float(g[q][e + 1])), dd)), a, b);
+                            if (edge) {
+                                a = mask >> e & 1 ? a : 0.f;
+                                b = mask >> (e + 1) & 1 ? b : 0.f;
+                            }
+                            ds[e / 2] = pack_bf16(a, b);
+                        }
+                        tmem_st16(lane + tDS + 64 * (k & 1) + 32 * w + 16 * q, ds);
+                    }
+                tmem_wait_st();
+                tc_fence_before();
+                warp_arrive(bar(Y::bDS));
+            }
+            if (!wwait(x, bar(Y::bOut), qn & 1)) return;
+            ++qn;
+            tc_fence_after();
+            bool nan = false;
+            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.dq) + at * D;
+            if (D == 128 || w == 0) nan = B::store64(lane + tDQ + 64 * w, out + 64 * w, p.scale, live);
+            tc_fence_before();
+            warp_arrive(bar(Y::bOutEmpty));
+            B::mark(nan, u.flag);
+        }
+    }
+};
+
+// ---- dk and dv ------------------------------------------------------------------
+
+// Items: a key tile of 128 tokens and a key head; then (parts) a run of query tiles that see the
+// sinks of a sequence alone.
+struct KeyPlan {
+    long long bos, flag;
+    int n, L, hk, k0, first, tiles;  // sequence; query tiles [first, first + tiles) of each of the group's heads
+    bool part, split;  // split: the sinks' rows are summed over parts
+    long long place;   // of the sinks' rows of this item among the parts
+};
+
+struct Parts {  // how the query tiles behind the window are cut
+    long long slots;  // of part_tiles x 128 tokens
+    int tiles;
+};
+
+__device__ __forceinline__ bool key_plan(KeyPlan &u, const WindowParams &p, long long slots, const Parts &parts, unsigned item) {
+    const Sight sight{p.window, p.sinks};
+    const long long main_items = slots * p.Nk;
+    u.hk = item % p.Nk;
+    u.part = item >= main_items;
+    const unsigned slot = (unsigned)((u.part ? item - main_items : item) / p.Nk);
+    u.flag = (long long)slot * 2 * (p.Nq + p.Nk) + p.Nq + u.hk;
+    const SeqTile s = seq_tile(p.seq, slot, u.part ? parts.tiles * 128 : 128);
+    if (!s.ok || s.t0 >= s.t1) return false;
+    u.n = s.n;
+    u.bos = s.bos;
+    u.L = (int)(s.eos - s.bos);
+    u.k0 = u.part ? 0 : (int)(s.t0 - s.bos);
+    const QueryTiles qt(u.k0, u.k0 + 128 < u.L ? u.k0 + 128 : u.L, u.L, 128, sight);
+    u.split = u.k0 < p.sinks && qt.end > qt.last;
+    if (u.part) {
+        const int from = s.c * parts.tiles, to = (int)(s.t1 - s.bos - 1) / 128;
+        u.first = from > qt.last + 1 ? from : qt.last + 1;
+        u.tiles = to - u.first + 1;
+        u.place = slot;
+        return u.split && u.tiles > 0;
+    }
+    u.first = qt.first;
+    u.tiles = qt.last - qt.first + 1;
+    u.place = parts.slots + s.n;
+    return true;
+}
+
+template <int D>
+struct Dkv : Base<D> {
+    using Y = Lay<D>;
+    using B = Base<D>;
+    using B::bar;
+    using B::p;
+    using B::tm;
+    using B::x;
+    unsigned items;
+    long long slots;
+    Parts parts;
+    static constexpr uint32_t tS = 0, tDP = 128, tDV = 256, tDK = 384;
+
+    __device__ __forceinline__ bool plan(KeyPlan &u, unsigned item) const { return key_plan(u, p, slots, parts, item); }
+    __device__ __forceinline__ int rounds(const KeyPlan &u) const { return u.tiles * (p.Nq / p.Nk); }
+    __device__ __forceinline__ void round(const KeyPlan &u, int i, int &h, int &q0) const {
+        h = u.hk * (p.Nq / p.Nk) + i / u.tiles;
+        q0 = (u.first + i % u.tiles) * 128;
+    }
+
+    __device__ void load(const CUtensorMap *mq, const CUtensorMap *mg, const CUtensorMap *mk, const CUtensorMap *mv) {
+        unsigned qs = 0, kn = 0;
+        bool fine = true;
+        for (unsigned item = blockIdx.x; fine && item < items; item += gridDim.x) {
+            KeyPlan u;
+            if (!plan(u, item)) continue;
+            if (!wait(x, bar(Y::bHoldEmpty), (kn & 1) ^ 1)) break;
+            mbar_arrive_expect_tx(bar(Y::bHold), 2 * Y::kTile);
+            B::tma_tile(Y::kA, mk, bar(Y::bHold), u.hk, (int)(u.bos + u.k0));
+            B::tma_tile(Y::kB, mv, bar(Y::bHold), u.hk, (int)(u.bos + u.k0));
+            ++kn;
+            const int n = rounds(u);
+            for (int i = 0; i < n; ++i, ++qs) {
+                const int s = qs % Y::NS;
+                if (!(fine = wait(x, bar(Y::bEmpty + s), ((qs / Y::NS) & 1) ^ 1))) break;
+                int h, q0;
+                round(u, i, h, q0);
+                mbar_arrive_expect_tx(bar(Y::bFull + s), 2 * Y::kTile);
+                B::tma_tile(Y::kX + s * Y::kTile, mq, bar(Y::bFull + s), h, (int)(u.bos + q0));
+                B::tma_tile(Y::kY + s * Y::kTile, mg, bar(Y::bFull + s), h, (int)(u.bos + q0));
+            }
+        }
+        if (kn) wait_drain(bar(Y::bHold), (kn - 1) & 1);
+        for (unsigned i = qs > Y::NS ? qs - Y::NS : 0; i < qs; ++i) wait_drain(bar(Y::bFull + i % Y::NS), (i / Y::NS) & 1);
+    }
+
+    // lse (times log2 e) and D of the streamed queries, a stage ahead like their tiles
+    __device__ void columns() {
+        const int lane = threadIdx.x & 31;
+        unsigned qs = 0;
+        for (unsigned item = blockIdx.x; item < items; item += gridDim.x) {
+            KeyPlan u;
+            if (!plan(u, item)) continue;
+            const int n = rounds(u);
+            for (int i = 0; i < n; ++i, ++qs) {
+                const int s = qs % Y::NS;
+                int h, q0;
+                round(u, i, h, q0);
+                float a[4], b[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int t = q0 + lane + 32 * e;
+                    const long long at = (u.bos + t) * p.Nq + h;
+                    a[e] = t < u.L ? -p.lse[at] * kLog2e : 0.f;
+                    b[e] = t < u.L ? -p.dsum[at] : 0.f;
+                }
+                if (!wwait(x, bar(Y::bEmpty + s), ((qs / Y::NS) & 1) ^ 1)) return;
+                float *to = reinterpret_cast<float *>(x.gbase + Y::kCols + s * 1024);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    to[lane + 32 * e] = a[e];
+                    to[128 + lane + 32 * e] = b[e];
+                }
+                warp_arrive(bar(Y::bCol + s));
+            }
+        }
+    }
+
+    __device__ __forceinline__ void mma_acc(uint32_t acc, uint32_t a, uint32_t b, bool more) const {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)  // the two halves of the queries lie 64 columns apart
+            mma_ts(tm + acc, tm + a + 64 * (kk >> 2) + 8 * (kk & 3), sdesc(x.base + b + kk * 2048, kPanel, 1024), idesc_bf16(128, D, 0, 1),
+                   more || kk != 0);
+    }
+
+    __device__ void mma() {
+        constexpr uint32_t id = idesc_bf16(128, 128, 0, 0);
+        unsigned qs = 0, kn = 0;
+        bool fine = true;
+        for (unsigned item = blockIdx.x; fine && item < items; item += gridDim.x) {
+            KeyPlan u;
+            if (!plan(u, item)) continue;
+            const int n = rounds(u);
+            auto full = [&](unsigned k) { return wait(x, bar(Y::bFull + k % Y::NS), (k / Y::NS) & 1); };
+            if (!(fine = wait(x, bar(Y::bHold), kn & 1) && full(qs))) break;
+            tc_fence_after();
+            B::mma_rows(tS, Y::kA, Y::kX + (qs % Y::NS) * Y::kTile, id);
+            mma_commit(bar(Y::bS));
+            B::mma_rows(tDP, Y::kB, Y::kY + (qs % Y::NS) * Y::kTile, id);
+            mma_commit(bar(Y::bDP));
+            if (!(fine = wait(x, bar(Y::bOutEmpty), (kn & 1) ^ 1))) break;
+            for (int i = 0; i < n; ++i) {
+                const unsigned k = qs + i;
+                const uint32_t here = (k % Y::NS) * Y::kTile, next = ((k + 1) % Y::NS) * Y::kTile;
+                if (!(fine = wait(x, bar(Y::bP), k & 1))) break;
+                tc_fence_after();
+                mma_acc(tDV, tS, Y::kY + here, i > 0);
+                if (i + 1 < n) {
+                    if (!(fine = full(k + 1))) break;
+                    B::mma_rows(tS, Y::kA, Y::kX + next, id);
+                    mma_commit(bar(Y::bS));
+                }
+                if (!(fine = wait(x, bar(Y::bDS), k & 1))) break;
+                tc_fence_after();
+                mma_acc(tDK, tDP, Y::kX + here, i > 0);
+                mma_commit(bar(Y::bEmpty + k % Y::NS));
+                if (i + 1 < n) {
+                    B::mma_rows(tDP, Y::kB, Y::kY + next, id);
+                    mma_commit(bar(Y::bDP));
+                } else {
+                    mma_commit(bar(Y::bHoldEmpty));
+                    mma_commit(bar(Y::bOut));
+                }
+            }
+            qs += n;
+            ++kn;
+        }
+        mma_commit(bar(Y::bDrain));
+        wait_drain(bar(Y::bDrain), 0);
+    }
+
+    __device__ void threads() {
+        const int warp = threadIdx.x >> 5, row = threadIdx.x & 127, w = warp >> 2;
+        const uint32_t lane = lane_base(tm, warp);
+        const float c = p.scale * kLog2e;
+        const f2 cc = both(c);
+        unsigned k = 0, kn = 0;
+        for (unsigned item = blockIdx.x; item < items; item += gridDim.x) {
+            KeyPlan u;
+            if (!plan(u, item)) {
+                if (!u.part && threadIdx.x < 2) p.redo[u.flag + threadIdx.x * (p.Nq + p.Nk)] = 0;
+                continue;
+            }
+            const int j = u.k0 + row;  // the thread's key
+            const int n = rounds(u);
+            for (int i = 0; i < n; ++i, ++k) {
+                int h, q0;
+                round(u, i, h, q0);
+                const float *cols = reinterpret_cast<const float *>(x.gbase + Y::kCols + (k % Y::NS) * 1024) + 64 * w;
+                // queries of the tile that see the key: [j, j + window - 1], or all behind j for a sink
+                const long long far = j < p.sinks ? (long long)u.L - 1 : (long long)j + p.window - 1;
+                const int lo = j - q0, hi = (int)((far < u.L - 1 ? far : u.L - 1) - q0);
+                const bool edge = q0 < u.k0 + 127 || q0 + 127 >= u.L || (long long)q0 + 127 - u.k0 >= p.window;
+                if (!wwait(x, bar(Y::bCol + k % Y::NS), (k / Y::NS) & 1)) return;
+                if (!wwait(x, bar(Y::bS), k & 1)) return;
+                tc_fence_after();
+                uint32_t s[2][32];
+                tmem_ld32(lane + tS + 64 * w, s[0]);
+                tmem_ld32(lane + tS + 64 * w + 32, s[1]);
+                tmem_wait_ld();
+                tmem_ld_dep(s[0]);
+                tmem_ld_dep(s[1]);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const uint32_t mask = edge ? bit_range(lo - 64 * w - 32 * q, hi - 64 * w - 32 * q) : 0xffffffffu;
+                    uint32_t v[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const ulonglong2 l = *reinterpret_cast<const ulonglong2 *>(cols + 32 * q + e);
+                        float a[4];
+                        split(fma2(pair(__uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1])), cc, l.x), a[0], a[1]);
+                        split(fma2(pair(__uint_as_float(s[q][e + 2]), __uint_as_float(s[q][e + 3])), cc, l.y), a[2], a[3]);
+#pragma unroll
+                        for (int f = 0; f < 4; ++f) {
+                            a[f] = ex2(a[f]);
+                            if (edge) a[f] = mask >> (e + f) & 1 ? a[f] : 0.f;
+                            s[q][e + f] = __float_as_uint(a[f]);
+                        }
+                        v[e / 2] = pack_bf16(a[0], a[1]);
+                        v[e / 2 + 1] = pack_bf16(a[2], a[3]);
+                    }
+                    tmem_st16(lane + tS + 64 * w + 16 * q, v);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                warp_arrive(bar(Y::bP));
+                if (!wwait(x, bar(Y::bDP), k & 1)) return;
+                tc_fence_after();
+                uint32_t g[2][32];
+                tmem_ld32(lane + tDP + 64 * w, g[0]);
+                tmem_ld32(lane + tDP + 64 * w + 32, g[1]);
+                tmem_wait_ld();
+                tmem_ld_dep(g[0]);
+                tmem_ld_dep(g[1]);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const uint32_t mask = edge ? bit_range(lo - 64 * w - 32 * q, hi - 64 * w - 32 * q) : 0xffffffffu;
+                    uint32_t v[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const ulonglong2 d = *reinterpret_cast<const ulonglong2 *>(cols + 128 + 32 * q + e);
+                        float a[4];
+                        split(mul2(pair(__uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1])),
+                                   add2(pair(__uint_as_float(g[q][e]), __uint_as_float(g[q][e + 1])), d.x)), a[0], a[1]);
+                        split(mul2(pair(__uint_as_float(s[q][e + 2]), __uint_as_float(s[q][e + 3])),
+                                   add2(pair(__uint_as_float(g[q][e + 2]), __uint_as_float(g[q][e + 3])), d.y)), a[2], a[3]);
+                        if (edge)
+#pragma unroll
+                            for (int f = 0; f < 4; ++f) a[f] = mask >> (e + f) & 1 ? a[f] : 0.f;
+                        v[e / 2] = pack_bf16(a[0], a[1]);
+                        v[e / 2 + 1] = pack_bf16(a[2], a[3]);
+                    }
+                    tmem_st16(lane + tDP + 64 * w + 16 * q, v);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                warp_arrive(bar(Y::bDS));
+            }
+            if (!wwait(x, bar(Y::bOut), kn & 1)) return;
+            ++kn;
+            tc_fence_after();
+            // dv by the first four warps, dk by the others; sinks that parts add to as fp32
+            const uint32_t from = lane + (w == 0 ? tDV : tDK);
+            const float f = w == 0 ? 1.f : p.scale;
+            const bool summed = u.split && j < p.sinks;
+            const bool live = j < u.L && !u.part && !summed;
+            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(w == 0 ? p.dv : p.dk) + ((u.bos + j) * p.Nk + u.hk) * D;
+            bool nan = false;
+#pragma unroll
+            for (int q = 0; q < D / 64; ++q) nan |= B::store64(from + 64 * q, out + 64 * q, f, live);
+            if (u.split) {
+                float *sum = p.sink_part + (((u.place * p.Nk + u.hk) * 2 + w) * p.sinks + row) * D;
+#pragma unroll
+                for (int q = 0; q < D / 16; ++q) {
+                    uint32_t o[16];
+                    tmem_ld16(from + 16 * q, o);
+                    tmem_wait_ld_dep16(o);
+                    if (summed)
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4)
+                            *reinterpret_cast<float4 *>(sum + 16 * q + e) =
+                                make_float4(__uint_as_float(o[e]) * f, __uint_as_float(o[e + 1]) * f, __uint_as_float(o[e + 2]) * f,
+                                            __uint_as_float(o[e + 3]) * f);
+                }
+            }
+            tc_fence_before();
+            warp_arrive(bar(Y::bOutEmpty));
+            if (!u.part) B::mark(nan, u.flag);
+        }
+    }
+};
+
+template <int D, typename F>
+__device__ __forceinline__ void set_up(F &f, uint8_t *raw_smem, unsigned *status) {
+    using Y = Lay<D>;
+    const uint32_t raw = smem_u32(raw_smem);
+    f.x.base = (raw + 1023u) & ~1023u;
+    f.x.gbase = raw_smem + (f.x.base - raw);
+    f.x.abort_flag = reinterpret_cast<volatile int *>(f.x.gbase + Y::kMisc + 4);
+    f.x.status = status;
+    if (threadIdx.x == 0) {
+        mbar_init(f.bar(Y::bHold), 1);
+        mbar_init(f.bar(Y::bHoldEmpty), 1);
+        for (int s = 0; s < Y::NS; ++s) {
+            mbar_init(f.bar(Y::bFull + s), 1);
+            mbar_init(f.bar(Y::bEmpty + s), 1);
+            mbar_init(f.bar(Y::bCol + s), 1);
+        }
+        mbar_init(f.bar(Y::bS), 1);
+        mbar_init(f.bar(Y::bDP), 1);
+        mbar_init(f.bar(Y::bP), 8);
+        mbar_init(f.bar(Y::bDS), 8);
+        mbar_init(f.bar(Y::bOut), 1);
+        mbar_init(f.bar(Y::bOutEmpty), 8);
+        mbar_init(f.bar(Y::bDrain), 1);
+        *f.x.abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (threadIdx.x >> 5 == 9) {
+        tmem_alloc(f.x.base + Y::kMisc, 512);
+        tmem_relinquish();
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    f.tm = *reinterpret_cast<volatile uint32_t *>(f.x.gbase + Y::kMisc);
+}
+
+__device__ __forceinline__ void clear_up(uint32_t tm) {
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (threadIdx.x >> 5 == 9) tmem_dealloc(tm, 512);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+window_dq(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mg, const __grid_constant__ CUtensorMap mk,
+          const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mks, const __grid_constant__ CUtensorMap mvs,
+          const __grid_constant__ WindowParams p, unsigned items, long long slots) {
+    extern __shared__ uint8_t smem_raw[];
+    Dq<D> f{{Ctx{}, p, 0u}, items, slots};
+    set_up<D>(f, smem_raw, p.seq.status);
+    wait_for_launches();
+    const int warp = threadIdx.x >> 5;
+    const bool one = (threadIdx.x & 31) == 0;
+    if (warp == 8) {
+        if (one) f.load(&mq, &mg, &mk, &mv, &mks, &mvs);
+        __syncwarp();
+    } else if (warp == 9) {
+        if (one) f.mma();
+        __syncwarp();
+    } else if (warp == 10) {
+        if (blockIdx.x == 0) check_offsets(p.seq, threadIdx.x & 31, 32);
+    } else {
+        f.threads();
+    }
+    clear_up(f.tm);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+window_dkv(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mg, const __grid_constant__ CUtensorMap mk,
+           const __grid_constant__ CUtensorMap mv, const __grid_constant__ WindowParams p, unsigned items, long long slots, Parts parts) {
+    extern __shared__ uint8_t smem_raw[];
+    Dkv<D> f{{Ctx{}, p, 0u}, items, slots, parts};
+    set_up<D>(f, smem_raw, p.seq.status);
+    wait_for_launches();
+    const int warp = threadIdx.x >> 5;
+    const bool one = (threadIdx.x & 31) == 0;
+    if (warp == 8) {
+        if (one) f.load(&mq, &mg, &mk, &mv);
+        __syncwarp();
+    } else if (warp == 9) {
+        if (one) f.mma();
+        __syncwarp();
+    } else if (warp == 10) {
+        f.columns();
+    } else {
+        f.threads();
+    }
+    clear_up(f.tm);
+}
+
+// The sinks' rows of dk and dv: the part of the first key tile's own item and those of the runs of
+// query tiles behind its window, in order.  Four columns a thread.
+template <int D>
+__global__ void __launch_bounds__(256) window_sink_sums(WindowParams p, Parts parts) {
+    wait_for_launches();
+    const int hk = blockIdx.x % p.Nk, n = blockIdx.x / p.Nk;
+    const SeqTile s = seq_whole(p.seq, n);
+    if (!s.ok || s.eos == s.bos) return;
+    const int L = (int)(s.eos - s.bos);
+    const QueryTiles qt(0, L < 128 ? L : 128, L, 128, Sight{p.window, p.sinks});
+    if (qt.end <= qt.last) return;
+    const int i = blockIdx.y * 256 + threadIdx.x, per = p.sinks * (D / 4);
+    if (i >= 2 * per) return;
+    const int w = i / per, row = i % per / (D / 4), col = i % (D / 4) * 4;
+    auto at = [&](long long place) {
+        return *reinterpret_cast<const float4 *>(p.sink_part + (((place * p.Nk + hk) * 2 + w) * p.sinks + row) * D + col);
+    };
+    const long long base = p.seq.cu ? s.bos / (parts.tiles * 128) + n
+                                    : (long long)n * ((p.seq.T + parts.tiles * 128 - 1) / (parts.tiles * 128));
+    float4 v = at(parts.slots + n);
+    for (int c = (qt.last + 1) / parts.tiles; c <= qt.end / parts.tiles; ++c) {
+        const float4 a = at(base + c);
+        v.x += a.x; v.y += a.y; v.z += a.z; v.w += a.w;
+    }
+    if (row >= L) return;
+    Vec<__nv_bfloat16, 4> y;
+    y.v[0] = v.x; y.v[1] = v.y; y.v[2] = v.z; y.v[3] = v.w;
+    y.store(static_cast<__nv_bfloat16 *>(w == 0 ? p.dv : p.dk) + ((s.bos + row) * p.Nk + hk) * D + col);
+    if (isnan(v.x) | isnan(v.y) | isnan(v.z) | isnan(v.w)) {
+        // the first key tile's slot, the half that the row lies in
+        const long long slot = p.seq.cu ? s.bos / 128 + n : (long long)n * ((p.seq.T + 127) / 128);
+        atomicOr(p.redo + (slot * 2 + row / 64) * (p.Nq + p.Nk) + p.Nq + hk, 1u);
+    }
+}
+
+template <int D>
+cudaError_t launch(const WindowParams &p, cudaStream_t stream) {
+    const long long slots = tile_slots(p.seq, 128);
+    if (slots <= 0) return cudaSuccess;
+    const Parts parts{p.parts ? tile_slots(p.seq, p.part_tiles * 128) : 0, p.part_tiles};
+    const long long qi = slots * p.Nq, ki = (slots + parts.slots) * p.Nk;
+    if (qi > 0x7fffffffll || ki > 0x7fffffffll) return cudaErrorInvalidValue;
+    CUtensorMap mq, mg, mk, mv, mks, mvs;
+    const uint64_t tokens = (uint64_t)p.seq.tokens;
+    if (!make_tmap_rows_heads_d(&mq, p.q, tokens, p.Nq, D, 64, 128) || !make_tmap_rows_heads_d(&mg, p.dout, tokens, p.Nq, D, 64, 128) ||
+        !make_tmap_rows_heads_d(&mk, p.k, tokens, p.Nk, D, 64, 128) || !make_tmap_rows_heads_d(&mv, p.v, tokens, p.Nk, D, 64, 128) ||
+        !make_tmap_rows_heads_d(&mks, p.k, tokens, p.Nk, D, 64, kSinkCols) || !make_tmap_rows_heads_d(&mvs, p.v, tokens, p.Nk, D, 64, kSinkCols))
+        return cudaErrorInvalidValue;
+    constexpr int bytes = (int)Lay<D>::kAlloc;
+    cudaError_t err = allow_smem<window_dq<D>>(bytes);
+    if (err == cudaSuccess) err = allow_smem<window_dkv<D>>(bytes);
+    if (err != cudaSuccess) return err;
+    err = launch_after(window_dq<D>, dim3((unsigned)(qi < kSms ? qi : kSms)), dim3(kThreads), bytes, stream, mq, mg, mk, mv, mks, mvs, p,
+                       (unsigned)qi, slots);
+    if (err != cudaSuccess) return err;
+    err = launch_after(window_dkv<D>, dim3((unsigned)(ki < kSms ? ki : kSms)), dim3(kThreads), bytes, stream, mq, mg, mk, mv, p, (unsigned)ki,
+                       slots, parts);
+    if (err != cudaSuccess || !parts.slots) return err;
+    return launch_after(window_sink_sums<D>, dim3((unsigned)p.seq.N * p.Nk, (2 * p.sinks * (D / 4) + 255) / 256), dim3(256), 0, stream, p, parts);
+}
+
+}  // namespace
+
+cudaError_t window_tc_bwd(const WindowParams &p, cudaStream_t stream) {
+    return p.d == 64 ? launch<64>(p, stream) : launch<128>(p, stream);
+}
+
+}  // namespace dn

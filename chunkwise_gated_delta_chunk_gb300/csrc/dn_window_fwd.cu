@@ -22,13 +22,7 @@
 // they fit in one.  P is rounded to bf16 for the product; the sum takes it unrounded.
 //
 // CTAs are persistent, one an SM; every wait is bounded (dn_tc_sync.cuh).
-#include <cuda.h>
-#include <cuda_bf16.h>
-
-#include "dn_tmap.h"
-#include "dn_window.cuh"
-#include "tc_ptx.cuh"
-#include "dn_tc_sync.cuh"
+#include "dn_window_tc.cuh"
 
 namespace dn {
 namespace {
@@ -37,7 +31,6 @@ using namespace ptx;
 using namespace tcs;
 
 constexpr int kThreads = 320;
-constexpr int kSinkCols = 32;  // keys of the narrow sink tile
 
 template <int D>
 struct Lay {
@@ -116,25 +109,6 @@ __device__ __forceinline__ bool plan(Plan &u, const WindowParams &p, unsigned it
     u.narrow = u.sink && p.sinks <= kSinkCols;
     u.n = hi - u.lo + 1 + (u.sink ? 1 : 0);
     return true;
-}
-
-__device__ __forceinline__ uint32_t bit_range(int lo, int hi) {  // bits lo..hi of 32, where they are any
-    lo = lo < 0 ? 0 : lo;
-    hi = hi > 31 ? 31 : hi;
-    return lo > hi ? 0u : (0xffffffffu >> (31 - hi)) & (0xffffffffu << lo);
-}
-
-// Which of the keys k0 + 0..31 token t sees.
-__device__ __forceinline__ uint32_t seen32(int t, int k0, const Sight &s) {
-    const int hi = t - k0;
-    const int lim = s.sinks - 1 - k0 < hi ? s.sinks - 1 - k0 : hi;
-    return bit_range(hi - s.window + 1, hi) | bit_range(0, lim);
-}
-
-__device__ __forceinline__ void store32(void *dst, const uint32_t (&r)[8]) {  // 32 bytes at once
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(r[0]), "r"(r[1]), "r"(r[2]),
-                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
 }
 
 template <int D>
@@ -217,7 +191,7 @@ struct Fwd {
             at[q] = u.next(q, -1);
             if (at[q] < u.n && !issue_s(u, q, at[q], kv)) return false;
         }
-        bool first[2] = {true, true};
+        bool first[2] = {true, true}, q_free = false;
         for (int i = 0; i < u.n; ++i) {
             const unsigned k = kv + i;
 #pragma unroll
@@ -246,7 +220,11 @@ struct Fwd {
                 }
             }
             mma_commit(bar(Y::bVEmpty + k % Y::NS));
-            if (at[0] >= u.n && at[1] >= u.n && i + 1 == u.n) mma_commit(bar(Y::bQEmpty));
+            // all scores of the item are issued: Q may change when they are done
+            if (!q_free && at[0] >= u.n && at[1] >= u.n) {
+                mma_commit(bar(Y::bQEmpty));
+                q_free = true;
+            }
         }
         return true;
     }
