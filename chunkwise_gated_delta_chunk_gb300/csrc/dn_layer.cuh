@@ -47,6 +47,20 @@ inline cudaError_t allow_smem(int bytes) {
     return err;
 }
 
+// Lets a kernel be launched in clusters of more than 8 blocks, once for every device.
+template <auto kKernel>
+inline cudaError_t allow_wide_cluster() {
+    static std::atomic<unsigned long long> done{0};
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    err = cudaFuncSetAttribute(kKernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return err;
+}
+
 // V consecutive elements of T in one access (V = 1, or a power of two whose
 // bytes are the pointer's alignment), as fp32.
 template <typename T, int V>

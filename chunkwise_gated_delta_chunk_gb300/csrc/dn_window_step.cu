@@ -8,6 +8,11 @@
 // (consecutive slots of the ring, wrapping once), then the new token, whose key and value
 // are read from the call's own arguments.  The slot that the new token goes to held the
 // position `ring` before it, which is outside the window (ring >= window): no block reads it.
+//
+// A warp takes 16 positions at a time, with a running maximum and sum of its own; the warps of a
+// block, and the blocks of a cluster that share a sequence where there are few of them, join
+// these at the end through shared memory.  Every position on the list is seen, so there is
+// nothing to mask but the end of the list.
 #include "dn_window.cuh"
 
 namespace dn {
@@ -38,72 +43,428 @@ __device__ __forceinline__ int slot_of(long long pos, const CacheParams &p) {
     return pos < p.sinks ? (int)pos : p.sinks + (int)((pos - p.sinks) % p.ring);
 }
 
+constexpr int kWarps = 4;   // of a block
+constexpr int kKeys = 16;   // positions that a warp takes at a time
+
+__device__ __forceinline__ unsigned smem_at(const void *p) { return (unsigned)__cvta_generic_to_shared(p); }
+// 16 bytes into shared memory; zeros where not `in`
+__device__ __forceinline__ void copy16(unsigned dst, const void *src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ unsigned cluster_rank() {
+    unsigned r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float remote(const float *p, unsigned rank) {  // the same place in another block of the cluster
+    unsigned at;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_at(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+
+// One block's sequence, key head and rows of queries.
 template <typename T, int D>
-__global__ void __launch_bounds__(128) step_simple(CacheParams p) {
-    constexpr int E = D / 32;
-    const int h = blockIdx.x % p.Nq, n = blockIdx.x / p.Nq;
-    const int G = p.Nq / p.Nk, hk = h / G;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long had = p.lengths[n];
-    if (had < 0) {
-        if (threadIdx.x == 0) atomicOr(p.status, kStatusBadSeq);
-        return;
+struct Job {
+    int n, hk, row0, rows;  // query heads hk G + row0 + 0..rows-1
+    long long had;
+    const T *kc, *vc, *kn, *vn;
+    bool ok;
+    __device__ __forceinline__ Job(const CacheParams &p, unsigned block, int tile) {
+        const int G = p.Nq / p.Nk, tiles = (G + tile - 1) / tile;
+        row0 = block % tiles * tile;
+        rows = G - row0 < tile ? G - row0 : tile;
+        hk = block / tiles % p.Nk;
+        n = block / tiles / p.Nk;
+        had = p.lengths[n];
+        const long long cache = ((long long)n * p.Nk + hk) * (p.sinks + p.ring) * D, one = ((long long)n * p.Nk + hk) * D;
+        kc = static_cast<const T *>(p.kc) + cache;
+        vc = static_cast<const T *>(p.vc) + cache;
+        kn = static_cast<const T *>(p.k) + one;
+        vn = static_cast<const T *>(p.v) + one;
+        ok = had >= 0;
+        if (!ok) {
+            if (threadIdx.x == 0) atomicOr(p.status, kStatusBadSeq);
+            had = 0;
+        }
     }
-    const long long cache = ((long long)n * p.Nk + hk) * (p.sinks + p.ring);
-    const T *kc = static_cast<const T *>(p.kc) + cache * D, *vc = static_cast<const T *>(p.vc) + cache * D;
-    const T *kn = static_cast<const T *>(p.k) + ((long long)n * p.Nk + hk) * D;
-    const T *vn = static_cast<const T *>(p.v) + ((long long)n * p.Nk + hk) * D;
-    const Seen seen(had, p);
-    const float c = p.scale * kLog2e;
-    Vec<T, E> q;
-    q.load(static_cast<const T *>(p.q) + ((long long)n * p.Nq + h) * D + lane * E);
-    float m = -CUDART_INF_F, l = 0.f, acc[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    for (int i = warp; i <= seen.n; i += 4) {
+    __device__ __forceinline__ long long query(const CacheParams &p, int r) const {
+        return ((long long)n * p.Nq + hk * (p.Nq / p.Nk) + row0 + r) * D;
+    }
+    // rows i of the list: key and value, and whether there is such a row
+    __device__ __forceinline__ bool row(const Seen &seen, int i, const T *&k, const T *&v) const {
         const long long at = i < seen.n ? (long long)seen.slot(i) * D : 0;
-        Vec<T, E> k, v;
-        k.load((i < seen.n ? kc + at : kn) + lane * E);
-        v.load((i < seen.n ? vc + at : vn) + lane * E);
-        float s = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) s = fmaf(q.v[e], k.v[e], s);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        s *= c;
-        const float top = fmaxf(m, s), base = top == -CUDART_INF_F ? 0.f : top;
-        const float f = ex2(m - base), w = ex2(s - base);
-        m = top;
-        l = l * f + w;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = acc[e] * f + w * v.v[e];
+        k = i < seen.n ? kc + at : kn;
+        v = i < seen.n ? vc + at : vn;
+        return i <= seen.n;
     }
-    __shared__ float sm[4], sl[4], so[4][D];
-    if (lane == 0) sm[warp] = m, sl[warp] = l;
-#pragma unroll
-    for (int e = 0; e < E; ++e) so[warp][lane * E + e] = acc[e];
+    // the new token's own slot (see above: no block of this launch reads it)
+    __device__ __forceinline__ void keep(const CacheParams &p) const {
+        constexpr int V = 16 / sizeof(T);
+        const long long at = (long long)slot_of(had, p) * D;
+        for (int i = threadIdx.x * V; i < 2 * D; i += 32 * kWarps * V) {
+            Pack<T, V> x;
+            x.load(i < D ? kn + i : vn + i - D);
+            x.store(const_cast<T *>(i < D ? kc + at + i : vc + at + i - D));
+        }
+    }
+};
+
+// Joins what the warps of a cluster's blocks found: for every row a maximum m (of scores times
+// log2 e), the sum l of the weights and the weighted values o, all in shared memory.  First within the block,
+// then every block adds up its share of the columns over all blocks, in their order.
+template <typename T, int D, int ROWS>
+__device__ __forceinline__ void join(const CacheParams &p, const Job<T, D> &job, const float *o, int stride, float (&m)[kWarps][ROWS],
+                                     float (&l)[kWarps][ROWS], float *sum, float (&top)[ROWS], float (&all)[ROWS], unsigned blocks) {
+    constexpr int NT = 32 * kWarps;
+    auto best = [&](int r) {
+        const float t = fmaxf(fmaxf(m[0][r], m[1][r]), fmaxf(m[2][r], m[3][r]));
+        return t;
+    };
     __syncthreads();
-    if (threadIdx.x < D) {
-        float top = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-        top = top == -CUDART_INF_F ? 0.f : top;
-        float sum = 0.f, o = 0.f;
+    for (int i = threadIdx.x; i < job.rows * D; i += NT) {
+        const int r = i / D;
+        const float t = best(r), base = t == -CUDART_INF_F ? 0.f : t;
+        float a = 0.f, s = 0.f;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const float f = ex2(sm[w] - top);
-            sum += sl[w] * f;
-            o += so[w][threadIdx.x] * f;
+        for (int w = 0; w < kWarps; ++w) {
+            const float f = ex2(m[w][r] - base);
+            a = fmaf(f, o[w * stride + i], a);
+            s = fmaf(f, l[w][r], s);
         }
-        Vec<T, 1> y;
-        y.v[0] = o / sum;
-        y.store(static_cast<T *>(p.o) + ((long long)n * p.Nq + h) * D + threadIdx.x);
-    }
-    if (h % G == 0) {
-        const long long at = (cache + slot_of(had, p)) * D;
-        for (int i = threadIdx.x; i < D; i += 128) {
-            static_cast<T *>(p.kc)[at + i] = kn[i];
-            static_cast<T *>(p.vc)[at + i] = vn[i];
+        sum[i] = a;
+        if (i % D == 0) {
+            top[r] = t;
+            all[r] = s;
         }
     }
+    if (blocks > 1) cluster_sync();
+    else __syncthreads();
+    const unsigned rank = blocks > 1 ? cluster_rank() : 0;
+    if (job.ok)
+        for (int i = rank * NT + threadIdx.x; i < job.rows * D; i += NT * blocks) {
+            const int r = i / D;
+            float a, s;
+            if (blocks > 1) {
+                float t = -CUDART_INF_F;
+                for (unsigned b = 0; b < blocks; ++b) t = fmaxf(t, remote(&top[r], b));
+                const float base = t == -CUDART_INF_F ? 0.f : t;
+                a = s = 0.f;
+                for (unsigned b = 0; b < blocks; ++b) {
+                    const float f = ex2(remote(&top[r], b) - base);
+                    a = fmaf(f, remote(sum + i, b), a);
+                    s = fmaf(f, remote(&all[r], b), s);
+                }
+            } else {
+                a = sum[i];
+                s = all[r];
+            }
+            Vec<T, 1> y;
+            y.v[0] = a / s;
+            y.store(static_cast<T *>(p.o) + job.query(p, 0) + i);
+        }
+    if (blocks > 1) cluster_sync();  // a block's shared memory stays until the others have read it
+}
+
+// ---- bf16 -------------------------------------------------------------------
+
+__device__ __forceinline__ void ldmatrix4(unsigned (&r)[4], unsigned at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4t(unsigned (&r)[4], unsigned at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const unsigned (&a)[4], unsigned b0, unsigned b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+constexpr int kRows = 16;  // query heads of a block, of one key head
+
+template <int D>
+struct StepSmem {
+    static constexpr int kStage = 2 * kKeys * D * 2;  // keys and values
+    static constexpr int kStages = 3;
+    static constexpr int kWarp = kStages * kStage;
+    static constexpr int kPart = kRows * D * 4;  // a warp's o, over its stages
+    static_assert(kPart <= kWarp, "a warp's sums lie over its stages");
+    static constexpr int kBytes = kWarps * kWarp + kPart;
+};
+
+extern __shared__ __align__(128) char s_step[];
+
+// Tensor-core form: 16 query heads of a key head (rows that do not exist are zeros) against 16
+// positions a warp at a time.  The memory rate bounds it: the products of 16 rows (mma.sync) take less
+// time than the positions' 2 x 16 x d values to come, which three stages of asynchronous
+// copies a warp keep in flight; no warp waits for another before the end.
+template <int D>
+__global__ void __launch_bounds__(32 * kWarps, 2) step_bf16(const __grid_constant__ CacheParams p, unsigned blocks) {
+    using T = __nv_bfloat16;
+    using S = StepSmem<D>;
+    constexpr int C = D / 8, NK = D / 16, PER = C / 2;  // 16-byte chunks of a row; k steps; rows that a lane copies
+    __shared__ float sm[kWarps][kRows], sl[kWarps][kRows], top[kRows], all[kRows];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Job<T, D> job(p, blockIdx.x / blocks, kRows);
+    const Seen seen(job.had, p);
+    const int total = job.ok ? (seen.n + kKeys) / kKeys : 0;  // groups of positions, the new token among them
+    const int first = (int)(blockIdx.x % blocks) * kWarps + warp, step = (int)blocks * kWarps;
+    char *mine = s_step + warp * S::kWarp;
+    const unsigned base = smem_at(mine);
+    auto fetch = [&](int g, int stage) {
+        if (g < total) {
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                const int r = lane / C + (32 / C) * j, c = lane % C;
+                const T *k, *v;
+                const bool in = job.row(seen, g * kKeys + r, k, v);
+                const unsigned to = base + stage * S::kStage + r * D * 2 + ((c ^ (r & 7)) << 4);
+                copy16(to, k + 8 * c, in);
+                copy16(to + kKeys * D * 2, v + 8 * c, in);
+            }
+        }
+        copy_commit();
+    };
+    for (int s = 0; s < S::kStages - 1; ++s) fetch(first + s * step, s);
+    unsigned q[NK][4];
+    {
+        const T *src = static_cast<const T *>(p.q) + job.query(p, 0) + (lane % 4) * 2;
+#pragma unroll
+        for (int i = 0; i < NK; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int r = lane / 4 + 8 * (e & 1);
+                q[i][e] = r < job.rows ? *reinterpret_cast<const unsigned *>(src + r * D + i * 16 + 8 * (e >> 1)) : 0u;
+            }
+    }
+    const float c = p.scale * kLog2e;
+    float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};  // rows lane / 4 and 8 behind it
+    float o[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+    int stage = 0;
+    for (int g = first; g < total; g += step) {
+        fetch(g + (S::kStages - 1) * step, stage + S::kStages - 1 >= S::kStages ? stage - 1 : stage + S::kStages - 1);
+        copy_wait<S::kStages - 1>();
+        __syncwarp();
+        const unsigned ks = base + stage * S::kStage, vs = ks + kKeys * D * 2;
+        float s[2][4] = {};
+#pragma unroll
+        for (int i = 0; i < NK; ++i) {
+            unsigned b[4];
+            // matrices: keys 0-7 and 8-15, columns 0-7 and 8-15 of the step
+            const int r = (lane & 7) + (lane >> 4) * 8, cc = 2 * i + (lane >> 3 & 1);
+            ldmatrix4(b, ks + r * D * 2 + ((cc ^ (r & 7)) << 4));
+            mma16816(s[0], q[i], b[0], b[1]);
+            mma16816(s[1], q[i], b[2], b[3]);
+        }
+        // positions behind the list weigh nothing
+        const int left = seen.n + 1 - g * kKeys;
+        float best[2] = {m[0], m[1]};
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[t][e] = t * 8 + (lane & 3) * 2 + (e & 1) < left ? s[t][e] * c : -CUDART_INF_F;
+                best[e >> 1] = fmaxf(best[e >> 1], s[t][e]);
+            }
+        bool moved = false;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            best[h] = fmaxf(best[h], __shfl_xor_sync(0xffffffffu, best[h], 1));
+            best[h] = fmaxf(best[h], __shfl_xor_sync(0xffffffffu, best[h], 2));
+            moved |= best[h] != m[h];
+        }
+        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float f = ex2(m[h] - (best[h] == -CUDART_INF_F ? 0.f : best[h]));
+                m[h] = best[h];
+                l[h] *= f;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    o[i][2 * h] *= f;
+                    o[i][2 * h + 1] *= f;
+                }
+            }
+        }
+        unsigned a[4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float from = m[h] == -CUDART_INF_F ? 0.f : m[h];
+                const float x = ex2(s[t][2 * h] - from), y = ex2(s[t][2 * h + 1] - from);
+                l[h] += x + y;
+                a[2 * t + h] = Vec<T, 2>::pack(x, y);
+            }
+#pragma unroll
+        for (int i = 0; i < NK; ++i) {
+            unsigned b[4];
+            // transposed: keys 0-7 and 8-15, columns 0-7 and 8-15 of the pair of tiles
+            const int r = (lane & 7) + (lane >> 3 & 1) * 8, cc = 2 * i + (lane >> 4);
+            ldmatrix4t(b, vs + r * D * 2 + ((cc ^ (r & 7)) << 4));
+            mma16816(o[2 * i], a, b[0], b[1]);
+            mma16816(o[2 * i + 1], a, b[2], b[3]);
+        }
+        __syncwarp();
+        stage = stage + 1 == S::kStages ? 0 : stage + 1;
+    }
+    copy_wait<0>();
+    __syncwarp();
+    float *part = reinterpret_cast<float *>(mine);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int r = lane / 4 + 8 * h;
+        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+        if ((lane & 3) == 0) {
+            sm[warp][r] = m[h];
+            sl[warp][r] = l[h];
+        }
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+            *reinterpret_cast<float2 *>(part + r * D + i * 8 + (lane & 3) * 2) = make_float2(o[i][2 * h], o[i][2 * h + 1]);
+    }
+    if (job.ok && job.row0 == 0 && blockIdx.x % blocks == 0) job.keep(p);
+    join<T, D, kRows>(p, job, reinterpret_cast<const float *>(s_step), S::kWarp / 4, sm, sl,
+                      reinterpret_cast<float *>(s_step + kWarps * S::kWarp), top, all, blocks);
+}
+
+// ---- fp32 -------------------------------------------------------------------
+
+// CUDA-core form: a lane takes one position's score over half of the columns (two lanes a position)
+// for ROWS query heads, then D / 32 columns of the weighted values.
+template <int D, int ROWS>
+struct StepSmem32 {
+    static constexpr int kRow = D + 4;  // floats: rows 16 bytes apart on the banks
+    static constexpr int kStage = 2 * kKeys * kRow * 4;
+    static constexpr int kStages = 2;
+    static constexpr int kWarp = kStages * kStage;
+    static constexpr int kPart = ROWS * D * 4;
+    static_assert(kPart <= kWarp, "a warp's sums lie over its stages");
+    static constexpr int kBytes = kWarps * kWarp + 2 * kPart;  // and the queries
+};
+
+template <int D, int ROWS>
+__global__ void __launch_bounds__(32 * kWarps) step_f32(const __grid_constant__ CacheParams p, unsigned blocks) {
+    using S = StepSmem32<D, ROWS>;
+    constexpr int C = D / 4, E = D / 32;  // 16-byte chunks of a row; columns of a lane
+    __shared__ float sm[kWarps][ROWS], sl[kWarps][ROWS], top[ROWS], all[ROWS];
+    __shared__ __align__(16) float weight[kWarps][kKeys][ROWS];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Job<float, D> job(p, blockIdx.x / blocks, ROWS);
+    const Seen seen(job.had, p);
+    const int total = job.ok ? (seen.n + kKeys) / kKeys : 0;
+    const int first = (int)(blockIdx.x % blocks) * kWarps + warp, step = (int)blocks * kWarps;
+    char *mine = s_step + warp * S::kWarp;
+    float *qs = reinterpret_cast<float *>(s_step + kWarps * S::kWarp);
+    const unsigned base = smem_at(mine);
+    auto fetch = [&](int g, int stage) {
+        if (g < total) {
+#pragma unroll
+            for (int j = 0; j < kKeys * C / 32; ++j) {
+                const int r = (lane + 32 * j) / C, c = (lane + 32 * j) % C;
+                const float *k, *v;
+                const bool in = job.row(seen, g * kKeys + r, k, v);
+                const unsigned to = base + stage * S::kStage + r * S::kRow * 4 + 16 * c;
+                copy16(to, k + 4 * c, in);
+                copy16(to + kKeys * S::kRow * 4, v + 4 * c, in);
+            }
+        }
+        copy_commit();
+    };
+    for (int s = 0; s < S::kStages - 1; ++s) fetch(first + s * step, s);
+    for (int i = threadIdx.x; i < ROWS * D; i += 32 * kWarps)
+        qs[i] = i < job.rows * D ? static_cast<const float *>(p.q)[job.query(p, 0) + i] : 0.f;
+    __syncthreads();
+    const float c = p.scale * kLog2e;
+    const int key = lane & 15, half = lane >> 4;
+    float m[ROWS], l[ROWS], o[ROWS][E];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+        m[r] = -CUDART_INF_F;
+        l[r] = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[r][e] = 0.f;
+    }
+    int stage = 0;
+    for (int g = first; g < total; g += step) {
+        fetch(g + (S::kStages - 1) * step, stage ^ 1);
+        copy_wait<S::kStages - 1>();
+        __syncwarp();
+        const float *ks = reinterpret_cast<const float *>(mine + stage * S::kStage), *vs = ks + kKeys * S::kRow;
+        f2 acc[ROWS];
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) acc[r] = 0ull;
+#pragma unroll 4
+        for (int i = 0; i < D / 2; i += 4) {
+            const ulonglong2 k = *reinterpret_cast<const ulonglong2 *>(ks + key * S::kRow + half * (D / 2) + i);
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) {
+                const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(qs + r * D + half * (D / 2) + i);
+                acc[r] = fma2(x.y, k.y, fma2(x.x, k.x, acc[r]));
+            }
+        }
+        const bool in = g * kKeys + key <= seen.n;
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            float s = sum_of(acc[r]);
+            s += __shfl_xor_sync(0xffffffffu, s, 16);
+            s = in ? s * c : -CUDART_INF_F;
+            float t = fmaxf(m[r], s);
+#pragma unroll
+            for (int x = 8; x > 0; x >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, x));
+            const float from = t == -CUDART_INF_F ? 0.f : t;
+            const float f = ex2(m[r] - from), w = ex2(s - from);
+            m[r] = t;
+            l[r] = l[r] * f + (half ? 0.f : w);
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[r][e] *= f;
+            if (!half) weight[warp][key][r] = w;
+        }
+        __syncwarp();
+#pragma unroll 4
+        for (int k = 0; k < kKeys; ++k) {
+            Vec<float, E> v;
+            v.load(vs + k * S::kRow + lane * E);
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[r][e] = fmaf(weight[warp][k][r], v.v[e], o[r][e]);
+        }
+        __syncwarp();
+        stage ^= 1;
+    }
+    copy_wait<0>();
+    __syncwarp();
+    float *part = reinterpret_cast<float *>(mine);
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], x);
+        if (lane == 0) {
+            sm[warp][r] = m[r];
+            sl[warp][r] = l[r];
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) part[r * D + lane * E + e] = o[r][e];
+    }
+    if (job.ok && job.row0 == 0 && blockIdx.x % blocks == 0) job.keep(p);
+    join<float, D, ROWS>(p, job, reinterpret_cast<const float *>(s_step), S::kWarp / 4, sm, sl, qs + ROWS * D, top, all, blocks);
 }
 
 // Tokens of the prompts into the caches: a tile of 32 tokens of one sequence per block,
@@ -154,15 +515,52 @@ cudaError_t window_fill_launch(const CacheParams &p, bool bf16, cudaStream_t str
     return cudaGetLastError();
 }
 
+namespace {
+
+// Blocks of a cluster, that share a sequence's positions: as many as it takes to put two blocks on
+// every SM, while each warp still has two groups of positions.
+template <auto kKernel>
+cudaError_t step_launch(const CacheParams &p, int rows, int bytes, cudaStream_t stream) {
+    const int G = p.Nq / p.Nk;
+    const long long jobs = (long long)p.N * p.Nk * ((G + rows - 1) / rows);
+    const long long most = (long long)p.sinks + p.window;
+    unsigned blocks = 1;
+    while (blocks < 16 && jobs * blocks < 2 * kSms && most > (long long)blocks * kWarps * kKeys * 2) blocks *= 2;
+    if (jobs * blocks > 0x7fffffffll) return cudaErrorInvalidValue;
+    cudaError_t err = allow_smem<kKernel>(bytes);
+    if (err == cudaSuccess && blocks > 8) err = allow_wide_cluster<kKernel>();
+    if (err != cudaSuccess) return err;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = blocks;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(jobs * blocks));
+    cfg.blockDim = dim3(32 * kWarps);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kKernel, p, blocks);
+}
+
+template <int D>
+cudaError_t step_f32_launch(const CacheParams &p, cudaStream_t stream) {
+    const int G = p.Nq / p.Nk;
+    if (G == 1) return step_launch<step_f32<D, 1>>(p, 1, StepSmem32<D, 1>::kBytes, stream);
+    if (G == 2) return step_launch<step_f32<D, 2>>(p, 2, StepSmem32<D, 2>::kBytes, stream);
+    if (G <= 4) return step_launch<step_f32<D, 4>>(p, 4, StepSmem32<D, 4>::kBytes, stream);
+    return step_launch<step_f32<D, 8>>(p, 8, StepSmem32<D, 8>::kBytes, stream);
+}
+
+}  // namespace
+
 cudaError_t window_step_launch(const CacheParams &p, bool bf16, cudaStream_t stream, const char **name) {
     *name = bf16 ? "window_step<bf16>" : "window_step<f32>";
-    const unsigned grid = (unsigned)p.N * p.Nq;
-    if (grid == 0) return cudaSuccess;
-    if (bf16 && p.d == 64) step_simple<__nv_bfloat16, 64><<<grid, 128, 0, stream>>>(p);
-    else if (bf16) step_simple<__nv_bfloat16, 128><<<grid, 128, 0, stream>>>(p);
-    else if (p.d == 64) step_simple<float, 64><<<grid, 128, 0, stream>>>(p);
-    else step_simple<float, 128><<<grid, 128, 0, stream>>>(p);
-    return cudaGetLastError();
+    if (p.N == 0) return cudaSuccess;
+    if (!bf16) return p.d == 64 ? step_f32_launch<64>(p, stream) : step_f32_launch<128>(p, stream);
+    return p.d == 64 ? step_launch<step_bf16<64>>(p, kRows, StepSmem<64>::kBytes, stream)
+                     : step_launch<step_bf16<128>>(p, kRows, StepSmem<128>::kBytes, stream);
 }
 
 }  // namespace dn
