@@ -12,15 +12,17 @@ namespace dn {
 // iterations ahead, in shared memory by asynchronous copies.  Rows that do not begin on 16
 // bytes, and those too long for a stage to fit, are loaded where they are used.  Tensors that are
 // null are zeros.
-template <typename T, typename TR, int V, int K, int R, int A, int B>
+template <typename T, typename TR, int V, int K, int R, int A, int B, int REGS>
 struct BlockRing {
     using L = Row<T, V, K, R>;
     static constexpr int kRes = (int)sizeof(TR) * V;  // bytes of a vector of TR: 16 or 32
     static constexpr int kOne = K * L::kThreads;      // vectors of one tensor
     static constexpr int kStage = kOne * (A * 16 + B * kRes);
-    static constexpr bool kAhead = L::kWhole && kStage <= 224 * 1024;
-    // half an SM's shared memory, so that two blocks can be there
-    static constexpr int kFit = 98304 / kStage;
+    // as many stages, up to 4, as leave room for the blocks that an SM's registers hold
+    static constexpr int kBlocks = 65536 / (REGS * L::kThreads) < 1 ? 1 : 65536 / (REGS * L::kThreads);
+    static constexpr int kRoom = 226 * 1024 / kBlocks - 2048;
+    static constexpr bool kAhead = L::kWhole && kStage <= kRoom;
+    static constexpr int kFit = kRoom / kStage;
     static constexpr int S = !kAhead || kFit < 1 ? 1 : kFit > 4 ? 4 : kFit;
     static constexpr int kBytes = kAhead ? S * kStage : 0;
     const T *a[A];
@@ -90,6 +92,45 @@ struct BlockRing {
     }
 };
 
+// One of the fp32 vectors: of a single vector a thread the values stay in registers for all rows
+// (loaded for every row they cost more time than memory does: 8192 rows of 2048 in the backward
+// 148 us), else they are loaded where they are used.
+template <typename L, int V, int K>
+struct Kept {
+    static constexpr int P = V / 2;
+    static constexpr bool kKeep = K == 1;
+    const float *src;
+    f2 v[kKeep ? P : 1];
+    __device__ __forceinline__ void init(const float *from, int D, float other) {
+        src = from;
+        if constexpr (kKeep) load_vec<L, V>(v, from, 0, D, other);
+    }
+    __device__ __forceinline__ void times(f2 (&x)[P], int k, int D) const {
+        if (!src) return;
+        f2 t[P];
+        get(t, k, D, 1.f);
+#pragma unroll
+        for (int i = 0; i < P; ++i) x[i] = mul2(x[i], t[i]);
+    }
+    __device__ __forceinline__ void plus(f2 (&x)[P], int k, int D) const {
+        if (!src) return;
+        f2 t[P];
+        get(t, k, D, 0.f);
+#pragma unroll
+        for (int i = 0; i < P; ++i) x[i] = add2(x[i], t[i]);
+    }
+
+private:
+    __device__ __forceinline__ void get(f2 (&t)[P], int k, int D, float other) const {
+        if constexpr (kKeep) {
+#pragma unroll
+            for (int i = 0; i < P; ++i) t[i] = v[i];
+        } else {
+            load_vec<L, V>(t, src, k, D, other);
+        }
+    }
+};
+
 // w v + b of one vector, where given.
 template <typename L, int V>
 __device__ __forceinline__ void affine(f2 (&v)[V / 2], const float *w, const float *b, int k, int D) {
@@ -136,6 +177,7 @@ cudaError_t block_types(const BlockParams &p, F &&f) {
 // Registers that a thread of the backward may have, and with it the blocks of its grid: from the
 // sizes alone, since every block has a row of workspace.
 template <int kThreads>
-constexpr int block_bwd_regs() { return kThreads <= 256 ? 128 : 65536 / kThreads > 128 ? 128 : 65536 / kThreads; }
+constexpr int block_bwd_regs() { return kThreads <= 512 ? 128 : 65536 / kThreads; }
+constexpr int kBlockFwdRegs = 64;
 
 }  // namespace dn

@@ -22,7 +22,7 @@ extern __shared__ __align__(16) char s_ring[];
 template <typename T, typename TR, int V, int K, int R>
 __global__ void __launch_bounds__(Row<T, V, K, R>::kThreads) block_bwd(BlockParams p) {
     using L = Row<T, V, K, R>;
-    using G = BlockRing<T, TR, V, K, R, 3, 2>;
+    using G = BlockRing<T, TR, V, K, R, 3, 2, block_bwd_regs<Row<T, V, K, R>::kThreads>()>;
     constexpr int P = L::P, kWarps = R / 32;
     __shared__ __align__(16) float buf[8 * kWarps];
     const float inv = 1.f / (float)p.D;
@@ -37,6 +37,10 @@ __global__ void __launch_bounds__(Row<T, V, K, R>::kThreads) block_bwd(BlockPara
     ring.b[1] = static_cast<const TR *>(p.dresidual_out);
 #pragma unroll
     for (int s = 0; s < G::S; ++s) ring.issue(s_ring, s, row + s * step, p.rows, p.D);
+    Kept<L, V, K> w2, w1, sc;
+    w2.init(p.weight, p.D, 1.f);
+    w1.init(p.post_weight, p.D, 1.f);
+    sc.init(p.scale, p.D, 1.f);
     f2 sums[kSums][K][P];
 #pragma unroll
     for (int q = 0; q < kSums; ++q)
@@ -60,7 +64,7 @@ __global__ void __launch_bounds__(Row<T, V, K, R>::kThreads) block_bwd(BlockPara
     };
     int stage = 0;
     for (long long first = (long long)blockIdx.x * L::kRows; first < p.rows; first += step, row += step) {
-        typename L::Pairs a, h, g;
+        typename L::Pairs a, h, g, sg;
         const bool live = row < p.rows;
         ring.wait();
 #pragma unroll
@@ -72,13 +76,17 @@ __global__ void __launch_bounds__(Row<T, V, K, R>::kThreads) block_bwd(BlockPara
             f2 r[P];
 #pragma unroll
             for (int i = 0; i < P; ++i) h[k][i] = a[k][i];
-            affine<L, V>(h[k], p.post_weight, p.post_bias, k, p.D);
+            w1.times(h[k], k, p.D);
+            affine<L, V>(h[k], nullptr, p.post_bias, k, p.D);
             if (p.z) {
-                ring.get_a(r, s_ring, stage, 1, k, row, p.rows, p.D);
+                ring.get_a(sg[k], s_ring, stage, 1, k, row, p.rows, p.D);
 #pragma unroll
-                for (int i = 0; i < P; ++i) h[k][i] = mul2(h[k][i], sigmoid2(r[i]));
+                for (int i = 0; i < P; ++i) {
+                    sg[k][i] = sigmoid2(sg[k][i]);
+                    h[k][i] = mul2(h[k][i], sg[k][i]);
+                }
             }
-            affine<L, V>(h[k], p.scale, nullptr, k, p.D);
+            sc.times(h[k], k, p.D);
             ring.get_b(r, s_ring, stage, 0, k, row, p.rows, p.D);
 #pragma unroll
             for (int i = 0; i < P; ++i) h[k][i] = add2(h[k][i], r[i]);
@@ -94,7 +102,7 @@ __global__ void __launch_bounds__(Row<T, V, K, R>::kThreads) block_bwd(BlockPara
                     sums[0][k][i] = fma2(g[k][i], h[k][i], sums[0][k][i]);
                     sums[1][k][i] = add2(sums[1][k][i], g[k][i]);
                 }
-            affine<L, V>(g[k], p.weight, nullptr, k, p.D);
+            w2.times(g[k], k, p.D);
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 t0 = fma2(g[k][i], h[k][i], t0);
@@ -118,33 +126,32 @@ __global__ void __launch_bounds__(Row<T, V, K, R>::kThreads) block_bwd(BlockPara
             f2 q[P];  // p
 #pragma unroll
             for (int i = 0; i < P; ++i) q[i] = a[k][i];
-            affine<L, V>(q, p.post_weight, p.post_bias, k, p.D);
+            w1.times(q, k, p.D);
+            affine<L, V>(q, nullptr, p.post_bias, k, p.D);
             if (p.z) {
-                f2 out[P], s[P];
-                ring.get_a(s, s_ring, stage, 1, k, row, p.rows, p.D);
-                const f2 one = both(1.f);
+                f2 out[P];
+                const f2 one = both(1.f), (&s)[P] = sg[k];
 #pragma unroll
                 for (int i = 0; i < P; ++i) {
-                    s[i] = sigmoid2(s[i]);
                     const f2 dp = mul2(g[k][i], q[i]);
                     g[k][i] = mul2(g[k][i], s[i]);
                     sums[4][k][i] = fma2(dp, s[i], sums[4][k][i]);
                     // dh p s (1 - s)
                     out[i] = mul2(mul2(dp, s[i]), fma2(s[i], both(-1.f), one));
                 }
-                affine<L, V>(out, p.scale, nullptr, k, p.D);
+                sc.times(out, k, p.D);
                 store_row<L, V>(static_cast<T *>(p.dz) + row * p.D, out, k, p.D);
             } else {
 #pragma unroll
                 for (int i = 0; i < P; ++i) sums[4][k][i] = fma2(g[k][i], q[i], sums[4][k][i]);
             }
-            affine<L, V>(g[k], p.scale, nullptr, k, p.D);  // dp
+            sc.times(g[k], k, p.D);  // dp
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 sums[2][k][i] = fma2(g[k][i], a[k][i], sums[2][k][i]);
                 sums[3][k][i] = add2(sums[3][k][i], g[k][i]);
             }
-            affine<L, V>(g[k], p.post_weight, nullptr, k, p.D);  // e
+            w1.times(g[k], k, p.D);  // e
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 t0 = fma2(g[k][i], a[k][i], t0);
@@ -228,7 +235,7 @@ struct Launch {
             return cudaSuccess;
         }
         if (grid > 0) {
-            constexpr int bytes = BlockRing<T, TR, V, K, R, 3, 2>::kBytes;
+            constexpr int bytes = BlockRing<T, TR, V, K, R, 3, 2, block_bwd_regs<Row<T, V, K, R>::kThreads>()>::kBytes;
             cudaError_t err = allow_smem<block_bwd<T, TR, V, K, R>>(bytes);
             if (err != cudaSuccess) return err;
             block_bwd<T, TR, V, K, R><<<grid, kThreads, bytes, stream>>>(p);

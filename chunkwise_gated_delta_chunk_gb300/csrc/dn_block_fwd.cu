@@ -12,9 +12,9 @@ namespace {
 extern __shared__ __align__(16) char s_ring[];
 
 template <typename T, typename TR, int V, int K, int R>
-__global__ void __launch_bounds__(Row<T, V, K, R>::kThreads) block_fwd(BlockParams p) {
+__global__ void __launch_bounds__(Row<T, V, K, R>::kThreads, 65536 / (kBlockFwdRegs * Row<T, V, K, R>::kThreads)) block_fwd(BlockParams p) {
     using L = Row<T, V, K, R>;
-    using G = BlockRing<T, TR, V, K, R, 2, 1>;
+    using G = BlockRing<T, TR, V, K, R, 2, 1, kBlockFwdRegs>;
     constexpr int P = L::P, kBuf = 2 * (R / 32);
     __shared__ __align__(16) float buf[2 * kBuf + 4];  // consecutive norms in turn
     const float inv = 1.f / (float)p.D;
@@ -27,6 +27,10 @@ __global__ void __launch_bounds__(Row<T, V, K, R>::kThreads) block_fwd(BlockPara
     ring.b[0] = static_cast<const TR *>(p.residual);
 #pragma unroll
     for (int s = 0; s < G::S; ++s) ring.issue(s_ring, s, row + s * step, p.rows, p.D);
+    Kept<L, V, K> w2, w1, sc;
+    w2.init(p.weight, p.D, 1.f);
+    w1.init(p.post_weight, p.D, 1.f);
+    sc.init(p.scale, p.D, 1.f);
     int stage = 0, turn = 0;
     for (long long first = (long long)blockIdx.x * L::kRows; first < p.rows; first += step, row += step) {
         typename L::Pairs h;
@@ -39,14 +43,15 @@ __global__ void __launch_bounds__(Row<T, V, K, R>::kThreads) block_fwd(BlockPara
         }
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            affine<L, V>(h[k], p.post_weight, p.post_bias, k, p.D);
+            w1.times(h[k], k, p.D);
+            affine<L, V>(h[k], nullptr, p.post_bias, k, p.D);
             if (p.z) {
                 f2 z[P];
                 ring.get_a(z, s_ring, stage, 1, k, row, p.rows, p.D);
 #pragma unroll
                 for (int i = 0; i < P; ++i) h[k][i] = mul2(h[k][i], sigmoid2(z[i]));
             }
-            affine<L, V>(h[k], p.scale, nullptr, k, p.D);
+            sc.times(h[k], k, p.D);
             f2 r[P];
             ring.get_b(r, s_ring, stage, 0, k, row, p.rows, p.D);
 #pragma unroll
@@ -62,7 +67,8 @@ __global__ void __launch_bounds__(Row<T, V, K, R>::kThreads) block_fwd(BlockPara
         if (row < p.rows)
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                affine<L, V>(h[k], p.weight, p.bias, k, p.D);
+                w2.times(h[k], k, p.D);
+                affine<L, V>(h[k], nullptr, p.bias, k, p.D);
                 store_row<L, V>(static_cast<T *>(p.y) + row * p.D, h[k], k, p.D);
             }
     }
@@ -74,10 +80,10 @@ struct Launch {
     template <typename T, typename TR, int V, int K, int R>
     cudaError_t operator()() const {
         constexpr int kThreads = Row<T, V, K, R>::kThreads;
-        constexpr int bytes = BlockRing<T, TR, V, K, R, 2, 1>::kBytes;
+        constexpr int bytes = BlockRing<T, TR, V, K, R, 2, 1, kBlockFwdRegs>::kBytes;
         const cudaError_t err = allow_smem<block_fwd<T, TR, V, K, R>>(bytes);
         if (err != cudaSuccess) return err;
-        block_fwd<T, TR, V, K, R><<<norm_blocks(p.rows, kThreads, Row<T, V, K, R>::kRows, 64), kThreads, bytes, stream>>>(p);
+        block_fwd<T, TR, V, K, R><<<norm_blocks(p.rows, kThreads, Row<T, V, K, R>::kRows, kBlockFwdRegs), kThreads, bytes, stream>>>(p);
         return cudaGetLastError();
     }
 };
