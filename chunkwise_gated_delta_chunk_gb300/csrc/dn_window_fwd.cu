@@ -7,13 +7,17 @@
 // where its group is even, else two neighbouring tiles of tokens of one head.  While one
 // tile's scores go through the softmax, the tensor cores work for the other.
 //
-// Warps 0-3 and 4-7: softmax of the first and the second query tile, one row a thread;
-// warp 8: TMA loads of Q, K and V; warp 9: issues the MMAs (one thread).
-// Tensor memory: scores of both tiles (128 fp32 columns each; the weights P overwrite them
-// as bf16) and both O (d columns each).
-// For every key tile j the issuer does, for the first and then the second query tile,
+// Warps 0-7 and 8-15: softmax of the first and the second query tile, four warps for each
+// half of the keys of a tile, two threads a row (one thread a row took 1900 cycles a tile, of which
+// the tensor cores need 1024: a warp alone on its scheduler does not keep up the rate of the
+// exponentials).  The two agree on the maximum through shared memory.
+// Warp 16: TMA loads of Q, K and V; warp 17: the MMAs.
+// Tensor memory: scores of both tiles (128 fp32 columns each; the weights P overwrite the
+// first half of each half of them as bf16) and both O (d columns each).
+// For every key tile j warp 17 does, for the first and then the second query tile,
 //     wait P(j);  O += P V(j);  S = Q K(j+1)
-// so S(j+1) of one tile is ready when the softmax of the other has just begun.
+// so S(j+1) of one tile is ready when the softmax of the other has just begun (with a warp for
+// each, the two tiles fell into step: both in the softmax, then both on the tensor cores, 15 % slower).
 //
 // O is rescaled only when a row's maximum has grown by more than 2^8 since the last time:
 // weights stay below 2^8, sums in fp32 lose nothing (and P in bf16 has the same relative
@@ -30,47 +34,43 @@ namespace {
 using namespace ptx;
 using namespace tcs;
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 576;
 
 template <int D>
 struct Lay {
     static constexpr uint32_t kPanel = 128 * 128;            // 128 rows of 64 columns
     static constexpr uint32_t kTile = (D / 64) * kPanel;     // 128 rows of D
-    static constexpr int NS = D == 64 ? 4 : 2;               // stages of K and of V
+    static constexpr int NS = D == 64 ? 4 : 2;               // stages of keys and values
     static constexpr uint32_t kQ = 0, kK = 2 * kTile, kV = kK + NS * kTile, kBar = kV + NS * kTile;
     // barriers
-    static constexpr int bQFull = 0, bQEmpty = 1, bKFull = 2, bKEmpty = bKFull + NS, bVFull = bKEmpty + NS,
-                         bVEmpty = bVFull + NS, bS = bVEmpty + NS, bP = bS + 2, bO = bP + 2, bOEmpty = bO + 2, bDrain = bOEmpty + 2,
-                         kBars = bDrain + 1;
-    static constexpr uint32_t kMisc = kBar + 8 * kBars, kAlloc = kMisc + 16 + 1024;
+    static constexpr int bQFull = 0, bQEmpty = 1, bFull = 2, bEmpty = bFull + NS, bS = bEmpty + NS, bP = bS + 2, bO = bP + 2,
+                         bOEmpty = bO + 2, bDrain = bOEmpty + 2, bPair = bDrain + 1, kBars = bPair + 8;
+    static constexpr uint32_t kBox = (kBar + 8 * kBars + 15) / 16 * 16, kWish = kBox + 2 * 2 * 128 * 4, kMisc = kWish + 2 * 2 * 128 * 4, kAlloc = kMisc + 16 + 1024;
     static_assert(kAlloc <= 232448, "exceeds the 227 KB of shared memory per CTA");
     // tensor memory columns
     static constexpr uint32_t tS = 0, tO = 256, kCols = 512;
 };
 
+// A tile's weights in a row, half of them, may sum to this before the row's reference moves up.
+constexpr float kGrown = 65536.f;
+
 constexpr uint32_t kIdS = idesc_bf16(128, 128, 0, 0), kIdSNarrow = idesc_bf16(128, kSinkCols, 0, 0);
 
-// One work item: two query tiles and the key tiles that either sees.
+// One work item: two query tiles and the list of key tiles that either sees.  Places of the
+// list that a query tile looks at: [from, to], and 0 where `zero`.
+struct Span {
+    int from, to, t0, h;
+    bool zero, act;
+    __device__ __forceinline__ bool has(int i) const { return i == 0 ? zero : i >= from && i <= to; }
+};
 struct Plan {
     long long bos;
     int L, hk;
-    int h[2], t0[2], first[2], last[2];
-    bool act[2];
+    Span q0, q1;
     bool sink, narrow;  // the list begins with the sinks' tile; as kSinkCols keys
-    int lo, n;          // the first of the other tiles, and the length of the list
-    int sinks;
-    __device__ __forceinline__ int tile(int i) const { return sink ? (i == 0 ? 0 : lo + i - 1) : lo + i; }
+    int lo, n;          // place i holds key tile lo + i (but the sinks' at 0); length of the list
+    __device__ __forceinline__ int tile(int i) const { return sink && i == 0 ? 0 : lo + i; }
     __device__ __forceinline__ bool small(int i) const { return narrow && i == 0; }
-    // whether query tile q looks at place i of the list
-    __device__ __forceinline__ bool takes(int q, int i) const {
-        const int k = tile(i);
-        return act[q] && ((k >= first[q] && k <= last[q]) || (k == 0 && sinks > 0));
-    }
-    __device__ __forceinline__ int next(int q, int i) const {
-        for (++i; i < n; ++i)
-            if (takes(q, i)) return i;
-        return n;
-    }
 };
 
 // Items are numbered with a key head's pairs next to each other and late tiles first: under a
@@ -86,28 +86,32 @@ __device__ __forceinline__ bool plan(Plan &u, const WindowParams &p, unsigned it
     if (!s.ok || s.t0 >= s.t1) return false;
     u.bos = s.bos;
     u.L = (int)(s.eos - s.bos);
-    u.sinks = p.sinks;
     const Sight sight{p.window, p.sinks};
-    const int t0 = (int)(s.t0 - s.bos);
-    u.lo = 1 << 30;
-    int hi = -1;
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        u.h[q] = u.hk * G + (by_head ? 2 * pr + q : pr);
-        u.t0[q] = t0 + (by_head ? 0 : 128 * q);
-        u.act[q] = u.t0[q] < u.L;
-        const int t1 = u.t0[q] + 128 < u.L ? u.t0[q] + 128 : u.L;
-        const KeyTiles kt(u.t0[q], u.act[q] ? t1 : u.t0[q] + 1, 128, sight);
-        u.first[q] = kt.first;
-        u.last[q] = kt.last;
-        if (u.act[q]) {
-            u.lo = kt.first < u.lo ? kt.first : u.lo;
-            hi = kt.last > hi ? kt.last : hi;
-        }
-    }
-    u.sink = u.lo > 0 && p.sinks > 0;
+    auto span = [&](int q, KeyTiles &kt) {
+        Span v;
+        v.h = u.hk * G + (by_head ? 2 * pr + q : pr);
+        v.t0 = (int)(s.t0 - s.bos) + (by_head ? 0 : 128 * q);
+        v.act = v.t0 < u.L;
+        const int t1 = v.t0 + 128 < u.L ? v.t0 + 128 : u.L;
+        kt = KeyTiles(v.t0, v.act ? t1 : v.t0 + 1, 128, sight);
+        return v;
+    };
+    KeyTiles k0, k1;
+    u.q0 = span(0, k0);  // always there
+    u.q1 = span(1, k1);
+    const int lo = k0.first, hi = u.q1.act ? k1.last : k0.last;
+    u.sink = lo > 0 && p.sinks > 0;
     u.narrow = u.sink && p.sinks <= kSinkCols;
-    u.n = hi - u.lo + 1 + (u.sink ? 1 : 0);
+    u.lo = u.sink ? lo - 1 : lo;
+    u.n = hi - u.lo + 1;
+    auto places = [&](Span &v, const KeyTiles &kt) {
+        v.from = kt.first - u.lo;
+        v.to = kt.last - u.lo;
+        v.zero = v.act && (v.from == 0 || (u.tile(0) == 0 && p.sinks > 0));
+        if (!v.act) v.from = 1, v.to = 0;
+    };
+    places(u.q0, k0);
+    places(u.q1, k1);
     return true;
 }
 
@@ -123,245 +127,247 @@ struct Fwd {
     __device__ __forceinline__ uint32_t bar(int i) const { return x.base + Y::kBar + 8u * i; }
 
     // ---- TMA ------------------------------------------------------------------
+    // Keys and values come in units: the keys of place 0; the values of place i with the keys
+    // of place i + 1.
     __device__ void load(const CUtensorMap *mq, const CUtensorMap *mk, const CUtensorMap *mv, const CUtensorMap *mks,
                          const CUtensorMap *mvs) {
-        unsigned kv = 0, qn = 0;
+        unsigned un = 0, qn = 0;
         bool fine = true;
         for (unsigned item = blockIdx.x; fine && item < items; item += gridDim.x) {
             Plan u;
             if (!plan(u, p, item, slots)) continue;
             if (!wait(x, bar(Y::bQEmpty), (qn & 1) ^ 1)) break;
-            mbar_arrive_expect_tx(bar(Y::bQFull), (u.act[0] + u.act[1]) * Y::kTile);
-            for (int q = 0; q < 2; ++q)
-                if (u.act[q])
-                    for (int c = 0; c < D / 64; ++c)
-                        tma_load_3d(x.base + Y::kQ + q * Y::kTile + c * Y::kPanel, mq, bar(Y::bQFull), 64 * c, u.h[q],
-                                    (int)(u.bos + u.t0[q]));
+            mbar_arrive_expect_tx(bar(Y::bQFull), u.q1.act ? 2 * Y::kTile : Y::kTile);
+            for (int c = 0; c < D / 64; ++c) {
+                tma_load_3d(x.base + Y::kQ + c * Y::kPanel, mq, bar(Y::bQFull), 64 * c, u.q0.h, (int)(u.bos + u.q0.t0));
+                if (u.q1.act)
+                    tma_load_3d(x.base + Y::kQ + Y::kTile + c * Y::kPanel, mq, bar(Y::bQFull), 64 * c, u.q1.h, (int)(u.bos + u.q1.t0));
+            }
             ++qn;
-            for (int i = 0; i < u.n; ++i, ++kv) {
-                const int s = kv % Y::NS;
-                const uint32_t ph = ((kv / Y::NS) & 1) ^ 1;
-                const bool small = u.small(i);
-                const uint32_t bytes = small ? kSinkCols * D * 2 : Y::kTile;
-                const int row = (int)(u.bos + (long long)u.tile(i) * 128);
-                if (!(fine = wait(x, bar(Y::bKEmpty + s), ph))) break;
-                mbar_arrive_expect_tx(bar(Y::bKFull + s), bytes);
-                for (int c = 0; c < D / 64; ++c)
-                    tma_load_3d(x.base + Y::kK + s * Y::kTile + c * Y::kPanel, small ? mks : mk, bar(Y::bKFull + s), 64 * c, u.hk, row);
-                if (!(fine = wait(x, bar(Y::bVEmpty + s), ph))) {
-                    wait_drain(bar(Y::bKFull + s), ph ^ 1);
-                    break;
+            for (int i = 0; i <= u.n; ++i, ++un) {
+                const int s = un % Y::NS;
+                if (!(fine = wait(x, bar(Y::bEmpty + s), ((un / Y::NS) & 1) ^ 1))) break;
+                const bool vs = i > 0 && u.small(i - 1), ks = u.small(i);
+                uint32_t bytes = 0;
+                if (i > 0) bytes += vs ? kSinkCols * D * 2 : Y::kTile;
+                if (i < u.n) bytes += ks ? kSinkCols * D * 2 : Y::kTile;
+                mbar_arrive_expect_tx(bar(Y::bFull + s), bytes);
+                for (int c = 0; c < D / 64; ++c) {
+                    if (i > 0)
+                        tma_load_3d(x.base + Y::kV + s * Y::kTile + c * Y::kPanel, vs ? mvs : mv, bar(Y::bFull + s), 64 * c, u.hk,
+                                    (int)(u.bos + (long long)u.tile(i - 1) * 128));
+                    if (i < u.n)
+                        tma_load_3d(x.base + Y::kK + s * Y::kTile + c * Y::kPanel, ks ? mks : mk, bar(Y::bFull + s), 64 * c, u.hk,
+                                    (int)(u.bos + (long long)u.tile(i) * 128));
                 }
-                mbar_arrive_expect_tx(bar(Y::bVFull + s), bytes);
-                for (int c = 0; c < D / 64; ++c)
-                    tma_load_3d(x.base + Y::kV + s * Y::kTile + c * Y::kPanel, small ? mvs : mv, bar(Y::bVFull + s), 64 * c, u.hk, row);
             }
         }
         // copies still in flight land before the CTA ends
         if (qn) wait_drain(bar(Y::bQFull), (qn - 1) & 1);
-        for (unsigned i = kv > Y::NS ? kv - Y::NS : 0; i < kv; ++i) {
-            wait_drain(bar(Y::bKFull + i % Y::NS), (i / Y::NS) & 1);
-            wait_drain(bar(Y::bVFull + i % Y::NS), (i / Y::NS) & 1);
-        }
+        for (unsigned i = un > Y::NS ? un - Y::NS : 0; i < un; ++i) wait_drain(bar(Y::bFull + i % Y::NS), (i / Y::NS) & 1);
     }
 
-    // ---- MMA ------------------------------------------------------------------
-    __device__ __forceinline__ bool issue_s(const Plan &u, int q, int i, unsigned kv) {
-        const unsigned k = kv + i;
-        if (!wait(x, bar(Y::bKFull + k % Y::NS), (k / Y::NS) & 1)) return false;
-        tc_fence_after();
-        const uint32_t a = x.base + Y::kQ + q * Y::kTile, b = x.base + Y::kK + (k % Y::NS) * Y::kTile;
-        const uint32_t id = u.small(i) ? kIdSNarrow : kIdS;
+    // ---- MMAs -----------------------------------------------------------------
+    __device__ __forceinline__ void issue_s(uint32_t lead, int q, unsigned unit, bool small) const {
+        const uint32_t a = rows_of(x.base + Y::kQ + q * Y::kTile), b = rows_of(x.base + Y::kK + (unit % Y::NS) * Y::kTile);
+        const uint32_t id = small ? kIdSNarrow : kIdS;
 #pragma unroll
         for (int c = 0; c < D / 64; ++c)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-                mma_ss(tm + Y::tS + 128 * q, sdesc(a + c * Y::kPanel + kk * 32, 16, 1024),
-                       sdesc(b + c * Y::kPanel + kk * 32, 16, 1024), id, (c | kk) != 0);
-        mma_commit(bar(Y::bS + q));
-        mma_commit(bar(Y::bKEmpty + k % Y::NS));
-        return true;
+                mma_ss_by(lead, tm + Y::tS + 128 * q, a + (c * Y::kPanel + kk * 32) / 16, b + (c * Y::kPanel + kk * 32) / 16, id,
+                          (c | kk) != 0);
+        commit_by(lead, bar(Y::bS + q));
     }
-
-    __device__ bool mma_item(const Plan &u, unsigned kv, unsigned qn, unsigned (&ns)[2], unsigned (&no)[2]) {
-        if (!wait(x, bar(Y::bQFull), qn & 1)) return false;
-        int at[2];
+    __device__ __forceinline__ void issue_o(uint32_t lead, int q, unsigned unit, bool small, bool more) const {
+        const uint32_t b = cols_of(x.base + Y::kV + (unit % Y::NS) * Y::kTile), d = tm + Y::tO + D * q, w = tm + Y::tS + 128 * q;
+        constexpr uint32_t id = idesc_bf16(128, D, 0, 1);
+        mma_ts_by(lead, d, w, b, id, more);
+        mma_ts_by(lead, d, w + 8, b + 128, id, 1);
+        static_assert(kSinkCols == 32, "two steps of 16 keys");
+        if (!small)
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            at[q] = u.next(q, -1);
-            if (at[q] < u.n && !issue_s(u, q, at[q], kv)) return false;
-        }
-        bool first[2] = {true, true}, q_free = false;
-        for (int i = 0; i < u.n; ++i) {
-            const unsigned k = kv + i;
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                if (at[q] != i) {  // not this one's: its share of the stage is free
-                    mbar_arrive(bar(Y::bKEmpty + k % Y::NS));
-                    continue;
-                }
-                if (!wait(x, bar(Y::bVFull + k % Y::NS), (k / Y::NS) & 1)) return false;
-                if (first[q] && !wait(x, bar(Y::bOEmpty + q), (no[q] & 1) ^ 1)) return false;
-                if (!wait(x, bar(Y::bP + q), ns[q] & 1)) return false;
-                ++ns[q];
-                tc_fence_after();
-                const uint32_t b = x.base + Y::kV + (k % Y::NS) * Y::kTile;
-                const int steps = u.small(i) ? kSinkCols / 16 : 8;
-                for (int kk = 0; kk < steps; ++kk)
-                    mma_ts(tm + Y::tO + D * q, tm + Y::tS + 128 * q + kk * 8, sdesc(b + kk * 2048, Y::kPanel, 1024),
-                           idesc_bf16(128, D, 0, 1), !(first[q] && kk == 0));
-                first[q] = false;
-                at[q] = u.next(q, i);
-                if (at[q] < u.n) {
-                    if (!issue_s(u, q, at[q], kv)) return false;
-                } else {
-                    mma_commit(bar(Y::bO + q));
-                    ++no[q];
-                }
-            }
-            mma_commit(bar(Y::bVEmpty + k % Y::NS));
-            // all scores of the item are issued: Q may change when they are done
-            if (!q_free && at[0] >= u.n && at[1] >= u.n) {
-                mma_commit(bar(Y::bQEmpty));
-                q_free = true;
-            }
-        }
-        return true;
+            for (int kk = 2; kk < 8; ++kk)  // the keys' halves lie 64 columns apart
+                mma_ts_by(lead, d, w + 64 * (kk >> 2) + 8 * (kk & 3), b + kk * 128, id, 1);
     }
 
     __device__ void mma() {
-        unsigned kv = 0, qn = 0, ns[2] = {0, 0}, no[2] = {0, 0};
-        for (unsigned item = blockIdx.x; item < items; item += gridDim.x) {
+        const uint32_t lead = elect();
+        unsigned un = 0, qn = 0, ns[2] = {0, 0}, no[2] = {0, 0};
+        bool fine = true;
+        for (unsigned item = blockIdx.x; fine && item < items; item += gridDim.x) {
             Plan u;
             if (!plan(u, p, item, slots)) continue;
-            if (!mma_item(u, kv, qn, ns, no)) break;
-            kv += u.n;
+            if (!(fine = hold(x, bar(Y::bQFull), qn & 1) && hold(x, bar(Y::bFull + un % Y::NS), (un / Y::NS) & 1))) break;
+            tc_fence_after();
+            if (u.q0.zero) issue_s(lead, 0, un, u.small(0));
+            if (u.q1.zero) issue_s(lead, 1, un, u.small(0));
+            commit_by(lead, bar(Y::bEmpty + un % Y::NS));
+            if (u.n == 1) commit_by(lead, bar(Y::bQEmpty));
+            ++un;
+            bool more[2] = {false, false};
+            for (int i = 0; i < u.n; ++i, ++un) {
+                if (!(fine = hold(x, bar(Y::bFull + un % Y::NS), (un / Y::NS) & 1))) break;
+                const bool small = u.small(i);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const Span &v = q ? u.q1 : u.q0;
+                    if (v.has(i)) {
+                        if (!more[q] && !(fine = hold(x, bar(Y::bOEmpty + q), (no[q] & 1) ^ 1))) break;
+                        if (!(fine = hold(x, bar(Y::bP + q), ns[q] & 1))) break;
+                        ++ns[q];
+                        tc_fence_after();
+                        issue_o(lead, q, un, small, more[q]);
+                        more[q] = true;
+                        if (i == v.to) {
+                            commit_by(lead, bar(Y::bO + q));
+                            ++no[q];
+                        }
+                    }
+                    if (v.has(i + 1)) issue_s(lead, q, un, false);
+                }
+                if (!fine) break;
+                commit_by(lead, bar(Y::bEmpty + un % Y::NS));
+                if (i + 2 == u.n) commit_by(lead, bar(Y::bQEmpty));  // the last scores are issued: Q may change after them
+            }
             ++qn;
         }
-        mma_commit(bar(Y::bDrain));
+        commit_by(lead, bar(Y::bDrain));
         wait_drain(bar(Y::bDrain), 0);
     }
 
-    // ---- softmax of query tile q ------------------------------------------------
-    __device__ void softmax(int q) {
+    // ---- softmax of query tile q, the keys' half h ----------------------------------
+    // Two threads share a row.  Each leaves a number for the other: what they agree on next.
+    __device__ __forceinline__ bool swap(int q, int h, float &mine, float &other, unsigned &n) const {
+        const int row = threadIdx.x & 127, pairs = q * 4 + (row >> 5);
+        float *box = reinterpret_cast<float *>(x.gbase + Y::kBox) + q * 256;
+        box[h * 128 + row] = mine;
+        warp_arrive(bar(Y::bPair + pairs));
+        if (!hold(x, bar(Y::bPair + pairs), n & 1)) return false;
+        ++n;
+        other = box[(h ^ 1) * 128 + row];
+        return true;
+    }
+
+    static __device__ __forceinline__ void hide(uint32_t (&s)[16], uint32_t mask) {  // what a row does not see
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[e] = mask >> e & 1 ? s[e] : 0xff800000u;
+    }
+
+    __device__ void softmax(int q, int h) {
         const int warp = threadIdx.x >> 5, row = threadIdx.x & 127;
-        const uint32_t ts = lane_base(tm, warp) + Y::tS + 128 * q, to = lane_base(tm, warp) + Y::tO + D * q;
+        const uint32_t ts = lane_base(tm, warp) + Y::tS + 128 * q + 64 * h, to = lane_base(tm, warp) + Y::tO + D * q + D / 2 * h;
+        volatile float *wish = reinterpret_cast<float *>(x.gbase + Y::kWish) + q * 256 + row;
         const float c = p.scale * kLog2e;
         const Sight sight{p.window, p.sinks};
-        unsigned ns = 0, no = 0;
+        unsigned ns = 0, no = 0, nx = 0;
         for (unsigned item = blockIdx.x; item < items; item += gridDim.x) {
             Plan u;
             if (!plan(u, p, item, slots)) continue;
-            if (!u.act[q]) continue;
-            const int t = u.t0[q] + row;
-            float m = -CUDART_INF_F, l = 0.f;  // maximum of the raw scores that O is scaled by; sum of the weights
-            bool first = true;
-            for (int i = 0; i < u.n; ++i) {
-                if (!u.takes(q, i)) continue;
-                const int k0 = u.tile(i) * 128;
-                if (!wwait(x, bar(Y::bS + q), ns & 1)) return;
+            const Span v = q ? u.q1 : u.q0;
+            if (!v.act) continue;
+            const int t = v.t0 + row;
+            // what weights are relative to, times log2 e scale: -infinity until the row has seen a key; sum of the weights
+            float m = -CUDART_INF_F, l = 0.f;
+            for (int i = v.zero ? 0 : v.from; i <= v.to; i = i + 1 < v.from ? v.from : i + 1) {
+                const int k0 = u.tile(i) * 128 + 64 * h;
+                const int groups = u.small(i) ? 2 - 2 * h : 4;  // of 16 keys
+                // some row of the tile does not see some key of it
+                const bool edge = k0 + 63 > v.t0 || v.t0 + 127 - k0 >= p.window;
+                if (!hold(x, bar(Y::bS + q), ns & 1)) return;
                 ++ns;
                 tc_fence_after();
-                uint32_t s[4][32];
-                const int parts = u.small(i) ? 1 : 4;
+                uint32_t s[2][16];
+                if (__any_sync(0xffffffffu, m == -CUDART_INF_F)) {
+                    // the first tile that a row sees: its maximum
+                    float top = -CUDART_INF_F, other;
+                    for (int g = 0; g < groups; ++g) {
+                        tmem_ld16(ts + 16 * g, s[0]);
+                        tmem_wait_ld_dep16(s[0]);
+                        if (edge) hide(s[0], seen32(t, k0 + 16 * g, sight));
 #pragma unroll
-                for (int g = 0; g < 4; ++g)
-                    if (g < parts) tmem_ld32(ts + 32 * g, s[g]);
-                tmem_wait_ld();
-#pragma unroll
-                for (int g = 0; g < 4; ++g) tmem_ld_dep(s[g]);
-                // some row of the tile does not see some key of it
-                const bool edge = k0 + 127 > u.t0[q] || u.t0[q] + 127 - k0 >= p.window;
-                float top = -CUDART_INF_F;
-#pragma unroll
-                for (int g = 0; g < 4; ++g)
-                    if (g < parts) {
-                        if (edge) {
-                            const uint32_t mask = seen32(t, k0 + 32 * g, sight);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                s[g][e] = mask >> e & 1 ? s[g][e] : 0xff800000u;
-                        }
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2)
-                            top = fmaxf(top, fmaxf(__uint_as_float(s[g][e]), __uint_as_float(s[g][e + 1])));
+                        for (int e = 0; e < 16; e += 2) top = max3(top, __uint_as_float(s[0][e]), __uint_as_float(s[0][e + 1]));
                     }
-                if ((top - m) * c > 8.f || m == -CUDART_INF_F) {
-                    const float f = ex2((m - top) * c);  // 0 where there was no maximum
-                    const bool scale = !first && m != -CUDART_INF_F;
-                    m = top;
-                    if (scale) l *= f;
-                    top = scale ? f : 1.f;
+                    if (!swap(q, h, top, other, nx)) return;
+                    if (m == -CUDART_INF_F) {
+                        m = fmaxf(top, other) * c;
+                        wish[128 * h] = m;
+                    }
                 } else {
-                    top = 1.f;
-                }
-                if (__any_sync(0xffffffffu, top != 1.f)) {
+                    const float want = fmaxf(wish[0], wish[128]);
+                    if (__any_sync(0xffffffffu, want > m)) {
+                        const float f = want > m ? ex2(m - want) : 1.f;
+                        m = want > m ? want : m;
+                        l *= f;
 #pragma unroll
-                    for (int g = 0; g < D / 16; ++g) {
-                        uint32_t o[16];
-                        tmem_ld16(to + 16 * g, o);
-                        tmem_wait_ld_dep16(o);
+                        for (int g = 0; g < D / 32; ++g) {
+                            tmem_ld16(to + 16 * g, s[0]);
+                            tmem_wait_ld_dep16(s[0]);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * top);
-                        tmem_st16(to + 16 * g, o);
+                            for (int e = 0; e < 16; ++e) s[0][e] = __float_as_uint(__uint_as_float(s[0][e]) * f);
+                            tmem_st16(to + 16 * g, s[0]);
+                        }
                     }
                 }
-                first = false;
-                const float mc = m == -CUDART_INF_F ? 0.f : -m * c;
-                const f2 cc = both(c), mm = both(mc);
+                const f2 cc = both(c), mm = both(m == -CUDART_INF_F ? 0.f : -m);
                 f2 sum[2] = {0ull, 0ull};
+                // P lies over scores that are read by then
+                if (groups) tmem_ld16(ts, s[0]);
 #pragma unroll
                 for (int g = 0; g < 4; ++g)
-                    if (g < parts) {
-                        uint32_t w[16];
+                    if (g < groups) {
+                        tmem_wait_ld_dep16(s[g & 1]);
+                        if (g + 1 < groups) tmem_ld16(ts + 16 * (g + 1), s[~g & 1]);
+                        if (edge) hide(s[g & 1], seen32(t, k0 + 16 * g, sight));
+                        uint32_t w[8];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
+                        for (int e = 0; e < 16; e += 2) {
                             float a, b;
-                            split(fma2(pair(__uint_as_float(s[g][e]), __uint_as_float(s[g][e + 1])), cc, mm), a, b);
+                            split(fma2(pair(__uint_as_float(s[g & 1][e]), __uint_as_float(s[g & 1][e + 1])), cc, mm), a, b);
                             a = ex2(a);
                             b = ex2(b);
                             sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pair(a, b));
                             w[e / 2] = pack_bf16(a, b);
                         }
-                        tmem_st16(ts + 16 * g, w);
+                        tmem_st8(ts + 8 * g, w);
                     }
-                l += sum_of(add2(sum[0], sum[1]));
+                const float part = sum_of(add2(sum[0], sum[1]));
+                l += part;
+                if (part > kGrown) wish[128 * h] = m + log2f(part);
                 tmem_wait_st();
                 tc_fence_before();
                 warp_arrive(bar(Y::bP + q));
             }
-            if (!wwait(x, bar(Y::bO + q), no & 1)) return;
+            if (!hold(x, bar(Y::bO + q), no & 1)) return;
             ++no;
             tc_fence_after();
+            float other;
+            if (!swap(q, h, l, other, nx)) return;
+            l += other;
             const float f = 1.f / l;
-            bool nan = false;
-            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.o) + ((u.bos + t) * p.Nq + u.h[q]) * D;
+            const long long at = (u.bos + t) * p.Nq + v.h;
+            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.o) + at * D + D / 2 * h;
+            float bad = 0.f;
+            uint32_t s[2][16];
+            tmem_ld16(to, s[0]);
 #pragma unroll
-            for (int g = 0; g < D / 64; ++g) {
-                uint32_t o[2][32];
-                tmem_ld32(to + 64 * g, o[0]);
-                tmem_ld32(to + 64 * g + 32, o[1]);
-                tmem_wait_ld();
-                tmem_ld_dep(o[0]);
-                tmem_ld_dep(o[1]);
-                if (g + 1 == D / 64) {  // all of O is read
-                    tc_fence_before();
-                    warp_arrive(bar(Y::bOEmpty + q));
+            for (int g = 0; g < D / 32; ++g) {
+                tmem_wait_ld_dep16(s[g & 1]);
+                if (g + 1 < D / 32) tmem_ld16(to + 16 * (g + 1), s[~g & 1]);
+                uint32_t w[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float a = __uint_as_float(s[g & 1][2 * e]) * f, b = __uint_as_float(s[g & 1][2 * e + 1]) * f;
+                    if (isnan(a) | isnan(b)) bad = 1.f;
+                    w[e] = pack_bf16(a, b);
                 }
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    uint32_t w[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float a = __uint_as_float(o[h / 2][(h & 1) * 16 + 2 * e]) * f;
-                        const float b = __uint_as_float(o[h / 2][(h & 1) * 16 + 2 * e + 1]) * f;
-                        nan |= isnan(a) | isnan(b);
-                        w[e] = pack_bf16(a, b);
-                    }
-                    if (t < u.L) store32(out + 64 * g + 16 * h, w);
-                }
+                if (t < u.L) store32(out + 16 * g, w);
             }
-            if (t < u.L) p.lse[(u.bos + t) * p.Nq + u.h[q]] = nan ? redo_mark() : m * p.scale + log2f(l) * 0.6931471805599453f;
+            tc_fence_before();
+            warp_arrive(bar(Y::bOEmpty + q));
+            if (!swap(q, h, bad, other, nx)) return;
+            if (h == 0 && t < u.L)
+                p.lse[at] = bad + other == 0.f && l < CUDART_INF_F ? (m + log2f(l)) * 0.6931471805599453f : redo_mark();
         }
     }
 };
@@ -385,22 +391,21 @@ window_fwd(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
         mbar_init(bar(Y::bQFull), 1);
         mbar_init(bar(Y::bQEmpty), 1);
         for (int s = 0; s < Y::NS; ++s) {
-            mbar_init(bar(Y::bKFull + s), 1);
-            mbar_init(bar(Y::bKEmpty + s), 2);  // both query tiles
-            mbar_init(bar(Y::bVFull + s), 1);
-            mbar_init(bar(Y::bVEmpty + s), 1);
+            mbar_init(bar(Y::bFull + s), 1);
+            mbar_init(bar(Y::bEmpty + s), 1);
         }
         for (int q = 0; q < 2; ++q) {
             mbar_init(bar(Y::bS + q), 1);
-            mbar_init(bar(Y::bP + q), 4);
+            mbar_init(bar(Y::bP + q), 8);
             mbar_init(bar(Y::bO + q), 1);
-            mbar_init(bar(Y::bOEmpty + q), 4);
+            mbar_init(bar(Y::bOEmpty + q), 8);
         }
+        for (int i = 0; i < 8; ++i) mbar_init(bar(Y::bPair + i), 2);
         mbar_init(bar(Y::bDrain), 1);
         *x.abort_flag = 0;
         fence_barrier_init();
     }
-    if (warp == 9) {
+    if (warp == 17) {
         tmem_alloc(x.base + Y::kMisc, Y::kCols);
         tmem_relinquish();
     }
@@ -410,21 +415,20 @@ window_fwd(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
     tc_fence_after();
     Fwd<D> f{x, p, items, slots, *reinterpret_cast<volatile uint32_t *>(x.gbase + Y::kMisc)};
     wait_for_launches();
-    if (warp == 8) {
+    if (warp == 16) {
         if (blockIdx.x == 0) check_offsets(p.seq, threadIdx.x & 31, 32);
         __syncwarp();
         if ((threadIdx.x & 31) == 0) f.load(&mq, &mk, &mv, &mks, &mvs);
         __syncwarp();
-    } else if (warp == 9) {
-        if ((threadIdx.x & 31) == 0) f.mma();
-        __syncwarp();
+    } else if (warp == 17) {
+        f.mma();
     } else {
-        f.softmax(warp >> 2);
+        f.softmax(warp >> 3, warp >> 2 & 1);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 9) tmem_dealloc(f.tm, Y::kCols);
+    if (warp == 17) tmem_dealloc(f.tm, Y::kCols);
 }
 
 template <int D>

@@ -26,10 +26,76 @@ __device__ __forceinline__ uint32_t seen32(int t, int k0, const Sight &s) {
     return bit_range(hi - s.window + 1, hi) | bit_range(0, lim);
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 __device__ __forceinline__ void store32(void *dst, const uint32_t (&r)[8]) {  // 32 bytes at once
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(r[0]), "r"(r[1]), "r"(r[2]),
                  "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
+}
+
+// Wait of a whole warp, bounded like wwait of dn_tc_sync.cuh but without a call: what is in
+// registers stays there.
+__device__ __forceinline__ bool hold(const tcs::Ctx &x, uint32_t bar, uint32_t parity) {
+    if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
+    const uint64_t t0 = ptx::globaltimer();
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+            if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
+        const bool late = ptx::globaltimer() - t0 > tcs::kTimeoutNs;
+        if (late) {
+            *x.abort_flag = 1;
+            atomicOr(x.status, kStatusTimeout);
+        }
+        if (__any_sync(0xffffffffu, late || *x.abort_flag)) return false;
+    }
+}
+
+// ---- MMAs of a whole warp ---------------------------------------------------
+// One lane of a converged warp issues; the others run along, so that loops, waits and descriptors
+// stay warp-uniform (a branch of one thread made every MMA take about 115 cycles to issue; it takes
+// as long as the tensor cores need).
+
+__device__ __forceinline__ uint32_t elect() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
+// Descriptors of swizzled rows by their halves: the upper one is the same for all (8 rows 1024 bytes apart,
+// version 1, 128-byte swizzle), the lower one holds the address in units of 16 bytes, to which
+// steps are added.  rows_of: operands read along their rows; cols_of: along their columns, panels of 64 of
+// them 16 KB apart.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (ptx::kSwizzle128 << 29);
+__device__ __forceinline__ uint32_t rows_of(uint32_t at) { return ((at & 0x3FFFFu) >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t cols_of(uint32_t at) { return ((at & 0x3FFFFu) >> 4) | ((16384u >> 4) << 16); }
+
+__device__ __forceinline__ void mma_ss_by(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t more) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "mov.b64 x, {%1, %6};\n\tmov.b64 y, {%2, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(more), "r"(lead), "r"(kDescHi)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts_by(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t more) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "mov.b64 y, {%2, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(more), "r"(lead), "r"(kDescHi)
+        : "memory");
+}
+__device__ __forceinline__ void commit_by(uint32_t lead, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(lead)
+        : "memory");
 }
 
 }  // namespace dn
