@@ -36,6 +36,8 @@ using namespace tcs;
 
 constexpr int kThreads = 576;
 
+constexpr int kPlans = 4;  // items whose plans are kept
+
 template <int D>
 struct Lay {
     static constexpr uint32_t kPanel = 128 * 128;            // 128 rows of 64 columns
@@ -44,8 +46,8 @@ struct Lay {
     static constexpr uint32_t kQ = 0, kK = 2 * kTile, kV = kK + NS * kTile, kBar = kV + NS * kTile;
     // barriers
     static constexpr int bQFull = 0, bQEmpty = 1, bFull = 2, bEmpty = bFull + NS, bS = bEmpty + NS, bP = bS + 2, bO = bP + 2,
-                         bOEmpty = bO + 2, bDrain = bOEmpty + 2, bPair = bDrain + 1, kBars = bPair + 8;
-    static constexpr uint32_t kBox = (kBar + 8 * kBars + 15) / 16 * 16, kWish = kBox + 2 * 2 * 128 * 4, kMisc = kWish + 2 * 2 * 128 * 4, kAlloc = kMisc + 16 + 1024;
+                         bOEmpty = bO + 2, bDrain = bOEmpty + 2, bPair = bDrain + 1, bPlan = bPair + 8, kBars = bPlan + kPlans;
+    static constexpr uint32_t kBox = (kBar + 8 * kBars + 15) / 16 * 16, kWish = kBox + 2 * 2 * 2 * 128 * 4, kPlan = kWish + 2 * 2 * 128 * 4, kMisc = kPlan + kPlans * 96, kAlloc = kMisc + 16 + 1024;
     static_assert(kAlloc <= 232448, "exceeds the 227 KB of shared memory per CTA");
     // tensor memory columns
     static constexpr uint32_t tS = 0, tO = 256, kCols = 512;
@@ -63,12 +65,12 @@ struct Span {
     bool zero, act;
     __device__ __forceinline__ bool has(int i) const { return i == 0 ? zero : i >= from && i <= to; }
 };
-struct Plan {
+struct __align__(16) Plan {
+    Span q0, q1;
     long long bos;
     int L, hk;
-    Span q0, q1;
+    int lo, n;          // place i holds key tile lo + i (but the sinks' at 0); length of the list (0: no item is left)
     bool sink, narrow;  // the list begins with the sinks' tile; as kSinkCols keys
-    int lo, n;          // place i holds key tile lo + i (but the sinks' at 0); length of the list
     __device__ __forceinline__ int tile(int i) const { return sink && i == 0 ? 0 : lo + i; }
     __device__ __forceinline__ bool small(int i) const { return narrow && i == 0; }
 };
@@ -115,6 +117,8 @@ __device__ __forceinline__ bool plan(Plan &u, const WindowParams &p, unsigned it
     return true;
 }
 
+static_assert(sizeof(Plan) <= 96, "a plan's place in shared memory");
+
 template <int D>
 struct Fwd {
     using Y = Lay<D>;
@@ -126,6 +130,18 @@ struct Fwd {
 
     __device__ __forceinline__ uint32_t bar(int i) const { return x.base + Y::kBar + 8u * i; }
 
+    // ---- plans ----------------------------------------------------------------
+    // The TMA warp works them out (a few hundred cycles of divisions and look-ups, and code that the other
+    // roles would fetch anew for every item: 3000 cycles an item each) and leaves the n-th item's in
+    // shared memory.  It writes plan n when all scores of item n - 1 are issued, when every other
+    // warp is past item n - 4, whose place it takes.
+    __device__ __forceinline__ Plan *place(unsigned n) const { return reinterpret_cast<Plan *>(x.gbase + Y::kPlan + n % kPlans * 96); }
+    __device__ __forceinline__ bool next_plan(const Plan *&u, unsigned n) const {
+        if (!hold(x, bar(Y::bPlan + n % kPlans), n / kPlans & 1)) return false;
+        u = place(n);
+        return u->n > 0;
+    }
+
     // ---- TMA ------------------------------------------------------------------
     // Keys and values come in units: the keys of place 0; the values of place i with the keys
     // of place i + 1.
@@ -133,10 +149,14 @@ struct Fwd {
                          const CUtensorMap *mvs) {
         unsigned un = 0, qn = 0;
         bool fine = true;
-        for (unsigned item = blockIdx.x; fine && item < items; item += gridDim.x) {
+        for (unsigned item = blockIdx.x; fine; item += gridDim.x) {
             Plan u;
-            if (!plan(u, p, item, slots)) continue;
-            if (!wait(x, bar(Y::bQEmpty), (qn & 1) ^ 1)) break;
+            if (item >= items) u.n = 0;
+            else if (!plan(u, p, item, slots)) continue;
+            if (!(fine = wait(x, bar(Y::bQEmpty), (qn & 1) ^ 1))) break;
+            *place(qn) = u;
+            mbar_arrive(bar(Y::bPlan + qn % kPlans));
+            if (u.n == 0) break;
             mbar_arrive_expect_tx(bar(Y::bQFull), u.q1.act ? 2 * Y::kTile : Y::kTile);
             for (int c = 0; c < D / 64; ++c) {
                 tma_load_3d(x.base + Y::kQ + c * Y::kPanel, mq, bar(Y::bQFull), 64 * c, u.q0.h, (int)(u.bos + u.q0.t0));
@@ -195,9 +215,8 @@ struct Fwd {
         const uint32_t lead = elect();
         unsigned un = 0, qn = 0, ns[2] = {0, 0}, no[2] = {0, 0};
         bool fine = true;
-        for (unsigned item = blockIdx.x; fine && item < items; item += gridDim.x) {
-            Plan u;
-            if (!plan(u, p, item, slots)) continue;
+        for (const Plan *next; fine && next_plan(next, qn);) {
+            const Plan u = *next;
             if (!(fine = hold(x, bar(Y::bQFull), qn & 1) && hold(x, bar(Y::bFull + un % Y::NS), (un / Y::NS) & 1))) break;
             tc_fence_after();
             if (u.q0.zero) issue_s(lead, 0, un, u.small(0));
@@ -237,10 +256,11 @@ struct Fwd {
     }
 
     // ---- softmax of query tile q, the keys' half h ----------------------------------
-    // Two threads share a row.  Each leaves a number for the other: what they agree on next.
+    // Two threads share a row.  Each leaves a number for the other: what they agree on next.  Two boxes in turn: the
+    // other thread may not have read the last one yet, but it has read the one before.
     __device__ __forceinline__ bool swap(int q, int h, float &mine, float &other, unsigned &n) const {
         const int row = threadIdx.x & 127, pairs = q * 4 + (row >> 5);
-        float *box = reinterpret_cast<float *>(x.gbase + Y::kBox) + q * 256;
+        volatile float *box = reinterpret_cast<float *>(x.gbase + Y::kBox) + (n & 1) * 512 + q * 256;
         box[h * 128 + row] = mine;
         warp_arrive(bar(Y::bPair + pairs));
         if (!hold(x, bar(Y::bPair + pairs), n & 1)) return false;
@@ -260,18 +280,20 @@ struct Fwd {
         volatile float *wish = reinterpret_cast<float *>(x.gbase + Y::kWish) + q * 256 + row;
         const float c = p.scale * kLog2e;
         const Sight sight{p.window, p.sinks};
-        unsigned ns = 0, no = 0, nx = 0;
-        for (unsigned item = blockIdx.x; item < items; item += gridDim.x) {
-            Plan u;
-            if (!plan(u, p, item, slots)) continue;
+        unsigned ns = 0, no = 0, nx = 0, qn = 0;
+        for (const Plan *next; next_plan(next, qn); ++qn) {
+            const Plan &u = *next;
             const Span v = q ? u.q1 : u.q0;
             if (!v.act) continue;
+            const int lo = u.lo, L = u.L;
+            const bool sink = u.sink, narrow = u.narrow;
+            const long long bos = u.bos;
             const int t = v.t0 + row;
             // what weights are relative to, times log2 e scale: -infinity until the row has seen a key; sum of the weights
             float m = -CUDART_INF_F, l = 0.f;
             for (int i = v.zero ? 0 : v.from; i <= v.to; i = i + 1 < v.from ? v.from : i + 1) {
-                const int k0 = u.tile(i) * 128 + 64 * h;
-                const int groups = u.small(i) ? 2 - 2 * h : 4;  // of 16 keys
+                const int k0 = (sink && i == 0 ? 0 : lo + i) * 128 + 64 * h;
+                const int groups = narrow && i == 0 ? 2 - 2 * h : 4;  // of 16 keys
                 // some row of the tile does not see some key of it
                 const bool edge = k0 + 63 > v.t0 || v.t0 + 127 - k0 >= p.window;
                 if (!hold(x, bar(Y::bS + q), ns & 1)) return;
@@ -345,7 +367,7 @@ struct Fwd {
             if (!swap(q, h, l, other, nx)) return;
             l += other;
             const float f = 1.f / l;
-            const long long at = (u.bos + t) * p.Nq + v.h;
+            const long long at = (bos + t) * p.Nq + v.h;
             __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.o) + at * D + D / 2 * h;
             float bad = 0.f;
             uint32_t s[2][16];
@@ -353,7 +375,12 @@ struct Fwd {
 #pragma unroll
             for (int g = 0; g < D / 32; ++g) {
                 tmem_wait_ld_dep16(s[g & 1]);
-                if (g + 1 < D / 32) tmem_ld16(to + 16 * (g + 1), s[~g & 1]);
+                if (g + 1 < D / 32) {
+                    tmem_ld16(to + 16 * (g + 1), s[~g & 1]);
+                } else {  // all of O is read
+                    tc_fence_before();
+                    warp_arrive(bar(Y::bOEmpty + q));
+                }
                 uint32_t w[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -361,12 +388,10 @@ struct Fwd {
                     if (isnan(a) | isnan(b)) bad = 1.f;
                     w[e] = pack_bf16(a, b);
                 }
-                if (t < u.L) store32(out + 16 * g, w);
+                if (t < L) store32(out + 16 * g, w);
             }
-            tc_fence_before();
-            warp_arrive(bar(Y::bOEmpty + q));
             if (!swap(q, h, bad, other, nx)) return;
-            if (h == 0 && t < u.L)
+            if (h == 0 && t < L)
                 p.lse[at] = bad + other == 0.f && l < CUDART_INF_F ? (m + log2f(l)) * 0.6931471805599453f : redo_mark();
         }
     }
@@ -401,6 +426,7 @@ window_fwd(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
             mbar_init(bar(Y::bOEmpty + q), 8);
         }
         for (int i = 0; i < 8; ++i) mbar_init(bar(Y::bPair + i), 2);
+        for (int i = 0; i < kPlans; ++i) mbar_init(bar(Y::bPlan + i), 1);
         mbar_init(bar(Y::bDrain), 1);
         *x.abort_flag = 0;
         fence_barrier_init();
