@@ -303,6 +303,7 @@ struct Fwd {
                 if (__any_sync(0xffffffffu, m == -CUDART_INF_F)) {
                     // the first tile that a row sees: its maximum
                     float top = -CUDART_INF_F, other;
+#pragma unroll 1
                     for (int g = 0; g < groups; ++g) {
                         tmem_ld16(ts + 16 * g, s[0]);
                         tmem_wait_ld_dep16(s[0]);
@@ -321,7 +322,7 @@ struct Fwd {
                         const float f = want > m ? ex2(m - want) : 1.f;
                         m = want > m ? want : m;
                         l *= f;
-#pragma unroll
+#pragma unroll 1
                         for (int g = 0; g < D / 32; ++g) {
                             tmem_ld16(to + 16 * g, s[0]);
                             tmem_wait_ld_dep16(s[0]);
@@ -333,29 +334,32 @@ struct Fwd {
                 }
                 const f2 cc = both(c), mm = both(m == -CUDART_INF_F ? 0.f : -m);
                 f2 sum[2] = {0ull, 0ull};
-                // P lies over scores that are read by then
+                // P lies over scores that are read by then.  Two groups a round, not all four unrolled: an item's code
+                // that does not stay in the instruction cache costs more than the loop.
                 if (groups) tmem_ld16(ts, s[0]);
+#pragma unroll 1
+                for (int r = 0; r < groups; r += 2) {
 #pragma unroll
-                for (int g = 0; g < 4; ++g)
-                    if (g < groups) {
-                        tmem_wait_ld_dep16(s[g & 1]);
-                        if (g + 1 < groups) tmem_ld16(ts + 16 * (g + 1), s[~g & 1]);
-                        if (edge) hide(s[g & 1], seen32(t, k0 + 16 * g, sight));
+                    for (int g = 0; g < 2; ++g) {
+                        tmem_wait_ld_dep16(s[g]);
+                        if (g == 0 || r + 2 < groups) tmem_ld16(ts + 16 * (r + g + 1), s[g ^ 1]);
+                        if (edge) hide(s[g], seen32(t, k0 + 16 * (r + g), sight));
                         uint32_t w[8];
 #pragma unroll
                         for (int e = 0; e < 16; e += 2) {
                             float a, b;
-                            split(fma2(pair(__uint_as_float(s[g & 1][e]), __uint_as_float(s[g & 1][e + 1])), cc, mm), a, b);
+                            split(fma2(pair(__uint_as_float(s[g][e]), __uint_as_float(s[g][e + 1])), cc, mm), a, b);
                             a = ex2(a);
                             b = ex2(b);
                             sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pair(a, b));
                             w[e / 2] = pack_bf16(a, b);
                         }
-                        tmem_st8(ts + 8 * g, w);
+                        tmem_st8(ts + 8 * (r + g), w);
                     }
+                }
                 const float part = sum_of(add2(sum[0], sum[1]));
                 l += part;
-                if (part > kGrown) wish[128 * h] = m + log2f(part);
+                if (part > kGrown) wish[128 * h] = m + lg2(part);
                 tmem_wait_st();
                 tc_fence_before();
                 warp_arrive(bar(Y::bP + q));
@@ -366,7 +370,7 @@ struct Fwd {
             float other;
             if (!swap(q, h, l, other, nx)) return;
             l += other;
-            const float f = 1.f / l;
+            const float f = rcp(l);
             const long long at = (bos + t) * p.Nq + v.h;
             __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.o) + at * D + D / 2 * h;
             float bad = 0.f;
@@ -392,7 +396,7 @@ struct Fwd {
             }
             if (!swap(q, h, bad, other, nx)) return;
             if (h == 0 && t < L)
-                p.lse[at] = bad + other == 0.f && l < CUDART_INF_F ? (m + log2f(l)) * 0.6931471805599453f : redo_mark();
+                p.lse[at] = bad + other == 0.f && l < CUDART_INF_F ? (m + lg2(l)) * 0.6931471805599453f : redo_mark();
         }
     }
 };

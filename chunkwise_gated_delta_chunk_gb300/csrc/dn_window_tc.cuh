@@ -26,6 +26,13 @@ __device__ __forceinline__ uint32_t seen32(int t, int k0, const Sight &s) {
     return bit_range(hi - s.window + 1, hi) | bit_range(0, lim);
 }
 
+// log2 x; off by 2^-22 at most where x is between 1 and 2, else by two units of fp32's last place
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
