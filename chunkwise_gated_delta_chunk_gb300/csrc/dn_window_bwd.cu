@@ -7,10 +7,11 @@
 //
 // Two kernels, so that no sum is added by atomics: 7 products of 128 x 128 x d a tile
 // instead of 5, but every sum stays in tensor memory until it is done, in a fixed order.
-// window_dq computes D of its rows (from o and do) and leaves it for window_dkv.
+// window_dq computes D of its rows (from the tiles of o and do in shared memory) and leaves it for
+// window_dkv.
 //
 // Warps 0-3 and 4-7: the first and the second 64 columns of every tile of scores, one row a
-// thread; warp 8: TMA loads; warp 9: issues the MMAs (one thread); warp 10 (window_dkv): the
+// thread; warp 8: TMA loads, and the plans of the items; warp 9: the MMAs; warp 10 (window_dkv): the
 // columns' lse and D into shared memory.
 //
 // window_dq, tensor memory: S, dP (128 columns each), dQ (d), dS as bf16 (2 x 64).  As soon as
@@ -34,39 +35,57 @@ using namespace tcs;
 constexpr int kThreads = 352;
 constexpr uint32_t kPanel = 128 * 128;  // 128 rows of 64 columns of bf16
 
-// Shared memory of both kernels: two tiles that stay, and two stages of two that stream by.
-template <int D>
+constexpr int kPlans = 4;  // items whose plans are kept
+
+// Shared memory of both kernels: the tiles that stay (three in window_dq: q, do, o; two in window_dkv: k,
+// v), and stages of two that stream by.
+template <int D, int HELD>
 struct Lay {
     static constexpr uint32_t kTile = (D / 64) * kPanel;
     static constexpr int NS = D == 64 ? 4 : 2;
-    static constexpr uint32_t kA = 0, kB = kTile, kX = 2 * kTile, kY = kX + NS * kTile, kCols = kY + NS * kTile;
-    static constexpr uint32_t kBar = kCols + NS * 1024;  // lse and D of the stage's queries before it
+    static constexpr uint32_t kA = 0, kB = kTile, kC = 2 * kTile, kX = HELD * kTile, kY = kX + NS * kTile, kEnd = kY + NS * kTile;
+    static constexpr uint32_t kCols = kEnd;  // window_dkv: lse and D of a stage's queries
+    static constexpr uint32_t kPlan = kCols + (HELD == 2 ? NS * 1024 : 0), kBar = kPlan + kPlans * 64;
     static constexpr int bHold = 0, bHoldEmpty = 1, bFull = 2, bEmpty = bFull + NS, bCol = bEmpty + NS, bS = bCol + NS, bDP = bS + 1,
-                         bP = bDP + 1, bDS = bP + 1, bOut = bDS + 1, bOutEmpty = bOut + 1, bDrain = bOutEmpty + 1, kBars = bDrain + 1;
+                         bP = bDP + 1, bDS = bP + 1, bOut = bDS + 1, bOutEmpty = bOut + 1, bPlan = bOutEmpty + 1, bDrain = bPlan + kPlans,
+                         kBars = bDrain + 1;
     static constexpr uint32_t kMisc = kBar + 8 * kBars, kAlloc = kMisc + 16 + 1024;
     static_assert(kAlloc <= 232448, "exceeds the 227 KB of shared memory per CTA");
 };
 
-template <int D>
+template <int D, int HELD, typename Plan>
 struct Base {
-    using Y = Lay<D>;
+    using Y = Lay<D, HELD>;
+    static_assert(sizeof(Plan) <= 64, "a plan's place in shared memory");
     Ctx x;
     const WindowParams &p;
     uint32_t tm;
     __device__ __forceinline__ uint32_t bar(int i) const { return x.base + Y::kBar + 8u * i; }
 
+    // The TMA warp works out the plans and leaves the n-th item's in shared memory: when all scores of
+    // item n - 1 are done, and every other warp is past item n - 4, whose place it takes.  A plan of
+    // no rounds: no item is left.
+    __device__ __forceinline__ void put_plan(const Plan &u, unsigned n) const {
+        *reinterpret_cast<Plan *>(x.gbase + Y::kPlan + n % kPlans * 64) = u;
+        mbar_arrive(bar(Y::bPlan + n % kPlans));
+    }
+    __device__ __forceinline__ bool next_plan(Plan &u, unsigned n) const {
+        if (!hold(x, bar(Y::bPlan + n % kPlans), n / kPlans & 1)) return false;
+        u = *reinterpret_cast<const Plan *>(x.gbase + Y::kPlan + n % kPlans * 64);
+        return u.rounds > 0;
+    }
     // rows of 128 x D by panels
     __device__ __forceinline__ void tma_tile(uint32_t at, const CUtensorMap *m, uint32_t b, int head, int row) const {
         for (int c = 0; c < D / 64; ++c) tma_load_3d(x.base + at + c * kPanel, m, b, 64 * c, head, row);
     }
     // C[128 x n] = A[128 x D] B[n x D]^T, both rows in shared memory
-    __device__ __forceinline__ void mma_rows(uint32_t c, uint32_t a, uint32_t b, uint32_t id) const {
+    __device__ __forceinline__ void mma_rows(uint32_t lead, uint32_t c, uint32_t at_a, uint32_t at_b, uint32_t id) const {
+        const uint32_t a = rows_of(x.base + at_a), b = rows_of(x.base + at_b);
 #pragma unroll
         for (int s = 0; s < D / 64; ++s)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-                mma_ss(tm + c, sdesc(x.base + a + s * kPanel + kk * 32, 16, 1024), sdesc(x.base + b + s * kPanel + kk * 32, 16, 1024), id,
-                       (s | kk) != 0);
+                mma_ss_by(lead, tm + c, a + (s * kPanel + kk * 32) / 16, b + (s * kPanel + kk * 32) / 16, id, (s | kk) != 0);
     }
     // the warp's byte in the mark of its half of the rows (two warps of each column half)
     __device__ __forceinline__ void mark(bool nan, long long flag) const {
@@ -75,14 +94,16 @@ struct Base {
         unsigned char *m = reinterpret_cast<unsigned char *>(p.redo + flag + (warp >> 1 & 1) * (p.Nq + p.Nk));
         if ((threadIdx.x & 31) == 0) m[2 * (warp >> 2) + (warp & 1)] = nan;
     }
-    // 64 columns of a row of an accumulator times f, to bf16; true where a NaN is among them
-    __device__ __forceinline__ bool store64(uint32_t from, __nv_bfloat16 *to, float f, bool write) const {
+    // 64 columns of a row of an accumulator times f, to bf16; true where a NaN is among them.  done(): they are read
+    template <typename F>
+    __device__ __forceinline__ bool store64(uint32_t from, __nv_bfloat16 *to, float f, bool write, F done) const {
         uint32_t o[2][32];
         tmem_ld32(from, o[0]);
         tmem_ld32(from + 32, o[1]);
         tmem_wait_ld();
         tmem_ld_dep(o[0]);
         tmem_ld_dep(o[1]);
+        done();
         bool nan = false;
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
@@ -102,10 +123,19 @@ struct Base {
 
 // ---- dq -------------------------------------------------------------------------
 
+struct QueryPlan {
+    long long bos, flag;
+    int L, h, hk, t0, rounds;
+    KeyTiles kt;
+    bool narrow;
+    __device__ __forceinline__ bool small(int i) const { return narrow && i == 0; }
+};
+
 template <int D>
-struct Dq : Base<D> {
-    using Y = Lay<D>;
-    using B = Base<D>;
+struct Dq : Base<D, 3, QueryPlan> {
+    using B = Base<D, 3, QueryPlan>;
+    using Y = typename B::Y;
+    using Plan = QueryPlan;
     using B::bar;
     using B::p;
     using B::tm;
@@ -114,13 +144,6 @@ struct Dq : Base<D> {
     long long slots;
     static constexpr uint32_t tS = 0, tDP = 128, tDQ = 256, tDS = 384;
 
-    struct Plan {
-        long long bos, flag;
-        int L, h, hk, t0;
-        KeyTiles kt;
-        bool narrow;
-        __device__ __forceinline__ bool small(int i) const { return narrow && i == 0; }
-    };
     // late tiles first: under a causal mask these are the long ones
     __device__ __forceinline__ bool plan(Plan &u, unsigned item) const {
         u.h = item % p.Nq;
@@ -134,22 +157,31 @@ struct Dq : Base<D> {
         u.t0 = (int)(s.t0 - s.bos);
         u.kt = KeyTiles(u.t0, (int)(s.t1 - s.bos), 128, Sight{p.window, p.sinks});
         u.narrow = u.kt.sink_end > 0 && p.sinks <= kSinkCols;
+        u.rounds = u.kt.count();
         return true;
     }
 
-    __device__ void load(const CUtensorMap *mq, const CUtensorMap *mg, const CUtensorMap *mk, const CUtensorMap *mv,
-                         const CUtensorMap *mks, const CUtensorMap *mvs) {
+    __device__ void load(const CUtensorMap *mq, const CUtensorMap *mg, const CUtensorMap *mo, const CUtensorMap *mk,
+                         const CUtensorMap *mv, const CUtensorMap *mks, const CUtensorMap *mvs) {
         unsigned kv = 0, qn = 0;
         bool fine = true;
-        for (unsigned item = blockIdx.x; fine && item < items; item += gridDim.x) {
+        for (unsigned item = blockIdx.x; fine; item += gridDim.x) {
             Plan u;
-            if (!plan(u, item)) continue;
-            if (!wait(x, bar(Y::bHoldEmpty), (qn & 1) ^ 1)) break;
-            mbar_arrive_expect_tx(bar(Y::bHold), 2 * Y::kTile);
+            if (item >= items) {
+                u.rounds = 0;
+            } else if (!plan(u, item)) {
+                p.redo[u.flag] = p.redo[u.flag + (p.Nq + p.Nk)] = 0;  // no tile there
+                continue;
+            }
+            if (!(fine = wait(x, bar(Y::bHoldEmpty), (qn & 1) ^ 1))) break;
+            B::put_plan(u, qn);
+            if (u.rounds == 0) break;
+            mbar_arrive_expect_tx(bar(Y::bHold), 3 * Y::kTile);
             B::tma_tile(Y::kA, mq, bar(Y::bHold), u.h, (int)(u.bos + u.t0));
             B::tma_tile(Y::kB, mg, bar(Y::bHold), u.h, (int)(u.bos + u.t0));
+            B::tma_tile(Y::kC, mo, bar(Y::bHold), u.h, (int)(u.bos + u.t0));
             ++qn;
-            for (int i = 0; i < u.kt.count(); ++i, ++kv) {
+            for (int i = 0; i < u.rounds; ++i, ++kv) {
                 const int s = kv % Y::NS;
                 if (!(fine = wait(x, bar(Y::bEmpty + s), ((kv / Y::NS) & 1) ^ 1))) break;
                 const int row = (int)(u.bos + (long long)u.kt.tile(i) * 128);
@@ -162,49 +194,48 @@ struct Dq : Base<D> {
         for (unsigned i = kv > Y::NS ? kv - Y::NS : 0; i < kv; ++i) wait_drain(bar(Y::bFull + i % Y::NS), (i / Y::NS) & 1);
     }
 
-    __device__ __forceinline__ bool issue_s(bool small, unsigned k) const {
+    __device__ __forceinline__ bool issue_s(uint32_t lead, bool small, unsigned k) const {
         const int s = k % Y::NS;
-        if (!wait(x, bar(Y::bFull + s), (k / Y::NS) & 1)) return false;
+        if (!hold(x, bar(Y::bFull + s), (k / Y::NS) & 1)) return false;
         tc_fence_after();
         const uint32_t id = small ? idesc_bf16(128, kSinkCols, 0, 0) : idesc_bf16(128, 128, 0, 0);
-        B::mma_rows(tS, Y::kA, Y::kX + s * Y::kTile, id);
-        B::mma_rows(tDP, Y::kB, Y::kY + s * Y::kTile, id);
-        mma_commit(bar(Y::bS));
+        B::mma_rows(lead, tS, Y::kA, Y::kX + s * Y::kTile, id);
+        B::mma_rows(lead, tDP, Y::kB, Y::kY + s * Y::kTile, id);
+        commit_by(lead, bar(Y::bS));
         return true;
     }
 
     __device__ void mma() {
-        unsigned kv = 0, qn = 0;
+        const uint32_t lead = elect();
+        unsigned k = 0, qn = 0;
         bool fine = true;
-        for (unsigned item = blockIdx.x; fine && item < items; item += gridDim.x) {
-            Plan u;
-            if (!plan(u, item)) continue;
-            const int n = u.kt.count();
-            fine = wait(x, bar(Y::bHold), qn & 1) && issue_s(u.small(0), kv);
-            for (int i = 0; fine && i < n; ++i) {
-                const unsigned k = kv + i;
+        Plan u;
+        for (; fine && B::next_plan(u, qn); ++qn) {
+            const int n = u.rounds;
+            fine = hold(x, bar(Y::bHold), qn & 1) && issue_s(lead, u.small(0), k);
+            for (int i = 0; fine && i < n; ++i, ++k) {
                 // both in registers: the next tile's may come
-                if (!(fine = wait(x, bar(Y::bP), k & 1))) break;
+                if (!(fine = hold(x, bar(Y::bP), k & 1))) break;
                 if (i + 1 < n) {
-                    if (!(fine = issue_s(u.small(i + 1), k + 1))) break;
+                    if (!(fine = issue_s(lead, false, k + 1))) break;
                 } else {
-                    mma_commit(bar(Y::bHoldEmpty));
+                    commit_by(lead, bar(Y::bHoldEmpty));
                 }
-                if (i == 0 && !(fine = wait(x, bar(Y::bOutEmpty), (qn & 1) ^ 1))) break;
-                if (!(fine = wait(x, bar(Y::bDS), k & 1))) break;
+                if (i == 0 && !(fine = hold(x, bar(Y::bOutEmpty), (qn & 1) ^ 1))) break;
+                if (!(fine = hold(x, bar(Y::bDS), k & 1))) break;
                 tc_fence_after();
-                const uint32_t b = x.base + Y::kX + (k % Y::NS) * Y::kTile;
-                const int steps = u.small(i) ? kSinkCols / 16 : 8;
-                for (int kk = 0; kk < steps; ++kk)
-                    mma_ts(tm + tDQ, tm + tDS + 64 * (k & 1) + 8 * kk, sdesc(b + kk * 2048, kPanel, 1024), idesc_bf16(128, D, 0, 1),
-                           (i | kk) != 0);
-                mma_commit(bar(Y::bEmpty + k % Y::NS));
-                if (i + 1 == n) mma_commit(bar(Y::bOut));
+                const uint32_t b = cols_of(x.base + Y::kX + (k % Y::NS) * Y::kTile), a = tm + tDS + 64 * (k & 1);
+                constexpr uint32_t id = idesc_bf16(128, D, 0, 1);
+                mma_ts_by(lead, tm + tDQ, a, b, id, i != 0);
+                mma_ts_by(lead, tm + tDQ, a + 8, b + 128, id, 1);
+                if (!u.small(i))
+#pragma unroll
+                    for (int kk = 2; kk < 8; ++kk) mma_ts_by(lead, tm + tDQ, a + 8 * kk, b + 128 * kk, id, 1);
+                commit_by(lead, bar(Y::bEmpty + k % Y::NS));
+                if (i + 1 == n) commit_by(lead, bar(Y::bOut));
             }
-            kv += n;
-            ++qn;
         }
-        mma_commit(bar(Y::bDrain));
+        commit_by(lead, bar(Y::bDrain));
         wait_drain(bar(Y::bDrain), 0);
     }
 
@@ -214,37 +245,37 @@ struct Dq : Base<D> {
         const float c = p.scale * kLog2e;
         const Sight sight{p.window, p.sinks};
         unsigned k = 0, qn = 0;
-        for (unsigned item = blockIdx.x; item < items; item += gridDim.x) {
-            Plan u;
-            if (!plan(u, item)) {
-                if (threadIdx.x < 2) p.redo[u.flag + threadIdx.x * (p.Nq + p.Nk)] = 0;
-                continue;
-            }
+        Plan u;
+        for (; B::next_plan(u, qn); ++qn) {
             const int t = u.t0 + row;
             const bool live = t < u.L;
             const long long at = (u.bos + t) * p.Nq + u.h;
-            // D of the row, by each of its two threads
-            float dsum = 0.f;
-            if (live) {
-                const __nv_bfloat16 *o = static_cast<const __nv_bfloat16 *>(p.o) + at * D;
-                const __nv_bfloat16 *g = static_cast<const __nv_bfloat16 *>(p.dout) + at * D;
-#pragma unroll 4
-                for (int i = 0; i < D; i += 8) {
-                    Vec<__nv_bfloat16, 8> a, b;
-                    a.load(o + i);
-                    b.load(g + i);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) dsum = fmaf(a.v[e], b.v[e], dsum);
-                }
-            }
-            if (w == 0 && live) p.dsum[at] = dsum;
             const float lse2 = live ? p.lse[at] * kLog2e : 0.f;
+            if (!hold(x, bar(Y::bHold), qn & 1)) return;
+            // D of the row, by each of its two threads, from the swizzled tiles of do and o
+            float dsum = 0.f;
+            {
+                const uint8_t *g = x.gbase + Y::kB + row * 128, *o = x.gbase + Y::kC + row * 128;
+#pragma unroll 1
+                for (int i = 0; i < D / 64; ++i, g += kPanel, o += kPanel)
+#pragma unroll 2
+                    for (int e = 0; e < 8; ++e) {
+                        Vec<__nv_bfloat16, 8> a, b;
+                        a.load(reinterpret_cast<const __nv_bfloat16 *>(g + ((e ^ (row & 7)) << 4)));
+                        b.load(reinterpret_cast<const __nv_bfloat16 *>(o + ((e ^ (row & 7)) << 4)));
+#pragma unroll
+                        for (int f = 0; f < 8; ++f) dsum = fmaf(a.v[f], b.v[f], dsum);
+                    }
+            }
+            warp_arrive(bar(Y::bHoldEmpty));
+            if (w == 0 && live) p.dsum[at] = dsum;
             const f2 cc = both(c), ll = both(-lse2), dd = both(-dsum);
-            for (int i = 0; i < u.kt.count(); ++i, ++k) {
-                const int k0 = u.kt.tile(i) * 128;
-                if (!wwait(x, bar(Y::bS), k & 1)) return;
-                tc_fence_after();
+            for (int i = 0; i < u.rounds; ++i, ++k) {
+                const int k0 = u.kt.tile(i) * 128 + 64 * w;
                 const int cols = u.small(i) ? (w == 0 ? 1 : 0) : 2;  // groups of 32 columns
+                const bool edge = k0 + 63 > u.t0 || u.t0 + 127 - k0 >= p.window;
+                if (!hold(x, bar(Y::bS), k & 1)) return;
+                tc_fence_after();
                 uint32_t s[2][32], g[2][32];
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
@@ -260,22 +291,22 @@ struct Dq : Base<D> {
                 }
                 tc_fence_before();
                 warp_arrive(bar(Y::bP));
-                const bool edge = k0 + 127 > u.t0 || u.t0 + 127 - k0 >= p.window;
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
                     if (q < cols) {
-                        const uint32_t mask = edge ? seen32(t, k0 + 64 * w + 32 * q, sight) : 0xffffffffu;
                         uint32_t ds[16];
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
                             float a, b;
                             split(fma2(pair(__uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1])), cc, ll), a, b);
                             split(mul2(pair(ex2(a), ex2(b)), add2(pair(__uint_as_float(g[q][e]), __uint_as_float(g[q][e + 1])), dd)), a, b);
-                            if (edge) {
-                                a = mask >> e & 1 ? a : 0.f;
-                                b = mask >> (e + 1) & 1 ? b : 0.f;
-                            }
                             ds[e / 2] = pack_bf16(a, b);
+                        }
+                        if (edge) {
+                            const uint32_t mask = seen32(t, k0 + 32 * q, sight);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)  // pairs of a 16-bit half each
+                                ds[e] &= (mask >> (2 * e) & 1 ? 0xffffu : 0u) | (mask >> (2 * e + 1) & 1 ? 0xffff0000u : 0u);
                         }
                         tmem_st16(lane + tDS + 64 * (k & 1) + 32 * w + 16 * q, ds);
                     }
@@ -283,14 +314,16 @@ struct Dq : Base<D> {
                 tc_fence_before();
                 warp_arrive(bar(Y::bDS));
             }
-            if (!wwait(x, bar(Y::bOut), qn & 1)) return;
-            ++qn;
+            if (!hold(x, bar(Y::bOut), qn & 1)) return;
             tc_fence_after();
             bool nan = false;
             __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.dq) + at * D;
-            if (D == 128 || w == 0) nan = B::store64(lane + tDQ + 64 * w, out + 64 * w, p.scale, live);
-            tc_fence_before();
-            warp_arrive(bar(Y::bOutEmpty));
+            auto done = [&] {
+                tc_fence_before();
+                warp_arrive(bar(Y::bOutEmpty));
+            };
+            if (D == 128 || w == 0) nan = B::store64(lane + tDQ + 64 * w, out + 64 * w, p.scale, live, done);
+            else done();
             B::mark(nan, u.flag);
         }
     }
@@ -302,9 +335,9 @@ struct Dq : Base<D> {
 // sinks of a sequence alone.
 struct KeyPlan {
     long long bos, flag;
-    int n, L, hk, k0, first, tiles;  // sequence; query tiles [first, first + tiles) of each of the group's heads
-    bool part, split;  // split: the sinks' rows are summed over parts
     long long place;   // of the sinks' rows of this item among the parts
+    int L, hk, k0, first, tiles, rounds;  // query tiles [first, first + tiles) of each of the group's heads
+    bool part, split;  // split: the sinks' rows are summed over parts
 };
 
 struct Parts {  // how the query tiles behind the window are cut
@@ -321,7 +354,6 @@ __device__ __forceinline__ bool key_plan(KeyPlan &u, const WindowParams &p, long
     u.flag = (long long)slot * 2 * (p.Nq + p.Nk) + p.Nq + u.hk;
     const SeqTile s = seq_tile(p.seq, slot, u.part ? parts.tiles * 128 : 128);
     if (!s.ok || s.t0 >= s.t1) return false;
-    u.n = s.n;
     u.bos = s.bos;
     u.L = (int)(s.eos - s.bos);
     u.k0 = u.part ? 0 : (int)(s.t0 - s.bos);
@@ -332,18 +364,20 @@ __device__ __forceinline__ bool key_plan(KeyPlan &u, const WindowParams &p, long
         u.first = from > qt.last + 1 ? from : qt.last + 1;
         u.tiles = to - u.first + 1;
         u.place = slot;
+        u.rounds = u.tiles * (p.Nq / p.Nk);
         return u.split && u.tiles > 0;
     }
     u.first = qt.first;
     u.tiles = qt.last - qt.first + 1;
     u.place = parts.slots + s.n;
+    u.rounds = u.tiles * (p.Nq / p.Nk);
     return true;
 }
 
 template <int D>
-struct Dkv : Base<D> {
-    using Y = Lay<D>;
-    using B = Base<D>;
+struct Dkv : Base<D, 2, KeyPlan> {
+    using B = Base<D, 2, KeyPlan>;
+    using Y = typename B::Y;
     using B::bar;
     using B::p;
     using B::tm;
@@ -353,33 +387,45 @@ struct Dkv : Base<D> {
     Parts parts;
     static constexpr uint32_t tS = 0, tDP = 128, tDV = 256, tDK = 384;
 
-    __device__ __forceinline__ bool plan(KeyPlan &u, unsigned item) const { return key_plan(u, p, slots, parts, item); }
-    __device__ __forceinline__ int rounds(const KeyPlan &u) const { return u.tiles * (p.Nq / p.Nk); }
-    __device__ __forceinline__ void round(const KeyPlan &u, int i, int &h, int &q0) const {
-        h = u.hk * (p.Nq / p.Nk) + i / u.tiles;
-        q0 = (u.first + i % u.tiles) * 128;
-    }
+    // The rounds of an item: its query tiles for the first of the group's heads, then the next one.
+    struct Round {
+        int h, tile, left;
+        __device__ __forceinline__ Round(const KeyPlan &u, int G) : h(u.hk * G), tile(u.first), left(u.tiles) {}
+        __device__ __forceinline__ void step(const KeyPlan &u) {
+            ++tile;
+            if (--left == 0) {
+                ++h;
+                tile = u.first;
+                left = u.tiles;
+            }
+        }
+    };
 
     __device__ void load(const CUtensorMap *mq, const CUtensorMap *mg, const CUtensorMap *mk, const CUtensorMap *mv) {
         unsigned qs = 0, kn = 0;
         bool fine = true;
-        for (unsigned item = blockIdx.x; fine && item < items; item += gridDim.x) {
+        for (unsigned item = blockIdx.x; fine; item += gridDim.x) {
             KeyPlan u;
-            if (!plan(u, item)) continue;
-            if (!wait(x, bar(Y::bHoldEmpty), (kn & 1) ^ 1)) break;
+            if (item >= items) {
+                u.rounds = 0;
+            } else if (!key_plan(u, p, slots, parts, item)) {
+                if (!u.part) p.redo[u.flag] = p.redo[u.flag + (p.Nq + p.Nk)] = 0;  // no tile there
+                continue;
+            }
+            if (!(fine = wait(x, bar(Y::bHoldEmpty), (kn & 1) ^ 1))) break;
+            B::put_plan(u, kn);
+            if (u.rounds == 0) break;
             mbar_arrive_expect_tx(bar(Y::bHold), 2 * Y::kTile);
             B::tma_tile(Y::kA, mk, bar(Y::bHold), u.hk, (int)(u.bos + u.k0));
             B::tma_tile(Y::kB, mv, bar(Y::bHold), u.hk, (int)(u.bos + u.k0));
             ++kn;
-            const int n = rounds(u);
-            for (int i = 0; i < n; ++i, ++qs) {
+            Round r(u, p.Nq / p.Nk);
+            for (int i = 0; i < u.rounds; ++i, ++qs, r.step(u)) {
                 const int s = qs % Y::NS;
                 if (!(fine = wait(x, bar(Y::bEmpty + s), ((qs / Y::NS) & 1) ^ 1))) break;
-                int h, q0;
-                round(u, i, h, q0);
                 mbar_arrive_expect_tx(bar(Y::bFull + s), 2 * Y::kTile);
-                B::tma_tile(Y::kX + s * Y::kTile, mq, bar(Y::bFull + s), h, (int)(u.bos + q0));
-                B::tma_tile(Y::kY + s * Y::kTile, mg, bar(Y::bFull + s), h, (int)(u.bos + q0));
+                B::tma_tile(Y::kX + s * Y::kTile, mq, bar(Y::bFull + s), r.h, (int)(u.bos + r.tile * 128));
+                B::tma_tile(Y::kY + s * Y::kTile, mg, bar(Y::bFull + s), r.h, (int)(u.bos + r.tile * 128));
             }
         }
         if (kn) wait_drain(bar(Y::bHold), (kn - 1) & 1);
@@ -389,24 +435,21 @@ struct Dkv : Base<D> {
     // lse (times log2 e) and D of the streamed queries, a stage ahead like their tiles
     __device__ void columns() {
         const int lane = threadIdx.x & 31;
-        unsigned qs = 0;
-        for (unsigned item = blockIdx.x; item < items; item += gridDim.x) {
-            KeyPlan u;
-            if (!plan(u, item)) continue;
-            const int n = rounds(u);
-            for (int i = 0; i < n; ++i, ++qs) {
+        unsigned qs = 0, kn = 0;
+        KeyPlan u;
+        for (; B::next_plan(u, kn); ++kn) {
+            Round r(u, p.Nq / p.Nk);
+            for (int i = 0; i < u.rounds; ++i, ++qs, r.step(u)) {
                 const int s = qs % Y::NS;
-                int h, q0;
-                round(u, i, h, q0);
                 float a[4], b[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int t = q0 + lane + 32 * e;
-                    const long long at = (u.bos + t) * p.Nq + h;
+                    const int t = r.tile * 128 + lane + 32 * e;
+                    const long long at = (u.bos + t) * p.Nq + r.h;
                     a[e] = t < u.L ? -p.lse[at] * kLog2e : 0.f;
                     b[e] = t < u.L ? -p.dsum[at] : 0.f;
                 }
-                if (!wwait(x, bar(Y::bEmpty + s), ((qs / Y::NS) & 1) ^ 1)) return;
+                if (!hold(x, bar(Y::bEmpty + s), ((qs / Y::NS) & 1) ^ 1)) return;
                 float *to = reinterpret_cast<float *>(x.gbase + Y::kCols + s * 1024);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -418,56 +461,55 @@ struct Dkv : Base<D> {
         }
     }
 
-    __device__ __forceinline__ void mma_acc(uint32_t acc, uint32_t a, uint32_t b, bool more) const {
+    __device__ __forceinline__ void mma_acc(uint32_t lead, uint32_t acc, uint32_t a, uint32_t at_b, bool more) const {
+        const uint32_t b = cols_of(x.base + at_b);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)  // the two halves of the queries lie 64 columns apart
-            mma_ts(tm + acc, tm + a + 64 * (kk >> 2) + 8 * (kk & 3), sdesc(x.base + b + kk * 2048, kPanel, 1024), idesc_bf16(128, D, 0, 1),
-                   more || kk != 0);
+            mma_ts_by(lead, tm + acc, tm + a + 64 * (kk >> 2) + 8 * (kk & 3), b + 128 * kk, idesc_bf16(128, D, 0, 1), more || kk != 0);
     }
 
     __device__ void mma() {
         constexpr uint32_t id = idesc_bf16(128, 128, 0, 0);
-        unsigned qs = 0, kn = 0;
+        const uint32_t lead = elect();
+        unsigned k = 0, kn = 0;
         bool fine = true;
-        for (unsigned item = blockIdx.x; fine && item < items; item += gridDim.x) {
-            KeyPlan u;
-            if (!plan(u, item)) continue;
-            const int n = rounds(u);
-            auto full = [&](unsigned k) { return wait(x, bar(Y::bFull + k % Y::NS), (k / Y::NS) & 1); };
-            if (!(fine = wait(x, bar(Y::bHold), kn & 1) && full(qs))) break;
+        KeyPlan u;
+        auto full = [&](unsigned k) { return hold(x, bar(Y::bFull + k % Y::NS), (k / Y::NS) & 1); };
+        for (; fine && B::next_plan(u, kn); ++kn) {
+            const int n = u.rounds;
+            if (!(fine = hold(x, bar(Y::bHold), kn & 1) && full(k))) break;
             tc_fence_after();
-            B::mma_rows(tS, Y::kA, Y::kX + (qs % Y::NS) * Y::kTile, id);
-            mma_commit(bar(Y::bS));
-            B::mma_rows(tDP, Y::kB, Y::kY + (qs % Y::NS) * Y::kTile, id);
-            mma_commit(bar(Y::bDP));
-            if (!(fine = wait(x, bar(Y::bOutEmpty), (kn & 1) ^ 1))) break;
-            for (int i = 0; i < n; ++i) {
-                const unsigned k = qs + i;
+            B::mma_rows(lead, tS, Y::kA, Y::kX + (k % Y::NS) * Y::kTile, id);
+            commit_by(lead, bar(Y::bS));
+            B::mma_rows(lead, tDP, Y::kB, Y::kY + (k % Y::NS) * Y::kTile, id);
+            commit_by(lead, bar(Y::bDP));
+            if (n == 1) commit_by(lead, bar(Y::bHoldEmpty));
+            if (!(fine = hold(x, bar(Y::bOutEmpty), (kn & 1) ^ 1))) break;
+#pragma unroll 1
+            for (int i = 0; i < n; ++i, ++k) {
                 const uint32_t here = (k % Y::NS) * Y::kTile, next = ((k + 1) % Y::NS) * Y::kTile;
-                if (!(fine = wait(x, bar(Y::bP), k & 1))) break;
+                if (!(fine = hold(x, bar(Y::bP), k & 1))) break;
                 tc_fence_after();
-                mma_acc(tDV, tS, Y::kY + here, i > 0);
+                mma_acc(lead, tDV, tS, Y::kY + here, i > 0);
                 if (i + 1 < n) {
                     if (!(fine = full(k + 1))) break;
-                    B::mma_rows(tS, Y::kA, Y::kX + next, id);
-                    mma_commit(bar(Y::bS));
+                    B::mma_rows(lead, tS, Y::kA, Y::kX + next, id);
+                    commit_by(lead, bar(Y::bS));
                 }
-                if (!(fine = wait(x, bar(Y::bDS), k & 1))) break;
+                if (!(fine = hold(x, bar(Y::bDS), k & 1))) break;
                 tc_fence_after();
-                mma_acc(tDK, tDP, Y::kX + here, i > 0);
-                mma_commit(bar(Y::bEmpty + k % Y::NS));
+                mma_acc(lead, tDK, tDP, Y::kX + here, i > 0);
+                commit_by(lead, bar(Y::bEmpty + k % Y::NS));
                 if (i + 1 < n) {
-                    B::mma_rows(tDP, Y::kB, Y::kY + next, id);
-                    mma_commit(bar(Y::bDP));
+                    B::mma_rows(lead, tDP, Y::kB, Y::kY + next, id);
+                    commit_by(lead, bar(Y::bDP));
+                    if (i + 2 == n) commit_by(lead, bar(Y::bHoldEmpty));  // the last that read the keys and values
                 } else {
-                    mma_commit(bar(Y::bHoldEmpty));
-                    mma_commit(bar(Y::bOut));
+                    commit_by(lead, bar(Y::bOut));
                 }
             }
-            qs += n;
-            ++kn;
         }
-        mma_commit(bar(Y::bDrain));
+        commit_by(lead, bar(Y::bDrain));
         wait_drain(bar(Y::bDrain), 0);
     }
 
@@ -477,24 +519,19 @@ struct Dkv : Base<D> {
         const float c = p.scale * kLog2e;
         const f2 cc = both(c);
         unsigned k = 0, kn = 0;
-        for (unsigned item = blockIdx.x; item < items; item += gridDim.x) {
-            KeyPlan u;
-            if (!plan(u, item)) {
-                if (!u.part && threadIdx.x < 2) p.redo[u.flag + threadIdx.x * (p.Nq + p.Nk)] = 0;
-                continue;
-            }
+        KeyPlan u;
+        for (; B::next_plan(u, kn); ++kn) {
             const int j = u.k0 + row;  // the thread's key
-            const int n = rounds(u);
-            for (int i = 0; i < n; ++i, ++k) {
-                int h, q0;
-                round(u, i, h, q0);
+            Round r(u, p.Nq / p.Nk);
+            for (int i = 0; i < u.rounds; ++i, ++k, r.step(u)) {
+                const int q0 = r.tile * 128;
                 const float *cols = reinterpret_cast<const float *>(x.gbase + Y::kCols + (k % Y::NS) * 1024) + 64 * w;
                 // queries of the tile that see the key: [j, j + window - 1], or all behind j for a sink
                 const long long far = j < p.sinks ? (long long)u.L - 1 : (long long)j + p.window - 1;
                 const int lo = j - q0, hi = (int)((far < u.L - 1 ? far : u.L - 1) - q0);
                 const bool edge = q0 < u.k0 + 127 || q0 + 127 >= u.L || (long long)q0 + 127 - u.k0 >= p.window;
-                if (!wwait(x, bar(Y::bCol + k % Y::NS), (k / Y::NS) & 1)) return;
-                if (!wwait(x, bar(Y::bS), k & 1)) return;
+                if (!hold(x, bar(Y::bCol + k % Y::NS), (k / Y::NS) & 1)) return;
+                if (!hold(x, bar(Y::bS), k & 1)) return;
                 tc_fence_after();
                 uint32_t s[2][32];
                 tmem_ld32(lane + tS + 64 * w, s[0]);
@@ -526,7 +563,7 @@ struct Dkv : Base<D> {
                 tmem_wait_st();
                 tc_fence_before();
                 warp_arrive(bar(Y::bP));
-                if (!wwait(x, bar(Y::bDP), k & 1)) return;
+                if (!hold(x, bar(Y::bDP), k & 1)) return;
                 tc_fence_after();
                 uint32_t g[2][32];
                 tmem_ld32(lane + tDP + 64 * w, g[0]);
@@ -558,8 +595,7 @@ struct Dkv : Base<D> {
                 tc_fence_before();
                 warp_arrive(bar(Y::bDS));
             }
-            if (!wwait(x, bar(Y::bOut), kn & 1)) return;
-            ++kn;
+            if (!hold(x, bar(Y::bOut), kn & 1)) return;
             tc_fence_after();
             // dv by the first four warps, dk by the others; sinks that parts add to as fp32
             const uint32_t from = lane + (w == 0 ? tDV : tDK);
@@ -569,7 +605,7 @@ struct Dkv : Base<D> {
             __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(w == 0 ? p.dv : p.dk) + ((u.bos + j) * p.Nk + u.hk) * D;
             bool nan = false;
 #pragma unroll
-            for (int q = 0; q < D / 64; ++q) nan |= B::store64(from + 64 * q, out + 64 * q, f, live);
+            for (int q = 0; q < D / 64; ++q) nan |= B::store64(from + 64 * q, out + 64 * q, f, live, [] {});
             if (u.split) {
                 float *sum = p.sink_part + (((u.place * p.Nk + u.hk) * 2 + w) * p.sinks + row) * D;
 #pragma unroll
@@ -592,9 +628,9 @@ struct Dkv : Base<D> {
     }
 };
 
-template <int D, typename F>
-__device__ __forceinline__ void set_up(F &f, uint8_t *raw_smem, unsigned *status) {
-    using Y = Lay<D>;
+template <typename F>
+__device__ __forceinline__ void set_up(F &f, uint8_t *raw_smem, unsigned *status, int held_by) {
+    using Y = typename F::Y;
     const uint32_t raw = smem_u32(raw_smem);
     f.x.base = (raw + 1023u) & ~1023u;
     f.x.gbase = raw_smem + (f.x.base - raw);
@@ -602,7 +638,7 @@ __device__ __forceinline__ void set_up(F &f, uint8_t *raw_smem, unsigned *status
     f.x.status = status;
     if (threadIdx.x == 0) {
         mbar_init(f.bar(Y::bHold), 1);
-        mbar_init(f.bar(Y::bHoldEmpty), 1);
+        mbar_init(f.bar(Y::bHoldEmpty), held_by);
         for (int s = 0; s < Y::NS; ++s) {
             mbar_init(f.bar(Y::bFull + s), 1);
             mbar_init(f.bar(Y::bEmpty + s), 1);
@@ -614,6 +650,7 @@ __device__ __forceinline__ void set_up(F &f, uint8_t *raw_smem, unsigned *status
         mbar_init(f.bar(Y::bDS), 8);
         mbar_init(f.bar(Y::bOut), 1);
         mbar_init(f.bar(Y::bOutEmpty), 8);
+        for (int i = 0; i < kPlans; ++i) mbar_init(f.bar(Y::bPlan + i), 1);
         mbar_init(f.bar(Y::bDrain), 1);
         *f.x.abort_flag = 0;
         fence_barrier_init();
@@ -638,21 +675,20 @@ __device__ __forceinline__ void clear_up(uint32_t tm) {
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-window_dq(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mg, const __grid_constant__ CUtensorMap mk,
-          const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mks, const __grid_constant__ CUtensorMap mvs,
-          const __grid_constant__ WindowParams p, unsigned items, long long slots) {
+window_dq(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mg, const __grid_constant__ CUtensorMap mo,
+          const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mks,
+          const __grid_constant__ CUtensorMap mvs, const __grid_constant__ WindowParams p, unsigned items, long long slots) {
     extern __shared__ uint8_t smem_raw[];
     Dq<D> f{{Ctx{}, p, 0u}, items, slots};
-    set_up<D>(f, smem_raw, p.seq.status);
+    set_up(f, smem_raw, p.seq.status, 9);  // the MMAs and eight warps that read do and o
     wait_for_launches();
     const int warp = threadIdx.x >> 5;
     const bool one = (threadIdx.x & 31) == 0;
     if (warp == 8) {
-        if (one) f.load(&mq, &mg, &mk, &mv, &mks, &mvs);
+        if (one) f.load(&mq, &mg, &mo, &mk, &mv, &mks, &mvs);
         __syncwarp();
     } else if (warp == 9) {
-        if (one) f.mma();
-        __syncwarp();
+        f.mma();
     } else if (warp == 10) {
         if (blockIdx.x == 0) check_offsets(p.seq, threadIdx.x & 31, 32);
     } else {
@@ -667,7 +703,7 @@ window_dkv(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
            const __grid_constant__ CUtensorMap mv, const __grid_constant__ WindowParams p, unsigned items, long long slots, Parts parts) {
     extern __shared__ uint8_t smem_raw[];
     Dkv<D> f{{Ctx{}, p, 0u}, items, slots, parts};
-    set_up<D>(f, smem_raw, p.seq.status);
+    set_up(f, smem_raw, p.seq.status, 1);
     wait_for_launches();
     const int warp = threadIdx.x >> 5;
     const bool one = (threadIdx.x & 31) == 0;
@@ -675,8 +711,7 @@ window_dkv(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
         if (one) f.load(&mq, &mg, &mk, &mv);
         __syncwarp();
     } else if (warp == 9) {
-        if (one) f.mma();
-        __syncwarp();
+        f.mma();
     } else if (warp == 10) {
         f.columns();
     } else {
@@ -727,20 +762,21 @@ cudaError_t launch(const WindowParams &p, cudaStream_t stream) {
     const Parts parts{p.parts ? tile_slots(p.seq, p.part_tiles * 128) : 0, p.part_tiles};
     const long long qi = slots * p.Nq, ki = (slots + parts.slots) * p.Nk;
     if (qi > 0x7fffffffll || ki > 0x7fffffffll) return cudaErrorInvalidValue;
-    CUtensorMap mq, mg, mk, mv, mks, mvs;
+    CUtensorMap mq, mg, mo, mk, mv, mks, mvs;
     const uint64_t tokens = (uint64_t)p.seq.tokens;
     if (!make_tmap_rows_heads_d(&mq, p.q, tokens, p.Nq, D, 64, 128) || !make_tmap_rows_heads_d(&mg, p.dout, tokens, p.Nq, D, 64, 128) ||
-        !make_tmap_rows_heads_d(&mk, p.k, tokens, p.Nk, D, 64, 128) || !make_tmap_rows_heads_d(&mv, p.v, tokens, p.Nk, D, 64, 128) ||
+        !make_tmap_rows_heads_d(&mo, p.o, tokens, p.Nq, D, 64, 128) || !make_tmap_rows_heads_d(&mk, p.k, tokens, p.Nk, D, 64, 128) ||
+        !make_tmap_rows_heads_d(&mv, p.v, tokens, p.Nk, D, 64, 128) ||
         !make_tmap_rows_heads_d(&mks, p.k, tokens, p.Nk, D, 64, kSinkCols) || !make_tmap_rows_heads_d(&mvs, p.v, tokens, p.Nk, D, 64, kSinkCols))
         return cudaErrorInvalidValue;
-    constexpr int bytes = (int)Lay<D>::kAlloc;
-    cudaError_t err = allow_smem<window_dq<D>>(bytes);
-    if (err == cudaSuccess) err = allow_smem<window_dkv<D>>(bytes);
+    constexpr int q_bytes = (int)Lay<D, 3>::kAlloc, k_bytes = (int)Lay<D, 2>::kAlloc;
+    cudaError_t err = allow_smem<window_dq<D>>(q_bytes);
+    if (err == cudaSuccess) err = allow_smem<window_dkv<D>>(k_bytes);
     if (err != cudaSuccess) return err;
-    err = launch_after(window_dq<D>, dim3((unsigned)(qi < kSms ? qi : kSms)), dim3(kThreads), bytes, stream, mq, mg, mk, mv, mks, mvs, p,
+    err = launch_after(window_dq<D>, dim3((unsigned)(qi < kSms ? qi : kSms)), dim3(kThreads), q_bytes, stream, mq, mg, mo, mk, mv, mks, mvs, p,
                        (unsigned)qi, slots);
     if (err != cudaSuccess) return err;
-    err = launch_after(window_dkv<D>, dim3((unsigned)(ki < kSms ? ki : kSms)), dim3(kThreads), bytes, stream, mq, mg, mk, mv, p, (unsigned)ki,
+    err = launch_after(window_dkv<D>, dim3((unsigned)(ki < kSms ? ki : kSms)), dim3(kThreads), k_bytes, stream, mq, mg, mk, mv, p, (unsigned)ki,
                        slots, parts);
     if (err != cudaSuccess || !parts.slots) return err;
     return launch_after(window_sink_sums<D>, dim3((unsigned)p.seq.N * p.Nk, (2 * p.sinks * (D / 4) + 255) / 256), dim3(256), 0, stream, p, parts);
