@@ -7,8 +7,7 @@
 //
 // Two kernels, so that no sum is added by atomics: 7 products of 128 x 128 x d a tile
 // instead of 5, but every sum stays in tensor memory until it is done, in a fixed order.
-// window_dq computes D of its rows (from the tiles of o and do in shared memory) and leaves it for
-// window_dkv.
+// D comes first, from a pass of its own over o and do at the memory's rate (window_dsum).
 //
 // Warps 0-3 and 4-7: the first and the second 64 columns of every tile of scores, one row a
 // thread; warp 8: TMA loads, and the plans of the items; warp 9: the MMAs; warp 10 (window_dkv): the
@@ -37,25 +36,26 @@ constexpr uint32_t kPanel = 128 * 128;  // 128 rows of 64 columns of bf16
 
 constexpr int kPlans = 4;  // items whose plans are kept
 
-// Shared memory of both kernels: the tiles that stay (three in window_dq: q, do, o; two in window_dkv: k,
-// v), and stages of two that stream by.
-template <int D, int HELD>
+// Shared memory of both kernels: two tiles that stay, and two rings of tiles that stream by, NX and NY
+// deep, each freed as soon as its own last reader is done.  window_dq: keys (read until dQ of their tile) and
+// values (until dP).  window_dkv: q (until dK) and do (until dV).
+template <int D, bool DQ>
 struct Lay {
     static constexpr uint32_t kTile = (D / 64) * kPanel;
-    static constexpr int NS = D == 64 ? 4 : 2;
-    static constexpr uint32_t kA = 0, kB = kTile, kC = 2 * kTile, kX = HELD * kTile, kY = kX + NS * kTile, kEnd = kY + NS * kTile;
-    static constexpr uint32_t kCols = kEnd;  // window_dkv: lse and D of a stage's queries
-    static constexpr uint32_t kPlan = kCols + (HELD == 2 ? NS * 1024 : 0), kBar = kPlan + kPlans * 64;
-    static constexpr int bHold = 0, bHoldEmpty = 1, bFull = 2, bEmpty = bFull + NS, bCol = bEmpty + NS, bS = bCol + NS, bDP = bS + 1,
-                         bP = bDP + 1, bDS = bP + 1, bOut = bDS + 1, bOutEmpty = bOut + 1, bPlan = bOutEmpty + 1, bDrain = bPlan + kPlans,
-                         kBars = bDrain + 1;
+    static constexpr int NX = DQ ? (D == 64 ? 6 : 3) : (D == 64 ? 4 : 2), NY = D == 64 ? 4 : 2;
+    static constexpr uint32_t kA = 0, kB = kTile, kX = 2 * kTile, kY = kX + NX * kTile, kEnd = kY + NY * kTile;
+    static constexpr uint32_t kCols = kEnd;  // window_dkv: lse and D of the queries
+    static constexpr uint32_t kPlan = kCols + (DQ ? 0 : NX * 1024), kBar = kPlan + kPlans * 64;
+    static constexpr int bHold = 0, bHoldEmpty = 1, bX = 2, bXEmpty = bX + NX, bY = bXEmpty + NX, bYEmpty = bY + NY, bCol = bYEmpty + NY,
+                         bS = bCol + NX, bDP = bS + 1, bP = bDP + 1, bDS = bP + 1, bOut = bDS + 1, bOutEmpty = bOut + 1,
+                         bPlan = bOutEmpty + 1, bDrain = bPlan + kPlans, kBars = bDrain + 1;
     static constexpr uint32_t kMisc = kBar + 8 * kBars, kAlloc = kMisc + 16 + 1024;
     static_assert(kAlloc <= 232448, "exceeds the 227 KB of shared memory per CTA");
 };
 
-template <int D, int HELD, typename Plan>
+template <int D, bool DQ, typename Plan>
 struct Base {
-    using Y = Lay<D, HELD>;
+    using Y = Lay<D, DQ>;
     static_assert(sizeof(Plan) <= 64, "a plan's place in shared memory");
     Ctx x;
     const WindowParams &p;
@@ -73,6 +73,19 @@ struct Base {
         if (!hold(x, bar(Y::bPlan + n % kPlans), n / kPlans & 1)) return false;
         u = *reinterpret_cast<const Plan *>(x.gbase + Y::kPlan + n % kPlans * 64);
         return u.rounds > 0;
+    }
+    // use k of a ring of N: whether its tile has landed; whether its place is free
+    __device__ __forceinline__ bool full_x(unsigned k) const { return hold(x, bar(Y::bX + k % Y::NX), (k / Y::NX) & 1); }
+    __device__ __forceinline__ bool full_y(unsigned k) const { return hold(x, bar(Y::bY + k % Y::NY), (k / Y::NY) & 1); }
+    __device__ __forceinline__ bool free_x(unsigned k) const { return wait(x, bar(Y::bXEmpty + k % Y::NX), ((k / Y::NX) & 1) ^ 1); }
+    __device__ __forceinline__ bool free_y(unsigned k) const { return wait(x, bar(Y::bYEmpty + k % Y::NY), ((k / Y::NY) & 1) ^ 1); }
+    static __device__ __forceinline__ uint32_t at_x(unsigned k) { return Y::kX + k % Y::NX * Y::kTile; }
+    static __device__ __forceinline__ uint32_t at_y(unsigned k) { return Y::kY + k % Y::NY * Y::kTile; }
+    // Copies still in flight land before the CTA ends: uses up to k of both rings.
+    __device__ __forceinline__ void drain(unsigned kx, unsigned ky, unsigned holds) const {
+        if (holds) wait_drain(bar(Y::bHold), (holds - 1) & 1);
+        for (unsigned i = kx > Y::NX ? kx - Y::NX : 0; i < kx; ++i) wait_drain(bar(Y::bX + i % Y::NX), (i / Y::NX) & 1);
+        for (unsigned i = ky > Y::NY ? ky - Y::NY : 0; i < ky; ++i) wait_drain(bar(Y::bY + i % Y::NY), (i / Y::NY) & 1);
     }
     // rows of 128 x D by panels
     __device__ __forceinline__ void tma_tile(uint32_t at, const CUtensorMap *m, uint32_t b, int head, int row) const {
@@ -132,8 +145,8 @@ struct QueryPlan {
 };
 
 template <int D>
-struct Dq : Base<D, 3, QueryPlan> {
-    using B = Base<D, 3, QueryPlan>;
+struct Dq : Base<D, true, QueryPlan> {
+    using B = Base<D, true, QueryPlan>;
     using Y = typename B::Y;
     using Plan = QueryPlan;
     using B::bar;
@@ -161,9 +174,9 @@ struct Dq : Base<D, 3, QueryPlan> {
         return true;
     }
 
-    __device__ void load(const CUtensorMap *mq, const CUtensorMap *mg, const CUtensorMap *mo, const CUtensorMap *mk,
-                         const CUtensorMap *mv, const CUtensorMap *mks, const CUtensorMap *mvs) {
-        unsigned kv = 0, qn = 0;
+    __device__ void load(const CUtensorMap *mq, const CUtensorMap *mg, const CUtensorMap *mk, const CUtensorMap *mv,
+                         const CUtensorMap *mks, const CUtensorMap *mvs) {
+        unsigned kx = 0, ky = 0, qn = 0;
         bool fine = true;
         for (unsigned item = blockIdx.x; fine; item += gridDim.x) {
             Plan u;
@@ -176,32 +189,36 @@ struct Dq : Base<D, 3, QueryPlan> {
             if (!(fine = wait(x, bar(Y::bHoldEmpty), (qn & 1) ^ 1))) break;
             B::put_plan(u, qn);
             if (u.rounds == 0) break;
-            mbar_arrive_expect_tx(bar(Y::bHold), 3 * Y::kTile);
+            mbar_arrive_expect_tx(bar(Y::bHold), 2 * Y::kTile);
             B::tma_tile(Y::kA, mq, bar(Y::bHold), u.h, (int)(u.bos + u.t0));
             B::tma_tile(Y::kB, mg, bar(Y::bHold), u.h, (int)(u.bos + u.t0));
-            B::tma_tile(Y::kC, mo, bar(Y::bHold), u.h, (int)(u.bos + u.t0));
             ++qn;
-            for (int i = 0; i < u.rounds; ++i, ++kv) {
-                const int s = kv % Y::NS;
-                if (!(fine = wait(x, bar(Y::bEmpty + s), ((kv / Y::NS) & 1) ^ 1))) break;
+            for (int i = 0; i < u.rounds; ++i) {
                 const int row = (int)(u.bos + (long long)u.kt.tile(i) * 128);
-                mbar_arrive_expect_tx(bar(Y::bFull + s), u.small(i) ? 2 * kSinkCols * D * 2 : 2 * Y::kTile);
-                B::tma_tile(Y::kX + s * Y::kTile, u.small(i) ? mks : mk, bar(Y::bFull + s), u.hk, row);
-                B::tma_tile(Y::kY + s * Y::kTile, u.small(i) ? mvs : mv, bar(Y::bFull + s), u.hk, row);
+                const uint32_t bytes = u.small(i) ? kSinkCols * D * 2 : Y::kTile;
+                if (!(fine = B::free_x(kx))) break;
+                mbar_arrive_expect_tx(bar(Y::bX + kx % Y::NX), bytes);
+                B::tma_tile(B::at_x(kx), u.small(i) ? mks : mk, bar(Y::bX + kx % Y::NX), u.hk, row);
+                ++kx;
+                if (!(fine = B::free_y(ky))) break;
+                mbar_arrive_expect_tx(bar(Y::bY + ky % Y::NY), bytes);
+                B::tma_tile(B::at_y(ky), u.small(i) ? mvs : mv, bar(Y::bY + ky % Y::NY), u.hk, row);
+                ++ky;
             }
         }
-        if (qn) wait_drain(bar(Y::bHold), (qn - 1) & 1);
-        for (unsigned i = kv > Y::NS ? kv - Y::NS : 0; i < kv; ++i) wait_drain(bar(Y::bFull + i % Y::NS), (i / Y::NS) & 1);
+        B::drain(kx, ky, qn);
     }
 
     __device__ __forceinline__ bool issue_s(uint32_t lead, bool small, unsigned k) const {
-        const int s = k % Y::NS;
-        if (!hold(x, bar(Y::bFull + s), (k / Y::NS) & 1)) return false;
-        tc_fence_after();
         const uint32_t id = small ? idesc_bf16(128, kSinkCols, 0, 0) : idesc_bf16(128, 128, 0, 0);
-        B::mma_rows(lead, tS, Y::kA, Y::kX + s * Y::kTile, id);
-        B::mma_rows(lead, tDP, Y::kB, Y::kY + s * Y::kTile, id);
+        if (!B::full_x(k)) return false;
+        tc_fence_after();
+        B::mma_rows(lead, tS, Y::kA, B::at_x(k), id);
+        if (!B::full_y(k)) return false;
+        tc_fence_after();
+        B::mma_rows(lead, tDP, Y::kB, B::at_y(k), id);
         commit_by(lead, bar(Y::bS));
+        commit_by(lead, bar(Y::bYEmpty + k % Y::NY));
         return true;
     }
 
@@ -218,20 +235,21 @@ struct Dq : Base<D, 3, QueryPlan> {
                 if (!(fine = hold(x, bar(Y::bP), k & 1))) break;
                 if (i + 1 < n) {
                     if (!(fine = issue_s(lead, false, k + 1))) break;
-                } else {
+                    if (i + 2 == n) commit_by(lead, bar(Y::bHoldEmpty));  // the last that read q and do
+                } else if (n == 1) {
                     commit_by(lead, bar(Y::bHoldEmpty));
                 }
                 if (i == 0 && !(fine = hold(x, bar(Y::bOutEmpty), (qn & 1) ^ 1))) break;
                 if (!(fine = hold(x, bar(Y::bDS), k & 1))) break;
                 tc_fence_after();
-                const uint32_t b = cols_of(x.base + Y::kX + (k % Y::NS) * Y::kTile), a = tm + tDS + 64 * (k & 1);
+                const uint32_t b = cols_of(x.base + B::at_x(k)), a = tm + tDS + 64 * (k & 1);
                 constexpr uint32_t id = idesc_bf16(128, D, 0, 1);
                 mma_ts_by(lead, tm + tDQ, a, b, id, i != 0);
                 mma_ts_by(lead, tm + tDQ, a + 8, b + 128, id, 1);
                 if (!u.small(i))
 #pragma unroll
                     for (int kk = 2; kk < 8; ++kk) mma_ts_by(lead, tm + tDQ, a + 8 * kk, b + 128 * kk, id, 1);
-                commit_by(lead, bar(Y::bEmpty + k % Y::NS));
+                commit_by(lead, bar(Y::bXEmpty + k % Y::NX));
                 if (i + 1 == n) commit_by(lead, bar(Y::bOut));
             }
         }
@@ -251,24 +269,7 @@ struct Dq : Base<D, 3, QueryPlan> {
             const bool live = t < u.L;
             const long long at = (u.bos + t) * p.Nq + u.h;
             const float lse2 = live ? p.lse[at] * kLog2e : 0.f;
-            if (!hold(x, bar(Y::bHold), qn & 1)) return;
-            // D of the row, by each of its two threads, from the swizzled tiles of do and o
-            float dsum = 0.f;
-            {
-                const uint8_t *g = x.gbase + Y::kB + row * 128, *o = x.gbase + Y::kC + row * 128;
-#pragma unroll 1
-                for (int i = 0; i < D / 64; ++i, g += kPanel, o += kPanel)
-#pragma unroll 2
-                    for (int e = 0; e < 8; ++e) {
-                        Vec<__nv_bfloat16, 8> a, b;
-                        a.load(reinterpret_cast<const __nv_bfloat16 *>(g + ((e ^ (row & 7)) << 4)));
-                        b.load(reinterpret_cast<const __nv_bfloat16 *>(o + ((e ^ (row & 7)) << 4)));
-#pragma unroll
-                        for (int f = 0; f < 8; ++f) dsum = fmaf(a.v[f], b.v[f], dsum);
-                    }
-            }
-            warp_arrive(bar(Y::bHoldEmpty));
-            if (w == 0 && live) p.dsum[at] = dsum;
+            const float dsum = live ? p.dsum[at] : 0.f;
             const f2 cc = both(c), ll = both(-lse2), dd = both(-dsum);
             for (int i = 0; i < u.rounds; ++i, ++k) {
                 const int k0 = u.kt.tile(i) * 128 + 64 * w;
@@ -375,8 +376,8 @@ __device__ __forceinline__ bool key_plan(KeyPlan &u, const WindowParams &p, long
 }
 
 template <int D>
-struct Dkv : Base<D, 2, KeyPlan> {
-    using B = Base<D, 2, KeyPlan>;
+struct Dkv : Base<D, false, KeyPlan> {
+    using B = Base<D, false, KeyPlan>;
     using Y = typename B::Y;
     using B::bar;
     using B::p;
@@ -402,7 +403,7 @@ struct Dkv : Base<D, 2, KeyPlan> {
     };
 
     __device__ void load(const CUtensorMap *mq, const CUtensorMap *mg, const CUtensorMap *mk, const CUtensorMap *mv) {
-        unsigned qs = 0, kn = 0;
+        unsigned kx = 0, ky = 0, kn = 0;
         bool fine = true;
         for (unsigned item = blockIdx.x; fine; item += gridDim.x) {
             KeyPlan u;
@@ -420,16 +421,19 @@ struct Dkv : Base<D, 2, KeyPlan> {
             B::tma_tile(Y::kB, mv, bar(Y::bHold), u.hk, (int)(u.bos + u.k0));
             ++kn;
             Round r(u, p.Nq / p.Nk);
-            for (int i = 0; i < u.rounds; ++i, ++qs, r.step(u)) {
-                const int s = qs % Y::NS;
-                if (!(fine = wait(x, bar(Y::bEmpty + s), ((qs / Y::NS) & 1) ^ 1))) break;
-                mbar_arrive_expect_tx(bar(Y::bFull + s), 2 * Y::kTile);
-                B::tma_tile(Y::kX + s * Y::kTile, mq, bar(Y::bFull + s), r.h, (int)(u.bos + r.tile * 128));
-                B::tma_tile(Y::kY + s * Y::kTile, mg, bar(Y::bFull + s), r.h, (int)(u.bos + r.tile * 128));
+            for (int i = 0; i < u.rounds; ++i, r.step(u)) {
+                const int row = (int)(u.bos + r.tile * 128);
+                if (!(fine = B::free_x(kx))) break;
+                mbar_arrive_expect_tx(bar(Y::bX + kx % Y::NX), Y::kTile);
+                B::tma_tile(B::at_x(kx), mq, bar(Y::bX + kx % Y::NX), r.h, row);
+                ++kx;
+                if (!(fine = B::free_y(ky))) break;
+                mbar_arrive_expect_tx(bar(Y::bY + ky % Y::NY), Y::kTile);
+                B::tma_tile(B::at_y(ky), mg, bar(Y::bY + ky % Y::NY), r.h, row);
+                ++ky;
             }
         }
-        if (kn) wait_drain(bar(Y::bHold), (kn - 1) & 1);
-        for (unsigned i = qs > Y::NS ? qs - Y::NS : 0; i < qs; ++i) wait_drain(bar(Y::bFull + i % Y::NS), (i / Y::NS) & 1);
+        B::drain(kx, ky, kn);
     }
 
     // lse (times log2 e) and D of the streamed queries, a stage ahead like their tiles
@@ -440,7 +444,7 @@ struct Dkv : Base<D, 2, KeyPlan> {
         for (; B::next_plan(u, kn); ++kn) {
             Round r(u, p.Nq / p.Nk);
             for (int i = 0; i < u.rounds; ++i, ++qs, r.step(u)) {
-                const int s = qs % Y::NS;
+                const int s = qs % Y::NX;
                 float a[4], b[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -449,7 +453,7 @@ struct Dkv : Base<D, 2, KeyPlan> {
                     a[e] = t < u.L ? -p.lse[at] * kLog2e : 0.f;
                     b[e] = t < u.L ? -p.dsum[at] : 0.f;
                 }
-                if (!hold(x, bar(Y::bEmpty + s), ((qs / Y::NS) & 1) ^ 1)) return;
+                if (!hold(x, bar(Y::bXEmpty + s), ((qs / Y::NX) & 1) ^ 1)) return;
                 float *to = reinterpret_cast<float *>(x.gbase + Y::kCols + s * 1024);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -474,34 +478,38 @@ struct Dkv : Base<D, 2, KeyPlan> {
         unsigned k = 0, kn = 0;
         bool fine = true;
         KeyPlan u;
-        auto full = [&](unsigned k) { return hold(x, bar(Y::bFull + k % Y::NS), (k / Y::NS) & 1); };
         for (; fine && B::next_plan(u, kn); ++kn) {
             const int n = u.rounds;
-            if (!(fine = hold(x, bar(Y::bHold), kn & 1) && full(k))) break;
+            if (!(fine = hold(x, bar(Y::bHold), kn & 1) && B::full_x(k))) break;
             tc_fence_after();
-            B::mma_rows(lead, tS, Y::kA, Y::kX + (k % Y::NS) * Y::kTile, id);
+            B::mma_rows(lead, tS, Y::kA, B::at_x(k), id);
             commit_by(lead, bar(Y::bS));
-            B::mma_rows(lead, tDP, Y::kB, Y::kY + (k % Y::NS) * Y::kTile, id);
+            if (!(fine = B::full_y(k))) break;
+            tc_fence_after();
+            B::mma_rows(lead, tDP, Y::kB, B::at_y(k), id);
             commit_by(lead, bar(Y::bDP));
             if (n == 1) commit_by(lead, bar(Y::bHoldEmpty));
             if (!(fine = hold(x, bar(Y::bOutEmpty), (kn & 1) ^ 1))) break;
 #pragma unroll 1
             for (int i = 0; i < n; ++i, ++k) {
-                const uint32_t here = (k % Y::NS) * Y::kTile, next = ((k + 1) % Y::NS) * Y::kTile;
                 if (!(fine = hold(x, bar(Y::bP), k & 1))) break;
                 tc_fence_after();
-                mma_acc(lead, tDV, tS, Y::kY + here, i > 0);
+                mma_acc(lead, tDV, tS, B::at_y(k), i > 0);
+                commit_by(lead, bar(Y::bYEmpty + k % Y::NY));
                 if (i + 1 < n) {
-                    if (!(fine = full(k + 1))) break;
-                    B::mma_rows(lead, tS, Y::kA, Y::kX + next, id);
+                    if (!(fine = B::full_x(k + 1))) break;
+                    tc_fence_after();
+                    B::mma_rows(lead, tS, Y::kA, B::at_x(k + 1), id);
                     commit_by(lead, bar(Y::bS));
                 }
                 if (!(fine = hold(x, bar(Y::bDS), k & 1))) break;
                 tc_fence_after();
-                mma_acc(lead, tDK, tDP, Y::kX + here, i > 0);
-                commit_by(lead, bar(Y::bEmpty + k % Y::NS));
+                mma_acc(lead, tDK, tDP, B::at_x(k), i > 0);
+                commit_by(lead, bar(Y::bXEmpty + k % Y::NX));
                 if (i + 1 < n) {
-                    B::mma_rows(lead, tDP, Y::kB, Y::kY + next, id);
+                    if (!(fine = B::full_y(k + 1))) break;
+                    tc_fence_after();
+                    B::mma_rows(lead, tDP, Y::kB, B::at_y(k + 1), id);
                     commit_by(lead, bar(Y::bDP));
                     if (i + 2 == n) commit_by(lead, bar(Y::bHoldEmpty));  // the last that read the keys and values
                 } else {
@@ -525,12 +533,12 @@ struct Dkv : Base<D, 2, KeyPlan> {
             Round r(u, p.Nq / p.Nk);
             for (int i = 0; i < u.rounds; ++i, ++k, r.step(u)) {
                 const int q0 = r.tile * 128;
-                const float *cols = reinterpret_cast<const float *>(x.gbase + Y::kCols + (k % Y::NS) * 1024) + 64 * w;
+                const float *cols = reinterpret_cast<const float *>(x.gbase + Y::kCols + k % Y::NX * 1024) + 64 * w;
                 // queries of the tile that see the key: [j, j + window - 1], or all behind j for a sink
                 const long long far = j < p.sinks ? (long long)u.L - 1 : (long long)j + p.window - 1;
                 const int lo = j - q0, hi = (int)((far < u.L - 1 ? far : u.L - 1) - q0);
                 const bool edge = q0 < u.k0 + 127 || q0 + 127 >= u.L || (long long)q0 + 127 - u.k0 >= p.window;
-                if (!hold(x, bar(Y::bCol + k % Y::NS), (k / Y::NS) & 1)) return;
+                if (!hold(x, bar(Y::bCol + k % Y::NX), (k / Y::NX) & 1)) return;
                 if (!hold(x, bar(Y::bS), k & 1)) return;
                 tc_fence_after();
                 uint32_t s[2][32];
@@ -629,7 +637,7 @@ struct Dkv : Base<D, 2, KeyPlan> {
 };
 
 template <typename F>
-__device__ __forceinline__ void set_up(F &f, uint8_t *raw_smem, unsigned *status, int held_by) {
+__device__ __forceinline__ void set_up(F &f, uint8_t *raw_smem, unsigned *status) {
     using Y = typename F::Y;
     const uint32_t raw = smem_u32(raw_smem);
     f.x.base = (raw + 1023u) & ~1023u;
@@ -638,11 +646,15 @@ __device__ __forceinline__ void set_up(F &f, uint8_t *raw_smem, unsigned *status
     f.x.status = status;
     if (threadIdx.x == 0) {
         mbar_init(f.bar(Y::bHold), 1);
-        mbar_init(f.bar(Y::bHoldEmpty), held_by);
-        for (int s = 0; s < Y::NS; ++s) {
-            mbar_init(f.bar(Y::bFull + s), 1);
-            mbar_init(f.bar(Y::bEmpty + s), 1);
+        mbar_init(f.bar(Y::bHoldEmpty), 1);
+        for (int s = 0; s < Y::NX; ++s) {
+            mbar_init(f.bar(Y::bX + s), 1);
+            mbar_init(f.bar(Y::bXEmpty + s), 1);
             mbar_init(f.bar(Y::bCol + s), 1);
+        }
+        for (int s = 0; s < Y::NY; ++s) {
+            mbar_init(f.bar(Y::bY + s), 1);
+            mbar_init(f.bar(Y::bYEmpty + s), 1);
         }
         mbar_init(f.bar(Y::bS), 1);
         mbar_init(f.bar(Y::bDP), 1);
@@ -675,23 +687,21 @@ __device__ __forceinline__ void clear_up(uint32_t tm) {
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-window_dq(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mg, const __grid_constant__ CUtensorMap mo,
-          const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mks,
-          const __grid_constant__ CUtensorMap mvs, const __grid_constant__ WindowParams p, unsigned items, long long slots) {
+window_dq(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mg, const __grid_constant__ CUtensorMap mk,
+          const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mks, const __grid_constant__ CUtensorMap mvs,
+          const __grid_constant__ WindowParams p, unsigned items, long long slots) {
     extern __shared__ uint8_t smem_raw[];
     Dq<D> f{{Ctx{}, p, 0u}, items, slots};
-    set_up(f, smem_raw, p.seq.status, 9);  // the MMAs and eight warps that read do and o
+    set_up(f, smem_raw, p.seq.status);
     wait_for_launches();
     const int warp = threadIdx.x >> 5;
     const bool one = (threadIdx.x & 31) == 0;
     if (warp == 8) {
-        if (one) f.load(&mq, &mg, &mo, &mk, &mv, &mks, &mvs);
+        if (one) f.load(&mq, &mg, &mk, &mv, &mks, &mvs);
         __syncwarp();
     } else if (warp == 9) {
         f.mma();
-    } else if (warp == 10) {
-        if (blockIdx.x == 0) check_offsets(p.seq, threadIdx.x & 31, 32);
-    } else {
+    } else if (warp < 8) {
         f.threads();
     }
     clear_up(f.tm);
@@ -703,7 +713,7 @@ window_dkv(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
            const __grid_constant__ CUtensorMap mv, const __grid_constant__ WindowParams p, unsigned items, long long slots, Parts parts) {
     extern __shared__ uint8_t smem_raw[];
     Dkv<D> f{{Ctx{}, p, 0u}, items, slots, parts};
-    set_up(f, smem_raw, p.seq.status, 1);
+    set_up(f, smem_raw, p.seq.status);
     wait_for_launches();
     const int warp = threadIdx.x >> 5;
     const bool one = (threadIdx.x & 31) == 0;
@@ -755,6 +765,39 @@ __global__ void __launch_bounds__(256) window_sink_sums(WindowParams p, Parts pa
     }
 }
 
+// D = sum do o of every token and head: 16 bytes of both a thread, D / 8 threads a row.
+template <int D>
+__global__ void __launch_bounds__(256) window_dsum(WindowParams p, long long rows) {
+    constexpr int L = D / 8, ROWS = 4;  // rows in flight of a thread
+    wait_for_launches();
+    if (blockIdx.x == 0) check_offsets(p.seq, threadIdx.x, 256);
+    const __nv_bfloat16 *o = static_cast<const __nv_bfloat16 *>(p.o), *g = static_cast<const __nv_bfloat16 *>(p.dout);
+    const int per = 256 / L, sub = threadIdx.x / L, at = threadIdx.x % L * 8;
+    for (long long r0 = (long long)blockIdx.x * per * ROWS; r0 < rows; r0 += (long long)gridDim.x * per * ROWS) {
+        Pack<__nv_bfloat16, 8> a[ROWS], b[ROWS];
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            const long long r = r0 + i * per + sub;
+            a[i].clear();
+            b[i].clear();
+            if (r < rows) {
+                a[i].load(o + r * D + at);
+                b[i].load(g + r * D + at);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            const long long r = r0 + i * per + sub;
+            float s = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s = fmaf(a[i][e], b[i][e], s);
+#pragma unroll
+            for (int x = L / 2; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+            if (at == 0 && r < rows) p.dsum[r] = s;
+        }
+    }
+}
+
 template <int D>
 cudaError_t launch(const WindowParams &p, cudaStream_t stream) {
     const long long slots = tile_slots(p.seq, 128);
@@ -762,18 +805,21 @@ cudaError_t launch(const WindowParams &p, cudaStream_t stream) {
     const Parts parts{p.parts ? tile_slots(p.seq, p.part_tiles * 128) : 0, p.part_tiles};
     const long long qi = slots * p.Nq, ki = (slots + parts.slots) * p.Nk;
     if (qi > 0x7fffffffll || ki > 0x7fffffffll) return cudaErrorInvalidValue;
-    CUtensorMap mq, mg, mo, mk, mv, mks, mvs;
+    CUtensorMap mq, mg, mk, mv, mks, mvs;
     const uint64_t tokens = (uint64_t)p.seq.tokens;
     if (!make_tmap_rows_heads_d(&mq, p.q, tokens, p.Nq, D, 64, 128) || !make_tmap_rows_heads_d(&mg, p.dout, tokens, p.Nq, D, 64, 128) ||
-        !make_tmap_rows_heads_d(&mo, p.o, tokens, p.Nq, D, 64, 128) || !make_tmap_rows_heads_d(&mk, p.k, tokens, p.Nk, D, 64, 128) ||
+        !make_tmap_rows_heads_d(&mk, p.k, tokens, p.Nk, D, 64, 128) ||
         !make_tmap_rows_heads_d(&mv, p.v, tokens, p.Nk, D, 64, 128) ||
         !make_tmap_rows_heads_d(&mks, p.k, tokens, p.Nk, D, 64, kSinkCols) || !make_tmap_rows_heads_d(&mvs, p.v, tokens, p.Nk, D, 64, kSinkCols))
         return cudaErrorInvalidValue;
-    constexpr int q_bytes = (int)Lay<D, 3>::kAlloc, k_bytes = (int)Lay<D, 2>::kAlloc;
+    constexpr int q_bytes = (int)Lay<D, true>::kAlloc, k_bytes = (int)Lay<D, false>::kAlloc;
     cudaError_t err = allow_smem<window_dq<D>>(q_bytes);
     if (err == cudaSuccess) err = allow_smem<window_dkv<D>>(k_bytes);
     if (err != cudaSuccess) return err;
-    err = launch_after(window_dq<D>, dim3((unsigned)(qi < kSms ? qi : kSms)), dim3(kThreads), q_bytes, stream, mq, mg, mo, mk, mv, mks, mvs, p,
+    const long long rows = p.seq.tokens * p.Nq, blocks = (rows + 8192 / D - 1) / (8192 / D);
+    err = launch_after(window_dsum<D>, dim3((unsigned)(blocks < kSms * 8 ? blocks : kSms * 8)), dim3(256), 0, stream, p, rows);
+    if (err != cudaSuccess) return err;
+    err = launch_after(window_dq<D>, dim3((unsigned)(qi < kSms ? qi : kSms)), dim3(kThreads), q_bytes, stream, mq, mg, mk, mv, mks, mvs, p,
                        (unsigned)qi, slots);
     if (err != cudaSuccess) return err;
     err = launch_after(window_dkv<D>, dim3((unsigned)(ki < kSms ? ki : kSms)), dim3(kThreads), k_bytes, stream, mq, mg, mk, mv, p, (unsigned)ki,
