@@ -107,34 +107,35 @@ struct Base {
         unsigned char *m = reinterpret_cast<unsigned char *>(p.redo + flag + (warp >> 1 & 1) * (p.Nq + p.Nk));
         if ((threadIdx.x & 31) == 0) m[2 * (warp >> 2) + (warp & 1)] = nan;
     }
-    // 64 columns of a row of an accumulator times f, to bf16; true where a NaN is among them.  done(): they are read
-    template <typename F>
-    __device__ __forceinline__ bool store64(uint32_t from, __nv_bfloat16 *to, float f, bool write, F done) const {
-        uint32_t o[2][32];
-        tmem_ld32(from, o[0]);
-        tmem_ld32(from + 32, o[1]);
-        tmem_wait_ld();
-        tmem_ld_dep(o[0]);
-        tmem_ld_dep(o[1]);
-        done();
-        bool nan = false;
+    // N columns of an accumulator times f, to bf16; true where one of the lane's row is not finite.  `to`: the
+    // lane's row, of a tensor with `stride` elements from row to row; of the warp's 32 rows those from
+    // from_row up to rows are written.
+    template <int N>
+    __device__ __forceinline__ bool store_cols(uint32_t from, __nv_bfloat16 *to, long long stride, int from_row, int rows, float f) const {
+        f2 bad = 0ull;
+        const f2 ff = both(f);
+#pragma unroll 1
+        for (int c = 0; c < N; c += 64) {
+            uint32_t o[2][32], w[4][8];
+            tmem_ld32(from + c, o[0]);
+            tmem_ld32(from + c + 32, o[1]);
+            tmem_wait_ld();
+            tmem_ld_dep(o[0]);
+            tmem_ld_dep(o[1]);
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-            uint32_t w[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float a = __uint_as_float(o[h / 2][(h & 1) * 16 + 2 * e]) * f;
-                const float b = __uint_as_float(o[h / 2][(h & 1) * 16 + 2 * e + 1]) * f;
-                nan |= isnan(a) | isnan(b);
-                w[e] = pack_bf16(a, b);
+            for (int e = 0; e < 32; ++e) {
+                const f2 v = mul2(pair(__uint_as_float(o[e >> 4][2 * (e & 15)]), __uint_as_float(o[e >> 4][2 * (e & 15) + 1])), ff);
+                bad = fma2(v, 0ull, bad);  // 0 times infinity or NaN stays
+                float lo, hi;
+                split(v, lo, hi);
+                w[e >> 3][e & 7] = pack_bf16(lo, hi);
             }
-            if (write) store32(to + 16 * h, w);
+            store_rows64(to + c, stride, from_row, rows, w);
         }
-        return nan && write;
+        const int r = threadIdx.x & 31;
+        return isnan(sum_of(bad)) && r >= from_row && r < rows;
     }
 };
-
-// ---- dq -------------------------------------------------------------------------
 
 struct QueryPlan {
     long long bos, flag;
@@ -317,14 +318,12 @@ struct Dq : Base<D, true, QueryPlan> {
             }
             if (!hold(x, bar(Y::bOut), qn & 1)) return;
             tc_fence_after();
-            bool nan = false;
             __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.dq) + at * D;
-            auto done = [&] {
-                tc_fence_before();
-                warp_arrive(bar(Y::bOutEmpty));
-            };
-            if (D == 128 || w == 0) nan = B::store64(lane + tDQ + 64 * w, out + 64 * w, p.scale, live, done);
-            else done();
+            bool nan = false;
+            if (D == 128 || w == 0)
+                nan = B::template store_cols<64>(lane + tDQ + 64 * w, out + 64 * w, (long long)p.Nq * D, 0, u.L - (t & ~31), p.scale);
+            tc_fence_before();
+            warp_arrive(bar(Y::bOutEmpty));
             B::mark(nan, u.flag);
         }
     }
@@ -609,14 +608,13 @@ struct Dkv : Base<D, false, KeyPlan> {
             const uint32_t from = lane + (w == 0 ? tDV : tDK);
             const float f = w == 0 ? 1.f : p.scale;
             const bool summed = u.split && j < p.sinks;
-            const bool live = j < u.L && !u.part && !summed;
             __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(w == 0 ? p.dv : p.dk) + ((u.bos + j) * p.Nk + u.hk) * D;
-            bool nan = false;
-#pragma unroll
-            for (int q = 0; q < D / 64; ++q) nan |= B::store64(from + 64 * q, out + 64 * q, f, live, [] {});
+            // rows of the warp that are this item's alone: [own0, own1)
+            const int j0 = j & ~31, own0 = u.split ? p.sinks - j0 : 0, own1 = u.part ? 0 : u.L - j0;
+            const bool nan = own0 < 32 && B::template store_cols<D>(from, out, (long long)p.Nk * D, own0, own1, f);
             if (u.split) {
                 float *sum = p.sink_part + (((u.place * p.Nk + u.hk) * 2 + w) * p.sinks + row) * D;
-#pragma unroll
+#pragma unroll 1
                 for (int q = 0; q < D / 16; ++q) {
                     uint32_t o[16];
                     tmem_ld16(from + 16 * q, o);

@@ -274,6 +274,17 @@ struct Fwd {
         for (int e = 0; e < 16; ++e) s[e] = mask >> e & 1 ? s[e] : 0xff800000u;
     }
 
+    static __device__ __forceinline__ void scaled(const uint32_t (&s)[16], uint32_t (&w)[8], f2 ff, f2 &bads) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const f2 v = mul2(pair(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), ff);
+            bads = fma2(v, 0ull, bads);  // 0 times infinity or NaN stays
+            float lo, hi;
+            split(v, lo, hi);
+            w[e] = pack_bf16(lo, hi);
+        }
+    }
+
     __device__ void softmax(int q, int h) {
         const int warp = threadIdx.x >> 5, row = threadIdx.x & 127;
         const uint32_t ts = lane_base(tm, warp) + Y::tS + 128 * q + 64 * h, to = lane_base(tm, warp) + Y::tO + D * q + D / 2 * h;
@@ -373,27 +384,31 @@ struct Fwd {
             const float f = rcp(l);
             const long long at = (bos + t) * p.Nq + v.h;
             __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.o) + at * D + D / 2 * h;
-            float bad = 0.f;
-            uint32_t s[2][16];
-            tmem_ld16(to, s[0]);
+            f2 bads = 0ull;
+            const f2 ff = both(f);
+            if constexpr (D == 128) {
+                uint32_t w[4][8];
 #pragma unroll
-            for (int g = 0; g < D / 32; ++g) {
-                tmem_wait_ld_dep16(s[g & 1]);
-                if (g + 1 < D / 32) {
-                    tmem_ld16(to + 16 * (g + 1), s[~g & 1]);
-                } else {  // all of O is read
-                    tc_fence_before();
-                    warp_arrive(bar(Y::bOEmpty + q));
+                for (int g = 0; g < 4; ++g) {
+                    uint32_t s[16];
+                    tmem_ld16(to + 16 * g, s);
+                    tmem_wait_ld_dep16(s);
+                    scaled(s, w[g], ff, bads);
                 }
-                uint32_t w[8];
+                store_rows64(out, (long long)p.Nq * D, 0, L - (t & ~31), w);
+            } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float a = __uint_as_float(s[g & 1][2 * e]) * f, b = __uint_as_float(s[g & 1][2 * e + 1]) * f;
-                    if (isnan(a) | isnan(b)) bad = 1.f;
-                    w[e] = pack_bf16(a, b);
+                for (int g = 0; g < 2; ++g) {
+                    uint32_t s[16], w[8];
+                    tmem_ld16(to + 16 * g, s);
+                    tmem_wait_ld_dep16(s);
+                    scaled(s, w, ff, bads);
+                    if (t < L) store32(out + 16 * g, w);
                 }
-                if (t < L) store32(out + 16 * g, w);
             }
+            tc_fence_before();
+            warp_arrive(bar(Y::bOEmpty + q));
+            float bad = sum_of(bads);
             if (!swap(q, h, bad, other, nx)) return;
             if (h == 0 && t < L)
                 p.lse[at] = bad + other == 0.f && l < CUDART_INF_F ? (m + lg2(l)) * 0.6931471805599453f : redo_mark();

@@ -45,6 +45,30 @@ __device__ __forceinline__ void store32(void *dst, const uint32_t (&r)[8]) {  //
                  : "memory");
 }
 
+// 64 columns of bf16 of 32 rows, a row a lane, to global memory: four neighbouring lanes swap their quarters
+// first, so that each store fills 128 bytes of a row (a row a lane, it takes twice as long).
+// `to`: the lane's own row; `stride`: elements from row to row; rows from `from` up to `rows` are written.
+__device__ __forceinline__ void store_rows64(__nv_bfloat16 *to, long long stride, int from, int rows, uint32_t (&w)[4][8]) {
+    const int lane = threadIdx.x & 31, q = lane & 3;
+#pragma unroll
+    for (int x = 1; x <= 2; x <<= 1)
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+            if (a & x) continue;
+            const int b = a | x;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, q & x ? w[a][e] : w[b][e], x);
+                if (q & x) w[a][e] = got;
+                else w[b][e] = got;
+            }
+        }
+    __nv_bfloat16 *first = to - q * stride + 16 * q;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if ((lane & ~3) + j >= from && (lane & ~3) + j < rows) store32(first + j * stride, w[j]);
+}
+
 // Wait of a whole warp, bounded like wwait of dn_tc_sync.cuh but without a call: what is in
 // registers stays there.
 __device__ __forceinline__ bool hold(const tcs::Ctx &x, uint32_t bar, uint32_t parity) {
