@@ -81,6 +81,8 @@ class DnError(RuntimeError):
 def load(path: str | None = None):
     """Load ``libdnchunk.so`` (raises if it has not been built)."""
     global _lib
+    if path is None and _lib is not None:  # set once, complete
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib
@@ -281,9 +283,9 @@ def dn_last_kernel() -> str:
 
 def dtype_code(dtype) -> int:
     import torch
-    if dtype == torch.bfloat16:
+    if dtype is torch.bfloat16:
         return DN_BF16
-    if dtype == torch.float32:
+    if dtype is torch.float32:
         return DN_F32
     raise ValueError("unsupported dtype %s (bf16 or fp32)" % dtype)
 
@@ -678,25 +680,33 @@ def layer_norm_bwd(x, weight=None, bias=None, z=None, eps=1e-5, rms=False, dy=No
     return out
 
 
+def _vector(name, t, D, device, f32):
+    """Address of an optional fp32 vector of D elements (else ValueError)."""
+    if t is None:
+        return None
+    if t.dtype is f32 and t.dim() == 1 and t.numel() == D and t.device == device and t.is_contiguous():
+        return t.data_ptr()
+    return _operand(name, t, (D,), f32, device)
+
+
 def _block_inputs(what, x, residual, z, scale, post_weight, post_bias, weight, bias, eps, rms, post):
     """Checked addresses and sizes of a block's norms, in the order of the C arguments."""
     import torch
     device = _device_of(x, torch)
-    D = x.shape[-1]
+    shape, f32, dt = x.shape, torch.float32, x.dtype
+    D = shape[-1]
     _fit(what, D)
-    f32, dt = torch.float32, x.dtype
     code = dtype_code(dt)
     if residual is None:
         raise ValueError("residual is required")
-    rt = f32 if residual.dtype == f32 else dt
-    vectors = [_operand(name, t, (D,), f32, device) for name, t in
-               (("scale", scale), ("post_weight", post_weight), ("post_bias", post_bias),
-                ("weight", weight), ("bias", bias))]
-    ptrs = (_operand("x", x, x.shape, dt, device), _operand("residual", residual, x.shape, rt, device),
-            _operand("z", z, x.shape, dt, device), *vectors)
-    rows = x.numel() // D if D else 0
-    flags = (DN_NORM_RMS if rms else 0) | (DN_NORM_POST if post else 0)
-    return device, rt, ptrs, (rows, D, code, dtype_code(rt)), (eps, flags)
+    rt = f32 if residual.dtype is f32 else dt
+    return device, rt, (_operand("x", x, shape, dt, device), _operand("residual", residual, shape, rt, device),
+                        None if z is None else _operand("z", z, shape, dt, device),
+                        _vector("scale", scale, D, device, f32), _vector("post_weight", post_weight, D, device, f32),
+                        _vector("post_bias", post_bias, D, device, f32), _vector("weight", weight, D, device, f32),
+                        _vector("bias", bias, D, device, f32),
+                        x.numel() // D if D else 0, D, code, code if rt is dt else DN_F32), (
+        eps, (DN_NORM_RMS if rms else 0) | (DN_NORM_POST if post else 0))
 
 
 def block_norm_fwd(x, residual, z=None, scale=None, post_weight=None, post_bias=None, weight=None,
@@ -718,13 +728,13 @@ def block_norm_fwd(x, residual, z=None, scale=None, post_weight=None, post_bias=
         with _under(stream, _device_of(x, torch), torch):
             return block_norm_fwd(x, residual, z, scale, post_weight, post_bias, weight, bias, eps,
                                   rms, post, None, y, residual_out)
-    device, rt, ptrs, sizes, kind = _block_inputs("dn_block_norm_fwd", x, residual, z, scale, post_weight,
-                                                  post_bias, weight, bias, eps, rms, post)
+    device, rt, args, kind = _block_inputs("dn_block_norm_fwd", x, residual, z, scale, post_weight,
+                                           post_bias, weight, bias, eps, rms, post)
     if y is None:
         y = torch.empty_like(x, memory_format=torch.contiguous_format)
     if residual_out is None:
         residual_out = torch.empty_like(residual, memory_format=torch.contiguous_format)
-    st = load().dn_block_norm_fwd(*ptrs, *sizes, *kind, _operand("y", y, x.shape, x.dtype, device),
+    st = load().dn_block_norm_fwd(*args, *kind, _operand("y", y, x.shape, x.dtype, device),
                                   _operand("residual_out", residual_out, x.shape, rt, device),
                                   torch._C._cuda_getCurrentRawStream(device.index))
     if st != DN_OK:
@@ -746,8 +756,8 @@ def block_norm_bwd(x, residual, z=None, scale=None, post_weight=None, post_bias=
         with _under(stream, _device_of(x, torch), torch):
             return block_norm_bwd(x, residual, z, scale, post_weight, post_bias, weight, bias, eps, rms,
                                   post, dy, dresidual_out, None, workspace)
-    device, rt, ptrs, sizes, kind = _block_inputs("dn_block_norm_bwd", x, residual, z, scale, post_weight,
-                                                  post_bias, weight, bias, eps, rms, post)
+    device, rt, args, kind = _block_inputs("dn_block_norm_bwd", x, residual, z, scale, post_weight,
+                                           post_bias, weight, bias, eps, rms, post)
     lib = load()
 
     def like(t):
@@ -757,10 +767,10 @@ def block_norm_bwd(x, residual, z=None, scale=None, post_weight=None, post_bias=
                dpost_weight=like(post_weight), dpost_bias=like(post_bias), dweight=like(weight),
                dbias=like(bias))
     need = 0
-    if any(out[k] is not None for k in ("dscale", "dpost_weight", "dpost_bias", "dweight", "dbias")):
-        need = _workspace_bytes("dn_block_norm_bwd_workspace_bytes", *sizes)
+    if not (scale is None and post_weight is None and post_bias is None and weight is None and bias is None):
+        need = _workspace_bytes("dn_block_norm_bwd_workspace_bytes", *args[-4:])
     workspace, ws, wsb = _space(need, workspace, device)
-    st = lib.dn_block_norm_bwd(*ptrs, *sizes, *kind, _operand("dy", dy, x.shape, x.dtype, device, False),
+    st = lib.dn_block_norm_bwd(*args, *kind, _operand("dy", dy, x.shape, x.dtype, device, False),
                                _operand("dresidual_out", dresidual_out, x.shape, rt, device),
                                *(_ptr(t) for t in out.values()), ws, wsb,
                                torch._C._cuda_getCurrentRawStream(device.index))
