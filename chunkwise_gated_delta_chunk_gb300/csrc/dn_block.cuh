@@ -8,22 +8,35 @@
 
 namespace dn {
 
-// The vectors of A tensors of T and of B tensors of TR that a thread works on, S
-// iterations ahead, in shared memory by asynchronous copies.  Rows that do not begin on 16
+// A row on threads that it fills exactly (FULL: D = R K V, as most widths do) needs no checks of columns;
+// one row a block at a time none of rows.  N: rows that a thread works on at a time.
+template <typename T, int V, int K, int R, bool FULL, int N = 1>
+struct BlockRow : Row<T, V, K, R> {
+    using B = Row<T, V, K, R>;
+    static __device__ __forceinline__ bool in(int k, int i, int D) { return FULL || B::in(k, i, D); }
+    static __device__ __forceinline__ bool live(long long row, long long rows) { return (B::kRows == 1 && N == 1) || row < rows; }
+    // v in the columns that exist, 0 elsewhere
+    static __device__ __forceinline__ f2 inside(int k, float v, int D) {
+        return FULL ? both(v) : pair(in(k, 0, D) ? v : 0.f, in(k, 1, D) ? v : 0.f);
+    }
+};
+
+// The vectors of A tensors of T and of B tensors of TR that a thread works on, of N rows at a time, S
+// rows ahead in all, in shared memory by asynchronous copies.  Rows that do not begin on 16
 // bytes, and those too long for a stage to fit, are loaded where they are used.  Tensors that are
 // null are zeros.
-template <typename T, typename TR, int V, int K, int R, int A, int B, int REGS>
+template <typename T, typename TR, int V, int K, int R, bool FULL, int N, int A, int B, int REGS>
 struct BlockRing {
-    using L = Row<T, V, K, R>;
+    using L = BlockRow<T, V, K, R, FULL, N>;
     static constexpr int kRes = (int)sizeof(TR) * V;  // bytes of a vector of TR: 16 or 32
     static constexpr int kOne = K * L::kThreads;      // vectors of one tensor
     static constexpr int kStage = kOne * (A * 16 + B * kRes);
     // as many stages, up to 4, as leave room for the blocks that an SM's registers hold
     static constexpr int kBlocks = 65536 / (REGS * L::kThreads) < 1 ? 1 : 65536 / (REGS * L::kThreads);
     static constexpr int kRoom = 226 * 1024 / kBlocks - 2048;
-    static constexpr bool kAhead = L::kWhole && kStage <= kRoom;
-    static constexpr int kFit = kRoom / kStage;
-    static constexpr int S = !kAhead || kFit < 1 ? 1 : kFit > 4 ? 4 : kFit;
+    static constexpr bool kAhead = L::kWhole && N * kStage <= kRoom;
+    static constexpr int kFit = kRoom / kStage / N * N;
+    static constexpr int S = !kAhead || kFit < N ? N : kFit > 4 ? 4 : kFit;
     static constexpr int kBytes = kAhead ? S * kStage : 0;
     const T *a[A];
     const TR *b[B];
@@ -53,7 +66,7 @@ struct BlockRing {
         }
     }
     __device__ __forceinline__ void wait() {
-        if constexpr (kAhead) asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+        if constexpr (kAhead) asm volatile("cp.async.wait_group %0;" ::"n"(S - N) : "memory");
     }
     // vector k of tensor i as pairs; zeros where the row or the column does not exist
     __device__ __forceinline__ void get_a(f2 (&v)[L::P], const char *ring, int s, int i, int k, long long row, long long rows,
@@ -61,7 +74,7 @@ struct BlockRing {
         if constexpr (L::kWhole) {
             Pack<T, V> r;
             r.clear();
-            if (a[i] && row < rows && L::in(k, 0, D))
+            if (a[i] && L::live(row, rows) && L::in(k, 0, D))
                 r.load(kAhead ? reinterpret_cast<const T *>(ring + s * kStage + (i * kOne + k * L::kThreads + threadIdx.x) * 16)
                               : a[i] + row * D + L::col(k, 0));
 #pragma unroll
@@ -74,17 +87,24 @@ struct BlockRing {
                                           int D) const {
         if constexpr (L::kWhole) {
             constexpr int W = 16 / sizeof(TR);  // elements of 16 bytes
-            const bool here = b[i] && row < rows && L::in(k, 0, D);
+            const bool here = b[i] && L::live(row, rows) && L::in(k, 0, D);
 #pragma unroll
             for (int q = 0; q < kRes / 16; ++q) {
-                Pack<TR, W> r;
-                r.clear();
-                if (here)
-                    r.load(kAhead ? reinterpret_cast<const TR *>(ring + s * kStage + A * kOne * 16 +
-                                                                 ((i * (kRes / 16) + q) * kOne + k * L::kThreads + threadIdx.x) * 16)
-                                  : b[i] + row * D + L::col(k, 0) + q * W);
+                const TR *src = kAhead ? reinterpret_cast<const TR *>(ring + s * kStage + A * kOne * 16 +
+                                                                      ((i * (kRes / 16) + q) * kOne + k * L::kThreads + threadIdx.x) * 16)
+                                       : b[i] + row * D + L::col(k, 0) + q * W;
+                if constexpr (sizeof(TR) == 4) {
+                    ulonglong2 r = make_ulonglong2(0ull, 0ull);
+                    if (here) r = *reinterpret_cast<const ulonglong2 *>(src);
+                    v[2 * q] = r.x;
+                    v[2 * q + 1] = r.y;
+                } else {
+                    Pack<TR, W> r;
+                    r.clear();
+                    if (here) r.load(src);
 #pragma unroll
-                for (int e = 0; e < W / 2; ++e) v[q * (W / 2) + e] = pair(r[2 * e], r[2 * e + 1]);
+                    for (int e = 0; e < W / 2; ++e) v[q * (W / 2) + e] = pair(r[2 * e], r[2 * e + 1]);
+                }
             }
         } else {
             v[0] = load_elements<L>(b[i] + row * D, k, b[i] && row < rows ? D : 0);
@@ -92,92 +112,228 @@ struct BlockRing {
     }
 };
 
-// One of the fp32 vectors: of a single vector a thread the values stay in registers for all rows
-// (loaded for every row they cost more time than memory does: 8192 rows of 2048 in the backward
-// 148 us), else they are loaded where they are used.
-template <typename L, int V, int K>
+// Sums of S = 1, 2 or 4 values over the R threads of a row; every one of them gets them.  The values share the
+// shuffles, each on its part of a warp (one after the other the sums were a third of the backward's
+// instructions).  R > 32: `buf` has S R / 32 floats, and consecutive sums use buffers of their own in turn.
+template <int R, int S>
+__device__ __forceinline__ void sum_row(float (&a)[S], float *buf) {
+    static_assert(R == 32 || R % 128 == 0, "a row on a warp, or one row per block");
+    constexpr int kPart = 32 / S, W = R / 32;  // lanes of a value; warps
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % kPart, which = lane / kPart;
+    float t;
+    auto add = [&](float mine, float theirs, int x) { return mine + __shfl_xor_sync(0xffffffffu, theirs, x); };
+    if constexpr (S == 4) {
+        const bool low = lane < 16, even = !(lane & 8);
+        const float u = add(low ? a[0] : a[2], low ? a[2] : a[0], 16), v = add(low ? a[1] : a[3], low ? a[3] : a[1], 16);
+        t = add(even ? u : v, even ? v : u, 8);
+    } else if constexpr (S == 2) {
+        t = add(lane < 16 ? a[0] : a[1], lane < 16 ? a[1] : a[0], 16);
+    } else {
+        t = add(a[0], a[0], 16);
+    }
+#pragma unroll
+    for (int x = S == 1 ? 8 : kPart / 2; x > 0; x >>= 1) t = add(t, t, x);
+    if constexpr (R > 32) {
+        if (sub == 0) buf[which * W + warp] = t;
+        __syncthreads();
+        if constexpr (W <= kPart) {
+            t = buf[which * W + sub % W];
+#pragma unroll
+            for (int x = W / 2; x > 0; x >>= 1) t = add(t, t, x);
+        } else {
+            t = buf[which * W + sub];
+#pragma unroll
+            for (int i = kPart; i < W; i += kPart) t += buf[which * W + sub + i];
+#pragma unroll
+            for (int x = kPart / 2; x > 0; x >>= 1) t = add(t, t, x);
+        }
+    }
+    if constexpr (S == 1) {
+        a[0] = t;
+    } else {
+#pragma unroll
+        for (int i = 0; i < S; ++i) a[i] = __shfl_sync(0xffffffffu, t, i * kPart);
+    }
+}
+
+// Means m (0 for the root-mean-square form) and reciprocal deviations r of N rows; columns behind D hold 0.
+// buf: 2 N R / 32 floats.
+template <typename L, int V, int K, int R, int N>
+__device__ __forceinline__ void row_stats(const f2 (&x)[N][K][V / 2], bool rms, float eps, float inv, int D, float *buf, float (&m)[N],
+                                          float (&r)[N]) {
+    constexpr int P = V / 2;
+    float s[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) m[n] = 0.f;
+    if (!rms) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            f2 t = 0ull;
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int i = 0; i < P; ++i) t = add2(t, x[n][k][i]);
+            s[n] = sum_of(t);
+        }
+        sum_row<R>(s, buf);
+#pragma unroll
+        for (int n = 0; n < N; ++n) m[n] = s[n] * inv;
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        f2 t = 0ull;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const f2 mm = L::inside(k, -m[n], D);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const f2 d = add2(x[n][k][i], mm);
+                t = fma2(d, d, t);
+            }
+        }
+        s[n] = sum_of(t);
+    }
+    sum_row<R>(s, buf + N * (R / 32));
+#pragma unroll
+    for (int n = 0; n < N; ++n) r[n] = rsqrtf(fmaf(s[n], inv, eps));
+}
+
+// Vector k of one of the fp32 vectors; 0 where the column does not exist.
+template <typename L, int V>
+__device__ __forceinline__ void load_given(f2 (&t)[V / 2], const float *w, int k, int D) {
+    if constexpr (L::kWhole) {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) {
+            ulonglong2 r = make_ulonglong2(0ull, 0ull);
+            if (L::in(k, 0, D)) r = reinterpret_cast<const ulonglong2 *>(w + L::col(k, 0))[i];
+            t[2 * i] = r.x;
+            t[2 * i + 1] = r.y;
+        }
+    } else {
+        t[0] = pair(L::in(k, 0, D) ? w[L::col(k, 0)] : 0.f, L::in(k, 1, D) ? w[L::col(k, 1)] : 0.f);
+    }
+}
+
+// One of the fp32 vectors, where it is given.  KEEP: its values stay in registers for all rows; else they
+// are loaded where they are used (which few warps cannot hide).
+template <typename L, int V, int K, bool KEEP>
 struct Kept {
     static constexpr int P = V / 2;
-    static constexpr bool kKeep = K == 1;
     const float *src;
-    f2 v[kKeep ? P : 1];
-    __device__ __forceinline__ void init(const float *from, int D, float other) {
+    f2 v[KEEP ? K : 1][KEEP ? P : 1];
+    __device__ __forceinline__ void init(const float *from, int D) {
         src = from;
-        if constexpr (kKeep) load_vec<L, V>(v, from, 0, D, other);
+        if constexpr (KEEP)
+            if (from)
+#pragma unroll
+                for (int k = 0; k < K; ++k) load_given<L, V>(v[k], from, k, D);
     }
     __device__ __forceinline__ void times(f2 (&x)[P], int k, int D) const {
         if (!src) return;
         f2 t[P];
-        get(t, k, D, 1.f);
+        get(t, k, D);
 #pragma unroll
         for (int i = 0; i < P; ++i) x[i] = mul2(x[i], t[i]);
     }
     __device__ __forceinline__ void plus(f2 (&x)[P], int k, int D) const {
         if (!src) return;
         f2 t[P];
-        get(t, k, D, 0.f);
+        get(t, k, D);
 #pragma unroll
         for (int i = 0; i < P; ++i) x[i] = add2(x[i], t[i]);
     }
 
 private:
-    __device__ __forceinline__ void get(f2 (&t)[P], int k, int D, float other) const {
-        if constexpr (kKeep) {
+    __device__ __forceinline__ void get(f2 (&t)[P], int k, int D) const {
+        if constexpr (KEEP) {
 #pragma unroll
-            for (int i = 0; i < P; ++i) t[i] = v[i];
+            for (int i = 0; i < P; ++i) t[i] = v[k][i];
         } else {
-            load_vec<L, V>(t, src, k, D, other);
+            load_given<L, V>(t, src, k, D);
         }
     }
 };
 
-// w v + b of one vector, where given.
-template <typename L, int V>
-__device__ __forceinline__ void affine(f2 (&v)[V / 2], const float *w, const float *b, int k, int D) {
-    f2 t[V / 2];
-    if (w) {
-        load_vec<L, V>(t, w, k, D, 1.f);
+// The product of two of the fp32 vectors, either of which may be absent (one).
+template <typename L, int V, int K, bool KEEP>
+struct Scaled {
+    static constexpr int P = V / 2;
+    const float *a, *b;
+    f2 v[KEEP ? K : 1][KEEP ? P : 1];
+    __device__ __forceinline__ void init(const float *x, const float *y, int D) {
+        a = x;
+        b = y;
+        if constexpr (KEEP)
 #pragma unroll
-        for (int i = 0; i < V / 2; ++i) v[i] = mul2(v[i], t[i]);
+            for (int k = 0; k < K; ++k) load(v[k], k, D);
     }
-    if (b) {
-        load_vec<L, V>(t, b, k, D, 0.f);
+    __device__ __forceinline__ void times(f2 (&x)[P], int k, int D) const {
+        f2 t[P];
+        get(t, k, D);
 #pragma unroll
-        for (int i = 0; i < V / 2; ++i) v[i] = add2(v[i], t[i]);
+        for (int i = 0; i < P; ++i) x[i] = mul2(x[i], t[i]);
     }
-}
+    __device__ __forceinline__ void plus(f2 (&x)[P], int k, int D) const {
+        f2 t[P];
+        get(t, k, D);
+#pragma unroll
+        for (int i = 0; i < P; ++i) x[i] = add2(x[i], t[i]);
+    }
 
-// Threads and vectors of a row: about one vector of 16 bytes a thread up to 512 of them, then
-// more.  F is given the types and sizes.
-template <typename T, typename TR, typename F>
+private:
+    __device__ __forceinline__ void load(f2 (&t)[P], int k, int D) const {
+#pragma unroll
+        for (int i = 0; i < P; ++i) t[i] = both(1.f);
+        if (a) load_given<L, V>(t, a, k, D);
+        if (b) {
+            f2 u[P];
+            load_given<L, V>(u, b, k, D);
+#pragma unroll
+            for (int i = 0; i < P; ++i) t[i] = mul2(t[i], u[i]);
+        }
+    }
+    __device__ __forceinline__ void get(f2 (&t)[P], int k, int D) const {
+        if constexpr (KEEP) {
+#pragma unroll
+            for (int i = 0; i < P; ++i) t[i] = v[k][i];
+        } else {
+            load(t, k, D);
+        }
+    }
+};
+
+// Threads and vectors of a row: E elements a thread where that fills at least a block of 128.  F is given the
+// types and sizes.
+template <typename T, typename TR, int E, typename F>
 cudaError_t block_dispatch(int D, F &&f) {
-    constexpr int V = 16 / sizeof(T);
+    constexpr int V = 16 / sizeof(T), K = E / V;
     if (D % V == 0) {
-        const int n = D / V;  // at most 4096 (fp32)
-        if (n <= 32) return f.template operator()<T, TR, V, 1, 32>();
-        if (n <= 128) return f.template operator()<T, TR, V, 1, 128>();
-        if (n <= 256) return f.template operator()<T, TR, V, 1, 256>();
-        if (n <= 512) return f.template operator()<T, TR, V, 1, 512>();
-        if (n <= 1024) return f.template operator()<T, TR, V, 2, 512>();
-        return f.template operator()<T, TR, V, 16 / V, 1024>();
+        if (D == 128 * E) return f.template operator()<T, TR, V, K, 128, true>();
+        if (D == 256 * E) return f.template operator()<T, TR, V, K, 256, true>();
+        if (D == 512 * E) return f.template operator()<T, TR, V, K, 512, true>();
+        if (D <= 32 * E) return f.template operator()<T, TR, V, K, 32, false>();
+        if (D <= 128 * E) return f.template operator()<T, TR, V, K, 128, false>();
+        if (D <= 256 * E) return f.template operator()<T, TR, V, K, 256, false>();
+        if (D <= 512 * E) return f.template operator()<T, TR, V, K, 512, false>();
+        return f.template operator()<T, TR, V, 16 / V, 1024, false>();
     }
-    if (D <= 128) return f.template operator()<T, TR, 2, 2, 32>();
-    if (D <= 512) return f.template operator()<T, TR, 2, 2, 128>();
-    if (D <= 2048) return f.template operator()<T, TR, 2, 4, 256>();
-    if (D <= 8192) return f.template operator()<T, TR, 2, 8, 512>();
-    return f.template operator()<T, TR, 2, 8, 1024>();
+    if (D <= 128) return f.template operator()<T, TR, 2, 2, 32, false>();
+    if (D <= 512) return f.template operator()<T, TR, 2, 2, 128, false>();
+    if (D <= 2048) return f.template operator()<T, TR, 2, 4, 256, false>();
+    if (D <= 8192) return f.template operator()<T, TR, 2, 8, 512, false>();
+    return f.template operator()<T, TR, 2, 8, 1024, false>();
 }
 
-template <typename F>
+template <int E, typename F>
 cudaError_t block_types(const BlockParams &p, F &&f) {
-    if (!p.bf16) return block_dispatch<float, float>(p.D, f);
-    return p.res_f32 ? block_dispatch<__nv_bfloat16, float>(p.D, f) : block_dispatch<__nv_bfloat16, __nv_bfloat16>(p.D, f);
+    if (!p.bf16) return block_dispatch<float, float, E>(p.D, f);
+    return p.res_f32 ? block_dispatch<__nv_bfloat16, float, E>(p.D, f) : block_dispatch<__nv_bfloat16, __nv_bfloat16, E>(p.D, f);
 }
 
-// Registers that a thread of the backward may have, and with it the blocks of its grid: from the
-// sizes alone, since every block has a row of workspace.
-template <int kThreads>
-constexpr int block_bwd_regs() { return kThreads <= 512 ? 128 : 65536 / kThreads; }
+// Registers that a thread may have, and with it the blocks of a grid: in the backward from the sizes
+// alone, since every block has a row of workspace.
 constexpr int kBlockFwdRegs = 64;
+// (blocks of 128 threads: three an SM, with more rows in flight each, not four)
+constexpr int block_bwd_regs(int threads) { return threads <= 128 ? 168 : threads <= 512 ? 128 : 65536 / threads; }
 
 }  // namespace dn

@@ -11,14 +11,13 @@ namespace {
 
 extern __shared__ __align__(16) char s_ring[];
 
-template <typename T, typename TR, int V, int K, int R>
+template <typename T, typename TR, int V, int K, int R, bool FULL>
 __global__ void __launch_bounds__(Row<T, V, K, R>::kThreads, 65536 / (kBlockFwdRegs * Row<T, V, K, R>::kThreads)) block_fwd(BlockParams p) {
-    using L = Row<T, V, K, R>;
-    using G = BlockRing<T, TR, V, K, R, 2, 1, kBlockFwdRegs>;
+    using L = BlockRow<T, V, K, R, FULL>;
+    using G = BlockRing<T, TR, V, K, R, FULL, 1, 2, 1, kBlockFwdRegs>;
     constexpr int P = L::P, kBuf = 2 * (R / 32);
     __shared__ __align__(16) float buf[2 * kBuf + 4];  // consecutive norms in turn
     const float inv = 1.f / (float)p.D;
-    const Norm norm{p.D, p.eps, p.rms};
     const long long step = (long long)gridDim.x * L::kRows;
     long long row = (long long)blockIdx.x * L::kRows + threadIdx.x / R;
     G ring;
@@ -27,24 +26,38 @@ __global__ void __launch_bounds__(Row<T, V, K, R>::kThreads, 65536 / (kBlockFwdR
     ring.b[0] = static_cast<const TR *>(p.residual);
 #pragma unroll
     for (int s = 0; s < G::S; ++s) ring.issue(s_ring, s, row + s * step, p.rows, p.D);
-    Kept<L, V, K> w2, w1, sc;
-    w2.init(p.weight, p.D, 1.f);
-    w1.init(p.post_weight, p.D, 1.f);
-    sc.init(p.scale, p.D, 1.f);
+    // a single vector a thread: the fp32 vectors stay in registers
+    Kept<L, V, K, K == 1> w2, w1, sc;
+    Kept<L, V, K, false> b2, b1;
+    w2.init(p.weight, p.D);
+    w1.init(p.post_weight, p.D);
+    sc.init(p.scale, p.D);
+    b2.init(p.bias, p.D);
+    b1.init(p.post_bias, p.D);
     int stage = 0, turn = 0;
     for (long long first = (long long)blockIdx.x * L::kRows; first < p.rows; first += step, row += step) {
-        typename L::Pairs h;
+        f2 hs[1][K][P];
+        f2 (&h)[K][P] = hs[0];
         ring.wait();
 #pragma unroll
         for (int k = 0; k < K; ++k) ring.get_a(h[k], s_ring, stage, 0, k, row, p.rows, p.D);
-        if (p.post) {
-            normalise<L, V, K, R>(h, norm, inv, buf + turn * kBuf);
+        auto norm = [&] {  // h becomes its deviations over their root mean square
+            float m[1], r[1];
+            row_stats<L, V, K, R>(hs, p.rms, p.eps, inv, p.D, buf + turn * kBuf, m, r);
             turn ^= 1;
-        }
+            const f2 rr = both(r[0]);
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const f2 mm = L::inside(k, -m[0], p.D);
+#pragma unroll
+                for (int i = 0; i < P; ++i) h[k][i] = mul2(add2(h[k][i], mm), rr);
+            }
+        };
+        if (p.post) norm();
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             w1.times(h[k], k, p.D);
-            affine<L, V>(h[k], nullptr, p.post_bias, k, p.D);
+            b1.plus(h[k], k, p.D);
             if (p.z) {
                 f2 z[P];
                 ring.get_a(z, s_ring, stage, 1, k, row, p.rows, p.D);
@@ -59,16 +72,15 @@ __global__ void __launch_bounds__(Row<T, V, K, R>::kThreads, 65536 / (kBlockFwdR
         }
         ring.issue(s_ring, stage, row + G::S * step, p.rows, p.D);
         stage = stage + 1 == G::S ? 0 : stage + 1;
-        if (row < p.rows)
+        if (L::live(row, p.rows))
 #pragma unroll
             for (int k = 0; k < K; ++k) store_row<L, V>(static_cast<TR *>(p.residual_out) + row * p.D, h[k], k, p.D);
-        normalise<L, V, K, R>(h, norm, inv, buf + turn * kBuf);
-        turn ^= 1;
-        if (row < p.rows)
+        norm();
+        if (L::live(row, p.rows))
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 w2.times(h[k], k, p.D);
-                affine<L, V>(h[k], nullptr, p.bias, k, p.D);
+                b2.plus(h[k], k, p.D);
                 store_row<L, V>(static_cast<T *>(p.y) + row * p.D, h[k], k, p.D);
             }
     }
@@ -77,13 +89,13 @@ __global__ void __launch_bounds__(Row<T, V, K, R>::kThreads, 65536 / (kBlockFwdR
 struct Launch {
     const BlockParams &p;
     cudaStream_t stream;
-    template <typename T, typename TR, int V, int K, int R>
+    template <typename T, typename TR, int V, int K, int R, bool FULL>
     cudaError_t operator()() const {
         constexpr int kThreads = Row<T, V, K, R>::kThreads;
-        constexpr int bytes = BlockRing<T, TR, V, K, R, 2, 1, kBlockFwdRegs>::kBytes;
-        const cudaError_t err = allow_smem<block_fwd<T, TR, V, K, R>>(bytes);
+        constexpr int bytes = BlockRing<T, TR, V, K, R, FULL, 1, 2, 1, kBlockFwdRegs>::kBytes;
+        const cudaError_t err = allow_smem<block_fwd<T, TR, V, K, R, FULL>>(bytes);
         if (err != cudaSuccess) return err;
-        block_fwd<T, TR, V, K, R><<<norm_blocks(p.rows, kThreads, Row<T, V, K, R>::kRows, kBlockFwdRegs), kThreads, bytes, stream>>>(p);
+        block_fwd<T, TR, V, K, R, FULL><<<norm_blocks(p.rows, kThreads, Row<T, V, K, R>::kRows, kBlockFwdRegs), kThreads, bytes, stream>>>(p);
         return cudaGetLastError();
     }
 };
@@ -92,7 +104,7 @@ struct Launch {
 
 cudaError_t block_fwd_launch(const BlockParams &p, cudaStream_t stream, const char **name) {
     *name = p.bf16 ? "block_fwd<bf16>" : "block_fwd<f32>";
-    return block_types(p, Launch{p, stream});
+    return block_types<8>(p, Launch{p, stream});
 }
 
 }  // namespace dn

@@ -113,7 +113,7 @@ struct BlockParams {
     const void *dy, *dresidual_out;
     void *dx, *dresidual, *dz;
     float *dscale, *dpost_weight, *dpost_bias, *dweight, *dbias;
-    float *partial;  // [blocks][5][D]
+    float *partial;  // [blocks][2 or 4][D]
 };
 cudaError_t block_fwd_launch(const BlockParams &p, cudaStream_t stream, const char **name);
 cudaError_t block_bwd_launch(const BlockParams &p, cudaStream_t stream, const char **name);

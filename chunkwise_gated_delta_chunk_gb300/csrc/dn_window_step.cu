@@ -191,32 +191,39 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const unsigned (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-constexpr int kRows = 16;  // query heads of a block, of one key head
+__device__ __forceinline__ unsigned transposed(unsigned x) {  // an 8 x 8 matrix of 16 bits, a pair of a row a lane
+    unsigned y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
 
-template <int D>
+template <int D, int ROWS>
 struct StepSmem {
     static constexpr int kStage = 2 * kKeys * D * 2;  // keys and values
     static constexpr int kStages = 3;
     static constexpr int kWarp = kStages * kStage;
-    static constexpr int kPart = kRows * D * 4;  // a warp's o, over its stages
+    static constexpr int kPart = ROWS * D * 4;  // a warp's o, over its stages
     static_assert(kPart <= kWarp, "a warp's sums lie over its stages");
     static constexpr int kBytes = kWarps * kWarp + kPart;
 };
 
 extern __shared__ __align__(128) char s_step[];
 
-// Tensor-core form: 16 query heads of a key head (rows that do not exist are zeros) against 16
-// positions a warp at a time.  The memory rate bounds it: the products of 16 rows (mma.sync) take less
-// time than the positions' 2 x 16 x d values to come, which three stages of asynchronous
-// copies a warp keep in flight; no warp waits for another before the end.
-template <int D>
+// Tensor-core form (mma.sync): keys and values are the operands with 16 rows, the query heads of a key
+// head the one with 8 columns, twice where there are more than 8 (the other way round, 8 heads fill
+// half of 16 rows, and the products alone took as long as memory):
+//     S^T = K q^T,   O^T += V^T P^T,   P^T from S^T by two 8 x 8 transpositions.
+// The reference that weights are relative to moves up only when a score exceeds it by 2^8, so that a
+// group of positions needs no reduction but a vote.  Bound by memory: three stages of asynchronous copies a
+// warp keep the positions' 2 x 16 x d values coming; no warp waits for another before the end.
+template <int D, int ROWS>
 __global__ void __launch_bounds__(32 * kWarps, 2) step_bf16(const __grid_constant__ CacheParams p, unsigned blocks) {
     using T = __nv_bfloat16;
-    using S = StepSmem<D>;
-    constexpr int C = D / 8, NK = D / 16, PER = C / 2;  // 16-byte chunks of a row; k steps; rows that a lane copies
-    __shared__ float sm[kWarps][kRows], sl[kWarps][kRows], top[kRows], all[kRows];
+    using S = StepSmem<D, ROWS>;
+    constexpr int C = D / 8, NK = D / 16, NT = ROWS / 8, PER = C / 2;  // 16-byte chunks of a row; steps of 16 columns; tiles of heads; rows that a lane copies
+    __shared__ float sm[kWarps][ROWS], sl[kWarps][ROWS], top[ROWS], all[ROWS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const Job<T, D> job(p, blockIdx.x / blocks, kRows);
+    const Job<T, D> job(p, blockIdx.x / blocks, ROWS);
     const Seen seen(job.had, p);
     const int total = job.ok ? (seen.n + kKeys) / kKeys : 0;  // groups of positions, the new token among them
     const int first = (int)(blockIdx.x % blocks) * kWarps + warp, step = (int)blocks * kWarps;
@@ -237,88 +244,99 @@ __global__ void __launch_bounds__(32 * kWarps, 2) step_bf16(const __grid_constan
         copy_commit();
     };
     for (int s = 0; s < S::kStages - 1; ++s) fetch(first + s * step, s);
-    unsigned q[NK][4];
-    {
-        const T *src = static_cast<const T *>(p.q) + job.query(p, 0) + (lane % 4) * 2;
+    unsigned q[NT][NK][2];  // heads lane / 4 (and 8 behind it), columns 2 (lane % 4) and 8 behind them of every step
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int r = lane / 4 + 8 * t;
+        const T *src = static_cast<const T *>(p.q) + job.query(p, r < job.rows ? r : 0) + (lane % 4) * 2;
 #pragma unroll
         for (int i = 0; i < NK; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int r = lane / 4 + 8 * (e & 1);
-                q[i][e] = r < job.rows ? *reinterpret_cast<const unsigned *>(src + r * D + i * 16 + 8 * (e >> 1)) : 0u;
-            }
+            for (int e = 0; e < 2; ++e) q[t][i][e] = r < job.rows ? *reinterpret_cast<const unsigned *>(src + i * 16 + 8 * e) : 0u;
     }
     const float c = p.scale * kLog2e;
-    float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};  // rows lane / 4 and 8 behind it
-    float o[D / 8][4];
+    float m[NT][2], l[NT][2];  // heads 2 (lane % 4) and the next one: reference; this lane's part of the sum
+    float o[NT][NK][4];
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i)
+    for (int t = 0; t < NT; ++t) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+        for (int e = 0; e < 2; ++e) {
+            m[t][e] = -CUDART_INF_F;
+            l[t][e] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < NK; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[t][i][e] = 0.f;
+    }
     int stage = 0;
     for (int g = first; g < total; g += step) {
         fetch(g + (S::kStages - 1) * step, stage + S::kStages - 1 >= S::kStages ? stage - 1 : stage + S::kStages - 1);
         copy_wait<S::kStages - 1>();
         __syncwarp();
         const unsigned ks = base + stage * S::kStage, vs = ks + kKeys * D * 2;
-        float s[2][4] = {};
-#pragma unroll
-        for (int i = 0; i < NK; ++i) {
-            unsigned b[4];
+        float s[NT][2][4] = {};  // even and odd steps apart: half the chain
+        {
             // matrices: keys 0-7 and 8-15, columns 0-7 and 8-15 of the step
-            const int r = (lane & 7) + (lane >> 4) * 8, cc = 2 * i + (lane >> 3 & 1);
-            ldmatrix4(b, ks + r * D * 2 + ((cc ^ (r & 7)) << 4));
-            mma16816(s[0], q[i], b[0], b[1]);
-            mma16816(s[1], q[i], b[2], b[3]);
-        }
-        // positions behind the list weigh nothing
-        const int left = seen.n + 1 - g * kKeys;
-        float best[2] = {m[0], m[1]};
+            const int r = lane & 15, cc = lane >> 4;
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+            for (int i = 0; i < NK; ++i) {
+                unsigned a[4];
+                ldmatrix4(a, ks + r * D * 2 + (((2 * i + cc) ^ (r & 7)) << 4));
+#pragma unroll
+                for (int t = 0; t < NT; ++t) mma16816(s[t][i & 1], a, q[t][i][0], q[t][i][1]);
+            }
+        }
+        // keys lane / 4 (elements 0, 1) and 8 behind it (2, 3); positions behind the list weigh nothing
+        const int left = seen.n + 1 - g * kKeys - lane / 4;
+        bool above = false;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                s[t][e] = t * 8 + (lane & 3) * 2 + (e & 1) < left ? s[t][e] * c : -CUDART_INF_F;
-                best[e >> 1] = fmaxf(best[e >> 1], s[t][e]);
+                s[t][0][e] = (e >> 1) * 8 < left ? (s[t][0][e] + s[t][1][e]) * c : -CUDART_INF_F;
+                above |= s[t][0][e] > m[t][e & 1] + 8.f;
             }
-        bool moved = false;
+        if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            best[h] = fmaxf(best[h], __shfl_xor_sync(0xffffffffu, best[h], 1));
-            best[h] = fmaxf(best[h], __shfl_xor_sync(0xffffffffu, best[h], 2));
-            moved |= best[h] != m[h];
-        }
-        if (__any_sync(0xffffffffu, moved)) {
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float f = ex2(m[h] - (best[h] == -CUDART_INF_F ? 0.f : best[h]));
-                m[h] = best[h];
-                l[h] *= f;
+                for (int e = 0; e < 2; ++e) {
+                    float best = fmaxf(m[t][e], fmaxf(s[t][0][e], s[t][0][e + 2]));
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    o[i][2 * h] *= f;
-                    o[i][2 * h + 1] *= f;
+                    for (int x = 4; x < 32; x <<= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, x));
+                    const float f = ex2(m[t][e] - (best == -CUDART_INF_F ? 0.f : best));
+                    m[t][e] = best;
+                    l[t][e] *= f;
+#pragma unroll
+                    for (int i = 0; i < NK; ++i) {
+                        o[t][i][e] *= f;
+                        o[t][i][e + 2] *= f;
+                    }
                 }
-            }
         }
-        unsigned a[4];
+        unsigned w[NT][2];
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < NT; ++t) {
+            float x[4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float from = m[h] == -CUDART_INF_F ? 0.f : m[h];
-                const float x = ex2(s[t][2 * h] - from), y = ex2(s[t][2 * h + 1] - from);
-                l[h] += x + y;
-                a[2 * t + h] = Vec<T, 2>::pack(x, y);
+            for (int e = 0; e < 4; ++e) {
+                x[e] = ex2(s[t][0][e] - (m[t][e & 1] == -CUDART_INF_F ? 0.f : m[t][e & 1]));
+                l[t][e & 1] += x[e];
             }
+            w[t][0] = transposed(Vec<T, 2>::pack(x[0], x[1]));
+            w[t][1] = transposed(Vec<T, 2>::pack(x[2], x[3]));
+        }
+        {
+            // transposed: columns 0-7 and 8-15 of the step, keys 0-7 and 8-15
+            const int r = (lane & 7) + (lane >> 4) * 8, cc = lane >> 3 & 1;
 #pragma unroll
-        for (int i = 0; i < NK; ++i) {
-            unsigned b[4];
-            // transposed: keys 0-7 and 8-15, columns 0-7 and 8-15 of the pair of tiles
-            const int r = (lane & 7) + (lane >> 3 & 1) * 8, cc = 2 * i + (lane >> 4);
-            ldmatrix4t(b, vs + r * D * 2 + ((cc ^ (r & 7)) << 4));
-            mma16816(o[2 * i], a, b[0], b[1]);
-            mma16816(o[2 * i + 1], a, b[2], b[3]);
+            for (int i = 0; i < NK; ++i) {
+                unsigned a[4];
+                ldmatrix4t(a, vs + r * D * 2 + (((2 * i + cc) ^ (r & 7)) << 4));
+#pragma unroll
+                for (int t = 0; t < NT; ++t) mma16816(o[t][i], a, w[t][0], w[t][1]);
+            }
         }
         __syncwarp();
         stage = stage + 1 == S::kStages ? 0 : stage + 1;
@@ -327,21 +345,25 @@ __global__ void __launch_bounds__(32 * kWarps, 2) step_bf16(const __grid_constan
     __syncwarp();
     float *part = reinterpret_cast<float *>(mine);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int r = lane / 4 + 8 * h;
-        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-        if ((lane & 3) == 0) {
-            sm[warp][r] = m[h];
-            sl[warp][r] = l[h];
-        }
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-            *reinterpret_cast<float2 *>(part + r * D + i * 8 + (lane & 3) * 2) = make_float2(o[i][2 * h], o[i][2 * h + 1]);
-    }
+        for (int e = 0; e < 2; ++e) {
+            const int r = 8 * t + 2 * (lane & 3) + e;
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], x);
+            if (lane < 4) {
+                sm[warp][r] = m[t][e];
+                sl[warp][r] = l[t][e];
+            }
+#pragma unroll
+            for (int i = 0; i < NK; ++i) {
+                part[r * D + i * 16 + lane / 4] = o[t][i][e];
+                part[r * D + i * 16 + lane / 4 + 8] = o[t][i][e + 2];
+            }
+        }
     if (job.ok && job.row0 == 0 && blockIdx.x % blocks == 0) job.keep(p);
-    join<T, D, kRows>(p, job, reinterpret_cast<const float *>(s_step), S::kWarp / 4, sm, sl,
-                      reinterpret_cast<float *>(s_step + kWarps * S::kWarp), top, all, blocks);
+    join<T, D, ROWS>(p, job, reinterpret_cast<const float *>(s_step), S::kWarp / 4, sm, sl,
+                     reinterpret_cast<float *>(s_step + kWarps * S::kWarp), top, all, blocks);
 }
 
 // ---- fp32 -------------------------------------------------------------------
@@ -536,15 +558,16 @@ cudaError_t window_fill_launch(const CacheParams &p, bool bf16, cudaStream_t str
 
 namespace {
 
-// Blocks of a cluster, that share a sequence's positions: as many as it takes to put two blocks on
-// every SM, while each warp still has two groups of positions.
+// Blocks of a cluster, that share a sequence's positions: as many as it takes to put a block on every
+// SM, while each warp still has two groups of positions (twice as many, 256 jobs of 2048 positions
+// took 47 us instead of 42).
 template <auto kKernel>
 cudaError_t step_launch(const CacheParams &p, int rows, int bytes, cudaStream_t stream) {
     const int G = p.Nq / p.Nk;
     const long long jobs = (long long)p.N * p.Nk * ((G + rows - 1) / rows);
     const long long most = (long long)p.sinks + p.window;
     unsigned blocks = 1;
-    while (blocks < 16 && jobs * blocks < 2 * kSms && most > (long long)blocks * kWarps * kKeys * 2) blocks *= 2;
+    while (blocks < 16 && jobs * blocks < kSms && most > (long long)blocks * kWarps * kKeys * 2) blocks *= 2;
     if (jobs * blocks > 0x7fffffffll) return cudaErrorInvalidValue;
     cudaError_t err = allow_smem<kKernel>(bytes);
     if (err == cudaSuccess && blocks > 8) err = allow_wide_cluster<kKernel>();
@@ -578,8 +601,11 @@ cudaError_t window_step_launch(const CacheParams &p, bool bf16, cudaStream_t str
     *name = bf16 ? "window_step<bf16>" : "window_step<f32>";
     if (p.N == 0) return cudaSuccess;
     if (!bf16) return p.d == 64 ? step_f32_launch<64>(p, stream) : step_f32_launch<128>(p, stream);
-    return p.d == 64 ? step_launch<step_bf16<64>>(p, kRows, StepSmem<64>::kBytes, stream)
-                     : step_launch<step_bf16<128>>(p, kRows, StepSmem<128>::kBytes, stream);
+    if (p.Nq / p.Nk <= 8)
+        return p.d == 64 ? step_launch<step_bf16<64, 8>>(p, 8, StepSmem<64, 8>::kBytes, stream)
+                         : step_launch<step_bf16<128, 8>>(p, 8, StepSmem<128, 8>::kBytes, stream);
+    return p.d == 64 ? step_launch<step_bf16<64, 16>>(p, 16, StepSmem<64, 16>::kBytes, stream)
+                     : step_launch<step_bf16<128, 16>>(p, 16, StepSmem<128, 16>::kBytes, stream);
 }
 
 }  // namespace dn
