@@ -5,20 +5,27 @@
 //     dk = scale ds^T q,  dv = p^T do   (window_dkv: tiles of 128 keys, one key head; the
 //                                        group's heads' queries and do stream by)
 //
-// Two kernels, so that no sum is added by atomics: 7 products of 128 x 128 x d a tile
-// instead of 5, but every sum stays in tensor memory until it is done, in a fixed order.
-// D comes first, from a pass of its own over o and do at the memory's rate (window_dsum).
+// Two kernels, so that no sum is added by atomics: every sum stays in tensor memory until it is
+// done, in a fixed order, for 8 products of 128 x 128 x d a tile instead of 5.
+//
+// D.  Taken from the rounded o it is off by about half a step of a bf16 of its terms, which at windows
+// of a few keys is more than the roundings of p and ds make (dq and dk 1.5 to 2.7 times as far off
+// as rounding the result alone; 1.42 with an exact D).  So a first pass over o and do (window_dsum) gives
+// an approximate D', and window_dq sums the exact D = sum p dp of its rows beside its products, along with
+// C = sum p k:
+//     dq = scale (sum p (dp - D') k + (D' - D) C)
+// and leaves D for window_dkv.
 //
 // Warps 0-3 and 4-7: the first and the second 64 columns of every tile of scores, one row a
 // thread; warp 8: TMA loads, and the plans of the items; warp 9: the MMAs; warp 10 (window_dkv): the
 // columns' lse and D into shared memory.
 //
-// window_dq, tensor memory: S, dP (128 columns each), dQ (d), dS as bf16 (2 x 64).  As soon as
-// S and dP of a tile are in registers the tensor cores go on with those of the next one.
-// window_dkv: S^T and dP^T (overwritten by P^T and dS^T as bf16), dV and dK.  The products
-// alternate with the threads' work on the other matrix:
-//     threads   P(n)        dS(n)          P(n+1)
-//     MMAs      ...         dV(n) S(n+1)   dK(n) dP(n+1)
+// Tensor memory: S and dP of a tile (128 columns each; P and dS overwrite the first half of each half of
+// them as bf16), and two accumulators of d columns.  The products alternate with the threads' work on the
+// other matrix:
+//     threads   P(n)        dS(n)                     P(n+1)
+//     MMAs      ...         C(n) or dV(n), S(n+1)     dQ(n) or dK(n), dP(n+1)
+// (window_dkv has the transposed tiles: rows are keys.)
 //
 // All queries see the sinks.  Query tiles behind the window of the first key tile are taken
 // in parts (a run of part_tiles tiles each) by items of their own, which leave fp32 sums of
@@ -48,8 +55,8 @@ struct Lay {
     static constexpr uint32_t kPlan = kCols + (DQ ? 0 : NX * 1024), kBar = kPlan + kPlans * 64;
     static constexpr int bHold = 0, bHoldEmpty = 1, bX = 2, bXEmpty = bX + NX, bY = bXEmpty + NX, bYEmpty = bY + NY, bCol = bYEmpty + NY,
                          bS = bCol + NX, bDP = bS + 1, bP = bDP + 1, bDS = bP + 1, bOut = bDS + 1, bOutEmpty = bOut + 1,
-                         bPlan = bOutEmpty + 1, bDrain = bPlan + kPlans, kBars = bDrain + 1;
-    static constexpr uint32_t kMisc = kBar + 8 * kBars, kAlloc = kMisc + 16 + 1024;
+                         bPlan = bOutEmpty + 1, bDrain = bPlan + kPlans, bPair = bDrain + 1, kBars = bPair + 4;
+    static constexpr uint32_t kBox = (kBar + 8 * kBars + 15) / 16 * 16, kMisc = kBox + (DQ ? 2 * 128 * 4 : 0), kAlloc = kMisc + 16 + 1024;
     static_assert(kAlloc <= 232448, "exceeds the 227 KB of shared memory per CTA");
 };
 
@@ -110,25 +117,32 @@ struct Base {
     // N columns of an accumulator times f, to bf16; true where one of the lane's row is not finite.  `to`: the
     // lane's row, of a tensor with `stride` elements from row to row; of the warp's 32 rows those from
     // from_row up to rows are written.
-    template <int N>
-    __device__ __forceinline__ bool store_cols(uint32_t from, __nv_bfloat16 *to, long long stride, int from_row, int rows, float f) const {
+    // ADD: plus f2nd times the accumulator at `second`.
+    template <int N, bool ADD = false>
+    __device__ __forceinline__ bool store_cols(uint32_t from, __nv_bfloat16 *to, long long stride, int from_row, int rows, float f,
+                                               uint32_t second = 0, float f2nd = 0.f) const {
         f2 bad = 0ull;
         const f2 ff = both(f);
 #pragma unroll 1
         for (int c = 0; c < N; c += 64) {
-            uint32_t o[2][32], w[4][8];
-            tmem_ld32(from + c, o[0]);
-            tmem_ld32(from + c + 32, o[1]);
-            tmem_wait_ld();
-            tmem_ld_dep(o[0]);
-            tmem_ld_dep(o[1]);
+            uint32_t w[4][8];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-                const f2 v = mul2(pair(__uint_as_float(o[e >> 4][2 * (e & 15)]), __uint_as_float(o[e >> 4][2 * (e & 15) + 1])), ff);
-                bad = fma2(v, 0ull, bad);  // 0 times infinity or NaN stays
-                float lo, hi;
-                split(v, lo, hi);
-                w[e >> 3][e & 7] = pack_bf16(lo, hi);
+            for (int h = 0; h < 2; ++h) {
+                uint32_t o[32], a[ADD ? 32 : 1];
+                tmem_ld32(from + c + 32 * h, o);
+                if constexpr (ADD) tmem_ld32(second + c + 32 * h, a);
+                tmem_wait_ld();
+                tmem_ld_dep(o);
+                if constexpr (ADD) tmem_ld_dep(a);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    f2 v = mul2(pair(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])), ff);
+                    if constexpr (ADD) v = fma2(pair(__uint_as_float(a[2 * e]), __uint_as_float(a[2 * e + 1])), both(f2nd), v);
+                    bad = fma2(v, 0ull, bad);  // 0 times infinity or NaN stays
+                    float lo, hi;
+                    split(v, lo, hi);
+                    w[2 * h + (e >> 3)][e & 7] = pack_bf16(lo, hi);
+                }
             }
             store_rows64(to + c, stride, from_row, rows, w);
         }
@@ -156,7 +170,7 @@ struct Dq : Base<D, true, QueryPlan> {
     using B::x;
     unsigned items;
     long long slots;
-    static constexpr uint32_t tS = 0, tDP = 128, tDQ = 256, tDS = 384;
+    static constexpr uint32_t tS = 0, tDP = 128, tDQ = 256, tC = 384;
 
     // late tiles first: under a causal mask these are the long ones
     __device__ __forceinline__ bool plan(Plan &u, unsigned item) const {
@@ -211,16 +225,29 @@ struct Dq : Base<D, true, QueryPlan> {
     }
 
     __device__ __forceinline__ bool issue_s(uint32_t lead, bool small, unsigned k) const {
-        const uint32_t id = small ? idesc_bf16(128, kSinkCols, 0, 0) : idesc_bf16(128, 128, 0, 0);
         if (!B::full_x(k)) return false;
         tc_fence_after();
-        B::mma_rows(lead, tS, Y::kA, B::at_x(k), id);
+        B::mma_rows(lead, tS, Y::kA, B::at_x(k), small ? idesc_bf16(128, kSinkCols, 0, 0) : idesc_bf16(128, 128, 0, 0));
+        commit_by(lead, bar(Y::bS));
+        return true;
+    }
+    __device__ __forceinline__ bool issue_dp(uint32_t lead, bool small, unsigned k) const {
         if (!B::full_y(k)) return false;
         tc_fence_after();
-        B::mma_rows(lead, tDP, Y::kB, B::at_y(k), id);
-        commit_by(lead, bar(Y::bS));
+        B::mma_rows(lead, tDP, Y::kB, B::at_y(k), small ? idesc_bf16(128, kSinkCols, 0, 0) : idesc_bf16(128, 128, 0, 0));
+        commit_by(lead, bar(Y::bDP));
         commit_by(lead, bar(Y::bYEmpty + k % Y::NY));
         return true;
+    }
+    // acc += a K, the bf16 halves of a 64 columns apart
+    __device__ __forceinline__ void issue_acc(uint32_t lead, uint32_t acc, uint32_t a, unsigned k, bool small, bool more) const {
+        const uint32_t b = cols_of(x.base + B::at_x(k));
+        constexpr uint32_t id = idesc_bf16(128, D, 0, 1);
+        mma_ts_by(lead, tm + acc, tm + a, b, id, more);
+        mma_ts_by(lead, tm + acc, tm + a + 8, b + 128, id, 1);
+        if (!small)
+#pragma unroll
+            for (int kk = 2; kk < 8; ++kk) mma_ts_by(lead, tm + acc, tm + a + 64 * (kk >> 2) + 8 * (kk & 3), b + 128 * kk, id, 1);
     }
 
     __device__ void mma() {
@@ -230,28 +257,26 @@ struct Dq : Base<D, true, QueryPlan> {
         Plan u;
         for (; fine && B::next_plan(u, qn); ++qn) {
             const int n = u.rounds;
-            fine = hold(x, bar(Y::bHold), qn & 1) && issue_s(lead, u.small(0), k);
-            for (int i = 0; fine && i < n; ++i, ++k) {
-                // both in registers: the next tile's may come
+            if (!(fine = hold(x, bar(Y::bHold), qn & 1) && issue_s(lead, u.small(0), k) && issue_dp(lead, u.small(0), k))) break;
+            if (n == 1) commit_by(lead, bar(Y::bHoldEmpty));
+            if (!(fine = hold(x, bar(Y::bOutEmpty), (qn & 1) ^ 1))) break;
+#pragma unroll 1
+            for (int i = 0; i < n; ++i, ++k) {
+                const bool small = u.small(i);
                 if (!(fine = hold(x, bar(Y::bP), k & 1))) break;
-                if (i + 1 < n) {
-                    if (!(fine = issue_s(lead, false, k + 1))) break;
-                    if (i + 2 == n) commit_by(lead, bar(Y::bHoldEmpty));  // the last that read q and do
-                } else if (n == 1) {
-                    commit_by(lead, bar(Y::bHoldEmpty));
-                }
-                if (i == 0 && !(fine = hold(x, bar(Y::bOutEmpty), (qn & 1) ^ 1))) break;
+                tc_fence_after();
+                issue_acc(lead, tC, tS, k, small, i > 0);
+                if (i + 1 < n && !(fine = issue_s(lead, false, k + 1))) break;
                 if (!(fine = hold(x, bar(Y::bDS), k & 1))) break;
                 tc_fence_after();
-                const uint32_t b = cols_of(x.base + B::at_x(k)), a = tm + tDS + 64 * (k & 1);
-                constexpr uint32_t id = idesc_bf16(128, D, 0, 1);
-                mma_ts_by(lead, tm + tDQ, a, b, id, i != 0);
-                mma_ts_by(lead, tm + tDQ, a + 8, b + 128, id, 1);
-                if (!u.small(i))
-#pragma unroll
-                    for (int kk = 2; kk < 8; ++kk) mma_ts_by(lead, tm + tDQ, a + 8 * kk, b + 128 * kk, id, 1);
+                issue_acc(lead, tDQ, tDP, k, small, i > 0);
                 commit_by(lead, bar(Y::bXEmpty + k % Y::NX));
-                if (i + 1 == n) commit_by(lead, bar(Y::bOut));
+                if (i + 1 < n) {
+                    if (!(fine = issue_dp(lead, false, k + 1))) break;
+                    if (i + 2 == n) commit_by(lead, bar(Y::bHoldEmpty));  // the last that read q and do
+                } else {
+                    commit_by(lead, bar(Y::bOut));
+                }
             }
         }
         commit_by(lead, bar(Y::bDrain));
@@ -272,56 +297,87 @@ struct Dq : Base<D, true, QueryPlan> {
             const float lse2 = live ? p.lse[at] * kLog2e : 0.f;
             const float dsum = live ? p.dsum[at] : 0.f;
             const f2 cc = both(c), ll = both(-lse2), dd = both(-dsum);
+            f2 exact = 0ull;  // this thread's part of sum p dp
             for (int i = 0; i < u.rounds; ++i, ++k) {
                 const int k0 = u.kt.tile(i) * 128 + 64 * w;
                 const int cols = u.small(i) ? (w == 0 ? 1 : 0) : 2;  // groups of 32 columns
                 const bool edge = k0 + 63 > u.t0 || u.t0 + 127 - k0 >= p.window;
                 if (!hold(x, bar(Y::bS), k & 1)) return;
                 tc_fence_after();
-                uint32_t s[2][32], g[2][32];
+                uint32_t s[2][32];
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
-                    if (q < cols) {
-                        tmem_ld32(lane + tS + 64 * w + 32 * q, s[q]);
-                        tmem_ld32(lane + tDP + 64 * w + 32 * q, g[q]);
-                    }
+                    if (q < cols) tmem_ld32(lane + tS + 64 * w + 32 * q, s[q]);
                 tmem_wait_ld();
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     tmem_ld_dep(s[q]);
-                    tmem_ld_dep(g[q]);
+                    if (q >= cols) continue;
+                    const uint32_t mask = edge ? seen32(t, k0 + 32 * q, sight) : 0xffffffffu;
+                    uint32_t v[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        float a, b;
+                        split(fma2(pair(__uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1])), cc, ll), a, b);
+                        a = ex2(a);
+                        b = ex2(b);
+                        if (edge) {
+                            a = mask >> e & 1 ? a : 0.f;
+                            b = mask >> (e + 1) & 1 ? b : 0.f;
+                        }
+                        s[q][e] = __float_as_uint(a);
+                        s[q][e + 1] = __float_as_uint(b);
+                        v[e / 2] = pack_bf16(a, b);
+                    }
+                    tmem_st16(lane + tS + 64 * w + 16 * q, v);
                 }
+                tmem_wait_st();
                 tc_fence_before();
                 warp_arrive(bar(Y::bP));
+                if (!hold(x, bar(Y::bDP), k & 1)) return;
+                tc_fence_after();
 #pragma unroll
-                for (int q = 0; q < 2; ++q)
-                    if (q < cols) {
-                        uint32_t ds[16];
+                for (int q = 0; q < 2; ++q) {  // one after the other: both do not fit beside p
+                    if (q >= cols) continue;
+                    uint32_t g[32], v[16];
+                    tmem_ld32(lane + tDP + 64 * w + 32 * q, g);
+                    tmem_wait_ld_dep(g);
+                    if (edge) {  // a masked value may be anything
+                        const uint32_t mask = seen32(t, k0 + 32 * q, sight);
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            float a, b;
-                            split(fma2(pair(__uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1])), cc, ll), a, b);
-                            split(mul2(pair(ex2(a), ex2(b)), add2(pair(__uint_as_float(g[q][e]), __uint_as_float(g[q][e + 1])), dd)), a, b);
-                            ds[e / 2] = pack_bf16(a, b);
-                        }
-                        if (edge) {
-                            const uint32_t mask = seen32(t, k0 + 32 * q, sight);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)  // pairs of a 16-bit half each
-                                ds[e] &= (mask >> (2 * e) & 1 ? 0xffffu : 0u) | (mask >> (2 * e + 1) & 1 ? 0xffff0000u : 0u);
-                        }
-                        tmem_st16(lane + tDS + 64 * (k & 1) + 32 * w + 16 * q, ds);
+                        for (int e = 0; e < 32; ++e) g[e] = mask >> e & 1 ? g[e] : 0u;
                     }
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const f2 w2 = pair(__uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]));
+                        const f2 dp = pair(__uint_as_float(g[e]), __uint_as_float(g[e + 1]));
+                        exact = fma2(w2, dp, exact);
+                        float a, b;
+                        split(mul2(w2, add2(dp, dd)), a, b);
+                        v[e / 2] = pack_bf16(a, b);
+                    }
+                    tmem_st16(lane + tDP + 64 * w + 16 * q, v);
+                }
                 tmem_wait_st();
                 tc_fence_before();
                 warp_arrive(bar(Y::bDS));
             }
+            // D of the row from its two threads
+            volatile float *box = reinterpret_cast<float *>(x.gbase + Y::kBox) + row;
+            const float mine = sum_of(exact);
+            box[128 * w] = mine;
+            warp_arrive(bar(Y::bPair + (warp & 3)));
+            if (!hold(x, bar(Y::bPair + (warp & 3)), qn & 1)) return;
+            const float full = mine + box[128 * (w ^ 1)];
+            if (w == 0 && live) p.dsum[at] = full;
             if (!hold(x, bar(Y::bOut), qn & 1)) return;
             tc_fence_after();
-            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.dq) + at * D;
             bool nan = false;
-            if (D == 128 || w == 0)
-                nan = B::template store_cols<64>(lane + tDQ + 64 * w, out + 64 * w, (long long)p.Nq * D, 0, u.L - (t & ~31), p.scale);
+            if (D == 128 || w == 0) {
+                const float off = dsum - full;
+                nan = B::template store_cols<64, true>(lane + tDQ + 64 * w, static_cast<__nv_bfloat16 *>(p.dq) + at * D + 64 * w,
+                                                       (long long)p.Nq * D, 0, u.L - (t & ~31), p.scale, lane + tC + 64 * w, off * p.scale);
+            }
             tc_fence_before();
             warp_arrive(bar(Y::bOutEmpty));
             B::mark(nan, u.flag);
@@ -662,6 +718,7 @@ __device__ __forceinline__ void set_up(F &f, uint8_t *raw_smem, unsigned *status
         mbar_init(f.bar(Y::bOutEmpty), 8);
         for (int i = 0; i < kPlans; ++i) mbar_init(f.bar(Y::bPlan + i), 1);
         mbar_init(f.bar(Y::bDrain), 1);
+        for (int i = 0; i < 4; ++i) mbar_init(f.bar(Y::bPair + i), 2);
         *f.x.abort_flag = 0;
         fence_barrier_init();
     }
@@ -763,7 +820,7 @@ __global__ void __launch_bounds__(256) window_sink_sums(WindowParams p, Parts pa
     }
 }
 
-// D = sum do o of every token and head: 16 bytes of both a thread, D / 8 threads a row.
+// D' = sum do o of every token and head: 16 bytes of both a thread, D / 8 threads a row.
 template <int D>
 __global__ void __launch_bounds__(256) window_dsum(WindowParams p, long long rows) {
     constexpr int L = D / 8, ROWS = 4;  // rows in flight of a thread
