@@ -302,32 +302,39 @@ private:
     }
 };
 
+constexpr int kBlockMaxCols = 16384;
+
 // Threads and vectors of a row: E elements a thread where that fills at least a block of 128.  F is given the
-// types and sizes.
-template <typename T, typename TR, int E, typename F>
+// types and sizes; it is called for widths from MIN to MAX, and only what these reach is compiled.
+template <typename T, typename TR, int E, int MIN = 1, int MAX = 1 << 30, typename F>
 cudaError_t block_dispatch(int D, F &&f) {
     constexpr int V = 16 / sizeof(T), K = E / V;
+    // a row of `w` columns, and the rows of up to `w` behind those of up to `below`
+#define DN_BLOCK_FULL(w, R) \
+    if constexpr (w >= MIN && w <= MAX)  \
+        if (D == w) return f.template operator()<T, TR, V, K, R, true>();
+#define DN_BLOCK_UP_TO(w, below, V, K, R) \
+    if constexpr (w >= MIN && below < MAX) \
+        if (D <= w) return f.template operator()<T, TR, V, K, R, false>();
     if (D % V == 0) {
-        if (D == 128 * E) return f.template operator()<T, TR, V, K, 128, true>();
-        if (D == 256 * E) return f.template operator()<T, TR, V, K, 256, true>();
-        if (D == 512 * E) return f.template operator()<T, TR, V, K, 512, true>();
-        if (D <= 32 * E) return f.template operator()<T, TR, V, K, 32, false>();
-        if (D <= 128 * E) return f.template operator()<T, TR, V, K, 128, false>();
-        if (D <= 256 * E) return f.template operator()<T, TR, V, K, 256, false>();
-        if (D <= 512 * E) return f.template operator()<T, TR, V, K, 512, false>();
-        return f.template operator()<T, TR, V, 16 / V, 1024, false>();
+        DN_BLOCK_FULL(128 * E, 128)
+        DN_BLOCK_FULL(256 * E, 256)
+        DN_BLOCK_FULL(512 * E, 512)
+        DN_BLOCK_UP_TO(32 * E, 0, V, K, 32)
+        DN_BLOCK_UP_TO(128 * E, 32 * E, V, K, 128)
+        DN_BLOCK_UP_TO(256 * E, 128 * E, V, K, 256)
+        DN_BLOCK_UP_TO(512 * E, 256 * E, V, K, 512)
+        DN_BLOCK_UP_TO(kBlockMaxCols, 512 * E, V, 16 / V, 1024)
+    } else {
+        DN_BLOCK_UP_TO(128, 0, 2, 2, 32)
+        DN_BLOCK_UP_TO(512, 128, 2, 2, 128)
+        DN_BLOCK_UP_TO(2048, 512, 2, 4, 256)
+        DN_BLOCK_UP_TO(8192, 2048, 2, 8, 512)
+        DN_BLOCK_UP_TO(kBlockMaxCols, 8192, 2, 8, 1024)
     }
-    if (D <= 128) return f.template operator()<T, TR, 2, 2, 32, false>();
-    if (D <= 512) return f.template operator()<T, TR, 2, 2, 128, false>();
-    if (D <= 2048) return f.template operator()<T, TR, 2, 4, 256, false>();
-    if (D <= 8192) return f.template operator()<T, TR, 2, 8, 512, false>();
-    return f.template operator()<T, TR, 2, 8, 1024, false>();
-}
-
-template <int E, typename F>
-cudaError_t block_types(const BlockParams &p, F &&f) {
-    if (!p.bf16) return block_dispatch<float, float, E>(p.D, f);
-    return p.res_f32 ? block_dispatch<__nv_bfloat16, float, E>(p.D, f) : block_dispatch<__nv_bfloat16, __nv_bfloat16, E>(p.D, f);
+#undef DN_BLOCK_FULL
+#undef DN_BLOCK_UP_TO
+    return cudaErrorInvalidValue;
 }
 
 // Registers that a thread may have, and with it the blocks of a grid: in the backward from the sizes
@@ -335,5 +342,11 @@ cudaError_t block_types(const BlockParams &p, F &&f) {
 constexpr int kBlockFwdRegs = 64;
 // (blocks of 128 threads: three an SM, with more rows in flight each, not four)
 constexpr int block_bwd_regs(int threads) { return threads <= 128 ? 168 : threads <= 512 ? 128 : 65536 / threads; }
+
+// The backward, of one type each; the grid's size alone where `blocks` is not null.
+cudaError_t block_bwd_f32(const BlockParams &p, bool bias, cudaStream_t stream, int *blocks);
+cudaError_t block_bwd_bf16(const BlockParams &p, bool bias, cudaStream_t stream, int *blocks);
+cudaError_t block_bwd_bf16_f32(const BlockParams &p, bool bias, cudaStream_t stream, int *blocks);
+cudaError_t block_bwd_sums_launch(const BlockParams &p, int blocks, int planes, cudaStream_t stream);
 
 }  // namespace dn

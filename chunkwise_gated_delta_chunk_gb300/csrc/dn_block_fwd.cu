@@ -104,7 +104,9 @@ struct Launch {
 
 cudaError_t block_fwd_launch(const BlockParams &p, cudaStream_t stream, const char **name) {
     *name = p.bf16 ? "block_fwd<bf16>" : "block_fwd<f32>";
-    return block_types<8>(p, Launch{p, stream});
+    const Launch f{p, stream};
+    if (!p.bf16) return block_dispatch<float, float, 8>(p.D, f);
+    return p.res_f32 ? block_dispatch<__nv_bfloat16, float, 8>(p.D, f) : block_dispatch<__nv_bfloat16, __nv_bfloat16, 8>(p.D, f);
 }
 
 }  // namespace dn
