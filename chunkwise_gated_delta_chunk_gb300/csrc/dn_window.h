@@ -25,11 +25,12 @@ struct WindowParams {
     void *dq, *dk, *dv;
     float *dsum;      // [tokens, Nq] sum over d of dout o
     unsigned *redo;   // [slots of kWinTile tokens][2 halves][Nq + Nk]: marks of dq, and of dk and dv
-    // tensor-core kernels: fp32 parts of the sinks' dv and dk, [slots of part_tiles tiles, then
-    // sequences][Nk][2][sinks][d], where some query sees the sinks by themselves (parts)
+    // fp32 parts of the sinks' dv and dk, where some query sees the sinks by themselves (parts):
+    // [slots of part_tiles tiles][part_heads, Nk or Nq], then [sequences][Nk], of [2][sinks][d]
     float *sink_part;
     bool parts;
-    int part_tiles;
+    int part_tiles, part_heads;
+    float *head_part;  // CUDA-core kernels: [tokens][Nq][2][d] dv and dk of single query heads, or null
 };
 
 // A row of o that came out with a NaN may hold what a masked key's value did (0 times
@@ -50,6 +51,9 @@ cudaError_t window_tc_bwd(const WindowParams &p, cudaStream_t stream);
 // CUDA-core kernels: fp32 tensors, and (redo) rows that the other kernels marked.
 cudaError_t window_simt_fwd(const WindowParams &p, bool bf16, bool redo, cudaStream_t stream);
 cudaError_t window_simt_bwd(const WindowParams &p, bool bf16, bool redo, cudaStream_t stream);
+
+// The sinks' rows of dk and dv from their parts, where there are any.
+cudaError_t window_sink_sums(const WindowParams &p, bool bf16, cudaStream_t stream);
 
 struct CacheParams {
     const void *q, *k, *v;  // step: [N, Nq, d], [N, Nk, d]; fill: k, v [tokens, Nk, d]

@@ -29,7 +29,7 @@
 //
 // All queries see the sinks.  Query tiles behind the window of the first key tile are taken
 // in parts (a run of part_tiles tiles each) by items of their own, which leave fp32 sums of
-// the sinks' rows; window_sink_sums adds them up in order.
+// the sinks' rows; window_sink_sums (dn_window.cu) adds them up in order.
 #include "dn_window_tc.cuh"
 
 namespace dn {
@@ -785,41 +785,6 @@ window_dkv(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
     clear_up(f.tm);
 }
 
-// The sinks' rows of dk and dv: the part of the first key tile's own item and those of the runs of
-// query tiles behind its window, in order.  Four columns a thread.
-template <int D>
-__global__ void __launch_bounds__(256) window_sink_sums(WindowParams p, Parts parts) {
-    wait_for_launches();
-    const int hk = blockIdx.x % p.Nk, n = blockIdx.x / p.Nk;
-    const SeqTile s = seq_whole(p.seq, n);
-    if (!s.ok || s.eos == s.bos) return;
-    const int L = (int)(s.eos - s.bos);
-    const QueryTiles qt(0, L < 128 ? L : 128, L, 128, Sight{p.window, p.sinks});
-    if (qt.end <= qt.last) return;
-    const int i = blockIdx.y * 256 + threadIdx.x, per = p.sinks * (D / 4);
-    if (i >= 2 * per) return;
-    const int w = i / per, row = i % per / (D / 4), col = i % (D / 4) * 4;
-    auto at = [&](long long place) {
-        return *reinterpret_cast<const float4 *>(p.sink_part + (((place * p.Nk + hk) * 2 + w) * p.sinks + row) * D + col);
-    };
-    const long long base = p.seq.cu ? s.bos / (parts.tiles * 128) + n
-                                    : (long long)n * ((p.seq.T + parts.tiles * 128 - 1) / (parts.tiles * 128));
-    float4 v = at(parts.slots + n);
-    for (int c = (qt.last + 1) / parts.tiles; c <= qt.end / parts.tiles; ++c) {
-        const float4 a = at(base + c);
-        v.x += a.x; v.y += a.y; v.z += a.z; v.w += a.w;
-    }
-    if (row >= L) return;
-    Vec<__nv_bfloat16, 4> y;
-    y.v[0] = v.x; y.v[1] = v.y; y.v[2] = v.z; y.v[3] = v.w;
-    y.store(static_cast<__nv_bfloat16 *>(w == 0 ? p.dv : p.dk) + ((s.bos + row) * p.Nk + hk) * D + col);
-    if (isnan(v.x) | isnan(v.y) | isnan(v.z) | isnan(v.w)) {
-        // the first key tile's slot, the half that the row lies in
-        const long long slot = p.seq.cu ? s.bos / 128 + n : (long long)n * ((p.seq.T + 127) / 128);
-        atomicOr(p.redo + (slot * 2 + row / 64) * (p.Nq + p.Nk) + p.Nq + hk, 1u);
-    }
-}
-
 // D' = sum do o of every token and head: 16 bytes of both a thread, D / 8 threads a row.
 template <int D>
 __global__ void __launch_bounds__(256) window_dsum(WindowParams p, long long rows) {
@@ -879,8 +844,7 @@ cudaError_t launch(const WindowParams &p, cudaStream_t stream) {
     if (err != cudaSuccess) return err;
     err = launch_after(window_dkv<D>, dim3((unsigned)(ki < kSms ? ki : kSms)), dim3(kThreads), k_bytes, stream, mq, mg, mk, mv, p, (unsigned)ki,
                        slots, parts);
-    if (err != cudaSuccess || !parts.slots) return err;
-    return launch_after(window_sink_sums<D>, dim3((unsigned)p.seq.N * p.Nk, (2 * p.sinks * (D / 4) + 255) / 256), dim3(256), 0, stream, p, parts);
+    return err == cudaSuccess ? window_sink_sums(p, true, stream) : err;
 }
 
 }  // namespace
