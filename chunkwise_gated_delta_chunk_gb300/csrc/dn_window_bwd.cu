@@ -55,7 +55,7 @@ struct Lay {
     static constexpr uint32_t kPlan = kCols + (DQ ? 0 : NX * 1024), kBar = kPlan + kPlans * 64;
     static constexpr int bHold = 0, bHoldEmpty = 1, bX = 2, bXEmpty = bX + NX, bY = bXEmpty + NX, bYEmpty = bY + NY, bCol = bYEmpty + NY,
                          bS = bCol + NX, bDP = bS + 1, bP = bDP + 1, bDS = bP + 1, bOut = bDS + 1, bOutEmpty = bOut + 1,
-                         bPlan = bOutEmpty + 1, bDrain = bPlan + kPlans, bPair = bDrain + 1, kBars = bPair + 4;
+                         bPlan = bOutEmpty + 1, bDrain = bPlan + kPlans, bPair = bDrain + 1, bTaken = bPair + 4, kBars = bTaken + 4;
     static constexpr uint32_t kBox = (kBar + 8 * kBars + 15) / 16 * 16, kMisc = kBox + (DQ ? 2 * 128 * 4 : 0), kAlloc = kMisc + 16 + 1024;
     static_assert(kAlloc <= 232448, "exceeds the 227 KB of shared memory per CTA");
 };
@@ -365,10 +365,12 @@ struct Dq : Base<D, true, QueryPlan> {
             // D of the row from its two threads
             volatile float *box = reinterpret_cast<float *>(x.gbase + Y::kBox) + row;
             const float mine = sum_of(exact);
+            if (!hold(x, bar(Y::bTaken + (warp & 3)), (qn & 1) ^ 1)) return;  // the last ones are read
             box[128 * w] = mine;
             warp_arrive(bar(Y::bPair + (warp & 3)));
             if (!hold(x, bar(Y::bPair + (warp & 3)), qn & 1)) return;
             const float full = mine + box[128 * (w ^ 1)];
+            warp_arrive(bar(Y::bTaken + (warp & 3)));
             if (w == 0 && live) p.dsum[at] = full;
             if (!hold(x, bar(Y::bOut), qn & 1)) return;
             tc_fence_after();
@@ -718,7 +720,10 @@ __device__ __forceinline__ void set_up(F &f, uint8_t *raw_smem, unsigned *status
         mbar_init(f.bar(Y::bOutEmpty), 8);
         for (int i = 0; i < kPlans; ++i) mbar_init(f.bar(Y::bPlan + i), 1);
         mbar_init(f.bar(Y::bDrain), 1);
-        for (int i = 0; i < 4; ++i) mbar_init(f.bar(Y::bPair + i), 2);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(f.bar(Y::bPair + i), 2);
+            mbar_init(f.bar(Y::bTaken + i), 2);
+        }
         *f.x.abort_flag = 0;
         fence_barrier_init();
     }

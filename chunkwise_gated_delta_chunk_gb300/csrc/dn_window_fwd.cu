@@ -19,11 +19,16 @@
 // so S(j+1) of one tile is ready when the softmax of the other has just begun (with a warp for
 // each, the two tiles fell into step: both in the softmax, then both on the tensor cores, 15 % slower).
 //
-// O is rescaled only when a row's maximum has grown by more than 2^8 since the last time:
-// weights stay below 2^8, sums in fp32 lose nothing (and P in bf16 has the same relative
-// rounding at every size).  Masks cost selects only in tiles that the window's or the
-// sequence's border crosses.  The sinks in front of the window are a tile of 32 keys where
-// they fit in one.  P is rounded to bf16 for the product; the sum takes it unrounded.
+// What a row's weights are relative to is the maximum of the first tile that it sees.  It moves up, and O and
+// the sum are rescaled, only when the weights of half a tile have summed to more than 2^16 (a maximum of every
+// tile took 12 % of a thread's time): sums in fp32 lose nothing, P in bf16 has the same relative rounding at
+// every size.  A row whose weights pass fp32 within one tile (scores that grow by more than 2^127 from
+// one tile to the next) comes out not finite, and is marked.  Masks cost selects only in tiles that the
+// window's or the sequence's border crosses.  The sinks in front of the window are a tile of 32 keys where they
+// fit in one.  P is rounded to bf16 for the product, by half a step of each weight; the sum takes it unrounded.
+//
+// A masked pair weighs 0, and 0 times an infinite or NaN value is NaN.  Rows that come out so are marked in
+// lse, and taken again by a kernel that leaves masked pairs out (dn_window_simt.cu).
 //
 // CTAs are persistent, one an SM; every wait is bounded (dn_tc_sync.cuh).
 #include "dn_window_tc.cuh"
@@ -46,7 +51,8 @@ struct Lay {
     static constexpr uint32_t kQ = 0, kK = 2 * kTile, kV = kK + NS * kTile, kBar = kV + NS * kTile;
     // barriers
     static constexpr int bQFull = 0, bQEmpty = 1, bFull = 2, bEmpty = bFull + NS, bS = bEmpty + NS, bP = bS + 2, bO = bP + 2,
-                         bOEmpty = bO + 2, bDrain = bOEmpty + 2, bPair = bDrain + 1, bPlan = bPair + 8, kBars = bPlan + kPlans;
+                         bOEmpty = bO + 2, bDrain = bOEmpty + 2, bPair = bDrain + 1, bPlan = bPair + 8, bPlanEmpty = bPlan + kPlans,
+                         kBars = bPlanEmpty + kPlans;
     static constexpr uint32_t kBox = (kBar + 8 * kBars + 15) / 16 * 16, kWish = kBox + 2 * 2 * 2 * 128 * 4, kPlan = kWish + 2 * 2 * 128 * 4, kMisc = kPlan + kPlans * 96, kAlloc = kMisc + 16 + 1024;
     static_assert(kAlloc <= 232448, "exceeds the 227 KB of shared memory per CTA");
     // tensor memory columns
@@ -133,14 +139,15 @@ struct Fwd {
     // ---- plans ----------------------------------------------------------------
     // The TMA warp works them out (a few hundred cycles of divisions and look-ups, and code that the other
     // roles would fetch anew for every item: 3000 cycles an item each) and leaves the n-th item's in
-    // shared memory.  It writes plan n when all scores of item n - 1 are issued, when every other
-    // warp is past item n - 4, whose place it takes.
+    // shared memory, when all scores of item n - 1 are issued and the other warps have read plan n - 4,
+    // whose place it takes.  What a plan holds is copied at once.
     __device__ __forceinline__ Plan *place(unsigned n) const { return reinterpret_cast<Plan *>(x.gbase + Y::kPlan + n % kPlans * 96); }
     __device__ __forceinline__ bool next_plan(const Plan *&u, unsigned n) const {
         if (!hold(x, bar(Y::bPlan + n % kPlans), n / kPlans & 1)) return false;
         u = place(n);
         return u->n > 0;
     }
+    __device__ __forceinline__ void read_plan(unsigned n) const { warp_arrive(bar(Y::bPlanEmpty + n % kPlans)); }
 
     // ---- TMA ------------------------------------------------------------------
     // Keys and values come in units: the keys of place 0; the values of place i with the keys
@@ -153,7 +160,7 @@ struct Fwd {
             Plan u;
             if (item >= items) u.n = 0;
             else if (!plan(u, p, item, slots)) continue;
-            if (!(fine = wait(x, bar(Y::bQEmpty), (qn & 1) ^ 1))) break;
+            if (!(fine = wait(x, bar(Y::bQEmpty), (qn & 1) ^ 1) && wait(x, bar(Y::bPlanEmpty + qn % kPlans), (qn / kPlans & 1) ^ 1))) break;
             *place(qn) = u;
             mbar_arrive(bar(Y::bPlan + qn % kPlans));
             if (u.n == 0) break;
@@ -217,6 +224,7 @@ struct Fwd {
         bool fine = true;
         for (const Plan *next; fine && next_plan(next, qn);) {
             const Plan u = *next;
+            read_plan(qn);
             if (!(fine = hold(x, bar(Y::bQFull), qn & 1) && hold(x, bar(Y::bFull + un % Y::NS), (un / Y::NS) & 1))) break;
             tc_fence_after();
             if (u.q0.zero) issue_s(lead, 0, un, u.small(0));
@@ -295,10 +303,11 @@ struct Fwd {
         for (const Plan *next; next_plan(next, qn); ++qn) {
             const Plan &u = *next;
             const Span v = q ? u.q1 : u.q0;
-            if (!v.act) continue;
             const int lo = u.lo, L = u.L;
             const bool sink = u.sink, narrow = u.narrow;
             const long long bos = u.bos;
+            read_plan(qn);
+            if (!v.act) continue;
             const int t = v.t0 + row;
             // what weights are relative to, times log2 e scale: -infinity until the row has seen a key; sum of the weights
             float m = -CUDART_INF_F, l = 0.f;
@@ -445,7 +454,10 @@ window_fwd(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
             mbar_init(bar(Y::bOEmpty + q), 8);
         }
         for (int i = 0; i < 8; ++i) mbar_init(bar(Y::bPair + i), 2);
-        for (int i = 0; i < kPlans; ++i) mbar_init(bar(Y::bPlan + i), 1);
+        for (int i = 0; i < kPlans; ++i) {
+            mbar_init(bar(Y::bPlan + i), 1);
+            mbar_init(bar(Y::bPlanEmpty + i), 17);
+        }
         mbar_init(bar(Y::bDrain), 1);
         *x.abort_flag = 0;
         fence_barrier_init();

@@ -13,6 +13,8 @@
 // block, and the blocks of a cluster that share a sequence where there are few of them, join
 // these at the end through shared memory.  Every position on the list is seen, so there is
 // nothing to mask but the end of the list.
+#include <type_traits>
+
 #include "dn_window.cuh"
 
 namespace dn {
@@ -125,10 +127,7 @@ template <typename T, int D, int ROWS>
 __device__ __forceinline__ void join(const CacheParams &p, const Job<T, D> &job, const float *o, int stride, float (&m)[kWarps][ROWS],
                                      float (&l)[kWarps][ROWS], float *sum, float (&top)[ROWS], float (&all)[ROWS], unsigned blocks) {
     constexpr int NT = 32 * kWarps;
-    auto best = [&](int r) {
-        const float t = fmaxf(fmaxf(m[0][r], m[1][r]), fmaxf(m[2][r], m[3][r]));
-        return t;
-    };
+    auto best = [&](int r) { return fmaxf(fmaxf(m[0][r], m[1][r]), fmaxf(m[2][r], m[3][r])); };
     __syncthreads();
     for (int i = threadIdx.x; i < job.rows * D; i += NT) {
         const int r = i / D;
@@ -149,19 +148,28 @@ __device__ __forceinline__ void join(const CacheParams &p, const Job<T, D> &job,
     if (blocks > 1) cluster_sync();
     else __syncthreads();
     const unsigned rank = blocks > 1 ? cluster_rank() : 0;
-    if (job.ok)
-        for (int i = rank * NT + threadIdx.x; i < job.rows * D; i += NT * blocks) {
+    auto add_up = [&](auto count) {  // all blocks' numbers are asked for at once
+        constexpr int N = decltype(count)::value;
+        for (int i = rank * NT + threadIdx.x; i < job.rows * D; i += NT * N) {
             const int r = i / D;
             float a, s;
-            if (blocks > 1) {
-                float t = -CUDART_INF_F;
-                for (unsigned b = 0; b < blocks; ++b) t = fmaxf(t, remote(&top[r], b));
+            if constexpr (N > 1) {
+                float ms[N], os[N], ls[N], t = -CUDART_INF_F;
+#pragma unroll
+                for (int b = 0; b < N; ++b) {
+                    ms[b] = remote(&top[r], b);
+                    os[b] = remote(sum + i, b);
+                    ls[b] = remote(&all[r], b);
+                }
+#pragma unroll
+                for (int b = 0; b < N; ++b) t = fmaxf(t, ms[b]);
                 const float base = t == -CUDART_INF_F ? 0.f : t;
                 a = s = 0.f;
-                for (unsigned b = 0; b < blocks; ++b) {
-                    const float f = ex2(remote(&top[r], b) - base);
-                    a = fmaf(f, remote(sum + i, b), a);
-                    s = fmaf(f, remote(&all[r], b), s);
+#pragma unroll
+                for (int b = 0; b < N; ++b) {
+                    const float f = ex2(ms[b] - base);
+                    a = fmaf(f, os[b], a);
+                    s = fmaf(f, ls[b], s);
                 }
             } else {
                 a = sum[i];
@@ -171,6 +179,14 @@ __device__ __forceinline__ void join(const CacheParams &p, const Job<T, D> &job,
             y.v[0] = a / s;
             y.store(static_cast<T *>(p.o) + job.query(p, 0) + i);
         }
+    };
+    if (job.ok) {
+        if (blocks == 1) add_up(std::integral_constant<int, 1>());
+        else if (blocks == 2) add_up(std::integral_constant<int, 2>());
+        else if (blocks == 4) add_up(std::integral_constant<int, 4>());
+        else if (blocks == 8) add_up(std::integral_constant<int, 8>());
+        else add_up(std::integral_constant<int, 16>());
+    }
     if (blocks > 1) cluster_sync();  // a block's shared memory stays until the others have read it
 }
 
@@ -504,11 +520,11 @@ __global__ void __launch_bounds__(256) fill(const __grid_constant__ CacheParams 
         const SeqTile s = seq_whole(p.seq, n);
         if (!s.ok) continue;
         const long long had = p.lengths ? p.lengths[n] : 0;
-        if (had < 0) {
+        const int len = (int)(s.eos - s.bos);
+        if (had < 0 || had > INT64_MAX - len) {
             if (threadIdx.x == 0) atomicOr(p.status, kStatusBadSeq);
             continue;
         }
-        const int len = (int)(s.eos - s.bos);
         const int head = had >= p.sinks ? 0 : p.sinks - had < len ? (int)(p.sinks - had) : len;  // tokens that are sinks
         const int tail = len - p.ring > head ? len - p.ring : head;                              // the first of the others that stays
         const int i0 = (int)(b % per_seq) * kFillTile, kept = head + len - tail;

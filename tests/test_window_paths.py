@@ -37,6 +37,14 @@ def test_sinks_seen_by_many_tiles(lib, dtype, lengths, Nq, Nk, sinks):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("Nq,Nk", [(3, 1), (2, 1)])
+def test_many_short_sequences(lib, dtype, Nq, Nk):
+    """Tiles that are mostly empty: a pair of tiles of tokens has one alone, many times in a row."""
+    lengths = [(7 * i) % 6 for i in range(1000)] + [200]
+    check(lib, inputs(dtype, lengths=lengths, Nq=Nq, Nk=Nk, seed=1), 4, 1, lengths, label="short")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_long_window(lib, dtype):
     """A window of more tiles than a run of the sinks' queries may have."""
     check(lib, inputs(dtype, B=1, T=5700, Nq=1, Nk=1, seed=2), 4200, 4, label="long window")
@@ -87,6 +95,21 @@ def test_block_many_rows(lib, D, biases, rows):
         # each side's sum of `rows` terms is off by at most rows 2^-24 of the terms' sizes; these add up at random
         # to sqrt(rows) of them, and the largest is some 6 deviations
         assert (out["d" + n].double() - want).abs().max() <= 2 * rows * 2.0 ** -24 * 6 * max(1.0, float(want.abs().max())), n
+
+
+def test_lengths_at_the_end_of_64_bits(lib):
+    """Positions that 64 bits hold are kept by the ring; a length that they would pass is reported, and nothing is
+    written for its sequence."""
+    top = 2 ** 63 - 1
+    t = inputs(torch.float32, B=2, T=3, Nq=1, Nk=1, seed=1)
+    kc, vc = (torch.full((2, 1, 9, 64), 7.0, device=DEV) for _ in range(2))
+    lib.dn_check()
+    lib.window_cache_fill(t["k"], t["v"], kc, vc, torch.tensor([top - 2, top - 3], device=DEV), 2)
+    assert lib.dn_check() == lib.DN_ERR_DEVICE_ARG
+    assert (kc[0] == 7).all() and (vc[0] == 7).all()
+    want = wref.cache_of(t["k"][1], top - 3, 2, 7, torch.full((1, 9, 64), 7.0, device=DEV))
+    assert torch.equal(kc[1], want)
+    ok(lib)
 
 
 # ---- streams, graphs, workspaces ---------------------------------------------------------
