@@ -20,8 +20,8 @@
  * except where an entry point says so; argument errors are found on the host.
  * Scores, the softmax's maxima and sums, and all accumulators are fp32.  With
  * bf16 tensors the products run on the tensor cores: the weights p (and in the
- * backward dp) are rounded to bf16 for them.  With fp32 tensors every product
- * is fp32.  Results do not depend on the order in which blocks run.
+ * backward ds = p (dp - D)) are rounded to bf16 for them.  With fp32 tensors
+ * every product is fp32.  Results do not depend on the order in which blocks run.
  *
  * What a masked key or its value holds (NaN and infinities too) reaches no
  * output.  A row whose own operands are not finite comes out as the formulas
@@ -79,7 +79,9 @@ size_t dn_window_attn_bwd_workspace_bytes(int packed, int n_seqs, int B, int T, 
  *   lengths           [n_seqs]       int64  tokens that each sequence had
  *                                           before these; NULL: none
  *   k_cache, v_cache  [n_seqs, Nk, sinks + ring, d]  dtype
- * d is 64 or 128; ring >= 1, sinks + ring <= 2^30.
+ * d is 64 or 128; ring >= 1, sinks + ring <= 2^30.  A length that is negative, or
+ * that 64 bits do not hold with the tokens added, makes dn_check return
+ * DN_ERR_DEVICE_ARG; nothing is written for that sequence.
  */
 dn_status dn_window_cache_fill(const void *k, const void *v, const int64_t *cu_seqlens, int n_seqs, int B, int T,
                                int Nk, int d, int sinks, int ring, dn_dtype dtype, const int64_t *lengths,
