@@ -51,16 +51,16 @@ cudaError_t window_sink_sums(const WindowParams &p, bool bf16, cudaStream_t stre
 
 cudaError_t window_fwd_launch(const WindowParams &p, bool bf16, cudaStream_t stream, const char **name) {
     *name = bf16 ? "window_fwd<bf16>" : "window_fwd<f32>";
-    const cudaError_t err = bf16 ? window_tc_fwd(p, stream) : window_simt_fwd(p, bf16, false, stream);
+    const cudaError_t err = bf16 ? window_tc_fwd(p, stream) : window_simt_fwd(p, stream);
     if (err != cudaSuccess) return err;
-    return window_simt_fwd(p, bf16, true, stream);
+    return window_fwd_redo(p, bf16, stream);
 }
 
 cudaError_t window_bwd_launch(const WindowParams &p, bool bf16, cudaStream_t stream, const char **name) {
     *name = bf16 ? "window_bwd<bf16>" : "window_bwd<f32>";
-    const cudaError_t err = bf16 ? window_tc_bwd(p, stream) : window_simt_bwd(p, bf16, false, stream);
+    const cudaError_t err = bf16 ? window_tc_bwd(p, stream) : window_simt_bwd(p, stream);
     if (err != cudaSuccess) return err;
-    return window_simt_bwd(p, bf16, true, stream);
+    return window_bwd_redo(p, bf16, stream);
 }
 
 namespace {

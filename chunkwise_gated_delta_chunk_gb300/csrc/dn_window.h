@@ -49,8 +49,10 @@ cudaError_t window_tc_fwd(const WindowParams &p, cudaStream_t stream);
 cudaError_t window_tc_bwd(const WindowParams &p, cudaStream_t stream);
 
 // CUDA-core kernels: fp32 tensors, and (redo) rows that the other kernels marked.
-cudaError_t window_simt_fwd(const WindowParams &p, bool bf16, bool redo, cudaStream_t stream);
-cudaError_t window_simt_bwd(const WindowParams &p, bool bf16, bool redo, cudaStream_t stream);
+cudaError_t window_simt_fwd(const WindowParams &p, cudaStream_t stream);
+cudaError_t window_simt_bwd(const WindowParams &p, cudaStream_t stream);
+cudaError_t window_fwd_redo(const WindowParams &p, bool bf16, cudaStream_t stream);  // the marked rows and tiles
+cudaError_t window_bwd_redo(const WindowParams &p, bool bf16, cudaStream_t stream);
 
 // The sinks' rows of dk and dv from their parts, where there are any.
 cudaError_t window_sink_sums(const WindowParams &p, bool bf16, cudaStream_t stream);

@@ -176,11 +176,11 @@ struct Half {
 // What a block of a grid does: item after item, or (REDO) a look at many marks at a time and only the
 // marked ones.  `marked(i)`: thread-wise, is group i of `group` items marked anywhere.
 template <bool REDO, typename Marked, typename Work>
-__device__ __forceinline__ void walk(long long items, int group, Marked marked, Work work) {
+__device__ __forceinline__ void walk(unsigned block, unsigned blocks, long long items, int group, Marked marked, Work work) {
     if constexpr (!REDO) {
-        for (long long item = blockIdx.x; item < items; item += gridDim.x) work(item);
+        for (long long item = block; item < items; item += blocks) work(item);
     } else {
-        for (long long g = blockIdx.x; g * group < items; g += gridDim.x) {
+        for (long long g = block; g * group < items; g += blocks) {
             if (!__syncthreads_or(marked(g))) continue;
             for (int i = 0; i < group && g * group + i < items; ++i) work(g * group + i);
         }
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(NT, D == 64 ? 2 : 1) simt_fwd(WindowParams p, 
                 any |= is_redo(p.lse[(it.s.bos + it.t0) * p.Nq + i]);
         return any;
     };
-    walk<REDO>(items, p.Nq, marked, [&](long long item) {
+    walk<REDO>(blockIdx.x, gridDim.x, items, p.Nq, marked, [&](long long item) {
         const Half it(p.seq, item, p.Nq);
         if (!it.ok) return;
         const long long bos = it.s.bos;
@@ -297,19 +297,18 @@ __device__ __forceinline__ void weights(float &s, float &g, bool seen, float c, 
 }
 
 template <typename T, int D, bool REDO>
-__global__ void __launch_bounds__(NT) simt_dq(WindowParams p, long long items) {
+__device__ __forceinline__ void work_dq(const WindowParams &p, unsigned block, unsigned blocks, long long items) {
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
     const Sight sight{p.window, p.sinks};
     const float c = p.scale * kLog2e;
     constexpr int kTile = Smem<D>::kTile;
     float *Qs = s_win, *Gs = Qs + kTile, *Kb = Gs + kTile, *Vs = Kb + 2 * kTile, *Ss = Vs + kTile;
-    wait_for_launches();
-    if (!REDO && blockIdx.x == 0) check_offsets(p.seq, threadIdx.x, NT);
+    if (!REDO && block == 0) check_offsets(p.seq, threadIdx.x, NT);
     auto marked = [&](long long g) {
         const long long i = g * NT + threadIdx.x;
         return i < items && p.redo[i / p.Nq * (p.Nq + p.Nk) + i % p.Nq] != 0;
     };
-    walk<REDO>(items, NT, marked, [&](long long item) {
+    walk<REDO>(block, blocks, items, NT, marked, [&](long long item) {
         const Half it(p.seq, item, p.Nq);
         unsigned *flag = p.redo + it.flag * (p.Nq + p.Nk) + it.head;
         if (REDO) {
@@ -322,7 +321,7 @@ __global__ void __launch_bounds__(NT) simt_dq(WindowParams p, long long items) {
         const int hk = it.head / (p.Nq / p.Nk);
         load_rows<T, D>(Qs, static_cast<const T *>(p.q), bos + it.t0, it.s.eos, p.Nq, it.head);
         load_rows<T, D>(Gs, static_cast<const T *>(p.dout), bos + it.t0, it.s.eos, p.Nq, it.head);
-        load_rows<T, D>(Vs, static_cast<const T *>(p.o), bos + it.t0, it.s.eos, p.Nq, it.head);
+        if (!REDO) load_rows<T, D>(Vs, static_cast<const T *>(p.o), bos + it.t0, it.s.eos, p.Nq, it.head);
         const KeyTiles kt(it.t0, it.t1, BT, sight);
         auto keys = [&](int n) {
             load_rows<T, D>(Kb + (n & 1) * kTile, static_cast<const T *>(p.k), bos + (long long)kt.tile(n) * BT, it.s.eos, p.Nk, hk);
@@ -338,12 +337,17 @@ __global__ void __launch_bounds__(NT) simt_dq(WindowParams p, long long items) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = 4 * ty + i, t = it.t0 + r;
-            float a = 0.f;
+            const long long at = (bos + t) * p.Nq + it.head;
+            lse2[i] = t < it.t1 ? p.lse[at] * kLog2e : 0.f;
+            if (REDO) {
+                dsum[i] = t < it.t1 ? p.dsum[at] : 0.f;
+            } else {
+                float a = 0.f;
 #pragma unroll
-            for (int u = 0; u < D / 16; ++u) a = fmaf(Gs[r * Smem<D>::kRow + tx + 16 * u], Vs[r * Smem<D>::kRow + tx + 16 * u], a);
-            dsum[i] = sum16(a);
-            lse2[i] = t < it.t1 ? p.lse[(bos + t) * p.Nq + it.head] * kLog2e : 0.f;
-            if (!REDO && tx == 0 && t < it.t1) p.dsum[(bos + t) * p.Nq + it.head] = dsum[i];
+                for (int u = 0; u < D / 16; ++u) a = fmaf(Gs[r * Smem<D>::kRow + tx + 16 * u], Vs[r * Smem<D>::kRow + tx + 16 * u], a);
+                dsum[i] = sum16(a);
+                if (tx == 0 && t < it.t1) p.dsum[at] = dsum[i];
+            }
 #pragma unroll
             for (int u = 0; u < D / 32; ++u) acc[i][u] = 0ull;
         }
@@ -446,18 +450,18 @@ struct KeyItem {
 };
 
 template <typename T, int D, bool REDO>
-__global__ void __launch_bounds__(NT) simt_dkv(WindowParams p, long long items, long long main_items, long long part_slots) {
+__device__ __forceinline__ void work_dkv(const WindowParams &p, unsigned block, unsigned blocks, long long items, long long main_items,
+                                         long long part_slots) {
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
     const Sight sight{p.window, p.sinks};
     const float c = p.scale * kLog2e;
     constexpr int kTile = Smem<D>::kTile;
     float *Ks = s_win, *Vs = Ks + kTile, *Qb = Vs + kTile, *Gs = Qb + 2 * kTile, *Ps = Gs + kTile, *Ss = Ps + BT * PS;
-    wait_for_launches();
     auto marked = [&](long long g) {
         const long long i = g * NT + threadIdx.x;
         return i < items && p.redo[i / p.Nk * (p.Nq + p.Nk) + p.Nq + i % p.Nk] != 0;
     };
-    walk<REDO>(items, NT, marked, [&](long long item) {
+    walk<REDO>(block, blocks, items, NT, marked, [&](long long item) {
         const KeyItem u = KeyItem::of<REDO>(p, item, main_items, part_slots);
         const bool by_head = !REDO && p.head_part && !u.part;
         if (REDO) {
@@ -537,6 +541,24 @@ __global__ void __launch_bounds__(NT) simt_dkv(WindowParams p, long long items, 
     });
 }
 
+template <typename T, int D>
+__global__ void __launch_bounds__(NT) simt_dq(WindowParams p, long long items) {
+    wait_for_launches();
+    work_dq<T, D, false>(p, blockIdx.x, gridDim.x, items);
+}
+template <typename T, int D>
+__global__ void __launch_bounds__(NT) simt_dkv(WindowParams p, long long items, long long main_items, long long part_slots) {
+    wait_for_launches();
+    work_dkv<T, D, false>(p, blockIdx.x, gridDim.x, items, main_items, part_slots);
+}
+// The marked tiles of both: the first `dq_blocks` blocks look at those of queries, the others at those of keys.
+template <typename T, int D>
+__global__ void __launch_bounds__(NT) simt_bwd_redo(WindowParams p, unsigned dq_blocks, long long dq_items, long long dkv_items) {
+    wait_for_launches();
+    if (blockIdx.x < dq_blocks) work_dq<T, D, true>(p, blockIdx.x, dq_blocks, dq_items);
+    else work_dkv<T, D, true>(p, blockIdx.x - dq_blocks, gridDim.x - dq_blocks, dkv_items, dkv_items, 0);
+}
+
 // The query heads' sums of a key tile, in order.
 template <typename T, int D>
 __global__ void __launch_bounds__(NT) simt_head_sums(WindowParams p, long long items, long long part_slots) {
@@ -581,20 +603,27 @@ cudaError_t launch_items(int bytes, long long items, int group, cudaStream_t str
     return launch_after(kKernel, dim3(grid), dim3(NT), bytes, stream, p, items, rest...);
 }
 
-template <typename T, int D, bool REDO>
+template <typename T, int D>
 cudaError_t bwd(const WindowParams &p, cudaStream_t stream) {
     const long long halves = 2 * tile_slots(p.seq, kWinTile);
-    cudaError_t err = launch_items<simt_dq<T, D, REDO>, REDO>(Smem<D>::kDq, halves * p.Nq, NT, stream, p);
+    cudaError_t err = launch_items<simt_dq<T, D>, false>(Smem<D>::kDq, halves * p.Nq, NT, stream, p);
     if (err != cudaSuccess) return err;
-    const long long part_slots = !REDO && p.parts ? tile_slots(p.seq, p.part_tiles * kWinTile) : 0;
-    const long long main_items = halves * (!REDO && p.head_part ? p.Nq : p.Nk), items = main_items + part_slots * p.part_heads * 2;
-    err = launch_items<simt_dkv<T, D, REDO>, REDO>(Smem<D>::kDkv, items, NT, stream, p, main_items, part_slots);
-    if constexpr (!REDO) {
-        if (err == cudaSuccess && p.head_part)
-            err = launch_items<simt_head_sums<T, D>, false>(0, halves * p.Nk, 1, stream, p, part_slots);
-        if (err == cudaSuccess) err = window_sink_sums(p, sizeof(T) == 2, stream);
-    }
-    return err;
+    const long long part_slots = p.parts ? tile_slots(p.seq, p.part_tiles * kWinTile) : 0;
+    const long long main_items = halves * (p.head_part ? p.Nq : p.Nk), items = main_items + part_slots * p.part_heads * 2;
+    err = launch_items<simt_dkv<T, D>, false>(Smem<D>::kDkv, items, NT, stream, p, main_items, part_slots);
+    if (err == cudaSuccess && p.head_part) err = launch_items<simt_head_sums<T, D>, false>(0, halves * p.Nk, 1, stream, p, part_slots);
+    return err == cudaSuccess ? window_sink_sums(p, sizeof(T) == 2, stream) : err;
+}
+
+template <typename T, int D>
+cudaError_t bwd_redo(const WindowParams &p, cudaStream_t stream) {
+    const long long halves = 2 * tile_slots(p.seq, kWinTile), dq_items = halves * p.Nq, dkv_items = halves * p.Nk;
+    constexpr int bytes = Smem<D>::kDq > Smem<D>::kDkv ? Smem<D>::kDq : Smem<D>::kDkv;
+    const cudaError_t err = allow_smem<simt_bwd_redo<T, D>>(bytes);
+    if (err != cudaSuccess) return err;
+    auto blocks = [](long long items) { return (unsigned)((items + NT - 1) / NT < kSms ? (items + NT - 1) / NT : kSms); };
+    return launch_after(simt_bwd_redo<T, D>, dim3(blocks(dq_items) + blocks(dkv_items)), dim3(NT), bytes, stream, p, blocks(dq_items), dq_items,
+                        dkv_items);
 }
 
 template <typename T, int D, bool REDO>
@@ -605,18 +634,22 @@ cudaError_t fwd(const WindowParams &p, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t window_simt_fwd(const WindowParams &p, bool bf16, bool redo, cudaStream_t stream) {
-    if (bf16 && !redo) return cudaErrorInvalidValue;  // the tensor-core kernels' own
-    if (bf16) return p.d == 64 ? fwd<__nv_bfloat16, 64, true>(p, stream) : fwd<__nv_bfloat16, 128, true>(p, stream);
-    if (redo) return p.d == 64 ? fwd<float, 64, true>(p, stream) : fwd<float, 128, true>(p, stream);
+cudaError_t window_simt_fwd(const WindowParams &p, cudaStream_t stream) {
     return p.d == 64 ? fwd<float, 64, false>(p, stream) : fwd<float, 128, false>(p, stream);
 }
 
-cudaError_t window_simt_bwd(const WindowParams &p, bool bf16, bool redo, cudaStream_t stream) {
-    if (bf16 && !redo) return cudaErrorInvalidValue;
-    if (bf16) return p.d == 64 ? bwd<__nv_bfloat16, 64, true>(p, stream) : bwd<__nv_bfloat16, 128, true>(p, stream);
-    if (redo) return p.d == 64 ? bwd<float, 64, true>(p, stream) : bwd<float, 128, true>(p, stream);
-    return p.d == 64 ? bwd<float, 64, false>(p, stream) : bwd<float, 128, false>(p, stream);
+cudaError_t window_fwd_redo(const WindowParams &p, bool bf16, cudaStream_t stream) {
+    if (bf16) return p.d == 64 ? fwd<__nv_bfloat16, 64, true>(p, stream) : fwd<__nv_bfloat16, 128, true>(p, stream);
+    return p.d == 64 ? fwd<float, 64, true>(p, stream) : fwd<float, 128, true>(p, stream);
+}
+
+cudaError_t window_simt_bwd(const WindowParams &p, cudaStream_t stream) {
+    return p.d == 64 ? bwd<float, 64>(p, stream) : bwd<float, 128>(p, stream);
+}
+
+cudaError_t window_bwd_redo(const WindowParams &p, bool bf16, cudaStream_t stream) {
+    if (bf16) return p.d == 64 ? bwd_redo<__nv_bfloat16, 64>(p, stream) : bwd_redo<__nv_bfloat16, 128>(p, stream);
+    return p.d == 64 ? bwd_redo<float, 64>(p, stream) : bwd_redo<float, 128>(p, stream);
 }
 
 }  // namespace dn
