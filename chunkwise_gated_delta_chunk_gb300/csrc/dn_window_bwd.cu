@@ -55,8 +55,8 @@ struct Lay {
     static constexpr uint32_t kPlan = kCols + (DQ ? 0 : NX * 1024), kBar = kPlan + kPlans * 64;
     static constexpr int bHold = 0, bHoldEmpty = 1, bX = 2, bXEmpty = bX + NX, bY = bXEmpty + NX, bYEmpty = bY + NY, bCol = bYEmpty + NY,
                          bS = bCol + NX, bDP = bS + 1, bP = bDP + 1, bDS = bP + 1, bOut = bDS + 1, bOutEmpty = bOut + 1,
-                         bPlan = bOutEmpty + 1, bDrain = bPlan + kPlans, bPair = bDrain + 1, bTaken = bPair + 4, kBars = bTaken + 4;
-    static constexpr uint32_t kBox = (kBar + 8 * kBars + 15) / 16 * 16, kMisc = kBox + (DQ ? 2 * 128 * 4 : 0), kAlloc = kMisc + 16 + 1024;
+                         bPlan = bOutEmpty + 1, bDrain = bPlan + kPlans, bPair = bDrain + 1, bTaken = bPair + 4, bItem = bTaken + 4, kBars = bItem + 1;
+    static constexpr uint32_t kBox = (kBar + 8 * kBars + 15) / 16 * 16, kMisc = kBox + (DQ ? 2 * 128 * 4 : 0), kAlloc = kMisc + 32 + 1024;
     static_assert(kAlloc <= 232448, "exceeds the 227 KB of shared memory per CTA");
 };
 
@@ -69,6 +69,7 @@ struct Base {
     uint32_t tm;
     __device__ __forceinline__ uint32_t bar(int i) const { return x.base + Y::kBar + 8u * i; }
 
+    __device__ __forceinline__ Items items() const { return Items{bar(Y::bItem), x.base + Y::kMisc + 16}; }
     // The TMA warp works out the plans and leaves the n-th item's in shared memory: when all scores of
     // item n - 1 are done, and every other warp is past item n - 4, whose place it takes.  A plan of
     // no rounds: no item is left.
@@ -168,14 +169,13 @@ struct Dq : Base<D, true, QueryPlan> {
     using B::p;
     using B::tm;
     using B::x;
-    unsigned items;
     long long slots;
     static constexpr uint32_t tS = 0, tDP = 128, tDQ = 256, tC = 384;
 
-    // late tiles first: under a causal mask these are the long ones
+    // late tiles first
     __device__ __forceinline__ bool plan(Plan &u, unsigned item) const {
         u.h = item % p.Nq;
-        const unsigned slot = (unsigned)(slots - 1 - item / p.Nq);
+        const unsigned slot = slot_in_order(p.seq, item / p.Nq, (unsigned)slots, false);
         u.flag = (long long)slot * 2 * (p.Nq + p.Nk) + u.h;
         const SeqTile s = seq_tile(p.seq, slot, 128);
         if (!s.ok || s.t0 >= s.t1) return false;
@@ -193,11 +193,12 @@ struct Dq : Base<D, true, QueryPlan> {
                          const CUtensorMap *mks, const CUtensorMap *mvs) {
         unsigned kx = 0, ky = 0, qn = 0;
         bool fine = true;
-        for (unsigned item = blockIdx.x; fine; item += gridDim.x) {
+        Items next = B::items();
+        for (; fine; fine = fine && next.next(x)) {
             Plan u;
-            if (item >= items) {
+            if (!next.any) {
                 u.rounds = 0;
-            } else if (!plan(u, item)) {
+            } else if (!plan(u, next.item)) {
                 p.redo[u.flag] = p.redo[u.flag + (p.Nq + p.Nk)] = 0;  // no tile there
                 continue;
             }
@@ -211,6 +212,7 @@ struct Dq : Base<D, true, QueryPlan> {
             for (int i = 0; i < u.rounds; ++i) {
                 const int row = (int)(u.bos + (long long)u.kt.tile(i) * 128);
                 const uint32_t bytes = u.small(i) ? kSinkCols * D * 2 : Y::kTile;
+                if (i + 2 >= u.rounds) next.ask();
                 if (!(fine = B::free_x(kx))) break;
                 mbar_arrive_expect_tx(bar(Y::bX + kx % Y::NX), bytes);
                 B::tma_tile(B::at_x(kx), u.small(i) ? mks : mk, bar(Y::bX + kx % Y::NX), u.hk, row);
@@ -221,6 +223,7 @@ struct Dq : Base<D, true, QueryPlan> {
                 ++ky;
             }
         }
+        next.drain();
         B::drain(kx, ky, qn);
     }
 
@@ -389,8 +392,8 @@ struct Dq : Base<D, true, QueryPlan> {
 
 // ---- dk and dv ------------------------------------------------------------------
 
-// Items: a key tile of 128 tokens and a key head; then (parts) a run of query tiles that see the
-// sinks of a sequence alone.
+// Items: (parts) a run of query tiles that see the sinks of a sequence alone; then a key tile of 128 tokens and a
+// key head.
 struct KeyPlan {
     long long bos, flag;
     long long place;   // of the sinks' rows of this item among the parts
@@ -405,10 +408,11 @@ struct Parts {  // how the query tiles behind the window are cut
 
 __device__ __forceinline__ bool key_plan(KeyPlan &u, const WindowParams &p, long long slots, const Parts &parts, unsigned item) {
     const Sight sight{p.window, p.sinks};
-    const long long main_items = slots * p.Nk;
+    // the parts first: they are long
+    const unsigned part_items = (unsigned)(parts.slots * p.Nk);
     u.hk = item % p.Nk;
-    u.part = item >= main_items;
-    const unsigned slot = (unsigned)((u.part ? item - main_items : item) / p.Nk);
+    u.part = item < part_items;
+    const unsigned slot = u.part ? item / p.Nk : slot_in_order(p.seq, (item - part_items) / p.Nk, (unsigned)slots, true);
     u.flag = (long long)slot * 2 * (p.Nq + p.Nk) + p.Nq + u.hk;
     const SeqTile s = seq_tile(p.seq, slot, u.part ? parts.tiles * 128 : 128);
     if (!s.ok || s.t0 >= s.t1) return false;
@@ -440,7 +444,6 @@ struct Dkv : Base<D, false, KeyPlan> {
     using B::p;
     using B::tm;
     using B::x;
-    unsigned items;
     long long slots;
     Parts parts;
     static constexpr uint32_t tS = 0, tDP = 128, tDV = 256, tDK = 384;
@@ -462,11 +465,12 @@ struct Dkv : Base<D, false, KeyPlan> {
     __device__ void load(const CUtensorMap *mq, const CUtensorMap *mg, const CUtensorMap *mk, const CUtensorMap *mv) {
         unsigned kx = 0, ky = 0, kn = 0;
         bool fine = true;
-        for (unsigned item = blockIdx.x; fine; item += gridDim.x) {
+        Items next = B::items();
+        for (; fine; fine = fine && next.next(x)) {
             KeyPlan u;
-            if (item >= items) {
+            if (!next.any) {
                 u.rounds = 0;
-            } else if (!key_plan(u, p, slots, parts, item)) {
+            } else if (!key_plan(u, p, slots, parts, next.item)) {
                 if (!u.part) p.redo[u.flag] = p.redo[u.flag + (p.Nq + p.Nk)] = 0;  // no tile there
                 continue;
             }
@@ -480,6 +484,7 @@ struct Dkv : Base<D, false, KeyPlan> {
             Round r(u, p.Nq / p.Nk);
             for (int i = 0; i < u.rounds; ++i, r.step(u)) {
                 const int row = (int)(u.bos + r.tile * 128);
+                if (i + 2 >= u.rounds) next.ask();
                 if (!(fine = B::free_x(kx))) break;
                 mbar_arrive_expect_tx(bar(Y::bX + kx % Y::NX), Y::kTile);
                 B::tma_tile(B::at_x(kx), mq, bar(Y::bX + kx % Y::NX), r.h, row);
@@ -490,6 +495,7 @@ struct Dkv : Base<D, false, KeyPlan> {
                 ++ky;
             }
         }
+        next.drain();
         B::drain(kx, ky, kn);
     }
 
@@ -720,6 +726,7 @@ __device__ __forceinline__ void set_up(F &f, uint8_t *raw_smem, unsigned *status
         mbar_init(f.bar(Y::bOutEmpty), 8);
         for (int i = 0; i < kPlans; ++i) mbar_init(f.bar(Y::bPlan + i), 1);
         mbar_init(f.bar(Y::bDrain), 1);
+        mbar_init(f.bar(Y::bItem), 1);
         for (int i = 0; i < 4; ++i) {
             mbar_init(f.bar(Y::bPair + i), 2);
             mbar_init(f.bar(Y::bTaken + i), 2);
@@ -749,9 +756,9 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 window_dq(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mg, const __grid_constant__ CUtensorMap mk,
           const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mks, const __grid_constant__ CUtensorMap mvs,
-          const __grid_constant__ WindowParams p, unsigned items, long long slots) {
+          const __grid_constant__ WindowParams p, long long slots) {
     extern __shared__ uint8_t smem_raw[];
-    Dq<D> f{{Ctx{}, p, 0u}, items, slots};
+    Dq<D> f{{Ctx{}, p, 0u}, slots};
     set_up(f, smem_raw, p.seq.status);
     wait_for_launches();
     const int warp = threadIdx.x >> 5;
@@ -770,9 +777,9 @@ window_dq(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 window_dkv(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mg, const __grid_constant__ CUtensorMap mk,
-           const __grid_constant__ CUtensorMap mv, const __grid_constant__ WindowParams p, unsigned items, long long slots, Parts parts) {
+           const __grid_constant__ CUtensorMap mv, const __grid_constant__ WindowParams p, long long slots, Parts parts) {
     extern __shared__ uint8_t smem_raw[];
-    Dkv<D> f{{Ctx{}, p, 0u}, items, slots, parts};
+    Dkv<D> f{{Ctx{}, p, 0u}, slots, parts};
     set_up(f, smem_raw, p.seq.status);
     wait_for_launches();
     const int warp = threadIdx.x >> 5;
@@ -844,11 +851,9 @@ cudaError_t launch(const WindowParams &p, cudaStream_t stream) {
     const long long rows = p.seq.tokens * p.Nq, blocks = (rows + 8192 / D - 1) / (8192 / D);
     err = launch_after(window_dsum<D>, dim3((unsigned)(blocks < kSms * 8 ? blocks : kSms * 8)), dim3(256), 0, stream, p, rows);
     if (err != cudaSuccess) return err;
-    err = launch_after(window_dq<D>, dim3((unsigned)(qi < kSms ? qi : kSms)), dim3(kThreads), q_bytes, stream, mq, mg, mk, mv, mks, mvs, p,
-                       (unsigned)qi, slots);
+    err = launch_after(window_dq<D>, dim3((unsigned)qi), dim3(kThreads), q_bytes, stream, mq, mg, mk, mv, mks, mvs, p, slots);
     if (err != cudaSuccess) return err;
-    err = launch_after(window_dkv<D>, dim3((unsigned)(ki < kSms ? ki : kSms)), dim3(kThreads), k_bytes, stream, mq, mg, mk, mv, p, (unsigned)ki,
-                       slots, parts);
+    err = launch_after(window_dkv<D>, dim3((unsigned)ki), dim3(kThreads), k_bytes, stream, mq, mg, mk, mv, p, slots, parts);
     return err == cudaSuccess ? window_sink_sums(p, true, stream) : err;
 }
 

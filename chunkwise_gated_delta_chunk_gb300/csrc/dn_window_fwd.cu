@@ -29,7 +29,7 @@
 // A masked pair weighs 0, and 0 times an infinite or NaN value is NaN.  Rows that come out so are marked in
 // lse, and taken again by a kernel that leaves masked pairs out (dn_window_simt.cu).
 //
-// CTAs are persistent, one an SM; every wait is bounded (dn_tc_sync.cuh).  Measured: one prompt of 32768 tokens,
+// CTAs are persistent, one an SM, and take items as they get done (Items); every wait is bounded (dn_tc_sync.cuh).  Measured: one prompt of 32768 tokens,
 // window 4096, 32 heads on 8 of 128 columns, 1.37 to 1.45 ms (1.09 at the measured rate of products in the pairs that
 // are seen); 4 x 2048 tokens, window 512, 16 heads, 56 us, the tensor pipe at work 40 % of the time: an item's first
 // and last tiles have nothing to overlap with.
@@ -54,8 +54,8 @@ struct Lay {
     // barriers
     static constexpr int bQFull = 0, bQEmpty = 1, bFull = 2, bEmpty = bFull + NS, bS = bEmpty + NS, bP = bS + 2, bO = bP + 2,
                          bOEmpty = bO + 2, bDrain = bOEmpty + 2, bPair = bDrain + 1, bPlan = bPair + 8, bPlanEmpty = bPlan + kPlans,
-                         kBars = bPlanEmpty + kPlans;
-    static constexpr uint32_t kBox = (kBar + 8 * kBars + 15) / 16 * 16, kWish = kBox + 2 * 2 * 2 * 128 * 4, kPlan = kWish + 2 * 2 * 128 * 4, kMisc = kPlan + kPlans * 96, kAlloc = kMisc + 16 + 1024;
+                         bItem = bPlanEmpty + kPlans, kBars = bItem + 1;
+    static constexpr uint32_t kBox = (kBar + 8 * kBars + 15) / 16 * 16, kWish = kBox + 2 * 2 * 2 * 128 * 4, kPlan = kWish + 2 * 2 * 128 * 4, kMisc = kPlan + kPlans * 96, kAlloc = kMisc + 32 + 1024;
     static_assert(kAlloc <= 232448, "exceeds the 227 KB of shared memory per CTA");
     // tensor memory columns
     static constexpr uint32_t tS = 0, tO = 256, kCols = 512;
@@ -83,15 +83,14 @@ struct __align__(16) Plan {
     __device__ __forceinline__ bool small(int i) const { return narrow && i == 0; }
 };
 
-// Items are numbered with a key head's pairs next to each other and late tiles first: under a
-// causal mask these are the long ones.
+// Items are numbered with a key head's pairs next to each other and late tiles first.
 __device__ __forceinline__ bool plan(Plan &u, const WindowParams &p, unsigned item, long long slots) {
     const int G = p.Nq / p.Nk;
     const bool by_head = G % 2 == 0;
     const int pairs = by_head ? G / 2 : G;
     const int pr = item % pairs;
     u.hk = item / pairs % p.Nk;
-    const unsigned slot = (unsigned)(slots - 1 - item / pairs / p.Nk);
+    const unsigned slot = slot_in_order(p.seq, item / pairs / p.Nk, (unsigned)slots, false);
     const SeqTile s = seq_tile(p.seq, slot, by_head ? 128 : 256);
     if (!s.ok || s.t0 >= s.t1) return false;
     u.bos = s.bos;
@@ -132,7 +131,6 @@ struct Fwd {
     using Y = Lay<D>;
     Ctx x;
     const WindowParams &p;
-    unsigned items;
     long long slots;
     uint32_t tm;
 
@@ -158,10 +156,11 @@ struct Fwd {
                          const CUtensorMap *mvs) {
         unsigned un = 0, qn = 0;
         bool fine = true;
-        for (unsigned item = blockIdx.x; fine; item += gridDim.x) {
+        Items next{bar(Y::bItem), x.base + Y::kMisc + 16};
+        for (; fine; fine = fine && next.next(x)) {
             Plan u;
-            if (item >= items) u.n = 0;
-            else if (!plan(u, p, item, slots)) continue;
+            if (!next.any) u.n = 0;
+            else if (!plan(u, p, next.item, slots)) continue;
             if (!(fine = wait(x, bar(Y::bQEmpty), (qn & 1) ^ 1) && wait(x, bar(Y::bPlanEmpty + qn % kPlans), (qn / kPlans & 1) ^ 1))) break;
             *place(qn) = u;
             mbar_arrive(bar(Y::bPlan + qn % kPlans));
@@ -175,6 +174,7 @@ struct Fwd {
             ++qn;
             for (int i = 0; i <= u.n; ++i, ++un) {
                 const int s = un % Y::NS;
+                if (i + 1 >= u.n) next.ask();
                 if (!(fine = wait(x, bar(Y::bEmpty + s), ((un / Y::NS) & 1) ^ 1))) break;
                 const bool vs = i > 0 && u.small(i - 1), ks = u.small(i);
                 uint32_t bytes = 0;
@@ -192,6 +192,7 @@ struct Fwd {
             }
         }
         // copies still in flight land before the CTA ends
+        next.drain();
         if (qn) wait_drain(bar(Y::bQFull), (qn - 1) & 1);
         for (unsigned i = un > Y::NS ? un - Y::NS : 0; i < un; ++i) wait_drain(bar(Y::bFull + i % Y::NS), (i / Y::NS) & 1);
     }
@@ -431,7 +432,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 window_fwd(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
            const __grid_constant__ CUtensorMap mks, const __grid_constant__ CUtensorMap mvs, const __grid_constant__ WindowParams p,
-           unsigned items, long long slots) {
+           long long slots) {
     using Y = Lay<D>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -461,6 +462,7 @@ window_fwd(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
             mbar_init(bar(Y::bPlanEmpty + i), 17);
         }
         mbar_init(bar(Y::bDrain), 1);
+        mbar_init(bar(Y::bItem), 1);
         *x.abort_flag = 0;
         fence_barrier_init();
     }
@@ -472,11 +474,9 @@ window_fwd(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    Fwd<D> f{x, p, items, slots, *reinterpret_cast<volatile uint32_t *>(x.gbase + Y::kMisc)};
+    Fwd<D> f{x, p, slots, *reinterpret_cast<volatile uint32_t *>(x.gbase + Y::kMisc)};
     wait_for_launches();
     if (warp == 16) {
-        if (blockIdx.x == 0) check_offsets(p.seq, threadIdx.x & 31, 32);
-        __syncwarp();
         if ((threadIdx.x & 31) == 0) f.load(&mq, &mk, &mv, &mks, &mvs);
         __syncwarp();
     } else if (warp == 17) {
@@ -505,8 +505,7 @@ cudaError_t launch(const WindowParams &p, cudaStream_t stream) {
         return cudaErrorInvalidValue;
     const cudaError_t err = allow_smem<window_fwd<D>>((int)Lay<D>::kAlloc);
     if (err != cudaSuccess) return err;
-    const unsigned grid = (unsigned)(items < kSms ? items : kSms);
-    return launch_after(window_fwd<D>, dim3(grid), dim3(kThreads), Lay<D>::kAlloc, stream, mq, mk, mv, mks, mvs, p, (unsigned)items, slots);
+    return launch_after(window_fwd<D>, dim3((unsigned)items), dim3(kThreads), Lay<D>::kAlloc, stream, mq, mk, mv, mks, mvs, p, slots);
 }
 
 }  // namespace

@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(NT, D == 64 ? 2 : 1) simt_fwd(WindowParams p, 
     constexpr int kTile = Smem<D>::kTile;
     float *Qs = s_win, *Kb = Qs + kTile, *Vs = Kb + 2 * kTile, *Ps = Vs + kTile;
     wait_for_launches();
-    if (!REDO && blockIdx.x == 0) check_offsets(p.seq, threadIdx.x, NT);
+    if (REDO && blockIdx.x == 0) check_offsets(p.seq, threadIdx.x, NT);  // the last kernel of every forward
     // a group: the heads of half a slot
     auto marked = [&](long long g) {
         const Half it(p.seq, g * p.Nq, p.Nq);

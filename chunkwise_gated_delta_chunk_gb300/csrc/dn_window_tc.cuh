@@ -87,6 +87,53 @@ __device__ __forceinline__ bool hold(const tcs::Ctx &x, uint32_t bar, uint32_t p
     }
 }
 
+// Slot number i in the order in which items are taken: the last tiles of the sequences first (under a causal mask the
+// long ones) or, `up`, the first ones.  Without offsets by tile, then by sequence, so that the short ones
+// come last of all and fill the gaps; with offsets sequence by sequence.
+__device__ __forceinline__ unsigned slot_in_order(const SeqView &s, unsigned i, unsigned slots, bool up) {
+    if (s.cu) return up ? i : slots - 1 - i;
+    const unsigned per = slots / s.N, c = i / s.N, n = i - c * s.N;
+    return n * per + (up ? c : per - 1 - c);
+}
+
+// ---- items of a block ---------------------------------------------------------
+// A block for every item is launched, as many as fit run, and a running block takes over items whose
+// blocks have not begun: whoever is done first takes the next one.  One thread asks, some time before the
+// block needs the item; `reply`: 16 bytes of shared memory.
+struct Items {
+    uint32_t bar, reply;
+    unsigned item = blockIdx.x, asked = 0, got = 0;
+    bool any = true;  // `item` is one
+    __device__ __forceinline__ void ask() {
+        if (!any || asked != got) return;
+        ++asked;
+        ptx::mbar_arrive_expect_tx(bar, 16);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the last reply was read
+        asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(reply),
+                     "r"(bar)
+                     : "memory");
+    }
+    __device__ __forceinline__ bool next(const tcs::Ctx &x) {  // false: the block is giving up
+        ask();
+        if (!any) return true;
+        if (!tcs::wait(x, bar, got & 1)) return false;
+        ++got;
+        uint32_t some;
+        asm volatile(
+            "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\tld.shared.b128 r, [%2];\n\t"
+            "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\tselp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+            "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+            : "=r"(some), "=r"(item)
+            : "r"(reply)
+            : "memory");
+        any = some != 0;
+        return true;
+    }
+    __device__ __forceinline__ void drain() const {
+        if (asked != got) tcs::wait_drain(bar, got & 1);
+    }
+};
+
 // ---- MMAs of a whole warp ---------------------------------------------------
 // One lane of a converged warp issues; the others run along, so that loops, waits and descriptors
 // stay warp-uniform (a branch of one thread made every MMA take about 115 cycles to issue; it takes
