@@ -20,19 +20,21 @@
 // each, the two tiles fell into step: both in the softmax, then both on the tensor cores, 15 % slower).
 //
 // What a row's weights are relative to is the maximum of the first tile that it sees.  It moves up, and O and
-// the sum are rescaled, only when the weights of half a tile have summed to more than 2^16, so that later tiles
-// need no maximum: sums in fp32 lose nothing, P in bf16 has the same relative rounding at every size.  A row whose weights pass fp32 within one tile (scores that grow by more than 2^127 from
-// one tile to the next) comes out not finite, and is marked.  Masks cost selects only in tiles that the
-// window's or the sequence's border crosses.  The sinks in front of the window are a tile of 32 keys where they
-// fit in one.  P is rounded to bf16 for the product, by half a step of each weight; the sum takes it unrounded.
+// the sum are rescaled, only when the weights of half a tile have summed to more than 2^16, so that later
+// tiles need no maximum: sums in fp32 lose nothing, P in bf16 has the same relative rounding at every
+// size.  A row whose weights pass fp32 within one tile (a score, in units of log 2, 128 above the reference)
+// comes out not finite, and is marked.  Masks cost selects only in tiles that the window's or the
+// sequence's border crosses.  The sinks in front of the window are a tile of 32 keys where they fit in
+// one.  P is rounded to bf16 for the product, by half a step of each weight; the sum takes it unrounded.
 //
 // A masked pair weighs 0, and 0 times an infinite or NaN value is NaN.  Rows that come out so are marked in
 // lse, and taken again by a kernel that leaves masked pairs out (dn_window_simt.cu).
 //
-// CTAs are persistent, one an SM, and take items as they get done (Items); every wait is bounded (dn_tc_sync.cuh).  Measured: one prompt of 32768 tokens,
-// window 4096, 32 heads on 8 of 128 columns, 1.37 to 1.45 ms (1.09 at the measured rate of products in the pairs that
-// are seen); 4 x 2048 tokens, window 512, 16 heads, 56 us, the tensor pipe at work 40 % of the time: an item's first
-// and last tiles have nothing to overlap with.
+// CTAs are persistent, one an SM, and take items as they get done (Items: 47 us for the training shape below, 56 with
+// items at a fixed stride); every wait is bounded (dn_tc_sync.cuh).  Measured: one prompt of 32768
+// tokens, window 4096, 32 heads on 8 of 128 columns, 1.35 to 1.42 ms (1.09 at the measured rate of products in
+// the pairs that are seen); 4 x 2048 tokens, window 512, 16 heads, 47 us, the tensor pipe at work 39 % of the time: an
+// item's first and last tiles have nothing to overlap with.
 #include "dn_window_tc.cuh"
 
 namespace dn {
