@@ -149,7 +149,7 @@ struct Base {
                     w[2 * h + (e >> 3)][e & 7] = pack_bf16(lo, hi);
                 }
             }
-            store_rows64(to + c, stride, from_row, rows, w);
+            store_rows<64>(to + c, stride, from_row, rows, w);
         }
         const int r = threadIdx.x & 31;
         return isnan(sum_of(bad)) && r >= from_row && r < rows;

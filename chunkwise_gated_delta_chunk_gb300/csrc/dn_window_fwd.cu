@@ -400,26 +400,17 @@ struct Fwd {
             __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.o) + at * D + D / 2 * h;
             f2 bads = 0ull;
             const f2 ff = both(f);
-            if constexpr (D == 128) {
-                uint32_t w[4][8];
+            uint32_t w[4][D / 16];
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    uint32_t s[16];
-                    tmem_ld16(to + 16 * g, s);
-                    tmem_wait_ld_dep16(s);
-                    scaled(s, w[g], ff, bads);
-                }
-                store_rows64(out, (long long)p.Nq * D, 0, L - (t & ~31), w);
-            } else {
+            for (int g = 0; g < D / 32; ++g) {
+                uint32_t s[16], v[8];
+                tmem_ld16(to + 16 * g, s);
+                tmem_wait_ld_dep16(s);
+                scaled(s, v, ff, bads);
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    uint32_t s[16], w[8];
-                    tmem_ld16(to + 16 * g, s);
-                    tmem_wait_ld_dep16(s);
-                    scaled(s, w, ff, bads);
-                    if (t < L) store32(out + 16 * g, w);
-                }
+                for (int e = 0; e < 8; ++e) w[(8 * g + e) / (D / 16)][(8 * g + e) % (D / 16)] = v[e];
             }
+            store_rows<D / 2>(out, (long long)p.Nq * D, 0, L - (t & ~31), w);
             tc_fence_before();
             warp_arrive(bar(Y::bOEmpty + q));
             float bad = sum_of(bads);

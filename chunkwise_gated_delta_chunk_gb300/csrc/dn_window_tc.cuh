@@ -39,16 +39,25 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
-__device__ __forceinline__ void store32(void *dst, const uint32_t (&r)[8]) {  // 32 bytes at once
+__device__ __forceinline__ void store16(void *dst, const uint32_t *r) {  // 16 bytes at once
+    asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(dst), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+}
+__device__ __forceinline__ void store32(void *dst, const uint32_t *r) {  // 32 bytes at once, to an address on 32 bytes
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(r[0]), "r"(r[1]), "r"(r[2]),
                  "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
 
-// 64 columns of bf16 of 32 rows, a row a lane, to global memory: four neighbouring lanes swap their quarters
-// first, so that each store fills 128 bytes of a row (a row a lane, it takes twice as long).
-// `to`: the lane's own row; `stride`: elements from row to row; rows from `from` up to `rows` are written.
-__device__ __forceinline__ void store_rows64(__nv_bfloat16 *to, long long stride, int from, int rows, uint32_t (&w)[4][8]) {
+// N columns of bf16 of 32 rows, a row a lane, to global memory: four neighbouring lanes swap their quarters
+// first, so that each store fills 2 N bytes of a row (a row a lane, it takes twice as long).
+// w: the columns two by two; `to`: the lane's own row; `stride`: elements from row to row, a multiple of 64; rows from
+// `from` up to `rows` are written.
+// Tensors begin on 16 bytes, and on 32 as a rule: then the quarters of 64 columns are stored whole.  By halves always
+// (with pieces of 16 bytes exchanged, so that a store fills 64 bytes of a row): training step 224 to 228 us, packed
+// prompts 298 to 301.
+template <int N>
+__device__ __forceinline__ void store_rows(__nv_bfloat16 *to, long long stride, int from, int rows, uint32_t (&w)[4][N / 8]) {
+    static_assert(N == 32 || N == 64, "quarters of 16 or 32 bytes");
     const int lane = threadIdx.x & 31, q = lane & 3;
 #pragma unroll
     for (int x = 1; x <= 2; x <<= 1)
@@ -57,16 +66,24 @@ __device__ __forceinline__ void store_rows64(__nv_bfloat16 *to, long long stride
             if (a & x) continue;
             const int b = a | x;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < N / 8; ++e) {
                 const uint32_t got = __shfl_xor_sync(0xffffffffu, q & x ? w[a][e] : w[b][e], x);
                 if (q & x) w[a][e] = got;
                 else w[b][e] = got;
             }
         }
-    __nv_bfloat16 *first = to - q * stride + 16 * q;
+    __nv_bfloat16 *first = to - q * stride + N / 4 * q;
+    const bool whole = N == 64 && (reinterpret_cast<uintptr_t>(first) & 31) == 0;  // the same for all rows
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        if ((lane & ~3) + j >= from && (lane & ~3) + j < rows) store32(first + j * stride, w[j]);
+    for (int j = 0; j < 4; ++j) {
+        if ((lane & ~3) + j < from || (lane & ~3) + j >= rows) continue;
+        if (whole) {
+            if constexpr (N == 64) store32(first + j * stride, w[j]);
+        } else {
+#pragma unroll
+            for (int h = 0; h < N / 32; ++h) store16(first + j * stride + 8 * h, w[j] + 4 * h);
+        }
+    }
 }
 
 // Wait of a whole warp, bounded like wwait of dn_tc_sync.cuh but without a call: what is in

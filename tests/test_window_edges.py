@@ -1,0 +1,116 @@
+"""GPU: attention over a window, its cache and the norms around a block at the edges of what their headers allow:
+tensors that begin on 16 bytes and on no more."""
+import pytest
+import torch
+
+from conftest import cuda_ok
+from test_block_norm import args
+from test_block_norm import inputs as block_inputs
+from test_window_attn import DEV, DTYPES, inputs, normal, ok
+
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not cuda_ok(), reason="needs a CUDA GPU")]
+
+
+# ---- tensors that begin on 16 bytes ------------------------------------------------------------
+
+
+class Behind:
+    """Tensors 16 bytes behind an aligned address, each with 16 bytes in front of it and behind it that hold 7."""
+
+    def __init__(self):
+        self.all = []
+
+    def __call__(self, x, keep=True):
+        if x is None:
+            return None
+        pad = 16 // x.element_size()
+        space = torch.full((x.numel() + 2 * pad,), 7, dtype=x.dtype, device=x.device)
+        view = space[pad:pad + x.numel()].view(x.shape)
+        if keep:
+            view.copy_(x)
+        assert view.data_ptr() % 32 == 16
+        self.all.append((space, pad, x.numel()))
+        return view
+
+    def untouched(self):
+        return all((s[:p] == 7).all() and (s[p + n:] == 7).all() for s, p, n in self.all)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Nq,Nk,T,window,sinks", [(4, 2, 150, 70, 4), (3, 1, 520, 100, 40), (2, 2, 1, 1, 0)])
+def test_attention_on_16_bytes(lib, dtype, d, Nq, Nk, T, window, sinks):
+    """The same bits as with tensors on 256 bytes, and nothing beside the tensors is written."""
+    t = inputs(dtype, B=2, T=T, Nq=Nq, Nk=Nk, d=d, seed=d + T)
+    o, lse = lib.window_attn_fwd(t["q"], t["k"], t["v"], window, sinks)
+    want = lib.window_attn_bwd(t["q"], t["k"], t["v"], o, lse, window, sinks, do=t["do"])
+    ok(lib)
+    off = Behind()
+    u = {n: off(x) for n, x in t.items()}
+    o2, lse2 = off(o, False), off(lse, False)
+    lib.window_attn_fwd(u["q"], u["k"], u["v"], window, sinks, o=o2, lse=lse2)
+    ok(lib)
+    assert torch.equal(o2, o) and torch.equal(lse2, lse)
+    got = {n: off(x, False) for n, x in want.items()}
+    code = lib.dtype_code(dtype)
+    need = lib.load().dn_window_attn_bwd_workspace_bytes(0, 2, 2, T, Nq, Nk, d, window, sinks, code)
+    space = off(torch.empty(need, dtype=torch.uint8, device=DEV), False)
+    at = lambda x: x.data_ptr()
+    assert lib.load().dn_window_attn_bwd(at(u["q"]), at(u["k"]), at(u["v"]), at(o2), at(lse2), None, 2, 2, T, Nq, Nk, d, window,
+                                         sinks, code, 0.0, at(u["do"]), at(got["dq"]), at(got["dk"]), at(got["dv"]), at(space),
+                                         need, torch.cuda.current_stream().cuda_stream) == lib.DN_OK
+    ok(lib)
+    assert all(torch.equal(got[n], want[n]) for n in want)
+    assert off.untouched()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d", [64, 128])
+def test_cache_on_16_bytes(lib, dtype, d):
+    N, Nq, Nk, window, sinks, ring = 2, 6, 2, 50, 3, 60
+    t = inputs(dtype, B=N, T=41, Nq=Nq, Nk=Nk, d=d, seed=d)
+    new = {n: t[n][:, :1].contiguous() for n in "qkv"}
+    g = torch.Generator().manual_seed(1)
+    cache = [normal(g, N, Nk, sinks + ring, d, dtype=dtype) for _ in range(2)]
+    had = torch.tensor([5, 777], device=DEV)
+
+    def calls(place, o):
+        k, v, kc, vc, ln = (place(x) for x in (t["k"], t["v"], *cache, had))
+        lib.window_cache_fill(k, v, kc, vc, ln, sinks)
+        lib.window_attn_step(*(place(new[n]) for n in "qkv"), kc, vc, place(ln + 41), window, sinks, o=o)
+        return kc, vc
+
+    o = torch.empty_like(new["q"])
+    want = calls(lambda x: x.clone(), o)
+    off = Behind()
+    o2 = off(o, False)
+    got = calls(off, o2)
+    ok(lib)
+    assert torch.equal(o2, o) and all(torch.equal(a, b) for a, b in zip(got, want))
+    assert off.untouched()
+
+
+@pytest.mark.parametrize("types", [(torch.bfloat16, torch.float32), (torch.bfloat16, torch.bfloat16), (torch.float32, torch.float32)])
+@pytest.mark.parametrize("D", [1024, 520, 33])
+def test_block_on_16_bytes(lib, types, D):
+    rows = 37
+    t, g = block_inputs(types, rows, D, seed=D)
+    y, h = lib.block_norm_fwd(*args(t))
+    want = lib.block_norm_bwd(*args(t), **g)
+    off = Behind()
+    u, ug = ({n: off(x) for n, x in m.items()} for m in (t, g))
+    y2, h2 = off(y, False), off(h, False)
+    lib.block_norm_fwd(*args(u), y=y2, residual_out=h2)
+    ok(lib)
+    assert torch.equal(y2, y) and torch.equal(h2, h)
+    got = {n: off(x, False) for n, x in want.items()}
+    code = [lib.dtype_code(x) for x in types]
+    need = lib.load().dn_block_norm_bwd_workspace_bytes(rows, D, *code)
+    space = off(torch.empty(need, dtype=torch.uint8, device=DEV), False)
+    at = lambda x: None if x is None else x.data_ptr()
+    assert lib.load().dn_block_norm_bwd(*(at(x) for x in args(u)), rows, D, *code, 1e-5, lib.DN_NORM_POST, at(ug["dy"]),
+                                        at(ug["dresidual_out"]), *(at(x) for x in got.values()), at(space), need,
+                                        torch.cuda.current_stream().cuda_stream) == lib.DN_OK
+    ok(lib)
+    assert all(want[n] is None or torch.equal(got[n], want[n]) for n in want)
+    assert off.untouched()
