@@ -57,7 +57,7 @@ struct Lay {
     static constexpr int bQFull = 0, bQEmpty = 1, bFull = 2, bEmpty = bFull + NS, bS = bEmpty + NS, bP = bS + 2, bO = bP + 2,
                          bOEmpty = bO + 2, bDrain = bOEmpty + 2, bPair = bDrain + 1, bPlan = bPair + 8, bPlanEmpty = bPlan + kPlans,
                          bItem = bPlanEmpty + kPlans, kBars = bItem + 1;
-    static constexpr uint32_t kBox = (kBar + 8 * kBars + 15) / 16 * 16, kWish = kBox + 2 * 2 * 2 * 128 * 4, kPlan = kWish + 2 * 2 * 128 * 4, kMisc = kPlan + kPlans * 96, kAlloc = kMisc + 32 + 1024;
+    static constexpr uint32_t kBox = (kBar + 8 * kBars + 15) / 16 * 16, kWish = kBox + 2 * 2 * 2 * 128 * 4, kPlan = kWish + 2 * 2 * 2 * 128 * 4, kMisc = kPlan + kPlans * 96, kAlloc = kMisc + 32 + 1024;
     static_assert(kAlloc <= 232448, "exceeds the 227 KB of shared memory per CTA");
     // tensor memory columns
     static constexpr uint32_t tS = 0, tO = 256, kCols = 512;
@@ -301,6 +301,9 @@ struct Fwd {
     __device__ void softmax(int q, int h) {
         const int warp = threadIdx.x >> 5, row = threadIdx.x & 127;
         const uint32_t ts = lane_base(tm, warp) + Y::tS + 128 * q + 64 * h, to = lane_base(tm, warp) + Y::tO + D * q + D / 2 * h;
+        // Wishes for a higher reference have two places, for tiles in turn: both threads of a row take up what tile j left in
+        // tile j + 1, and whoever is done with that first may write before the other one has read.  (A write in every
+        // tile costs 1 % of the kernel; one in two tiles from each new wish on, 3 %.)
         volatile float *wish = reinterpret_cast<float *>(x.gbase + Y::kWish) + q * 256 + row;
         const float c = p.scale * kLog2e;
         const Sight sight{p.window, p.sinks};
@@ -314,8 +317,9 @@ struct Fwd {
             read_plan(qn);
             if (!v.act) continue;
             const int t = v.t0 + row;
-            // what weights are relative to, times log2 e scale: -infinity until the row has seen a key; sum of the weights
-            float m = -CUDART_INF_F, l = 0.f;
+            // what weights are relative to, times log2 e scale: -infinity until the row has seen a key; sum of the weights;
+            // the highest reference that this thread has wished for
+            float m = -CUDART_INF_F, l = 0.f, mine = -CUDART_INF_F;
             for (int i = v.zero ? 0 : v.from; i <= v.to; i = i + 1 < v.from ? v.from : i + 1) {
                 const int k0 = (sink && i == 0 ? 0 : lo + i) * 128 + 64 * h;
                 const int groups = narrow && i == 0 ? 2 - 2 * h : 4;  // of 16 keys
@@ -339,10 +343,10 @@ struct Fwd {
                     if (!swap(q, h, top, other, nx)) return;
                     if (m == -CUDART_INF_F) {
                         m = fmaxf(top, other) * c;
-                        wish[128 * h] = m;
                     }
                 } else {
-                    const float want = fmaxf(wish[0], wish[128]);
+                    // what the two threads left in the tile before
+                    const float want = fmaxf(mine, wish[512 * (ns & 1) + 128 * (h ^ 1)]);
                     if (__any_sync(0xffffffffu, want > m)) {
                         const float f = want > m ? ex2(m - want) : 1.f;
                         m = want > m ? want : m;
@@ -384,7 +388,8 @@ struct Fwd {
                 }
                 const float part = sum_of(add2(sum[0], sum[1]));
                 l += part;
-                if (part > kGrown) wish[128 * h] = m + lg2(part);
+                if (part > kGrown) mine = fmaxf(mine, m + lg2(part));
+                wish[512 * ((ns & 1) ^ 1) + 128 * h] = mine;
                 tmem_wait_st();
                 tc_fence_before();
                 warp_arrive(bar(Y::bP + q));

@@ -1,12 +1,12 @@
 """GPU: attention over a window, its cache and the norms around a block at the edges of what their headers allow:
-tensors that begin on 16 bytes and on no more."""
+tensors that begin on 16 bytes and on no more; scores that rise steeply along the keys."""
 import pytest
 import torch
 
 from conftest import cuda_ok
 from test_block_norm import args
 from test_block_norm import inputs as block_inputs
-from test_window_attn import DEV, DTYPES, inputs, normal, ok
+from test_window_attn import DEV, DTYPES, check, inputs, normal, ok
 
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not cuda_ok(), reason="needs a CUDA GPU")]
 
@@ -114,3 +114,28 @@ def test_block_on_16_bytes(lib, types, D):
     ok(lib)
     assert all(want[n] is None or torch.equal(got[n], want[n]) for n in want)
     assert off.untouched()
+
+
+# ---- references of the weights that move ---------------------------------------------------------
+
+
+def steep(Nq, Nk, d, T, seed):
+    """bf16 operands whose scores (scale 1) rise by 13 from one half of a key tile to the next, so that the reference
+    that a row's weights are relative to moves in every tile, for one half's sake or the other's."""
+    t = inputs(torch.bfloat16, B=1, T=T, Nq=Nq, Nk=Nk, d=d, seed=seed)
+    t["q"] *= 0.125
+    t["q"][..., 0] = 1
+    t["k"][..., 0] = 13 * (torch.arange(T, device=DEV)[None, :, None] // 64)  # whole numbers that bf16 holds
+    return t
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Nq,Nk,window,sinks", [(4, 2, 5000, 0), (3, 1, 700, 40)])
+def test_references_that_move_in_every_tile(lib, d, Nq, Nk, window, sinks):
+    """Both threads of a row move on in the same tile: results within their bounds, and the same bits every time."""
+    t = steep(Nq, Nk, d, 1250, d)
+    o, lse, out = check(lib, t, window, sinks, scale=1.0, label="steep")
+    for _ in range(50):
+        again = lib.window_attn_fwd(t["q"], t["k"], t["v"], window, sinks, scale=1.0)
+        assert torch.equal(again[0], o) and torch.equal(again[1], lse)
+    ok(lib)
