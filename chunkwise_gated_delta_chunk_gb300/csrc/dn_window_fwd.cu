@@ -22,8 +22,8 @@
 // What a row's weights are relative to is the maximum of the first tile that it sees.  It moves up, and O and
 // the sum are rescaled, only when the weights of half a tile have summed to more than 2^16, so that later
 // tiles need no maximum: sums in fp32 lose nothing, P in bf16 has the same relative rounding at every
-// size.  A row whose weights pass fp32 within one tile (a score, in units of log 2, 128 above the reference)
-// comes out not finite, and is marked.  Masks cost selects only in tiles that the window's or the
+// size.  A row whose weights sum to 2^124 within half a tile (a score, in units of log 2, 124 above the reference)
+// is marked.  Masks cost selects only in tiles that the window's or the
 // sequence's border crosses.  The sinks in front of the window are a tile of 32 keys where they fit in
 // one.  P is rounded to bf16 for the product, by half a step of each weight; the sum takes it unrounded.
 //
@@ -65,6 +65,10 @@ struct Lay {
 
 // A tile's weights in a row, half of them, may sum to this before the row's reference moves up.
 constexpr float kGrown = 65536.f;
+// Above this they count as infinite, and so does a row's sum above twice as much (both halves), which marks the row: the
+// approximate instructions flush what is below 2^-126 to 0, the reciprocal of a sum above 2^126 and the factor
+// that such a rise of the reference scales by among it.
+constexpr float kMost = 0x1p124f;
 
 constexpr uint32_t kIdS = idesc_bf16(128, 128, 0, 0), kIdSNarrow = idesc_bf16(128, kSinkCols, 0, 0);
 
@@ -387,7 +391,7 @@ struct Fwd {
                     }
                 }
                 const float part = sum_of(add2(sum[0], sum[1]));
-                l += part;
+                l += part < kMost ? part : CUDART_INF_F;  // a NaN as well
                 if (part > kGrown) mine = fmaxf(mine, m + lg2(part));
                 wish[512 * ((ns & 1) ^ 1) + 128 * h] = mine;
                 tmem_wait_st();
@@ -421,7 +425,7 @@ struct Fwd {
             float bad = sum_of(bads);
             if (!swap(q, h, bad, other, nx)) return;
             if (h == 0 && t < L)
-                p.lse[at] = bad + other == 0.f && l < CUDART_INF_F ? (m + lg2(l)) * 0.6931471805599453f : redo_mark();
+                p.lse[at] = bad + other == 0.f && l <= 2.f * kMost ? (m + lg2(l)) * 0.6931471805599453f : redo_mark();
         }
     }
 };

@@ -1,5 +1,5 @@
 """GPU: attention over a window, its cache and the norms around a block at the edges of what their headers allow:
-tensors that begin on 16 bytes and on no more; scores that rise steeply along the keys."""
+tensors that begin on 16 bytes and on no more; scores that rise steeply along the keys, and to the end of fp32."""
 import pytest
 import torch
 
@@ -139,3 +139,22 @@ def test_references_that_move_in_every_tile(lib, d, Nq, Nk, window, sinks):
         again = lib.window_attn_fwd(t["q"], t["k"], t["v"], window, sinks, scale=1.0)
         assert torch.equal(again[0], o) and torch.equal(again[1], lse)
     ok(lib)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Nq,Nk", [(2, 1), (3, 1)])
+@pytest.mark.parametrize("rise,at", [(80, [300]), (85.5, [300]), (86, [300]), (86.5, [300]), (87, [300]), (87.5, [300]), (88, [300]),
+                                     (88.5, [300]), (89, [300]), (100, [300]), (86.5, [320, 321, 322, 323]), (87, [300, 330]),
+                                     (86.5, [300, 331, 400, 470, 590]), (85.5, list(range(300, 316)))])
+def test_scores_that_rise_to_the_end_of_fp32(lib, d, Nq, Nk, rise, at):
+    """Keys whose scores lie `rise` above those of all others (e^87.3 is 2^126, e^88.7 2^128): in the last tile that a
+    row sees, and in one before it.  Values of 1 at most, so that no product passes fp32."""
+    t = inputs(torch.bfloat16, B=1, T=600, Nq=Nq, Nk=Nk, d=d, seed=3)
+    t["q"].zero_()
+    t["q"][..., 0] = 8
+    t["k"][..., 0] = 0
+    t["k"][:, at, :, 0] = rise / 8  # bf16 holds it
+    t["v"].clamp_(-1, 1)
+    assert float(t["k"][0, at[0], 0, 0]) * 8 == rise
+    check(lib, t, 5000, 0, scale=1.0, label="rise %g" % rise)
+    check(lib, t, 290, 4, scale=1.0, label="rise %g, window" % rise)
