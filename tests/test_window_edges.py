@@ -3,10 +3,11 @@ tensors that begin on 16 bytes and on no more; scores that rise steeply along th
 import pytest
 import torch
 
+import window_reference as wref
 from conftest import cuda_ok
 from test_block_norm import args
 from test_block_norm import inputs as block_inputs
-from test_window_attn import DEV, DTYPES, check, inputs, normal, ok
+from test_window_attn import DEV, DTYPES, check, half_of, inputs, normal, ok, wide
 
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not cuda_ok(), reason="needs a CUDA GPU")]
 
@@ -158,3 +159,57 @@ def test_scores_that_rise_to_the_end_of_fp32(lib, d, Nq, Nk, rise, at):
     assert float(t["k"][0, at[0], 0, 0]) * 8 == rise
     check(lib, t, 5000, 0, scale=1.0, label="rise %g" % rise)
     check(lib, t, 290, 4, scale=1.0, label="rise %g, window" % rise)
+
+
+# ---- rows that do see what is not finite ------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_rows_that_see_a_bad_value(lib, dtype, d, bad):
+    """Every row that sees it has it in its column, and in all others what it has without it; lse and dv, which
+    do not depend on values, are as without it everywhere; dq, through D, is NaN."""
+    T, window, sinks, at = 600, 150, 4, 290
+    t = inputs(dtype, B=1, T=T, Nq=2, Nk=1, d=d, seed=6)
+    w = wide(t)
+    want = wref.attention(w["q"], w["k"], w["v"], window, sinks, None, None, w["do"], half_of(dtype))
+    seeing = torch.tensor([at <= i < at + window for i in range(T)])
+    others = torch.arange(d) != 5
+    t["v"][0, at, 0, 5] = bad
+    o, lse = lib.window_attn_fwd(t["q"], t["k"], t["v"], window, sinks)
+    out = lib.window_attn_bwd(t["q"], t["k"], t["v"], o, lse, window, sinks, do=t["do"])
+    ok(lib)
+    column = o[0, seeing][:, :, 5].float()
+    assert torch.isnan(column).all() if bad != bad else (column == bad).all()
+    wref.close(o[..., others], (want["o"][0][..., others], want["o"][1][..., others]), "other columns")
+    wref.close(o[:, ~seeing], (want["o"][0][:, ~seeing], want["o"][1][:, ~seeing]), "other rows")
+    wref.close(lse, want["lse"], "lse")
+    wref.close(out["dv"], want["dv"], "dv")
+    assert torch.isnan(out["dq"][0, seeing]).all()
+    wref.close(out["dq"][:, ~seeing], (want["dq"][0][:, ~seeing], want["dq"][1][:, ~seeing]), "dq")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_rows_that_see_a_bad_key(lib, dtype, d, bad):
+    """A key's infinity times a query's sign: a score of -infinity is a weight of 0, one of +infinity or NaN a row
+    of NaN."""
+    T, window, sinks, at = 600, 150, 4, 290
+    t = inputs(dtype, B=1, T=T, Nq=2, Nk=1, d=d, seed=6)
+    t["q"][..., 5] = t["q"][..., 5].sign() + (t["q"][..., 5] == 0)
+    # for the reference: a score 40 below its others' sizes on the rows whose weight is 0 (e^-40 of theirs)
+    finite = 0.0 if bad != bad else 40.0 * d ** 0.5 * (1 if bad > 0 else -1)
+    w = wide(t)
+    w["k"][0, at, 0, 5] = finite
+    want = wref.attention(w["q"], w["k"], w["v"], window, sinks, half=half_of(dtype))
+    t["k"][0, at, 0, 5] = bad
+    o, lse = lib.window_attn_fwd(t["q"], t["k"], t["v"], window, sinks)
+    ok(lib)
+    seeing = torch.tensor([at <= i < at + window for i in range(T)])[:, None]
+    gone = seeing & ~(t["q"][0, :, :, 5].cpu() * bad < 0)  # NaN: all that see it
+    assert gone.any() and (bad != bad or (seeing & ~gone).any())
+    assert torch.isnan(o[0].cpu()[gone]).all() and torch.isnan(lse[0].cpu()[gone]).all()
+    for n, x in (("o", o), ("lse", lse)):
+        wref.close(x[0].cpu()[~gone], (want[n][0][0][~gone], want[n][1][0][~gone]), n)
