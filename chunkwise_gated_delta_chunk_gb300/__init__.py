@@ -808,7 +808,8 @@ def window_attn_fwd(q, k, v, window, sinks=0, cu_seqlens=None, scale=None, strea
     ``sinks`` ones (``dn_window_attn_fwd``).
 
     q ``[B, T, Nq, d]``; k, v ``[B, T, Nk, d]``, Nq a multiple of Nk; d = 64 or 128; bf16 or
-    fp32; sinks up to 128; cu_seqlens int64 ``[N+1]`` on the device; ``scale`` None: 1 / sqrt(d).
+    fp32; sinks up to 128; cu_seqlens int64 ``[N+1]`` on the device; ``scale`` None, or 0 and
+    less: 1 / sqrt(d).
     Returns ``(o, lse)``, the latter ``[B, T, Nq]`` fp32: the logarithms of the softmax's sums,
     which :func:`window_attn_bwd` takes.
     """

@@ -5,6 +5,8 @@
 //     dk = scale ds^T q,  dv = p^T do   (window_dkv: tiles of 128 keys, one key head; the
 //                                        group's heads' queries and do stream by)
 //
+// p and ds are rounded to bf16 for their products, by half a step of each; D and the recomputed weights are fp32.
+//
 // Two kernels, so that no sum is added by atomics: every sum stays in tensor memory until it is
 // done, in a fixed order, for 8 products of 128 x 128 x d a tile instead of 5.
 //
@@ -31,7 +33,7 @@
 // in parts (a run of part_tiles tiles each) by items of their own, which leave fp32 sums of
 // the sinks' rows; window_sink_sums (dn_window.cu) adds them up in order.
 //
-// Measured (4 x 2048 tokens, window 512, 16 heads of 128 columns): window_dsum 12 us, window_dq 77, window_dkv 79, the
+// Measured (4 x 2048 tokens, window 512, 16 heads of 128 columns): window_dsum 12 us, window_dq 78, window_dkv 80, the
 // tensor pipe at work 45 to 49 % of the time.  Bound by the threads' phases and the products taking turns, and by the
 // accumulators' way out between items, when the tensor cores wait.
 #include "dn_window_tc.cuh"

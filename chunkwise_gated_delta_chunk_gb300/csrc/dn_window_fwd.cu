@@ -32,9 +32,9 @@
 //
 // CTAs are persistent, one an SM, and take items as they get done (Items: 47 us for the training shape below, 56 with
 // items at a fixed stride); every wait is bounded (dn_tc_sync.cuh).  Measured: one prompt of 32768
-// tokens, window 4096, 32 heads on 8 of 128 columns, 1.35 to 1.42 ms (1.09 at the measured rate of products in
-// the pairs that are seen); 4 x 2048 tokens, window 512, 16 heads, 47 us, the tensor pipe at work 39 % of the time: an
-// item's first and last tiles have nothing to overlap with.
+// tokens, window 4096, 32 heads on 8 of 128 columns, 1.35 ms, 1.45 in a run of calls under the power cap (1.09 at the
+// measured rate of products in the pairs that are seen); 4 x 2048 tokens, window 512, 16 heads, 48 us, the tensor
+// pipe at work 39 % of the time: an item's first and last tiles have nothing to overlap with.
 #include "dn_window_tc.cuh"
 
 namespace dn {

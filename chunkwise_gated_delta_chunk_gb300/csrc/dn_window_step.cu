@@ -229,6 +229,7 @@ extern __shared__ __align__(128) char s_step[];
 // head the one with 8 columns, twice where there are more than 8 (the other way round, 8 heads fill
 // half of 16 rows, and the products alone took as long as memory):
 //     S^T = K q^T,   O^T += V^T P^T,   P^T from S^T by two 8 x 8 transpositions.
+// The weights are rounded to bf16 for the second product, by half a step of each; their sum takes them unrounded.
 // The reference that weights are relative to moves up only when a score exceeds it by 2^8, so that a
 // group of positions needs no reduction but a vote.  Bound by memory: three stages of asynchronous copies a
 // warp keep the positions' 2 x 16 x d values coming; no warp waits for another before the end.

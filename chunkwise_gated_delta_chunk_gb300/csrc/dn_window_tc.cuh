@@ -104,7 +104,7 @@ __device__ __forceinline__ bool hold(const tcs::Ctx &x, uint32_t bar, uint32_t p
     }
 }
 
-// Slot number i in the order in which items are taken: the last tiles of the sequences first (under a causal mask the
+// Slot number i in the order in which items are taken: the last tiles of a sequence first (under a causal mask the
 // long ones) or, `up`, the first ones.  Without offsets by tile, then by sequence, so that the short ones
 // come last of all and fill the gaps; with offsets sequence by sequence.
 __device__ __forceinline__ unsigned slot_in_order(const SeqView &s, unsigned i, unsigned slots, bool up) {

@@ -25,7 +25,11 @@
  *
  * What a masked key or its value holds (NaN and infinities too) reaches no
  * output.  A row whose own operands are not finite comes out as the formulas
- * say; it costs a second, slower pass over its tile.
+ * say; it costs a second, slower pass over its tile, as does one of bf16 whose
+ * scores rise by 85 and more from one tile of 128 keys to a later one.
+ *
+ * Limits beside those of the entry points (DN_ERR_UNSUPPORTED): B T <= 2^31 - 256,
+ * T <= 2^30.
  */
 #ifndef DN_WINDOW_OPS_H
 #define DN_WINDOW_OPS_H
@@ -79,7 +83,7 @@ size_t dn_window_attn_bwd_workspace_bytes(int packed, int n_seqs, int B, int T, 
  *   lengths           [n_seqs]       int64  tokens that each sequence had
  *                                           before these; NULL: none
  *   k_cache, v_cache  [n_seqs, Nk, sinks + ring, d]  dtype
- * d is 64 or 128; ring >= 1, sinks + ring <= 2^30.  A length that is negative, or
+ * d is 64 or 128; ring >= 1, sinks + ring <= 2^30; Nk <= 65536.  A length that is negative, or
  * that 64 bits do not hold with the tokens added, makes dn_check return
  * DN_ERR_DEVICE_ARG; nothing is written for that sequence.
  */
@@ -93,7 +97,7 @@ dn_status dn_window_cache_fill(const void *k, const void *v, const int64_t *cu_s
  * token at position lengths[n] see.
  *   q        [n_seqs, Nq, d], k, v [n_seqs, Nk, d], o [n_seqs, Nq, d]  dtype
  *   lengths  [n_seqs] int64  tokens in the cache before the call (not changed)
- * window <= ring.  A negative length makes dn_check return
+ * window <= ring, sinks + ring <= 2^30; n_seqs Nq <= 2^27 - 16.  scale as above.  A negative length makes dn_check return
  * DN_ERR_DEVICE_ARG and leaves that sequence's outputs unspecified.
  */
 dn_status dn_window_attn_step(const void *q, const void *k, const void *v, int n_seqs, int Nq, int Nk, int d, int window,
